@@ -521,6 +521,134 @@ int sd_best_first_select(const int32_t* parents, const float* logprob, const int
                          int32_t* out_src, int32_t* out_parents, int32_t* out_tokens, float* out_score,
                          int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------- 4-bit key/value cache -- */
+/* A paged cache that holds keys and values in 4 bits, the tree attention that
+ * reads it, the attention weight its keys collect, and eviction by that
+ * weight.  No counterpart in the pages: at long contexts the bf16 cache is
+ * what a batched step reads most, and what limits the requests on a card.
+ *
+ * A row (one slot, one kv head, key or value) is held as a code 0..15 per
+ * dim with a scale s and a middle m, both bf16:
+ *   value = s (code - 8) + m,  s = bf16((hi - lo) / 15),  m = bf16(lo + 8 s),
+ *   code = round_half_even((x - m) / s) + 8, clamped to 0..15,
+ * lo and hi the row's least and greatest value, in fp32; where s is 0 the
+ * code is 8 and m = bf16(lo).  A row with a NaN or an infinity (or whose hi - lo is
+ * beyond fp32) is held as NaN in every dim.
+ *
+ * blocks: [n_pages][n_kv_heads][page_size / 32][sd_kv4_group_bytes(head_dim)]
+ * bytes, 16-byte aligned; request r's slot t lies in page page_table[r *
+ * max_pages + t / page_size].  A page may belong to several requests (a
+ * shared prefix).  pos and weight: [R][n_kv_heads][max_pages * page_size],
+ * 16-byte aligned, per request and slot the key's position in the text
+ * (ascending with the slot) and the attention weight it collected.  ctx_len:
+ * slots held per request.  page_size is a multiple of 32, head_dim 64 or 128.
+ *
+ * Rows of a call: request r owns rows cu[r] .. cu[r+1]-1 (cu int32 [R+1] on
+ * the device, the same values in cu_host).  A page id outside the pool or a
+ * context beyond the capacity sets *status (device int32, caller-owned) to
+ * SD_ERR_CAPACITY; such slots are neither read nor written.  Calls are
+ * asynchronous on `stream`. */
+typedef struct {
+  uint8_t* blocks;
+  int32_t* pos;
+  float* weight;
+  int32_t n_pages, page_size, n_kv_heads, head_dim;
+  const int32_t* page_table; /* device [R][max_pages] */
+  int32_t max_pages;
+  int32_t* ctx_len;          /* device [R] */
+} sd_kv4;
+
+/* Scores of sd_kv4_attn and sd_kv4_observe:
+ *   t = q.k scale;  t = softcap tanh(t / softcap) where softcap > 0;
+ *   t += slopes[q head] (position of k - position of q) where slopes is set;
+ * a key is hidden where window > 0 and it lies window or more positions
+ * back, or where start is set and its position is below start[r] (the
+ * request's document begins there).  scale 0: 1 / sqrt(head_dim). */
+typedef struct {
+  float scale, softcap;
+  const float* slopes;   /* device [n_q_heads] or null */
+  int32_t window;        /* 0: none */
+  const int32_t* start;  /* device [R] or null */
+} sd_kv4_score;
+
+/* Bytes of the 32 slots of one kv head (0 for a head_dim other than 64, 128). */
+int64_t sd_kv4_group_bytes(int32_t head_dim);
+
+/* Store rows: row cu[r] + i goes to slot at[r] + i of request r with position
+ * pos[row] (pos null: the slot's number), weight 0, and ctx_len[r] becomes
+ * at[r] + the rows stored (a request without rows keeps its length).  at
+ * null: ctx_len itself.  count (optional, device
+ * [R]): only the first count[r] rows of a request are stored (accepted_len +
+ * 1 of a verified tree).  src (optional, device int32 [rows]): row e's keys and
+ * values are taken from row src[e] of k and v (the accepted path), 0 <=
+ * src[e] < n_src.  k, v: bf16, rows row_stride elements apart, each
+ * [n_kv_heads][head_dim], 16-byte aligned, n_src rows.  A request that would
+ * pass its capacity stores nothing and keeps its length.  Errors:
+ * SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED (head_dim, page_size), SD_ERR_CUDA. */
+int sd_kv4_append(const sd_kv4* c, const uint16_t* k, const uint16_t* v, int64_t row_stride, int32_t n_src,
+                  const int32_t* cu, const int32_t* cu_host, int32_t R, const int32_t* src, const int32_t* count,
+                  const int32_t* pos, const int32_t* at, int32_t* status, void* stream);
+
+/* The values held: row cu[r] + i of k_out and v_out (bf16 [rows][n_kv_heads]
+ * [head_dim], 16-byte aligned) gets slot at[r] + i of request r (at null:
+ * slot i).  Errors as sd_kv4_append. */
+int sd_kv4_read(const sd_kv4* c, const int32_t* cu, const int32_t* cu_host, int32_t R, const int32_t* at,
+                uint16_t* k_out, uint16_t* v_out, int32_t* status, void* stream);
+
+/* Attention of each request's rows (1..64 per request; a request may have
+ * none) over its cached keys and, with k_new and v_new set, over the rows'
+ * own bf16 keys and values, row i seeing row j where bit j of anc[row] is set
+ * (sd_tree_info; anc null: j <= i).  q: bf16, rows q_stride elements apart,
+ * each [n_q_heads][head_dim]; k_new, v_new: rows kv_stride apart, each
+ * [n_kv_heads][head_dim]; all 16-byte aligned; n_q_heads a multiple of
+ * n_kv_heads, at most 16 query heads a kv head.  row_pos: position of each
+ * row (null: ctx_len[r] + i); a request's first row has its least.  max_ctx:
+ * the largest ctx_len the call can meet (0: the capacity), which sizes the
+ * launch; a longer request is read whole all the same.
+ * out: bf16 [rows][n_q_heads][head_dim], 0 in a row that sees no key; lse
+ * (optional): fp32 [rows][n_q_heads], the natural log of the sum of exp of
+ * the scores, -inf in such a row.  P enters the products as two bf16 terms
+ * (about 16 bits), the sums are fp32.
+ * workspace: sd_kv4_attn_workspace bytes (rows = cu_host[R]), 256-byte
+ * aligned, zeroed once by the caller and left ready for the next call; calls
+ * that share one must not overlap.  Errors: SD_ERR_INVALID_ARG,
+ * SD_ERR_UNSUPPORTED, SD_ERR_WORKSPACE, SD_ERR_CUDA. */
+size_t sd_kv4_attn_workspace(int32_t R, int32_t rows, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim);
+int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride, int32_t n_q_heads, const int32_t* cu,
+                const int32_t* cu_host, int32_t R, const uint16_t* k_new, const uint16_t* v_new, int64_t kv_stride,
+                const uint64_t* anc, const int32_t* row_pos, const sd_kv4_score* score, int32_t max_ctx, uint16_t* out,
+                float* lse, void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/* The weight the rows give to the cached keys: for each request, kv head and
+ * held slot t,
+ *   weight_out = decay * weight + sum over rows and the query heads of the kv
+ *                head of row_weight[row] exp(score - lse[row][q head]),
+ * hidden keys and rows of lse -inf giving 0.  lse as sd_kv4_attn leaves it
+ * (own keys included), row_weight fp32 [rows] (null: 1; the accepted rows' 1
+ * and the others' 0 after a verified tree).  weight_out: laid out as
+ * c->weight, may be c->weight itself.  The sums run in a fixed order (no
+ * atomics).  Errors as sd_kv4_attn. */
+int sd_kv4_observe(const sd_kv4* c, const uint16_t* q, int64_t q_stride, int32_t n_q_heads, const float* lse,
+                   const int32_t* cu, const int32_t* cu_host, int32_t R, const int32_t* row_pos,
+                   const float* row_weight, const sd_kv4_score* score, int32_t max_ctx, float decay,
+                   float* weight_out, int32_t* status, void* stream);
+
+/* Bring every request to at most `budget` slots, copying what stays into
+ * dst's pages in slot order: per kv head the first `sinks` slots, the last
+ * `recent` ones and, of the others, those of most weight (equal weights: the
+ * lower slot; a NaN weight counts as the least).  dst has the same heads and
+ * R requests, a capacity of at least `budget`, and pages, pos, weight and
+ * ctx_len of its own that src does not use: shared pages stay as they are, and
+ * the caller frees src's afterwards.  dst's ctx_len becomes min(ctx_len,
+ * budget), pos and weight move with their keys.  sinks + recent <= budget.
+ * workspace: sd_kv4_evict_workspace bytes, 256-byte aligned, any content;
+ * after the call it holds int32 [R][n_kv_heads][budget], the source slot of
+ * each slot kept.  Errors: SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED,
+ * SD_ERR_WORKSPACE, SD_ERR_CUDA. */
+size_t sd_kv4_evict_workspace(int32_t R, int32_t n_kv_heads, int32_t budget);
+int sd_kv4_evict(const sd_kv4* src, const sd_kv4* dst, int32_t R, int32_t budget, int32_t recent, int32_t sinks,
+                 void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
 /* -------------------------------------------------------- tiny verify -- */
 /* One linear layer and an lm_head: logits = (bf16(act W1^T)) Wlm^T, argmax
  * per node in fp32, then greedy acceptance over the tree.  act: bf16 [M][K];

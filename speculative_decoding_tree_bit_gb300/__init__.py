@@ -64,6 +64,16 @@ class PagedKV(ctypes.Structure):
                 ("max_pages", i32), ("S", vp), ("z", vp), ("ctx_len", vp)]
 
 
+class KV4(ctypes.Structure):
+    _fields_ = [("blocks", vp), ("pos", vp), ("weight", vp), ("n_pages", i32), ("page_size", i32),
+                ("n_kv_heads", i32), ("head_dim", i32), ("page_table", vp), ("max_pages", i32), ("ctx_len", vp)]
+
+
+class KV4ScoreArgs(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", vp), ("window", i32),
+                ("start", vp)]
+
+
 P = ctypes.POINTER
 _SIGS = {
     "sd_last_error": (ctypes.c_char_p, []),
@@ -106,6 +116,16 @@ _SIGS = {
     "sd_select_workspace": (ctypes.c_size_t, [i32]),
     "sd_best_first_select": (ctypes.c_int, [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp,
                                             ctypes.c_size_t, vp]),
+    "sd_kv4_group_bytes": (i64, [i32]),
+    "sd_kv4_append": (ctypes.c_int, [P(KV4), vp, vp, i64, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp]),
+    "sd_kv4_read": (ctypes.c_int, [P(KV4), vp, vp, i32, vp, vp, vp, vp, vp]),
+    "sd_kv4_attn_workspace": (ctypes.c_size_t, [i32, i32, i32, i32, i32]),
+    "sd_kv4_attn": (ctypes.c_int, [P(KV4), vp, i64, i32, vp, vp, i32, vp, vp, i64, vp, vp, P(KV4ScoreArgs), i32, vp,
+                                   vp, vp, ctypes.c_size_t, vp, vp]),
+    "sd_kv4_observe": (ctypes.c_int, [P(KV4), vp, i64, i32, vp, vp, vp, i32, vp, vp, P(KV4ScoreArgs), i32,
+                                      ctypes.c_float, vp, vp, vp]),
+    "sd_kv4_evict_workspace": (ctypes.c_size_t, [i32, i32, i32]),
+    "sd_kv4_evict": (ctypes.c_int, [P(KV4), P(KV4), i32, i32, i32, i32, vp, ctypes.c_size_t, vp, vp]),
     "sd_tiny_workspace": (ctypes.c_size_t, [i64, i64, i64, i32]),
     "sd_tiny_verify": (ctypes.c_int, [P(W12Tensor), P(W12Tensor), vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp,
                                       ctypes.c_size_t, vp]),

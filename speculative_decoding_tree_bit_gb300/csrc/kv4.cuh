@@ -1,0 +1,76 @@
+// The 4-bit key/value cache: layout and the helpers its kernels share.
+//
+// Slots come in groups of 32.  The record of a group, for one kv head of D
+// dims, is one run of 32 D + 256 bytes:
+//   K codes [32][D/2] | K (s, m) [32] | V codes [32][D/2] | V (s, m) [32]
+// A slot's codes lie in dim order, two a byte, the lower nibble first; with D
+// = 128 the two 32-byte halves of a V row are exchanged in the slots whose
+// bit 1 is set, so that the attention kernel's reads of four keys at once
+// fall into different shared-memory banks.  (s, m): scale and middle as a
+// bf16 pair, s in the lower half.  A record is one contiguous bulk copy, its
+// K part (the first half) another.
+#pragma once
+
+#include "common.cuh"
+
+namespace sdv {
+
+constexpr int kKvGroup = 32;  // slots of a record
+
+__host__ __device__ constexpr int kv4_rec(int D) { return 32 * D + 256; }
+__host__ __device__ constexpr int kv4_half(int D) { return 16 * D + 128; }  // the K part; V codes follow
+
+struct Kv4View {
+  uint8_t* blocks;   // [n_pages][hkv][groups per page][record]
+  int32_t* pos;      // [R][hkv][cap]
+  float* weight;     // [R][hkv][cap]
+  const int32_t* page_table;  // [R][max_pages]
+  int32_t* ctx_len;  // [R]
+  int32_t n_pages, gpp, hkv, max_pages;  // gpp: groups per page
+  int64_t cap;       // slots a request can hold
+
+  // record of group g of request r and kv head h; null where the page table
+  // has no page of the pool
+  __device__ __forceinline__ uint8_t* record(int D, int r, int h, int g) const {
+    const int pi = g / gpp;
+    const int page = page_table[(int64_t)r * max_pages + pi];
+    if (page < 0 || page >= n_pages) return nullptr;
+    return blocks + (((int64_t)page * hkv + h) * gpp + (g - pi * gpp)) * kv4_rec(D);
+  }
+  __device__ __forceinline__ int64_t slot0(int r, int h) const { return ((int64_t)r * hkv + h) * cap; }
+};
+
+// Byte of code pair `b` (dims 2b, 2b + 1) within the V row of slot t.
+template <int D>
+__device__ __forceinline__ int kv4_vbyte(int t, int b) {
+  return D == 128 ? b ^ ((t & 2) << 4) : b;
+}
+
+// What the scores of a call go by.
+struct Kv4Score {
+  float scale, cap;        // cap 0: none
+  const float* slopes;     // [hq] or null
+  int32_t window;          // 0: none
+  const int32_t* start;    // [R] or null
+};
+
+// First slot any row of a request can see, its rows standing at position p0
+// or later: positions ascend with the slots and no two are equal, so at most
+// (window - 1) cached keys lie inside the window and at most p0 - start
+// inside the document, the last ones.
+__device__ __forceinline__ int kv4_first(const Kv4Score& s, int r, int ctx, int p0) {
+  int64_t n = ctx;
+  if (s.window > 0 && s.window - 1 < n) n = s.window - 1;
+  if (s.start) {
+    const int64_t d = (int64_t)p0 - s.start[r];
+    if (d < n) n = d < 0 ? 0 : d;
+  }
+  return ctx - (int)n;
+}
+
+int kv4_check(const sd_kv4* c, int32_t R, const char* who, Kv4View* view);
+int kv4_check_rows(const int32_t* cu, const int32_t* cu_host, int32_t R, const char* who);
+int kv4_bad(int code, const char* who, const char* what);
+int kv4_check_score(const sd_kv4_score* sc, const char* who, Kv4Score* out, int head_dim);
+
+}  // namespace sdv

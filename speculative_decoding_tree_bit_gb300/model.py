@@ -12,7 +12,8 @@ import ctypes
 import numpy as np
 import torch
 
-from . import KV, LayerWeights, ModelConfig, ModelWeights, PagedKV, W12Meta, W12Tensor, check, lib, stream_ptr
+from . import (KV, KV4, KV4ScoreArgs, LayerWeights, ModelConfig, ModelWeights, PagedKV, W12Meta, W12Tensor, check, lib,
+               stream_ptr)
 
 
 def _ptr(t) -> int:
@@ -615,3 +616,215 @@ class GdnLayer:
         la = last if isinstance(last, torch.Tensor) else _i32(last, self.device)
         check(lib().sd_gdn_commit(par.data_ptr(), cu_d.data_ptr(), cu_h.ctypes.data, cu_h.size - 1, self.nh,
                                   la.data_ptr(), S.data_ptr(), self.ws.ptr, self.ws.nbytes, stream_ptr(stream)))
+
+
+class RequestRows:
+    """The rows of R requests in one call: request r owns rows cu[r] ..
+    cu[r+1]-1.  Keeps the offsets on the host and on the device, so calls
+    that share a layout copy nothing."""
+
+    def __init__(self, cu, device="cuda"):
+        self.cu = np.ascontiguousarray(np.asarray(cu, dtype=np.int32))
+        if self.cu.ndim != 1 or self.cu.size < 2 or self.cu[0] != 0 or np.any(np.diff(self.cu) < 0):
+            raise ValueError("cu must be [R+1] offsets that start at 0 and do not decrease")
+        self.R, self.n = self.cu.size - 1, int(self.cu[-1])
+        self.cu_dev = _i32(self.cu, device)
+
+
+class KV4Score:
+    """Scoring options of KV4Cache.attend and observe (sd_kv4_score)."""
+
+    def __init__(self, scale: float = 0.0, softcap: float = 0.0, slopes: torch.Tensor | None = None, window: int = 0,
+                 start: torch.Tensor | None = None):
+        if slopes is not None and (slopes.dtype != torch.float32 or not slopes.is_contiguous()):
+            raise ValueError("slopes must be contiguous float32")
+        if start is not None and (start.dtype != torch.int32 or not start.is_contiguous()):
+            raise ValueError("start must be contiguous int32")
+        self.slopes, self.start = slopes, start
+        self.args = KV4ScoreArgs(float(scale), float(softcap), _ptr(slopes), int(window), _ptr(start))
+
+
+def _rows16(t, heads, dim, what):
+    """A bf16 tensor (bfloat16 or int16 bits) [rows][heads][dim] whose rows
+    may be strided: (pointer, row stride in elements)."""
+    if t.element_size() != 2 or t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
+        raise ValueError(f"{what} must be 16-bit [rows][{heads}][{dim}], got {tuple(t.shape)} {t.dtype}")
+    if t.dtype == torch.float16:
+        raise ValueError(f"{what} must hold bf16")
+    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{what}: the heads of a row must lie together")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else heads * dim)
+
+
+def _ints(t, n, what, dtype=torch.int32):
+    if t is None:
+        return 0
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what} must be contiguous {dtype} of at least {n} entries")
+    return t.data_ptr()
+
+
+class KV4Cache:
+    """Paged key/value cache of R requests in 4 bits (sd_kv4): blocks, and per
+    request, kv head and slot the key's position and collected weight.  One
+    layer; `append` stores rows, `attend` is the tree attention over them,
+    `observe` adds up the weight that rows give to the keys, `evict` copies
+    what a budget keeps into another cache, `read` returns the values held.
+    Calls that share a cache object share its workspace: issue them on one
+    stream."""
+
+    def __init__(self, page_table, n_pages: int, n_kv_heads: int, head_dim: int = 128, page_size: int = 64,
+                 device="cuda"):
+        if head_dim not in (64, 128) or page_size < 32 or page_size % 32:
+            raise ValueError("head_dim must be 64 or 128, page_size a multiple of 32")
+        host = np.ascontiguousarray(np.asarray(page_table, dtype=np.int32))
+        if host.ndim != 2:
+            raise ValueError("page_table must be [R][max_pages]")
+        self.device, self.n_pages, self.page_size = device, int(n_pages), int(page_size)
+        self.n_kv_heads, self.head_dim = int(n_kv_heads), int(head_dim)
+        self.R, self.max_pages = host.shape
+        self.cap = self.max_pages * self.page_size
+        rec = 32 * self.head_dim + 256
+        self.page_table = _i32(host, device)
+        self.blocks = torch.zeros((self.n_pages, self.n_kv_heads, self.page_size // 32, rec), dtype=torch.uint8,
+                                  device=device)
+        self.pos = torch.zeros((self.R, self.n_kv_heads, self.cap), dtype=torch.int32, device=device)
+        self.weight = torch.zeros((self.R, self.n_kv_heads, self.cap), dtype=torch.float32, device=device)
+        self.ctx_len = torch.zeros(self.R, dtype=torch.int32, device=device)
+        self._status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._zero = torch.zeros(self.R, dtype=torch.int32, device=device)
+        self._ws = {}
+        s = KV4()
+        s.blocks, s.pos, s.weight = self.blocks.data_ptr(), self.pos.data_ptr(), self.weight.data_ptr()
+        s.n_pages, s.page_size, s.n_kv_heads, s.head_dim = (self.n_pages, self.page_size, self.n_kv_heads,
+                                                            self.head_dim)
+        s.page_table, s.max_pages, s.ctx_len = self.page_table.data_ptr(), self.max_pages, self.ctx_len.data_ptr()
+        self._s = s
+
+    def status(self) -> int:
+        """The device status of the calls so far (synchronises), then cleared."""
+        st = int(self._status.item())
+        self._status.zero_()
+        return st
+
+    def nbytes(self) -> int:
+        return self.blocks.numel() + 8 * self.pos.numel()
+
+    def _workspace(self, kind, n):
+        """A workspace of at least n bytes, zeroed when made."""
+        if kind not in self._ws or self._ws[kind].numel() < n:
+            self._ws[kind] = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.device)
+        return self._ws[kind]
+
+    def _at(self, at):
+        if at is None or isinstance(at, torch.Tensor):
+            return _ints(at, self.R, "at")
+        if at != 0:
+            raise ValueError("at must be an int32 device tensor [R], or 0")
+        return self._zero.data_ptr()
+
+    def _rows(self, rows):
+        if rows.R != self.R:
+            raise ValueError(f"rows of {rows.R} requests on a cache of {self.R}")
+        return rows
+
+    def append(self, k, v, rows: RequestRows, pos=None, at=None, src=None, count=None, stream=None):
+        """Store rows (sd_kv4_append).  k, v: [n][n_kv_heads][head_dim], rows
+        may be strided; pos int32 [rows]; at: first slot per request (int32
+        [R] or 0; default ctx_len); src int32 [rows]: the row of k and v that
+        each entry takes; count int32 [R]: entries of each request stored."""
+        rows = self._rows(rows)
+        kp, ks = _rows16(k, self.n_kv_heads, self.head_dim, "k")
+        vp_, vs = _rows16(v, self.n_kv_heads, self.head_dim, "v")
+        if k.shape[0] != v.shape[0] or (k.shape[0] > 1 and ks != vs):
+            raise ValueError("k and v must have the same rows and row stride")
+        check(lib().sd_kv4_append(ctypes.byref(self._s), kp, vp_, ks, k.shape[0], rows.cu_dev.data_ptr(),
+                                  rows.cu.ctypes.data, rows.R, _ints(src, rows.n, "src"),
+                                  _ints(count, rows.R, "count"), _ints(pos, rows.n, "pos"), self._at(at),
+                                  self._status.data_ptr(), stream_ptr(stream)))
+
+    def read(self, rows: RequestRows, at=0, dtype=torch.bfloat16, stream=None):
+        """The values held: (k, v) bf16 [rows][n_kv_heads][head_dim], row i
+        of request r from slot at[r] + i (sd_kv4_read)."""
+        rows = self._rows(rows)
+        shape = (rows.n, self.n_kv_heads, self.head_dim)
+        k = torch.empty(shape, dtype=dtype, device=self.device)
+        v = torch.empty(shape, dtype=dtype, device=self.device)
+        if k.element_size() != 2:
+            raise ValueError("dtype must be bfloat16, or int16 for its bits")
+        check(lib().sd_kv4_read(ctypes.byref(self._s), rows.cu_dev.data_ptr(), rows.cu.ctypes.data, rows.R,
+                                self._at(at), k.data_ptr(), v.data_ptr(), self._status.data_ptr(),
+                                stream_ptr(stream)))
+        return k, v
+
+    def attend(self, q, rows: RequestRows, k=None, v=None, anc=None, pos=None, score: KV4Score | None = None,
+               max_ctx: int = 0, out=None, lse=None, stream=None):
+        """Attention of the rows over the cache and their own keys
+        (sd_kv4_attn).  q [n][n_q_heads][head_dim], k, v [n][n_kv_heads]
+        [head_dim] (or both None), anc int64 ancestor bits [n] (sd_tree_info;
+        None: causal), pos int32 [n].  Returns (out like q, lse float32
+        [n][n_q_heads])."""
+        rows = self._rows(rows)
+        if q.dim() != 3 or q.shape[0] != rows.n or q.shape[1] % self.n_kv_heads:
+            raise ValueError("q must be [rows][n_q_heads][head_dim], n_q_heads a multiple of n_kv_heads")
+        hq = q.shape[1]
+        qp, qs = _rows16(q, hq, self.head_dim, "q")
+        kp = vp_ = ks = 0
+        if (k is None) != (v is None):
+            raise ValueError("k and v go together")
+        if k is not None:
+            kp, ks = _rows16(k, self.n_kv_heads, self.head_dim, "k")
+            vp_, vs = _rows16(v, self.n_kv_heads, self.head_dim, "v")
+            if k.shape[0] != rows.n or v.shape[0] != rows.n or (rows.n > 1 and ks != vs):
+                raise ValueError("k and v must have the rows of q and one row stride")
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif out.shape != q.shape or out.element_size() != 2 or not out.is_contiguous():
+            raise ValueError("out must be contiguous and of q's shape")
+        if lse is None:
+            lse = torch.empty((rows.n, hq), dtype=torch.float32, device=q.device)
+        elif lse.dtype != torch.float32 or not lse.is_contiguous() or tuple(lse.shape) != (rows.n, hq):
+            raise ValueError("lse must be contiguous float32 [rows][n_q_heads]")
+        ws = self._workspace("attn", int(lib().sd_kv4_attn_workspace(rows.R, rows.n, hq, self.n_kv_heads,
+                                                                     self.head_dim)))
+        check(lib().sd_kv4_attn(ctypes.byref(self._s), qp, qs, hq, rows.cu_dev.data_ptr(), rows.cu.ctypes.data, rows.R,
+                                kp, vp_, ks, _ints(anc, rows.n, "anc", torch.int64), _ints(pos, rows.n, "pos"),
+                                ctypes.byref(score.args) if score is not None else None, int(max_ctx), out.data_ptr(),
+                                lse.data_ptr(), ws.data_ptr(), ws.numel(), self._status.data_ptr(),
+                                stream_ptr(stream)))
+        return out, lse
+
+    def observe(self, q, lse, rows: RequestRows, pos=None, row_weight=None, score: KV4Score | None = None,
+                decay: float = 1.0, max_ctx: int = 0, out=None, stream=None):
+        """decay * weight + the weight the rows give to each cached key
+        (sd_kv4_observe), into out (default: self.weight itself); lse as
+        attend returned it, row_weight float32 [n].  Returns out."""
+        rows = self._rows(rows)
+        if q.dim() != 3 or q.shape[0] != rows.n or q.shape[1] % self.n_kv_heads:
+            raise ValueError("q must be [rows][n_q_heads][head_dim], n_q_heads a multiple of n_kv_heads")
+        hq = q.shape[1]
+        qp, qs = _rows16(q, hq, self.head_dim, "q")
+        if out is None:
+            out = self.weight
+        elif out.shape != self.weight.shape or out.dtype != torch.float32 or not out.is_contiguous():
+            raise ValueError("out must be contiguous float32 of the shape of weight")
+        check(lib().sd_kv4_observe(ctypes.byref(self._s), qp, qs, hq, _ints(lse, rows.n * hq, "lse", torch.float32),
+                                   rows.cu_dev.data_ptr(), rows.cu.ctypes.data, rows.R, _ints(pos, rows.n, "pos"),
+                                   _ints(row_weight, rows.n, "row_weight", torch.float32),
+                                   ctypes.byref(score.args) if score is not None else None, int(max_ctx), float(decay),
+                                   out.data_ptr(), self._status.data_ptr(), stream_ptr(stream)))
+        return out
+
+    def evict(self, dst: "KV4Cache", budget: int, recent: int = 0, sinks: int = 0, stream=None) -> torch.Tensor:
+        """Copy what a budget keeps of every request into dst (sd_kv4_evict):
+        the first `sinks` slots, the last `recent` and the heaviest others.
+        Returns the source slot of each slot kept, int32 [R][n_kv_heads]
+        [budget] (valid until the next evict of this cache; entries past
+        dst.ctx_len are unspecified)."""
+        if dst is self or dst.R != self.R:
+            raise ValueError("dst must be another cache of the same requests")
+        n = int(lib().sd_kv4_evict_workspace(self.R, self.n_kv_heads, int(budget)))
+        ws = self._workspace("evict", n)
+        check(lib().sd_kv4_evict(ctypes.byref(self._s), ctypes.byref(dst._s), self.R, int(budget), int(recent),
+                                 int(sinks), ws.data_ptr(), ws.numel(), self._status.data_ptr(), stream_ptr(stream)))
+        return ws[:n].view(torch.int32).view(self.R, self.n_kv_heads, int(budget))

@@ -19,6 +19,8 @@ struct Kv4AttnArgs {
   uint16_t* out;
   float* lse;
   int32_t* status;
+  int32_t* tickets;  // [grid], zero between calls
+  float* part;       // [2 grid][rows of a tile][D + 2]
 };
 
 __device__ __forceinline__ float nib(uint32_t byte, int d) { return (float)(int)((byte >> (4 * (d & 1))) & 15) - 8.f; }
@@ -31,85 +33,770 @@ __device__ __forceinline__ float kv4_score(const Kv4Score& s, float qk, float sl
   return t;
 }
 
-// One CTA per (row, query head): a thread per key for the scores, a thread
-// per dim for the values.  Right for every case, and the measure of the rest.
-template <int D>
-__global__ void __launch_bounds__(128) k_kv4_attn_simple(Kv4AttnArgs a) {
-  __shared__ float sq[D], sp[128], red[4];
-  const int e = blockIdx.x, hq = blockIdx.y, h = hq / a.G, tid = threadIdx.x;
-  int r = 0;
-  while (r + 1 < a.R && a.cu[r + 1] <= e) r++;
-  const int n0 = a.cu[r], i = e - n0, m = a.cu[r + 1] - n0;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+// 8x8 transpose of 16-bit values across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// The four nibbles of each 16-bit half of w as fp16 pairs, from two words (w
+// and w >> 8) and two masks: nibble i even lies at bits 0..3 and reads as the
+// subnormal code 2^-24, i odd at bits 4..7 and reads as code 2^-20.
+template <int I>
+__device__ __forceinline__ uint32_t codes2(uint32_t w) {
+  return (I < 2 ? w : w >> 8) & (I & 1 ? 0x00F000F0u : 0x000F000Fu);
+}
+// (code - 8) 2^-9 of the same pair: one fused multiply-add, exact.
+template <int I>
+__device__ __forceinline__ uint32_t centred2(uint32_t w) {
+  uint32_t y;
+  // 2^15 or 2^11, and -8 2^-9
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(codes2<I>(w)), "r"(I & 1 ? 0x68006800u : 0x78007800u), "r"(0xA400A400u));
+  return y;
+}
+__device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t y;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+  return y;
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+// What a call's requests hold, as the attention kernels split them: a request
+// is hkv x nc segments (kv head, tile of RT rows) of nu units each - `ng`
+// groups of 32 cached slots from group g0 on, then the rows' own keys in runs
+// of 32; at least one unit, so that a row that sees nothing is written too.
+struct Kv4Req {
+  int n0, m, ctx, g0, ng, nu, nc;
+};
+
+template <int RT>
+__device__ __forceinline__ Kv4Req kv4_req(const Kv4AttnArgs& a, int r) {
+  Kv4Req q;
+  q.n0 = a.cu[r];
+  q.m = min(max(a.cu[r + 1] - q.n0, 0), 64);
   int ctx = a.c.ctx_len[r];
   if (ctx < 0 || ctx > a.c.cap) {
-    if (tid == 0) set_status(a.status, SD_ERR_CAPACITY);
+    set_status(a.status, SD_ERR_CAPACITY);
     ctx = ctx < 0 ? 0 : (int)a.c.cap;
   }
-  if (tid < D) sq[tid] = bf2f(a.q[(int64_t)e * a.q_stride + hq * D + tid]);
-  __syncthreads();
-  const int qp = a.row_pos ? a.row_pos[e] : ctx + i;
-  const int p0 = a.row_pos ? a.row_pos[n0] : ctx;
-  const float slope = a.s.slopes ? a.s.slopes[hq] : 0.f;
-  const int start = a.s.start ? a.s.start[r] : INT32_MIN;
-  const int first = kv4_first(a.s, r, ctx, p0);
-  const uint64_t sees = a.anc ? a.anc[e] : (2ull << i) - 1;
-  const int own = a.k_new ? m : 0;
-  float mx = -INFINITY, l = 0.f, o = 0.f;
-  for (int base = first; base < ctx + own; base += 128) {
-    const int t = base + tid;
-    float sc = -INFINITY;
-    if (t < ctx) {
-      const uint8_t* rec = a.c.record(D, r, h, t / 32);
-      if (!rec) {
-        set_status(a.status, SD_ERR_CAPACITY);
-      } else {
-        const uint32_t sm = *reinterpret_cast<const uint32_t*>(rec + 16 * D + (t & 31) * 4);
-        float dot = 0.f, qs = 0.f;
-        for (int d = 0; d < D; d++) {
-          dot = fmaf(sq[d], nib(rec[(t & 31) * (D / 2) + d / 2], d), dot);
-          qs += sq[d];
+  q.ctx = ctx;
+  int first = 0;
+  if (a.s.window > 0 || a.s.start) first = kv4_first(a.s, r, ctx, a.row_pos && q.m ? a.row_pos[q.n0] : ctx);
+  q.g0 = first / kKvGroup;
+  q.ng = ctx > first ? (ctx - 1) / kKvGroup - q.g0 + 1 : 0;
+  q.nu = max(1, q.ng + (a.k_new ? (q.m + 31) / 32 : 0));
+  q.nc = (a.G * q.m + RT - 1) / RT;
+  return q;
+}
+
+// ------------------------------------------------ attention, warp MMA --
+//
+// Scores and outputs are computed transposed, S^T = K Q^T and O^T = V^T P^T,
+// with mma.m16n8k16: the codes are the 16-row A side, the query rows the
+// 8-wide B side, so that the few rows of a decode step (the heads of a group)
+// fill half or all of a tile.
+//
+// What bounds it is not the bytes alone but the integer pipe, at 2 cycles a
+// warp instruction, that makes operands of the nibbles: 4 bits of a 16-bit
+// lane are read in place as an fp16 subnormal (code 2^-24, or 2^-20 for the
+// odd nibbles, whose 2^-4 is in the queries), so eight codes cost four masks
+// and one shift.  K's codes enter as they are, 0..15: score = s (c.q) +
+// (m - 8 s) sum(q).  V's are centred by a fused multiply-add on the other pipe
+// (a sum over many keys would lose what the offset 8 sum(p s) cancels):
+// output = sum (p s)(c - 8) + sum p m.  Queries are bf16, exact in fp16 after
+// a power of two that brings a row's greatest value below 2^15 (values
+// 2^-31 of it and less lose bits).  A weight p s enters as one fp16 term
+// with 11 bits, 2^-12 of its value against the 2^-9 of the output's own
+// rounding; a power of two that follows the greatest s keeps it at most 2^13,
+// so weights down to 2^-38 of the greatest count.  The rows' own keys and
+// values are bf16 products, their weights two bf16 terms.
+//
+// A warp works on its own: it takes every W-th unit of the CTA's segment, and
+// keeps a ring of two 32-slot records, one bulk copy each, filled a unit
+// ahead; the next segment's first two are on their way while a segment is
+// joined.  Running maxima are per warp; the warps' parts are joined in shared
+// memory at the segment's end, the CTAs' parts of a segment in global memory
+// by the last CTA to finish, in CTA order (the same bits every time).  The
+// segments' units are dealt evenly over the CTAs (one per SM), whatever the
+// requests' lengths.
+
+template <int D, int NT, int W>
+struct AttnShape {
+  static constexpr int RT = 8 * NT;
+  static constexpr int kStage = kv4_rec(D) + 128;
+  static constexpr int off_o = W * 2 * kStage;                   // [W][RT][D] fp32
+  static constexpr int off_q = off_o + W * RT * D * 4;           // [NT][D/16][32] uint2: fp16 queries
+  static constexpr int off_qb = off_q + NT * (D / 16) * 32 * 8;  // the same, bf16
+  static constexpr int off_anc = off_qb + NT * (D / 16) * 32 * 8;  // [RT] u64
+  static constexpr int off_bar = off_anc + RT * 8;               // [W][2]
+  static constexpr int off_ml = off_bar + W * 2 * 8;             // [2][W][RT]
+  static constexpr int off_row = off_ml + 2 * W * RT * 4;        // qsum, factor, slope, pos, L [RT] each
+  static constexpr int off_ok = off_row + 5 * RT * 4;            // [W][2]
+  static constexpr int smem = off_ok + W * 2 * 4;
+};
+
+template <int D, int NT, int W, bool BIAS>
+__global__ void __launch_bounds__(W * 32, 1) k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
+  using S = AttnShape<D, NT, W>;
+  constexpr int RT = S::RT;
+  constexpr int KK = D / 16;  // k-steps of a score, and 16-dim tiles of an output
+  extern __shared__ __align__(128) uint8_t sm[];
+  float* s_o = reinterpret_cast<float*>(sm + S::off_o);
+  uint2* s_q = reinterpret_cast<uint2*>(sm + S::off_q);
+  uint2* s_qb = reinterpret_cast<uint2*>(sm + S::off_qb);
+  uint64_t* s_anc = reinterpret_cast<uint64_t*>(sm + S::off_anc);
+  uint64_t* s_bar = reinterpret_cast<uint64_t*>(sm + S::off_bar);
+  float* s_m = reinterpret_cast<float*>(sm + S::off_ml);
+  float* s_l = s_m + W * RT;
+  float* s_qs = reinterpret_cast<float*>(sm + S::off_row);
+  float* s_fac = s_qs + RT;
+  float* s_slope = s_fac + RT;
+  int* s_pos = reinterpret_cast<int*>(s_slope + RT);
+  float* s_L = reinterpret_cast<float*>(s_pos + RT);
+  int* s_ok = reinterpret_cast<int*>(sm + S::off_ok);
+  __shared__ int s_r0, s_s0, s_abort, s_last;
+  __shared__ long long s_u0, s_u1, s_seg0, s_U;
+  __shared__ int s_C;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+
+  // this CTA's share of the units
+  if (warp == 0) {
+    long long U = 0;
+    for (int base = 0; base < a.R; base += 32) {
+      const int r = base + lane;
+      long long n = 0;
+      if (r < a.R) {
+        const Kv4Req rq = kv4_req<RT>(a, r);
+        n = (long long)a.c.hkv * rq.nc * rq.nu;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      U += n;
+    }
+    const long long C = min((long long)gridDim.x, (U + W - 1) / W);
+    const long long u0 = blockIdx.x < C ? (long long)blockIdx.x * U / C : U;
+    const long long u1 = blockIdx.x < C ? (long long)(blockIdx.x + 1) * U / C : U;
+    if (u0 < u1) {
+      long long before = 0;
+      for (int base = 0; base < a.R; base += 32) {
+        const int r = base + lane;
+        Kv4Req rq = {};
+        if (r < a.R) rq = kv4_req<RT>(a, r);
+        const long long n = (long long)a.c.hkv * rq.nc * rq.nu;
+        long long run = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, run, o);
+          if (lane >= o) run += v;
         }
-        dot = fmaf(bf2f((uint16_t)sm), dot, bf2f((uint16_t)(sm >> 16)) * qs);
-        sc = kv4_score(a.s, dot, slope, qp, a.c.pos[a.c.slot0(r, h) + t], start);
+        const long long lo = before + run - n;
+        if (u0 >= lo && u0 < lo + n) {
+          s_r0 = r;
+          s_s0 = (int)((u0 - lo) / rq.nu);
+          s_seg0 = lo + (u0 - lo) / rq.nu * rq.nu;
+        }
+        before += __shfl_sync(0xffffffffu, run, 31);
+        if (before > u0) break;
       }
-    } else if (t < ctx + own && (sees >> (t - ctx) & 1)) {
-      const int j = n0 + t - ctx;
-      float dot = 0.f;
-      for (int d = 0; d < D; d++) dot = fmaf(sq[d], bf2f(a.k_new[(int64_t)j * a.kv_stride + h * D + d]), dot);
-      sc = kv4_score(a.s, dot, slope, qp, a.row_pos ? a.row_pos[j] : ctx + t - ctx, start);
     }
-    float w = sc;
-    for (int x = 16; x > 0; x >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, x));
-    if ((tid & 31) == 0) red[tid >> 5] = w;
-    __syncthreads();
-    const float mn = fmaxf(mx, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float ms = mn == -INFINITY ? 0.f : mn;
-    const float al = __expf(mx - ms);
-    sp[tid] = __expf(sc - ms);
-    __syncthreads();
-    mx = mn;
-    l *= al;
-    o *= al;
-    for (int j = 0; j < 128 && base + j < ctx + own; j++) {
-      const float p = sp[j];
-      l += p;
-      if (p == 0.f || tid >= D) continue;
-      const int u = base + j;
-      float val;
-      if (u < ctx) {
-        const uint8_t* rec = a.c.record(D, r, h, u / 32) + kv4_half(D);
-        const uint32_t sm = *reinterpret_cast<const uint32_t*>(rec + 16 * D + (u & 31) * 4);
-        val = fmaf(bf2f((uint16_t)sm), nib(rec[(u & 31) * (D / 2) + kv4_vbyte<D>(u, tid / 2)], tid),
-                   bf2f((uint16_t)(sm >> 16)));
-      } else {
-        val = bf2f(a.v_new[(int64_t)(n0 + u - ctx) * a.kv_stride + h * D + tid]);
-      }
-      o = fmaf(p, val, o);
+    if (lane == 0) {
+      s_u0 = u0;
+      s_u1 = u1;
+      s_U = U;
+      s_C = (int)C;
+      s_abort = 0;
     }
-    __syncthreads();
   }
-  if (tid < D) a.out[((int64_t)e * a.hq + hq) * D + tid] = f2bf(l > 0.f ? o / l : l == 0.f ? 0.f : l);
-  if (tid == 0 && a.lse) a.lse[(int64_t)e * a.hq + hq] = l == 0.f ? -INFINITY : mx + logf(l);
+  if (lane == 0) {
+    mbar_init(&s_bar[warp * 2], 1);
+    mbar_init(&s_bar[warp * 2 + 1], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (s_u0 >= s_u1) return;
+
+  uint64_t* const bar = s_bar + warp * 2;
+  uint8_t* const ring = sm + warp * 2 * S::kStage;
+  uint32_t used = 0;  // records this warp has taken from its ring
+
+  // the segment at hand: unit range [ua, ub), of which the units below ng are
+  // records.  A lane holds the address of every 32nd of the warp's records.
+  int r = s_r0, s = s_s0;
+  long long seg = s_seg0;
+  Kv4Req rq = kv4_req<RT>(a, r);
+  int ua = (int)(s_u0 - seg), ub = (int)min((long long)rq.nu, s_u1 - seg);
+  const uint8_t* addr;
+  auto look_up = [&](int u) {  // u: the warp's unit that lane 0 stands for
+    const int x = u + lane * W;
+    addr = x < min(ub, rq.ng) ? a.c.record(D, r, s / rq.nc, rq.g0 + x) : nullptr;
+  };
+  auto issue = [&](int u, int k, int stage) {  // k: the lane that holds unit u's address
+    const uint8_t* rec = reinterpret_cast<const uint8_t*>(
+        __shfl_sync(0xffffffffu, (unsigned long long)reinterpret_cast<uintptr_t>(addr), k));
+    if (lane == 0) {
+      s_ok[warp * 2 + stage] = rec != nullptr;
+      if (rec) {
+        uint8_t* dst = ring + stage * S::kStage;
+        mbar_arrive_expect_tx(&bar[stage], kv4_rec(D) + (BIAS ? 128 : 0));
+        bulk_g2s(dst, rec, kv4_rec(D), &bar[stage]);
+        if (BIAS) bulk_g2s(dst + kv4_rec(D), a.c.pos + a.c.slot0(r, s / rq.nc) + (rq.g0 + u) * kKvGroup, 128, &bar[stage]);
+      } else {
+        set_status(a.status, SD_ERR_CAPACITY);
+        mbar_arrive(&bar[stage]);
+      }
+    }
+    __syncwarp();
+  };
+  auto begin = [&]() {
+    const int u = ua + warp, e = min(ub, rq.ng);
+    if (u < e) {
+      look_up(u);
+      issue(u, 0, used & 1);
+      if (u + W < e) issue(u + W, 1, (used + 1) & 1);
+    }
+  };
+  begin();
+
+  const int e0 = q >> 1;  // which of a key pair this lane reads first (bank spread)
+  const uint32_t sel_lo = e0 ? 0x1054u : 0x5410u, sel_hi = e0 ? 0x3276u : 0x7632u;
+  const float sc2 = BIAS ? 1.f : a.s.scale * kLog2e;
+
+  for (;;) {
+    const int h = s / rq.nc, rc = s - h * rq.nc;
+    const int rows = min(RT, a.G * rq.m - rc * RT);
+    const int start = BIAS && a.s.start ? a.s.start[r] : INT32_MIN;
+
+    // the tile's query rows as B fragments; dims are taken in the order the
+    // codes' nibbles give them
+    for (int i = tid; i < RT * (D / 8); i += W * 32) {
+      const int row = i / (D / 8), oct = i % (D / 8);
+      const int rho = rc * RT + row;
+      const bool ok = row < rows;
+      const int node = ok ? rho % rq.m : 0, hq = h * a.G + (ok ? rho / rq.m : 0);
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (ok) x = *reinterpret_cast<const uint4*>(a.q + (int64_t)(rq.n0 + node) * a.q_stride + hq * D + oct * 8);
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+      float f[8], qs = 0.f, big = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        f[k] = bf2f((uint16_t)(xs[k >> 1] >> (16 * (k & 1))));
+        qs += f[k];
+        big = fmaxf(big, fabsf(f[k]));
+      }
+#pragma unroll
+      for (int o = D / 16; o > 0; o >>= 1) {
+        qs += __shfl_xor_sync(0xffffffffu, qs, o);
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      }
+      // 2^e brings the row's greatest value into [2^14, 2^15)
+      const int e = min(max(14 + 127 - (int)(__float_as_uint(big) >> 23), -100), 100);
+      const float up = pow2i(e), up4 = pow2i(e - 4);
+      const int ql = oct / (D / 32), j = oct % (D / 32);
+      const int at = ((row >> 3) * KK + 2 * j) * 32 + 4 * (row & 7) + ql;
+      s_q[at] = make_uint2(pack_f16x2(f[0] * up, f[4] * up), pack_f16x2(f[1] * up4, f[5] * up4));
+      s_q[at + 32] = make_uint2(pack_f16x2(f[2] * up, f[6] * up), pack_f16x2(f[3] * up4, f[7] * up4));
+      s_qb[at] = make_uint2(prmt(x.x, x.z, 0x5410), prmt(x.x, x.z, 0x7632));
+      s_qb[at + 32] = make_uint2(prmt(x.y, x.w, 0x5410), prmt(x.y, x.w, 0x7632));
+      if (oct == 0) {
+        s_qs[row] = qs * sc2;
+        s_fac[row] = pow2i(24 - e) * sc2;
+        s_slope[row] = BIAS && a.s.slopes ? a.s.slopes[hq] : 0.f;
+        s_pos[row] = a.row_pos ? a.row_pos[rq.n0 + node] : rq.ctx + node;
+        s_anc[row] = !ok ? 0ull : a.anc ? a.anc[rq.n0 + node] : (2ull << node) - 1;
+      }
+    }
+    __syncthreads();
+    float o[NT][KK][4];
+    float mx[NT][2], l[NT][2], mv[NT][2], fac[NT][2], qs[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+      for (int t = 0; t < KK; t++) o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        mx[nt][e] = -INFINITY;
+        l[nt][e] = mv[nt][e] = 0.f;
+        fac[nt][e] = s_fac[nt * 8 + 2 * q + e];
+        qs[nt][e] = s_qs[nt * 8 + 2 * q + e];
+      }
+    }
+    // values' weights are p s vup: vup 2^13 over the power of two at or above
+    // the greatest s so far (bits vtop), which leaves o short by vup 2^-9
+    float vup = 512.f;
+    uint32_t vtop = 0;
+
+    float sc[2][NT][4];  // scores (base 2), then weights, of keys 16 i + g, 16 i + g + 8
+    // a greater maximum anywhere in the warp rescales what it has so far
+    auto grow = [&](const float (&top)[NT][2]) {
+      bool grows = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) grows |= top[nt][0] > mx[nt][0] || top[nt][1] > mx[nt][1];
+      if (!__any_sync(0xffffffffu, grows)) return;
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) {
+        float al[2];
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          float t = top[nt][e];
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+          const float mn = fmaxf(mx[nt][e], t);
+          al[e] = mn == -INFINITY ? 1.f : ex2(mx[nt][e] - mn);
+          mx[nt][e] = mn;
+          l[nt][e] *= al[e];
+          mv[nt][e] *= al[e];
+        }
+#pragma unroll
+        for (int t = 0; t < KK; t++) {
+          o[nt][t][0] *= al[0];
+          o[nt][t][1] *= al[1];
+          o[nt][t][2] *= al[0];
+          o[nt][t][3] *= al[1];
+        }
+      }
+    };
+
+    const int ue = min(ub, rq.ng);
+    int k = 0;
+    for (int u = ua + warp; u < ue; u += W) {
+      const int stage = used & 1;
+      const uint8_t* st = ring + stage * S::kStage;
+      if (!mbar_wait_or_abort(&bar[stage], (used >> 1) & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(30));
+      {
+        // K: lane (g, q) holds dims q D/4 .. of keys g, g + 8, g + 16, g + 24
+        uint32_t kw[4][D / 32];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const uint8_t* p = st + (g + 8 * i) * (D / 2) + q * (D / 8);
+          if constexpr (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            kw[i][0] = v.x, kw[i][1] = v.y, kw[i][2] = v.z, kw[i][3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            kw[i][0] = v.x, kw[i][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) sc[i][nt][0] = sc[i][nt][1] = sc[i][nt][2] = sc[i][nt][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 32; j++) {
+          uint32_t f[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            f[i][0] = codes2<0>(kw[i][j]);
+            f[i][1] = codes2<1>(kw[i][j]);
+            f[i][2] = codes2<2>(kw[i][j]);
+            f[i][3] = codes2<3>(kw[i][j]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            const uint2 b0 = s_q[(nt * KK + 2 * j) * 32 + lane], b1 = s_q[(nt * KK + 2 * j + 1) * 32 + lane];
+            mma_f16(sc[0][nt], f[0][0], f[1][0], f[0][1], f[1][1], b0.x, b0.y);
+            mma_f16(sc[1][nt], f[2][0], f[3][0], f[2][1], f[3][1], b0.x, b0.y);
+            mma_f16(sc[0][nt], f[0][2], f[1][2], f[0][3], f[1][3], b1.x, b1.y);
+            mma_f16(sc[1][nt], f[2][2], f[3][2], f[2][3], f[3][3], b1.x, b1.y);
+          }
+        }
+      }
+      // slots of this record that the request holds
+      const int lim = s_ok[warp * 2 + stage] ? rq.ctx - (rq.g0 + u) * kKvGroup : 0;
+      float vs[4], vm[4];
+      float top[NT][2];
+      uint32_t vb = 0;
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) top[nt][0] = top[nt][1] = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {  // key 8 i + g of the unit
+        const int kl = 8 * i + g;
+        const uint32_t kw = *reinterpret_cast<const uint32_t*>(st + 16 * D + kl * 4);
+        const uint32_t vw = *reinterpret_cast<const uint32_t*>(st + kv4_half(D) + 16 * D + kl * 4);
+        const bool in = kl < lim;
+        const float ks = __uint_as_float(kw << 16);
+        const float km = fmaf(-8.f, ks, __uint_as_float(kw & 0xFFFF0000u));
+        vs[i] = in ? __uint_as_float(vw << 16) : 0.f;
+        vm[i] = in ? __uint_as_float(vw & 0xFFFF0000u) : 0.f;
+        if (vs[i] == vs[i]) vb = max(vb, __float_as_uint(vs[i]));
+        const int kp = BIAS ? *reinterpret_cast<const int*>(st + kv4_rec(D) + kl * 4) : 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            float& x = sc[i >> 1][nt][2 * (i & 1) + e];
+            float t = fmaf(ks, x * fac[nt][e], km * qs[nt][e]);
+            if (BIAS) {
+              const int row = nt * 8 + 2 * q + e;
+              t = kv4_score(a.s, t, s_slope[row], s_pos[row], kp, start) * kLog2e;
+            }
+            x = in ? t : -INFINITY;
+            top[nt][e] = fmaxf(top[nt][e], x);
+          }
+      }
+      grow(top);
+      if (__any_sync(0xffffffffu, vb > vtop)) {
+        const uint32_t b = __reduce_max_sync(0xffffffffu, vb);
+        vtop = b | 0x007FFFFFu;  // up to the next power of two
+        const float up = pow2i(min(max(13 + 126 - (int)(b >> 23), -100), 100)), ratio = up / vup;
+        vup = up;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int t = 0; t < KK; t++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[nt][t][e] *= ratio;
+      }
+      // weights, transposed into B fragments [16-key step]
+      uint32_t pf[NT][2][2];
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const float vsu = vs[i] * vup;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+          float w[2];
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const float x = sc[i >> 1][nt][2 * (i & 1) + e];
+            const float p = ex2(x - (mx[nt][e] == -INFINITY ? 0.f : mx[nt][e]));
+            l[nt][e] += p;
+            w[e] = p * vsu;
+            if (BIAS) {  // a hidden key's scale may be NaN
+              w[e] = x == -INFINITY ? 0.f : w[e];
+              mv[nt][e] += x == -INFINITY ? 0.f : p * vm[i];
+            } else {
+              mv[nt][e] = fmaf(p, vm[i], mv[nt][e]);
+            }
+          }
+          pf[nt][i >> 1][i & 1] = transpose8(pack_f16x2(w[0], w[1]));
+        }
+      }
+      // V: lane (g, q) holds dims g D/8 .. of keys 2q, 2q + 1, 2q + 8, 2q + 9
+      // of a 16-key step, merged into words of one key pair's four dims
+      const uint8_t* pv = st + kv4_half(D);
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        uint32_t w[2][D / 32];
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+          const int k0 = 16 * i + 8 * b + 2 * q;
+          const int ka = k0 + e0, kb = k0 + 1 - e0;
+          if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(pv + ka * 64 + kv4_vbyte<128>(ka, g * 8));
+            const uint2 y = *reinterpret_cast<const uint2*>(pv + kb * 64 + kv4_vbyte<128>(kb, g * 8));
+            w[b][0] = prmt(x.x, y.x, sel_lo), w[b][1] = prmt(x.x, y.x, sel_hi);
+            w[b][2] = prmt(x.y, y.y, sel_lo), w[b][3] = prmt(x.y, y.y, sel_hi);
+          } else {
+            const uint32_t x = *reinterpret_cast<const uint32_t*>(pv + ka * 32 + g * 4);
+            const uint32_t y = *reinterpret_cast<const uint32_t*>(pv + kb * 32 + g * 4);
+            w[b][0] = prmt(x, y, sel_lo), w[b][1] = prmt(x, y, sel_hi);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < D / 32; j++) {
+          const uint32_t a0 = centred2<0>(w[0][j]), a1 = centred2<1>(w[0][j]), a2 = centred2<0>(w[1][j]),
+                         a3 = centred2<1>(w[1][j]), b0 = centred2<2>(w[0][j]), b1 = centred2<3>(w[0][j]),
+                         b2 = centred2<2>(w[1][j]), b3 = centred2<3>(w[1][j]);
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            mma_f16(o[nt][2 * j], a0, a1, a2, a3, pf[nt][i][0], pf[nt][i][1]);
+            mma_f16(o[nt][2 * j + 1], b0, b1, b2, b3, pf[nt][i][0], pf[nt][i][1]);
+          }
+        }
+      }
+      __syncwarp();
+      used++;
+      k++;
+      if (u + 2 * W < ue) {
+        if (k == 31) {  // the lanes' addresses run out
+          look_up(u + 2 * W);
+          k = -1;
+        }
+        issue(u + 2 * W, k + 1, stage);
+      }
+    }
+
+    // the rows' own keys, in runs of 32
+    for (int u = max(ua, rq.ng) + (warp + W - (max(ua, rq.ng) - ua) % W) % W; u < ub; u += W) {
+      const int j0 = (u - rq.ng) * 32;
+      if (!a.k_new || j0 >= rq.m) break;  // the unit of a request that sees nothing
+      const uint16_t* kn = a.k_new + (int64_t)rq.n0 * a.kv_stride + h * D + q * (D / 4);
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) sc[i][nt][0] = sc[i][nt][1] = sc[i][nt][2] = sc[i][nt][3] = 0.f;
+        const int ka = j0 + 16 * i + g, kb = ka + 8;
+        const uint16_t* pa = kn + (ka < rq.m ? ka : 0) * a.kv_stride;
+        const uint16_t* pb = kn + (kb < rq.m ? kb : 0) * a.kv_stride;
+#pragma unroll
+        for (int j = 0; j < D / 32; j++) {
+          const uint4 xa = *reinterpret_cast<const uint4*>(pa + 8 * j), xb = *reinterpret_cast<const uint4*>(pb + 8 * j);
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            const uint2 b0 = s_qb[(nt * KK + 2 * j) * 32 + lane], b1 = s_qb[(nt * KK + 2 * j + 1) * 32 + lane];
+            mma_bf16(sc[i][nt], prmt(xa.x, xa.z, 0x5410), prmt(xb.x, xb.z, 0x5410), prmt(xa.x, xa.z, 0x7632),
+                     prmt(xb.x, xb.z, 0x7632), b0.x, b0.y);
+            mma_bf16(sc[i][nt], prmt(xa.y, xa.w, 0x5410), prmt(xb.y, xb.w, 0x5410), prmt(xa.y, xa.w, 0x7632),
+                     prmt(xb.y, xb.w, 0x7632), b1.x, b1.y);
+          }
+        }
+      }
+      float top[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) top[nt][0] = top[nt][1] = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int j = j0 + 8 * i + g;
+        const int kp = BIAS && j < rq.m ? (a.row_pos ? a.row_pos[rq.n0 + j] : rq.ctx + j) : 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const int row = nt * 8 + 2 * q + e;
+            float& x = sc[i >> 1][nt][2 * (i & 1) + e];
+            float t = x * sc2;
+            if (BIAS) t = kv4_score(a.s, t, s_slope[row], s_pos[row], kp, start) * kLog2e;
+            x = j < rq.m && (s_anc[row] >> j & 1) ? t : -INFINITY;
+            top[nt][e] = fmaxf(top[nt][e], x);
+          }
+      }
+      grow(top);
+      const float wup = vup * (1.f / 512.f);
+      uint32_t ph[NT][2][2], pl[NT][2][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          float w[2];
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            float& x = sc[i >> 1][nt][2 * (i & 1) + e];
+            const float p = ex2(x - (mx[nt][e] == -INFINITY ? 0.f : mx[nt][e]));
+            l[nt][e] += p;
+            x = w[e] = p * wup;
+          }
+          const uint32_t hi = pack_bf16x2(w[0], w[1]);
+          const uint32_t lo = pack_bf16x2(w[0] - __uint_as_float(hi << 16), w[1] - __uint_as_float(hi & 0xFFFF0000u));
+          ph[nt][i >> 1][i & 1] = transpose8(hi);
+          pl[nt][i >> 1][i & 1] = transpose8(lo);
+        }
+      // A product with a weight of 0 would carry a NaN or an infinity of a
+      // row's values to rows that do not see it: such a run is added key by key
+      const uint16_t* vn = a.v_new + (int64_t)rq.n0 * a.kv_stride + h * D + g * (D / 8);
+      uint32_t odd = 0;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const int kx = j0 + 8 * (i >> 1) + 2 * q + (i & 1);
+        const uint16_t* p = vn + (kx < rq.m ? kx : 0) * a.kv_stride;
+#pragma unroll
+        for (int c = 0; c < D / 64; c++) {
+          const uint4 x = *reinterpret_cast<const uint4*>(p + 8 * c);
+          odd |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
+                 ((x.z & 0x7F807F80u) + 0x00800080u) | ((x.w & 0x7F807F80u) + 0x00800080u);
+        }
+      }
+      if (!__any_sync(0xffffffffu, (odd & 0x80008000u) != 0)) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          const uint16_t* p[4];
+#pragma unroll
+          for (int b = 0; b < 4; b++) {
+            const int kx = j0 + 16 * i + 8 * (b >> 1) + 2 * q + (b & 1);
+            p[b] = vn + (kx < rq.m ? kx : 0) * a.kv_stride;
+          }
+#pragma unroll
+          for (int c = 0; c < D / 64; c++) {
+            uint32_t x[4][4];
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+              const uint4 v = *reinterpret_cast<const uint4*>(p[b] + 8 * c);
+              x[b][0] = v.x, x[b][1] = v.y, x[b][2] = v.z, x[b][3] = v.w;
+            }
+#pragma unroll
+            for (int t = 0; t < 4; t++) {
+              const uint32_t f0 = prmt(x[0][t], x[1][t], 0x5410), f1 = prmt(x[0][t], x[1][t], 0x7632),
+                             f2 = prmt(x[2][t], x[3][t], 0x5410), f3 = prmt(x[2][t], x[3][t], 0x7632);
+#pragma unroll
+              for (int nt = 0; nt < NT; nt++) {
+                mma_bf16(o[nt][4 * c + t], f0, f1, f2, f3, ph[nt][i][0], ph[nt][i][1]);
+                mma_bf16(o[nt][4 * c + t], f0, f1, f2, f3, pl[nt][i][0], pl[nt][i][1]);
+              }
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          for (int gk = 0; gk < 8; gk++) {
+            const int j = j0 + 8 * i + gk;
+            if (j >= rq.m) break;
+            const uint16_t* p = vn + j * a.kv_stride;
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+              for (int e = 0; e < 2; e++) {
+                const float w = __shfl_sync(0xffffffffu, sc[i >> 1][nt][2 * (i & 1) + e], 4 * gk + q);
+                if ((s_anc[nt * 8 + 2 * q + e] >> j & 1) && w != 0.f)
+#pragma unroll
+                  for (int t = 0; t < KK; t++) {
+                    o[nt][t][e] = fmaf(w, bf2f(p[2 * t]), o[nt][t][e]);
+                    o[nt][t][2 + e] = fmaf(w, bf2f(p[2 * t + 1]), o[nt][t][2 + e]);
+                  }
+              }
+          }
+      }
+    }
+
+    // the next segment: its first records are fetched while this one is joined
+    const bool whole = ua == 0 && ub == rq.nu;
+    // a part's slot: 2 c for the first segment of CTA c, 2 c + 1 for its last
+    const int64_t slot = 2ll * blockIdx.x + (seg + ua > s_u0 ? 1 : 0);
+    const long long this_seg = seg;
+    const Kv4Req tq = rq;
+    seg += rq.nu;
+    const bool more = seg < s_u1;
+    if (more) {
+      if (++s == a.c.hkv * rq.nc) {
+        s = 0;
+        do rq = kv4_req<RT>(a, ++r);
+        while (rq.nc == 0);
+      }
+      ua = 0;
+      ub = (int)min((long long)rq.nu, s_u1 - seg);
+      begin();
+    }
+
+    // join the warps
+    const float down = 512.f / vup;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
+          mv[nt][e] += __shfl_xor_sync(0xffffffffu, mv[nt][e], x);
+        }
+        const int row = nt * 8 + 2 * q + e;
+        if (g == 0) {
+          s_m[warp * RT + row] = mx[nt][e];
+          s_l[warp * RT + row] = l[nt][e];
+        }
+        float* dst = s_o + (warp * RT + row) * D + g * (D / 8);
+#pragma unroll
+        for (int t = 0; t < KK; t++)
+          *reinterpret_cast<float2*>(dst + 2 * t) =
+              make_float2(fmaf(o[nt][t][e], down, mv[nt][e]), fmaf(o[nt][t][2 + e], down, mv[nt][e]));
+      }
+    __syncthreads();
+    float* part = a.part + slot * (RT * (D + 2));
+    if (tid < rows) {
+      float M = -INFINITY, L = 0.f;
+      for (int w = 0; w < W; w++) M = fmaxf(M, s_m[w * RT + tid]);
+      const float Ms = M == -INFINITY ? 0.f : M;
+      for (int w = 0; w < W; w++) {
+        const float f = ex2(s_m[w * RT + tid] - Ms);
+        // a warp whose every score was NaN has no maximum, but a sum
+        L += s_l[w * RT + tid] == 0.f ? 0.f : f * s_l[w * RT + tid];
+        s_m[w * RT + tid] = f;
+      }
+      s_L[tid] = L;
+      if (whole) {
+        const int rho = rc * RT + tid;
+        if (a.lse)
+          a.lse[(int64_t)(tq.n0 + rho % tq.m) * a.hq + h * a.G + rho / tq.m] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
+      } else {
+        __stcg(part + RT * D + 2 * tid, M);
+        __stcg(part + RT * D + 2 * tid + 1, L);
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < rows * (D / 4); i += W * 32) {
+      const int row = i / (D / 4), d4 = i % (D / 4);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int w = 0; w < W; w++) {
+        const float f = s_m[w * RT + row];
+        const float4 v = *reinterpret_cast<const float4*>(s_o + (w * RT + row) * D + 4 * d4);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+      if (whole) {
+        const float L = s_L[row], inv = L == 0.f ? 0.f : 1.f / L;
+        const int rho = rc * RT + row;
+        uint16_t* dst = a.out + ((int64_t)(tq.n0 + rho % tq.m) * a.hq + h * a.G + rho / tq.m) * D + 4 * d4;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      } else {
+        __stcg(reinterpret_cast<float4*>(part + row * D + 4 * d4), acc);
+      }
+    }
+    if (!whole) {
+      // the last of the segment's CTAs joins their parts
+      const long long U = s_U, C = s_C;
+      const int c0 = (int)(((this_seg + 1) * C - 1) / U), c1 = (int)(((this_seg + tq.nu) * C - 1) / U);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int old = atomic_add_acq_rel(a.tickets + c0, 1);
+        s_last = old == c1 - c0;
+        if (s_last) a.tickets[c0] = 0;
+      }
+      __syncthreads();
+      if (s_last) {
+        const int64_t slot0 = 2ll * c0 + ((long long)c0 * U / C < this_seg ? 1 : 0);
+        auto part_of = [&](int c) { return a.part + (c == c0 ? slot0 : 2ll * c) * (RT * (D + 2)); };
+        for (int i = tid; i < rows * (D / 4); i += W * 32) {
+          const int row = i / (D / 4), d4 = i % (D / 4);
+          float M = -INFINITY;
+          for (int c = c0; c <= c1; c++) M = fmaxf(M, __ldcg(part_of(c) + RT * D + 2 * row));
+          const float Ms = M == -INFINITY ? 0.f : M;
+          float L = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int c = c0; c <= c1; c++) {
+            const float* pc = part_of(c);
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pc + RT * D + 2 * row));
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(pc + row * D + 4 * d4));
+            const float f = ex2(ml.x - Ms);
+            L = fmaf(f, ml.y, L);
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z);
+            acc.w = fmaf(f, v.w, acc.w);
+          }
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          const int rho = rc * RT + row;
+          const int64_t at = (int64_t)(tq.n0 + rho % tq.m) * a.hq + h * a.G + rho / tq.m;
+          *reinterpret_cast<uint2*>(a.out + at * D + 4 * d4) =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          if (d4 == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
+        }
+      }
+    }
+    if (!more) break;
+    __syncthreads();  // s_o, s_q and the rows' data are free again
+  }
 }
 
 struct Kv4ObserveArgs {
@@ -168,6 +855,32 @@ __global__ void __launch_bounds__(128) k_kv4_observe_simple(Kv4ObserveArgs b) {
   }
 }
 
+// ---------------------------------------------------------------- launch --
+
+constexpr size_t kTicketBytes = 4096;  // one ticket a CTA
+constexpr int kMaxCtas = 1024;
+
+template <int D, int NT, int W>
+static int launch_attn_tile(const Kv4AttnArgs& a, int64_t units, bool bias, cudaStream_t st) {
+  auto kern = bias ? k_kv4_attn<D, NT, W, true> : k_kv4_attn<D, NT, W, false>;
+  constexpr int smem = AttnShape<D, NT, W>::smem;
+  SD_CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>({(int64_t)num_sms(), kMaxCtas, units}));
+  kern<<<(unsigned)grid, W * 32, smem, st>>>(a);
+  SD_CK(cudaGetLastError());
+  return SD_OK;
+}
+
+// Rows of a tile by the most rows that a (request, kv head) has; warps by what
+// the tile leaves in registers and shared memory.
+template <int D>
+static int launch_attn(const Kv4AttnArgs& a, int rows, int64_t units, bool bias, cudaStream_t st) {
+  if (rows <= 8) return launch_attn_tile<D, 1, 16>(a, units, bias, st);
+  if (rows <= 16) return launch_attn_tile<D, 2, 12>(a, units, bias, st);
+  if (rows <= 24) return launch_attn_tile<D, 3, 8>(a, units, bias, st);
+  return launch_attn_tile<D, 4, 8>(a, units, bias, st);
+}
+
 // ---------------------------------------------------------------- checks --
 
 static int check_call(const char* who, const sd_kv4* c, const uint16_t* q, int64_t q_stride, int32_t hq,
@@ -203,7 +916,7 @@ extern "C" size_t sd_kv4_attn_workspace(int32_t R, int32_t rows, int32_t n_q_hea
   if (R < 1 || rows < 0 || n_kv_heads < 1 || n_q_heads < n_kv_heads || n_q_heads % n_kv_heads ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  return 256;
+  return kTicketBytes + (size_t)2 * num_sms() * 32 * (head_dim + 2) * sizeof(float);
 }
 
 extern "C" int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride, int32_t n_q_heads, const int32_t* cu,
@@ -236,10 +949,16 @@ extern "C" int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride,
   a.out = out;
   a.lse = lse;
   a.status = status;
-  auto kern = c->head_dim == 128 ? k_kv4_attn_simple<128> : k_kv4_attn_simple<64>;
-  kern<<<dim3(rows, n_q_heads), 128, 0, (cudaStream_t)stream>>>(a);
-  SD_CK(cudaGetLastError());
-  return SD_OK;
+  a.tickets = (int32_t*)workspace;
+  a.part = (float*)((uint8_t*)workspace + kTicketBytes);
+  int most = 0;
+  for (int r = 0; r < R; r++) most = std::max(most, cu_host[r + 1] - cu_host[r]);
+  most *= a.G;
+  const int64_t ctx = max_ctx > 0 ? std::min<int64_t>(max_ctx, a.c.cap) : a.c.cap;
+  const int64_t units = (int64_t)R * c->n_kv_heads * ((most + 31) / 32) * ((ctx + 31) / 32 + 2);
+  const bool bias = a.s.cap > 0.f || a.s.slopes || a.s.window > 0 || a.s.start;
+  return c->head_dim == 128 ? launch_attn<128>(a, most, units, bias, (cudaStream_t)stream)
+                            : launch_attn<64>(a, most, units, bias, (cudaStream_t)stream);
 }
 
 extern "C" int sd_kv4_observe(const sd_kv4* c, const uint16_t* q, int64_t q_stride, int32_t n_q_heads,

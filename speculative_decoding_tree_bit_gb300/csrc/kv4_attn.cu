@@ -81,11 +81,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
 // What a call's requests hold, as the attention kernels split them: a request
-// is hkv x nc segments (kv head, tile of RT rows) of nu units each - `ng`
-// groups of 32 cached slots from group g0 on, then the rows' own keys in runs
-// of 32; at least one unit, so that a row that sees nothing is written too.
+// is hkv x nc segments (kv head, tile of RT rows) of nu units each: the rows'
+// own keys in `no` runs of 32, then the groups of 32 cached slots from group
+// g0 on; at least one unit, so that a row that sees nothing is written too.
 struct Kv4Req {
-  int n0, m, ctx, g0, ng, nu, nc;
+  int n0, m, ctx, g0, no, nu, nc;
 };
 
 template <int RT>
@@ -102,8 +102,9 @@ __device__ __forceinline__ Kv4Req kv4_req(const Kv4AttnArgs& a, int r) {
   int first = 0;
   if (a.s.window > 0 || a.s.start) first = kv4_first(a.s, r, ctx, a.row_pos && q.m ? a.row_pos[q.n0] : ctx);
   q.g0 = first / kKvGroup;
-  q.ng = ctx > first ? (ctx - 1) / kKvGroup - q.g0 + 1 : 0;
-  q.nu = max(1, q.ng + (a.k_new ? (q.m + 31) / 32 : 0));
+  q.no = a.k_new ? (q.m + 31) / 32 : 0;
+  q.nu = q.no + (ctx > first ? (ctx - 1) / kKvGroup - q.g0 + 1 : 0);
+  if (q.nu == 0) q.no = q.nu = 1;  // an empty run
   q.nc = (a.G * q.m + RT - 1) / RT;
   return q;
 }
@@ -136,15 +137,16 @@ __device__ __forceinline__ Kv4Req kv4_req(const Kv4AttnArgs& a, int r) {
 // joined.  Running maxima are per warp; the warps' parts are joined in shared
 // memory at the segment's end, the CTAs' parts of a segment in global memory
 // by the last CTA to finish, in CTA order (the same bits every time).  The
-// segments' units are dealt evenly over the CTAs (one per SM), whatever the
-// requests' lengths.
+// segments' units are dealt evenly over the CTAs, whatever the requests'
+// lengths; two CTAs an SM, so that one works while the other joins.
 
 template <int D, int NT, int W>
 struct AttnShape {
   static constexpr int RT = 8 * NT;
   static constexpr int kStage = kv4_rec(D) + 128;
-  static constexpr int off_o = W * 2 * kStage;                   // [W][RT][D] fp32
-  static constexpr int off_q = off_o + W * RT * D * 4;           // [NT][D/16][32] uint2: fp16 queries
+  static constexpr int kPairs = D / 2 + 2;                       // float pairs of a row of a warp's output
+  static constexpr int off_o = W * 2 * kStage;                   // [W][RT][kPairs] float pairs
+  static constexpr int off_q = off_o + W * RT * kPairs * 8;           // [NT][D/16][32] uint2: fp16 queries
   static constexpr int off_qb = off_q + NT * (D / 16) * 32 * 8;  // the same, bf16
   static constexpr int off_anc = off_qb + NT * (D / 16) * 32 * 8;  // [RT] u64
   static constexpr int off_bar = off_anc + RT * 8;               // [W][2]
@@ -155,7 +157,7 @@ struct AttnShape {
 };
 
 template <int D, int NT, int W, bool BIAS>
-__global__ void __launch_bounds__(W * 32, 1) k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
+__global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
   using S = AttnShape<D, NT, W>;
   constexpr int RT = S::RT;
   constexpr int KK = D / 16;  // k-steps of a score, and 16-dim tiles of an output
@@ -173,56 +175,65 @@ __global__ void __launch_bounds__(W * 32, 1) k_kv4_attn(const __grid_constant__ 
   int* s_pos = reinterpret_cast<int*>(s_slope + RT);
   float* s_L = reinterpret_cast<float*>(s_pos + RT);
   int* s_ok = reinterpret_cast<int*>(sm + S::off_ok);
-  __shared__ int s_r0, s_s0, s_abort, s_last;
-  __shared__ long long s_u0, s_u1, s_seg0, s_U;
-  __shared__ int s_C;
+  __shared__ int s_r0, s_s0, s_abort, s_last, s_u0, s_u1, s_seg0, s_each, s_more;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
 
-  // this CTA's share of the units
+  // this CTA's share of the units: U over C CTAs, the first U % C of them
+  // one more
   if (warp == 0) {
-    long long U = 0;
+    int U = 0, segs = 0, lo = 0;
+    Kv4Req rq = {};
     for (int base = 0; base < a.R; base += 32) {
-      const int r = base + lane;
-      long long n = 0;
-      if (r < a.R) {
-        const Kv4Req rq = kv4_req<RT>(a, r);
-        n = (long long)a.c.hkv * rq.nc * rq.nu;
+      rq = {};
+      if (base + lane < a.R) rq = kv4_req<RT>(a, base + lane);
+      const int n = a.c.hkv * rq.nc * rq.nu;
+      int run = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += v;
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-      U += n;
+      lo = U + run - n;
+      U += __shfl_sync(0xffffffffu, run, 31);
+      segs += __reduce_add_sync(0xffffffffu, a.c.hkv * rq.nc);
     }
-    const long long C = min((long long)gridDim.x, (U + W - 1) / W);
-    const long long u0 = blockIdx.x < C ? (long long)blockIdx.x * U / C : U;
-    const long long u1 = blockIdx.x < C ? (long long)(blockIdx.x + 1) * U / C : U;
+    // little work: whole segments to a CTA, or even parts of one, so that
+    // fewer parts are joined; else every CTA
+    int C = gridDim.x;
+    if (U < C * W * 2) C = min(C, segs * ((U + segs * W - 1) / max(1, segs * W)));
+    C = max(C, 1);
+    const int each = U / C, more = U - each * C;
+    const int u0 = (int)blockIdx.x < C ? (int)blockIdx.x * each + min((int)blockIdx.x, more) : U;
+    const int u1 = (int)blockIdx.x < C ? u0 + each + ((int)blockIdx.x < more) : U;
     if (u0 < u1) {
-      long long before = 0;
+      int before = 0;
       for (int base = 0; base < a.R; base += 32) {
-        const int r = base + lane;
-        Kv4Req rq = {};
-        if (r < a.R) rq = kv4_req<RT>(a, r);
-        const long long n = (long long)a.c.hkv * rq.nc * rq.nu;
-        long long run = n;
+        if (a.R > 32) {
+          rq = {};
+          if (base + lane < a.R) rq = kv4_req<RT>(a, base + lane);
+          const int n = a.c.hkv * rq.nc * rq.nu;
+          int run = n;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long v = __shfl_up_sync(0xffffffffu, run, o);
-          if (lane >= o) run += v;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += v;
+          }
+          lo = before + run - n;
+          before += __shfl_sync(0xffffffffu, run, 31);
         }
-        const long long lo = before + run - n;
-        if (u0 >= lo && u0 < lo + n) {
-          s_r0 = r;
-          s_s0 = (int)((u0 - lo) / rq.nu);
-          s_seg0 = lo + (u0 - lo) / rq.nu * rq.nu;
+        if (u0 >= lo && u0 < lo + a.c.hkv * rq.nc * rq.nu) {
+          s_r0 = base + lane;
+          s_s0 = (u0 - lo) / rq.nu;
+          s_seg0 = lo + s_s0 * rq.nu;
         }
-        before += __shfl_sync(0xffffffffu, run, 31);
         if (before > u0) break;
       }
     }
     if (lane == 0) {
       s_u0 = u0;
       s_u1 = u1;
-      s_U = U;
-      s_C = (int)C;
+      s_each = each;
+      s_more = more;
       s_abort = 0;
     }
   }
@@ -238,16 +249,19 @@ __global__ void __launch_bounds__(W * 32, 1) k_kv4_attn(const __grid_constant__ 
   uint8_t* const ring = sm + warp * 2 * S::kStage;
   uint32_t used = 0;  // records this warp has taken from its ring
 
-  // the segment at hand: unit range [ua, ub), of which the units below ng are
+  // the segment at hand: unit range [ua, ub), of which the units from no on are
   // records.  A lane holds the address of every 32nd of the warp's records.
-  int r = s_r0, s = s_s0;
-  long long seg = s_seg0;
+  int r = s_r0, s = s_s0, seg = s_seg0;
+  const int u0 = s_u0, u1 = s_u1;
   Kv4Req rq = kv4_req<RT>(a, r);
-  int ua = (int)(s_u0 - seg), ub = (int)min((long long)rq.nu, s_u1 - seg);
+  int ua = u0 - seg, ub = min(rq.nu, u1 - seg);
   const uint8_t* addr;
+  auto first_record = [&]() {  // the first of the segment's records that falls to this warp
+    return ua + warp + (rq.no - ua - warp > 0 ? (rq.no - ua - warp + W - 1) / W * W : 0);
+  };
   auto look_up = [&](int u) {  // u: the warp's unit that lane 0 stands for
     const int x = u + lane * W;
-    addr = x < min(ub, rq.ng) ? a.c.record(D, r, s / rq.nc, rq.g0 + x) : nullptr;
+    addr = x < ub ? a.c.record(D, r, s / rq.nc, rq.g0 + x - rq.no) : nullptr;
   };
   auto issue = [&](int u, int k, int stage) {  // k: the lane that holds unit u's address
     const uint8_t* rec = reinterpret_cast<const uint8_t*>(
@@ -258,7 +272,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_kv4_attn(const __grid_constant__ 
         uint8_t* dst = ring + stage * S::kStage;
         mbar_arrive_expect_tx(&bar[stage], kv4_rec(D) + (BIAS ? 128 : 0));
         bulk_g2s(dst, rec, kv4_rec(D), &bar[stage]);
-        if (BIAS) bulk_g2s(dst + kv4_rec(D), a.c.pos + a.c.slot0(r, s / rq.nc) + (rq.g0 + u) * kKvGroup, 128, &bar[stage]);
+        if (BIAS) bulk_g2s(dst + kv4_rec(D), a.c.pos + a.c.slot0(r, s / rq.nc) + (rq.g0 + u - rq.no) * kKvGroup, 128, &bar[stage]);
       } else {
         set_status(a.status, SD_ERR_CAPACITY);
         mbar_arrive(&bar[stage]);
@@ -267,11 +281,11 @@ __global__ void __launch_bounds__(W * 32, 1) k_kv4_attn(const __grid_constant__ 
     __syncwarp();
   };
   auto begin = [&]() {
-    const int u = ua + warp, e = min(ub, rq.ng);
-    if (u < e) {
+    const int u = first_record();
+    if (u < ub) {
       look_up(u);
       issue(u, 0, used & 1);
-      if (u + W < e) issue(u + W, 1, (used + 1) & 1);
+      if (u + W < ub) issue(u + W, 1, (used + 1) & 1);
     }
   };
   begin();
@@ -376,9 +390,129 @@ __global__ void __launch_bounds__(W * 32, 1) k_kv4_attn(const __grid_constant__ 
       }
     };
 
-    const int ue = min(ub, rq.ng);
+    // the rows' own keys, in runs of 32, 16 at a time
+    for (int u = ua + warp; u < min(ub, rq.no); u += W)
+#pragma unroll 1
+      for (int j0 = u * 32; j0 < min(u * 32 + 32, a.k_new ? rq.m : 0); j0 += 16) {
+        float so[NT][4];  // scores, then weights, of keys g and g + 8
+        const int ja = j0 + g, jb = ja + 8;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) so[nt][0] = so[nt][1] = so[nt][2] = so[nt][3] = 0.f;
+        {
+          const uint16_t* kn = a.k_new + (int64_t)rq.n0 * a.kv_stride + h * D + q * (D / 4);
+          const uint16_t* pa = kn + (ja < rq.m ? ja : 0) * a.kv_stride;
+          const uint16_t* pb = kn + (jb < rq.m ? jb : 0) * a.kv_stride;
+#pragma unroll
+          for (int j = 0; j < D / 32; j++) {
+            const uint4 xa = *reinterpret_cast<const uint4*>(pa + 8 * j), xb = *reinterpret_cast<const uint4*>(pb + 8 * j);
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+              const uint2 b0 = s_qb[(nt * KK + 2 * j) * 32 + lane], b1 = s_qb[(nt * KK + 2 * j + 1) * 32 + lane];
+              mma_bf16(so[nt], prmt(xa.x, xa.z, 0x5410), prmt(xb.x, xb.z, 0x5410), prmt(xa.x, xa.z, 0x7632),
+                       prmt(xb.x, xb.z, 0x7632), b0.x, b0.y);
+              mma_bf16(so[nt], prmt(xa.y, xa.w, 0x5410), prmt(xb.y, xb.w, 0x5410), prmt(xa.y, xa.w, 0x7632),
+                       prmt(xb.y, xb.w, 0x7632), b1.x, b1.y);
+            }
+          }
+        }
+        float top[NT][2];
+        const int kpa = BIAS && ja < rq.m ? (a.row_pos ? a.row_pos[rq.n0 + ja] : rq.ctx + ja) : 0;
+        const int kpb = BIAS && jb < rq.m ? (a.row_pos ? a.row_pos[rq.n0 + jb] : rq.ctx + jb) : 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const int row = nt * 8 + 2 * q + e;
+            const uint64_t anc = s_anc[row];
+            float ta = so[nt][e] * sc2, tb = so[nt][2 + e] * sc2;
+            if (BIAS) {
+              ta = kv4_score(a.s, ta, s_slope[row], s_pos[row], kpa, start) * kLog2e;
+              tb = kv4_score(a.s, tb, s_slope[row], s_pos[row], kpb, start) * kLog2e;
+            }
+            so[nt][e] = ja < rq.m && (anc >> ja & 1) ? ta : -INFINITY;
+            so[nt][2 + e] = jb < rq.m && (anc >> jb & 1) ? tb : -INFINITY;
+            top[nt][e] = fmaxf(so[nt][e], so[nt][2 + e]);
+          }
+        grow(top);
+        const float wup = vup * (1.f / 512.f);
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int i = 0; i < 2; i++) {
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              float& x = so[nt][2 * i + e];
+              const float p = ex2(x - (mx[nt][e] == -INFINITY ? 0.f : mx[nt][e]));
+              l[nt][e] += p;
+              x = p * wup;
+            }
+            const float w0 = so[nt][2 * i], w1 = so[nt][2 * i + 1];
+            const uint32_t hi = pack_bf16x2(w0, w1);
+            const uint32_t lo = pack_bf16x2(w0 - __uint_as_float(hi << 16), w1 - __uint_as_float(hi & 0xFFFF0000u));
+            ph[nt][i] = transpose8(hi);
+            pl[nt][i] = transpose8(lo);
+          }
+        // A product with a weight of 0 would carry a NaN or an infinity of a
+        // row's values to rows that do not see it: such keys are added one by one
+        const uint16_t* vn = a.v_new + (int64_t)rq.n0 * a.kv_stride + h * D + g * (D / 8);
+        uint32_t odd = 0;
+#pragma unroll
+        for (int b = 0; b < 4; b++) {
+          const int kx = j0 + 8 * (b >> 1) + 2 * q + (b & 1);
+#pragma unroll
+          for (int c = 0; c < D / 64; c++) {
+            const uint4 x = *reinterpret_cast<const uint4*>(vn + (kx < rq.m ? kx : 0) * a.kv_stride + 8 * c);
+            odd |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
+                   ((x.z & 0x7F807F80u) + 0x00800080u) | ((x.w & 0x7F807F80u) + 0x00800080u);
+          }
+        }
+        if (!__any_sync(0xffffffffu, (odd & 0x80008000u) != 0)) {
+#pragma unroll
+          for (int c = 0; c < D / 64; c++) {
+            uint32_t x[4][4];
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+              const int kx = j0 + 8 * (b >> 1) + 2 * q + (b & 1);
+              const uint4 v = *reinterpret_cast<const uint4*>(vn + (kx < rq.m ? kx : 0) * a.kv_stride + 8 * c);
+              x[b][0] = v.x, x[b][1] = v.y, x[b][2] = v.z, x[b][3] = v.w;
+            }
+#pragma unroll
+            for (int t = 0; t < 4; t++) {
+              const uint32_t f0 = prmt(x[0][t], x[1][t], 0x5410), f1 = prmt(x[0][t], x[1][t], 0x7632),
+                             f2 = prmt(x[2][t], x[3][t], 0x5410), f3 = prmt(x[2][t], x[3][t], 0x7632);
+#pragma unroll
+              for (int nt = 0; nt < NT; nt++) {
+                mma_bf16(o[nt][4 * c + t], f0, f1, f2, f3, ph[nt][0], ph[nt][1]);
+                mma_bf16(o[nt][4 * c + t], f0, f1, f2, f3, pl[nt][0], pl[nt][1]);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; i++)
+            for (int gk = 0; gk < 8; gk++) {
+              const int j = j0 + 8 * i + gk;
+              if (j >= rq.m) break;
+              const uint16_t* p = vn + j * a.kv_stride;
+#pragma unroll
+              for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                  const float w = __shfl_sync(0xffffffffu, so[nt][2 * i + e], 4 * gk + q);
+                  if ((s_anc[nt * 8 + 2 * q + e] >> j & 1) && w != 0.f)
+#pragma unroll
+                    for (int t = 0; t < KK; t++) {
+                      o[nt][t][e] = fmaf(w, bf2f(p[2 * t]), o[nt][t][e]);
+                      o[nt][t][2 + e] = fmaf(w, bf2f(p[2 * t + 1]), o[nt][t][2 + e]);
+                    }
+                }
+            }
+        }
+      }
+
     int k = 0;
-    for (int u = ua + warp; u < ue; u += W) {
+    for (int u = first_record(); u < ub; u += W) {
       const int stage = used & 1;
       const uint8_t* st = ring + stage * S::kStage;
       if (!mbar_wait_or_abort(&bar[stage], (used >> 1) & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(30));
@@ -400,6 +534,10 @@ __global__ void __launch_bounds__(W * 32, 1) k_kv4_attn(const __grid_constant__ 
         for (int i = 0; i < 2; i++)
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) sc[i][nt][0] = sc[i][nt][1] = sc[i][nt][2] = sc[i][nt][3] = 0.f;
+        float s2[2][4];  // a second chain of sums, for one tile of rows alone
+        if (NT == 1)
+#pragma unroll
+          for (int e = 0; e < 4; e++) s2[0][e] = s2[1][e] = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 32; j++) {
           uint32_t f[4][4];
@@ -415,13 +553,16 @@ __global__ void __launch_bounds__(W * 32, 1) k_kv4_attn(const __grid_constant__ 
             const uint2 b0 = s_q[(nt * KK + 2 * j) * 32 + lane], b1 = s_q[(nt * KK + 2 * j + 1) * 32 + lane];
             mma_f16(sc[0][nt], f[0][0], f[1][0], f[0][1], f[1][1], b0.x, b0.y);
             mma_f16(sc[1][nt], f[2][0], f[3][0], f[2][1], f[3][1], b0.x, b0.y);
-            mma_f16(sc[0][nt], f[0][2], f[1][2], f[0][3], f[1][3], b1.x, b1.y);
-            mma_f16(sc[1][nt], f[2][2], f[3][2], f[2][3], f[3][3], b1.x, b1.y);
+            mma_f16(NT == 1 ? s2[0] : sc[0][nt], f[0][2], f[1][2], f[0][3], f[1][3], b1.x, b1.y);
+            mma_f16(NT == 1 ? s2[1] : sc[1][nt], f[2][2], f[3][2], f[2][3], f[3][3], b1.x, b1.y);
           }
         }
+        if (NT == 1)
+#pragma unroll
+          for (int e = 0; e < 4; e++) sc[0][0][e] += s2[0][e], sc[1][0][e] += s2[1][e];
       }
       // slots of this record that the request holds
-      const int lim = s_ok[warp * 2 + stage] ? rq.ctx - (rq.g0 + u) * kKvGroup : 0;
+      const int lim = s_ok[warp * 2 + stage] ? rq.ctx - (rq.g0 + u - rq.no) * kKvGroup : 0;
       float vs[4], vm[4];
       float top[NT][2];
       uint32_t vb = 0;
@@ -526,7 +667,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_kv4_attn(const __grid_constant__ 
       __syncwarp();
       used++;
       k++;
-      if (u + 2 * W < ue) {
+      if (u + 2 * W < ub) {
         if (k == 31) {  // the lanes' addresses run out
           look_up(u + 2 * W);
           k = -1;
@@ -535,145 +676,14 @@ __global__ void __launch_bounds__(W * 32, 1) k_kv4_attn(const __grid_constant__ 
       }
     }
 
-    // the rows' own keys, in runs of 32
-    for (int u = max(ua, rq.ng) + (warp + W - (max(ua, rq.ng) - ua) % W) % W; u < ub; u += W) {
-      const int j0 = (u - rq.ng) * 32;
-      if (!a.k_new || j0 >= rq.m) break;  // the unit of a request that sees nothing
-      const uint16_t* kn = a.k_new + (int64_t)rq.n0 * a.kv_stride + h * D + q * (D / 4);
-#pragma unroll
-      for (int i = 0; i < 2; i++) {
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++) sc[i][nt][0] = sc[i][nt][1] = sc[i][nt][2] = sc[i][nt][3] = 0.f;
-        const int ka = j0 + 16 * i + g, kb = ka + 8;
-        const uint16_t* pa = kn + (ka < rq.m ? ka : 0) * a.kv_stride;
-        const uint16_t* pb = kn + (kb < rq.m ? kb : 0) * a.kv_stride;
-#pragma unroll
-        for (int j = 0; j < D / 32; j++) {
-          const uint4 xa = *reinterpret_cast<const uint4*>(pa + 8 * j), xb = *reinterpret_cast<const uint4*>(pb + 8 * j);
-#pragma unroll
-          for (int nt = 0; nt < NT; nt++) {
-            const uint2 b0 = s_qb[(nt * KK + 2 * j) * 32 + lane], b1 = s_qb[(nt * KK + 2 * j + 1) * 32 + lane];
-            mma_bf16(sc[i][nt], prmt(xa.x, xa.z, 0x5410), prmt(xb.x, xb.z, 0x5410), prmt(xa.x, xa.z, 0x7632),
-                     prmt(xb.x, xb.z, 0x7632), b0.x, b0.y);
-            mma_bf16(sc[i][nt], prmt(xa.y, xa.w, 0x5410), prmt(xb.y, xb.w, 0x5410), prmt(xa.y, xa.w, 0x7632),
-                     prmt(xb.y, xb.w, 0x7632), b1.x, b1.y);
-          }
-        }
-      }
-      float top[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; nt++) top[nt][0] = top[nt][1] = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int j = j0 + 8 * i + g;
-        const int kp = BIAS && j < rq.m ? (a.row_pos ? a.row_pos[rq.n0 + j] : rq.ctx + j) : 0;
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-          for (int e = 0; e < 2; e++) {
-            const int row = nt * 8 + 2 * q + e;
-            float& x = sc[i >> 1][nt][2 * (i & 1) + e];
-            float t = x * sc2;
-            if (BIAS) t = kv4_score(a.s, t, s_slope[row], s_pos[row], kp, start) * kLog2e;
-            x = j < rq.m && (s_anc[row] >> j & 1) ? t : -INFINITY;
-            top[nt][e] = fmaxf(top[nt][e], x);
-          }
-      }
-      grow(top);
-      const float wup = vup * (1.f / 512.f);
-      uint32_t ph[NT][2][2], pl[NT][2][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          float w[2];
-#pragma unroll
-          for (int e = 0; e < 2; e++) {
-            float& x = sc[i >> 1][nt][2 * (i & 1) + e];
-            const float p = ex2(x - (mx[nt][e] == -INFINITY ? 0.f : mx[nt][e]));
-            l[nt][e] += p;
-            x = w[e] = p * wup;
-          }
-          const uint32_t hi = pack_bf16x2(w[0], w[1]);
-          const uint32_t lo = pack_bf16x2(w[0] - __uint_as_float(hi << 16), w[1] - __uint_as_float(hi & 0xFFFF0000u));
-          ph[nt][i >> 1][i & 1] = transpose8(hi);
-          pl[nt][i >> 1][i & 1] = transpose8(lo);
-        }
-      // A product with a weight of 0 would carry a NaN or an infinity of a
-      // row's values to rows that do not see it: such a run is added key by key
-      const uint16_t* vn = a.v_new + (int64_t)rq.n0 * a.kv_stride + h * D + g * (D / 8);
-      uint32_t odd = 0;
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        const int kx = j0 + 8 * (i >> 1) + 2 * q + (i & 1);
-        const uint16_t* p = vn + (kx < rq.m ? kx : 0) * a.kv_stride;
-#pragma unroll
-        for (int c = 0; c < D / 64; c++) {
-          const uint4 x = *reinterpret_cast<const uint4*>(p + 8 * c);
-          odd |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
-                 ((x.z & 0x7F807F80u) + 0x00800080u) | ((x.w & 0x7F807F80u) + 0x00800080u);
-        }
-      }
-      if (!__any_sync(0xffffffffu, (odd & 0x80008000u) != 0)) {
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-          const uint16_t* p[4];
-#pragma unroll
-          for (int b = 0; b < 4; b++) {
-            const int kx = j0 + 16 * i + 8 * (b >> 1) + 2 * q + (b & 1);
-            p[b] = vn + (kx < rq.m ? kx : 0) * a.kv_stride;
-          }
-#pragma unroll
-          for (int c = 0; c < D / 64; c++) {
-            uint32_t x[4][4];
-#pragma unroll
-            for (int b = 0; b < 4; b++) {
-              const uint4 v = *reinterpret_cast<const uint4*>(p[b] + 8 * c);
-              x[b][0] = v.x, x[b][1] = v.y, x[b][2] = v.z, x[b][3] = v.w;
-            }
-#pragma unroll
-            for (int t = 0; t < 4; t++) {
-              const uint32_t f0 = prmt(x[0][t], x[1][t], 0x5410), f1 = prmt(x[0][t], x[1][t], 0x7632),
-                             f2 = prmt(x[2][t], x[3][t], 0x5410), f3 = prmt(x[2][t], x[3][t], 0x7632);
-#pragma unroll
-              for (int nt = 0; nt < NT; nt++) {
-                mma_bf16(o[nt][4 * c + t], f0, f1, f2, f3, ph[nt][i][0], ph[nt][i][1]);
-                mma_bf16(o[nt][4 * c + t], f0, f1, f2, f3, pl[nt][i][0], pl[nt][i][1]);
-              }
-            }
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-          for (int gk = 0; gk < 8; gk++) {
-            const int j = j0 + 8 * i + gk;
-            if (j >= rq.m) break;
-            const uint16_t* p = vn + j * a.kv_stride;
-#pragma unroll
-            for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-              for (int e = 0; e < 2; e++) {
-                const float w = __shfl_sync(0xffffffffu, sc[i >> 1][nt][2 * (i & 1) + e], 4 * gk + q);
-                if ((s_anc[nt * 8 + 2 * q + e] >> j & 1) && w != 0.f)
-#pragma unroll
-                  for (int t = 0; t < KK; t++) {
-                    o[nt][t][e] = fmaf(w, bf2f(p[2 * t]), o[nt][t][e]);
-                    o[nt][t][2 + e] = fmaf(w, bf2f(p[2 * t + 1]), o[nt][t][2 + e]);
-                  }
-              }
-          }
-      }
-    }
-
     // the next segment: its first records are fetched while this one is joined
     const bool whole = ua == 0 && ub == rq.nu;
     // a part's slot: 2 c for the first segment of CTA c, 2 c + 1 for its last
-    const int64_t slot = 2ll * blockIdx.x + (seg + ua > s_u0 ? 1 : 0);
-    const long long this_seg = seg;
+    const int slot = 2 * blockIdx.x + (seg + ua > u0 ? 1 : 0);
+    const int this_seg = seg;
     const Kv4Req tq = rq;
     seg += rq.nu;
-    const bool more = seg < s_u1;
+    const bool more = seg < u1;
     if (more) {
       if (++s == a.c.hkv * rq.nc) {
         s = 0;
@@ -681,7 +691,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_kv4_attn(const __grid_constant__ 
         while (rq.nc == 0);
       }
       ua = 0;
-      ub = (int)min((long long)rq.nu, s_u1 - seg);
+      ub = min(rq.nu, u1 - seg);
       begin();
     }
 
@@ -701,96 +711,107 @@ __global__ void __launch_bounds__(W * 32, 1) k_kv4_attn(const __grid_constant__ 
           s_m[warp * RT + row] = mx[nt][e];
           s_l[warp * RT + row] = l[nt][e];
         }
-        float* dst = s_o + (warp * RT + row) * D + g * (D / 8);
+        // float pairs [dims 2t, 2t + 1 of lane group g]: 8 t + g, rows 4 banks
+        // of pairs apart for the lanes that write together
+        float2* dst = reinterpret_cast<float2*>(s_o) + (warp * RT + row) * S::kPairs + g;
 #pragma unroll
         for (int t = 0; t < KK; t++)
-          *reinterpret_cast<float2*>(dst + 2 * t) =
-              make_float2(fmaf(o[nt][t][e], down, mv[nt][e]), fmaf(o[nt][t][2 + e], down, mv[nt][e]));
+          dst[8 * t] = make_float2(fmaf(o[nt][t][e], down, mv[nt][e]), fmaf(o[nt][t][2 + e], down, mv[nt][e]));
       }
     __syncthreads();
-    float* part = a.part + slot * (RT * (D + 2));
+    float* part = a.part + (int64_t)slot * (RT * (D + 2));  // [RT][D/2] pairs, then [RT] (max, sum)
+    auto row_out = [&](int row) {  // (row, query head) of the outputs
+      const int rho = rc * RT + row, gq = rho / tq.m;
+      return (int64_t)(tq.n0 + rho - gq * tq.m) * a.hq + h * a.G + gq;
+    };
     if (tid < rows) {
       float M = -INFINITY, L = 0.f;
+#pragma unroll
       for (int w = 0; w < W; w++) M = fmaxf(M, s_m[w * RT + tid]);
       const float Ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
       for (int w = 0; w < W; w++) {
-        const float f = ex2(s_m[w * RT + tid] - Ms);
-        // a warp whose every score was NaN has no maximum, but a sum
-        L += s_l[w * RT + tid] == 0.f ? 0.f : f * s_l[w * RT + tid];
+        const float f = ex2(s_m[w * RT + tid] - Ms);  // 0 for a warp that saw no key; 0 x NaN for one that saw only NaN
+        L += f * s_l[w * RT + tid];
         s_m[w * RT + tid] = f;
       }
-      s_L[tid] = L;
+      s_L[tid] = L == 0.f ? 0.f : 1.f / L;
       if (whole) {
-        const int rho = rc * RT + tid;
-        if (a.lse)
-          a.lse[(int64_t)(tq.n0 + rho % tq.m) * a.hq + h * a.G + rho / tq.m] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
+        if (a.lse) a.lse[row_out(tid)] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
       } else {
-        __stcg(part + RT * D + 2 * tid, M);
-        __stcg(part + RT * D + 2 * tid + 1, L);
+        __stcg(reinterpret_cast<float2*>(part + RT * D) + tid, make_float2(M, L));
       }
     }
     __syncthreads();
-    for (int i = tid; i < rows * (D / 4); i += W * 32) {
-      const int row = i / (D / 4), d4 = i % (D / 4);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+    for (int i = tid; i < rows * (D / 2); i += W * 32) {
+      const int row = i / (D / 2), x = i % (D / 2);
+      float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
       for (int w = 0; w < W; w++) {
         const float f = s_m[w * RT + row];
-        const float4 v = *reinterpret_cast<const float4*>(s_o + (w * RT + row) * D + 4 * d4);
+        const float2 v = reinterpret_cast<const float2*>(s_o)[(w * RT + row) * S::kPairs + x];
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
       }
       if (whole) {
-        const float L = s_L[row], inv = L == 0.f ? 0.f : 1.f / L;
-        const int rho = rc * RT + row;
-        uint16_t* dst = a.out + ((int64_t)(tq.n0 + rho % tq.m) * a.hq + h * a.G + rho / tq.m) * D + 4 * d4;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        const float inv = s_L[row];
+        *reinterpret_cast<uint32_t*>(a.out + row_out(row) * D + (x & 7) * (D / 8) + (x >> 3) * 2) =
+            pack_bf16x2(acc.x * inv, acc.y * inv);
       } else {
-        __stcg(reinterpret_cast<float4*>(part + row * D + 4 * d4), acc);
+        __stcg(reinterpret_cast<float2*>(part) + i, acc);
       }
     }
     if (!whole) {
       // the last of the segment's CTAs joins their parts
-      const long long U = s_U, C = s_C;
-      const int c0 = (int)(((this_seg + 1) * C - 1) / U), c1 = (int)(((this_seg + tq.nu) * C - 1) / U);
+      const int each = s_each, extra = s_more, big = extra * (each + 1);
+      auto cta_of = [&](int u) { return u < big ? u / (each + 1) : extra + (u - big) / each; };
+      const int c0 = cta_of(this_seg), n = cta_of(this_seg + tq.nu - 1) - c0 + 1;
       __threadfence();
       __syncthreads();
       if (tid == 0) {
         const int old = atomic_add_acq_rel(a.tickets + c0, 1);
-        s_last = old == c1 - c0;
+        s_last = old == n - 1;
         if (s_last) a.tickets[c0] = 0;
       }
       __syncthreads();
       if (s_last) {
-        const int64_t slot0 = 2ll * c0 + ((long long)c0 * U / C < this_seg ? 1 : 0);
-        auto part_of = [&](int c) { return a.part + (c == c0 ? slot0 : 2ll * c) * (RT * (D + 2)); };
-        for (int i = tid; i < rows * (D / 4); i += W * 32) {
-          const int row = i / (D / 4), d4 = i % (D / 4);
-          float M = -INFINITY;
-          for (int c = c0; c <= c1; c++) M = fmaxf(M, __ldcg(part_of(c) + RT * D + 2 * row));
-          const float Ms = M == -INFINITY ? 0.f : M;
-          float L = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int c = c0; c <= c1; c++) {
-            const float* pc = part_of(c);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pc + RT * D + 2 * row));
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(pc + row * D + 4 * d4));
-            const float f = ex2(ml.x - Ms);
-            L = fmaf(f, ml.y, L);
-            acc.x = fmaf(f, v.x, acc.x);
-            acc.y = fmaf(f, v.y, acc.y);
-            acc.z = fmaf(f, v.z, acc.z);
-            acc.w = fmaf(f, v.w, acc.w);
+        // c0's part is its last segment's unless the segment begins its share
+        const int slot0 = 2 * c0 + (c0 * each + min(c0, extra) < this_seg ? 1 : 0);
+        auto part_of = [&](int c) { return a.part + (int64_t)(c == 0 ? slot0 : 2 * (c0 + c)) * (RT * (D + 2)); };
+        for (int i = tid; i < rows * (D / 2); i += W * 32) {
+          const int row = i / (D / 2), x = i % (D / 2);
+          float M = -INFINITY, L = 0.f;
+          float2 acc = make_float2(0.f, 0.f);
+          for (int c = 0; c < n; c += 8) {  // eight parts in flight
+            float2 ml[8], v[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+              const float* pc = part_of(min(c + k, n - 1));
+              ml[k] = __ldcg(reinterpret_cast<const float2*>(pc + RT * D) + row);
+              v[k] = __ldcg(reinterpret_cast<const float2*>(pc) + i);
+            }
+            float Mn = M;
+#pragma unroll
+            for (int k = 0; k < 8; k++) Mn = fmaxf(Mn, ml[k].x);
+            const float Ms = Mn == -INFINITY ? 0.f : Mn, al = ex2(M - Ms);
+            M = Mn;
+            L *= al;
+            acc.x *= al;
+            acc.y *= al;
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+              if (c + k < n) {
+                const float f = ex2(ml[k].x - Ms);
+                L = fmaf(f, ml[k].y, L);
+                acc.x = fmaf(f, v[k].x, acc.x);
+                acc.y = fmaf(f, v[k].y, acc.y);
+              }
           }
           const float inv = L == 0.f ? 0.f : 1.f / L;
-          const int rho = rc * RT + row;
-          const int64_t at = (int64_t)(tq.n0 + rho % tq.m) * a.hq + h * a.G + rho / tq.m;
-          *reinterpret_cast<uint2*>(a.out + at * D + 4 * d4) =
-              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-          if (d4 == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
+          const int64_t at = row_out(row);
+          *reinterpret_cast<uint32_t*>(a.out + at * D + (x & 7) * (D / 8) + (x >> 3) * 2) =
+              pack_bf16x2(acc.x * inv, acc.y * inv);
+          if (x == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
         }
       }
     }
@@ -864,8 +885,11 @@ template <int D, int NT, int W>
 static int launch_attn_tile(const Kv4AttnArgs& a, int64_t units, bool bias, cudaStream_t st) {
   auto kern = bias ? k_kv4_attn<D, NT, W, true> : k_kv4_attn<D, NT, W, false>;
   constexpr int smem = AttnShape<D, NT, W>::smem;
-  SD_CK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>({(int64_t)num_sms(), kMaxCtas, units}));
+  static const cudaError_t set[2] = {
+      cudaFuncSetAttribute(k_kv4_attn<D, NT, W, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+      cudaFuncSetAttribute(k_kv4_attn<D, NT, W, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)};
+  SD_CK(set[bias]);
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>({(NT <= 2 ? 2ll : 1ll) * num_sms(), kMaxCtas, units}));
   kern<<<(unsigned)grid, W * 32, smem, st>>>(a);
   SD_CK(cudaGetLastError());
   return SD_OK;
@@ -875,8 +899,8 @@ static int launch_attn_tile(const Kv4AttnArgs& a, int64_t units, bool bias, cuda
 // the tile leaves in registers and shared memory.
 template <int D>
 static int launch_attn(const Kv4AttnArgs& a, int rows, int64_t units, bool bias, cudaStream_t st) {
-  if (rows <= 8) return launch_attn_tile<D, 1, 16>(a, units, bias, st);
-  if (rows <= 16) return launch_attn_tile<D, 2, 12>(a, units, bias, st);
+  if (rows <= 8) return launch_attn_tile<D, 1, 8>(a, units, bias, st);
+  if (rows <= 16) return launch_attn_tile<D, 2, 6>(a, units, bias, st);
   if (rows <= 24) return launch_attn_tile<D, 3, 8>(a, units, bias, st);
   return launch_attn_tile<D, 4, 8>(a, units, bias, st);
 }
@@ -916,7 +940,7 @@ extern "C" size_t sd_kv4_attn_workspace(int32_t R, int32_t rows, int32_t n_q_hea
   if (R < 1 || rows < 0 || n_kv_heads < 1 || n_q_heads < n_kv_heads || n_q_heads % n_kv_heads ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  return kTicketBytes + (size_t)2 * num_sms() * 32 * (head_dim + 2) * sizeof(float);
+  return kTicketBytes + (size_t)4 * num_sms() * 32 * (head_dim + 2) * sizeof(float);
 }
 
 extern "C" int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride, int32_t n_q_heads, const int32_t* cu,
@@ -956,6 +980,7 @@ extern "C" int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride,
   most *= a.G;
   const int64_t ctx = max_ctx > 0 ? std::min<int64_t>(max_ctx, a.c.cap) : a.c.cap;
   const int64_t units = (int64_t)R * c->n_kv_heads * ((most + 31) / 32) * ((ctx + 31) / 32 + 2);
+  if (units > 0x7FFFFFFF) return kv4_bad(SD_ERR_UNSUPPORTED, who, "more than 2^31 runs of 32 keys");
   const bool bias = a.s.cap > 0.f || a.s.slopes || a.s.window > 0 || a.s.start;
   return c->head_dim == 128 ? launch_attn<128>(a, most, units, bias, (cudaStream_t)stream)
                             : launch_attn<64>(a, most, units, bias, (cudaStream_t)stream);

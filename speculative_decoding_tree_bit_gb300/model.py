@@ -629,6 +629,7 @@ class RequestRows:
             raise ValueError("cu must be [R+1] offsets that start at 0 and do not decrease")
         self.R, self.n = self.cu.size - 1, int(self.cu[-1])
         self.cu_dev = _i32(self.cu, device)
+        self.cu_ptr, self.cu_host_ptr = self.cu_dev.data_ptr(), self.cu.ctypes.data
 
 
 class KV4Score:
@@ -642,24 +643,33 @@ class KV4Score:
             raise ValueError("start must be contiguous int32")
         self.slopes, self.start = slopes, start
         self.args = KV4ScoreArgs(float(scale), float(softcap), _ptr(slopes), int(window), _ptr(start))
+        self.ref = ctypes.byref(self.args)
 
 
-def _rows16(t, heads, dim, what):
-    """A bf16 tensor (bfloat16 or int16 bits) [rows][heads][dim] whose rows
-    may be strided: (pointer, row stride in elements)."""
-    if t.element_size() != 2 or t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
-        raise ValueError(f"{what} must be 16-bit [rows][{heads}][{dim}], got {tuple(t.shape)} {t.dtype}")
-    if t.dtype == torch.float16:
-        raise ValueError(f"{what} must hold bf16")
-    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+_BITS16 = (torch.bfloat16, torch.int16)
+
+
+def _rows16(t, n, heads, dim, what):
+    """The row stride in elements of a bf16 tensor (bfloat16 or int16 bits)
+    [n][heads][dim] whose rows may be strided; n None: any."""
+    shape = t.shape
+    if t.dtype not in _BITS16 or len(shape) != 3 or shape[1] != heads or shape[2] != dim or (n is not None and
+                                                                                           shape[0] != n):
+        raise ValueError(f"{what} must be bf16 [{'rows' if n is None else n}][{heads}][{dim}], got {tuple(shape)} "
+                         f"{t.dtype}")
+    if t.is_contiguous():
+        return heads * dim
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != dim):
         raise ValueError(f"{what}: the heads of a row must lie together")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else heads * dim)
+    return st[0] if shape[0] > 1 else heads * dim
 
 
-def _ints(t, n, what, dtype=torch.int32):
+def _entries(t, n, what, dtype=torch.int32):
+    """Pointer of an optional contiguous tensor of at least n entries."""
     if t is None:
-        return 0
-    if t.dtype != dtype or not t.is_contiguous() or t.numel() < n:
+        return None
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous {dtype} of at least {n} entries")
     return t.data_ptr()
 
@@ -699,7 +709,15 @@ class KV4Cache:
         s.n_pages, s.page_size, s.n_kv_heads, s.head_dim = (self.n_pages, self.page_size, self.n_kv_heads,
                                                             self.head_dim)
         s.page_table, s.max_pages, s.ctx_len = self.page_table.data_ptr(), self.max_pages, self.ctx_len.data_ptr()
-        self._s = s
+        self._s, self._ref = s, ctypes.byref(s)
+        self._status_ptr, self._zero_ptr = self._status.data_ptr(), self._zero.data_ptr()
+        self._index = self.blocks.device.index
+        self._lib = lib()
+
+    def _stream(self, stream):
+        if stream is not None or self._index is None:
+            return stream_ptr(stream)
+        return torch._C._cuda_getCurrentRawStream(self._index)
 
     def status(self) -> int:
         """The device status of the calls so far (synchronises), then cleared."""
@@ -710,51 +728,64 @@ class KV4Cache:
     def nbytes(self) -> int:
         return self.blocks.numel() + 8 * self.pos.numel()
 
-    def _workspace(self, kind, n):
-        """A workspace of at least n bytes, zeroed when made."""
-        if kind not in self._ws or self._ws[kind].numel() < n:
-            self._ws[kind] = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.device)
-        return self._ws[kind]
+    def _workspace(self, kind, size, *args):
+        """The workspace of `size(*args)` bytes, zeroed when made."""
+        key = (kind, args)
+        ws = self._ws.get(key)
+        if ws is None:
+            n = int(size(*args))
+            for k, (t, _, _) in self._ws.items():
+                if k[0] == kind and t.numel() >= n:  # one buffer serves every call it is large enough for
+                    break
+            else:
+                t = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.device)
+            ws = self._ws[key] = (t, t.data_ptr(), t.numel())
+        return ws
 
     def _at(self, at):
-        if at is None or isinstance(at, torch.Tensor):
-            return _ints(at, self.R, "at")
+        if at is None:
+            return None
+        if isinstance(at, torch.Tensor):
+            return _entries(at, self.R, "at")
         if at != 0:
             raise ValueError("at must be an int32 device tensor [R], or 0")
-        return self._zero.data_ptr()
+        return self._zero_ptr
 
     def _rows(self, rows):
         if rows.R != self.R:
             raise ValueError(f"rows of {rows.R} requests on a cache of {self.R}")
-        return rows
+
+    def _heads(self, q):
+        hq = q.shape[1] if q.dim() == 3 else 0
+        if hq == 0 or hq % self.n_kv_heads:
+            raise ValueError("q must be [rows][n_q_heads][head_dim], n_q_heads a multiple of n_kv_heads")
+        return hq
 
     def append(self, k, v, rows: RequestRows, pos=None, at=None, src=None, count=None, stream=None):
         """Store rows (sd_kv4_append).  k, v: [n][n_kv_heads][head_dim], rows
         may be strided; pos int32 [rows]; at: first slot per request (int32
         [R] or 0; default ctx_len); src int32 [rows]: the row of k and v that
         each entry takes; count int32 [R]: entries of each request stored."""
-        rows = self._rows(rows)
-        kp, ks = _rows16(k, self.n_kv_heads, self.head_dim, "k")
-        vp_, vs = _rows16(v, self.n_kv_heads, self.head_dim, "v")
-        if k.shape[0] != v.shape[0] or (k.shape[0] > 1 and ks != vs):
-            raise ValueError("k and v must have the same rows and row stride")
-        check(lib().sd_kv4_append(ctypes.byref(self._s), kp, vp_, ks, k.shape[0], rows.cu_dev.data_ptr(),
-                                  rows.cu.ctypes.data, rows.R, _ints(src, rows.n, "src"),
-                                  _ints(count, rows.R, "count"), _ints(pos, rows.n, "pos"), self._at(at),
-                                  self._status.data_ptr(), stream_ptr(stream)))
+        self._rows(rows)
+        n = k.shape[0]
+        ks = _rows16(k, None, self.n_kv_heads, self.head_dim, "k")
+        if _rows16(v, n, self.n_kv_heads, self.head_dim, "v") != ks:
+            raise ValueError("k and v must have one row stride")
+        check(self._lib.sd_kv4_append(self._ref, k.data_ptr(), v.data_ptr(), ks, n, rows.cu_ptr, rows.cu_host_ptr,
+                                      rows.R, _entries(src, rows.n, "src"), _entries(count, rows.R, "count"),
+                                      _entries(pos, rows.n, "pos"), self._at(at), self._status_ptr,
+                                      self._stream(stream)))
 
     def read(self, rows: RequestRows, at=0, dtype=torch.bfloat16, stream=None):
         """The values held: (k, v) bf16 [rows][n_kv_heads][head_dim], row i
         of request r from slot at[r] + i (sd_kv4_read)."""
-        rows = self._rows(rows)
-        shape = (rows.n, self.n_kv_heads, self.head_dim)
-        k = torch.empty(shape, dtype=dtype, device=self.device)
-        v = torch.empty(shape, dtype=dtype, device=self.device)
-        if k.element_size() != 2:
+        self._rows(rows)
+        if dtype not in _BITS16:
             raise ValueError("dtype must be bfloat16, or int16 for its bits")
-        check(lib().sd_kv4_read(ctypes.byref(self._s), rows.cu_dev.data_ptr(), rows.cu.ctypes.data, rows.R,
-                                self._at(at), k.data_ptr(), v.data_ptr(), self._status.data_ptr(),
-                                stream_ptr(stream)))
+        k = torch.empty(rows.n, self.n_kv_heads, self.head_dim, dtype=dtype, device=self.device)
+        v = torch.empty_like(k)
+        check(self._lib.sd_kv4_read(self._ref, rows.cu_ptr, rows.cu_host_ptr, rows.R, self._at(at), k.data_ptr(),
+                                    v.data_ptr(), self._status_ptr, self._stream(stream)))
         return k, v
 
     def attend(self, q, rows: RequestRows, k=None, v=None, anc=None, pos=None, score: KV4Score | None = None,
@@ -764,34 +795,31 @@ class KV4Cache:
         [head_dim] (or both None), anc int64 ancestor bits [n] (sd_tree_info;
         None: causal), pos int32 [n].  Returns (out like q, lse float32
         [n][n_q_heads])."""
-        rows = self._rows(rows)
-        if q.dim() != 3 or q.shape[0] != rows.n or q.shape[1] % self.n_kv_heads:
-            raise ValueError("q must be [rows][n_q_heads][head_dim], n_q_heads a multiple of n_kv_heads")
-        hq = q.shape[1]
-        qp, qs = _rows16(q, hq, self.head_dim, "q")
-        kp = vp_ = ks = 0
-        if (k is None) != (v is None):
-            raise ValueError("k and v go together")
-        if k is not None:
-            kp, ks = _rows16(k, self.n_kv_heads, self.head_dim, "k")
-            vp_, vs = _rows16(v, self.n_kv_heads, self.head_dim, "v")
-            if k.shape[0] != rows.n or v.shape[0] != rows.n or (rows.n > 1 and ks != vs):
-                raise ValueError("k and v must have the rows of q and one row stride")
+        self._rows(rows)
+        n, hq, D = rows.n, self._heads(q), self.head_dim
+        qs = _rows16(q, n, hq, D, "q")
+        kp = vp_ = None
+        ks = 0
+        if k is not None or v is not None:
+            if k is None or v is None:
+                raise ValueError("k and v go together")
+            ks = _rows16(k, n, self.n_kv_heads, D, "k")
+            if _rows16(v, n, self.n_kv_heads, D, "v") != ks:
+                raise ValueError("k and v must have one row stride")
+            kp, vp_ = k.data_ptr(), v.data_ptr()
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif out.shape != q.shape or out.element_size() != 2 or not out.is_contiguous():
-            raise ValueError("out must be contiguous and of q's shape")
+            out = torch.empty_like(q) if q.is_contiguous() else torch.empty(n, hq, D, dtype=q.dtype, device=q.device)
+        elif out.shape != q.shape or out.dtype not in _BITS16 or not out.is_contiguous():
+            raise ValueError("out must be contiguous bf16 of q's shape")
         if lse is None:
-            lse = torch.empty((rows.n, hq), dtype=torch.float32, device=q.device)
-        elif lse.dtype != torch.float32 or not lse.is_contiguous() or tuple(lse.shape) != (rows.n, hq):
+            lse = torch.empty(n, hq, dtype=torch.float32, device=q.device)
+        elif lse.dtype is not torch.float32 or lse.shape != (n, hq) or not lse.is_contiguous():
             raise ValueError("lse must be contiguous float32 [rows][n_q_heads]")
-        ws = self._workspace("attn", int(lib().sd_kv4_attn_workspace(rows.R, rows.n, hq, self.n_kv_heads,
-                                                                     self.head_dim)))
-        check(lib().sd_kv4_attn(ctypes.byref(self._s), qp, qs, hq, rows.cu_dev.data_ptr(), rows.cu.ctypes.data, rows.R,
-                                kp, vp_, ks, _ints(anc, rows.n, "anc", torch.int64), _ints(pos, rows.n, "pos"),
-                                ctypes.byref(score.args) if score is not None else None, int(max_ctx), out.data_ptr(),
-                                lse.data_ptr(), ws.data_ptr(), ws.numel(), self._status.data_ptr(),
-                                stream_ptr(stream)))
+        _, ws, ws_n = self._workspace("attn", self._lib.sd_kv4_attn_workspace, self.R, n, hq, self.n_kv_heads, D)
+        check(self._lib.sd_kv4_attn(self._ref, q.data_ptr(), qs, hq, rows.cu_ptr, rows.cu_host_ptr, self.R, kp, vp_, ks,
+                                    _entries(anc, n, "anc", torch.int64), _entries(pos, n, "pos"),
+                                    None if score is None else score.ref, max_ctx, out.data_ptr(), lse.data_ptr(), ws,
+                                    ws_n, self._status_ptr, self._stream(stream)))
         return out, lse
 
     def observe(self, q, lse, rows: RequestRows, pos=None, row_weight=None, score: KV4Score | None = None,
@@ -799,20 +827,18 @@ class KV4Cache:
         """decay * weight + the weight the rows give to each cached key
         (sd_kv4_observe), into out (default: self.weight itself); lse as
         attend returned it, row_weight float32 [n].  Returns out."""
-        rows = self._rows(rows)
-        if q.dim() != 3 or q.shape[0] != rows.n or q.shape[1] % self.n_kv_heads:
-            raise ValueError("q must be [rows][n_q_heads][head_dim], n_q_heads a multiple of n_kv_heads")
-        hq = q.shape[1]
-        qp, qs = _rows16(q, hq, self.head_dim, "q")
+        self._rows(rows)
+        n, hq = rows.n, self._heads(q)
+        qs = _rows16(q, n, hq, self.head_dim, "q")
         if out is None:
             out = self.weight
-        elif out.shape != self.weight.shape or out.dtype != torch.float32 or not out.is_contiguous():
+        elif out.dtype is not torch.float32 or out.shape != self.weight.shape or not out.is_contiguous():
             raise ValueError("out must be contiguous float32 of the shape of weight")
-        check(lib().sd_kv4_observe(ctypes.byref(self._s), qp, qs, hq, _ints(lse, rows.n * hq, "lse", torch.float32),
-                                   rows.cu_dev.data_ptr(), rows.cu.ctypes.data, rows.R, _ints(pos, rows.n, "pos"),
-                                   _ints(row_weight, rows.n, "row_weight", torch.float32),
-                                   ctypes.byref(score.args) if score is not None else None, int(max_ctx), float(decay),
-                                   out.data_ptr(), self._status.data_ptr(), stream_ptr(stream)))
+        check(self._lib.sd_kv4_observe(self._ref, q.data_ptr(), qs, hq, _entries(lse, n * hq, "lse", torch.float32),
+                                       rows.cu_ptr, rows.cu_host_ptr, self.R, _entries(pos, n, "pos"),
+                                       _entries(row_weight, n, "row_weight", torch.float32),
+                                       None if score is None else score.ref, max_ctx, decay, out.data_ptr(),
+                                       self._status_ptr, self._stream(stream)))
         return out
 
     def evict(self, dst: "KV4Cache", budget: int, recent: int = 0, sinks: int = 0, stream=None) -> torch.Tensor:
@@ -823,8 +849,9 @@ class KV4Cache:
         dst.ctx_len are unspecified)."""
         if dst is self or dst.R != self.R:
             raise ValueError("dst must be another cache of the same requests")
-        n = int(lib().sd_kv4_evict_workspace(self.R, self.n_kv_heads, int(budget)))
-        ws = self._workspace("evict", n)
-        check(lib().sd_kv4_evict(ctypes.byref(self._s), ctypes.byref(dst._s), self.R, int(budget), int(recent),
-                                 int(sinks), ws.data_ptr(), ws.numel(), self._status.data_ptr(), stream_ptr(stream)))
-        return ws[:n].view(torch.int32).view(self.R, self.n_kv_heads, int(budget))
+        budget = int(budget)
+        ws, ws_ptr, ws_n = self._workspace("evict", self._lib.sd_kv4_evict_workspace, self.R, self.n_kv_heads, budget)
+        check(self._lib.sd_kv4_evict(self._ref, dst._ref, self.R, budget, recent, sinks, ws_ptr, ws_n,
+                                     self._status_ptr, self._stream(stream)))
+        n = self.R * self.n_kv_heads * budget * 4
+        return ws[:n].view(torch.int32).view(self.R, self.n_kv_heads, budget)

@@ -140,13 +140,18 @@ __device__ __forceinline__ Kv4Req kv4_req(const Kv4AttnArgs& a, int r) {
 // segments' units are dealt evenly over the CTAs, whatever the requests'
 // lengths; two CTAs an SM, so that one works while the other joins.
 
+// A segment to join at a CTA's end: n parts (0: none) from CTA c0 on.
+struct Kv4Join {
+  int seg, n, c0, n0, m, h, rc;
+};
+
 template <int D, int NT, int W>
 struct AttnShape {
   static constexpr int RT = 8 * NT;
   static constexpr int kStage = kv4_rec(D) + 128;
   static constexpr int kPairs = D / 2 + 2;                       // float pairs of a row of a warp's output
   static constexpr int off_o = W * 2 * kStage;                   // [W][RT][kPairs] float pairs
-  static constexpr int off_q = off_o + W * RT * kPairs * 8;           // [NT][D/16][32] uint2: fp16 queries
+  static constexpr int off_q = off_o + W * RT * kPairs * 8;           // [NT][D/32][32] uint4: fp16 queries, two k-steps each
   static constexpr int off_qb = off_q + NT * (D / 16) * 32 * 8;  // the same, bf16
   static constexpr int off_anc = off_qb + NT * (D / 16) * 32 * 8;  // [RT] u64
   static constexpr int off_bar = off_anc + RT * 8;               // [W][2]
@@ -163,8 +168,8 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
   constexpr int KK = D / 16;  // k-steps of a score, and 16-dim tiles of an output
   extern __shared__ __align__(128) uint8_t sm[];
   float* s_o = reinterpret_cast<float*>(sm + S::off_o);
-  uint2* s_q = reinterpret_cast<uint2*>(sm + S::off_q);
-  uint2* s_qb = reinterpret_cast<uint2*>(sm + S::off_qb);
+  uint4* s_q = reinterpret_cast<uint4*>(sm + S::off_q);
+  uint4* s_qb = reinterpret_cast<uint4*>(sm + S::off_qb);
   uint64_t* s_anc = reinterpret_cast<uint64_t*>(sm + S::off_anc);
   uint64_t* s_bar = reinterpret_cast<uint64_t*>(sm + S::off_bar);
   float* s_m = reinterpret_cast<float*>(sm + S::off_ml);
@@ -175,7 +180,8 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
   int* s_pos = reinterpret_cast<int*>(s_slope + RT);
   float* s_L = reinterpret_cast<float*>(s_pos + RT);
   int* s_ok = reinterpret_cast<int*>(sm + S::off_ok);
-  __shared__ int s_r0, s_s0, s_abort, s_last, s_u0, s_u1, s_seg0, s_each, s_more;
+  __shared__ int s_r0, s_s0, s_abort, s_u0, s_u1, s_seg0, s_each, s_more;
+  __shared__ Kv4Join s_join[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
 
   // this CTA's share of the units: U over C CTAs, the first U % C of them
@@ -235,6 +241,7 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
       s_each = each;
       s_more = more;
       s_abort = 0;
+      s_join[0] = s_join[1] = Kv4Join{};
     }
   }
   if (lane == 0) {
@@ -288,19 +295,20 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
       if (u + W < ub) issue(u + W, 1, (used + 1) & 1);
     }
   };
-  begin();
-
   const int e0 = q >> 1;  // which of a key pair this lane reads first (bank spread)
   const uint32_t sel_lo = e0 ? 0x1054u : 0x5410u, sel_hi = e0 ? 0x3276u : 0x7632u;
   const float sc2 = BIAS ? 1.f : a.s.scale * kLog2e;
 
-  for (;;) {
+  const int each = s_each, extra = s_more, big = extra * (each + 1);
+  auto cta_of = [&](int u) { return u < big ? u / (each + 1) : extra + (u - big) / each; };
+  for (bool first = true;; first = false) {
     const int h = s / rq.nc, rc = s - h * rq.nc;
     const int rows = min(RT, a.G * rq.m - rc * RT);
     const int start = BIAS && a.s.start ? a.s.start[r] : INT32_MIN;
 
     // the tile's query rows as B fragments; dims are taken in the order the
     // codes' nibbles give them
+    if (first && tid / 32 * 32 >= RT * (D / 8)) begin();
     for (int i = tid; i < RT * (D / 8); i += W * 32) {
       const int row = i / (D / 8), oct = i % (D / 8);
       const int rho = rc * RT + row;
@@ -308,6 +316,7 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
       const int node = ok ? rho % rq.m : 0, hq = h * a.G + (ok ? rho / rq.m : 0);
       uint4 x = make_uint4(0, 0, 0, 0);
       if (ok) x = *reinterpret_cast<const uint4*>(a.q + (int64_t)(rq.n0 + node) * a.q_stride + hq * D + oct * 8);
+      if (first && i == tid) begin();  // behind the queries' own loads
       const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
       float f[8], qs = 0.f, big = 0.f;
 #pragma unroll
@@ -325,11 +334,11 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
       const int e = min(max(14 + 127 - (int)(__float_as_uint(big) >> 23), -100), 100);
       const float up = pow2i(e), up4 = pow2i(e - 4);
       const int ql = oct / (D / 32), j = oct % (D / 32);
-      const int at = ((row >> 3) * KK + 2 * j) * 32 + 4 * (row & 7) + ql;
-      s_q[at] = make_uint2(pack_f16x2(f[0] * up, f[4] * up), pack_f16x2(f[1] * up4, f[5] * up4));
-      s_q[at + 32] = make_uint2(pack_f16x2(f[2] * up, f[6] * up), pack_f16x2(f[3] * up4, f[7] * up4));
-      s_qb[at] = make_uint2(prmt(x.x, x.z, 0x5410), prmt(x.x, x.z, 0x7632));
-      s_qb[at + 32] = make_uint2(prmt(x.y, x.w, 0x5410), prmt(x.y, x.w, 0x7632));
+      const int at = ((row >> 3) * (KK / 2) + j) * 32 + 4 * (row & 7) + ql;
+      s_q[at] = make_uint4(pack_f16x2(f[0] * up, f[4] * up), pack_f16x2(f[1] * up4, f[5] * up4),
+                           pack_f16x2(f[2] * up, f[6] * up), pack_f16x2(f[3] * up4, f[7] * up4));
+      s_qb[at] = make_uint4(prmt(x.x, x.z, 0x5410), prmt(x.x, x.z, 0x7632), prmt(x.y, x.w, 0x5410),
+                            prmt(x.y, x.w, 0x7632));
       if (oct == 0) {
         s_qs[row] = qs * sc2;
         s_fac[row] = pow2i(24 - e) * sc2;
@@ -407,11 +416,11 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
             const uint4 xa = *reinterpret_cast<const uint4*>(pa + 8 * j), xb = *reinterpret_cast<const uint4*>(pb + 8 * j);
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
-              const uint2 b0 = s_qb[(nt * KK + 2 * j) * 32 + lane], b1 = s_qb[(nt * KK + 2 * j + 1) * 32 + lane];
+              const uint4 b = s_qb[(nt * (KK / 2) + j) * 32 + lane];
               mma_bf16(so[nt], prmt(xa.x, xa.z, 0x5410), prmt(xb.x, xb.z, 0x5410), prmt(xa.x, xa.z, 0x7632),
-                       prmt(xb.x, xb.z, 0x7632), b0.x, b0.y);
+                       prmt(xb.x, xb.z, 0x7632), b.x, b.y);
               mma_bf16(so[nt], prmt(xa.y, xa.w, 0x5410), prmt(xb.y, xb.w, 0x5410), prmt(xa.y, xa.w, 0x7632),
-                       prmt(xb.y, xb.w, 0x7632), b1.x, b1.y);
+                       prmt(xb.y, xb.w, 0x7632), b.z, b.w);
             }
           }
         }
@@ -516,50 +525,37 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
       const int stage = used & 1;
       const uint8_t* st = ring + stage * S::kStage;
       if (!mbar_wait_or_abort(&bar[stage], (used >> 1) & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(30));
-      {
-        // K: lane (g, q) holds dims q D/4 .. of keys g, g + 8, g + 16, g + 24
-        uint32_t kw[4][D / 32];
+      // K: lane (g, q) holds dims q D/4 .. of keys g and g + 8 of a 16-key tile
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const uint8_t* p = st + (g + 8 * i) * (D / 2) + q * (D / 8);
+      for (int i = 0; i < 2; i++) {
+        uint32_t kw[2][D / 32];
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+          const uint8_t* p = st + (16 * i + 8 * b + g) * (D / 2) + q * (D / 8);
           if constexpr (D == 128) {
             const uint4 v = *reinterpret_cast<const uint4*>(p);
-            kw[i][0] = v.x, kw[i][1] = v.y, kw[i][2] = v.z, kw[i][3] = v.w;
+            kw[b][0] = v.x, kw[b][1] = v.y, kw[b][2] = v.z, kw[b][3] = v.w;
           } else {
             const uint2 v = *reinterpret_cast<const uint2*>(p);
-            kw[i][0] = v.x, kw[i][1] = v.y;
+            kw[b][0] = v.x, kw[b][1] = v.y;
           }
         }
+        float s2[4] = {0.f, 0.f, 0.f, 0.f};  // a second chain of sums, for one tile of rows alone
 #pragma unroll
-        for (int i = 0; i < 2; i++)
-#pragma unroll
-          for (int nt = 0; nt < NT; nt++) sc[i][nt][0] = sc[i][nt][1] = sc[i][nt][2] = sc[i][nt][3] = 0.f;
-        float s2[2][4];  // a second chain of sums, for one tile of rows alone
-        if (NT == 1)
-#pragma unroll
-          for (int e = 0; e < 4; e++) s2[0][e] = s2[1][e] = 0.f;
+        for (int nt = 0; nt < NT; nt++) sc[i][nt][0] = sc[i][nt][1] = sc[i][nt][2] = sc[i][nt][3] = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 32; j++) {
-          uint32_t f[4][4];
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            f[i][0] = codes2<0>(kw[i][j]);
-            f[i][1] = codes2<1>(kw[i][j]);
-            f[i][2] = codes2<2>(kw[i][j]);
-            f[i][3] = codes2<3>(kw[i][j]);
-          }
+          const uint32_t wa = kw[0][j], wb = kw[1][j];
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
-            const uint2 b0 = s_q[(nt * KK + 2 * j) * 32 + lane], b1 = s_q[(nt * KK + 2 * j + 1) * 32 + lane];
-            mma_f16(sc[0][nt], f[0][0], f[1][0], f[0][1], f[1][1], b0.x, b0.y);
-            mma_f16(sc[1][nt], f[2][0], f[3][0], f[2][1], f[3][1], b0.x, b0.y);
-            mma_f16(NT == 1 ? s2[0] : sc[0][nt], f[0][2], f[1][2], f[0][3], f[1][3], b1.x, b1.y);
-            mma_f16(NT == 1 ? s2[1] : sc[1][nt], f[2][2], f[3][2], f[2][3], f[3][3], b1.x, b1.y);
+            const uint4 b = s_q[(nt * (KK / 2) + j) * 32 + lane];
+            mma_f16(sc[i][nt], codes2<0>(wa), codes2<0>(wb), codes2<1>(wa), codes2<1>(wb), b.x, b.y);
+            mma_f16(NT == 1 ? s2 : sc[i][nt], codes2<2>(wa), codes2<2>(wb), codes2<3>(wa), codes2<3>(wb), b.z, b.w);
           }
         }
         if (NT == 1)
 #pragma unroll
-          for (int e = 0; e < 4; e++) sc[0][0][e] += s2[0][e], sc[1][0][e] += s2[1][e];
+          for (int e = 0; e < 4; e++) sc[i][0][e] += s2[e];
       }
       // slots of this record that the request holds
       const int lim = s_ok[warp * 2 + stage] ? rq.ctx - (rq.g0 + u - rq.no) * kKvGroup : 0;
@@ -761,62 +757,64 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
         __stcg(reinterpret_cast<float2*>(part) + i, acc);
       }
     }
-    if (!whole) {
-      // the last of the segment's CTAs joins their parts
-      const int each = s_each, extra = s_more, big = extra * (each + 1);
-      auto cta_of = [&](int u) { return u < big ? u / (each + 1) : extra + (u - big) / each; };
+    __syncthreads();  // s_o, s_q and the rows' data are free again; a part is written
+    if (!whole && tid == W * 32 - 32) {
+      // Is this the last of the segment's CTAs to write its part?  Only the
+      // warp with the fewest records waits for the answer, which is acted on
+      // at this CTA's end: a part is the first of its segments or the last.
       const int c0 = cta_of(this_seg), n = cta_of(this_seg + tq.nu - 1) - c0 + 1;
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const int old = atomic_add_acq_rel(a.tickets + c0, 1);
-        s_last = old == n - 1;
-        if (s_last) a.tickets[c0] = 0;
-      }
-      __syncthreads();
-      if (s_last) {
-        // c0's part is its last segment's unless the segment begins its share
-        const int slot0 = 2 * c0 + (c0 * each + min(c0, extra) < this_seg ? 1 : 0);
-        auto part_of = [&](int c) { return a.part + (int64_t)(c == 0 ? slot0 : 2 * (c0 + c)) * (RT * (D + 2)); };
-        for (int i = tid; i < rows * (D / 2); i += W * 32) {
-          const int row = i / (D / 2), x = i % (D / 2);
-          float M = -INFINITY, L = 0.f;
-          float2 acc = make_float2(0.f, 0.f);
-          for (int c = 0; c < n; c += 8) {  // eight parts in flight
-            float2 ml[8], v[8];
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-              const float* pc = part_of(min(c + k, n - 1));
-              ml[k] = __ldcg(reinterpret_cast<const float2*>(pc + RT * D) + row);
-              v[k] = __ldcg(reinterpret_cast<const float2*>(pc) + i);
-            }
-            float Mn = M;
-#pragma unroll
-            for (int k = 0; k < 8; k++) Mn = fmaxf(Mn, ml[k].x);
-            const float Ms = Mn == -INFINITY ? 0.f : Mn, al = ex2(M - Ms);
-            M = Mn;
-            L *= al;
-            acc.x *= al;
-            acc.y *= al;
-#pragma unroll
-            for (int k = 0; k < 8; k++)
-              if (c + k < n) {
-                const float f = ex2(ml[k].x - Ms);
-                L = fmaf(f, ml[k].y, L);
-                acc.x = fmaf(f, v[k].x, acc.x);
-                acc.y = fmaf(f, v[k].y, acc.y);
-              }
-          }
-          const float inv = L == 0.f ? 0.f : 1.f / L;
-          const int64_t at = row_out(row);
-          *reinterpret_cast<uint32_t*>(a.out + at * D + (x & 7) * (D / 8) + (x >> 3) * 2) =
-              pack_bf16x2(acc.x * inv, acc.y * inv);
-          if (x == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
-        }
-      }
+      const bool last = atomic_add_acq_rel(a.tickets + c0, 1) == n - 1;
+      if (last) a.tickets[c0] = 0;
+      s_join[more ? 0 : 1] = last ? Kv4Join{this_seg, n, c0, tq.n0, tq.m, h, rc} : Kv4Join{};
     }
     if (!more) break;
-    __syncthreads();  // s_o, s_q and the rows' data are free again
+  }
+
+  // join the parts of the segments that this CTA was the last to finish
+  __syncthreads();
+  for (int d = 0; d < 2; d++) {
+    const Kv4Join jn = s_join[d];
+    if (jn.n == 0) continue;
+    const int rows = min(RT, a.G * jn.m - jn.rc * RT);
+    // c0's part is its last segment's unless the segment begins its share
+    const int slot0 = 2 * jn.c0 + (jn.c0 * s_each + min(jn.c0, s_more) < jn.seg ? 1 : 0);
+    auto part_of = [&](int c) { return a.part + (int64_t)(c == 0 ? slot0 : 2 * (jn.c0 + c)) * (RT * (D + 2)); };
+    for (int i = tid; i < rows * (D / 2); i += W * 32) {
+      const int row = i / (D / 2), x = i % (D / 2);
+      float M = -INFINITY, L = 0.f;
+      float2 acc = make_float2(0.f, 0.f);
+      for (int c = 0; c < jn.n; c += 8) {  // eight parts in flight
+        float2 ml[8], v[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+          const float* pc = part_of(min(c + k, jn.n - 1));
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(pc + RT * D) + row);
+          v[k] = __ldcg(reinterpret_cast<const float2*>(pc) + i);
+        }
+        float Mn = M;
+#pragma unroll
+        for (int k = 0; k < 8; k++) Mn = fmaxf(Mn, ml[k].x);
+        const float Ms = Mn == -INFINITY ? 0.f : Mn, al = ex2(M - Ms);
+        M = Mn;
+        L *= al;
+        acc.x *= al;
+        acc.y *= al;
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+          if (c + k < jn.n) {
+            const float f = ex2(ml[k].x - Ms);
+            L = fmaf(f, ml[k].y, L);
+            acc.x = fmaf(f, v[k].x, acc.x);
+            acc.y = fmaf(f, v[k].y, acc.y);
+          }
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const int rho = jn.rc * RT + row, gq = rho / jn.m;
+      const int64_t at = (int64_t)(jn.n0 + rho - gq * jn.m) * a.hq + jn.h * a.G + gq;
+      *reinterpret_cast<uint32_t*>(a.out + at * D + (x & 7) * (D / 8) + (x >> 3) * 2) =
+          pack_bf16x2(acc.x * inv, acc.y * inv);
+      if (x == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
+    }
   }
 }
 

@@ -23,8 +23,6 @@ struct Kv4AttnArgs {
   float* part;       // [2 grid][rows of a tile][D + 2]
 };
 
-__device__ __forceinline__ float nib(uint32_t byte, int d) { return (float)(int)((byte >> (4 * (d & 1))) & 15) - 8.f; }
-
 __device__ __forceinline__ float kv4_score(const Kv4Score& s, float qk, float slope, int q_pos, int k_pos, int start) {
   float t = qk * s.scale;
   if (s.cap > 0.f) t = s.cap * tanhf(t / s.cap);
@@ -826,50 +824,279 @@ struct Kv4ObserveArgs {
   float* out;
 };
 
-// One thread per slot of a (request, kv head), over every row and query head.
+// ------------------------------------------------------------- observe --
+//
+// S^T tiles as above, from the K half of the records alone: exp(score - lse)
+// of a key is summed over the tile's rows in the lane, over the four lanes
+// that share the key at the end.  Rows of weight 0 are left out before the
+// products (a verified tree's rejected nodes).  Bound by the bytes of K while
+// a kv head has up to about three tiles of eight rows, by the products past
+// that.  No sum crosses a warp, so there is nothing to join: a (request, kv
+// head)'s groups of 32 slots are dealt over the CTAs like the attention's.
+// More than kObsRows rows are taken in passes that add to the output.
+
+constexpr int kObsWarps = 8, kObsRows = 128, kObsStages = 3;
+
 template <int D>
-__global__ void __launch_bounds__(128) k_kv4_observe_simple(Kv4ObserveArgs b) {
+struct ObserveShape {
+  static constexpr int kStage = kv4_half(D) + 128;
+  static constexpr int off_q = kObsWarps * kObsStages * kStage;   // [rows/8][D/32][32] uint4
+  static constexpr int off_row = off_q + kObsRows * D * 2;        // [rows] (factor, sum q, lse, weight)
+  static constexpr int off_bias = off_row + kObsRows * 16;        // [rows] (slope, position)
+  static constexpr int off_node = off_bias + kObsRows * 8;        // [64] nodes of weight other than 0
+  static constexpr int off_bar = off_node + 64 * 4;
+  static constexpr int off_ok = off_bar + kObsWarps * kObsStages * 8;
+  static constexpr int smem = off_ok + kObsWarps * kObsStages * 4;
+};
+
+template <int D, bool BIAS>
+__global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_constant__ Kv4ObserveArgs b) {
+  using S = ObserveShape<D>;
+  constexpr int W = kObsWarps, NS = kObsStages;
   const Kv4AttnArgs& a = b.a;
-  __shared__ float sq[D];
-  const int h = blockIdx.y, r = blockIdx.z, tid = threadIdx.x;
-  int ctx = a.c.ctx_len[r];
-  if (ctx < 0 || ctx > a.c.cap) {
-    if (tid == 0) set_status(a.status, SD_ERR_CAPACITY);
-    ctx = ctx < 0 ? 0 : (int)a.c.cap;
-  }
-  const int n0 = a.cu[r], m = a.cu[r + 1] - n0;
-  const int start = a.s.start ? a.s.start[r] : INT32_MIN;
-  for (int base = blockIdx.x * 128; base < ctx; base += gridDim.x * 128) {
-    const int t = base + tid;
-    const uint8_t* rec = t < ctx ? a.c.record(D, r, h, t / 32) : nullptr;
-    if (t < ctx && !rec) set_status(a.status, SD_ERR_CAPACITY);
-    const int kp = t < ctx ? a.c.pos[a.c.slot0(r, h) + t] : 0;
-    float sum = 0.f;
-    for (int i = 0; i < m; i++) {
-      const float rw = b.row_weight ? b.row_weight[n0 + i] : 1.f;
-      if (rw == 0.f) continue;
-      const int qp = a.row_pos ? a.row_pos[n0 + i] : ctx + i;
-      for (int gq = 0; gq < a.G; gq++) {
-        const int hq = h * a.G + gq;
-        __syncthreads();
-        if (tid < D) sq[tid] = bf2f(a.q[(int64_t)(n0 + i) * a.q_stride + hq * D + tid]);
-        __syncthreads();
-        const float lse = b.lse_in[(int64_t)(n0 + i) * a.hq + hq];
-        if (!rec || lse == -INFINITY) continue;
-        const uint32_t sm = *reinterpret_cast<const uint32_t*>(rec + 16 * D + (t & 31) * 4);
-        float dot = 0.f, qs = 0.f;
-        for (int d = 0; d < D; d++) {
-          dot = fmaf(sq[d], nib(rec[(t & 31) * (D / 2) + d / 2], d), dot);
-          qs += sq[d];
+  extern __shared__ __align__(128) uint8_t sm[];
+  uint4* s_q = reinterpret_cast<uint4*>(sm + S::off_q);
+  float4* s_row = reinterpret_cast<float4*>(sm + S::off_row);
+  float2* s_bias = reinterpret_cast<float2*>(sm + S::off_bias);
+  int* s_node = reinterpret_cast<int*>(sm + S::off_node);
+  uint64_t* s_bar = reinterpret_cast<uint64_t*>(sm + S::off_bar);
+  int* s_ok = reinterpret_cast<int*>(sm + S::off_ok);
+  __shared__ int s_r0, s_u0, s_u1, s_req0, s_abort, s_n;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+
+  auto context = [&](int r) {
+    int ctx = a.c.ctx_len[r];
+    if (ctx < 0 || ctx > a.c.cap) {
+      set_status(a.status, SD_ERR_CAPACITY);
+      ctx = ctx < 0 ? 0 : (int)a.c.cap;
+    }
+    return ctx;
+  };
+  if (warp == 0) {
+    int U = 0, lo = 0, n = 0;
+    for (int pass = 0, u0 = 0, u1 = 0; pass < 2; pass++) {
+      int before = 0;
+      for (int base = 0; base < a.R; base += 32) {
+        if (pass == 0 || a.R > 32) {
+          n = base + lane < a.R ? a.c.hkv * ((context(base + lane) + 31) / 32) : 0;
+          int run = n;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += v;
+          }
+          lo = before + run - n;
+          before += __shfl_sync(0xffffffffu, run, 31);
         }
-        dot = fmaf(bf2f((uint16_t)sm), dot, bf2f((uint16_t)(sm >> 16)) * qs);
-        const float sc = kv4_score(a.s, dot, a.s.slopes ? a.s.slopes[hq] : 0.f, qp, kp, start);
-        sum = fmaf(rw, __expf(sc - lse), sum);
+        if (pass == 1 && u0 >= lo && u0 < lo + n) {
+          s_r0 = base + lane;
+          s_req0 = lo;
+        }
+      }
+      if (pass == 0) {
+        U = before;
+        const int C = max(1, min((int)gridDim.x, (U + W - 1) / W)), each = U / C, more = U - each * C;
+        u0 = (int)blockIdx.x < C ? (int)blockIdx.x * each + min((int)blockIdx.x, more) : U;
+        u1 = (int)blockIdx.x < C ? u0 + each + ((int)blockIdx.x < more) : U;
+        if (lane == 0) {
+          s_u0 = u0;
+          s_u1 = u1;
+          s_abort = 0;
+        }
       }
     }
-    if (t < ctx) {
-      const int64_t o = a.c.slot0(r, h) + t;
-      b.out[o] = fmaf(b.decay, a.c.weight[o], sum);
+  }
+  if (lane == 0) {
+    for (int i = 0; i < NS; i++) mbar_init(&s_bar[warp * NS + i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int u1 = s_u1;
+  if (s_u0 >= u1) return;
+  uint64_t* const bar = s_bar + warp * NS;
+  uint8_t* const ring = sm + warp * NS * S::kStage;
+  const float sc2 = BIAS ? 1.f : a.s.scale * kLog2e;
+  uint32_t used = 0;
+
+  int r = s_r0, req0 = s_req0, u = s_u0;  // request, its first unit, the segment's first unit of this CTA
+  int ctx = context(r);
+  while (u < u1) {
+    int ng = (ctx + 31) / 32;
+    while (u >= req0 + a.c.hkv * ng) {
+      req0 += a.c.hkv * ng;
+      ctx = context(++r);
+      ng = (ctx + 31) / 32;
+    }
+    const int h = (u - req0) / ng, g0 = u - req0 - h * ng, g1 = min(ng, g0 + u1 - u);
+    u += g1 - g0;
+    const int n0 = a.cu[r], m = min(max(a.cu[r + 1] - n0, 0), 64);
+    const int start = BIAS && a.s.start ? a.s.start[r] : INT32_MIN;
+    const int first = a.s.window > 0 || a.s.start
+                          ? kv4_first(a.s, r, ctx, a.row_pos && m ? a.row_pos[n0] : ctx) / kKvGroup
+                          : 0;  // groups before it collect nothing
+    if (warp == 0) {  // the rows that count
+      int n = 0;
+      for (int i = 0; i < m; i += 32) {
+        const bool on = i + lane < m && (!b.row_weight || b.row_weight[n0 + i + lane] != 0.f);
+        const uint32_t on32 = __ballot_sync(0xffffffffu, on);
+        if (on) s_node[n + __popc(on32 & ((1u << lane) - 1))] = i + lane;
+        n += __popc(on32);
+      }
+      if (lane == 0) s_n = n;
+    }
+    __syncthreads();
+    const int n = s_n, rows = n * a.G;
+    const float* w_in = a.c.weight + a.c.slot0(r, h);
+    float* w_out = b.out + a.c.slot0(r, h);
+    for (int pass = 0; pass == 0 || pass * kObsRows < rows; pass++) {
+      const int left = min(kObsRows, rows - pass * kObsRows), tiles = (left + 7) / 8;
+      // the records of this warp: groups ga, ga + W, ...; a lane holds the
+      // address of every 32nd
+      const int ga = g0 + warp + (rows > 0 && first > g0 + warp ? (first - g0 - warp + W - 1) / W * W : 0);
+      const int ge = rows > 0 ? g1 : g0;
+      const uint8_t* addr = nullptr;
+      auto look_up = [&](int x) {
+        x += lane * W;
+        addr = x < ge ? a.c.record(D, r, h, x) : nullptr;
+      };
+      auto issue = [&](int x, int k, int stage) {
+        const uint8_t* rec = reinterpret_cast<const uint8_t*>(
+            __shfl_sync(0xffffffffu, (unsigned long long)reinterpret_cast<uintptr_t>(addr), k));
+        if (lane == 0) {
+          s_ok[warp * NS + stage] = rec != nullptr;
+          if (rec) {
+            uint8_t* dst = ring + stage * S::kStage;
+            mbar_arrive_expect_tx(&bar[stage], kv4_half(D) + (BIAS ? 128 : 0));
+            bulk_g2s(dst, rec, kv4_half(D), &bar[stage]);
+            if (BIAS) bulk_g2s(dst + kv4_half(D), a.c.pos + a.c.slot0(r, h) + x * kKvGroup, 128, &bar[stage]);
+          } else {
+            set_status(a.status, SD_ERR_CAPACITY);
+            mbar_arrive(&bar[stage]);
+          }
+        }
+        __syncwarp();
+      };
+      if (ga < ge) look_up(ga);
+#pragma unroll
+      for (int i = 0; i < NS; i++)
+        if (ga + i * W < ge) issue(ga + i * W, i, (used + i) % NS);
+      // groups before the first that any row sees only fade
+      if (pass == 0)
+        for (int x = g0 + warp; x < (rows > 0 ? min(g1, first) : g1); x += W) {
+          const int t = x * kKvGroup + lane;
+          if (t < ctx) w_out[t] = b.decay * w_in[t];
+        }
+      for (int i = tid; i < tiles * 8 * (D / 8); i += W * 32) {
+        const int row = i / (D / 8), oct = i % (D / 8);
+        const int rho = pass * kObsRows + row;
+        const bool ok = rho < rows;
+        const int gq = ok ? rho / n : 0, node = ok ? s_node[rho - gq * n] : 0, hq = h * a.G + gq;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (ok) x = *reinterpret_cast<const uint4*>(a.q + (int64_t)(n0 + node) * a.q_stride + hq * D + oct * 8);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+        float f[8], qs = 0.f, big = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+          f[k] = bf2f((uint16_t)(xs[k >> 1] >> (16 * (k & 1))));
+          qs += f[k];
+          big = fmaxf(big, fabsf(f[k]));
+        }
+#pragma unroll
+        for (int o = D / 16; o > 0; o >>= 1) {
+          qs += __shfl_xor_sync(0xffffffffu, qs, o);
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        }
+        const int e = min(max(14 + 127 - (int)(__float_as_uint(big) >> 23), -100), 100);
+        const float up = pow2i(e), up4 = pow2i(e - 4);
+        s_q[((row >> 3) * (D / 32) + oct % (D / 32)) * 32 + 4 * (row & 7) + oct / (D / 32)] =
+            make_uint4(pack_f16x2(f[0] * up, f[4] * up), pack_f16x2(f[1] * up4, f[5] * up4),
+                       pack_f16x2(f[2] * up, f[6] * up), pack_f16x2(f[3] * up4, f[7] * up4));
+        if (oct == 0) {
+          const float lse = ok ? b.lse_in[(int64_t)(n0 + node) * a.hq + hq] : -INFINITY;
+          s_row[row] = make_float4(pow2i(24 - e) * sc2, qs * sc2, lse == -INFINITY ? INFINITY : lse * kLog2e,
+                                   ok ? (b.row_weight ? b.row_weight[n0 + node] : 1.f) : 0.f);
+          s_bias[row] = make_float2(BIAS && a.s.slopes ? a.s.slopes[hq] : 0.f,
+                                    __int_as_float(a.row_pos ? a.row_pos[n0 + node] : ctx + node));
+        }
+      }
+      __syncthreads();
+      int k = 0;
+      for (int x = ga; x < ge; x += W) {
+        const int stage = used % NS;
+        const uint8_t* st = ring + stage * S::kStage;
+        const int t = x * kKvGroup + 8 * q + g;  // the slot whose sum this lane writes
+        const float old = t < ctx ? (pass ? w_out[t] : b.decay * w_in[t]) : 0.f;
+        if (!mbar_wait_or_abort(&bar[stage], (used / NS) & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(31));
+        const bool ok = s_ok[warp * NS + stage] != 0;
+        uint32_t kw[4][D / 32];
+        float ks[4], km[4];
+        int kp[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const uint8_t* p = st + (8 * i + g) * (D / 2) + q * (D / 8);
+          if constexpr (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            kw[i][0] = v.x, kw[i][1] = v.y, kw[i][2] = v.z, kw[i][3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            kw[i][0] = v.x, kw[i][1] = v.y;
+          }
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(st + 16 * D + (8 * i + g) * 4);
+          ks[i] = __uint_as_float(w << 16);
+          km[i] = fmaf(-8.f, ks[i], __uint_as_float(w & 0xFFFF0000u));
+          kp[i] = BIAS ? *reinterpret_cast<const int*>(st + kv4_half(D) + (8 * i + g) * 4) : 0;
+        }
+        __syncwarp();
+        used++;
+        k++;
+        if (x + NS * W < ge) {
+          if (k + NS - 1 == 32) {  // the lanes' addresses run out
+            look_up(x + NS * W);
+            k = 1 - NS;
+          }
+          issue(x + NS * W, k + NS - 1, stage);
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int nt = 0; nt < tiles; nt++) {
+          float sc[2][2][4];  // [16-key tile][chain]
+#pragma unroll
+          for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) sc[i][0][e] = sc[i][1][e] = 0.f;
+#pragma unroll
+          for (int j = 0; j < D / 32; j++) {
+            const uint4 bq = s_q[(nt * (D / 32) + j) * 32 + lane];
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+              const uint32_t wa = kw[2 * i][j], wb = kw[2 * i + 1][j];
+              mma_f16(sc[i][0], codes2<0>(wa), codes2<0>(wb), codes2<1>(wa), codes2<1>(wb), bq.x, bq.y);
+              mma_f16(sc[i][1], codes2<2>(wa), codes2<2>(wb), codes2<3>(wa), codes2<3>(wb), bq.z, bq.w);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const int row = nt * 8 + 2 * q + e;
+            const float4 rw = s_row[row];
+            const float2 bi = BIAS ? s_bias[row] : make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+              float v = (sc[i >> 1][0][2 * (i & 1) + e] + sc[i >> 1][1][2 * (i & 1) + e]) * rw.x;
+              v = fmaf(ks[i], v, km[i] * rw.y);
+              if (BIAS) v = kv4_score(a.s, v, bi.x, __float_as_int(bi.y), kp[i], start) * kLog2e;
+              sum[i] = fmaf(rw.w, ex2(v - rw.z), sum[i]);
+            }
+          }
+        }
+        float mine = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+          if (q == i) mine = sum[i];
+        }
+        if (t < ctx) w_out[t] = old + (ok ? mine : 0.f);
+      }
+      __syncthreads();  // s_q, s_row and s_node are free again
     }
   }
 }
@@ -889,6 +1116,19 @@ static int launch_attn_tile(const Kv4AttnArgs& a, int64_t units, bool bias, cuda
   SD_CK(set[bias]);
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>({(NT <= 2 ? 2ll : 1ll) * num_sms(), kMaxCtas, units}));
   kern<<<(unsigned)grid, W * 32, smem, st>>>(a);
+  SD_CK(cudaGetLastError());
+  return SD_OK;
+}
+
+template <int D>
+static int launch_observe(const Kv4ObserveArgs& b, int64_t units, bool bias, cudaStream_t st) {
+  constexpr int smem = ObserveShape<D>::smem;
+  static const cudaError_t set[2] = {
+      cudaFuncSetAttribute(k_kv4_observe<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+      cudaFuncSetAttribute(k_kv4_observe<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)};
+  SD_CK(set[bias]);
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(2ll * num_sms(), (units + kObsWarps - 1) / kObsWarps));
+  (bias ? k_kv4_observe<D, true> : k_kv4_observe<D, false>)<<<(unsigned)grid, kObsWarps * 32, smem, st>>>(b);
   SD_CK(cudaGetLastError());
   return SD_OK;
 }
@@ -978,7 +1218,8 @@ extern "C" int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride,
   most *= a.G;
   const int64_t ctx = max_ctx > 0 ? std::min<int64_t>(max_ctx, a.c.cap) : a.c.cap;
   const int64_t units = (int64_t)R * c->n_kv_heads * ((most + 31) / 32) * ((ctx + 31) / 32 + 2);
-  if (units > 0x7FFFFFFF) return kv4_bad(SD_ERR_UNSUPPORTED, who, "more than 2^31 runs of 32 keys");
+  if ((int64_t)R * c->n_kv_heads * ((most + 7) / 8) * ((a.c.cap + 31) / 32 + 2) > 0x7FFFFFFF)
+    return kv4_bad(SD_ERR_UNSUPPORTED, who, "more than 2^31 runs of 32 keys");
   const bool bias = a.s.cap > 0.f || a.s.slopes || a.s.window > 0 || a.s.start;
   return c->head_dim == 128 ? launch_attn<128>(a, most, units, bias, (cudaStream_t)stream)
                             : launch_attn<64>(a, most, units, bias, (cudaStream_t)stream);
@@ -1001,10 +1242,12 @@ extern "C" int sd_kv4_observe(const sd_kv4* c, const uint16_t* q, int64_t q_stri
   b.row_weight = row_weight;
   b.decay = decay;
   b.out = weight_out;
-  const int64_t most = max_ctx > 0 ? std::min<int64_t>(max_ctx, b.a.c.cap) : b.a.c.cap;
-  const unsigned gx = (unsigned)std::max<int64_t>(1, std::min<int64_t>((most + 127) / 128, 1024));
-  auto kern = c->head_dim == 128 ? k_kv4_observe_simple<128> : k_kv4_observe_simple<64>;
-  kern<<<dim3(gx, c->n_kv_heads, R), 128, 0, (cudaStream_t)stream>>>(b);
-  SD_CK(cudaGetLastError());
-  return SD_OK;
+  // a request longer than max_ctx is still read whole: the CTAs share the units there are
+  const int64_t ctx = max_ctx > 0 ? std::min<int64_t>(max_ctx, b.a.c.cap) : b.a.c.cap;
+  const int64_t units = (int64_t)R * c->n_kv_heads * ((ctx + 31) / 32);
+  if ((int64_t)R * c->n_kv_heads * ((b.a.c.cap + 31) / 32) > 0x7FFFFFFF)
+    return kv4_bad(SD_ERR_UNSUPPORTED, who, "more than 2^31 runs of 32 keys");
+  const bool bias = b.a.s.cap > 0.f || b.a.s.slopes || b.a.s.window > 0 || b.a.s.start;
+  return c->head_dim == 128 ? launch_observe<128>(b, units, bias, (cudaStream_t)stream)
+                            : launch_observe<64>(b, units, bias, (cudaStream_t)stream);
 }

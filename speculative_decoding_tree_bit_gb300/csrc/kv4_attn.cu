@@ -1,111 +1,9 @@
 // Attention over the 4-bit cache, and the weight its keys collect.
 #include <algorithm>
 
-#include "kv4.cuh"
+#include "kv4_attn.cuh"
 
 namespace sdv {
-
-struct Kv4AttnArgs {
-  Kv4View c;
-  Kv4Score s;
-  const uint16_t* q;
-  int64_t q_stride, kv_stride;
-  const uint16_t* k_new;
-  const uint16_t* v_new;
-  const int32_t* cu;
-  const uint64_t* anc;
-  const int32_t* row_pos;
-  int R, hq, G;
-  uint16_t* out;
-  float* lse;
-  int32_t* status;
-  int32_t* tickets;  // [grid], zero between calls
-  float* part;       // [2 grid][rows of a tile][D + 2]
-};
-
-__device__ __forceinline__ float kv4_score(const Kv4Score& s, float qk, float slope, int q_pos, int k_pos, int start) {
-  float t = qk * s.scale;
-  if (s.cap > 0.f) t = s.cap * tanhf(t / s.cap);
-  if (s.slopes) t = fmaf(slope, (float)(k_pos - q_pos), t);
-  if ((s.window > 0 && q_pos - k_pos >= s.window) || k_pos < start) t = -INFINITY;
-  return t;
-}
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
-// 8x8 transpose of 16-bit values across the warp.
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-// The four nibbles of each 16-bit half of w as fp16 pairs, from two words (w
-// and w >> 8) and two masks: nibble i even lies at bits 0..3 and reads as the
-// subnormal code 2^-24, i odd at bits 4..7 and reads as code 2^-20.
-template <int I>
-__device__ __forceinline__ uint32_t codes2(uint32_t w) {
-  return (I < 2 ? w : w >> 8) & (I & 1 ? 0x00F000F0u : 0x000F000Fu);
-}
-// (code - 8) 2^-9 of the same pair: one fused multiply-add, exact.
-template <int I>
-__device__ __forceinline__ uint32_t centred2(uint32_t w) {
-  uint32_t y;
-  // 2^15 or 2^11, and -8 2^-9
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(codes2<I>(w)), "r"(I & 1 ? 0x68006800u : 0x78007800u), "r"(0xA400A400u));
-  return y;
-}
-__device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t y;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
-  return y;
-}
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
-
-// What a call's requests hold, as the attention kernels split them: a request
-// is hkv x nc segments (kv head, tile of RT rows) of nu units each: the rows'
-// own keys in `no` runs of 32, then the groups of 32 cached slots from group
-// g0 on; at least one unit, so that a row that sees nothing is written too.
-struct Kv4Req {
-  int n0, m, ctx, g0, no, nu, nc;
-};
-
-template <int RT>
-__device__ __forceinline__ Kv4Req kv4_req(const Kv4AttnArgs& a, int r) {
-  Kv4Req q;
-  q.n0 = a.cu[r];
-  q.m = min(max(a.cu[r + 1] - q.n0, 0), 64);
-  int ctx = a.c.ctx_len[r];
-  if (ctx < 0 || ctx > a.c.cap) {
-    set_status(a.status, SD_ERR_CAPACITY);
-    ctx = ctx < 0 ? 0 : (int)a.c.cap;
-  }
-  q.ctx = ctx;
-  int first = 0;
-  if (a.s.window > 0 || a.s.start) first = kv4_first(a.s, r, ctx, a.row_pos && q.m ? a.row_pos[q.n0] : ctx);
-  q.g0 = first / kKvGroup;
-  q.no = a.k_new ? (q.m + 31) / 32 : 0;
-  q.nu = q.no + (ctx > first ? (ctx - 1) / kKvGroup - q.g0 + 1 : 0);
-  if (q.nu == 0) q.no = q.nu = 1;  // an empty run
-  q.nc = (a.G * q.m + RT - 1) / RT;
-  return q;
-}
 
 // ------------------------------------------------ attention, warp MMA --
 //
@@ -138,11 +36,6 @@ __device__ __forceinline__ Kv4Req kv4_req(const Kv4AttnArgs& a, int r) {
 // segments' units are dealt evenly over the CTAs, whatever the requests'
 // lengths; two CTAs an SM, so that one works while the other joins.
 
-// A segment to join at a CTA's end: n parts (0: none) from CTA c0 on.
-struct Kv4Join {
-  int seg, n, c0, n0, m, h, rc;
-};
-
 template <int D, int NT, int W>
 struct AttnShape {
   static constexpr int RT = 8 * NT;
@@ -160,7 +53,7 @@ struct AttnShape {
 };
 
 template <int D, int NT, int W, bool BIAS>
-__global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
+__global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
   using S = AttnShape<D, NT, W>;
   constexpr int RT = S::RT;
   constexpr int KK = D / 16;  // k-steps of a score, and 16-dim tiles of an output
@@ -178,69 +71,15 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
   int* s_pos = reinterpret_cast<int*>(s_slope + RT);
   float* s_L = reinterpret_cast<float*>(s_pos + RT);
   int* s_ok = reinterpret_cast<int*>(sm + S::off_ok);
-  __shared__ int s_r0, s_s0, s_abort, s_u0, s_u1, s_seg0, s_each, s_more;
+  __shared__ int s_abort;
+  __shared__ Kv4Share sh;
   __shared__ Kv4Join s_join[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
 
-  // this CTA's share of the units: U over C CTAs, the first U % C of them
-  // one more
-  if (warp == 0) {
-    int U = 0, segs = 0, lo = 0;
-    Kv4Req rq = {};
-    for (int base = 0; base < a.R; base += 32) {
-      rq = {};
-      if (base + lane < a.R) rq = kv4_req<RT>(a, base + lane);
-      const int n = a.c.hkv * rq.nc * rq.nu;
-      int run = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += v;
-      }
-      lo = U + run - n;
-      U += __shfl_sync(0xffffffffu, run, 31);
-      segs += __reduce_add_sync(0xffffffffu, a.c.hkv * rq.nc);
-    }
-    // little work: whole segments to a CTA, or even parts of one, so that
-    // fewer parts are joined; else every CTA
-    int C = gridDim.x;
-    if (U < C * W * 2) C = min(C, segs * ((U + segs * W - 1) / max(1, segs * W)));
-    C = max(C, 1);
-    const int each = U / C, more = U - each * C;
-    const int u0 = (int)blockIdx.x < C ? (int)blockIdx.x * each + min((int)blockIdx.x, more) : U;
-    const int u1 = (int)blockIdx.x < C ? u0 + each + ((int)blockIdx.x < more) : U;
-    if (u0 < u1) {
-      int before = 0;
-      for (int base = 0; base < a.R; base += 32) {
-        if (a.R > 32) {
-          rq = {};
-          if (base + lane < a.R) rq = kv4_req<RT>(a, base + lane);
-          const int n = a.c.hkv * rq.nc * rq.nu;
-          int run = n;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, run, o);
-            if (lane >= o) run += v;
-          }
-          lo = before + run - n;
-          before += __shfl_sync(0xffffffffu, run, 31);
-        }
-        if (u0 >= lo && u0 < lo + a.c.hkv * rq.nc * rq.nu) {
-          s_r0 = base + lane;
-          s_s0 = (u0 - lo) / rq.nu;
-          s_seg0 = lo + s_s0 * rq.nu;
-        }
-        if (before > u0) break;
-      }
-    }
-    if (lane == 0) {
-      s_u0 = u0;
-      s_u1 = u1;
-      s_each = each;
-      s_more = more;
-      s_abort = 0;
-      s_join[0] = s_join[1] = Kv4Join{};
-    }
+  if (warp == 0) kv4_share<RT, 1>(a, W, sh);
+  if (tid == 0) {
+    s_abort = 0;
+    s_join[0] = s_join[1] = Kv4Join{};
   }
   if (lane == 0) {
     mbar_init(&s_bar[warp * 2], 1);
@@ -248,7 +87,7 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
     fence_mbar_init();
   }
   __syncthreads();
-  if (s_u0 >= s_u1) return;
+  if (sh.u0 >= sh.u1) return;
 
   uint64_t* const bar = s_bar + warp * 2;
   uint8_t* const ring = sm + warp * 2 * S::kStage;
@@ -256,8 +95,8 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
 
   // the segment at hand: unit range [ua, ub), of which the units from no on are
   // records.  A lane holds the address of every 32nd of the warp's records.
-  int r = s_r0, s = s_s0, seg = s_seg0;
-  const int u0 = s_u0, u1 = s_u1;
+  int r = sh.r0, s = sh.s0, seg = sh.seg0;
+  const int u0 = sh.u0, u1 = sh.u1;
   Kv4Req rq = kv4_req<RT>(a, r);
   int ua = u0 - seg, ub = min(rq.nu, u1 - seg);
   const uint8_t* addr;
@@ -297,8 +136,6 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
   const uint32_t sel_lo = e0 ? 0x1054u : 0x5410u, sel_hi = e0 ? 0x3276u : 0x7632u;
   const float sc2 = BIAS ? 1.f : a.s.scale * kLog2e;
 
-  const int each = s_each, extra = s_more, big = extra * (each + 1);
-  auto cta_of = [&](int u) { return u < big ? u / (each + 1) : extra + (u - big) / each; };
   for (bool first = true;; first = false) {
     const int h = s / rq.nc, rc = s - h * rq.nc;
     const int rows = min(RT, a.G * rq.m - rc * RT);
@@ -760,7 +597,7 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
       // Is this the last of the segment's CTAs to write its part?  Only the
       // warp with the fewest records waits for the answer, which is acted on
       // at this CTA's end: a part is the first of its segments or the last.
-      const int c0 = cta_of(this_seg), n = cta_of(this_seg + tq.nu - 1) - c0 + 1;
+      const int c0 = sh.cta_of(this_seg), n = sh.cta_of(this_seg + tq.nu - 1) - c0 + 1;
       const bool last = atomic_add_acq_rel(a.tickets + c0, 1) == n - 1;
       if (last) a.tickets[c0] = 0;
       s_join[more ? 0 : 1] = last ? Kv4Join{this_seg, n, c0, tq.n0, tq.m, h, rc} : Kv4Join{};
@@ -775,7 +612,7 @@ __global__ void __launch_bounds__(W * 32, NT <= 2 ? 2 : 1) k_kv4_attn(const __gr
     if (jn.n == 0) continue;
     const int rows = min(RT, a.G * jn.m - jn.rc * RT);
     // c0's part is its last segment's unless the segment begins its share
-    const int slot0 = 2 * jn.c0 + (jn.c0 * s_each + min(jn.c0, s_more) < jn.seg ? 1 : 0);
+    const int slot0 = 2 * jn.c0 + (sh.first(jn.c0) < jn.seg ? 1 : 0);
     auto part_of = [&](int c) { return a.part + (int64_t)(c == 0 ? slot0 : 2 * (jn.c0 + c)) * (RT * (D + 2)); };
     for (int i = tid; i < rows * (D / 2); i += W * 32) {
       const int row = i / (D / 2), x = i % (D / 2);
@@ -1114,7 +951,7 @@ static int launch_attn_tile(const Kv4AttnArgs& a, int64_t units, bool bias, cuda
       cudaFuncSetAttribute(k_kv4_attn<D, NT, W, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
       cudaFuncSetAttribute(k_kv4_attn<D, NT, W, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)};
   SD_CK(set[bias]);
-  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>({(NT <= 2 ? 2ll : 1ll) * num_sms(), kMaxCtas, units}));
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>({2ll * num_sms(), kMaxCtas, units}));
   kern<<<(unsigned)grid, W * 32, smem, st>>>(a);
   SD_CK(cudaGetLastError());
   return SD_OK;
@@ -1133,14 +970,15 @@ static int launch_observe(const Kv4ObserveArgs& b, int64_t units, bool bias, cud
   return SD_OK;
 }
 
-// Rows of a tile by the most rows that a (request, kv head) has; warps by what
-// the tile leaves in registers and shared memory.
+// Rows (query heads x nodes) that one kv head may have on the warp kernel;
+// more take the tensor cores.
+constexpr int kWarpRows = 16;
+
 template <int D>
 static int launch_attn(const Kv4AttnArgs& a, int rows, int64_t units, bool bias, cudaStream_t st) {
   if (rows <= 8) return launch_attn_tile<D, 1, 8>(a, units, bias, st);
-  if (rows <= 16) return launch_attn_tile<D, 2, 6>(a, units, bias, st);
-  if (rows <= 24) return launch_attn_tile<D, 3, 8>(a, units, bias, st);
-  return launch_attn_tile<D, 4, 8>(a, units, bias, st);
+  if (rows <= kWarpRows) return launch_attn_tile<D, 2, 6>(a, units, bias, st);
+  return kv4_launch_attn_tc(a, D, (units + 1) / 2, bias, st);
 }
 
 // ---------------------------------------------------------------- checks --
@@ -1178,7 +1016,9 @@ extern "C" size_t sd_kv4_attn_workspace(int32_t R, int32_t rows, int32_t n_q_hea
   if (R < 1 || rows < 0 || n_kv_heads < 1 || n_q_heads < n_kv_heads || n_q_heads % n_kv_heads ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  return kTicketBytes + (size_t)4 * num_sms() * 32 * (head_dim + 2) * sizeof(float);
+  const size_t warp = (size_t)4 * num_sms() * kWarpRows * (head_dim + 2) * sizeof(float);
+  const int most = std::min(rows, 64) * (n_q_heads / n_kv_heads);
+  return kTicketBytes + (most > kWarpRows ? std::max(warp, kv4_tc_workspace(head_dim)) : warp);
 }
 
 extern "C" int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride, int32_t n_q_heads, const int32_t* cu,

@@ -1,0 +1,192 @@
+// Attention over the 4-bit cache: what its kernels share.
+#pragma once
+
+#include "kv4.cuh"
+
+namespace sdv {
+
+struct Kv4AttnArgs {
+  Kv4View c;
+  Kv4Score s;
+  const uint16_t* q;
+  int64_t q_stride, kv_stride;
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  const int32_t* cu;
+  const uint64_t* anc;
+  const int32_t* row_pos;
+  int R, hq, G;
+  uint16_t* out;
+  float* lse;
+  int32_t* status;
+  int32_t* tickets;  // [grid], zero between calls
+  float* part;       // [2 grid][rows of a tile][D + 2]
+};
+
+__device__ __forceinline__ float kv4_score(const Kv4Score& s, float qk, float slope, int q_pos, int k_pos, int start) {
+  float t = qk * s.scale;
+  if (s.cap > 0.f) t = s.cap * tanhf(t / s.cap);
+  if (s.slopes) t = fmaf(slope, (float)(k_pos - q_pos), t);
+  if ((s.window > 0 && q_pos - k_pos >= s.window) || k_pos < start) t = -INFINITY;
+  return t;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+// 8x8 transpose of 16-bit values across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// The four nibbles of each 16-bit half of w as fp16 pairs, from two words (w
+// and w >> 8) and two masks: nibble i even lies at bits 0..3 and reads as the
+// subnormal code 2^-24, i odd at bits 4..7 and reads as code 2^-20.
+template <int I>
+__device__ __forceinline__ uint32_t codes2(uint32_t w) {
+  return (I < 2 ? w : w >> 8) & (I & 1 ? 0x00F000F0u : 0x000F000Fu);
+}
+// (code - 8) 2^-9 of the same pair: one fused multiply-add, exact.
+template <int I>
+__device__ __forceinline__ uint32_t centred2(uint32_t w) {
+  uint32_t y;
+  // 2^15 or 2^11, and -8 2^-9
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(codes2<I>(w)), "r"(I & 1 ? 0x68006800u : 0x78007800u), "r"(0xA400A400u));
+  return y;
+}
+__device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t y;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+  return y;
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+// What a call's requests hold, as the attention kernels split them: a request
+// is hkv x nc segments (kv head, tile of RT rows) of nu units each: the rows'
+// own keys in `no` runs of 32 GU, then the groups of 32 cached slots from group
+// g0 on, GU a unit; at least one unit, so that a row that sees nothing is
+// written too.
+struct Kv4Req {
+  int n0, m, ctx, g0, no, nu, nc;
+};
+
+template <int RT, int GU = 1>
+__device__ __forceinline__ Kv4Req kv4_req(const Kv4AttnArgs& a, int r) {
+  Kv4Req q;
+  q.n0 = a.cu[r];
+  q.m = min(max(a.cu[r + 1] - q.n0, 0), 64);
+  int ctx = a.c.ctx_len[r];
+  if (ctx < 0 || ctx > a.c.cap) {
+    set_status(a.status, SD_ERR_CAPACITY);
+    ctx = ctx < 0 ? 0 : (int)a.c.cap;
+  }
+  q.ctx = ctx;
+  int first = 0;
+  if (a.s.window > 0 || a.s.start) first = kv4_first(a.s, r, ctx, a.row_pos && q.m ? a.row_pos[q.n0] : ctx);
+  q.g0 = first / kKvGroup;
+  q.no = a.k_new ? (q.m + 32 * GU - 1) / (32 * GU) : 0;
+  q.nu = q.no + (ctx > first ? ((ctx - 1) / kKvGroup - q.g0 + GU) / GU : 0);
+  if (q.nu == 0) q.no = q.nu = 1;  // an empty run
+  q.nc = (a.G * q.m + RT - 1) / RT;
+  return q;
+}
+
+// A CTA's share of a call's units: U over C CTAs, the first `more` of them one
+// more than `each`; [u0, u1), beginning in segment s0 (first unit seg0) of
+// request r0.
+struct Kv4Share {
+  int r0, s0, seg0, u0, u1, each, more;
+  __device__ __forceinline__ int first(int c) const { return c * each + min(c, more); }
+  __device__ __forceinline__ int cta_of(int u) const {
+    const int big = more * (each + 1);
+    return u < big ? u / (each + 1) : more + (u - big) / each;
+  }
+};
+
+// By one warp, into shared memory.  With less work than 2 `width` units a CTA,
+// a CTA takes whole segments, or even parts of one of about `width` units, so
+// that fewer parts are joined; else every CTA takes its part.
+template <int RT, int GU>
+__device__ __forceinline__ void kv4_share(const Kv4AttnArgs& a, int width, Kv4Share& sh) {
+  const int lane = threadIdx.x & 31;
+  int U = 0, segs = 0, lo = 0;
+  Kv4Req rq = {};
+  for (int base = 0; base < a.R; base += 32) {
+    rq = {};
+    if (base + lane < a.R) rq = kv4_req<RT, GU>(a, base + lane);
+    const int n = a.c.hkv * rq.nc * rq.nu;
+    int run = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += v;
+    }
+    lo = U + run - n;
+    U += __shfl_sync(0xffffffffu, run, 31);
+    segs += __reduce_add_sync(0xffffffffu, a.c.hkv * rq.nc);
+  }
+  int C = gridDim.x;
+  if (U < C * width * 2) C = min(C, segs * ((U + segs * width - 1) / max(1, segs * width)));
+  C = max(C, 1);
+  const int each = U / C, more = U - each * C;
+  const int u0 = (int)blockIdx.x < C ? (int)blockIdx.x * each + min((int)blockIdx.x, more) : U;
+  const int u1 = (int)blockIdx.x < C ? u0 + each + ((int)blockIdx.x < more) : U;
+  if (u0 < u1) {
+    int before = 0;
+    for (int base = 0; base < a.R; base += 32) {
+      if (a.R > 32) {
+        rq = {};
+        if (base + lane < a.R) rq = kv4_req<RT, GU>(a, base + lane);
+        const int n = a.c.hkv * rq.nc * rq.nu;
+        int run = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, run, o);
+          if (lane >= o) run += v;
+        }
+        lo = before + run - n;
+        before += __shfl_sync(0xffffffffu, run, 31);
+      }
+      if (u0 >= lo && u0 < lo + a.c.hkv * rq.nc * rq.nu) {
+        sh.r0 = base + lane;
+        sh.s0 = (u0 - lo) / rq.nu;
+        sh.seg0 = lo + (u0 - lo) / rq.nu * rq.nu;
+      }
+      if (before > u0) break;
+    }
+  }
+  if (lane == 0) {
+    sh.u0 = u0;
+    sh.u1 = u1;
+    sh.each = each;
+    sh.more = more;
+  }
+}
+
+// A segment to join at a CTA's end: n parts (0: none) from CTA c0 on.
+struct Kv4Join {
+  int seg, n, c0, n0, m, h, rc;
+};
+
+// Many rows a kv head (kv4_attn_tc.cu).
+size_t kv4_tc_workspace(int head_dim);
+int kv4_launch_attn_tc(const Kv4AttnArgs& a, int head_dim, int64_t units, bool bias, cudaStream_t st);
+
+}  // namespace sdv

@@ -1,0 +1,720 @@
+// Attention over the 4-bit cache on the tensor cores (tcgen05 + TMEM), for
+// many rows a kv head: trees of many nodes, wide head groups.
+//
+// S = Q K^T and O += P V with up to two tiles t of 128 query rows, per tile of
+// 64 keys (two records).  Q lies in tensor memory for the whole segment, P
+// replaces S there, so the tensor core reads only K and V from shared memory:
+//   columns of tile t: [S or P 64][Q D/2][O D].
+// Warps, each role walking the CTA's units on its own:
+// (14 and 15 do nothing: they complete a warpgroup, whose registers the
+// softmax warps take over: 4 warps x 128 = 120 + 168 + 168 + 56 a scheduler.)
+//  * 12: records into a ring of eight, one bulk copy each;
+//  * 0..3: nibbles to fp16 operands.  K's codes as they are (subnormal code
+//    2^-24; the key's scale and middle are applied to its score, as in the
+//    warp kernel); V's as values, s (code - 8) + m in one fp16 multiply-add
+//    per pair, times a power of two that follows the greatest value (11 bits,
+//    against the output's 8).  The rows' own keys are a tile of 64 in the same
+//    form, bf16 to fp16 after a power of two per key;
+//  * 13: the products.  Two tiles of S and P alternate, so that one tile's
+//    softmax runs under the other's products.  With at most 128 rows both tiles
+//    hold the same rows and take alternate key tiles, two partial sums;
+//  * 4..11: softmax, a thread per row: scores of 64 keys from TMEM, maximum,
+//    exponentials, P back.  The running maximum may lag by 2^8 before O is
+//    rescaled in TMEM (fp16 P: exponentials are taken 2^5 up, at most 2^13).
+// Every segment's result goes through global parts (L2), joined by the CTA
+// itself or, where a segment spans CTAs, by the last of them to finish, in a
+// fixed order.
+//
+// Bound (D = 128, per 64 keys and two tiles): products 1024 cycles, softmax
+// issue about 900 per scheduler, decoding 160, shared memory about 1000.
+#include <algorithm>
+
+#include "kv4_attn.cuh"
+#include "tcgen05.cuh"
+
+namespace sdv {
+
+namespace kt {
+constexpr int kSoft = 4, kLoad = 12, kMma = 13, kThreads = 16 * 32;
+constexpr int kRaw = 8, kStages = 3;
+constexpr int kRows = 256;  // of a segment
+}  // namespace kt
+
+template <int D>
+struct TcShape {
+  static constexpr int kStage = kv4_rec(D) + 128;
+  static constexpr int kOp = 64 * D * 2;                             // 64 keys, fp16
+  static constexpr int off_raw = kt::kStages * 2 * kOp;              // [kRaw][kStage]
+  static constexpr int off_sc = off_raw + kt::kRaw * kStage;         // [kStages][64] (m / s - 8, s)
+  static constexpr int off_pos = off_sc + kt::kStages * 64 * 8;      // [kStages][64]
+  static constexpr int off_info = off_pos + kt::kStages * 64 * 4;    // [kStages] (keys held of either half, exponent of V)
+  static constexpr int off_bar = off_info + kt::kStages * 16;
+  static constexpr int off_ok = off_bar + (2 * kt::kRaw + 2 * kt::kStages + 8) * 8;
+  static constexpr int off_vmax = off_ok + kt::kRaw * 4;             // [4]
+  static constexpr int smem = off_vmax + 16 + 1024;
+  static constexpr int kPart = kt::kRows * (D + 2);                  // floats of a part: [2][128][D], then [2][128] (max, sum)
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+// D (tmem) (+)= A (tmem) * B (smem), fp16.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// B operand with its N side contiguous, 128-byte swizzle: rows of 64 values, 8
+// rows 1024 bytes, panels of 64 values 8192 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint32_t h2dup(float x) { return pack_f16x2(x, x); }
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t y;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+  return y;
+}
+// Exponent e of |x| < 2^(e+1); -127 of 0 and subnormals.
+__device__ __forceinline__ int expo(uint32_t bits) { return (int)(bits >> 23 & 255) - 127; }
+
+// A CTA's walk over its segments.
+struct TcWalk {
+  int r, s, seg, ua, ub;
+  Kv4Req rq;
+  __device__ __forceinline__ TcWalk(const Kv4AttnArgs& a, const Kv4Share& sh) : r(sh.r0), s(sh.s0), seg(sh.seg0) {
+    rq = kv4_req<kt::kRows, 2>(a, r);
+    ua = sh.u0 - seg;
+    ub = min(rq.nu, sh.u1 - seg);
+  }
+  __device__ __forceinline__ bool next(const Kv4AttnArgs& a, const Kv4Share& sh) {
+    seg += rq.nu;
+    if (seg >= sh.u1) return false;
+    if (++s == a.c.hkv * rq.nc) {
+      s = 0;
+      do rq = kv4_req<kt::kRows, 2>(a, ++r);
+      while (rq.nc == 0);
+    }
+    ua = 0;
+    ub = min(rq.nu, sh.u1 - seg);
+    return true;
+  }
+  __device__ __forceinline__ int head() const { return s / rq.nc; }
+  __device__ __forceinline__ int groups_end() const { return (rq.ctx + kKvGroup - 1) / kKvGroup; }
+  // groups of 32 keys of unit u
+  __device__ __forceinline__ int groups(const Kv4AttnArgs& a, int u) const {
+    if (u < rq.no) return a.k_new ? (rq.m + 31) / 32 : 1;
+    return min(2, groups_end() - (rq.g0 + 2 * (u - rq.no)));
+  }
+};
+
+// Rows of a segment: a request's G m rows in nc even runs.  At most 128: both
+// tiles hold them (alternate key tiles); else the first `split` are tile 0's.
+struct TcRowsOf {
+  int base, rows, split;
+  bool dual;
+  __device__ __forceinline__ TcRowsOf(int gm, int nc, int rc) {
+    const int run = ((gm + nc - 1) / nc + 31) / 32 * 32;
+    base = rc * run;
+    rows = min(run, gm - base);
+    dual = rows <= 128;
+    split = dual ? rows : (rows / 2 + 31) / 32 * 32;
+  }
+  __device__ __forceinline__ int of(int t) const { return dual || t == 0 ? split : rows - split; }
+  __device__ __forceinline__ int first(int t) const { return base + (dual || t == 0 ? 0 : split); }
+};
+
+// Joins the parts of a segment and writes its rows, by the 256 softmax threads.
+template <int D>
+__device__ __forceinline__ void tc_join(const Kv4AttnArgs& a, const Kv4Share& sh, const Kv4Join& jn, int slot0, int st) {
+  const int gm = a.G * jn.m, nc = (gm + kt::kRows - 1) / kt::kRows;
+  const TcRowsOf rw(gm, nc, jn.rc);
+  const int parts = rw.dual ? 2 * jn.n : jn.n;
+  for (int i = st; i < rw.rows * (D / 4); i += 256) {
+    const int row = i / (D / 4), x = i % (D / 4);
+    const int t0 = !rw.dual && row >= rw.split ? 1 : 0, idx = row - (t0 ? rw.split : 0);
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < parts; c += 4) {  // four parts in flight
+      float2 ml[4];
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const int p = min(c + k, parts - 1), cta = rw.dual ? p >> 1 : p, t = rw.dual ? p & 1 : t0;
+        const float* pc = a.part + (int64_t)(cta == 0 ? slot0 : 2 * (jn.c0 + cta)) * TcShape<D>::kPart;
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(pc + kt::kRows * D) + t * 128 + idx);
+        v[k] = __ldcg(reinterpret_cast<const float4*>(pc + (t * 128 + idx) * D) + x);
+      }
+      float Mn = M;
+#pragma unroll
+      for (int k = 0; k < 4; k++) Mn = fmaxf(Mn, ml[k].x);
+      const float Ms = Mn == -INFINITY ? 0.f : Mn, al = ex2(M - Ms);
+      M = Mn;
+      L *= al;
+      acc.x *= al, acc.y *= al, acc.z *= al, acc.w *= al;
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        if (c + k < parts) {
+          const float f = ex2(ml[k].x - Ms);
+          L = fmaf(f, ml[k].y, L);
+          acc.x = fmaf(f, v[k].x, acc.x);
+          acc.y = fmaf(f, v[k].y, acc.y);
+          acc.z = fmaf(f, v[k].z, acc.z);
+          acc.w = fmaf(f, v[k].w, acc.w);
+        }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int rho = rw.base + row, gq = rho / jn.m;
+    const int64_t at = (int64_t)(jn.n0 + rho - gq * jn.m) * a.hq + jn.h * a.G + gq;
+    *reinterpret_cast<uint2*>(a.out + at * D + 4 * x) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (x == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
+  }
+}
+
+template <int D, bool BIAS>
+__global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
+  using S = TcShape<D>;
+  constexpr int NS = kt::kStages;
+  extern __shared__ uint8_t smem_tc[];
+  uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_tc) + 1023) & ~uintptr_t(1023));
+  uint8_t* const raw = sm + S::off_raw;
+  float2* const s_sc = reinterpret_cast<float2*>(sm + S::off_sc);
+  int* const s_pos = reinterpret_cast<int*>(sm + S::off_pos);
+  int4* const s_info = reinterpret_cast<int4*>(sm + S::off_info);
+  uint64_t* const raw_full = reinterpret_cast<uint64_t*>(sm + S::off_bar);  // record landed
+  uint64_t* const raw_empty = raw_full + kt::kRaw;   // record decoded (4 warps)
+  uint64_t* const op_full = raw_empty + kt::kRaw;    // operands, scales written (4 warps)
+  uint64_t* const op_empty = op_full + NS;           // products done with them (commit)
+  uint64_t* const q_full = op_empty + NS;            // [t] queries in TMEM (4 warps)
+  uint64_t* const s_full = q_full + 2;               // [t] scores ready (commit)
+  uint64_t* const p_full = s_full + 2;               // [t] weights written (4 warps)
+  uint64_t* const o_full = p_full + 2;               // [t] the segment's last product done (commit)
+  int* const s_ok = reinterpret_cast<int*>(sm + S::off_ok);
+  uint32_t* const s_vmax = reinterpret_cast<uint32_t*>(sm + S::off_vmax);
+  __shared__ int s_abort;
+  __shared__ uint32_t s_tmem;
+  __shared__ Kv4Share sh;
+  __shared__ Kv4Join s_join[2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (warp == kt::kSoft) kv4_share<kt::kRows, 2>(a, 2, sh);
+  if (warp == kt::kMma) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kt::kRaw; i++) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 4);
+    for (int i = 0; i < NS; i++) mbar_init(&op_full[i], 4), mbar_init(&op_empty[i], 1);
+    for (int t = 0; t < 2; t++) {
+      mbar_init(&q_full[t], 4);
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);
+      mbar_init(&o_full[t], 1);
+    }
+    s_abort = 0;
+    s_join[0] = s_join[1] = Kv4Join{};
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = s_tmem;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!mbar_wait_or_abort(bar, parity & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(32));
+  };
+
+  if (sh.u0 >= sh.u1) {
+    // no work for this CTA
+  } else if (warp >= kt::kLoad) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == kt::kLoad) {
+      TcWalk w(a, sh);
+      uint32_t n = 0;
+      do {
+        const int h = w.head(), c0 = max(w.ua, w.rq.no);
+        const int ga = w.rq.g0 + 2 * (c0 - w.rq.no), gb = w.ub > c0 ? min(w.groups_end(), w.rq.g0 + 2 * (w.ub - w.rq.no)) : ga;
+        for (int base = ga; base < gb; base += 32) {
+          const uint8_t* addr = base + lane < gb ? a.c.record(D, w.r, h, base + lane) : nullptr;
+          for (int i = 0; i < 32 && base + i < gb; i++, n++) {
+            const uint8_t* rec = reinterpret_cast<const uint8_t*>(
+                __shfl_sync(0xffffffffu, (unsigned long long)reinterpret_cast<uintptr_t>(addr), i));
+            const int slot = n % kt::kRaw;
+            wait(&raw_empty[slot], (n / kt::kRaw & 1) ^ 1);
+            if (lane == 0) {
+              s_ok[slot] = rec != nullptr;
+              if (rec) {
+                uint8_t* dst = raw + slot * S::kStage;
+                mbar_arrive_expect_tx(&raw_full[slot], kv4_rec(D) + (BIAS ? 128 : 0));
+                bulk_g2s(dst, rec, kv4_rec(D), &raw_full[slot]);
+                if (BIAS) bulk_g2s(dst + kv4_rec(D), a.c.pos + a.c.slot0(w.r, h) + (base + i) * kKvGroup, 128, &raw_full[slot]);
+              } else {
+                set_status(a.status, SD_ERR_CAPACITY);
+                mbar_arrive(&raw_full[slot]);
+              }
+            }
+            __syncwarp();
+          }
+        }
+      } while (w.next(a, sh));
+    } else if (warp == kt::kMma) {
+      if (lane == 0) {
+        TcWalk w(a, sh);
+        const uint32_t id0 = (1u << 4) | (8u << 24);  // fp32 += fp16 fp16, M = 128
+        uint32_t op0 = 0, np[2] = {0, 0}, segs = 0;
+        do {
+          const int h = w.head();
+          const TcRowsOf rw(a.G * w.rq.m, w.rq.nc, w.s - h * w.rq.nc);
+          const int n = w.ub - w.ua;
+          auto scores = [&](int t, int i) {
+            const uint32_t st = (op0 + i) % NS;
+            wait(&op_full[st], (op0 + i) / NS);
+            tc_fence_after();
+            const uint64_t b = sdesc_sw128(smem_u32(sm + st * 2 * S::kOp));
+            const uint32_t id = id0 | ((uint32_t)(w.groups(a, w.ua + i) * 4) << 17);
+#pragma unroll
+            for (int k = 0; k < D / 16; k++)
+              umma_f16_ts(tm + t * 256, tm + t * 256 + 64 + 8 * k, b + (k >> 2) * (8192 >> 4) + (k & 3) * 2, id, k > 0);
+            umma_commit(&s_full[t]);
+          };
+          auto values = [&](int t, int i, bool first) {
+            wait(&p_full[t], np[t]++);
+            tc_fence_after();
+            const uint32_t st = (op0 + i) % NS;
+            const uint64_t b = sdesc_mn(smem_u32(sm + st * 2 * S::kOp + S::kOp));
+            const uint32_t id = id0 | (1u << 16) | ((uint32_t)(D / 8) << 17);
+            const int ks = 2 * w.groups(a, w.ua + i);
+            for (int k = 0; k < ks; k++)
+              umma_f16_ts(tm + t * 256 + 128, tm + t * 256 + 8 * k, b + k * (2048 >> 4), id, !first || k > 0);
+          };
+          wait(&q_full[0], segs);
+          wait(&q_full[1], segs);
+          tc_fence_after();
+          scores(0, 0);
+          if (rw.dual) {
+            if (n > 1) scores(1, 1);
+            for (int i = 0; i < n; i++) {
+              const int t = i & 1;
+              values(t, i, i < 2);
+              umma_commit(&op_empty[(op0 + i) % NS]);
+              if (i + 2 < n) scores(t, i + 2);
+              else umma_commit(&o_full[t]);
+            }
+          } else {
+            scores(1, 0);
+            for (int i = 0; i < n; i++) {
+              values(0, i, i == 0);
+              if (i + 1 < n) scores(0, i + 1);
+              else umma_commit(&o_full[0]);
+              values(1, i, i == 0);
+              umma_commit(&op_empty[(op0 + i) % NS]);
+              if (i + 1 < n) scores(1, i + 1);
+              else umma_commit(&o_full[1]);
+            }
+          }
+          op0 += n;
+          segs++;
+        } while (w.next(a, sh));
+      }
+      __syncwarp();
+    }
+  } else if (warp < kt::kSoft) {
+      // ------------------------------------------------------- operands --
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+      TcWalk w(a, sh);
+      uint32_t op = 0, nraw = 0;
+      do {
+        int E = -100;  // V operands are values times 2^-E, below 2^-6
+        const int h = w.head();
+        for (int u = w.ua; u < w.ub; u++, op++) {
+          const int st = op % NS;
+          uint8_t* const ko = sm + st * 2 * S::kOp;
+          uint8_t* const vo = ko + S::kOp;
+          wait(&op_empty[st], (op / NS & 1) ^ 1);
+          if (u >= w.rq.no) {
+            const int ga = w.rq.g0 + 2 * (u - w.rq.no), ng = w.groups(a, u);
+            int lim[2] = {0, 0};
+            const uint8_t* rec[2];
+            uint32_t vb = 0;
+#pragma unroll
+            for (int gi = 0; gi < 2; gi++) {
+              const uint32_t c = nraw + gi;
+              rec[gi] = raw + c % kt::kRaw * S::kStage;
+              if (gi >= ng) continue;
+              wait(&raw_full[c % kt::kRaw], c / kt::kRaw);
+              lim[gi] = s_ok[c % kt::kRaw] ? min(kKvGroup, w.rq.ctx - (ga + gi) * kKvGroup) : 0;
+              const uint32_t vw = *reinterpret_cast<const uint32_t*>(rec[gi] + kv4_half(D) + 16 * D + lane * 4);
+              const float b = fmaf(8.f, __uint_as_float(vw << 16), fabsf(__uint_as_float(vw & 0xFFFF0000u)));
+              if (lane < lim[gi] && b <= 3.4e38f) vb = max(vb, __float_as_uint(b));
+            }
+            E = min(max(E, expo(__reduce_max_sync(0xffffffffu, vb)) + 7), 120);
+            if (tid < 64) {
+              const int gi = tid >> 5;
+              float2 sc = make_float2(0.f, 0.f);
+              if (lane < (gi ? lim[1] : lim[0])) {
+                const uint8_t* rc = gi ? rec[1] : rec[0];
+                const uint32_t kw = *reinterpret_cast<const uint32_t*>(rc + 16 * D + lane * 4);
+                const uint32_t vw = *reinterpret_cast<const uint32_t*>(rc + kv4_half(D) + 16 * D + lane * 4);
+                const float s = __uint_as_float(kw << 16), m = __uint_as_float(kw & 0xFFFF0000u);
+                // a row of one value has s = 0 and every code 8: any s will do
+                sc.y = s == 0.f ? fmaxf(fabsf(m) * 0.0625f, 1e-30f) : s;
+                sc.x = m / sc.y - 8.f;
+                if (!(fabsf(__uint_as_float(vw << 16)) <= 3.4e38f)) sc.x = __int_as_float(0x7FC00000);  // V held as NaN
+                if (BIAS) s_pos[st * 64 + tid] = *reinterpret_cast<const int*>(rc + kv4_rec(D) + lane * 4);
+              }
+              s_sc[st * 64 + tid] = sc;
+            }
+            if (tid == 0) s_info[st] = make_int4(lim[0], lim[1], E, 0);
+            // eight lanes take four rows' neighbouring 16-byte pieces: two
+            // phases a read, none shared a write
+            const int row = 16 * (warp & 1) + 4 * (lane >> 3) + (lane >> 1 & 3);
+            const int cg = (D == 128 ? 2 * (warp >> 1) : 0) + (lane & 1);
+#pragma unroll
+            for (int gi = 0; gi < 2; gi++) {
+              if (gi >= ng) break;
+              const int R = gi * 32 + row;
+              const uint32_t at = (cg >> 1) * 8192 + R * 128;
+              if (D == 128 || warp < 2) {
+                const uint4 x = *reinterpret_cast<const uint4*>(rec[gi] + row * (D / 2) + cg * 16);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                  *reinterpret_cast<uint4*>(ko + at + ((((cg & 1) * 4 + j) ^ (R & 7)) << 4)) =
+                      make_uint4(codes2<0>(xs[j]), codes2<1>(xs[j]), codes2<2>(xs[j]), codes2<3>(xs[j]));
+              }
+              if (D == 128 || warp >= 2) {
+                const uint32_t vw = *reinterpret_cast<const uint32_t*>(rec[gi] + kv4_half(D) + 16 * D + row * 4);
+                float s = __uint_as_float(vw << 16), m = __uint_as_float(vw & 0xFFFF0000u);
+                if (row >= lim[gi] || !(s <= 3.4e38f)) s = m = 0.f;  // not held, or NaN: its scores say so
+                const float down = pow2i(-E);
+                const uint32_t me = h2dup(s * pow2i(24 - E)), mo = h2dup(s * pow2i(20 - E)),
+                               cc = h2dup(fmaf(-8.f, s, m) * down);
+                const uint4 x = *reinterpret_cast<const uint4*>(rec[gi] + kv4_half(D) + row * (D / 2) +
+                                                                (D == 128 ? cg ^ (row & 2) : cg) * 16);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                  *reinterpret_cast<uint4*>(vo + at + ((((cg & 1) * 4 + j) ^ (R & 7)) << 4)) =
+                      make_uint4(hfma2(codes2<0>(xs[j]), me, cc), hfma2(codes2<1>(xs[j]), mo, cc),
+                                 hfma2(codes2<2>(xs[j]), me, cc), hfma2(codes2<3>(xs[j]), mo, cc));
+              }
+            }
+            __syncwarp();
+            if (lane == 0)
+              for (int gi = 0; gi < ng; gi++) mbar_arrive(&raw_empty[(nraw + gi) % kt::kRaw]);
+            nraw += ng;
+          } else {
+            // the rows' own keys: two threads a row
+            const int j = tid >> 1, half = tid & 1;
+            const bool in = a.k_new && j < w.rq.m;
+            const int64_t off = (int64_t)(w.rq.n0 + j) * a.kv_stride + h * D + half * (D / 2);
+            uint4 x[D / 16];
+            uint32_t big = 0;
+#pragma unroll
+            for (int i = 0; i < D / 16; i++) {
+              x[i] = in ? *reinterpret_cast<const uint4*>(a.v_new + off + 8 * i) : make_uint4(0, 0, 0, 0);
+              const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+              for (int k = 0; k < 4; k++) big = max(big, max(xs[k] << 16 & 0x7FFF0000u, xs[k] & 0x7FFF0000u));
+            }
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            const bool odd = big >= 0x7F800000u;  // a NaN or an infinity
+            const uint32_t wm = __reduce_max_sync(0xffffffffu, odd ? 0u : big);
+            if (lane == 0) s_vmax[warp] = wm;
+            bar_sync(1, 128);
+            E = min(max(E, expo(max(max(s_vmax[0], s_vmax[1]), max(s_vmax[2], s_vmax[3]))) + 7), 120);
+            bar_sync(1, 128);
+            const float down = odd ? 0.f : pow2i(-E);
+#pragma unroll
+            for (int i = 0; i < D / 16; i++) {
+              const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+              float f[8];
+#pragma unroll
+              for (int k = 0; k < 4; k++) {
+                f[2 * k] = odd ? 0.f : __uint_as_float(xs[k] << 16) * down;
+                f[2 * k + 1] = odd ? 0.f : __uint_as_float(xs[k] & 0xFFFF0000u) * down;
+              }
+              const int c = half * (D / 16) + i;  // 16-byte piece of the row
+              *reinterpret_cast<uint4*>(vo + (c >> 3) * 8192 + j * 128 + (((c & 7) ^ (j & 7)) << 4)) =
+                  make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
+            }
+            big = 0;
+#pragma unroll
+            for (int i = 0; i < D / 16; i++) {
+              x[i] = in ? *reinterpret_cast<const uint4*>(a.k_new + off + 8 * i) : make_uint4(0, 0, 0, 0);
+              const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+              for (int k = 0; k < 4; k++) big = max(big, max(xs[k] << 16 & 0x7FFF0000u, xs[k] & 0x7FFF0000u));
+            }
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            const int e = min(max(10 - expo(big), -100), 100);  // the greatest below 2^11; odd dims 2^4 up
+            const float up = pow2i(e), up4 = pow2i(e + 4);
+#pragma unroll
+            for (int i = 0; i < D / 16; i++) {
+              const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+              float f[8];
+#pragma unroll
+              for (int k = 0; k < 4; k++) {
+                f[2 * k] = __uint_as_float(xs[k] << 16) * up;
+                f[2 * k + 1] = __uint_as_float(xs[k] & 0xFFFF0000u) * up4;
+              }
+              const int c = half * (D / 16) + i;
+              *reinterpret_cast<uint4*>(ko + (c >> 3) * 8192 + j * 128 + (((c & 7) ^ (j & 7)) << 4)) =
+                  make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
+            }
+            if (half == 0) {
+              s_sc[st * 64 + j] = make_float2(odd ? __int_as_float(0x7FC00000) : 0.f, pow2i(-24 - e));
+              if (BIAS && in) s_pos[st * 64 + j] = a.row_pos ? a.row_pos[w.rq.n0 + j] : w.rq.ctx + j;
+            }
+            const int m = a.k_new ? w.rq.m : 0;
+            if (tid == 0) s_info[st] = make_int4(min(m, 32), max(m - 32, 0), E, 1);
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&op_full[st]);
+        }
+      } while (w.next(a, sh));
+  } else {
+      // -------------------------------------------------------- softmax --
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+      TcWalk w(a, sh);
+      const int t = (warp - kt::kSoft) >> 2, ridx = (warp & 3) * 32 + lane, st256 = tid - kt::kSoft * 32;
+      const uint32_t tb = tm + t * 256 + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+      const float scale = BIAS ? 1.f : a.s.scale * kLog2e;
+      uint32_t op0 = 0, nsc = 0, nsum = 0;
+      do {
+        const int h = w.head(), rc = w.s - h * w.rq.nc, n = w.ub - w.ua;
+        const TcRowsOf rw(a.G * w.rq.m, w.rq.nc, rc);
+        const bool ok = ridx < rw.of(t);
+        const bool live = (warp & 3) * 32 < rw.of(t);  // the warp has rows
+        const int rho = rw.first(t) + (ok ? ridx : 0), gq = rho / w.rq.m, node = rho - gq * w.rq.m;
+        const int hq = h * a.G + gq;
+        const int start = BIAS && a.s.start ? a.s.start[w.r] : INT32_MIN;
+        const float slope = BIAS && a.s.slopes ? a.s.slopes[hq] : 0.f;
+        const int qpos = a.row_pos ? a.row_pos[w.rq.n0 + node] : w.rq.ctx + node;
+        const uint64_t anc = a.anc ? a.anc[w.rq.n0 + node] : (2ull << node) - 1;
+        float qsf, fac;
+        {
+          uint4 x[D / 8];
+          const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(w.rq.n0 + node) * a.q_stride + hq * D);
+          float qs = 0.f, big = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 8; i++) {
+            x[i] = ok ? src[i] : make_uint4(0, 0, 0, 0);
+            const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+              const float f0 = __uint_as_float(xs[k] << 16), f1 = __uint_as_float(xs[k] & 0xFFFF0000u);
+              qs += f0 + f1;
+              big = fmaxf(big, fmaxf(fabsf(f0), fabsf(f1)));
+            }
+          }
+          const int e = min(max(14 - expo(__float_as_uint(big)), -100), 100);
+          const float up = pow2i(e), up4 = pow2i(e - 4);
+          qsf = qs * pow2i(e - 24);
+          fac = pow2i(24 - e) * scale;
+          uint32_t y[32];
+#pragma unroll
+          for (int i = 0; i < D / 8; i++) {
+            const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+              f[2 * k] = __uint_as_float(xs[k] << 16) * up;
+              f[2 * k + 1] = __uint_as_float(xs[k] & 0xFFFF0000u) * up4;
+            }
+            y[4 * (i & 7)] = pack_f16x2(f[0], f[4]);
+            y[4 * (i & 7) + 1] = pack_f16x2(f[1], f[5]);
+            y[4 * (i & 7) + 2] = pack_f16x2(f[2], f[6]);
+            y[4 * (i & 7) + 3] = pack_f16x2(f[3], f[7]);
+            if ((i & 7) == 7) tmem_st32(tb + 64 + (i >> 3) * 32, y);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[t]);
+
+        float m = -INFINITY, l = 0.f;
+        int E = 0;
+        bool any = false;
+        for (int i = rw.dual ? t : 0; i < n; i += rw.dual ? 2 : 1) {
+          const uint32_t st = (op0 + i) % NS;
+          wait(&s_full[t], nsc++);
+          wait(&op_full[st], (op0 + i) / NS);
+          tc_fence_after();
+          const int4 info = s_info[st];
+          if (live) {
+            float x[64];
+            tmem_ld32(tb, x);
+            tmem_ld32(tb + 32, x + 32);
+            const float4* sc = reinterpret_cast<const float4*>(s_sc + st * 64);
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              const float4 v = sc[c / 2];
+              x[c] = fmaf(v.x, qsf, x[c]) * v.y;
+              x[c + 1] = fmaf(v.z, qsf, x[c + 1]) * v.w;
+            }
+            if (BIAS) {
+#pragma unroll
+              for (int c = 0; c < 64; c++)
+                x[c] = kv4_score(a.s, x[c] * fac, slope, qpos, s_pos[st * 64 + c], start) * kLog2e;
+            }
+            if (info.x < 32 || info.y < 32) {
+#pragma unroll
+              for (int c = 0; c < 32; c++) {
+                if (c >= info.x) x[c] = -INFINITY;
+                if (c >= info.y) x[c + 32] = -INFINITY;
+              }
+            }
+            if (info.w) {
+#pragma unroll
+              for (int c = 0; c < 64; c++)
+                if (!(anc >> c & 1)) x[c] = -INFINITY;
+            }
+#pragma unroll
+            for (int c = 0; c < 64; c++) top = fmaxf(top, x[c]);
+            const float f = BIAS ? 1.f : fac;
+            top *= f;  // f > 0
+            const bool grows = top > m + 8.f || (m == -INFINITY && top > m);
+            const bool moves = any && info.z != E;
+            if (__any_sync(0xffffffffu, grows) || moves) {
+              float al = 1.f;
+              if (grows) {
+                al = ex2(m - top);
+                m = top;
+                l *= al;
+              }
+              if (any) {
+                if (moves) al *= pow2i(max(E - info.z, -126));
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                  float o[32];
+                  tmem_ld32(tb + 128 + c, o);
+#pragma unroll
+                  for (int k = 0; k < 32; k++) o[k] *= al;
+                  tmem_st32(tb + 128 + c, reinterpret_cast<const uint32_t*>(o));
+                }
+              }
+            }
+            const float off = 5.f - (m == -INFINITY ? 0.f : m);
+            uint32_t p[32];
+            float l2 = 0.f;
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              const float p0 = ex2(fmaf(x[c], f, off)), p1 = ex2(fmaf(x[c + 1], f, off));
+              l += p0;
+              l2 += p1;
+              p[c / 2] = pack_f16x2(p0, p1);
+            }
+            l += l2;
+            tmem_st32(tb, p);
+          }
+          E = info.z;
+          any = true;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[t]);
+        }
+
+        // this tile's part
+        const bool whole = w.ua == 0 && w.ub == w.rq.nu;
+        const int slot = 2 * blockIdx.x + (w.seg + w.ua > sh.u0 ? 1 : 0);
+        float* part = a.part + (int64_t)slot * S::kPart;
+        if (any) {
+          wait(&o_full[t], nsum++);
+          tc_fence_after();
+        }
+        if (live) {
+          const float up = any ? pow2i(E) : 0.f;
+          float* dst = part + (t * 128 + ridx) * D;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            if (any) tmem_ld32(tb + 128 + c, o);
+            if (ok)
+#pragma unroll
+              for (int k = 0; k < 32; k += 8) {
+                float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+                if (any) {
+                  lo = make_float4(o[k] * up, o[k + 2] * up, o[k + 4] * up, o[k + 6] * up);
+                  hi = make_float4(o[k + 1] * up, o[k + 3] * up, o[k + 5] * up, o[k + 7] * up);
+                }
+                __stcg(reinterpret_cast<float4*>(dst + c + k), lo);
+                __stcg(reinterpret_cast<float4*>(dst + c + k) + 1, hi);
+              }
+          }
+          if (ok) __stcg(reinterpret_cast<float2*>(part + kt::kRows * D) + t * 128 + ridx, make_float2(m - 5.f, l));
+        }
+        tc_fence_before();
+        bar_sync(2, 256);
+        Kv4Join jn{w.seg, 1, (int)blockIdx.x, w.rq.n0, w.rq.m, h, rc};
+        if (whole) {
+          tc_join<D>(a, sh, jn, slot, st256);
+          bar_sync(2, 256);
+        } else if (st256 == 0) {
+          jn.c0 = sh.cta_of(w.seg);
+          jn.n = sh.cta_of(w.seg + w.rq.nu - 1) - jn.c0 + 1;
+          const bool last = atomic_add_acq_rel(a.tickets + jn.c0, 1) == jn.n - 1;
+          if (last) {
+            a.tickets[jn.c0] = 0;
+            s_join[w.seg + w.rq.nu < sh.u1 ? 0 : 1] = jn;
+          }
+        }
+        op0 += n;
+      } while (w.next(a, sh));
+      bar_sync(2, 256);
+      for (int d = 0; d < 2; d++) {
+        const Kv4Join jn = s_join[d];
+        if (jn.n) tc_join<D>(a, sh, jn, 2 * jn.c0 + (sh.first(jn.c0) < jn.seg ? 1 : 0), st256);
+      }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kt::kMma) {
+    tc_fence_after();
+    tmem_dealloc(tm, 512);
+  }
+}
+
+size_t kv4_tc_workspace(int head_dim) { return (size_t)2 * num_sms() * kt::kRows * (head_dim + 2) * sizeof(float); }
+
+template <int D>
+static int launch_tc(const Kv4AttnArgs& a, int64_t units, bool bias, cudaStream_t st) {
+  constexpr int smem = TcShape<D>::smem;
+  static const cudaError_t set[2] = {
+      cudaFuncSetAttribute(k_kv4_attn_tc<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+      cudaFuncSetAttribute(k_kv4_attn_tc<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)};
+  SD_CK(set[bias]);
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(num_sms(), units));
+  (bias ? k_kv4_attn_tc<D, true> : k_kv4_attn_tc<D, false>)<<<(unsigned)grid, kt::kThreads, smem, st>>>(a);
+  SD_CK(cudaGetLastError());
+  return SD_OK;
+}
+
+int kv4_launch_attn_tc(const Kv4AttnArgs& a, int head_dim, int64_t units, bool bias, cudaStream_t st) {
+  return head_dim == 128 ? launch_tc<128>(a, units, bias, st) : launch_tc<64>(a, units, bias, st);
+}
+
+}  // namespace sdv

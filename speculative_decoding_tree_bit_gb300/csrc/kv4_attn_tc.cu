@@ -1,33 +1,39 @@
 // Attention over the 4-bit cache on the tensor cores (tcgen05 + TMEM), for
 // many rows a kv head: trees of many nodes, wide head groups.
 //
-// S = Q K^T and O += P V with up to two tiles t of 128 query rows, per tile of
+// S = Q K^T and O += P V with two tiles t of up to 128 query rows, per tile of
 // 64 keys (two records).  Q lies in tensor memory for the whole segment, P
 // replaces S there, so the tensor core reads only K and V from shared memory:
 //   columns of tile t: [S or P 64][Q D/2][O D].
 // Warps, each role walking the CTA's units on its own:
-// (14 and 15 do nothing: they complete a warpgroup, whose registers the
-// softmax warps take over: 4 warps x 128 = 120 + 168 + 168 + 56 a scheduler.)
-//  * 12: records into a ring of eight, one bulk copy each;
+//  * 20: records into a ring of eight, one bulk copy each;
 //  * 0..3: nibbles to fp16 operands.  K's codes as they are (subnormal code
 //    2^-24; the key's scale and middle are applied to its score, as in the
 //    warp kernel); V's as values, s (code - 8) + m in one fp16 multiply-add
 //    per pair, times a power of two that follows the greatest value (11 bits,
 //    against the output's 8).  The rows' own keys are a tile of 64 in the same
 //    form, bf16 to fp16 after a power of two per key;
-//  * 13: the products.  Two tiles of S and P alternate, so that one tile's
-//    softmax runs under the other's products.  With at most 128 rows both tiles
-//    hold the same rows and take alternate key tiles, two partial sums;
-//  * 4..11: softmax, a thread per row: scores of 64 keys from TMEM, maximum,
-//    exponentials, P back.  The running maximum may lag by 2^8 before O is
-//    rescaled in TMEM (fp16 P: exponentials are taken 2^5 up, at most 2^13).
-// Every segment's result goes through global parts (L2), joined by the CTA
-// itself or, where a segment spans CTAs, by the last of them to finish, in a
+//  * 21: the products.  Two tiles of S and P alternate, so that one tile's
+//    softmax runs under the other's products;
+//  * 4..19: softmax, a thread per row and half of the 64 keys: scores from
+//    TMEM, maximum (exchanged with the other half's warp), exponentials, P
+//    back.  The running maximum may lag by 2^8 before O is rescaled in TMEM
+//    (fp16 P: exponentials are taken 2^5 up, at most 2^13).
+// (22 and 23 do nothing: they complete a warpgroup.  Registers a scheduler:
+// 6 warps x 80 = 88 + 4 x 88 + 40.)
+// With at most 128 rows both tiles hold the same rows and take alternate key
+// tiles.  With at most 64 (32) rows a tile holds them twice (four times), a
+// copy in other lanes taking half (a quarter) of the keys and leaving P 0 in
+// the others': the products cost the same, the softmax is shared by all
+// schedulers, each of which reaches only its quarter of the lanes.  The copies'
+// partial sums are added in shared memory at a segment's end; a segment that
+// spans CTAs is joined in global memory by the last of them to finish, in a
 // fixed order.
 //
 // Bound (D = 128, per 64 keys and two tiles): products 1024 cycles, softmax
-// issue about 900 per scheduler, decoding 160, shared memory about 1000.
+// issue about 1200 a scheduler, decoding 160, shared memory about 1000.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4_attn.cuh"
 #include "tcgen05.cuh"
@@ -35,7 +41,7 @@
 namespace sdv {
 
 namespace kt {
-constexpr int kSoft = 4, kLoad = 12, kMma = 13, kThreads = 16 * 32;
+constexpr int kSoft = 4, kLoad = 20, kMma = 21, kThreads = 24 * 32, kSoftThreads = 512;
 constexpr int kRaw = 8, kStages = 3;
 constexpr int kRows = 256;  // of a segment
 }  // namespace kt
@@ -51,30 +57,53 @@ struct TcShape {
   static constexpr int off_bar = off_info + kt::kStages * 16;
   static constexpr int off_ok = off_bar + (2 * kt::kRaw + 2 * kt::kStages + 8) * 8;
   static constexpr int off_vmax = off_ok + kt::kRaw * 4;             // [4]
-  static constexpr int smem = off_vmax + 16 + 1024;
-  static constexpr int kPart = kt::kRows * (D + 2);                  // floats of a part: [2][128][D], then [2][128] (max, sum)
+  static constexpr int off_top = off_vmax + 16;                      // [2 t][2 halves][128]
+  static constexpr int off_l = off_top + 4 * 128 * 4;                // [2 t][2 halves][128]
+  static constexpr int off_x = (off_l + 4 * 128 * 4 + 15) / 16 * 16;  // [2 t][128][kX] floats
+  static constexpr int kX = 68;
+  static constexpr int smem = off_x + 256 * kX * 4 + 1024;
+  static constexpr int kPart = kt::kRows * (D + 2);                  // floats of a part: [rows][D], then [rows] (max, sum)
 };
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+// N consecutive 32-bit columns of this thread's TMEM lane, waited for.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
       : "r"(taddr)
       : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
 }
 // D (tmem) (+)= A (tmem) * B (smem), fp16.
@@ -130,9 +159,10 @@ struct TcWalk {
 };
 
 // Rows of a segment: a request's G m rows in nc even runs.  At most 128: both
-// tiles hold them (alternate key tiles); else the first `split` are tile 0's.
+// tiles hold them; else the first `split` are tile 0's.  A tile's `copies` of
+// them lie 128 / copies lanes apart.
 struct TcRowsOf {
-  int base, rows, split;
+  int base, rows, split, copies;
   bool dual;
   __device__ __forceinline__ TcRowsOf(int gm, int nc, int rc) {
     const int run = ((gm + nc - 1) / nc + 31) / 32 * 32;
@@ -140,31 +170,30 @@ struct TcRowsOf {
     rows = min(run, gm - base);
     dual = rows <= 128;
     split = dual ? rows : (rows / 2 + 31) / 32 * 32;
+    copies = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
   }
   __device__ __forceinline__ int of(int t) const { return dual || t == 0 ? split : rows - split; }
   __device__ __forceinline__ int first(int t) const { return base + (dual || t == 0 ? 0 : split); }
 };
 
-// Joins the parts of a segment and writes its rows, by the 256 softmax threads.
+// Joins the parts of a segment and writes its rows, by the softmax threads.
 template <int D>
-__device__ __forceinline__ void tc_join(const Kv4AttnArgs& a, const Kv4Share& sh, const Kv4Join& jn, int slot0, int st) {
+__device__ __forceinline__ void tc_join(const Kv4AttnArgs& a, const Kv4Join& jn, int slot0, int st) {
   const int gm = a.G * jn.m, nc = (gm + kt::kRows - 1) / kt::kRows;
   const TcRowsOf rw(gm, nc, jn.rc);
-  const int parts = rw.dual ? 2 * jn.n : jn.n;
-  for (int i = st; i < rw.rows * (D / 4); i += 256) {
+  for (int i = st; i < rw.rows * (D / 4); i += kt::kSoftThreads) {
     const int row = i / (D / 4), x = i % (D / 4);
-    const int t0 = !rw.dual && row >= rw.split ? 1 : 0, idx = row - (t0 ? rw.split : 0);
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = 0; c < parts; c += 4) {  // four parts in flight
+    for (int c = 0; c < jn.n; c += 4) {  // four parts in flight
       float2 ml[4];
       float4 v[4];
 #pragma unroll
       for (int k = 0; k < 4; k++) {
-        const int p = min(c + k, parts - 1), cta = rw.dual ? p >> 1 : p, t = rw.dual ? p & 1 : t0;
-        const float* pc = a.part + (int64_t)(cta == 0 ? slot0 : 2 * (jn.c0 + cta)) * TcShape<D>::kPart;
-        ml[k] = __ldcg(reinterpret_cast<const float2*>(pc + kt::kRows * D) + t * 128 + idx);
-        v[k] = __ldcg(reinterpret_cast<const float4*>(pc + (t * 128 + idx) * D) + x);
+        const int p = min(c + k, jn.n - 1);
+        const float* pc = a.part + (int64_t)(p == 0 ? slot0 : 2 * (jn.c0 + p)) * TcShape<D>::kPart;
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(pc + kt::kRows * D) + row);
+        v[k] = __ldcg(reinterpret_cast<const float4*>(pc) + i);
       }
       float Mn = M;
 #pragma unroll
@@ -175,7 +204,7 @@ __device__ __forceinline__ void tc_join(const Kv4AttnArgs& a, const Kv4Share& sh
       acc.x *= al, acc.y *= al, acc.z *= al, acc.w *= al;
 #pragma unroll
       for (int k = 0; k < 4; k++)
-        if (c + k < parts) {
+        if (c + k < jn.n) {
           const float f = ex2(ml[k].x - Ms);
           L = fmaf(f, ml[k].y, L);
           acc.x = fmaf(f, v[k].x, acc.x);
@@ -193,6 +222,114 @@ __device__ __forceinline__ void tc_join(const Kv4AttnArgs& a, const Kv4Share& sh
   }
 }
 
+// A softmax thread's row in a segment, and what its loop leaves.
+struct TcRow {
+  float qsf, fac, slope;   // sum of q, factor of a score, slope
+  int qpos, start, lane0;  // position, document start, the copy's first key of a half
+  uint64_t anc;
+  bool live;               // the warp has rows
+  float m, l;
+  int E;                   // V's exponent in O
+  bool any;
+};
+
+// The softmax of one half of the keys of a segment's units of tile t, NC keys
+// of each (the copy's share).
+template <int D, bool BIAS, int NC>
+__device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint32_t tb, int t, int hf, int idx, int bar,
+                                           int i0, int n, int step, uint32_t op0, uint32_t& nsc, uint64_t* s_full,
+                                           uint64_t* op_full, uint64_t* p_full, const float2* s_sc, const int* s_pos,
+                                           const int4* s_info, float* s_top, int* s_abort) {
+  constexpr int NS = kt::kStages;
+  const int lane = threadIdx.x & 31;
+  const int k0 = hf * 32 + w.lane0;  // first key of this thread in a tile
+  for (int i = i0; i < n; i += step) {
+    const uint32_t st = (op0 + i) % NS;
+    if (!mbar_wait_or_abort(s_full, nsc++ & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(33));
+    if (!mbar_wait_or_abort(&op_full[st], (op0 + i) / NS & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(34));
+    tc_fence_after();
+    const int4 info = s_info[st];
+    if (w.live) {
+      float x[NC];
+      tmem_ld(tb + k0, x);
+      const float4* sc = reinterpret_cast<const float4*>(s_sc + st * 64 + k0);
+#pragma unroll
+      for (int c = 0; c < NC; c += 2) {
+        const float4 v = sc[c / 2];
+        x[c] = fmaf(v.x, w.qsf, x[c]) * v.y;
+        x[c + 1] = fmaf(v.z, w.qsf, x[c + 1]) * v.w;
+      }
+      if (BIAS) {
+#pragma unroll
+        for (int c = 0; c < NC; c++)
+          x[c] = kv4_score(a.s, x[c] * w.fac, w.slope, w.qpos, s_pos[st * 64 + k0 + c], w.start) * kLog2e;
+      }
+      const int lim = (hf ? info.y : info.x) - w.lane0;
+      if (lim < NC) {
+#pragma unroll
+        for (int c = 0; c < NC; c++)
+          if (c >= lim) x[c] = -INFINITY;
+      }
+      if (info.w) {
+        const uint32_t see = (uint32_t)(w.anc >> k0);
+#pragma unroll
+        for (int c = 0; c < NC; c++)
+          if (!(see >> c & 1)) x[c] = -INFINITY;
+      }
+      float t4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int c = 4; c < NC; c++) t4[c & 3] = fmaxf(t4[c & 3], x[c]);
+      const float f = BIAS ? 1.f : w.fac;
+      float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f;  // f > 0
+      s_top[hf * 128 + idx] = top;
+      bar_sync(bar, 64);  // every score of these lanes is read: P may replace them
+      top = fmaxf(top, s_top[(hf ^ 1) * 128 + idx]);
+      const bool grows = top > w.m + 8.f || (w.m == -INFINITY && top > w.m);
+      const bool moves = w.any && info.z != w.E;
+      if (__any_sync(0xffffffffu, grows) || moves) {
+        float al = 1.f;
+        if (grows) {
+          al = ex2(w.m - top);
+          w.m = top;
+          w.l *= al;
+        }
+        if (w.any) {
+          if (moves) al *= pow2i(max(w.E - info.z, -126));
+#pragma unroll 1
+          for (int c = 0; c < D / 2; c += 16) {
+            float o[16];
+            tmem_ld(tb + 128 + hf * (D / 2) + c, o);
+            uint32_t y[16];
+#pragma unroll
+            for (int k = 0; k < 16; k++) y[k] = __float_as_uint(o[k] * al);
+            tmem_st(tb + 128 + hf * (D / 2) + c, y);
+          }
+        }
+      }
+      const float off = 5.f - (w.m == -INFINITY ? 0.f : w.m);
+      uint32_t p[NC / 2];
+      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < NC; c += 2) {
+        const float p0 = ex2(fmaf(x[c], f, off)), p1 = ex2(fmaf(x[c + 1], f, off));
+        l4[c & 2] += p0;
+        l4[(c & 2) + 1] += p1;
+        p[c / 2] = pack_f16x2(p0, p1);
+      }
+      w.l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+      uint32_t y[16];
+#pragma unroll
+      for (int c = 0; c < 16; c++) y[c] = NC == 32 || c / (NC / 2) * NC == w.lane0 ? p[c % (NC / 2)] : 0u;
+      tmem_st(tb + hf * 16, y);
+    }
+    w.E = info.z;
+    w.any = true;
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(p_full);
+  }
+}
+
 template <int D, bool BIAS>
 __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
   using S = TcShape<D>;
@@ -207,19 +344,22 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   uint64_t* const raw_empty = raw_full + kt::kRaw;   // record decoded (4 warps)
   uint64_t* const op_full = raw_empty + kt::kRaw;    // operands, scales written (4 warps)
   uint64_t* const op_empty = op_full + NS;           // products done with them (commit)
-  uint64_t* const q_full = op_empty + NS;            // [t] queries in TMEM (4 warps)
+  uint64_t* const q_full = op_empty + NS;            // [t] queries in TMEM (8 warps)
   uint64_t* const s_full = q_full + 2;               // [t] scores ready (commit)
-  uint64_t* const p_full = s_full + 2;               // [t] weights written (4 warps)
+  uint64_t* const p_full = s_full + 2;               // [t] weights written (8 warps)
   uint64_t* const o_full = p_full + 2;               // [t] the segment's last product done (commit)
   int* const s_ok = reinterpret_cast<int*>(sm + S::off_ok);
   uint32_t* const s_vmax = reinterpret_cast<uint32_t*>(sm + S::off_vmax);
+  float* const s_top = reinterpret_cast<float*>(sm + S::off_top);
+  float* const s_l = reinterpret_cast<float*>(sm + S::off_l);
+  float* const s_x = reinterpret_cast<float*>(sm + S::off_x);
   __shared__ int s_abort;
   __shared__ uint32_t s_tmem;
   __shared__ Kv4Share sh;
   __shared__ Kv4Join s_join[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (warp == kt::kSoft) kv4_share<kt::kRows, 2>(a, 2, sh);
+  if (warp == kt::kSoft) kv4_share<kt::kRows, 2>(a, 4, sh);
   if (warp == kt::kMma) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
@@ -228,9 +368,9 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
     for (int i = 0; i < kt::kRaw; i++) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 4);
     for (int i = 0; i < NS; i++) mbar_init(&op_full[i], 4), mbar_init(&op_empty[i], 1);
     for (int t = 0; t < 2; t++) {
-      mbar_init(&q_full[t], 4);
+      mbar_init(&q_full[t], 8);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
+      mbar_init(&p_full[t], 8);
       mbar_init(&o_full[t], 1);
     }
     s_abort = 0;
@@ -248,7 +388,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   if (sh.u0 >= sh.u1) {
     // no work for this CTA
   } else if (warp >= kt::kLoad) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == kt::kLoad) {
       TcWalk w(a, sh);
       uint32_t n = 0;
@@ -341,7 +481,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
     }
   } else if (warp < kt::kSoft) {
       // ------------------------------------------------------- operands --
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
       TcWalk w(a, sh);
       uint32_t op = 0, nraw = 0;
       do {
@@ -497,197 +637,178 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
       } while (w.next(a, sh));
   } else {
       // -------------------------------------------------------- softmax --
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
       TcWalk w(a, sh);
-      const int t = (warp - kt::kSoft) >> 2, ridx = (warp & 3) * 32 + lane, st256 = tid - kt::kSoft * 32;
+      const int t = (warp - kt::kSoft) >> 3, hf = (warp - kt::kSoft) >> 2 & 1, st512 = tid - kt::kSoft * 32;
+      const int idx = (warp & 3) * 32 + lane;                                // TMEM lane
       const uint32_t tb = tm + t * 256 + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+      const int pair = 3 + t * 4 + (warp & 3);
       const float scale = BIAS ? 1.f : a.s.scale * kLog2e;
       uint32_t op0 = 0, nsc = 0, nsum = 0;
       do {
         const int h = w.head(), rc = w.s - h * w.rq.nc, n = w.ub - w.ua;
         const TcRowsOf rw(a.G * w.rq.m, w.rq.nc, rc);
-        const bool ok = ridx < rw.of(t);
-        const bool live = (warp & 3) * 32 < rw.of(t);  // the warp has rows
-        const int rho = rw.first(t) + (ok ? ridx : 0), gq = rho / w.rq.m, node = rho - gq * w.rq.m;
-        const int hq = h * a.G + gq;
-        const int start = BIAS && a.s.start ? a.s.start[w.r] : INT32_MIN;
-        const float slope = BIAS && a.s.slopes ? a.s.slopes[hq] : 0.f;
-        const int qpos = a.row_pos ? a.row_pos[w.rq.n0 + node] : w.rq.ctx + node;
-        const uint64_t anc = a.anc ? a.anc[w.rq.n0 + node] : (2ull << node) - 1;
-        float qsf, fac;
+        const int span = 128 / rw.copies;  // lanes of a copy
+        TcRow x;
         {
-          uint4 x[D / 8];
+          const int ridx = idx % span;
+          const bool ok = ridx < rw.of(t);
+          x.live = (ridx & ~31) < rw.of(t);
+          x.lane0 = idx / span * (32 / rw.copies);
+          const int rho = rw.first(t) + (ok ? ridx : 0), gq = rho / w.rq.m, node = rho - gq * w.rq.m;
+          const int hq = h * a.G + gq;
+          x.start = BIAS && a.s.start ? a.s.start[w.r] : INT32_MIN;
+          x.slope = BIAS && a.s.slopes ? a.s.slopes[hq] : 0.f;
+          x.qpos = a.row_pos ? a.row_pos[w.rq.n0 + node] : w.rq.ctx + node;
+          x.anc = a.anc ? a.anc[w.rq.n0 + node] : (2ull << node) - 1;
+          x.m = -INFINITY;
+          x.l = 0.f;
+          x.E = 0;
+          x.any = false;
+          // both halves' threads read the row; each puts its half in TMEM
           const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(w.rq.n0 + node) * a.q_stride + hq * D);
           float qs = 0.f, big = 0.f;
-#pragma unroll
+#pragma unroll 4
           for (int i = 0; i < D / 8; i++) {
-            x[i] = ok ? src[i] : make_uint4(0, 0, 0, 0);
-            const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            const uint4 v = ok ? src[i] : make_uint4(0, 0, 0, 0);
+            const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 4; k++) {
-              const float f0 = __uint_as_float(xs[k] << 16), f1 = __uint_as_float(xs[k] & 0xFFFF0000u);
+              const float f0 = __uint_as_float(vs[k] << 16), f1 = __uint_as_float(vs[k] & 0xFFFF0000u);
               qs += f0 + f1;
               big = fmaxf(big, fmaxf(fabsf(f0), fabsf(f1)));
             }
           }
           const int e = min(max(14 - expo(__float_as_uint(big)), -100), 100);
           const float up = pow2i(e), up4 = pow2i(e - 4);
-          qsf = qs * pow2i(e - 24);
-          fac = pow2i(24 - e) * scale;
-          uint32_t y[32];
+          x.qsf = qs * pow2i(e - 24);
+          x.fac = pow2i(24 - e) * scale;
 #pragma unroll
-          for (int i = 0; i < D / 8; i++) {
-            const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            float f[8];
+          for (int c = 0; c < D / 64; c++) {
+            uint32_t y[16];
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-              f[2 * k] = __uint_as_float(xs[k] << 16) * up;
-              f[2 * k + 1] = __uint_as_float(xs[k] & 0xFFFF0000u) * up4;
+            for (int i = 0; i < 4; i++) {
+              const uint4 v = ok ? src[hf * (D / 16) + c * 4 + i] : make_uint4(0, 0, 0, 0);
+              const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+              float f[8];
+#pragma unroll
+              for (int k = 0; k < 4; k++) {
+                f[2 * k] = __uint_as_float(vs[k] << 16) * up;
+                f[2 * k + 1] = __uint_as_float(vs[k] & 0xFFFF0000u) * up4;
+              }
+#pragma unroll
+              for (int k = 0; k < 4; k++) y[4 * i + k] = pack_f16x2(f[k], f[k + 4]);
             }
-            y[4 * (i & 7)] = pack_f16x2(f[0], f[4]);
-            y[4 * (i & 7) + 1] = pack_f16x2(f[1], f[5]);
-            y[4 * (i & 7) + 2] = pack_f16x2(f[2], f[6]);
-            y[4 * (i & 7) + 3] = pack_f16x2(f[3], f[7]);
-            if ((i & 7) == 7) tmem_st32(tb + 64 + (i >> 3) * 32, y);
+            tmem_st(tb + 64 + hf * (D / 4) + c * 16, y);
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
 
-        float m = -INFINITY, l = 0.f;
-        int E = 0;
-        bool any = false;
-        for (int i = rw.dual ? t : 0; i < n; i += rw.dual ? 2 : 1) {
-          const uint32_t st = (op0 + i) % NS;
-          wait(&s_full[t], nsc++);
-          wait(&op_full[st], (op0 + i) / NS);
-          tc_fence_after();
-          const int4 info = s_info[st];
-          if (live) {
-            float x[64];
-            tmem_ld32(tb, x);
-            tmem_ld32(tb + 32, x + 32);
-            const float4* sc = reinterpret_cast<const float4*>(s_sc + st * 64);
-            float top = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-              const float4 v = sc[c / 2];
-              x[c] = fmaf(v.x, qsf, x[c]) * v.y;
-              x[c + 1] = fmaf(v.z, qsf, x[c + 1]) * v.w;
-            }
-            if (BIAS) {
-#pragma unroll
-              for (int c = 0; c < 64; c++)
-                x[c] = kv4_score(a.s, x[c] * fac, slope, qpos, s_pos[st * 64 + c], start) * kLog2e;
-            }
-            if (info.x < 32 || info.y < 32) {
-#pragma unroll
-              for (int c = 0; c < 32; c++) {
-                if (c >= info.x) x[c] = -INFINITY;
-                if (c >= info.y) x[c + 32] = -INFINITY;
-              }
-            }
-            if (info.w) {
-#pragma unroll
-              for (int c = 0; c < 64; c++)
-                if (!(anc >> c & 1)) x[c] = -INFINITY;
-            }
-#pragma unroll
-            for (int c = 0; c < 64; c++) top = fmaxf(top, x[c]);
-            const float f = BIAS ? 1.f : fac;
-            top *= f;  // f > 0
-            const bool grows = top > m + 8.f || (m == -INFINITY && top > m);
-            const bool moves = any && info.z != E;
-            if (__any_sync(0xffffffffu, grows) || moves) {
-              float al = 1.f;
-              if (grows) {
-                al = ex2(m - top);
-                m = top;
-                l *= al;
-              }
-              if (any) {
-                if (moves) al *= pow2i(max(E - info.z, -126));
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                  float o[32];
-                  tmem_ld32(tb + 128 + c, o);
-#pragma unroll
-                  for (int k = 0; k < 32; k++) o[k] *= al;
-                  tmem_st32(tb + 128 + c, reinterpret_cast<const uint32_t*>(o));
-                }
-              }
-            }
-            const float off = 5.f - (m == -INFINITY ? 0.f : m);
-            uint32_t p[32];
-            float l2 = 0.f;
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-              const float p0 = ex2(fmaf(x[c], f, off)), p1 = ex2(fmaf(x[c + 1], f, off));
-              l += p0;
-              l2 += p1;
-              p[c / 2] = pack_f16x2(p0, p1);
-            }
-            l += l2;
-            tmem_st32(tb, p);
-          }
-          E = info.z;
-          any = true;
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[t]);
+        {
+          const int i0 = rw.dual ? t : 0, step = rw.dual ? 2 : 1;
+          auto run = [&](auto nc) {
+            tc_softmax<D, BIAS, decltype(nc)::value>(a, x, tb, t, hf, idx, pair, i0, n, step, op0, nsc, &s_full[t], op_full,
+                                                     &p_full[t], s_sc, s_pos, s_info, s_top + t * 256, &s_abort);
+          };
+          if (rw.copies == 1) run(std::integral_constant<int, 32>());
+          else if (rw.copies == 2) run(std::integral_constant<int, 16>());
+          else run(std::integral_constant<int, 8>());
         }
-
-        // this tile's part
-        const bool whole = w.ua == 0 && w.ub == w.rq.nu;
-        const int slot = 2 * blockIdx.x + (w.seg + w.ua > sh.u0 ? 1 : 0);
-        float* part = a.part + (int64_t)slot * S::kPart;
-        if (any) {
+        if (x.any) {
           wait(&o_full[t], nsum++);
           tc_fence_after();
         }
-        if (live) {
-          const float up = any ? pow2i(E) : 0.f;
-          float* dst = part + (t * 128 + ridx) * D;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            if (any) tmem_ld32(tb + 128 + c, o);
-            if (ok)
-#pragma unroll
-              for (int k = 0; k < 32; k += 8) {
-                float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
-                if (any) {
-                  lo = make_float4(o[k] * up, o[k + 2] * up, o[k + 4] * up, o[k + 6] * up);
-                  hi = make_float4(o[k + 1] * up, o[k + 3] * up, o[k + 5] * up, o[k + 7] * up);
-                }
-                __stcg(reinterpret_cast<float4*>(dst + c + k), lo);
-                __stcg(reinterpret_cast<float4*>(dst + c + k) + 1, hi);
-              }
+        // Add up the copies, 64 dims at a time, and write the rows: the outputs
+        // where the CTA has the whole segment, else a part.
+        const bool whole = w.ua == 0 && w.ub == w.rq.nu;
+        const int slot = 2 * blockIdx.x + (w.seg + w.ua > sh.u0 ? 1 : 0);
+        float* part = a.part + (int64_t)slot * S::kPart;
+        if (hf == 0) s_top[t * 256 + idx] = x.live ? x.m : -INFINITY;
+        s_l[t * 256 + hf * 128 + idx] = x.live ? x.l : 0.f;
+        bar_sync(2, kt::kSoftThreads);
+        const int tiles = rw.dual ? 2 : 1;
+        auto lane_of = [&](int row, int j) {  // copy j of a row: [t][lane]
+          const int tt = rw.dual ? j / rw.copies : row >= rw.split, c = rw.dual ? j % rw.copies : 0;
+          return tt * 256 + c * span + (!rw.dual && tt ? row - rw.split : row);
+        };
+        const int nsub = tiles * rw.copies;
+        float f;  // of this thread's O: its weight in the row's sum
+        {
+          const int ridx = idx % span;
+          float M = -INFINITY;
+          if (ridx < rw.of(t)) {
+            const int row = ridx + (!rw.dual && t ? rw.split : 0);
+            for (int j = 0; j < nsub; j++) M = fmaxf(M, s_top[lane_of(row, j)]);
           }
-          if (ok) __stcg(reinterpret_cast<float2*>(part + kt::kRows * D) + t * 128 + ridx, make_float2(m - 5.f, l));
+          f = x.any ? ex2(x.m - (M == -INFINITY ? 0.f : M)) * pow2i(x.E) : 0.f;
+        }
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += 32) {
+          if (x.live) {
+            float* dst = s_x + (t * 128 + idx) * S::kX + hf * 32;
+#pragma unroll
+            for (int k = 0; k < 32; k += 16) {
+              float o[16];
+              if (x.any) tmem_ld(tb + 128 + hf * (D / 2) + c + k, o);
+#pragma unroll
+              for (int e = 0; e < 16; e++) o[e] = x.any ? o[e] * f : 0.f;
+#pragma unroll
+              for (int e = 0; e < 16; e += 8) {  // columns hold dims 0 4 1 5 2 6 3 7 of each eight
+                *reinterpret_cast<float4*>(dst + k + e) = make_float4(o[e], o[e + 2], o[e + 4], o[e + 6]);
+                *reinterpret_cast<float4*>(dst + k + e + 4) = make_float4(o[e + 1], o[e + 3], o[e + 5], o[e + 7]);
+              }
+            }
+          }
+          bar_sync(2, kt::kSoftThreads);
+          for (int i = st512; i < rw.rows * 16; i += kt::kSoftThreads) {
+            const int row = i >> 4, x4 = i & 15;
+            const int d = (x4 >> 3) * (D / 2) + c + (x4 & 7) * 4;
+            float M = -INFINITY;
+            for (int j = 0; j < nsub; j++) M = fmaxf(M, s_top[lane_of(row, j)]);
+            const float Ms = M == -INFINITY ? 0.f : M;
+            float L = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j = 0; j < nsub; j++) {
+              const int at = lane_of(row, j);
+              L = fmaf(ex2(s_top[at] - Ms), s_l[at] + s_l[at + 128], L);
+              const float4 v = *reinterpret_cast<const float4*>(s_x + (at - (at >> 8) * 128) * S::kX + x4 * 4);
+              acc.x += v.x;
+              acc.y += v.y;
+              acc.z += v.z;
+              acc.w += v.w;
+            }
+            if (whole) {
+              const float inv = L == 0.f ? 0.f : 1.f / L;
+              const int rho = rw.base + row, gq = rho / w.rq.m;
+              const int64_t at = (int64_t)(w.rq.n0 + rho - gq * w.rq.m) * a.hq + h * a.G + gq;
+              *reinterpret_cast<uint2*>(a.out + at * D + d) =
+                  make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+              if (d == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M - 5.f + log2f(L)) * (1.f / kLog2e);
+            } else {
+              __stcg(reinterpret_cast<float4*>(part + row * D + d), acc);
+              if (d == 0) __stcg(reinterpret_cast<float2*>(part + kt::kRows * D) + row, make_float2(M - 5.f, L));
+            }
+          }
+          bar_sync(2, kt::kSoftThreads);
         }
         tc_fence_before();
-        bar_sync(2, 256);
-        Kv4Join jn{w.seg, 1, (int)blockIdx.x, w.rq.n0, w.rq.m, h, rc};
-        if (whole) {
-          tc_join<D>(a, sh, jn, slot, st256);
-          bar_sync(2, 256);
-        } else if (st256 == 0) {
-          jn.c0 = sh.cta_of(w.seg);
+        if (!whole && st512 == 0) {
+          // is this the last of the segment's CTAs?  Acted on at this CTA's end.
+          Kv4Join jn{w.seg, 0, sh.cta_of(w.seg), w.rq.n0, w.rq.m, h, rc};
           jn.n = sh.cta_of(w.seg + w.rq.nu - 1) - jn.c0 + 1;
-          const bool last = atomic_add_acq_rel(a.tickets + jn.c0, 1) == jn.n - 1;
-          if (last) {
+          if (atomic_add_acq_rel(a.tickets + jn.c0, 1) == jn.n - 1) {
             a.tickets[jn.c0] = 0;
             s_join[w.seg + w.rq.nu < sh.u1 ? 0 : 1] = jn;
           }
         }
         op0 += n;
       } while (w.next(a, sh));
-      bar_sync(2, 256);
+      bar_sync(2, kt::kSoftThreads);
       for (int d = 0; d < 2; d++) {
         const Kv4Join jn = s_join[d];
-        if (jn.n) tc_join<D>(a, sh, jn, 2 * jn.c0 + (sh.first(jn.c0) < jn.seg ? 1 : 0), st256);
+        if (jn.n) tc_join<D>(a, jn, 2 * jn.c0 + (sh.first(jn.c0) < jn.seg ? 1 : 0), st512);
       }
   }
   tc_fence_before();

@@ -19,8 +19,6 @@
 //    TMEM, maximum (exchanged with the other half's warp), exponentials, P
 //    back.  The running maximum may lag by 2^8 before O is rescaled in TMEM
 //    (fp16 P: exponentials are taken 2^5 up, at most 2^13).
-// (22 and 23 do nothing: they complete a warpgroup.  Registers a scheduler:
-// 6 warps x 80 = 88 + 4 x 88 + 40.)
 // With at most 128 rows both tiles hold the same rows and take alternate key
 // tiles.  With at most 64 (32) rows a tile holds them twice (four times), a
 // copy in other lanes taking half (a quarter) of the keys and leaving P 0 in
@@ -41,7 +39,7 @@
 namespace sdv {
 
 namespace kt {
-constexpr int kSoft = 4, kLoad = 20, kMma = 21, kThreads = 24 * 32, kSoftThreads = 512;
+constexpr int kSoft = 4, kLoad = 20, kMma = 21, kThreads = 22 * 32, kSoftThreads = 512;
 constexpr int kRaw = 8, kStages = 3;
 constexpr int kRows = 256;  // of a segment
 }  // namespace kt
@@ -388,7 +386,6 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   if (sh.u0 >= sh.u1) {
     // no work for this CTA
   } else if (warp >= kt::kLoad) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == kt::kLoad) {
       TcWalk w(a, sh);
       uint32_t n = 0;
@@ -419,7 +416,10 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
         }
       } while (w.next(a, sh));
     } else if (warp == kt::kMma) {
-      if (lane == 0) {
+      {
+        // the whole warp walks and waits; one lane, elected, issues: so the
+        // compiler keeps the operands in uniform registers (33 cycles a
+        // product of 64 columns, against 45 and more under lane == 0)
         TcWalk w(a, sh);
         const uint32_t id0 = (1u << 4) | (8u << 24);  // fp32 += fp16 fp16, M = 128
         uint32_t op0 = 0, np[2] = {0, 0}, segs = 0;
@@ -433,20 +433,33 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
             tc_fence_after();
             const uint64_t b = sdesc_sw128(smem_u32(sm + st * 2 * S::kOp));
             const uint32_t id = id0 | ((uint32_t)(w.groups(a, w.ua + i) * 4) << 17);
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < D / 16; k++)
-              umma_f16_ts(tm + t * 256, tm + t * 256 + 64 + 8 * k, b + (k >> 2) * (8192 >> 4) + (k & 3) * 2, id, k > 0);
-            umma_commit(&s_full[t]);
+              for (int k = 0; k < D / 16; k++)
+                umma_f16_ts(tm + t * 256, tm + t * 256 + 64 + 8 * k, b + (k >> 2) * (8192 >> 4) + (k & 3) * 2, id, k > 0);
+              umma_commit(&s_full[t]);
+            }
+            __syncwarp();
           };
-          auto values = [&](int t, int i, bool first) {
+          auto values = [&](int t, int i, bool first, bool release) {
             wait(&p_full[t], np[t]++);
             tc_fence_after();
             const uint32_t st = (op0 + i) % NS;
             const uint64_t b = sdesc_mn(smem_u32(sm + st * 2 * S::kOp + S::kOp));
             const uint32_t id = id0 | (1u << 16) | ((uint32_t)(D / 8) << 17);
-            const int ks = 2 * w.groups(a, w.ua + i);
-            for (int k = 0; k < ks; k++)
-              umma_f16_ts(tm + t * 256 + 128, tm + t * 256 + 8 * k, b + k * (2048 >> 4), id, !first || k > 0);
+            const bool two = w.groups(a, w.ua + i) == 2;
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 4; k++)
+                if (k < 2 || two)
+                  umma_f16_ts(tm + t * 256 + 128, tm + t * 256 + 8 * k, b + k * (2048 >> 4), id, !first || k > 0);
+              if (release) umma_commit(&op_empty[st]);
+            }
+            __syncwarp();
+          };
+          auto finish = [&](int t) {
+            if (elect_one()) umma_commit(&o_full[t]);
+            __syncwarp();
           };
           wait(&q_full[0], segs);
           wait(&q_full[1], segs);
@@ -456,21 +469,19 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
             if (n > 1) scores(1, 1);
             for (int i = 0; i < n; i++) {
               const int t = i & 1;
-              values(t, i, i < 2);
-              umma_commit(&op_empty[(op0 + i) % NS]);
+              values(t, i, i < 2, true);
               if (i + 2 < n) scores(t, i + 2);
-              else umma_commit(&o_full[t]);
+              else finish(t);
             }
           } else {
             scores(1, 0);
             for (int i = 0; i < n; i++) {
-              values(0, i, i == 0);
+              values(0, i, i == 0, false);
               if (i + 1 < n) scores(0, i + 1);
-              else umma_commit(&o_full[0]);
-              values(1, i, i == 0);
-              umma_commit(&op_empty[(op0 + i) % NS]);
+              else finish(0);
+              values(1, i, i == 0, true);
               if (i + 1 < n) scores(1, i + 1);
-              else umma_commit(&o_full[1]);
+              else finish(1);
             }
           }
           op0 += n;
@@ -481,7 +492,6 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
     }
   } else if (warp < kt::kSoft) {
       // ------------------------------------------------------- operands --
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
       TcWalk w(a, sh);
       uint32_t op = 0, nraw = 0;
       do {
@@ -637,7 +647,6 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
       } while (w.next(a, sh));
   } else {
       // -------------------------------------------------------- softmax --
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
       TcWalk w(a, sh);
       const int t = (warp - kt::kSoft) >> 3, hf = (warp - kt::kSoft) >> 2 & 1, st512 = tid - kt::kSoft * 32;
       const int idx = (warp & 3) * 32 + lane;                                // TMEM lane

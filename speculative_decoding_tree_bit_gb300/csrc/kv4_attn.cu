@@ -270,8 +270,9 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
             const uint64_t anc = s_anc[row];
             float ta = so[nt][e] * sc2, tb = so[nt][2 + e] * sc2;
             if (BIAS) {
-              ta = kv4_score(a.s, ta, s_slope[row], s_pos[row], kpa, start) * kLog2e;
-              tb = kv4_score(a.s, tb, s_slope[row], s_pos[row], kpb, start) * kLog2e;
+              float tt[2] = {ta, tb};
+              kv4_scores(a.s, tt, s_slope[row], s_pos[row], start, [&](int i) { return i ? kpb : kpa; });
+              ta = tt[0], tb = tt[1];
             }
             so[nt][e] = ja < rq.m && (anc >> ja & 1) ? ta : -INFINITY;
             so[nt][2 + e] = jb < rq.m && (anc >> jb & 1) ? tb : -INFINITY;
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
     for (int u = first_record(); u < ub; u += W) {
       const int stage = used & 1;
       const uint8_t* st = ring + stage * S::kStage;
-      if (!mbar_wait_or_abort(&bar[stage], (used >> 1) & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(30));
+      if (!kv4_wait(&bar[stage], (used >> 1) & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(30));
       // K: lane (g, q) holds dims q D/4 .. of keys g and g + 8 of a 16-key tile
 #pragma unroll
       for (int i = 0; i < 2; i++) {
@@ -395,6 +396,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
       // slots of this record that the request holds
       const int lim = s_ok[warp * 2 + stage] ? rq.ctx - (rq.g0 + u - rq.no) * kKvGroup : 0;
       float vs[4], vm[4];
+      int kp[4];
       float top[NT][2];
       uint32_t vb = 0;
 #pragma unroll
@@ -410,21 +412,33 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
         vs[i] = in ? __uint_as_float(vw << 16) : 0.f;
         vm[i] = in ? __uint_as_float(vw & 0xFFFF0000u) : 0.f;
         if (vs[i] == vs[i]) vb = max(vb, __float_as_uint(vs[i]));
-        const int kp = BIAS ? *reinterpret_cast<const int*>(st + kv4_rec(D) + kl * 4) : 0;
+        kp[i] = BIAS ? *reinterpret_cast<const int*>(st + kv4_rec(D) + kl * 4) : 0;
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
           for (int e = 0; e < 2; e++) {
             float& x = sc[i >> 1][nt][2 * (i & 1) + e];
-            float t = fmaf(ks, x * fac[nt][e], km * qs[nt][e]);
-            if (BIAS) {
-              const int row = nt * 8 + 2 * q + e;
-              t = kv4_score(a.s, t, s_slope[row], s_pos[row], kp, start) * kLog2e;
-            }
-            x = in ? t : -INFINITY;
-            top[nt][e] = fmaxf(top[nt][e], x);
+            x = fmaf(ks, x * fac[nt][e], km * qs[nt][e]);
           }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          if (BIAS) {
+            const int row = nt * 8 + 2 * q + e;
+            float t[4] = {sc[0][nt][e], sc[0][nt][2 + e], sc[1][nt][e], sc[1][nt][2 + e]};
+            kv4_scores(a.s, t, s_slope[row], s_pos[row], start, [&](int i) { return kp[i]; });
+#pragma unroll
+            for (int i = 0; i < 4; i++) sc[i >> 1][nt][2 * (i & 1) + e] = t[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            float& x = sc[i >> 1][nt][2 * (i & 1) + e];
+            x = 8 * i + g < lim ? x : -INFINITY;
+            top[nt][e] = fmaxf(top[nt][e], x);
+          }
+        }
       grow(top);
       if (__any_sync(0xffffffffu, vb > vtop)) {
         const uint32_t b = __reduce_max_sync(0xffffffffu, vb);
@@ -863,7 +877,7 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
         const uint8_t* st = ring + stage * S::kStage;
         const int t = x * kKvGroup + 8 * q + g;  // the slot whose sum this lane writes
         const float old = t < ctx ? (pass ? w_out[t] : b.decay * w_in[t]) : 0.f;
-        if (!mbar_wait_or_abort(&bar[stage], (used / NS) & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(31));
+        if (!kv4_wait(&bar[stage], (used / NS) & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(31));
         const bool ok = s_ok[warp * NS + stage] != 0;
         uint32_t kw[4][D / 32];
         float ks[4], km[4];
@@ -915,13 +929,13 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
             const int row = nt * 8 + 2 * q + e;
             const float4 rw = s_row[row];
             const float2 bi = BIAS ? s_bias[row] : make_float2(0.f, 0.f);
+            float v[4];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-              float v = (sc[i >> 1][0][2 * (i & 1) + e] + sc[i >> 1][1][2 * (i & 1) + e]) * rw.x;
-              v = fmaf(ks[i], v, km[i] * rw.y);
-              if (BIAS) v = kv4_score(a.s, v, bi.x, __float_as_int(bi.y), kp[i], start) * kLog2e;
-              sum[i] = fmaf(rw.w, ex2(v - rw.z), sum[i]);
-            }
+            for (int i = 0; i < 4; i++)
+              v[i] = fmaf(ks[i], (sc[i >> 1][0][2 * (i & 1) + e] + sc[i >> 1][1][2 * (i & 1) + e]) * rw.x, km[i] * rw.y);
+            if (BIAS) kv4_scores(a.s, v, bi.x, __float_as_int(bi.y), start, [&](int i) { return kp[i]; });
+#pragma unroll
+            for (int i = 0; i < 4; i++) sum[i] = fmaf(rw.w, ex2(v[i] - rw.z), sum[i]);
           }
         }
         float mine = 0.f;

@@ -43,12 +43,49 @@ __device__ __forceinline__ float capped(float t, float cap) {
   return u < 0.09f ? p : y;
 }
 
-__device__ __forceinline__ float kv4_score(const Kv4Score& s, float qk, float slope, int q_pos, int k_pos, int start) {
-  float t = qk * s.scale;
-  if (s.cap > 0.f) t = capped(t, s.cap);
-  if (s.slopes) t = fmaf(slope, (float)(k_pos - q_pos), t);
-  if ((s.window > 0 && q_pos - k_pos >= s.window) || k_pos < start) t = -INFINITY;
-  return t;
+// Scores of N keys from q.k (natural units in, base 2 out): cap, slope, masks.
+// The options' branches are outside the loops over the keys, which so overlap.
+// pos(i): position of key i.
+template <int N, typename Pos>
+__device__ __forceinline__ void kv4_scores(const Kv4Score& s, float (&t)[N], float slope, int q_pos, int start, Pos pos) {
+#pragma unroll
+  for (int i = 0; i < N; i++) t[i] *= s.scale;
+  if (s.cap > 0.f) {
+#pragma unroll
+    for (int i = 0; i < N; i++) t[i] = capped(t[i], s.cap);
+  }
+  if (s.slopes) {
+#pragma unroll
+    for (int i = 0; i < N; i++) t[i] = fmaf(slope, (float)(pos(i) - q_pos), t[i]);
+  }
+  if (s.window > 0 || s.start) {
+    const int64_t since = (int64_t)q_pos - (s.window > 0 ? s.window : INT32_MAX);
+    const int first = (int)max(since + 1, (int64_t)start);  // the least position seen
+#pragma unroll
+    for (int i = 0; i < N; i++)
+      if (pos(i) < first) t[i] = -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < N; i++) t[i] *= kLog2e;
+}
+
+// A bounded wait that looks at the clock and at the other warps' abort flag
+// only every so many tries: a try suspends the warp for a while by itself, and
+// reading the clock costs more than a wake-up.
+__device__ __forceinline__ bool kv4_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t addr = smem_u32(bar);
+  for (int i = 0; i < 64; i++)
+    if (mbar_try_wait(addr, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (;;) {
+    for (int i = 0; i < 64; i++)
+      if (mbar_try_wait(addr, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {

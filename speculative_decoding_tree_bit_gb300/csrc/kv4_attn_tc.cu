@@ -6,19 +6,20 @@
 // replaces S there, so the tensor core reads only K and V from shared memory:
 //   columns of tile t: [S or P 64][Q D/2][O D].
 // Warps, each role walking the CTA's units on its own:
-//  * 20: records into a ring of eight, one bulk copy each;
-//  * 0..3: nibbles to fp16 operands.  K's codes as they are (subnormal code
+//  * 16: records into a ring of eight, one bulk copy each;
+//  * 0..7: nibbles to fp16 operands, four warps a key tile, alternate tiles.  K's codes as they are (subnormal code
 //    2^-24; the key's scale and middle are applied to its score, as in the
 //    warp kernel); V's as values, s (code - 8) + m in one fp16 multiply-add
 //    per pair, times a power of two that follows the greatest value (11 bits,
 //    against the output's 8).  The rows' own keys are a tile of 64 in the same
 //    form, bf16 to fp16 after a power of two per key;
-//  * 21: the products.  Two tiles of S and P alternate, so that one tile's
+//  * 17: the products.  Two tiles of S and P alternate, so that one tile's
 //    softmax runs under the other's products;
-//  * 4..19: softmax, a thread per row and half of the 64 keys: scores from
-//    TMEM, maximum (exchanged with the other half's warp), exponentials, P
-//    back.  The running maximum may lag by 2^8 before O is rescaled in TMEM
-//    (fp16 P: exponentials are taken 2^5 up, at most 2^13).
+//  * 8..15: softmax, a thread per row: the scores of 64 keys from TMEM, maximum,
+//    exponentials, P back.  The running maximum may lag by 2^8 before O is
+//    rescaled in TMEM (fp16 P: exponentials are taken 2^5 up, at most 2^13).
+// (18 and 19 do nothing: they complete a warpgroup.  Registers a scheduler:
+// 5 warps x 96 = 2 x 64 decoding + 2 x 152 softmax + 48.)
 // With at most 128 rows both tiles hold the same rows and take alternate key
 // tiles.  With at most 64 (32) rows a tile holds them twice (four times), a
 // copy in other lanes taking half (a quarter) of the keys and leaving P 0 in
@@ -39,7 +40,7 @@
 namespace sdv {
 
 namespace kt {
-constexpr int kSoft = 4, kLoad = 20, kMma = 21, kThreads = 22 * 32, kSoftThreads = 512;
+constexpr int kSoft = 8, kLoad = 16, kMma = 17, kThreads = 20 * 32, kSoftThreads = 256;
 constexpr int kRaw = 8, kStages = 3;
 constexpr int kRows = 256;  // of a segment
 }  // namespace kt
@@ -49,31 +50,20 @@ struct TcShape {
   static constexpr int kStage = kv4_rec(D) + 128;
   static constexpr int kOp = 64 * D * 2;                             // 64 keys, fp16
   static constexpr int off_raw = kt::kStages * 2 * kOp;              // [kRaw][kStage]
-  static constexpr int off_sc = off_raw + kt::kRaw * kStage;         // [kStages][64] (m / s - 8, s)
+  static constexpr int off_sc = off_raw + kt::kRaw * kStage;         // [kStages][32] key pairs: (m / s - 8) twice, s twice
   static constexpr int off_pos = off_sc + kt::kStages * 64 * 8;      // [kStages][64]
-  static constexpr int off_info = off_pos + kt::kStages * 64 * 4;    // [kStages] (keys held of either half, exponent of V)
+  static constexpr int off_info = off_pos + kt::kStages * 64 * 4;    // [kStages] (keys held, masks of either half, exponent of V << 1 | own)
   static constexpr int off_bar = off_info + kt::kStages * 16;
   static constexpr int off_ok = off_bar + (2 * kt::kRaw + 2 * kt::kStages + 8) * 8;
-  static constexpr int off_vmax = off_ok + kt::kRaw * 4;             // [4]
-  static constexpr int off_top = off_vmax + 16;                      // [2 t][2 halves][128]
-  static constexpr int off_l = off_top + 4 * 128 * 4;                // [2 t][2 halves][128]
-  static constexpr int off_x = (off_l + 4 * 128 * 4 + 15) / 16 * 16;  // [2 t][128][kX] floats
+  static constexpr int off_vmax = off_ok + kt::kRaw * 4;             // [8]
+  static constexpr int off_ml = off_vmax + 32;                       // [2 t][128] (max, sum)
+  static constexpr int off_x = (off_ml + 256 * 8 + 15) / 16 * 16;    // [2 t][128][kX] floats
   static constexpr int kX = 68;
   static constexpr int smem = off_x + 256 * kX * 4 + 1024;
   static constexpr int kPart = kt::kRows * (D + 2);                  // floats of a part: [rows][D], then [rows] (max, sum)
 };
 
 // N consecutive 32-bit columns of this thread's TMEM lane, waited for.
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[8]) {
-  uint32_t r[8];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]);
-}
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[16]) {
   uint32_t r[16];
   asm volatile(
@@ -93,6 +83,16 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[64]) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; i++) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -117,6 +117,30 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
+// Pairs of fp32 values: one instruction for two.
+__device__ __forceinline__ uint64_t f2pack(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void f2unpack(uint64_t r, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+__device__ __forceinline__ uint64_t f2fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t h2dup(float x) { return pack_f16x2(x, x); }
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t y;
@@ -125,6 +149,11 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
 }
 // Exponent e of |x| < 2^(e+1); -127 of 0 and subnormals.
 __device__ __forceinline__ int expo(uint32_t bits) { return (int)(bits >> 23 & 255) - 127; }
+
+// Exponent that keeps a tile's V operands below 2^-6, a multiple of 4: the two
+// decoding groups keep one each, the greatest of their own tiles, and a change
+// from tile to tile costs a rescaling of O.
+__device__ __forceinline__ int tc_exponent(uint32_t bits) { return (expo(bits) + 7 + 3) & ~3; }
 
 // A CTA's walk over its segments.
 struct TcWalk {
@@ -223,7 +252,7 @@ __device__ __forceinline__ void tc_join(const Kv4AttnArgs& a, const Kv4Join& jn,
 // A softmax thread's row in a segment, and what its loop leaves.
 struct TcRow {
   float qsf, fac, slope;   // sum of q, factor of a score, slope
-  int qpos, start, lane0;  // position, document start, the copy's first key of a half
+  int qpos, start, key0;   // position, document start, the copy's first key of a tile
   uint64_t anc;
   bool live;               // the warp has rows
   float m, l;
@@ -231,45 +260,40 @@ struct TcRow {
   bool any;
 };
 
-// The softmax of one half of the keys of a segment's units of tile t, NC keys
-// of each (the copy's share).
+// The softmax of a segment's units of tile t, NC keys of each (the copy's share).
 template <int D, bool BIAS, int NC>
-__device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint32_t tb, int t, int hf, int idx, int bar,
-                                           int i0, int n, int step, uint32_t op0, uint32_t& nsc, uint64_t* s_full,
-                                           uint64_t* op_full, uint64_t* p_full, const float2* s_sc, const int* s_pos,
-                                           const int4* s_info, float* s_top, int* s_abort) {
+__device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint32_t tb, int i0, int n, int step,
+                                           uint32_t op0, uint32_t& nsc, uint64_t* s_full, uint64_t* op_full,
+                                           uint64_t* p_full, const float2* s_sc, const int* s_pos, const int4* s_info,
+                                           int* s_abort) {
   constexpr int NS = kt::kStages;
   const int lane = threadIdx.x & 31;
-  const int k0 = hf * 32 + w.lane0;  // first key of this thread in a tile
+#pragma unroll 1
   for (int i = i0; i < n; i += step) {
     const uint32_t st = (op0 + i) % NS;
-    if (!mbar_wait_or_abort(s_full, nsc++ & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(33));
-    if (!mbar_wait_or_abort(&op_full[st], (op0 + i) / NS & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(34));
+    if (!kv4_wait(s_full, nsc++ & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(33));
+    if (!kv4_wait(&op_full[st], (op0 + i) / NS & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(34));
     tc_fence_after();
     const int4 info = s_info[st];
     if (w.live) {
       float x[NC];
-      tmem_ld(tb + k0, x);
-      const float4* sc = reinterpret_cast<const float4*>(s_sc + st * 64 + k0);
+      tmem_ld(tb + w.key0, x);
+      const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(s_sc + st * 64 + w.key0);
+      const uint64_t qq = f2pack(w.qsf, w.qsf);
 #pragma unroll
       for (int c = 0; c < NC; c += 2) {
-        const float4 v = sc[c / 2];
-        x[c] = fmaf(v.x, w.qsf, x[c]) * v.y;
-        x[c + 1] = fmaf(v.z, w.qsf, x[c + 1]) * v.w;
+        const ulonglong2 v = sc[c / 2];
+        f2unpack(f2mul(f2fma(v.x, qq, f2pack(x[c], x[c + 1])), v.y), x[c], x[c + 1]);
       }
       if (BIAS) {
 #pragma unroll
-        for (int c = 0; c < NC; c++)
-          x[c] = kv4_score(a.s, x[c] * w.fac, w.slope, w.qpos, s_pos[st * 64 + k0 + c], w.start) * kLog2e;
+        for (int c = 0; c < NC; c++) x[c] *= w.fac;
+        const int* kp = s_pos + st * 64 + w.key0;
+        kv4_scores(a.s, x, w.slope, w.qpos, w.start, [&](int c) { return kp[c]; });
       }
-      const int lim = (hf ? info.y : info.x) - w.lane0;
-      if (lim < NC) {
-#pragma unroll
-        for (int c = 0; c < NC; c++)
-          if (c >= lim) x[c] = -INFINITY;
-      }
-      if (info.w) {
-        const uint32_t see = (uint32_t)(w.anc >> k0);
+      if (info.x < 64 || (info.w & 1)) {  // not every key is held, or the rows' own keys
+        const uint64_t held = (uint64_t)(uint32_t)info.z << 32 | (uint32_t)info.y;
+        const uint64_t see = (info.w & 1 ? held & w.anc : held) >> w.key0;
 #pragma unroll
         for (int c = 0; c < NC; c++)
           if (!(see >> c & 1)) x[c] = -INFINITY;
@@ -278,12 +302,10 @@ __device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint3
 #pragma unroll
       for (int c = 4; c < NC; c++) t4[c & 3] = fmaxf(t4[c & 3], x[c]);
       const float f = BIAS ? 1.f : w.fac;
-      float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f;  // f > 0
-      s_top[hf * 128 + idx] = top;
-      bar_sync(bar, 64);  // every score of these lanes is read: P may replace them
-      top = fmaxf(top, s_top[(hf ^ 1) * 128 + idx]);
+      const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f;  // f > 0
+      const int E = info.w >> 1;
       const bool grows = top > w.m + 8.f || (w.m == -INFINITY && top > w.m);
-      const bool moves = w.any && info.z != w.E;
+      const bool moves = w.any && E != w.E;
       if (__any_sync(0xffffffffu, grows) || moves) {
         float al = 1.f;
         if (grows) {
@@ -292,35 +314,46 @@ __device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint3
           w.l *= al;
         }
         if (w.any) {
-          if (moves) al *= pow2i(max(w.E - info.z, -126));
+          if (moves) al *= pow2i(max(w.E - E, -126));
 #pragma unroll 1
-          for (int c = 0; c < D / 2; c += 16) {
+          for (int c = 0; c < D; c += 16) {
             float o[16];
-            tmem_ld(tb + 128 + hf * (D / 2) + c, o);
+            tmem_ld(tb + 128 + c, o);
             uint32_t y[16];
 #pragma unroll
             for (int k = 0; k < 16; k++) y[k] = __float_as_uint(o[k] * al);
-            tmem_st(tb + 128 + hf * (D / 2) + c, y);
+            tmem_st(tb + 128 + c, y);
           }
         }
       }
       const float off = 5.f - (w.m == -INFINITY ? 0.f : w.m);
       uint32_t p[NC / 2];
-      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+      uint64_t l4[2] = {0, 0};
+      const uint64_t ff = f2pack(f, f), oo = f2pack(off, off);
 #pragma unroll
       for (int c = 0; c < NC; c += 2) {
-        const float p0 = ex2(fmaf(x[c], f, off)), p1 = ex2(fmaf(x[c + 1], f, off));
-        l4[c & 2] += p0;
-        l4[(c & 2) + 1] += p1;
+        float p0, p1;
+        f2unpack(f2fma(f2pack(x[c], x[c + 1]), ff, oo), p0, p1);
+        p0 = ex2(p0);
+        p1 = ex2(p1);
+        l4[c >> 1 & 1] = f2add(l4[c >> 1 & 1], f2pack(p0, p1));
         p[c / 2] = pack_f16x2(p0, p1);
       }
-      w.l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-      uint32_t y[16];
+      {
+        float l0, l1;
+        f2unpack(f2add(l4[0], l4[1]), l0, l1);
+        w.l += l0 + l1;
+      }
+      if constexpr (NC == 64) {
+        tmem_st(tb, p);
+      } else {
+        uint32_t y[32];
 #pragma unroll
-      for (int c = 0; c < 16; c++) y[c] = NC == 32 || c / (NC / 2) * NC == w.lane0 ? p[c % (NC / 2)] : 0u;
-      tmem_st(tb + hf * 16, y);
+        for (int c = 0; c < 32; c++) y[c] = c / (NC / 2) * NC == w.key0 ? p[c % (NC / 2)] : 0u;
+        tmem_st(tb, y);
+      }
     }
-    w.E = info.z;
+    w.E = info.w >> 1;
     w.any = true;
     tc_fence_before();
     __syncwarp();
@@ -342,14 +375,13 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   uint64_t* const raw_empty = raw_full + kt::kRaw;   // record decoded (4 warps)
   uint64_t* const op_full = raw_empty + kt::kRaw;    // operands, scales written (4 warps)
   uint64_t* const op_empty = op_full + NS;           // products done with them (commit)
-  uint64_t* const q_full = op_empty + NS;            // [t] queries in TMEM (8 warps)
+  uint64_t* const q_full = op_empty + NS;            // [t] queries in TMEM (4 warps)
   uint64_t* const s_full = q_full + 2;               // [t] scores ready (commit)
-  uint64_t* const p_full = s_full + 2;               // [t] weights written (8 warps)
+  uint64_t* const p_full = s_full + 2;               // [t] weights written (4 warps)
   uint64_t* const o_full = p_full + 2;               // [t] the segment's last product done (commit)
   int* const s_ok = reinterpret_cast<int*>(sm + S::off_ok);
   uint32_t* const s_vmax = reinterpret_cast<uint32_t*>(sm + S::off_vmax);
-  float* const s_top = reinterpret_cast<float*>(sm + S::off_top);
-  float* const s_l = reinterpret_cast<float*>(sm + S::off_l);
+  float2* const s_ml = reinterpret_cast<float2*>(sm + S::off_ml);
   float* const s_x = reinterpret_cast<float*>(sm + S::off_x);
   __shared__ int s_abort;
   __shared__ uint32_t s_tmem;
@@ -366,9 +398,9 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
     for (int i = 0; i < kt::kRaw; i++) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 4);
     for (int i = 0; i < NS; i++) mbar_init(&op_full[i], 4), mbar_init(&op_empty[i], 1);
     for (int t = 0; t < 2; t++) {
-      mbar_init(&q_full[t], 8);
+      mbar_init(&q_full[t], 4);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 8);
+      mbar_init(&p_full[t], 4);
       mbar_init(&o_full[t], 1);
     }
     s_abort = 0;
@@ -380,12 +412,13 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   tc_fence_after();
   const uint32_t tm = s_tmem;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!mbar_wait_or_abort(bar, parity & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(32));
+    if (!kv4_wait(bar, parity & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(32));
   };
 
   if (sh.u0 >= sh.u1) {
     // no work for this CTA
   } else if (warp >= kt::kLoad) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == kt::kLoad) {
       TcWalk w(a, sh);
       uint32_t n = 0;
@@ -492,12 +525,19 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
     }
   } else if (warp < kt::kSoft) {
       // ------------------------------------------------------- operands --
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
       TcWalk w(a, sh);
+      // group dg takes the even or the odd tiles of the CTA's walk
+      const int dg = warp >> 2, dt = tid & 127, dw = warp & 3;
       uint32_t op = 0, nraw = 0;
       do {
         int E = -100;  // V operands are values times 2^-E, below 2^-6
         const int h = w.head();
         for (int u = w.ua; u < w.ub; u++, op++) {
+          if ((op & 1) != dg) {
+            if (u >= w.rq.no) nraw += w.groups(a, u);
+            continue;
+          }
           const int st = op % NS;
           uint8_t* const ko = sm + st * 2 * S::kOp;
           uint8_t* const vo = ko + S::kOp;
@@ -513,14 +553,14 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
               rec[gi] = raw + c % kt::kRaw * S::kStage;
               if (gi >= ng) continue;
               wait(&raw_full[c % kt::kRaw], c / kt::kRaw);
-              lim[gi] = s_ok[c % kt::kRaw] ? min(kKvGroup, w.rq.ctx - (ga + gi) * kKvGroup) : 0;
+              lim[gi] = s_ok[c % kt::kRaw] ? max(0, min(kKvGroup, w.rq.ctx - (ga + gi) * kKvGroup)) : 0;
               const uint32_t vw = *reinterpret_cast<const uint32_t*>(rec[gi] + kv4_half(D) + 16 * D + lane * 4);
               const float b = fmaf(8.f, __uint_as_float(vw << 16), fabsf(__uint_as_float(vw & 0xFFFF0000u)));
               if (lane < lim[gi] && b <= 3.4e38f) vb = max(vb, __float_as_uint(b));
             }
-            E = min(max(E, expo(__reduce_max_sync(0xffffffffu, vb)) + 7), 120);
-            if (tid < 64) {
-              const int gi = tid >> 5;
+            E = min(max(E, tc_exponent(__reduce_max_sync(0xffffffffu, vb))), 120);
+            if (dt < 64) {
+              const int gi = dt >> 5;
               float2 sc = make_float2(0.f, 0.f);
               if (lane < (gi ? lim[1] : lim[0])) {
                 const uint8_t* rc = gi ? rec[1] : rec[0];
@@ -531,21 +571,23 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
                 sc.y = s == 0.f ? fmaxf(fabsf(m) * 0.0625f, 1e-30f) : s;
                 sc.x = m / sc.y - 8.f;
                 if (!(fabsf(__uint_as_float(vw << 16)) <= 3.4e38f)) sc.x = __int_as_float(0x7FC00000);  // V held as NaN
-                if (BIAS) s_pos[st * 64 + tid] = *reinterpret_cast<const int*>(rc + kv4_rec(D) + lane * 4);
+                if (BIAS) s_pos[st * 64 + dt] = *reinterpret_cast<const int*>(rc + kv4_rec(D) + lane * 4);
               }
-              s_sc[st * 64 + tid] = sc;
+              reinterpret_cast<float*>(s_sc + st * 64)[(dt >> 1) * 4 + (dt & 1)] = sc.x;
+              reinterpret_cast<float*>(s_sc + st * 64)[(dt >> 1) * 4 + 2 + (dt & 1)] = sc.y;
             }
-            if (tid == 0) s_info[st] = make_int4(lim[0], lim[1], E, 0);
+            if (dt == 0)
+              s_info[st] = make_int4(lim[0] + lim[1], lim[0] == 32 ? -1 : (1 << lim[0]) - 1, lim[1] == 32 ? -1 : (1 << lim[1]) - 1, E * 2);
             // eight lanes take four rows' neighbouring 16-byte pieces: two
             // phases a read, none shared a write
-            const int row = 16 * (warp & 1) + 4 * (lane >> 3) + (lane >> 1 & 3);
-            const int cg = (D == 128 ? 2 * (warp >> 1) : 0) + (lane & 1);
+            const int row = 16 * (dw & 1) + 4 * (lane >> 3) + (lane >> 1 & 3);
+            const int cg = (D == 128 ? 2 * (dw >> 1) : 0) + (lane & 1);
 #pragma unroll
             for (int gi = 0; gi < 2; gi++) {
               if (gi >= ng) break;
               const int R = gi * 32 + row;
               const uint32_t at = (cg >> 1) * 8192 + R * 128;
-              if (D == 128 || warp < 2) {
+              if (D == 128 || dw < 2) {
                 const uint4 x = *reinterpret_cast<const uint4*>(rec[gi] + row * (D / 2) + cg * 16);
                 const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -553,7 +595,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
                   *reinterpret_cast<uint4*>(ko + at + ((((cg & 1) * 4 + j) ^ (R & 7)) << 4)) =
                       make_uint4(codes2<0>(xs[j]), codes2<1>(xs[j]), codes2<2>(xs[j]), codes2<3>(xs[j]));
               }
-              if (D == 128 || warp >= 2) {
+              if (D == 128 || dw >= 2) {
                 const uint32_t vw = *reinterpret_cast<const uint32_t*>(rec[gi] + kv4_half(D) + 16 * D + row * 4);
                 float s = __uint_as_float(vw << 16), m = __uint_as_float(vw & 0xFFFF0000u);
                 if (row >= lim[gi] || !(s <= 3.4e38f)) s = m = 0.f;  // not held, or NaN: its scores say so
@@ -576,7 +618,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
             nraw += ng;
           } else {
             // the rows' own keys: two threads a row
-            const int j = tid >> 1, half = tid & 1;
+            const int j = dt >> 1, half = dt & 1;
             const bool in = a.k_new && j < w.rq.m;
             const int64_t off = (int64_t)(w.rq.n0 + j) * a.kv_stride + h * D + half * (D / 2);
             uint4 x[D / 16];
@@ -592,9 +634,9 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
             const bool odd = big >= 0x7F800000u;  // a NaN or an infinity
             const uint32_t wm = __reduce_max_sync(0xffffffffu, odd ? 0u : big);
             if (lane == 0) s_vmax[warp] = wm;
-            bar_sync(1, 128);
-            E = min(max(E, expo(max(max(s_vmax[0], s_vmax[1]), max(s_vmax[2], s_vmax[3]))) + 7), 120);
-            bar_sync(1, 128);
+            bar_sync(1 + dg * 10, 128);
+            E = min(max(E, tc_exponent(max(max(s_vmax[4 * dg], s_vmax[4 * dg + 1]), max(s_vmax[4 * dg + 2], s_vmax[4 * dg + 3])))), 120);
+            bar_sync(1 + dg * 10, 128);
             const float down = odd ? 0.f : pow2i(-E);
 #pragma unroll
             for (int i = 0; i < D / 16; i++) {
@@ -634,11 +676,13 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
                   make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
             }
             if (half == 0) {
-              s_sc[st * 64 + j] = make_float2(odd ? __int_as_float(0x7FC00000) : 0.f, pow2i(-24 - e));
+              reinterpret_cast<float*>(s_sc + st * 64)[(j >> 1) * 4 + (j & 1)] = odd ? __int_as_float(0x7FC00000) : 0.f;
+              reinterpret_cast<float*>(s_sc + st * 64)[(j >> 1) * 4 + 2 + (j & 1)] = pow2i(-24 - e);
               if (BIAS && in) s_pos[st * 64 + j] = a.row_pos ? a.row_pos[w.rq.n0 + j] : w.rq.ctx + j;
             }
             const int m = a.k_new ? w.rq.m : 0;
-            if (tid == 0) s_info[st] = make_int4(min(m, 32), max(m - 32, 0), E, 1);
+            if (dt == 0)
+              s_info[st] = make_int4(m, m >= 32 ? -1 : (1 << m) - 1, m >= 64 ? -1 : m > 32 ? (1 << (m - 32)) - 1 : 0, E * 2 + 1);
           }
           fence_async_smem();
           __syncwarp();
@@ -647,11 +691,11 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
       } while (w.next(a, sh));
   } else {
       // -------------------------------------------------------- softmax --
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
       TcWalk w(a, sh);
-      const int t = (warp - kt::kSoft) >> 3, hf = (warp - kt::kSoft) >> 2 & 1, st512 = tid - kt::kSoft * 32;
+      const int t = (warp - kt::kSoft) >> 2, st256 = tid - kt::kSoft * 32;
       const int idx = (warp & 3) * 32 + lane;                                // TMEM lane
       const uint32_t tb = tm + t * 256 + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
-      const int pair = 3 + t * 4 + (warp & 3);
       const float scale = BIAS ? 1.f : a.s.scale * kLog2e;
       uint32_t op0 = 0, nsc = 0, nsum = 0;
       do {
@@ -663,7 +707,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
           const int ridx = idx % span;
           const bool ok = ridx < rw.of(t);
           x.live = (ridx & ~31) < rw.of(t);
-          x.lane0 = idx / span * (32 / rw.copies);
+          x.key0 = idx / span * (64 / rw.copies);
           const int rho = rw.first(t) + (ok ? ridx : 0), gq = rho / w.rq.m, node = rho - gq * w.rq.m;
           const int hq = h * a.G + gq;
           x.start = BIAS && a.s.start ? a.s.start[w.r] : INT32_MIN;
@@ -674,7 +718,6 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
           x.l = 0.f;
           x.E = 0;
           x.any = false;
-          // both halves' threads read the row; each puts its half in TMEM
           const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(w.rq.n0 + node) * a.q_stride + hq * D);
           float qs = 0.f, big = 0.f;
 #pragma unroll 4
@@ -693,11 +736,11 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
           x.qsf = qs * pow2i(e - 24);
           x.fac = pow2i(24 - e) * scale;
 #pragma unroll
-          for (int c = 0; c < D / 64; c++) {
+          for (int c = 0; c < D / 32; c++) {
             uint32_t y[16];
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-              const uint4 v = ok ? src[hf * (D / 16) + c * 4 + i] : make_uint4(0, 0, 0, 0);
+              const uint4 v = ok ? src[c * 4 + i] : make_uint4(0, 0, 0, 0);
               const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
               float f[8];
 #pragma unroll
@@ -708,7 +751,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
 #pragma unroll
               for (int k = 0; k < 4; k++) y[4 * i + k] = pack_f16x2(f[k], f[k + 4]);
             }
-            tmem_st(tb + 64 + hf * (D / 4) + c * 16, y);
+            tmem_st(tb + 64 + c * 16, y);
           }
         }
         tc_fence_before();
@@ -718,12 +761,12 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
         {
           const int i0 = rw.dual ? t : 0, step = rw.dual ? 2 : 1;
           auto run = [&](auto nc) {
-            tc_softmax<D, BIAS, decltype(nc)::value>(a, x, tb, t, hf, idx, pair, i0, n, step, op0, nsc, &s_full[t], op_full,
-                                                     &p_full[t], s_sc, s_pos, s_info, s_top + t * 256, &s_abort);
+            tc_softmax<D, BIAS, decltype(nc)::value>(a, x, tb, i0, n, step, op0, nsc, &s_full[t], op_full, &p_full[t], s_sc,
+                                                     s_pos, s_info, &s_abort);
           };
-          if (rw.copies == 1) run(std::integral_constant<int, 32>());
-          else if (rw.copies == 2) run(std::integral_constant<int, 16>());
-          else run(std::integral_constant<int, 8>());
+          if (rw.copies == 1) run(std::integral_constant<int, 64>());
+          else if (rw.copies == 2) run(std::integral_constant<int, 32>());
+          else run(std::integral_constant<int, 16>());
         }
         if (x.any) {
           wait(&o_full[t], nsum++);
@@ -734,13 +777,12 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
         const bool whole = w.ua == 0 && w.ub == w.rq.nu;
         const int slot = 2 * blockIdx.x + (w.seg + w.ua > sh.u0 ? 1 : 0);
         float* part = a.part + (int64_t)slot * S::kPart;
-        if (hf == 0) s_top[t * 256 + idx] = x.live ? x.m : -INFINITY;
-        s_l[t * 256 + hf * 128 + idx] = x.live ? x.l : 0.f;
+        s_ml[t * 128 + idx] = x.live ? make_float2(x.m, x.l) : make_float2(-INFINITY, 0.f);
         bar_sync(2, kt::kSoftThreads);
         const int tiles = rw.dual ? 2 : 1;
         auto lane_of = [&](int row, int j) {  // copy j of a row: [t][lane]
           const int tt = rw.dual ? j / rw.copies : row >= rw.split, c = rw.dual ? j % rw.copies : 0;
-          return tt * 256 + c * span + (!rw.dual && tt ? row - rw.split : row);
+          return tt * 128 + c * span + (!rw.dual && tt ? row - rw.split : row);
         };
         const int nsub = tiles * rw.copies;
         float f;  // of this thread's O: its weight in the row's sum
@@ -749,18 +791,18 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
           float M = -INFINITY;
           if (ridx < rw.of(t)) {
             const int row = ridx + (!rw.dual && t ? rw.split : 0);
-            for (int j = 0; j < nsub; j++) M = fmaxf(M, s_top[lane_of(row, j)]);
+            for (int j = 0; j < nsub; j++) M = fmaxf(M, s_ml[lane_of(row, j)].x);
           }
           f = x.any ? ex2(x.m - (M == -INFINITY ? 0.f : M)) * pow2i(x.E) : 0.f;
         }
 #pragma unroll 1
-        for (int c = 0; c < D / 2; c += 32) {
+        for (int c = 0; c < D; c += 64) {
           if (x.live) {
-            float* dst = s_x + (t * 128 + idx) * S::kX + hf * 32;
+            float* dst = s_x + (t * 128 + idx) * S::kX;
 #pragma unroll
-            for (int k = 0; k < 32; k += 16) {
+            for (int k = 0; k < 64; k += 16) {
               float o[16];
-              if (x.any) tmem_ld(tb + 128 + hf * (D / 2) + c + k, o);
+              if (x.any) tmem_ld(tb + 128 + c + k, o);
 #pragma unroll
               for (int e = 0; e < 16; e++) o[e] = x.any ? o[e] * f : 0.f;
 #pragma unroll
@@ -771,18 +813,18 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
             }
           }
           bar_sync(2, kt::kSoftThreads);
-          for (int i = st512; i < rw.rows * 16; i += kt::kSoftThreads) {
+          for (int i = st256; i < rw.rows * 16; i += kt::kSoftThreads) {
             const int row = i >> 4, x4 = i & 15;
-            const int d = (x4 >> 3) * (D / 2) + c + (x4 & 7) * 4;
+            const int d = c + x4 * 4;
             float M = -INFINITY;
-            for (int j = 0; j < nsub; j++) M = fmaxf(M, s_top[lane_of(row, j)]);
+            for (int j = 0; j < nsub; j++) M = fmaxf(M, s_ml[lane_of(row, j)].x);
             const float Ms = M == -INFINITY ? 0.f : M;
             float L = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int j = 0; j < nsub; j++) {
               const int at = lane_of(row, j);
-              L = fmaf(ex2(s_top[at] - Ms), s_l[at] + s_l[at + 128], L);
-              const float4 v = *reinterpret_cast<const float4*>(s_x + (at - (at >> 8) * 128) * S::kX + x4 * 4);
+              L = fmaf(ex2(s_ml[at].x - Ms), s_ml[at].y, L);
+              const float4 v = *reinterpret_cast<const float4*>(s_x + at * S::kX + x4 * 4);
               acc.x += v.x;
               acc.y += v.y;
               acc.z += v.z;
@@ -803,7 +845,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
           bar_sync(2, kt::kSoftThreads);
         }
         tc_fence_before();
-        if (!whole && st512 == 0) {
+        if (!whole && st256 == 0) {
           // is this the last of the segment's CTAs?  Acted on at this CTA's end.
           Kv4Join jn{w.seg, 0, sh.cta_of(w.seg), w.rq.n0, w.rq.m, h, rc};
           jn.n = sh.cta_of(w.seg + w.rq.nu - 1) - jn.c0 + 1;
@@ -817,7 +859,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
       bar_sync(2, kt::kSoftThreads);
       for (int d = 0; d < 2; d++) {
         const Kv4Join jn = s_join[d];
-        if (jn.n) tc_join<D>(a, jn, 2 * jn.c0 + (sh.first(jn.c0) < jn.seg ? 1 : 0), st512);
+        if (jn.n) tc_join<D>(a, jn, 2 * jn.c0 + (sh.first(jn.c0) < jn.seg ? 1 : 0), st256);
       }
   }
   tc_fence_before();

@@ -992,7 +992,7 @@ template <int D>
 static int launch_attn(const Kv4AttnArgs& a, int rows, int64_t units, bool bias, cudaStream_t st) {
   if (rows <= 8) return launch_attn_tile<D, 1, 8>(a, units, bias, st);
   if (rows <= kWarpRows) return launch_attn_tile<D, 2, 6>(a, units, bias, st);
-  return kv4_launch_attn_tc(a, D, (units + 1) / 2, bias, st);
+  return kv4_launch_attn_tc(a, D, rows, (units + 1) / 2, bias, st);
 }
 
 // ---------------------------------------------------------------- checks --

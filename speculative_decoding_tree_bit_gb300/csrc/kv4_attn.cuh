@@ -237,6 +237,6 @@ struct Kv4Join {
 
 // Many rows a kv head (kv4_attn_tc.cu).
 size_t kv4_tc_workspace(int head_dim);
-int kv4_launch_attn_tc(const Kv4AttnArgs& a, int head_dim, int64_t units, bool bias, cudaStream_t st);
+int kv4_launch_attn_tc(const Kv4AttnArgs& a, int head_dim, int rows, int64_t units, bool bias, cudaStream_t st);
 
 }  // namespace sdv

@@ -2,35 +2,33 @@
 // many rows a kv head: trees of many nodes, wide head groups.
 //
 // S = Q K^T and O += P V with two tiles t of up to 128 query rows, per tile of
-// 64 keys (two records).  Q lies in tensor memory for the whole segment, P
-// replaces S there, so the tensor core reads only K and V from shared memory:
-//   columns of tile t: [S or P 64][Q D/2][O D].
-// Warps, each role walking the CTA's units on its own:
+// 64 keys (two records).  Tensor memory of a tile: [S or P 64][S or P 64][O D]:
+// P replaces its S, and the next key tile's S is there before this one's P is,
+// so the softmax warps never wait for a product.  Warps, each role walking the
+// CTA's units on its own:
 //  * 16: records into a ring of eight, one bulk copy each;
-//  * 0..7: nibbles to fp16 operands, four warps a key tile, alternate tiles.  K's codes as they are (subnormal code
-//    2^-24; the key's scale and middle are applied to its score, as in the
-//    warp kernel); V's as values, s (code - 8) + m in one fp16 multiply-add
-//    per pair, times a power of two that follows the greatest value (11 bits,
-//    against the output's 8).  The rows' own keys are a tile of 64 in the same
-//    form, bf16 to fp16 after a power of two per key;
-//  * 17: the products.  Two tiles of S and P alternate, so that one tile's
-//    softmax runs under the other's products;
+//  * 0..7: nibbles to fp16 operands, four warps a key tile, alternate tiles.
+//    K's codes as they are (subnormal code 2^-24; the key's scale and middle
+//    are applied to its score, as in the warp kernel); V's as values, s (code -
+//    8) + m in one fp16 multiply-add per pair, times a power of two that
+//    follows the greatest value (11 bits, against the output's 8).  The rows'
+//    own keys are a tile of 64 in the same form, bf16 to fp16 after a power of
+//    two per key;
+//  * 17: the products;
 //  * 8..15: softmax, a thread per row: the scores of 64 keys from TMEM, maximum,
 //    exponentials, P back.  The running maximum may lag by 2^8 before O is
 //    rescaled in TMEM (fp16 P: exponentials are taken 2^5 up, at most 2^13).
 // (18 and 19 do nothing: they complete a warpgroup.  Registers a scheduler:
 // 5 warps x 96 = 2 x 64 decoding + 2 x 152 softmax + 48.)
-// With at most 128 rows both tiles hold the same rows and take alternate key
-// tiles.  With at most 64 (32) rows a tile holds them twice (four times), a
-// copy in other lanes taking half (a quarter) of the keys and leaving P 0 in
-// the others': the products cost the same, the softmax is shared by all
-// schedulers, each of which reaches only its quarter of the lanes.  The copies'
-// partial sums are added in shared memory at a segment's end; a segment that
-// spans CTAs is joined in global memory by the last of them to finish, in a
-// fixed order.
-//
-// Bound (D = 128, per 64 keys and two tiles): products 1024 cycles, softmax
-// issue about 1200 a scheduler, decoding 160, shared memory about 1000.
+// WIDE: the first rows of a segment are tile 0's, the others tile 1's, up to
+// 256.  Not WIDE (at most 128 rows a segment): both tiles hold the same rows and
+// take alternate key tiles.  With at most 64 (32) rows a tile holds them twice
+// (four times), a copy in other lanes taking half (a quarter) of the keys and
+// leaving P 0 in the others': the products cost the same, the softmax is shared
+// by all schedulers, each of which reaches only its quarter of the lanes.  The
+// copies' partial sums are added in shared memory at a segment's end; a segment
+// that spans CTAs is joined in global memory by the last of them to finish, in
+// a fixed order.
 #include <algorithm>
 #include <type_traits>
 
@@ -41,25 +39,28 @@ namespace sdv {
 
 namespace kt {
 constexpr int kSoft = 8, kLoad = 16, kMma = 17, kThreads = 20 * 32, kSoftThreads = 256;
-constexpr int kRaw = 8, kStages = 3;
-constexpr int kRows = 256;  // of a segment
+constexpr int kRaw = 8;
+constexpr int kRows = 256;  // of a segment, at most
 }  // namespace kt
 
-template <int D>
+template <int D, bool WIDE>
 struct TcShape {
+  static constexpr int NS = WIDE ? 3 : 4;                            // operand stages
   static constexpr int kStage = kv4_rec(D) + 128;
   static constexpr int kOp = 64 * D * 2;                             // 64 keys, fp16
-  static constexpr int off_raw = kt::kStages * 2 * kOp;              // [kRaw][kStage]
-  static constexpr int off_sc = off_raw + kt::kRaw * kStage;         // [kStages][32] key pairs: (m / s - 8) twice, s twice
-  static constexpr int off_pos = off_sc + kt::kStages * 64 * 8;      // [kStages][64]
-  static constexpr int off_info = off_pos + kt::kStages * 64 * 4;    // [kStages] (keys held, masks of either half, exponent of V << 1 | own)
-  static constexpr int off_bar = off_info + kt::kStages * 16;
-  static constexpr int off_ok = off_bar + (2 * kt::kRaw + 2 * kt::kStages + 8) * 8;
+  static constexpr int kQ = 128 * D * 2;                             // a tile of queries, fp16
+  static constexpr int kX = 36;                                      // floats of a row being added up
+  static constexpr int off_q = NS * 2 * kOp;                         // [WIDE ? 2 : 1]; shared with [2 t][128][kX] floats
+  static constexpr int kQs = (WIDE ? 2 : 1) * kQ;
+  static constexpr int off_raw = off_q + (kQs > 256 * kX * 4 ? kQs : 256 * kX * 4);  // [kRaw][kStage]
+  static constexpr int off_sc = off_raw + kt::kRaw * kStage;         // [NS][32] key pairs: (m / s - 8) twice, s twice
+  static constexpr int off_pos = off_sc + NS * 64 * 8;               // [NS][64]
+  static constexpr int off_info = off_pos + NS * 64 * 4;             // [NS] (keys held, masks of either half, exponent of V << 1 | own)
+  static constexpr int off_bar = off_info + NS * 16;
+  static constexpr int off_ok = off_bar + (2 * kt::kRaw + 2 * NS + 12) * 8;
   static constexpr int off_vmax = off_ok + kt::kRaw * 4;             // [8]
   static constexpr int off_ml = off_vmax + 32;                       // [2 t][128] (max, sum)
-  static constexpr int off_x = (off_ml + 256 * 8 + 15) / 16 * 16;    // [2 t][128][kX] floats
-  static constexpr int kX = 68;
-  static constexpr int smem = off_x + 256 * kX * 4 + 1024;
+  static constexpr int smem = off_ml + 256 * 8 + 1024;
   static constexpr int kPart = kt::kRows * (D + 2);                  // floats of a part: [rows][D], then [rows] (max, sum)
 };
 
@@ -104,7 +105,10 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32])
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
 }
-// D (tmem) (+)= A (tmem) * B (smem), fp16.
+// D (tmem) (+)= A (smem) * B (smem)^T, or A (tmem) * B (smem), fp16.
+__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  umma_bf16(d, a, b, idesc, accumulate);  // the operands' type is in the descriptor
+}
 __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
@@ -185,29 +189,27 @@ struct TcWalk {
   }
 };
 
-// Rows of a segment: a request's G m rows in nc even runs.  At most 128: both
-// tiles hold them; else the first `split` are tile 0's.  A tile's `copies` of
-// them lie 128 / copies lanes apart.
+// Rows of a segment: a request's G m rows in nc even runs.  Tile t holds `of(t)`
+// of them from row first(t) on, `copies` times, 128 / copies lanes apart.
+template <bool WIDE>
 struct TcRowsOf {
   int base, rows, split, copies;
-  bool dual;
   __device__ __forceinline__ TcRowsOf(int gm, int nc, int rc) {
     const int run = ((gm + nc - 1) / nc + 31) / 32 * 32;
     base = rc * run;
     rows = min(run, gm - base);
-    dual = rows <= 128;
-    split = dual ? rows : (rows / 2 + 31) / 32 * 32;
-    copies = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+    split = WIDE ? min(rows, (rows / 2 + 31) / 32 * 32) : rows;
+    copies = WIDE || rows > 64 ? 1 : rows > 32 ? 2 : 4;
   }
-  __device__ __forceinline__ int of(int t) const { return dual || t == 0 ? split : rows - split; }
-  __device__ __forceinline__ int first(int t) const { return base + (dual || t == 0 ? 0 : split); }
+  __device__ __forceinline__ int of(int t) const { return !WIDE || t == 0 ? split : rows - split; }
+  __device__ __forceinline__ int first(int t) const { return base + (!WIDE || t == 0 ? 0 : split); }
 };
 
 // Joins the parts of a segment and writes its rows, by the softmax threads.
-template <int D>
+template <int D, bool WIDE>
 __device__ __forceinline__ void tc_join(const Kv4AttnArgs& a, const Kv4Join& jn, int slot0, int st) {
   const int gm = a.G * jn.m, nc = (gm + kt::kRows - 1) / kt::kRows;
-  const TcRowsOf rw(gm, nc, jn.rc);
+  const TcRowsOf<WIDE> rw(gm, nc, jn.rc);
   for (int i = st; i < rw.rows * (D / 4); i += kt::kSoftThreads) {
     const int row = i / (D / 4), x = i % (D / 4);
     float M = -INFINITY, L = 0.f;
@@ -218,7 +220,7 @@ __device__ __forceinline__ void tc_join(const Kv4AttnArgs& a, const Kv4Join& jn,
 #pragma unroll
       for (int k = 0; k < 4; k++) {
         const int p = min(c + k, jn.n - 1);
-        const float* pc = a.part + (int64_t)(p == 0 ? slot0 : 2 * (jn.c0 + p)) * TcShape<D>::kPart;
+        const float* pc = a.part + (int64_t)(p == 0 ? slot0 : 2 * (jn.c0 + p)) * TcShape<D, WIDE>::kPart;
         ml[k] = __ldcg(reinterpret_cast<const float2*>(pc + kt::kRows * D) + row);
         v[k] = __ldcg(reinterpret_cast<const float4*>(pc) + i);
       }
@@ -261,23 +263,27 @@ struct TcRow {
 };
 
 // The softmax of a segment's units of tile t, NC keys of each (the copy's share).
-template <int D, bool BIAS, int NC>
-__device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint32_t tb, int i0, int n, int step,
-                                           uint32_t op0, uint32_t& nsc, uint64_t* s_full, uint64_t* op_full,
-                                           uint64_t* p_full, const float2* s_sc, const int* s_pos, const int4* s_info,
+template <int D, bool BIAS, bool WIDE, int NC>
+__device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint32_t tb, int i0, int n, uint32_t op0,
+                                           uint32_t& nsc, uint32_t& par, uint64_t* s_full, uint64_t* op_full, uint64_t* p_full,
+                                           uint64_t* o_full, const float2* s_sc, const int* s_pos, const int4* s_info,
                                            int* s_abort) {
-  constexpr int NS = kt::kStages;
+  constexpr int NS = TcShape<D, WIDE>::NS, step = WIDE ? 1 : 2;
+  uint32_t buf = 0;  // first TMEM column of the unit's scores: 0 or 64
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int i = i0; i < n; i += step) {
+  for (int i = i0; i < n; i += step, buf ^= 64) {
     const uint32_t st = (op0 + i) % NS;
-    if (!kv4_wait(s_full, nsc++ & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(33));
+    const int b = buf >> 6;
+    if (!kv4_wait(s_full + b, par >> b & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(33));
+    par ^= 1u << b;
+    nsc++;
     if (!kv4_wait(&op_full[st], (op0 + i) / NS & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(34));
     tc_fence_after();
     const int4 info = s_info[st];
     if (w.live) {
       float x[NC];
-      tmem_ld(tb + w.key0, x);
+      tmem_ld(tb + buf + w.key0, x);
       const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(s_sc + st * 64 + w.key0);
       const uint64_t qq = f2pack(w.qsf, w.qsf);
 #pragma unroll
@@ -315,6 +321,9 @@ __device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint3
         }
         if (w.any) {
           if (moves) al *= pow2i(max(w.E - E, -126));
+          // the product before may still be adding to O
+          if (!kv4_wait(o_full, nsc & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(35));
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
             float o[16];
@@ -345,26 +354,26 @@ __device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint3
         w.l += l0 + l1;
       }
       if constexpr (NC == 64) {
-        tmem_st(tb, p);
+        tmem_st(tb + buf, p);
       } else {
         uint32_t y[32];
 #pragma unroll
         for (int c = 0; c < 32; c++) y[c] = c / (NC / 2) * NC == w.key0 ? p[c % (NC / 2)] : 0u;
-        tmem_st(tb, y);
+        tmem_st(tb + buf, y);
       }
     }
     w.E = info.w >> 1;
     w.any = true;
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(p_full);
+    if (lane == 0) mbar_arrive(p_full + b);
   }
 }
 
-template <int D, bool BIAS>
+template <int D, bool BIAS, bool WIDE>
 __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
-  using S = TcShape<D>;
-  constexpr int NS = kt::kStages;
+  using S = TcShape<D, WIDE>;
+  constexpr int NS = S::NS;
   extern __shared__ uint8_t smem_tc[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_tc) + 1023) & ~uintptr_t(1023));
   uint8_t* const raw = sm + S::off_raw;
@@ -376,13 +385,13 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   uint64_t* const op_full = raw_empty + kt::kRaw;    // operands, scales written (4 warps)
   uint64_t* const op_empty = op_full + NS;           // products done with them (commit)
   uint64_t* const q_full = op_empty + NS;            // [t] queries in TMEM (4 warps)
-  uint64_t* const s_full = q_full + 2;               // [t] scores ready (commit)
-  uint64_t* const p_full = s_full + 2;               // [t] weights written (4 warps)
-  uint64_t* const o_full = p_full + 2;               // [t] the segment's last product done (commit)
+  uint64_t* const s_full = q_full + 2;               // [t][buffer] scores ready (commit)
+  uint64_t* const p_full = s_full + 4;               // [t][buffer] weights written (4 warps)
+  uint64_t* const o_full = p_full + 4;               // [t] a product with V done (commit)
   int* const s_ok = reinterpret_cast<int*>(sm + S::off_ok);
   uint32_t* const s_vmax = reinterpret_cast<uint32_t*>(sm + S::off_vmax);
   float2* const s_ml = reinterpret_cast<float2*>(sm + S::off_ml);
-  float* const s_x = reinterpret_cast<float*>(sm + S::off_x);
+  float* const s_x = reinterpret_cast<float*>(sm + S::off_q);
   __shared__ int s_abort;
   __shared__ uint32_t s_tmem;
   __shared__ Kv4Share sh;
@@ -399,8 +408,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
     for (int i = 0; i < NS; i++) mbar_init(&op_full[i], 4), mbar_init(&op_empty[i], 1);
     for (int t = 0; t < 2; t++) {
       mbar_init(&q_full[t], 4);
-      mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
+      for (int b = 0; b < 2; b++) mbar_init(&s_full[2 * t + b], 1), mbar_init(&p_full[2 * t + b], 4);
       mbar_init(&o_full[t], 1);
     }
     s_abort = 0;
@@ -455,66 +463,59 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
         // product of 64 columns, against 45 and more under lane == 0)
         TcWalk w(a, sh);
         const uint32_t id0 = (1u << 4) | (8u << 24);  // fp32 += fp16 fp16, M = 128
-        uint32_t op0 = 0, np[2] = {0, 0}, segs = 0;
+        const uint32_t idv = id0 | (1u << 16) | ((uint32_t)(D / 8) << 17);
+        const uint64_t kop = sdesc_sw128(smem_u32(sm)), vop = sdesc_mn(smem_u32(sm) + S::kOp),
+                       qop = sdesc_sw128(smem_u32(sm + S::off_q));
+        uint32_t op0 = 0, np = 0, segs = 0;  // np: parity of each p_full
         do {
-          const int h = w.head();
-          const TcRowsOf rw(a.G * w.rq.m, w.rq.nc, w.s - h * w.rq.nc);
           const int n = w.ub - w.ua;
-          auto scores = [&](int t, int i) {
+          // scores of tile t and unit i into buffer b
+          auto scores = [&](int t, int i, int b) {
             const uint32_t st = (op0 + i) % NS;
+            const uint64_t kd = kop + st * (2 * S::kOp >> 4), qd = qop + (WIDE ? t : 0) * (S::kQ >> 4);
+            const uint32_t id = id0 | ((uint32_t)(w.groups(a, w.ua + i) * 4) << 17), d = tm + t * 256 + b * 64;
             wait(&op_full[st], (op0 + i) / NS);
             tc_fence_after();
-            const uint64_t b = sdesc_sw128(smem_u32(sm + st * 2 * S::kOp));
-            const uint32_t id = id0 | ((uint32_t)(w.groups(a, w.ua + i) * 4) << 17);
             if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < D / 16; k++)
-                umma_f16_ts(tm + t * 256, tm + t * 256 + 64 + 8 * k, b + (k >> 2) * (8192 >> 4) + (k & 3) * 2, id, k > 0);
-              umma_commit(&s_full[t]);
+              for (int x = 0; x < D / 16; x++)
+                umma_f16_ss(d, qd + (x >> 2) * (16384 >> 4) + (x & 3) * 2, kd + (x >> 2) * (8192 >> 4) + (x & 3) * 2, id, x > 0);
+              umma_commit(&s_full[2 * t + b]);
             }
             __syncwarp();
           };
-          auto values = [&](int t, int i, bool first, bool release) {
-            wait(&p_full[t], np[t]++);
-            tc_fence_after();
+          auto values = [&](int t, int i, int b, bool first, bool release) {
             const uint32_t st = (op0 + i) % NS;
-            const uint64_t b = sdesc_mn(smem_u32(sm + st * 2 * S::kOp + S::kOp));
-            const uint32_t id = id0 | (1u << 16) | ((uint32_t)(D / 8) << 17);
+            const uint64_t vd = vop + st * (2 * S::kOp >> 4);
             const bool two = w.groups(a, w.ua + i) == 2;
+            const uint32_t o = tm + t * 256 + 128, p = tm + t * 256 + b * 64;
+            wait(&p_full[2 * t + b], np >> (2 * t + b));
+            np ^= 1u << (2 * t + b);
+            tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < 4; k++)
-                if (k < 2 || two)
-                  umma_f16_ts(tm + t * 256 + 128, tm + t * 256 + 8 * k, b + k * (2048 >> 4), id, !first || k > 0);
+              for (int x = 0; x < 4; x++)
+                if (x < 2 || two) umma_f16_ts(o, p + 8 * x, vd + x * (2048 >> 4), idv, !first || x > 0);
+              umma_commit(&o_full[t]);
               if (release) umma_commit(&op_empty[st]);
             }
             __syncwarp();
           };
-          auto finish = [&](int t) {
-            if (elect_one()) umma_commit(&o_full[t]);
-            __syncwarp();
-          };
           wait(&q_full[0], segs);
-          wait(&q_full[1], segs);
+          if (WIDE) wait(&q_full[1], segs);
           tc_fence_after();
-          scores(0, 0);
-          if (rw.dual) {
-            if (n > 1) scores(1, 1);
+          if (WIDE) {
+            for (int i = 0; i < min(n, 2); i++) scores(0, i, i), scores(1, i, i);
             for (int i = 0; i < n; i++) {
-              const int t = i & 1;
-              values(t, i, i < 2, true);
-              if (i + 2 < n) scores(t, i + 2);
-              else finish(t);
+              values(0, i, i & 1, i == 0, false);
+              values(1, i, i & 1, i == 0, true);
+              if (i + 2 < n) scores(0, i + 2, i & 1), scores(1, i + 2, i & 1);
             }
           } else {
-            scores(1, 0);
+            for (int i = 0; i < min(n, 3); i++) scores(i & 1, i, i >> 1);
             for (int i = 0; i < n; i++) {
-              values(0, i, i == 0, false);
-              if (i + 1 < n) scores(0, i + 1);
-              else finish(0);
-              values(1, i, i == 0, true);
-              if (i + 1 < n) scores(1, i + 1);
-              else finish(1);
+              values(i & 1, i, i >> 1 & 1, i < 2, true);
+              if (i + 3 < n) scores((i + 3) & 1, i + 3, (i + 3) >> 1 & 1);
             }
           }
           op0 += n;
@@ -541,70 +542,78 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
           const int st = op % NS;
           uint8_t* const ko = sm + st * 2 * S::kOp;
           uint8_t* const vo = ko + S::kOp;
-          wait(&op_empty[st], (op / NS & 1) ^ 1);
           if (u >= w.rq.no) {
             const int ga = w.rq.g0 + 2 * (u - w.rq.no), ng = w.groups(a, u);
+            // everything this thread needs of the records, then their slots are
+            // free.  Eight lanes take four rows' neighbouring 16-byte pieces:
+            // two phases a read, none shared a write
+            const int row = 16 * (dw & 1) + 4 * (lane >> 3) + (lane >> 1 & 3);
+            const int cg = (D == 128 ? 2 * (dw >> 1) : 0) + (lane & 1);
+            const bool do_k = D == 128 || dw < 2, do_v = D == 128 || dw >= 2;
             int lim[2] = {0, 0};
-            const uint8_t* rec[2];
-            uint32_t vb = 0;
+            uint32_t vsm[2] = {0, 0}, ksm = 0, ksv = 0, vb = 0;
+            uint4 xk[2], xv[2];
+            int kpos = 0;
 #pragma unroll
             for (int gi = 0; gi < 2; gi++) {
-              const uint32_t c = nraw + gi;
-              rec[gi] = raw + c % kt::kRaw * S::kStage;
               if (gi >= ng) continue;
-              wait(&raw_full[c % kt::kRaw], c / kt::kRaw);
-              lim[gi] = s_ok[c % kt::kRaw] ? max(0, min(kKvGroup, w.rq.ctx - (ga + gi) * kKvGroup)) : 0;
-              const uint32_t vw = *reinterpret_cast<const uint32_t*>(rec[gi] + kv4_half(D) + 16 * D + lane * 4);
+              const uint32_t slot = (nraw + gi) % kt::kRaw;
+              wait(&raw_full[slot], (nraw + gi) / kt::kRaw);
+              const uint8_t* rec = raw + slot * S::kStage;
+              lim[gi] = s_ok[slot] ? max(0, min(kKvGroup, w.rq.ctx - (ga + gi) * kKvGroup)) : 0;
+              const uint32_t vw = *reinterpret_cast<const uint32_t*>(rec + kv4_half(D) + 16 * D + lane * 4);
+              if (do_k) xk[gi] = *reinterpret_cast<const uint4*>(rec + row * (D / 2) + cg * 16);
+              if (do_v) {
+                xv[gi] = *reinterpret_cast<const uint4*>(rec + kv4_half(D) + row * (D / 2) + (D == 128 ? cg ^ (row & 2) : cg) * 16);
+                vsm[gi] = *reinterpret_cast<const uint32_t*>(rec + kv4_half(D) + 16 * D + row * 4);
+              }
+              if (dt >> 5 == gi) {
+                ksm = *reinterpret_cast<const uint32_t*>(rec + 16 * D + lane * 4);
+                ksv = vw;
+                if (BIAS) kpos = *reinterpret_cast<const int*>(rec + kv4_rec(D) + lane * 4);
+              }
               const float b = fmaf(8.f, __uint_as_float(vw << 16), fabsf(__uint_as_float(vw & 0xFFFF0000u)));
               if (lane < lim[gi] && b <= 3.4e38f) vb = max(vb, __float_as_uint(b));
             }
+            __syncwarp();
+            if (lane == 0)
+              for (int gi = 0; gi < ng; gi++) mbar_arrive(&raw_empty[(nraw + gi) % kt::kRaw]);
+            nraw += ng;
             E = min(max(E, tc_exponent(__reduce_max_sync(0xffffffffu, vb))), 120);
+            wait(&op_empty[st], (op / NS & 1) ^ 1);
             if (dt < 64) {
-              const int gi = dt >> 5;
               float2 sc = make_float2(0.f, 0.f);
-              if (lane < (gi ? lim[1] : lim[0])) {
-                const uint8_t* rc = gi ? rec[1] : rec[0];
-                const uint32_t kw = *reinterpret_cast<const uint32_t*>(rc + 16 * D + lane * 4);
-                const uint32_t vw = *reinterpret_cast<const uint32_t*>(rc + kv4_half(D) + 16 * D + lane * 4);
-                const float s = __uint_as_float(kw << 16), m = __uint_as_float(kw & 0xFFFF0000u);
+              if (lane < (dt < 32 ? lim[0] : lim[1])) {
+                const float s = __uint_as_float(ksm << 16), m = __uint_as_float(ksm & 0xFFFF0000u);
                 // a row of one value has s = 0 and every code 8: any s will do
                 sc.y = s == 0.f ? fmaxf(fabsf(m) * 0.0625f, 1e-30f) : s;
                 sc.x = m / sc.y - 8.f;
-                if (!(fabsf(__uint_as_float(vw << 16)) <= 3.4e38f)) sc.x = __int_as_float(0x7FC00000);  // V held as NaN
-                if (BIAS) s_pos[st * 64 + dt] = *reinterpret_cast<const int*>(rc + kv4_rec(D) + lane * 4);
+                if (!(fabsf(__uint_as_float(ksv << 16)) <= 3.4e38f)) sc.x = __int_as_float(0x7FC00000);  // V held as NaN
+                if (BIAS) s_pos[st * 64 + dt] = kpos;
               }
               reinterpret_cast<float*>(s_sc + st * 64)[(dt >> 1) * 4 + (dt & 1)] = sc.x;
               reinterpret_cast<float*>(s_sc + st * 64)[(dt >> 1) * 4 + 2 + (dt & 1)] = sc.y;
             }
             if (dt == 0)
               s_info[st] = make_int4(lim[0] + lim[1], lim[0] == 32 ? -1 : (1 << lim[0]) - 1, lim[1] == 32 ? -1 : (1 << lim[1]) - 1, E * 2);
-            // eight lanes take four rows' neighbouring 16-byte pieces: two
-            // phases a read, none shared a write
-            const int row = 16 * (dw & 1) + 4 * (lane >> 3) + (lane >> 1 & 3);
-            const int cg = (D == 128 ? 2 * (dw >> 1) : 0) + (lane & 1);
+            const float down = pow2i(-E), up = pow2i(24 - E), up4 = pow2i(20 - E);
 #pragma unroll
             for (int gi = 0; gi < 2; gi++) {
               if (gi >= ng) break;
               const int R = gi * 32 + row;
               const uint32_t at = (cg >> 1) * 8192 + R * 128;
-              if (D == 128 || dw < 2) {
-                const uint4 x = *reinterpret_cast<const uint4*>(rec[gi] + row * (D / 2) + cg * 16);
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+              if (do_k) {
+                const uint32_t xs[4] = {xk[gi].x, xk[gi].y, xk[gi].z, xk[gi].w};
 #pragma unroll
                 for (int j = 0; j < 4; j++)
                   *reinterpret_cast<uint4*>(ko + at + ((((cg & 1) * 4 + j) ^ (R & 7)) << 4)) =
                       make_uint4(codes2<0>(xs[j]), codes2<1>(xs[j]), codes2<2>(xs[j]), codes2<3>(xs[j]));
               }
-              if (D == 128 || dw >= 2) {
-                const uint32_t vw = *reinterpret_cast<const uint32_t*>(rec[gi] + kv4_half(D) + 16 * D + row * 4);
-                float s = __uint_as_float(vw << 16), m = __uint_as_float(vw & 0xFFFF0000u);
+              if (do_v) {
+                float s = __uint_as_float(vsm[gi] << 16), m = __uint_as_float(vsm[gi] & 0xFFFF0000u);
                 if (row >= lim[gi] || !(s <= 3.4e38f)) s = m = 0.f;  // not held, or NaN: its scores say so
-                const float down = pow2i(-E);
-                const uint32_t me = h2dup(s * pow2i(24 - E)), mo = h2dup(s * pow2i(20 - E)),
-                               cc = h2dup(fmaf(-8.f, s, m) * down);
-                const uint4 x = *reinterpret_cast<const uint4*>(rec[gi] + kv4_half(D) + row * (D / 2) +
-                                                                (D == 128 ? cg ^ (row & 2) : cg) * 16);
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                const uint32_t me = h2dup(s * up), mo = h2dup(s * up4), cc = h2dup(fmaf(-8.f, s, m) * down);
+                const uint32_t xs[4] = {xv[gi].x, xv[gi].y, xv[gi].z, xv[gi].w};
 #pragma unroll
                 for (int j = 0; j < 4; j++)
                   *reinterpret_cast<uint4*>(vo + at + ((((cg & 1) * 4 + j) ^ (R & 7)) << 4)) =
@@ -612,12 +621,9 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
                                  hfma2(codes2<2>(xs[j]), me, cc), hfma2(codes2<3>(xs[j]), mo, cc));
               }
             }
-            __syncwarp();
-            if (lane == 0)
-              for (int gi = 0; gi < ng; gi++) mbar_arrive(&raw_empty[(nraw + gi) % kt::kRaw]);
-            nraw += ng;
           } else {
             // the rows' own keys: two threads a row
+            wait(&op_empty[st], (op / NS & 1) ^ 1);
             const int j = dt >> 1, half = dt & 1;
             const bool in = a.k_new && j < w.rq.m;
             const int64_t off = (int64_t)(w.rq.n0 + j) * a.kv_stride + h * D + half * (D / 2);
@@ -697,10 +703,10 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
       const int idx = (warp & 3) * 32 + lane;                                // TMEM lane
       const uint32_t tb = tm + t * 256 + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
       const float scale = BIAS ? 1.f : a.s.scale * kLog2e;
-      uint32_t op0 = 0, nsc = 0, nsum = 0;
+      uint32_t op0 = 0, nsc = 0, par = 0;  // units done; parity of either s_full
       do {
         const int h = w.head(), rc = w.s - h * w.rq.nc, n = w.ub - w.ua;
-        const TcRowsOf rw(a.G * w.rq.m, w.rq.nc, rc);
+        const TcRowsOf<WIDE> rw(a.G * w.rq.m, w.rq.nc, rc);
         const int span = 128 / rw.copies;  // lanes of a copy
         TcRow x;
         {
@@ -735,12 +741,11 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
           const float up = pow2i(e), up4 = pow2i(e - 4);
           x.qsf = qs * pow2i(e - 24);
           x.fac = pow2i(24 - e) * scale;
-#pragma unroll
-          for (int c = 0; c < D / 32; c++) {
-            uint32_t y[16];
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-              const uint4 v = ok ? src[c * 4 + i] : make_uint4(0, 0, 0, 0);
+          if (WIDE || t == 0) {
+            uint8_t* const qt = sm + S::off_q + (WIDE ? t : 0) * S::kQ + idx * 128;
+#pragma unroll 4
+            for (int c = 0; c < D / 8; c++) {
+              const uint4 v = ok ? src[c] : make_uint4(0, 0, 0, 0);
               const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
               float f[8];
 #pragma unroll
@@ -748,59 +753,56 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
                 f[2 * k] = __uint_as_float(vs[k] << 16) * up;
                 f[2 * k + 1] = __uint_as_float(vs[k] & 0xFFFF0000u) * up4;
               }
-#pragma unroll
-              for (int k = 0; k < 4; k++) y[4 * i + k] = pack_f16x2(f[k], f[k + 4]);
+              *reinterpret_cast<uint4*>(qt + (c >> 3) * 16384 + (((c & 7) ^ (idx & 7)) << 4)) =
+                  make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
             }
-            tmem_st(tb + 64 + c * 16, y);
           }
         }
-        tc_fence_before();
+        fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[t]);
+        if (lane == 0 && (WIDE || t == 0)) mbar_arrive(&q_full[t]);
 
         {
-          const int i0 = rw.dual ? t : 0, step = rw.dual ? 2 : 1;
           auto run = [&](auto nc) {
-            tc_softmax<D, BIAS, decltype(nc)::value>(a, x, tb, i0, n, step, op0, nsc, &s_full[t], op_full, &p_full[t], s_sc,
-                                                     s_pos, s_info, &s_abort);
+            tc_softmax<D, BIAS, WIDE, decltype(nc)::value>(a, x, tb, WIDE ? 0 : t, n, op0, nsc, par, &s_full[2 * t], op_full, &p_full[2 * t],
+                                                           &o_full[t], s_sc, s_pos, s_info, &s_abort);
           };
           if (rw.copies == 1) run(std::integral_constant<int, 64>());
           else if (rw.copies == 2) run(std::integral_constant<int, 32>());
           else run(std::integral_constant<int, 16>());
         }
         if (x.any) {
-          wait(&o_full[t], nsum++);
+          wait(&o_full[t], nsc - 1);
           tc_fence_after();
         }
-        // Add up the copies, 64 dims at a time, and write the rows: the outputs
+        // Add up the copies, 32 dims at a time, and write the rows: the outputs
         // where the CTA has the whole segment, else a part.
         const bool whole = w.ua == 0 && w.ub == w.rq.nu;
         const int slot = 2 * blockIdx.x + (w.seg + w.ua > sh.u0 ? 1 : 0);
         float* part = a.part + (int64_t)slot * S::kPart;
         s_ml[t * 128 + idx] = x.live ? make_float2(x.m, x.l) : make_float2(-INFINITY, 0.f);
         bar_sync(2, kt::kSoftThreads);
-        const int tiles = rw.dual ? 2 : 1;
         auto lane_of = [&](int row, int j) {  // copy j of a row: [t][lane]
-          const int tt = rw.dual ? j / rw.copies : row >= rw.split, c = rw.dual ? j % rw.copies : 0;
-          return tt * 128 + c * span + (!rw.dual && tt ? row - rw.split : row);
+          if (WIDE) return row < rw.split ? row : 128 + row - rw.split;
+          return j / rw.copies * 128 + j % rw.copies * span + row;
         };
-        const int nsub = tiles * rw.copies;
+        const int nsub = WIDE ? 1 : 2 * rw.copies;
         float f;  // of this thread's O: its weight in the row's sum
         {
           const int ridx = idx % span;
           float M = -INFINITY;
           if (ridx < rw.of(t)) {
-            const int row = ridx + (!rw.dual && t ? rw.split : 0);
+            const int row = ridx + (WIDE && t ? rw.split : 0);
             for (int j = 0; j < nsub; j++) M = fmaxf(M, s_ml[lane_of(row, j)].x);
           }
           f = x.any ? ex2(x.m - (M == -INFINITY ? 0.f : M)) * pow2i(x.E) : 0.f;
         }
 #pragma unroll 1
-        for (int c = 0; c < D; c += 64) {
+        for (int c = 0; c < D; c += 32) {
           if (x.live) {
             float* dst = s_x + (t * 128 + idx) * S::kX;
 #pragma unroll
-            for (int k = 0; k < 64; k += 16) {
+            for (int k = 0; k < 32; k += 16) {
               float o[16];
               if (x.any) tmem_ld(tb + 128 + c + k, o);
 #pragma unroll
@@ -813,8 +815,8 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
             }
           }
           bar_sync(2, kt::kSoftThreads);
-          for (int i = st256; i < rw.rows * 16; i += kt::kSoftThreads) {
-            const int row = i >> 4, x4 = i & 15;
+          for (int i = st256; i < rw.rows * 8; i += kt::kSoftThreads) {
+            const int row = i >> 3, x4 = i & 7;
             const int d = c + x4 * 4;
             float M = -INFINITY;
             for (int j = 0; j < nsub; j++) M = fmaxf(M, s_ml[lane_of(row, j)].x);
@@ -859,7 +861,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
       bar_sync(2, kt::kSoftThreads);
       for (int d = 0; d < 2; d++) {
         const Kv4Join jn = s_join[d];
-        if (jn.n) tc_join<D>(a, jn, 2 * jn.c0 + (sh.first(jn.c0) < jn.seg ? 1 : 0), st256);
+        if (jn.n) tc_join<D, WIDE>(a, jn, 2 * jn.c0 + (sh.first(jn.c0) < jn.seg ? 1 : 0), st256);
       }
   }
   tc_fence_before();
@@ -872,21 +874,22 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
 
 size_t kv4_tc_workspace(int head_dim) { return (size_t)2 * num_sms() * kt::kRows * (head_dim + 2) * sizeof(float); }
 
-template <int D>
+template <int D, bool WIDE>
 static int launch_tc(const Kv4AttnArgs& a, int64_t units, bool bias, cudaStream_t st) {
-  constexpr int smem = TcShape<D>::smem;
+  constexpr int smem = TcShape<D, WIDE>::smem;
   static const cudaError_t set[2] = {
-      cudaFuncSetAttribute(k_kv4_attn_tc<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
-      cudaFuncSetAttribute(k_kv4_attn_tc<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)};
+      cudaFuncSetAttribute(k_kv4_attn_tc<D, false, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+      cudaFuncSetAttribute(k_kv4_attn_tc<D, true, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)};
   SD_CK(set[bias]);
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(num_sms(), units));
-  (bias ? k_kv4_attn_tc<D, true> : k_kv4_attn_tc<D, false>)<<<(unsigned)grid, kt::kThreads, smem, st>>>(a);
+  (bias ? k_kv4_attn_tc<D, true, WIDE> : k_kv4_attn_tc<D, false, WIDE>)<<<(unsigned)grid, kt::kThreads, smem, st>>>(a);
   SD_CK(cudaGetLastError());
   return SD_OK;
 }
 
-int kv4_launch_attn_tc(const Kv4AttnArgs& a, int head_dim, int64_t units, bool bias, cudaStream_t st) {
-  return head_dim == 128 ? launch_tc<128>(a, units, bias, st) : launch_tc<64>(a, units, bias, st);
+int kv4_launch_attn_tc(const Kv4AttnArgs& a, int head_dim, int rows, int64_t units, bool bias, cudaStream_t st) {
+  if (head_dim == 128) return rows > 128 ? launch_tc<128, true>(a, units, bias, st) : launch_tc<128, false>(a, units, bias, st);
+  return rows > 128 ? launch_tc<64, true>(a, units, bias, st) : launch_tc<64, false>(a, units, bias, st);
 }
 
 }  // namespace sdv

@@ -5,20 +5,37 @@ namespace sdv {
 
 // ---------------------------------------------------------------- append --
 //
-// One warp stores the key and the value row of one (row, kv head): a half
-// warp each, D / 16 values a lane (one or half a 32-bit word of codes).  The
-// row's least and greatest value come from four shuffles.  Bound: bytes (4 D
-// in, D + 12 out per row and head).
+// One warp stores a row's keys and values of kHeads kv heads: a half warp the
+// key, the other the value, D / 16 values a lane (one or half a 32-bit word of
+// codes); the heads' rows are all in flight before the first is used.  A row's
+// least and greatest value come from four shuffles.  Bound: bytes (4 D in, D +
+// 12 out per row and head).
 
-// The row of a call that entry e is, by a search over the request offsets.
+constexpr int kHeads = 4;
+
+// The request of row e, by the whole warp: a search 32 offsets at a time.
 __device__ __forceinline__ int request_of(const int32_t* __restrict__ cu, int R, int e) {
+  const int lane = threadIdx.x & 31;
   int lo = 0, hi = R;  // cu[lo] <= e < cu[hi]
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= e) lo = mid;
-    else hi = mid;
+    const int step = (hi - lo + 31) / 32, x = lo + lane * step;
+    const int n = __popc(__ballot_sync(0xffffffffu, x < hi && cu[x] <= e));
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
   }
   return lo;
+}
+
+// N consecutive 16-bit values of a row as 32-bit words.
+template <int N>
+__device__ __forceinline__ void load_row(const uint16_t* p, uint32_t (&w)[N / 2]) {
+  if constexpr (N == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x, w[1] = u.y;
+  }
 }
 
 template <int D>
@@ -29,76 +46,89 @@ __global__ void __launch_bounds__(256) k_kv4_append(Kv4View c, const uint16_t* _
                                                     const int32_t* __restrict__ pos, const int32_t* at, bool advance,
                                                     int32_t* status) {
   constexpr int kV = D / 16;  // values of a lane
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (w >= (int64_t)rows * c.hkv) return;
+  const int e = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (e >= rows) return;
   const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
-  const int e = (int)(w / c.hkv), h = (int)(w - (int64_t)e * c.hkv);
+  const int h0 = blockIdx.y * kHeads, nh = min(kHeads, c.hkv - h0);
+  const int s = src ? src[e] : e;
+  const bool s_ok = s >= 0 && s < n_src;
+  uint32_t raw[kHeads][kV / 2];
+#pragma unroll
+  for (int i = 0; i < kHeads; i++)
+    if (s_ok && i < nh) load_row<kV>((half ? v : k) + (int64_t)s * row_stride + (h0 + i) * D + l * kV, raw[i]);
+  const int p = pos ? pos[e] : 0;
   const int r = request_of(cu, R, e);
-  const int i = e - cu[r];
+  const int i0 = e - cu[r];
   const int n = count ? min(max(count[r], 0), cu[r + 1] - cu[r]) : cu[r + 1] - cu[r];
   const int a = at[r];
   if (a < 0 || (int64_t)a + n > c.cap) {
     if (lane == 0) set_status(status, SD_ERR_CAPACITY);
     return;
   }
-  if (i == 0 && h == 0 && lane == 0 && advance) c.ctx_len[r] = a + n;
-  if (i >= n) return;
-  const int s = src ? src[e] : e;
-  if (s < 0 || s >= n_src) {
-    if (lane == 0) set_status(status, SD_ERR_CAPACITY);
-    return;
-  }
-  const int t = a + i;
-  uint8_t* rec = c.record(D, r, h, t / kKvGroup);
+  if (i0 == 0 && h0 == 0 && lane == 0 && advance) c.ctx_len[r] = a + n;
+  if (i0 >= n) return;
+  const int t = a + i0;
+  uint8_t* rec = s_ok ? c.record(D, r, h0, t / kKvGroup) : nullptr;
   if (!rec) {
     if (lane == 0) set_status(status, SD_ERR_CAPACITY);
     return;
   }
-  const uint16_t* x = (half ? v : k) + (int64_t)s * row_stride + h * D + l * kV;
-  uint32_t raw[kV / 2];
-  if constexpr (kV == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(x);
-    raw[0] = u.x, raw[1] = u.y, raw[2] = u.z, raw[3] = u.w;
-  } else {
-    const uint2 u = *reinterpret_cast<const uint2*>(x);
-    raw[0] = u.x, raw[1] = u.y;
-  }
-  float f[kV], lo = INFINITY, hi = -INFINITY;
-  bool nan = false;
 #pragma unroll
-  for (int j = 0; j < kV; j++) {
-    f[j] = bf2f((uint16_t)(raw[j >> 1] >> (16 * (j & 1))));
-    lo = fminf(lo, f[j]);
-    hi = fmaxf(hi, f[j]);
-    nan |= f[j] != f[j];  // fminf and fmaxf pass NaN over
-  }
+  for (int i = 0; i < kHeads; i++) {
+    if (i >= nh) break;
+    float f[kV], lo = INFINITY, hi = -INFINITY;
+    bool nan = false;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  const uint32_t bad = __ballot_sync(0xffffffffu, nan) >> (16 * half) & 0xFFFFu;
-  const float range = hi - lo;
-  float sc = rbf(__fdiv_rn(range, 15.f)), md = rbf(fmaf(8.f, sc, lo));
-  if (bad || !(range <= 3.4028234e38f)) sc = md = __int_as_float(0x7FC00000);  // not finite: the row is held as NaN
-  uint32_t word = 0;
+    for (int j = 0; j < kV; j++) {
+      f[j] = __uint_as_float(j & 1 ? raw[i][j >> 1] & 0xFFFF0000u : raw[i][j >> 1] << 16);
+      lo = fminf(lo, f[j]);
+      hi = fmaxf(hi, f[j]);
+      nan |= f[j] != f[j];  // fminf and fmaxf pass NaN over
+    }
 #pragma unroll
-  for (int j = 0; j < kV; j++) {
-    // the quotient is a true division: a product with 1 / s could fall on the
-    // other side of a half.  NaN and s = 0 give code 8.
-    const float qf = sc > 0.f ? rintf(__fdiv_rn(f[j] - md, sc)) : 0.f;
-    word |= (uint32_t)((int)fminf(fmaxf(qf, -8.f), 7.f) + 8) << (4 * j);
-  }
-  uint8_t* codes = rec + half * kv4_half(D) + (t & 31) * (D / 2);
-  const int b = half ? kv4_vbyte<D>(t, l * (kV / 2)) : l * (kV / 2);
-  if constexpr (kV == 8) *reinterpret_cast<uint32_t*>(codes + b) = word;
-  else *reinterpret_cast<uint16_t*>(codes + b) = (uint16_t)word;
-  if (l == 0) {
-    *reinterpret_cast<uint32_t*>(rec + half * kv4_half(D) + 16 * D + (t & 31) * 4) =
-        (uint32_t)f2bf(sc) | (uint32_t)f2bf(md) << 16;
-    const int64_t o = c.slot0(r, h) + t;
-    if (half) c.weight[o] = 0.f;
-    else c.pos[o] = pos ? pos[e] : t;
+    for (int o = 8; o > 0; o >>= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    const uint32_t bad = __ballot_sync(0xffffffffu, nan) >> (16 * half) & 0xFFFFu;
+    const float range = hi - lo;
+    float sc = rbf(__fdiv_rn(range, 15.f)), md = rbf(fmaf(8.f, sc, lo));
+    if (bad || !(range <= 3.4028234e38f)) sc = md = __int_as_float(0x7FC00000);  // not finite: the row is held as NaN
+    // A code is the nearest step, halves to even.  The product with 1 / s is
+    // within 2^-19 of the quotient (at most 8 or so); where that leaves a half
+    // in doubt anywhere in the warp, the quotients themselves decide.
+    const float inv = sc > 1e-30f && sc < 1e30f ? __fdiv_rn(1.f, sc) : 0.f;
+    float st[kV];
+    bool doubt = sc > 0.f && inv == 0.f;
+#pragma unroll
+    for (int j = 0; j < kV; j++) {
+      const float q = (f[j] - md) * inv;
+      st[j] = rintf(q);
+      doubt |= fabsf(fabsf(q - st[j]) - 0.5f) < 4e-6f;
+    }
+    if (__any_sync(0xffffffffu, doubt)) {
+#pragma unroll
+      for (int j = 0; j < kV; j++) st[j] = sc > 0.f ? rintf(__fdiv_rn(f[j] - md, sc)) : 0.f;
+    }
+    uint32_t word = 0;
+#pragma unroll
+    for (int j = 0; j < kV; j++) {
+      // NaN and s = 0 give code 8
+      const float q = sc > 0.f ? st[j] : 0.f;
+      word |= (uint32_t)((int)fminf(fmaxf(q, -8.f), 7.f) + 8) << (4 * j);
+    }
+    uint8_t* const rh = rec + (int64_t)i * c.gpp * kv4_rec(D);
+    uint8_t* codes = rh + half * kv4_half(D) + (t & 31) * (D / 2);
+    const int b = half ? kv4_vbyte<D>(t, l * (kV / 2)) : l * (kV / 2);
+    if constexpr (kV == 8) *reinterpret_cast<uint32_t*>(codes + b) = word;
+    else *reinterpret_cast<uint16_t*>(codes + b) = (uint16_t)word;
+    if (l == 0) {
+      *reinterpret_cast<uint32_t*>(rh + half * kv4_half(D) + 16 * D + (t & 31) * 4) =
+          (uint32_t)f2bf(sc) | (uint32_t)f2bf(md) << 16;
+      const int64_t o = c.slot0(r, h0 + i) + t;
+      if (half) c.weight[o] = 0.f;
+      else c.pos[o] = pos ? p : t;
+    }
   }
 }
 
@@ -114,47 +144,58 @@ __global__ void k_kv4_advance(int32_t* ctx_len, const int32_t* __restrict__ cu, 
 
 // ------------------------------------------------------------------ read --
 //
-// The warp and lane shape of the append, the other way.
+// The append's warp and lanes, the other way.
 template <int D>
 __global__ void __launch_bounds__(256) k_kv4_read(Kv4View c, const int32_t* __restrict__ cu, int R, int rows,
                                                   const int32_t* __restrict__ at, uint16_t* __restrict__ k_out,
                                                   uint16_t* __restrict__ v_out, int32_t* status) {
   constexpr int kV = D / 16;
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (w >= (int64_t)rows * c.hkv) return;
+  const int e = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (e >= rows) return;
   const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
-  const int e = (int)(w / c.hkv), h = (int)(w - (int64_t)e * c.hkv);
+  const int h0 = blockIdx.y * kHeads, nh = min(kHeads, c.hkv - h0);
   const int r = request_of(cu, R, e);
   const int64_t t64 = (int64_t)(at ? at[r] : 0) + e - cu[r];
-  const uint8_t* rec = t64 >= 0 && t64 < c.cap ? c.record(D, r, h, (int)(t64 / kKvGroup)) : nullptr;
+  const uint8_t* rec = t64 >= 0 && t64 < c.cap ? c.record(D, r, h0, (int)(t64 / kKvGroup)) : nullptr;
   if (!rec) {
     if (lane == 0) set_status(status, SD_ERR_CAPACITY);
     return;
   }
   const int t = (int)t64;
-  const uint8_t* codes = rec + half * kv4_half(D) + (t & 31) * (D / 2);
   const int b = half ? kv4_vbyte<D>(t, l * (kV / 2)) : l * (kV / 2);
-  const uint32_t word = kV == 8 ? *reinterpret_cast<const uint32_t*>(codes + b)
-                                : *reinterpret_cast<const uint16_t*>(codes + b);
-  const uint32_t sm = *reinterpret_cast<const uint32_t*>(rec + half * kv4_half(D) + 16 * D + (t & 31) * 4);
-  const float sc = bf2f((uint16_t)sm), md = bf2f((uint16_t)(sm >> 16));
-  uint32_t o[kV / 2];
+  uint32_t word[kHeads], sm[kHeads];
 #pragma unroll
-  for (int j = 0; j < kV / 2; j++) {
-    const int c0 = (int)(word >> (8 * j) & 15) - 8, c1 = (int)(word >> (8 * j + 4) & 15) - 8;
-    o[j] = pack_bf16x2(fmaf(sc, (float)c0, md), fmaf(sc, (float)c1, md));
+  for (int i = 0; i < kHeads; i++)
+    if (i < nh) {
+      const uint8_t* part = rec + (int64_t)i * c.gpp * kv4_rec(D) + half * kv4_half(D);
+      const uint8_t* codes = part + (t & 31) * (D / 2) + b;
+      word[i] = kV == 8 ? *reinterpret_cast<const uint32_t*>(codes) : *reinterpret_cast<const uint16_t*>(codes);
+      sm[i] = *reinterpret_cast<const uint32_t*>(part + 16 * D + (t & 31) * 4);
+    }
+#pragma unroll
+  for (int i = 0; i < kHeads; i++) {
+    if (i >= nh) break;
+    const float sc = __uint_as_float(sm[i] << 16), md = __uint_as_float(sm[i] & 0xFFFF0000u);
+    uint32_t o[kV / 2];
+#pragma unroll
+    for (int j = 0; j < kV / 2; j++) {
+      const int c0 = (int)(word[i] >> (8 * j) & 15) - 8, c1 = (int)(word[i] >> (8 * j + 4) & 15) - 8;
+      o[j] = pack_bf16x2(fmaf(sc, (float)c0, md), fmaf(sc, (float)c1, md));
+    }
+    uint16_t* dst = (half ? v_out : k_out) + ((int64_t)e * c.hkv + h0 + i) * D + l * kV;
+    if constexpr (kV == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    else *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
   }
-  uint16_t* dst = (half ? v_out : k_out) + w * D + l * kV;
-  if constexpr (kV == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-  else *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
 }
 
 // ----------------------------------------------------------------- evict --
 //
 // Which slots stay: one CTA per (request, kv head).  The weight of the last
-// slot that stays is found by radix selection (four passes of eight bits over
-// order-preserving integer keys); a last pass in slot order lists the slots
-// that stay and moves their positions and weights.
+// slot that stays is found by radix selection (11, 11 and 10 bits of
+// order-preserving integer keys); then each warp counts what stays of its run
+// of slots, and lists them in slot order with their positions and weights.
+// Bound: latency (the weights are read from the caches five times); the bytes
+// are few.
 
 constexpr int kSelThreads = 1024;
 
@@ -167,9 +208,8 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 __global__ void __launch_bounds__(kSelThreads) k_kv4_select(Kv4View s, Kv4View d, int budget, int recent, int sinks,
                                                             int32_t* __restrict__ list, int32_t* status) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t s_prefix, s_need;
-  __shared__ uint32_t s_cnt[2][32];
+  __shared__ uint32_t hist[2048];
+  __shared__ uint32_t s_prefix, s_need, s_sum[2][32];
   const int h = blockIdx.x, r = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int ctx = s.ctx_len[r];
@@ -179,11 +219,11 @@ __global__ void __launch_bounds__(kSelThreads) k_kv4_select(Kv4View s, Kv4View d
   }
   const int kept = min(ctx, budget);
   if (h == 0 && tid == 0) d.ctx_len[r] = kept;
-  const float* w = s.weight + s.slot0(r, h);
-  const int32_t* pos = s.pos + s.slot0(r, h);
-  float* wd = d.weight + d.slot0(r, h);
-  int32_t* pd = d.pos + d.slot0(r, h);
-  int32_t* out = list + ((int64_t)r * s.hkv + h) * budget;
+  const float* __restrict__ w = s.weight + s.slot0(r, h);
+  const int32_t* __restrict__ pos = s.pos + s.slot0(r, h);
+  float* __restrict__ wd = d.weight + d.slot0(r, h);
+  int32_t* __restrict__ pd = d.pos + d.slot0(r, h);
+  int32_t* __restrict__ out = list + ((int64_t)r * s.hkv + h) * budget;
   if (ctx <= budget) {
     for (int t = tid; t < ctx; t += kSelThreads) {
       out[t] = t;
@@ -193,128 +233,135 @@ __global__ void __launch_bounds__(kSelThreads) k_kv4_select(Kv4View s, Kv4View d
     return;
   }
   const int lo = sinks, hi = ctx - recent;  // ctx > budget >= sinks + recent
+  const bool any = budget > sinks + recent;
   uint32_t prefix = 0, need = (uint32_t)(budget - sinks - recent);
-  for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+  for (int pass = 0; pass < 3 && any; pass++) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    hist[tid] = hist[tid + 1024] = 0;
     __syncthreads();
+#pragma unroll 4
     for (int t = lo + tid; t < hi; t += kSelThreads) {
       const uint32_t key = weight_key(w[t]);
-      if (shift == 24 || key >> (shift + 8) == prefix >> (shift + 8)) atomicAdd(&hist[key >> shift & 255], 1u);
+      if (pass == 0 || (key ^ prefix) >> (shift + bits) == 0) atomicAdd(&hist[key >> shift & ((1u << bits) - 1)], 1u);
     }
     __syncthreads();
-    if (warp == 0) {
-      // the bucket in which the need-th greatest key lies, counted from the top
-      uint32_t c[8], sum = 0;
+    // the bin in which the need-th greatest key lies, counted from the top: two
+    // bins a thread
+    const int b1 = 2047 - 2 * tid, b0 = b1 - 1;
+    const uint32_t c1 = hist[b1], c0 = hist[b0];
+    uint32_t run = c0 + c1;
 #pragma unroll
-      for (int j = 0; j < 8; j++) sum += c[j] = hist[255 - (lane * 8 + j)];
-      uint32_t run = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += v;
-      }
-      uint32_t before = run - sum;
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        if (before < need && before + c[j] >= need) {
-          s_prefix = prefix | (uint32_t)(255 - (lane * 8 + j)) << shift;
-          s_need = need - before;
-        }
-        before += c[j];
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += v;
+    }
+    if (lane == 31) s_sum[0][warp] = run;
+    __syncthreads();
+    uint32_t warps = s_sum[0][lane];  // sums of the warps before this one
+    warps = __reduce_add_sync(0xffffffffu, lane < warp ? warps : 0u);
+    const uint32_t before = warps + run - c0 - c1;
+    if (before < need && before + c1 >= need) {
+      s_prefix = prefix | (uint32_t)b1 << shift;
+      s_need = need - before;
+    } else if (before + c1 < need && before + c1 + c0 >= need) {
+      s_prefix = prefix | (uint32_t)b0 << shift;
+      s_need = need - before - c1;
     }
     __syncthreads();
     prefix = s_prefix;
     need = s_need;
-    __syncthreads();
   }
   // prefix: the least key that stays; need: how many of that key, the lowest slots first
-  const bool any = budget > sinks + recent;
-  uint32_t n_eq = 0, n_out = 0;
-  for (int base = 0; base < ctx; base += kSelThreads) {
-    const int t = base + tid;
-    const bool in = t < ctx;
-    const bool safe = in && (t < lo || t >= hi);
-    const float wt = in ? w[t] : 0.f;
+  auto kind = [&](int t, float wt) {  // 0 goes, 1 stays, 2 has the least key
+    if (t < lo || t >= hi) return 1;
     const uint32_t key = weight_key(wt);
-    const bool eq = any && in && !safe && key == prefix;
-    const bool gt = any && in && !safe && key > prefix;
-    const uint32_t be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) s_cnt[0][warp] = __popc(be);
-    __syncthreads();
-    uint32_t eq_before = n_eq, eq_all = 0;
-    for (int i = 0; i < 32; i++) {
-      if (i < warp) eq_before += s_cnt[0][i];
-      eq_all += s_cnt[0][i];
-    }
-    const uint32_t rank = eq_before + __popc(be & ((1u << lane) - 1));
-    const bool stay = safe || gt || (eq && rank < need);
+    return !any ? 0 : key > prefix ? 1 : key == prefix ? 2 : 0;
+  };
+  const int per = (ctx + kSelThreads - 1) / kSelThreads * 32, t0 = warp * per, t1 = min(ctx, t0 + per);
+  uint32_t n1 = 0, n2 = 0;
+#pragma unroll 4
+  for (int t = t0 + lane; t < t1; t += 32) {
+    const int x = kind(t, w[t]);
+    n1 += x == 1;
+    n2 += x == 2;
+  }
+  n1 = __reduce_add_sync(0xffffffffu, n1);
+  n2 = __reduce_add_sync(0xffffffffu, n2);
+  __syncthreads();
+  if (lane == 0) s_sum[0][warp] = n1, s_sum[1][warp] = n2;
+  __syncthreads();
+  n1 = lane < warp ? s_sum[0][lane] : 0;
+  n2 = lane < warp ? s_sum[1][lane] : 0;
+  uint32_t eq = __reduce_add_sync(0xffffffffu, n2);                         // of the least key, before this warp
+  uint32_t o = __reduce_add_sync(0xffffffffu, n1) + min(eq, need);          // staying before this warp
+  const uint32_t below = (1u << lane) - 1;
+  for (int t = t0 + lane; t - lane < t1; t += 32) {
+    const float wt = t < t1 ? w[t] : 0.f;
+    const int x = t < t1 ? kind(t, wt) : 0;
+    const uint32_t be = __ballot_sync(0xffffffffu, x == 2);
+    const bool stay = x == 1 || (x == 2 && eq + __popc(be & below) < need);
     const uint32_t bs = __ballot_sync(0xffffffffu, stay);
-    if (lane == 0) s_cnt[1][warp] = __popc(bs);
-    __syncthreads();
-    uint32_t before = n_out, all = 0;
-    for (int i = 0; i < 32; i++) {
-      if (i < warp) before += s_cnt[1][i];
-      all += s_cnt[1][i];
+    const uint32_t at = o + __popc(bs & below);
+    if (stay && at < (uint32_t)budget) {
+      out[at] = t;
+      wd[at] = wt;
+      pd[at] = pos[t];
     }
-    if (stay) {
-      const uint32_t o = before + __popc(bs & ((1u << lane) - 1));
-      if (o < (uint32_t)budget) {
-        out[o] = t;
-        wd[o] = wt;
-        pd[o] = pos[t];
-      }
-    }
-    n_eq += eq_all;
-    n_out += all;
+    eq += __popc(be);
+    o += __popc(bs);
   }
 }
 
-// Moves the rows that stay: one warp per group of 32 slots of dst.
+// Moves the rows that stay: one warp per group of 32 slots of dst, all of its
+// reads in flight before the first write.  Bound: bytes.
 template <int D>
-__global__ void __launch_bounds__(256) k_kv4_move(Kv4View s, Kv4View d, int R, int budget, int groups,
-                                                  const int32_t* __restrict__ list, int32_t* status) {
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (w >= (int64_t)R * s.hkv * groups) return;
-  const int lane = threadIdx.x & 31;
-  const int g = (int)(w % groups);
-  const int h = (int)(w / groups % s.hkv), r = (int)(w / groups / s.hkv);
+__global__ void __launch_bounds__(256) k_kv4_move(Kv4View s, Kv4View d, int budget, const int32_t* __restrict__ list,
+                                                  int32_t* status) {
+  const int h = blockIdx.y, r = blockIdx.z, lane = threadIdx.x & 31;
+  const int g = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int kept = min(d.ctx_len[r], budget);
   if (g * kKvGroup >= kept) return;
   uint8_t* dst = d.record(D, r, h, g);
-  if (!dst) {
-    if (lane == 0) set_status(status, SD_ERR_CAPACITY);
-    return;
-  }
   const int t = g * kKvGroup + lane;
-  int from = -1;
+  int from = 0;
   const uint8_t* src = nullptr;
   if (t < kept) {
     from = list[((int64_t)r * s.hkv + h) * budget + t];
     src = s.record(D, r, h, from / kKvGroup);
-    if (!src) set_status(status, SD_ERR_CAPACITY);
   }
-  if (src) {
-#pragma unroll
-    for (int half = 0; half < 2; half++)
-      *reinterpret_cast<uint32_t*>(dst + half * kv4_half(D) + 16 * D + lane * 4) =
-          *reinterpret_cast<const uint32_t*>(src + half * kv4_half(D) + 16 * D + (from & 31) * 4);
-  }
+  if (!dst || (t < kept && !src)) set_status(status, SD_ERR_CAPACITY);
+  if (!dst) return;
   constexpr int kCh = D / 32;      // 16-byte pieces of a row of codes
   constexpr int kKeys = 32 / kCh;  // rows moved at once
+  uint32_t sm[2];
+  uint4 x[2][32 / kKeys];
+  bool ok[32 / kKeys];
 #pragma unroll
-  for (int half = 0; half < 2; half++)
+  for (int half = 0; half < 2; half++) {
+    if (src) sm[half] = *reinterpret_cast<const uint32_t*>(src + half * kv4_half(D) + 16 * D + (from & 31) * 4);
 #pragma unroll
-    for (int j0 = 0; j0 < 32; j0 += kKeys) {
-      const int j = j0 + lane / kCh, ch = lane % kCh;
+    for (int i = 0; i < 32 / kKeys; i++) {
+      const int j = i * kKeys + lane / kCh, ch = lane % kCh;
       const uint8_t* sj = reinterpret_cast<const uint8_t*>(
           __shfl_sync(0xffffffffu, (unsigned long long)reinterpret_cast<uintptr_t>(src), j));
       const int fj = __shfl_sync(0xffffffffu, from, j);
-      if (!sj) continue;
-      const int bs = half ? kv4_vbyte<D>(fj, ch * 16) : ch * 16, bd = half ? kv4_vbyte<D>(j, ch * 16) : ch * 16;
-      *reinterpret_cast<uint4*>(dst + half * kv4_half(D) + j * (D / 2) + bd) =
-          *reinterpret_cast<const uint4*>(sj + half * kv4_half(D) + (fj & 31) * (D / 2) + bs);
+      ok[i] = sj != nullptr;
+      if (ok[i])
+        x[half][i] = *reinterpret_cast<const uint4*>(sj + half * kv4_half(D) + (fj & 31) * (D / 2) +
+                                                     (half ? kv4_vbyte<D>(fj, ch * 16) : ch * 16));
     }
+  }
+#pragma unroll
+  for (int half = 0; half < 2; half++) {
+    if (src) *reinterpret_cast<uint32_t*>(dst + half * kv4_half(D) + 16 * D + lane * 4) = sm[half];
+#pragma unroll
+    for (int i = 0; i < 32 / kKeys; i++) {
+      const int j = i * kKeys + lane / kCh, ch = lane % kCh;
+      if (ok[i])
+        *reinterpret_cast<uint4*>(dst + half * kv4_half(D) + j * (D / 2) + (half ? kv4_vbyte<D>(j, ch * 16) : ch * 16)) =
+            x[half][i];
+    }
+  }
 }
 
 // ---------------------------------------------------------------- checks --
@@ -398,11 +445,10 @@ extern "C" int sd_kv4_append(const sd_kv4* c, const uint16_t* k, const uint16_t*
   if (n_src < 0 || (!src && n_src < rows)) return kv4_bad(SD_ERR_INVALID_ARG, who, "fewer rows in k and v than in cu");
   if (rows == 0) return SD_OK;
   const bool in_place = !at || at == c->ctx_len;
-  const int64_t blocks = ((int64_t)rows * c->n_kv_heads + 7) / 8;
-  if (blocks > 0x7FFFFFFF) return kv4_bad(SD_ERR_UNSUPPORTED, who, "too many rows");
+  const dim3 grid((rows + 7) / 8, (c->n_kv_heads + kHeads - 1) / kHeads);
   cudaStream_t st = (cudaStream_t)stream;
   auto kern = c->head_dim == 128 ? k_kv4_append<128> : k_kv4_append<64>;
-  kern<<<(unsigned)blocks, 256, 0, st>>>(view, k, v, row_stride, n_src, cu, R, rows, src, count, pos,
+  kern<<<grid, 256, 0, st>>>(view, k, v, row_stride, n_src, cu, R, rows, src, count, pos,
                                          in_place ? c->ctx_len : at, !in_place, status);
   SD_CK(cudaGetLastError());
   if (in_place) {
@@ -422,10 +468,9 @@ extern "C" int sd_kv4_read(const sd_kv4* c, const int32_t* cu, const int32_t* cu
     return kv4_bad(SD_ERR_INVALID_ARG, who, "k_out and v_out must be set and 16-byte aligned");
   const int rows = cu_host[R];
   if (rows == 0) return SD_OK;
-  const int64_t blocks = ((int64_t)rows * c->n_kv_heads + 7) / 8;
-  if (blocks > 0x7FFFFFFF) return kv4_bad(SD_ERR_UNSUPPORTED, who, "too many rows");
+  const dim3 grid((rows + 7) / 8, (c->n_kv_heads + kHeads - 1) / kHeads);
   auto kern = c->head_dim == 128 ? k_kv4_read<128> : k_kv4_read<64>;
-  kern<<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(view, cu, R, rows, at, k_out, v_out, status);
+  kern<<<grid, 256, 0, (cudaStream_t)stream>>>(view, cu, R, rows, at, k_out, v_out, status);
   SD_CK(cudaGetLastError());
   return SD_OK;
 }
@@ -457,10 +502,8 @@ extern "C" int sd_kv4_evict(const sd_kv4* src, const sd_kv4* dst, int32_t R, int
   k_kv4_select<<<dim3(src->n_kv_heads, R), kSelThreads, 0, st>>>(s, d, budget, recent, sinks, list, status);
   SD_CK(cudaGetLastError());
   const int groups = (int)(((int64_t)budget + kKvGroup - 1) / kKvGroup);
-  const int64_t blocks = ((int64_t)R * src->n_kv_heads * groups + 7) / 8;
-  if (blocks > 0x7FFFFFFF) return kv4_bad(SD_ERR_UNSUPPORTED, who, "too many slots");
   auto kern = src->head_dim == 128 ? k_kv4_move<128> : k_kv4_move<64>;
-  kern<<<(unsigned)blocks, 256, 0, st>>>(s, d, R, budget, groups, list, status);
+  kern<<<dim3((groups + 7) / 8, src->n_kv_heads, R), 256, 0, st>>>(s, d, budget, list, status);
   SD_CK(cudaGetLastError());
   return SD_OK;
 }

@@ -207,48 +207,81 @@ struct TcRowsOf {
 
 // Joins the parts of a segment and writes its rows, by the softmax threads.
 template <int D, bool WIDE>
-__device__ __forceinline__ void tc_join(const Kv4AttnArgs& a, const Kv4Join& jn, int slot0, int st) {
+__device__ __forceinline__ void tc_join(const Kv4AttnArgs& a, const Kv4Join& jn, int slot0, int st,
+                                        float2* s_ml) {
   const int gm = a.G * jn.m, nc = (gm + kt::kRows - 1) / kt::kRows;
   const TcRowsOf<WIDE> rw(gm, nc, jn.rc);
-  for (int i = st; i < rw.rows * (D / 4); i += kt::kSoftThreads) {
-    const int row = i / (D / 4), x = i % (D / 4);
+  auto part_of = [&](int p) {
+    return a.part + (int64_t)(p == 0 ? slot0 : 2 * (jn.c0 + p)) * TcShape<D, WIDE>::kPart;
+  };
+  auto row_out = [&](int row) {
+    const int rho = rw.base + row, gq = rho / jn.m;
+    return (int64_t)(jn.n0 + rho - gq * jn.m) * a.hq + jn.h * a.G + gq;
+  };
+  // a row's maximum and sum, eight parts in flight
+  if (st < rw.rows) {
     float M = -INFINITY, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = 0; c < jn.n; c += 4) {  // four parts in flight
-      float2 ml[4];
-      float4 v[4];
+    for (int c = 0; c < jn.n; c += 8) {
+      float2 ml[8];
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
-        const int p = min(c + k, jn.n - 1);
-        const float* pc = a.part + (int64_t)(p == 0 ? slot0 : 2 * (jn.c0 + p)) * TcShape<D, WIDE>::kPart;
-        ml[k] = __ldcg(reinterpret_cast<const float2*>(pc + kt::kRows * D) + row);
-        v[k] = __ldcg(reinterpret_cast<const float4*>(pc) + i);
-      }
+      for (int k = 0; k < 8; k++) ml[k] = __ldcg(reinterpret_cast<const float2*>(part_of(min(c + k, jn.n - 1)) + kt::kRows * D) + st);
       float Mn = M;
 #pragma unroll
-      for (int k = 0; k < 4; k++) Mn = fmaxf(Mn, ml[k].x);
-      const float Ms = Mn == -INFINITY ? 0.f : Mn, al = ex2(M - Ms);
+      for (int k = 0; k < 8; k++) Mn = fmaxf(Mn, ml[k].x);
+      const float Ms = Mn == -INFINITY ? 0.f : Mn;
+      L *= ex2(M - Ms);
       M = Mn;
-      L *= al;
-      acc.x *= al, acc.y *= al, acc.z *= al, acc.w *= al;
 #pragma unroll
-      for (int k = 0; k < 4; k++)
-        if (c + k < jn.n) {
-          const float f = ex2(ml[k].x - Ms);
-          L = fmaf(f, ml[k].y, L);
-          acc.x = fmaf(f, v[k].x, acc.x);
-          acc.y = fmaf(f, v[k].y, acc.y);
-          acc.z = fmaf(f, v[k].z, acc.z);
-          acc.w = fmaf(f, v[k].w, acc.w);
-        }
+      for (int k = 0; k < 8; k++)
+        if (c + k < jn.n) L = fmaf(ex2(ml[k].x - Ms), ml[k].y, L);
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int rho = rw.base + row, gq = rho / jn.m;
-    const int64_t at = (int64_t)(jn.n0 + rho - gq * jn.m) * a.hq + jn.h * a.G + gq;
-    *reinterpret_cast<uint2*>(a.out + at * D + 4 * x) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (x == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
+    if (a.lse) a.lse[row_out(st)] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
+    s_ml[st] = make_float2(M == -INFINITY ? 0.f : M, L == 0.f ? 0.f : 1.f / L);
   }
+  bar_sync(2, kt::kSoftThreads);
+  // four pieces of four dims a thread, four parts of each in flight
+  const int items = rw.rows * (D / 4);
+  for (int i0 = st; i0 < items; i0 += 4 * kt::kSoftThreads) {
+    float4 acc[4];
+#pragma unroll
+    for (int q = 0; q < 4; q++) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < jn.n; c += 4) {
+      float m[4][4];
+      float4 v[4][4];
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const int i = min(i0 + q * kt::kSoftThreads, items - 1);
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const float* pc = part_of(min(c + k, jn.n - 1));
+          m[q][k] = __ldcg(pc + kt::kRows * D + 2 * (i / (D / 4)));
+          v[q][k] = __ldcg(reinterpret_cast<const float4*>(pc) + i);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const float2 ml = s_ml[min(i0 + q * kt::kSoftThreads, items - 1) / (D / 4)];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const float f = c + k < jn.n ? ex2(m[q][k] - ml.x) * ml.y : 0.f;
+          if (c + k < jn.n) {
+            acc[q].x = fmaf(f, v[q][k].x, acc[q].x);
+            acc[q].y = fmaf(f, v[q][k].y, acc[q].y);
+            acc[q].z = fmaf(f, v[q][k].z, acc[q].z);
+            acc[q].w = fmaf(f, v[q][k].w, acc[q].w);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      const int i = i0 + q * kt::kSoftThreads;
+      if (i < items)
+        *reinterpret_cast<uint2*>(a.out + row_out(i / (D / 4)) * D + 4 * (i % (D / 4))) =
+            make_uint2(pack_bf16x2(acc[q].x, acc[q].y), pack_bf16x2(acc[q].z, acc[q].w));
+    }
+  }
+  bar_sync(2, kt::kSoftThreads);
 }
 
 // A softmax thread's row in a segment, and what its loop leaves.
@@ -861,7 +894,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
       bar_sync(2, kt::kSoftThreads);
       for (int d = 0; d < 2; d++) {
         const Kv4Join jn = s_join[d];
-        if (jn.n) tc_join<D, WIDE>(a, jn, 2 * jn.c0 + (sh.first(jn.c0) < jn.seg ? 1 : 0), st256);
+        if (jn.n) tc_join<D, WIDE>(a, jn, 2 * jn.c0 + (sh.first(jn.c0) < jn.seg ? 1 : 0), st256, s_ml);
       }
   }
   tc_fence_before();

@@ -13,19 +13,6 @@ namespace sdv {
 
 constexpr int kHeads = 4;
 
-// The request of row e, by the whole warp: a search 32 offsets at a time.
-__device__ __forceinline__ int request_of(const int32_t* __restrict__ cu, int R, int e) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = R;  // cu[lo] <= e < cu[hi]
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, x = lo + lane * step;
-    const int n = __popc(__ballot_sync(0xffffffffu, x < hi && cu[x] <= e));
-    lo += (n - 1) * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
-
 // N consecutive 16-bit values of a row as 32-bit words.
 template <int N>
 __device__ __forceinline__ void load_row(const uint16_t* p, uint32_t (&w)[N / 2]) {

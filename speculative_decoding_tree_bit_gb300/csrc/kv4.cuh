@@ -46,6 +46,19 @@ __device__ __forceinline__ int kv4_vbyte(int t, int b) {
   return D == 128 ? b ^ ((t & 2) << 4) : b;
 }
 
+// The request of row e, by the whole warp: a search 32 offsets at a time.
+__device__ __forceinline__ int request_of(const int32_t* __restrict__ cu, int R, int e) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = R;  // cu[lo] <= e < cu[hi]
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, x = lo + lane * step;
+    const int n = __popc(__ballot_sync(0xffffffffu, x < hi && cu[x] <= e));
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
 // What the scores of a call go by.
 struct Kv4Score {
   float scale, cap;        // cap 0: none

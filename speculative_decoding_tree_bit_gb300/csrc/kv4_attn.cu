@@ -989,10 +989,10 @@ static int launch_observe(const Kv4ObserveArgs& b, int64_t units, bool bias, cud
 constexpr int kWarpRows = 16;
 
 template <int D>
-static int launch_attn(const Kv4AttnArgs& a, int rows, int64_t units, bool bias, cudaStream_t st) {
+static int launch_attn(const Kv4AttnArgs& a, int total, int rows, int64_t segs, int64_t units, bool bias, cudaStream_t st) {
   if (rows <= 8) return launch_attn_tile<D, 1, 8>(a, units, bias, st);
   if (rows <= kWarpRows) return launch_attn_tile<D, 2, 6>(a, units, bias, st);
-  return kv4_launch_attn_tc(a, D, rows, (units + 1) / 2, bias, st);
+  return kv4_launch_attn_tc(a, D, total, rows, segs, (units + 1) / 2, bias, st);
 }
 
 // ---------------------------------------------------------------- checks --
@@ -1032,7 +1032,7 @@ extern "C" size_t sd_kv4_attn_workspace(int32_t R, int32_t rows, int32_t n_q_hea
     return 0;
   const size_t warp = (size_t)4 * num_sms() * kWarpRows * (head_dim + 2) * sizeof(float);
   const int most = std::min(rows, 64) * (n_q_heads / n_kv_heads);
-  return kTicketBytes + (most > kWarpRows ? std::max(warp, kv4_tc_workspace(head_dim)) : warp);
+  return kTicketBytes + (most > kWarpRows ? std::max(warp, kv4_tc_workspace(R, n_kv_heads, head_dim)) : warp);
 }
 
 extern "C" int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride, int32_t n_q_heads, const int32_t* cu,
@@ -1068,15 +1068,19 @@ extern "C" int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride,
   a.tickets = (int32_t*)workspace;
   a.part = (float*)((uint8_t*)workspace + kTicketBytes);
   int most = 0;
-  for (int r = 0; r < R; r++) most = std::max(most, cu_host[r + 1] - cu_host[r]);
-  most *= a.G;
+  int64_t segs = 0;  // of the tensor-core kernel
+  for (int r = 0; r < R; r++) {
+    const int n = (cu_host[r + 1] - cu_host[r]) * a.G;
+    most = std::max(most, n);
+    segs += (int64_t)c->n_kv_heads * ((n + 255) / 256);
+  }
   const int64_t ctx = max_ctx > 0 ? std::min<int64_t>(max_ctx, a.c.cap) : a.c.cap;
   const int64_t units = (int64_t)R * c->n_kv_heads * ((most + 31) / 32) * ((ctx + 31) / 32 + 2);
   if ((int64_t)R * c->n_kv_heads * ((most + 7) / 8) * ((a.c.cap + 31) / 32 + 2) > 0x7FFFFFFF)
     return kv4_bad(SD_ERR_UNSUPPORTED, who, "more than 2^31 runs of 32 keys");
   const bool bias = a.s.cap > 0.f || a.s.slopes || a.s.window > 0 || a.s.start;
-  return c->head_dim == 128 ? launch_attn<128>(a, most, units, bias, (cudaStream_t)stream)
-                            : launch_attn<64>(a, most, units, bias, (cudaStream_t)stream);
+  return c->head_dim == 128 ? launch_attn<128>(a, rows, most, segs, units, bias, (cudaStream_t)stream)
+                            : launch_attn<64>(a, rows, most, segs, units, bias, (cudaStream_t)stream);
 }
 
 extern "C" int sd_kv4_observe(const sd_kv4* c, const uint16_t* q, int64_t q_stride, int32_t n_q_heads,

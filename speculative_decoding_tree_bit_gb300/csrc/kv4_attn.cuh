@@ -21,6 +21,7 @@ struct Kv4AttnArgs {
   int32_t* status;
   int32_t* tickets;  // [grid], zero between calls
   float* part;       // [2 grid][rows of a tile][D + 2]
+  int4* joins;       // many rows: where a segment's parts lie, if a kernel of its own joins them
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -236,7 +237,8 @@ struct Kv4Join {
 };
 
 // Many rows a kv head (kv4_attn_tc.cu).
-size_t kv4_tc_workspace(int head_dim);
-int kv4_launch_attn_tc(const Kv4AttnArgs& a, int head_dim, int rows, int64_t units, bool bias, cudaStream_t st);
+size_t kv4_tc_workspace(int R, int hkv, int head_dim);
+int kv4_launch_attn_tc(const Kv4AttnArgs& a, int head_dim, int rows, int most, int64_t segs, int64_t units, bool bias,
+                       cudaStream_t st);
 
 }  // namespace sdv

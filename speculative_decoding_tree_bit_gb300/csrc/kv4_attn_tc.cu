@@ -7,7 +7,7 @@
 // so the softmax warps never wait for a product.  Warps, each role walking the
 // CTA's units on its own:
 //  * 16: records into a ring of eight, one bulk copy each;
-//  * 0..7: nibbles to fp16 operands, four warps a key tile, alternate tiles.
+//  * 0..3 and 4..7: nibbles to fp16 operands, K's and V's.
 //    K's codes as they are (subnormal code 2^-24; the key's scale and middle
 //    are applied to its score, as in the warp kernel); V's as values, s (code -
 //    8) + m in one fp16 multiply-add per pair, times a power of two that
@@ -41,6 +41,7 @@ namespace kt {
 constexpr int kSoft = 8, kLoad = 16, kMma = 17, kThreads = 20 * 32, kSoftThreads = 256;
 constexpr int kRaw = 8;
 constexpr int kRows = 256;  // of a segment, at most
+constexpr int kJoins = 4;   // segments of a (request, kv head), at most: 64 rows x 16 heads
 }  // namespace kt
 
 template <int D, bool WIDE>
@@ -57,10 +58,11 @@ struct TcShape {
   static constexpr int off_pos = off_sc + NS * 64 * 8;               // [NS][64]
   static constexpr int off_info = off_pos + NS * 64 * 4;             // [NS] (keys held, masks of either half, exponent of V << 1 | own)
   static constexpr int off_bar = off_info + NS * 16;
-  static constexpr int off_ok = off_bar + (2 * kt::kRaw + 2 * NS + 12) * 8;
-  static constexpr int off_vmax = off_ok + kt::kRaw * 4;             // [8]
-  static constexpr int off_ml = off_vmax + 32;                       // [2 t][128] (max, sum)
-  static constexpr int smem = off_ml + 256 * 8 + 1024;
+  static constexpr int off_ok = off_bar + (2 * kt::kRaw + 2 * NS + 14) * 8;
+  static constexpr int off_vmax = off_ok + kt::kRaw * 4;             // [4]
+  static constexpr int off_ml = off_vmax + 16;                       // [2 t][128] (max, sum)
+  static constexpr int off_inv = off_ml + 256 * 8;                   // [kRows] 1 / sum
+  static constexpr int smem = off_inv + kt::kRows * 4 + 1024;
   static constexpr int kPart = kt::kRows * (D + 2);                  // floats of a part: [rows][D], then [rows] (max, sum)
 };
 
@@ -154,10 +156,8 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
 // Exponent e of |x| < 2^(e+1); -127 of 0 and subnormals.
 __device__ __forceinline__ int expo(uint32_t bits) { return (int)(bits >> 23 & 255) - 127; }
 
-// Exponent that keeps a tile's V operands below 2^-6, a multiple of 4: the two
-// decoding groups keep one each, the greatest of their own tiles, and a change
-// from tile to tile costs a rescaling of O.
-__device__ __forceinline__ int tc_exponent(uint32_t bits) { return (expo(bits) + 7 + 3) & ~3; }
+// Exponent that keeps V operands of magnitude at most |x| (bits) below 2^-6.
+__device__ __forceinline__ int tc_exponent(uint32_t bits) { return expo(bits) + 7; }
 
 // A CTA's walk over its segments.
 struct TcWalk {
@@ -193,9 +193,9 @@ struct TcWalk {
 // of them from row first(t) on, `copies` times, 128 / copies lanes apart.
 template <bool WIDE>
 struct TcRowsOf {
-  int base, rows, split, copies;
+  int base, rows, split, copies, run;
   __device__ __forceinline__ TcRowsOf(int gm, int nc, int rc) {
-    const int run = ((gm + nc - 1) / nc + 31) / 32 * 32;
+    run = ((gm + nc - 1) / nc + 31) / 32 * 32;
     base = rc * run;
     rows = min(run, gm - base);
     split = WIDE ? min(rows, (rows / 2 + 31) / 32 * 32) : rows;
@@ -284,6 +284,62 @@ __device__ __forceinline__ void tc_join(const Kv4AttnArgs& a, const Kv4Join& jn,
   bar_sync(2, kt::kSoftThreads);
 }
 
+// The same by a kernel of its own, a warp a row, where a segment has many parts
+// (a few CTAs would join what the others wrote, 10 us of a 64-row tree over
+// 2048 keys against 3 for the launch).
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(256) k_kv4_join(Kv4AttnArgs a, int rows) {
+  pdl_wait();
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);  // (row, query head)
+  if (i >= (int64_t)rows * a.hq) return;
+  const int lane = threadIdx.x & 31;
+  const int e = (int)(i / a.hq), hq = (int)(i - (int64_t)e * a.hq), h = hq / a.G;
+  const int r = request_of(a.cu, a.R, e);
+  const Kv4Req rq = kv4_req<kt::kRows, 2>(a, r);
+  if (rq.m == 0) return;
+  const int rho = (hq - h * a.G) * rq.m + e - rq.n0;
+  const int run = TcRowsOf<WIDE>(a.G * rq.m, rq.nc, 0).run, rc = rho / run, row = rho - rc * run;
+  const int4 jn = a.joins[((int64_t)r * a.c.hkv + h) * kt::kJoins + rc];  // (first CTA, parts, first slot, -)
+  if (jn.y == 0) return;  // whole in one CTA, which wrote it
+  auto part_of = [&](int p) { return a.part + (int64_t)(p == 0 ? jn.z : 2 * (jn.x + p)) * TcShape<D, WIDE>::kPart; };
+  float M = -INFINITY, L = 0.f;
+  for (int p = lane; p < jn.y; p += 32) M = fmaxf(M, __ldcg(part_of(p) + kt::kRows * D + 2 * row));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float Ms = M == -INFINITY ? 0.f : M;
+  constexpr int kF = D / 32;  // dims of a lane
+  float acc[kF] = {};
+  for (int c = 0; c < jn.y; c += 8) {
+    float2 ml[8];
+    float v[8][kF];
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      const float* pc = part_of(min(c + k, jn.y - 1));
+      ml[k] = __ldcg(reinterpret_cast<const float2*>(pc + kt::kRows * D) + row);
+      if constexpr (kF == 4) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(pc + row * D) + lane);
+        v[k][0] = u.x, v[k][1] = u.y, v[k][2] = u.z, v[k][3] = u.w;
+      } else {
+        const float2 u = __ldcg(reinterpret_cast<const float2*>(pc + row * D) + lane);
+        v[k][0] = u.x, v[k][1] = u.y;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+      if (c + k < jn.y) {
+        const float f = ex2(ml[k].x - Ms);
+        L = fmaf(f, ml[k].y, L);
+#pragma unroll
+        for (int q = 0; q < kF; q++) acc[q] = fmaf(f, v[k][q], acc[q]);
+      }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint32_t* out = reinterpret_cast<uint32_t*>(a.out + i * D) + lane * (kF / 2);
+#pragma unroll
+  for (int q = 0; q < kF; q += 2) out[q / 2] = pack_bf16x2(acc[q] * inv, acc[q + 1] * inv);
+  if (lane == 0 && a.lse) a.lse[i] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
+}
+
 // A softmax thread's row in a segment, and what its loop leaves.
 struct TcRow {
   float qsf, fac, slope;   // sum of q, factor of a score, slope
@@ -298,7 +354,7 @@ struct TcRow {
 // The softmax of a segment's units of tile t, NC keys of each (the copy's share).
 template <int D, bool BIAS, bool WIDE, int NC>
 __device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint32_t tb, int i0, int n, uint32_t op0,
-                                           uint32_t& nsc, uint32_t& par, uint64_t* s_full, uint64_t* op_full, uint64_t* p_full,
+                                           uint32_t& par, uint64_t* s_full, uint64_t* op_full, uint64_t* p_full,
                                            uint64_t* o_full, const float2* s_sc, const int* s_pos, const int4* s_info,
                                            int* s_abort) {
   constexpr int NS = TcShape<D, WIDE>::NS, step = WIDE ? 1 : 2;
@@ -310,7 +366,6 @@ __device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint3
     const int b = buf >> 6;
     if (!kv4_wait(s_full + b, par >> b & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(33));
     par ^= 1u << b;
-    nsc++;
     if (!kv4_wait(&op_full[st], (op0 + i) / NS & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(34));
     tc_fence_after();
     const int4 info = s_info[st];
@@ -354,8 +409,9 @@ __device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint3
         }
         if (w.any) {
           if (moves) al *= pow2i(max(w.E - E, -126));
-          // the product before may still be adding to O
-          if (!kv4_wait(o_full, nsc & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(35));
+          // the product before may still be adding to O (the one before that was
+          // done before these scores)
+          if (!kv4_wait(o_full + (b ^ 1), par >> (b ^ 1) & 1 ^ 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(35));
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
@@ -414,22 +470,24 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   int* const s_pos = reinterpret_cast<int*>(sm + S::off_pos);
   int4* const s_info = reinterpret_cast<int4*>(sm + S::off_info);
   uint64_t* const raw_full = reinterpret_cast<uint64_t*>(sm + S::off_bar);  // record landed
-  uint64_t* const raw_empty = raw_full + kt::kRaw;   // record decoded (4 warps)
-  uint64_t* const op_full = raw_empty + kt::kRaw;    // operands, scales written (4 warps)
+  uint64_t* const raw_empty = raw_full + kt::kRaw;   // record decoded (8 warps)
+  uint64_t* const op_full = raw_empty + kt::kRaw;    // operands, scales written (8 warps)
   uint64_t* const op_empty = op_full + NS;           // products done with them (commit)
   uint64_t* const q_full = op_empty + NS;            // [t] queries in TMEM (4 warps)
   uint64_t* const s_full = q_full + 2;               // [t][buffer] scores ready (commit)
   uint64_t* const p_full = s_full + 4;               // [t][buffer] weights written (4 warps)
-  uint64_t* const o_full = p_full + 4;               // [t] a product with V done (commit)
+  uint64_t* const o_full = p_full + 4;               // [t][buffer] the product with V done (commit)
   int* const s_ok = reinterpret_cast<int*>(sm + S::off_ok);
   uint32_t* const s_vmax = reinterpret_cast<uint32_t*>(sm + S::off_vmax);
   float2* const s_ml = reinterpret_cast<float2*>(sm + S::off_ml);
+  float* const s_inv = reinterpret_cast<float*>(sm + S::off_inv);
   float* const s_x = reinterpret_cast<float*>(sm + S::off_q);
   __shared__ int s_abort;
   __shared__ uint32_t s_tmem;
   __shared__ Kv4Share sh;
   __shared__ Kv4Join s_join[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch();
 
   if (warp == kt::kSoft) kv4_share<kt::kRows, 2>(a, 4, sh);
   if (warp == kt::kMma) {
@@ -437,12 +495,12 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < kt::kRaw; i++) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 4);
-    for (int i = 0; i < NS; i++) mbar_init(&op_full[i], 4), mbar_init(&op_empty[i], 1);
+    for (int i = 0; i < kt::kRaw; i++) mbar_init(&raw_full[i], 1), mbar_init(&raw_empty[i], 8);
+    for (int i = 0; i < NS; i++) mbar_init(&op_full[i], 8), mbar_init(&op_empty[i], 1);
     for (int t = 0; t < 2; t++) {
       mbar_init(&q_full[t], 4);
-      for (int b = 0; b < 2; b++) mbar_init(&s_full[2 * t + b], 1), mbar_init(&p_full[2 * t + b], 4);
-      mbar_init(&o_full[t], 1);
+      for (int b = 0; b < 2; b++)
+        mbar_init(&s_full[2 * t + b], 1), mbar_init(&p_full[2 * t + b], 4), mbar_init(&o_full[2 * t + b], 1);
     }
     s_abort = 0;
     s_join[0] = s_join[1] = Kv4Join{};
@@ -529,7 +587,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
 #pragma unroll
               for (int x = 0; x < 4; x++)
                 if (x < 2 || two) umma_f16_ts(o, p + 8 * x, vd + x * (2048 >> 4), idv, !first || x > 0);
-              umma_commit(&o_full[t]);
+              umma_commit(&o_full[2 * t + b]);
               if (release) umma_commit(&op_empty[st]);
             }
             __syncwarp();
@@ -561,31 +619,27 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
       // ------------------------------------------------------- operands --
       asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
       TcWalk w(a, sh);
-      // group dg takes the even or the odd tiles of the CTA's walk
-      const int dg = warp >> 2, dt = tid & 127, dw = warp & 3;
+      const bool is_k = warp < 4;
+      const int dt = tid & 127, dw = warp & 3;
+      // eight lanes take four rows' neighbouring 16-byte pieces: two phases a
+      // read, none shared a write
+      const int row = 16 * (dw & 1) + 4 * (lane >> 3) + (lane >> 1 & 3);
+      const int cg = (D == 128 ? 2 * (dw >> 1) : 0) + (lane & 1);
+      const bool mine = D == 128 || dw < 2;
+      const uint32_t at0 = (is_k ? 0 : S::kOp) + (cg >> 1) * 8192 + row * 128;
       uint32_t op = 0, nraw = 0;
       do {
         int E = -100;  // V operands are values times 2^-E, below 2^-6
         const int h = w.head();
         for (int u = w.ua; u < w.ub; u++, op++) {
-          if ((op & 1) != dg) {
-            if (u >= w.rq.no) nraw += w.groups(a, u);
-            continue;
-          }
           const int st = op % NS;
-          uint8_t* const ko = sm + st * 2 * S::kOp;
-          uint8_t* const vo = ko + S::kOp;
+          uint8_t* const dst = sm + st * 2 * S::kOp;
           if (u >= w.rq.no) {
             const int ga = w.rq.g0 + 2 * (u - w.rq.no), ng = w.groups(a, u);
-            // everything this thread needs of the records, then their slots are
-            // free.  Eight lanes take four rows' neighbouring 16-byte pieces:
-            // two phases a read, none shared a write
-            const int row = 16 * (dw & 1) + 4 * (lane >> 3) + (lane >> 1 & 3);
-            const int cg = (D == 128 ? 2 * (dw >> 1) : 0) + (lane & 1);
-            const bool do_k = D == 128 || dw < 2, do_v = D == 128 || dw >= 2;
+            // everything this thread needs of the records, then their slots are free
             int lim[2] = {0, 0};
-            uint32_t vsm[2] = {0, 0}, ksm = 0, ksv = 0, vb = 0;
-            uint4 xk[2], xv[2];
+            uint32_t sm0[2] = {0, 0}, ksm = 0, ksv = 0, vb = 0;
+            uint4 x[2];
             int kpos = 0;
 #pragma unroll
             for (int gi = 0; gi < 2; gi++) {
@@ -594,134 +648,130 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
               wait(&raw_full[slot], (nraw + gi) / kt::kRaw);
               const uint8_t* rec = raw + slot * S::kStage;
               lim[gi] = s_ok[slot] ? max(0, min(kKvGroup, w.rq.ctx - (ga + gi) * kKvGroup)) : 0;
-              const uint32_t vw = *reinterpret_cast<const uint32_t*>(rec + kv4_half(D) + 16 * D + lane * 4);
-              if (do_k) xk[gi] = *reinterpret_cast<const uint4*>(rec + row * (D / 2) + cg * 16);
-              if (do_v) {
-                xv[gi] = *reinterpret_cast<const uint4*>(rec + kv4_half(D) + row * (D / 2) + (D == 128 ? cg ^ (row & 2) : cg) * 16);
-                vsm[gi] = *reinterpret_cast<const uint32_t*>(rec + kv4_half(D) + 16 * D + row * 4);
+              if (is_k) {
+                if (mine) x[gi] = *reinterpret_cast<const uint4*>(rec + row * (D / 2) + cg * 16);
+                if (dw == gi) {
+                  ksm = *reinterpret_cast<const uint32_t*>(rec + 16 * D + lane * 4);
+                  ksv = *reinterpret_cast<const uint32_t*>(rec + kv4_half(D) + 16 * D + lane * 4);
+                  if (BIAS) kpos = *reinterpret_cast<const int*>(rec + kv4_rec(D) + lane * 4);
+                }
+              } else {
+                const uint8_t* v = rec + kv4_half(D);
+                if (mine) x[gi] = *reinterpret_cast<const uint4*>(v + row * (D / 2) + (D == 128 ? cg ^ (row & 2) : cg) * 16);
+                sm0[gi] = *reinterpret_cast<const uint32_t*>(v + 16 * D + row * 4);
+                const uint32_t vw = *reinterpret_cast<const uint32_t*>(v + 16 * D + lane * 4);
+                const float b = fmaf(8.f, __uint_as_float(vw << 16), fabsf(__uint_as_float(vw & 0xFFFF0000u)));
+                if (lane < lim[gi] && b <= 3.4e38f) vb = max(vb, __float_as_uint(b));
               }
-              if (dt >> 5 == gi) {
-                ksm = *reinterpret_cast<const uint32_t*>(rec + 16 * D + lane * 4);
-                ksv = vw;
-                if (BIAS) kpos = *reinterpret_cast<const int*>(rec + kv4_rec(D) + lane * 4);
-              }
-              const float b = fmaf(8.f, __uint_as_float(vw << 16), fabsf(__uint_as_float(vw & 0xFFFF0000u)));
-              if (lane < lim[gi] && b <= 3.4e38f) vb = max(vb, __float_as_uint(b));
             }
             __syncwarp();
             if (lane == 0)
               for (int gi = 0; gi < ng; gi++) mbar_arrive(&raw_empty[(nraw + gi) % kt::kRaw]);
             nraw += ng;
-            E = min(max(E, tc_exponent(__reduce_max_sync(0xffffffffu, vb))), 120);
             wait(&op_empty[st], (op / NS & 1) ^ 1);
-            if (dt < 64) {
-              float2 sc = make_float2(0.f, 0.f);
-              if (lane < (dt < 32 ? lim[0] : lim[1])) {
-                const float s = __uint_as_float(ksm << 16), m = __uint_as_float(ksm & 0xFFFF0000u);
-                // a row of one value has s = 0 and every code 8: any s will do
-                sc.y = s == 0.f ? fmaxf(fabsf(m) * 0.0625f, 1e-30f) : s;
-                sc.x = m / sc.y - 8.f;
-                if (!(fabsf(__uint_as_float(ksv << 16)) <= 3.4e38f)) sc.x = __int_as_float(0x7FC00000);  // V held as NaN
-                if (BIAS) s_pos[st * 64 + dt] = kpos;
+            if (is_k) {
+              if (dw < 2) {
+                float2 sc = make_float2(0.f, 0.f);
+                if (lane < (dw ? lim[1] : lim[0])) {
+                  const float s = __uint_as_float(ksm << 16), m = __uint_as_float(ksm & 0xFFFF0000u);
+                  // a row of one value has s = 0 and every code 8: any s will do
+                  sc.y = s == 0.f ? fmaxf(fabsf(m) * 0.0625f, 1e-30f) : s;
+                  sc.x = m / sc.y - 8.f;
+                  if (!(fabsf(__uint_as_float(ksv << 16)) <= 3.4e38f)) sc.x = __int_as_float(0x7FC00000);  // V held as NaN
+                  if (BIAS) s_pos[st * 64 + dt] = kpos;
+                }
+                float* const p = reinterpret_cast<float*>(s_sc + st * 64) + (dt >> 1) * 4 + (dt & 1);
+                p[0] = sc.x;
+                p[2] = sc.y;
               }
-              reinterpret_cast<float*>(s_sc + st * 64)[(dt >> 1) * 4 + (dt & 1)] = sc.x;
-              reinterpret_cast<float*>(s_sc + st * 64)[(dt >> 1) * 4 + 2 + (dt & 1)] = sc.y;
-            }
-            if (dt == 0)
-              s_info[st] = make_int4(lim[0] + lim[1], lim[0] == 32 ? -1 : (1 << lim[0]) - 1, lim[1] == 32 ? -1 : (1 << lim[1]) - 1, E * 2);
-            const float down = pow2i(-E), up = pow2i(24 - E), up4 = pow2i(20 - E);
 #pragma unroll
-            for (int gi = 0; gi < 2; gi++) {
-              if (gi >= ng) break;
-              const int R = gi * 32 + row;
-              const uint32_t at = (cg >> 1) * 8192 + R * 128;
-              if (do_k) {
-                const uint32_t xs[4] = {xk[gi].x, xk[gi].y, xk[gi].z, xk[gi].w};
+              for (int gi = 0; gi < 2; gi++) {
+                if (gi >= ng || !mine) break;
+                const uint32_t xs[4] = {x[gi].x, x[gi].y, x[gi].z, x[gi].w};
 #pragma unroll
                 for (int j = 0; j < 4; j++)
-                  *reinterpret_cast<uint4*>(ko + at + ((((cg & 1) * 4 + j) ^ (R & 7)) << 4)) =
+                  *reinterpret_cast<uint4*>(dst + at0 + gi * 4096 + ((((cg & 1) * 4 + j) ^ (row & 7)) << 4)) =
                       make_uint4(codes2<0>(xs[j]), codes2<1>(xs[j]), codes2<2>(xs[j]), codes2<3>(xs[j]));
               }
-              if (do_v) {
-                float s = __uint_as_float(vsm[gi] << 16), m = __uint_as_float(vsm[gi] & 0xFFFF0000u);
+            } else {
+              E = min(max(E, tc_exponent(__reduce_max_sync(0xffffffffu, vb))), 120);
+              if (dt == 0)
+                s_info[st] = make_int4(lim[0] + lim[1], lim[0] == 32 ? -1 : (1 << lim[0]) - 1,
+                                       lim[1] == 32 ? -1 : (1 << lim[1]) - 1, E * 2);
+#pragma unroll
+              for (int gi = 0; gi < 2; gi++) {
+                if (gi >= ng || !mine) break;
+                float s = __uint_as_float(sm0[gi] << 16), m = __uint_as_float(sm0[gi] & 0xFFFF0000u);
                 if (row >= lim[gi] || !(s <= 3.4e38f)) s = m = 0.f;  // not held, or NaN: its scores say so
-                const uint32_t me = h2dup(s * up), mo = h2dup(s * up4), cc = h2dup(fmaf(-8.f, s, m) * down);
-                const uint32_t xs[4] = {xv[gi].x, xv[gi].y, xv[gi].z, xv[gi].w};
+                const uint32_t me = h2dup(s * pow2i(24 - E)), mo = h2dup(s * pow2i(20 - E)),
+                               cc = h2dup(fmaf(-8.f, s, m) * pow2i(-E));
+                const uint32_t xs[4] = {x[gi].x, x[gi].y, x[gi].z, x[gi].w};
 #pragma unroll
                 for (int j = 0; j < 4; j++)
-                  *reinterpret_cast<uint4*>(vo + at + ((((cg & 1) * 4 + j) ^ (R & 7)) << 4)) =
+                  *reinterpret_cast<uint4*>(dst + at0 + gi * 4096 + ((((cg & 1) * 4 + j) ^ (row & 7)) << 4)) =
                       make_uint4(hfma2(codes2<0>(xs[j]), me, cc), hfma2(codes2<1>(xs[j]), mo, cc),
                                  hfma2(codes2<2>(xs[j]), me, cc), hfma2(codes2<3>(xs[j]), mo, cc));
               }
             }
           } else {
-            // the rows' own keys: two threads a row
+            // the rows' own keys (or values): two threads a row
             wait(&op_empty[st], (op / NS & 1) ^ 1);
-            const int j = dt >> 1, half = dt & 1;
-            const bool in = a.k_new && j < w.rq.m;
+            const int j = dt >> 1, half = dt & 1, m = a.k_new ? w.rq.m : 0;
+            const bool in = j < m;
             const int64_t off = (int64_t)(w.rq.n0 + j) * a.kv_stride + h * D + half * (D / 2);
-            uint4 x[D / 16];
-            uint32_t big = 0;
+            // greatest magnitude of a row, as bits: at 0x7F800000 and above, a
+            // NaN or an infinity
+            auto row_max = [&](const uint16_t* src) {
+              uint32_t big = 0;
 #pragma unroll
-            for (int i = 0; i < D / 16; i++) {
-              x[i] = in ? *reinterpret_cast<const uint4*>(a.v_new + off + 8 * i) : make_uint4(0, 0, 0, 0);
-              const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+              for (int i = 0; i < D / 16; i++) {
+                const uint4 v = in ? *reinterpret_cast<const uint4*>(src + off + 8 * i) : make_uint4(0, 0, 0, 0);
+                const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-              for (int k = 0; k < 4; k++) big = max(big, max(xs[k] << 16 & 0x7FFF0000u, xs[k] & 0x7FFF0000u));
-            }
-            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            const bool odd = big >= 0x7F800000u;  // a NaN or an infinity
-            const uint32_t wm = __reduce_max_sync(0xffffffffu, odd ? 0u : big);
-            if (lane == 0) s_vmax[warp] = wm;
-            bar_sync(1 + dg * 10, 128);
-            E = min(max(E, tc_exponent(max(max(s_vmax[4 * dg], s_vmax[4 * dg + 1]), max(s_vmax[4 * dg + 2], s_vmax[4 * dg + 3])))), 120);
-            bar_sync(1 + dg * 10, 128);
-            const float down = odd ? 0.f : pow2i(-E);
-#pragma unroll
-            for (int i = 0; i < D / 16; i++) {
-              const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-              float f[8];
-#pragma unroll
-              for (int k = 0; k < 4; k++) {
-                f[2 * k] = odd ? 0.f : __uint_as_float(xs[k] << 16) * down;
-                f[2 * k + 1] = odd ? 0.f : __uint_as_float(xs[k] & 0xFFFF0000u) * down;
+                for (int k = 0; k < 4; k++) big = max(big, max(vs[k] << 16 & 0x7FFF0000u, vs[k] & 0x7FFF0000u));
               }
-              const int c = half * (D / 16) + i;  // 16-byte piece of the row
-              *reinterpret_cast<uint4*>(vo + (c >> 3) * 8192 + j * 128 + (((c & 7) ^ (j & 7)) << 4)) =
-                  make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
-            }
-            big = 0;
+              return max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            };
+            // even and odd dims times up and up4, as the nibbles' order has them
+            auto store = [&](const uint16_t* src, float up, float up4, bool zero) {
+              uint8_t* const d = dst + (is_k ? 0 : S::kOp) + j * 128;
 #pragma unroll
-            for (int i = 0; i < D / 16; i++) {
-              x[i] = in ? *reinterpret_cast<const uint4*>(a.k_new + off + 8 * i) : make_uint4(0, 0, 0, 0);
-              const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+              for (int i = 0; i < D / 16; i++) {
+                const uint4 v = in ? *reinterpret_cast<const uint4*>(src + off + 8 * i) : make_uint4(0, 0, 0, 0);
+                const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+                float f[8];
 #pragma unroll
-              for (int k = 0; k < 4; k++) big = max(big, max(xs[k] << 16 & 0x7FFF0000u, xs[k] & 0x7FFF0000u));
-            }
-            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            const int e = min(max(10 - expo(big), -100), 100);  // the greatest below 2^11; odd dims 2^4 up
-            const float up = pow2i(e), up4 = pow2i(e + 4);
-#pragma unroll
-            for (int i = 0; i < D / 16; i++) {
-              const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-              float f[8];
-#pragma unroll
-              for (int k = 0; k < 4; k++) {
-                f[2 * k] = __uint_as_float(xs[k] << 16) * up;
-                f[2 * k + 1] = __uint_as_float(xs[k] & 0xFFFF0000u) * up4;
+                for (int k = 0; k < 4; k++) {
+                  f[2 * k] = zero ? 0.f : __uint_as_float(vs[k] << 16) * up;
+                  f[2 * k + 1] = zero ? 0.f : __uint_as_float(vs[k] & 0xFFFF0000u) * up4;
+                }
+                const int c = half * (D / 16) + i;  // 16-byte piece of the row
+                *reinterpret_cast<uint4*>(d + (c >> 3) * 8192 + (((c & 7) ^ (j & 7)) << 4)) =
+                    make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
               }
-              const int c = half * (D / 16) + i;
-              *reinterpret_cast<uint4*>(ko + (c >> 3) * 8192 + j * 128 + (((c & 7) ^ (j & 7)) << 4)) =
-                  make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
+            };
+            if (is_k) {
+              const bool odd = a.k_new && row_max(a.v_new) >= 0x7F800000u;
+              const int e = min(max(10 - expo(a.k_new ? row_max(a.k_new) : 0), -100), 100);  // the greatest below 2^11; odd dims 2^4 up
+              store(a.k_new, pow2i(e), pow2i(e + 4), false);
+              if (half == 0) {
+                float* const p = reinterpret_cast<float*>(s_sc + st * 64) + (j >> 1) * 4 + (j & 1);
+                p[0] = odd ? __int_as_float(0x7FC00000) : 0.f;  // rows that see such a value are NaN
+                p[2] = pow2i(-24 - e);
+                if (BIAS && in) s_pos[st * 64 + j] = a.row_pos ? a.row_pos[w.rq.n0 + j] : w.rq.ctx + j;
+              }
+            } else {
+              const uint32_t big = a.k_new ? row_max(a.v_new) : 0;
+              const bool odd = big >= 0x7F800000u;
+              const uint32_t wm = __reduce_max_sync(0xffffffffu, odd ? 0u : big);
+              if (lane == 0) s_vmax[dw] = wm;
+              bar_sync(1, 128);
+              E = min(max(E, tc_exponent(max(max(s_vmax[0], s_vmax[1]), max(s_vmax[2], s_vmax[3])))), 120);
+              bar_sync(1, 128);
+              store(a.v_new, pow2i(-E), pow2i(-E), odd);
+              if (dt == 0)
+                s_info[st] = make_int4(m, m >= 32 ? -1 : (1 << m) - 1, m >= 64 ? -1 : m > 32 ? (1 << (m - 32)) - 1 : 0, E * 2 + 1);
             }
-            if (half == 0) {
-              reinterpret_cast<float*>(s_sc + st * 64)[(j >> 1) * 4 + (j & 1)] = odd ? __int_as_float(0x7FC00000) : 0.f;
-              reinterpret_cast<float*>(s_sc + st * 64)[(j >> 1) * 4 + 2 + (j & 1)] = pow2i(-24 - e);
-              if (BIAS && in) s_pos[st * 64 + j] = a.row_pos ? a.row_pos[w.rq.n0 + j] : w.rq.ctx + j;
-            }
-            const int m = a.k_new ? w.rq.m : 0;
-            if (dt == 0)
-              s_info[st] = make_int4(m, m >= 32 ? -1 : (1 << m) - 1, m >= 64 ? -1 : m > 32 ? (1 << (m - 32)) - 1 : 0, E * 2 + 1);
           }
           fence_async_smem();
           __syncwarp();
@@ -736,7 +786,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
       const int idx = (warp & 3) * 32 + lane;                                // TMEM lane
       const uint32_t tb = tm + t * 256 + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
       const float scale = BIAS ? 1.f : a.s.scale * kLog2e;
-      uint32_t op0 = 0, nsc = 0, par = 0;  // units done; parity of either s_full
+      uint32_t op0 = 0, par = 0;  // par: parity of the units done in either buffer
       do {
         const int h = w.head(), rc = w.s - h * w.rq.nc, n = w.ub - w.ua;
         const TcRowsOf<WIDE> rw(a.G * w.rq.m, w.rq.nc, rc);
@@ -758,11 +808,13 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
           x.E = 0;
           x.any = false;
           const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(w.rq.n0 + node) * a.q_stride + hq * D);
+          uint4 v[D / 8];
+#pragma unroll
+          for (int i = 0; i < D / 8; i++) v[i] = ok ? src[i] : make_uint4(0, 0, 0, 0);
           float qs = 0.f, big = 0.f;
-#pragma unroll 4
+#pragma unroll
           for (int i = 0; i < D / 8; i++) {
-            const uint4 v = ok ? src[i] : make_uint4(0, 0, 0, 0);
-            const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t vs[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
             for (int k = 0; k < 4; k++) {
               const float f0 = __uint_as_float(vs[k] << 16), f1 = __uint_as_float(vs[k] & 0xFFFF0000u);
@@ -776,10 +828,9 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
           x.fac = pow2i(24 - e) * scale;
           if (WIDE || t == 0) {
             uint8_t* const qt = sm + S::off_q + (WIDE ? t : 0) * S::kQ + idx * 128;
-#pragma unroll 4
+#pragma unroll
             for (int c = 0; c < D / 8; c++) {
-              const uint4 v = ok ? src[c] : make_uint4(0, 0, 0, 0);
-              const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+              const uint32_t vs[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
               float f[8];
 #pragma unroll
               for (int k = 0; k < 4; k++) {
@@ -797,15 +848,16 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
 
         {
           auto run = [&](auto nc) {
-            tc_softmax<D, BIAS, WIDE, decltype(nc)::value>(a, x, tb, WIDE ? 0 : t, n, op0, nsc, par, &s_full[2 * t], op_full, &p_full[2 * t],
-                                                           &o_full[t], s_sc, s_pos, s_info, &s_abort);
+            tc_softmax<D, BIAS, WIDE, decltype(nc)::value>(a, x, tb, WIDE ? 0 : t, n, op0, par, &s_full[2 * t], op_full, &p_full[2 * t],
+                                                           &o_full[2 * t], s_sc, s_pos, s_info, &s_abort);
           };
-          if (rw.copies == 1) run(std::integral_constant<int, 64>());
+          if (WIDE || rw.copies == 1) run(std::integral_constant<int, 64>());
           else if (rw.copies == 2) run(std::integral_constant<int, 32>());
           else run(std::integral_constant<int, 16>());
         }
         if (x.any) {
-          wait(&o_full[t], nsc - 1);
+          // the last two products may be under way
+          for (int b = 0; b < 2; b++) wait(&o_full[2 * t + b], (par >> b) ^ 1);
           tc_fence_after();
         }
         // Add up the copies, 32 dims at a time, and write the rows: the outputs
@@ -822,65 +874,81 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
         const int nsub = WIDE ? 1 : 2 * rw.copies;
         float f;  // of this thread's O: its weight in the row's sum
         {
-          const int ridx = idx % span;
-          float M = -INFINITY;
+          const int ridx = idx % span, row = ridx + (WIDE && t ? rw.split : 0);
+          float M = -INFINITY, L = 0.f;
           if (ridx < rw.of(t)) {
-            const int row = ridx + (WIDE && t ? rw.split : 0);
-            for (int j = 0; j < nsub; j++) M = fmaxf(M, s_ml[lane_of(row, j)].x);
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+              if (j < nsub) M = fmaxf(M, s_ml[lane_of(row, j)].x);
           }
-          f = x.any ? ex2(x.m - (M == -INFINITY ? 0.f : M)) * pow2i(x.E) : 0.f;
+          const float Ms = M == -INFINITY ? 0.f : M;
+          f = x.any ? ex2(x.m - Ms) * pow2i(x.E) : 0.f;
+          if (ridx < rw.of(t) && (WIDE || idx + t * 128 == row)) {  // one thread a row
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+              if (j < nsub) {
+                const float2 ml = s_ml[lane_of(row, j)];
+                L = fmaf(ex2(ml.x - Ms), ml.y, L);
+              }
+            if (whole) {
+              if (a.lse) {
+                const int rho = rw.base + row, gq = rho / w.rq.m;
+                a.lse[(int64_t)(w.rq.n0 + rho - gq * w.rq.m) * a.hq + h * a.G + gq] =
+                    L == 0.f ? -INFINITY : (M - 5.f + log2f(L)) * (1.f / kLog2e);
+              }
+            } else {
+              __stcg(reinterpret_cast<float2*>(part + kt::kRows * D) + row, make_float2(M - 5.f, L));
+            }
+            s_inv[row] = L == 0.f ? 0.f : 1.f / L;
+          }
         }
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           if (x.live) {
             float* dst = s_x + (t * 128 + idx) * S::kX;
+            float o[32];
+            if (x.any) tmem_ld(tb + 128 + c, o);
 #pragma unroll
-            for (int k = 0; k < 32; k += 16) {
-              float o[16];
-              if (x.any) tmem_ld(tb + 128 + c + k, o);
+            for (int e = 0; e < 32; e++) o[e] = x.any ? o[e] * f : 0.f;
 #pragma unroll
-              for (int e = 0; e < 16; e++) o[e] = x.any ? o[e] * f : 0.f;
-#pragma unroll
-              for (int e = 0; e < 16; e += 8) {  // columns hold dims 0 4 1 5 2 6 3 7 of each eight
-                *reinterpret_cast<float4*>(dst + k + e) = make_float4(o[e], o[e + 2], o[e + 4], o[e + 6]);
-                *reinterpret_cast<float4*>(dst + k + e + 4) = make_float4(o[e + 1], o[e + 3], o[e + 5], o[e + 7]);
-              }
+            for (int e = 0; e < 32; e += 8) {  // columns hold dims 0 4 1 5 2 6 3 7 of each eight
+              *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 2], o[e + 4], o[e + 6]);
+              *reinterpret_cast<float4*>(dst + e + 4) = make_float4(o[e + 1], o[e + 3], o[e + 5], o[e + 7]);
             }
           }
           bar_sync(2, kt::kSoftThreads);
           for (int i = st256; i < rw.rows * 8; i += kt::kSoftThreads) {
-            const int row = i >> 3, x4 = i & 7;
-            const int d = c + x4 * 4;
-            float M = -INFINITY;
-            for (int j = 0; j < nsub; j++) M = fmaxf(M, s_ml[lane_of(row, j)].x);
-            const float Ms = M == -INFINITY ? 0.f : M;
-            float L = 0.f;
+            const int row = i >> 3, x4 = i & 7, d = c + x4 * 4;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int j = 0; j < nsub; j++) {
-              const int at = lane_of(row, j);
-              L = fmaf(ex2(s_ml[at].x - Ms), s_ml[at].y, L);
-              const float4 v = *reinterpret_cast<const float4*>(s_x + at * S::kX + x4 * 4);
-              acc.x += v.x;
-              acc.y += v.y;
-              acc.z += v.z;
-              acc.w += v.w;
-            }
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+              if (j < nsub) {
+                const float4 v = *reinterpret_cast<const float4*>(s_x + lane_of(row, j) * S::kX + x4 * 4);
+                acc.x += v.x;
+                acc.y += v.y;
+                acc.z += v.z;
+                acc.w += v.w;
+              }
             if (whole) {
-              const float inv = L == 0.f ? 0.f : 1.f / L;
+              const float inv = s_inv[row];
               const int rho = rw.base + row, gq = rho / w.rq.m;
               const int64_t at = (int64_t)(w.rq.n0 + rho - gq * w.rq.m) * a.hq + h * a.G + gq;
               *reinterpret_cast<uint2*>(a.out + at * D + d) =
                   make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-              if (d == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M - 5.f + log2f(L)) * (1.f / kLog2e);
             } else {
               __stcg(reinterpret_cast<float4*>(part + row * D + d), acc);
-              if (d == 0) __stcg(reinterpret_cast<float2*>(part + kt::kRows * D) + row, make_float2(M - 5.f, L));
             }
           }
           bar_sync(2, kt::kSoftThreads);
         }
         tc_fence_before();
-        if (!whole && st256 == 0) {
+        if (a.joins) {
+          if (st256 == 0 && w.ua == 0) {
+            const int last = sh.cta_of(w.seg + w.rq.nu - 1);
+            a.joins[((int64_t)w.r * a.c.hkv + h) * kt::kJoins + rc] =
+                make_int4(blockIdx.x, whole ? 0 : last - (int)blockIdx.x + 1, slot, 0);
+          }
+        } else if (!whole && st256 == 0) {
           // is this the last of the segment's CTAs?  Acted on at this CTA's end.
           Kv4Join jn{w.seg, 0, sh.cta_of(w.seg), w.rq.n0, w.rq.m, h, rc};
           jn.n = sh.cta_of(w.seg + w.rq.nu - 1) - jn.c0 + 1;
@@ -905,24 +973,37 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   }
 }
 
-size_t kv4_tc_workspace(int head_dim) { return (size_t)2 * num_sms() * kt::kRows * (head_dim + 2) * sizeof(float); }
+// [joins of each (request, kv head)] [2 grid parts]
+static size_t joins_bytes(int R, int hkv) { return ((size_t)R * hkv * kt::kJoins * sizeof(int4) + 255) / 256 * 256; }
+size_t kv4_tc_workspace(int R, int hkv, int head_dim) {
+  return joins_bytes(R, hkv) + (size_t)2 * num_sms() * kt::kRows * (head_dim + 2) * sizeof(float);
+}
 
 template <int D, bool WIDE>
-static int launch_tc(const Kv4AttnArgs& a, int64_t units, bool bias, cudaStream_t st) {
+static int launch_tc(Kv4AttnArgs a, int rows, int64_t segs, int64_t units, bool bias, cudaStream_t st) {
   constexpr int smem = TcShape<D, WIDE>::smem;
   static const cudaError_t set[2] = {
       cudaFuncSetAttribute(k_kv4_attn_tc<D, false, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
       cudaFuncSetAttribute(k_kv4_attn_tc<D, true, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)};
   SD_CK(set[bias]);
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(num_sms(), units));
+  // many parts a segment: a kernel of its own joins them
+  const bool later = grid >= 3 * segs;
+  int4* joins = reinterpret_cast<int4*>(a.part);
+  a.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.part) + joins_bytes(a.R, a.c.hkv));
+  a.joins = later ? joins : nullptr;
   (bias ? k_kv4_attn_tc<D, true, WIDE> : k_kv4_attn_tc<D, false, WIDE>)<<<(unsigned)grid, kt::kThreads, smem, st>>>(a);
   SD_CK(cudaGetLastError());
+  if (later)
+    SD_CK(launch(k_kv4_join<D, WIDE>, dim3((unsigned)(((int64_t)rows * a.hq + 7) / 8)), dim3(256), 0, st, true, a, rows));
   return SD_OK;
 }
 
-int kv4_launch_attn_tc(const Kv4AttnArgs& a, int head_dim, int rows, int64_t units, bool bias, cudaStream_t st) {
-  if (head_dim == 128) return rows > 128 ? launch_tc<128, true>(a, units, bias, st) : launch_tc<128, false>(a, units, bias, st);
-  return rows > 128 ? launch_tc<64, true>(a, units, bias, st) : launch_tc<64, false>(a, units, bias, st);
+int kv4_launch_attn_tc(const Kv4AttnArgs& a, int head_dim, int rows, int most, int64_t segs, int64_t units, bool bias,
+                       cudaStream_t st) {
+  if (head_dim == 128)
+    return most > 128 ? launch_tc<128, true>(a, rows, segs, units, bias, st) : launch_tc<128, false>(a, rows, segs, units, bias, st);
+  return most > 128 ? launch_tc<64, true>(a, rows, segs, units, bias, st) : launch_tc<64, false>(a, rows, segs, units, bias, st);
 }
 
 }  // namespace sdv

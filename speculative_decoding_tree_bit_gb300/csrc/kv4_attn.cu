@@ -986,7 +986,7 @@ static int launch_observe(const Kv4ObserveArgs& b, int64_t units, bool bias, cud
 
 // Rows (query heads x nodes) that one kv head may have on the warp kernel;
 // more take the tensor cores.
-constexpr int kWarpRows = 16;
+constexpr int kWarpRows = 64;
 
 template <int D>
 static int launch_attn(const Kv4AttnArgs& a, int total, int rows, int64_t segs, int64_t units, bool bias, cudaStream_t st) {
@@ -1030,7 +1030,7 @@ extern "C" size_t sd_kv4_attn_workspace(int32_t R, int32_t rows, int32_t n_q_hea
   if (R < 1 || rows < 0 || n_kv_heads < 1 || n_q_heads < n_kv_heads || n_q_heads % n_kv_heads ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  const size_t warp = (size_t)4 * num_sms() * kWarpRows * (head_dim + 2) * sizeof(float);
+  const size_t warp = (size_t)4 * num_sms() * 32 * (head_dim + 2) * sizeof(float);
   const int most = std::min(rows, 64) * (n_q_heads / n_kv_heads);
   return kTicketBytes + (most > kWarpRows ? std::max(warp, kv4_tc_workspace(R, n_kv_heads, head_dim)) : warp);
 }

@@ -13,6 +13,17 @@ namespace sdv {
 
 constexpr int kHeads = 4;
 
+__device__ __forceinline__ uint32_t bf2_min(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf2_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // N consecutive 16-bit values of a row as 32-bit words.
 template <int N>
 __device__ __forceinline__ void load_row(const uint16_t* p, uint32_t (&w)[N / 2]) {
@@ -63,47 +74,58 @@ __global__ void __launch_bounds__(256) k_kv4_append(Kv4View c, const uint16_t* _
 #pragma unroll
   for (int i = 0; i < kHeads; i++) {
     if (i >= nh) break;
-    float f[kV], lo = INFINITY, hi = -INFINITY;
-    bool nan = false;
+    // least and greatest, bf16 pairs at a time; a NaN stays one
+    uint32_t lo2 = raw[i][0], hi2 = raw[i][0];
 #pragma unroll
-    for (int j = 0; j < kV; j++) {
-      f[j] = __uint_as_float(j & 1 ? raw[i][j >> 1] & 0xFFFF0000u : raw[i][j >> 1] << 16);
-      lo = fminf(lo, f[j]);
-      hi = fmaxf(hi, f[j]);
-      nan |= f[j] != f[j];  // fminf and fmaxf pass NaN over
-    }
+    for (int j = 1; j < kV / 2; j++) lo2 = bf2_min(lo2, raw[i][j]), hi2 = bf2_max(hi2, raw[i][j]);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      lo2 = bf2_min(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
+      hi2 = bf2_max(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
     }
-    const uint32_t bad = __ballot_sync(0xffffffffu, nan) >> (16 * half) & 0xFFFFu;
-    const float range = hi - lo;
-    float sc = rbf(__fdiv_rn(range, 15.f)), md = rbf(fmaf(8.f, sc, lo));
-    if (bad || !(range <= 3.4028234e38f)) sc = md = __int_as_float(0x7FC00000);  // not finite: the row is held as NaN
-    // A code is the nearest step, halves to even.  The product with 1 / s is
-    // within 2^-19 of the quotient (at most 8 or so); where that leaves a half
-    // in doubt anywhere in the warp, the quotients themselves decide.
-    const float inv = sc > 1e-30f && sc < 1e30f ? __fdiv_rn(1.f, sc) : 0.f;
-    float st[kV];
-    bool doubt = sc > 0.f && inv == 0.f;
+    lo2 = bf2_min(lo2, lo2 >> 16 | lo2 << 16);
+    hi2 = bf2_max(hi2, hi2 >> 16 | hi2 << 16);
+    const float lo = __uint_as_float(lo2 << 16), range = __uint_as_float(hi2 << 16) - lo;
+    // s: the product with 1 / 15 is within two units of the quotient; the
+    // division decides where that could turn the rounding to bf16
+    float sq = range * (1.f / 15.f);
+    const uint32_t tail = (__float_as_uint(sq) & 0xFFFFu) - 0x7FFCu;
+    if (__any_sync(0xffffffffu, tail <= 8u || !(sq > 1e-30f))) sq = __fdiv_rn(range, 15.f);
+    float sc = rbf(sq), md = rbf(fmaf(8.f, sc, lo));
+    if (!(range <= 3.4028234e38f)) sc = md = __int_as_float(0x7FC00000);  // not finite: the row is held as NaN
+    // A code is the nearest step, halves to even: the low bits of (x - m) / s +
+    // 8 + 1.5 2^23, clamped.  The product with the approximate 1 / s is within 2^-19
+    // of the quotient (at most 8 or so); where that leaves a half in doubt
+    // anywhere in the warp, the remainder x - m - n s, which is exact, decides.
+    constexpr float kBase = 12582912.f;  // 1.5 2^23: integers to a unit
+    const bool fine = sc > 1e-30f && sc < 1e30f;
+    const float inv = fine ? __fdividef(1.f, sc) : 0.f;
+    float far = 0.f, st[kV];
 #pragma unroll
     for (int j = 0; j < kV; j++) {
-      const float q = (f[j] - md) * inv;
-      st[j] = rintf(q);
-      doubt |= fabsf(fabsf(q - st[j]) - 0.5f) < 4e-6f;
+      const float d = __uint_as_float(j & 1 ? raw[i][j >> 1] & 0xFFFF0000u : raw[i][j >> 1] << 16) - md;
+      st[j] = fmaf(d, inv, kBase + 8.f);
+      far = fmaxf(far, fabsf(fmaf(d, inv, (kBase + 8.f) - st[j])));
     }
-    if (__any_sync(0xffffffffu, doubt)) {
+    if (__any_sync(0xffffffffu, far > 0.5f - 4e-6f || !fine)) {
+      const float h = 0.5f * sc;
 #pragma unroll
-      for (int j = 0; j < kV; j++) st[j] = sc > 0.f ? rintf(__fdiv_rn(f[j] - md, sc)) : 0.f;
+      for (int j = 0; j < kV; j++) {
+        const float d = __uint_as_float(j & 1 ? raw[i][j >> 1] & 0xFFFF0000u : raw[i][j >> 1] << 16) - md;
+        if (fine) {
+          const float r = fmaf(-(st[j] - (kBase + 8.f)), sc, d);
+          const bool odd = __float_as_uint(st[j]) & 1u;
+          if (r > h || (r == h && odd)) st[j] += 1.f;
+          else if (r < -h || (r == -h && odd)) st[j] -= 1.f;
+        } else {  // NaN and s = 0 give code 8
+          st[j] = kBase + 8.f + (sc > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(d, sc)), -8.f), 7.f) : 0.f);
+        }
+      }
     }
     uint32_t word = 0;
 #pragma unroll
-    for (int j = 0; j < kV; j++) {
-      // NaN and s = 0 give code 8
-      const float q = sc > 0.f ? st[j] : 0.f;
-      word |= (uint32_t)((int)fminf(fmaxf(q, -8.f), 7.f) + 8) << (4 * j);
-    }
+    for (int j = 0; j < kV; j++)
+      word += (__float_as_uint(fminf(fmaxf(st[j], kBase), kBase + 15.f)) - 0x4B400000u) << (4 * j);
     uint8_t* const rh = rec + (int64_t)i * c.gpp * kv4_rec(D);
     uint8_t* codes = rh + half * kv4_half(D) + (t & 31) * (D / 2);
     const int b = half ? kv4_vbyte<D>(t, l * (kV / 2)) : l * (kV / 2);

@@ -184,18 +184,16 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
     }
     __syncthreads();
     float o[NT][KK][4];
-    float mx[NT][2], l[NT][2], mv[NT][2], fac[NT][2], qs[NT][2];
+    float mx[NT][2];
+    uint64_t l[NT], mv[NT], fac[NT], qs[NT];  // of a lane's two rows
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
 #pragma unroll
       for (int t = 0; t < KK; t++) o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; e++) {
-        mx[nt][e] = -INFINITY;
-        l[nt][e] = mv[nt][e] = 0.f;
-        fac[nt][e] = s_fac[nt * 8 + 2 * q + e];
-        qs[nt][e] = s_qs[nt * 8 + 2 * q + e];
-      }
+      mx[nt][0] = mx[nt][1] = -INFINITY;
+      l[nt] = mv[nt] = 0;
+      fac[nt] = f2pack(s_fac[nt * 8 + 2 * q], s_fac[nt * 8 + 2 * q + 1]);
+      qs[nt] = f2pack(s_qs[nt * 8 + 2 * q], s_qs[nt * 8 + 2 * q + 1]);
     }
     // values' weights are p s vup: vup 2^13 over the power of two at or above
     // the greatest s so far (bits vtop), which leaves o short by vup 2^-9
@@ -221,9 +219,10 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
           const float mn = fmaxf(mx[nt][e], t);
           al[e] = mn == -INFINITY ? 1.f : ex2(mx[nt][e] - mn);
           mx[nt][e] = mn;
-          l[nt][e] *= al[e];
-          mv[nt][e] *= al[e];
         }
+        const uint64_t al2 = f2pack(al[0], al[1]);
+        l[nt] = f2mul(l[nt], al2);
+        mv[nt] = f2mul(mv[nt], al2);
 #pragma unroll
         for (int t = 0; t < KK; t++) {
           o[nt][t][0] *= al[0];
@@ -285,13 +284,13 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
           for (int i = 0; i < 2; i++) {
+            float p[2];
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-              float& x = so[nt][2 * i + e];
-              const float p = ex2(x - (mx[nt][e] == -INFINITY ? 0.f : mx[nt][e]));
-              l[nt][e] += p;
-              x = p * wup;
+              p[e] = ex2(so[nt][2 * i + e] - (mx[nt][e] == -INFINITY ? 0.f : mx[nt][e]));
+              so[nt][2 * i + e] = p[e] * wup;
             }
+            l[nt] = f2add(l[nt], f2pack(p[0], p[1]));
             const float w0 = so[nt][2 * i], w1 = so[nt][2 * i + 1];
             const uint32_t hi = pack_bf16x2(w0, w1);
             const uint32_t lo = pack_bf16x2(w0 - __uint_as_float(hi << 16), w1 - __uint_as_float(hi & 0xFFFF0000u));
@@ -398,7 +397,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
       float vs[4], vm[4];
       int kp[4];
       float top[NT][2];
-      uint32_t vb = 0;
+      uint32_t vb = 0, nan = 0;
 #pragma unroll
       for (int nt = 0; nt < NT; nt++) top[nt][0] = top[nt][1] = -INFINITY;
 #pragma unroll
@@ -411,15 +410,15 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
         const float km = fmaf(-8.f, ks, __uint_as_float(kw & 0xFFFF0000u));
         vs[i] = in ? __uint_as_float(vw << 16) : 0.f;
         vm[i] = in ? __uint_as_float(vw & 0xFFFF0000u) : 0.f;
-        if (vs[i] == vs[i]) vb = max(vb, __float_as_uint(vs[i]));
+        // a value row held as NaN: 0 here, and the sum of whoever sees it NaN below
+        if (vs[i] != vs[i]) vs[i] = vm[i] = 0.f, nan |= 1u << i;
+        vb = max(vb, __float_as_uint(vs[i]));
         kp[i] = BIAS ? *reinterpret_cast<const int*>(st + kv4_rec(D) + kl * 4) : 0;
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-          for (int e = 0; e < 2; e++) {
-            float& x = sc[i >> 1][nt][2 * (i & 1) + e];
-            x = fmaf(ks, x * fac[nt][e], km * qs[nt][e]);
-          }
+        for (int nt = 0; nt < NT; nt++) {
+          float* x = sc[i >> 1][nt] + 2 * (i & 1);
+          f2unpack(f2fma(f2pack(ks, ks), f2mul(f2pack(x[0], x[1]), fac[nt]), f2mul(f2pack(km, km), qs[nt])), x[0], x[1]);
+        }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; nt++)
@@ -452,27 +451,32 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
 #pragma unroll
             for (int e = 0; e < 4; e++) o[nt][t][e] *= ratio;
       }
+      if (__any_sync(0xffffffffu, nan != 0)) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            const float* x = sc[i >> 1][nt] + 2 * (i & 1);
+            const float bad = __int_as_float(0x7FC00000);
+            if (nan >> i & 1)
+              l[nt] = f2add(l[nt], f2pack(x[0] == -INFINITY ? 0.f : bad, x[1] == -INFINITY ? 0.f : bad));
+          }
+      }
       // weights, transposed into B fragments [16-key step]
       uint32_t pf[NT][2][2];
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const float vsu = vs[i] * vup;
+      for (int nt = 0; nt < NT; nt++) {
+        const uint64_t ms = f2pack(mx[nt][0] == -INFINITY ? 0.f : -mx[nt][0], mx[nt][1] == -INFINITY ? 0.f : -mx[nt][1]);
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-          float w[2];
-#pragma unroll
-          for (int e = 0; e < 2; e++) {
-            const float x = sc[i >> 1][nt][2 * (i & 1) + e];
-            const float p = ex2(x - (mx[nt][e] == -INFINITY ? 0.f : mx[nt][e]));
-            l[nt][e] += p;
-            w[e] = p * vsu;
-            if (BIAS) {  // a hidden key's scale may be NaN
-              w[e] = x == -INFINITY ? 0.f : w[e];
-              mv[nt][e] += x == -INFINITY ? 0.f : p * vm[i];
-            } else {
-              mv[nt][e] = fmaf(p, vm[i], mv[nt][e]);
-            }
-          }
+        for (int i = 0; i < 4; i++) {
+          const float* x = sc[i >> 1][nt] + 2 * (i & 1);
+          const float vsu = vs[i] * vup;
+          float p[2], w[2];
+          f2unpack(f2add(f2pack(x[0], x[1]), ms), p[0], p[1]);
+          const uint64_t pp = f2pack(ex2(p[0]), ex2(p[1]));
+          l[nt] = f2add(l[nt], pp);
+          mv[nt] = f2fma(pp, f2pack(vm[i], vm[i]), mv[nt]);
+          f2unpack(f2mul(pp, f2pack(vsu, vsu)), w[0], w[1]);
           pf[nt][i >> 1][i & 1] = transpose8(pack_f16x2(w[0], w[1]));
         }
       }
@@ -546,22 +550,23 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
       for (int e = 0; e < 2; e++) {
+        float le = __uint_as_float((uint32_t)(l[nt] >> (32 * e))), mve = __uint_as_float((uint32_t)(mv[nt] >> (32 * e)));
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
-          l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
-          mv[nt][e] += __shfl_xor_sync(0xffffffffu, mv[nt][e], x);
+          le += __shfl_xor_sync(0xffffffffu, le, x);
+          mve += __shfl_xor_sync(0xffffffffu, mve, x);
         }
         const int row = nt * 8 + 2 * q + e;
         if (g == 0) {
           s_m[warp * RT + row] = mx[nt][e];
-          s_l[warp * RT + row] = l[nt][e];
+          s_l[warp * RT + row] = le;
         }
         // float pairs [dims 2t, 2t + 1 of lane group g]: 8 t + g, rows 4 banks
         // of pairs apart for the lanes that write together
         float2* dst = reinterpret_cast<float2*>(s_o) + (warp * RT + row) * S::kPairs + g;
 #pragma unroll
         for (int t = 0; t < KK; t++)
-          dst[8 * t] = make_float2(fmaf(o[nt][t][e], down, mv[nt][e]), fmaf(o[nt][t][2 + e], down, mv[nt][e]));
+          dst[8 * t] = make_float2(fmaf(o[nt][t][e], down, mve), fmaf(o[nt][t][2 + e], down, mve));
       }
     __syncthreads();
     float* part = a.part + (int64_t)slot * (RT * (D + 2));  // [RT][D/2] pairs, then [RT] (max, sum)
@@ -907,7 +912,7 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
           }
           issue(x + NS * W, k + NS - 1, stage);
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t sum2[4] = {0, 0, 0, 0};  // of either row of a pair
         for (int nt = 0; nt < tiles; nt++) {
           float sc[2][2][4];  // [16-key tile][chain]
 #pragma unroll
@@ -924,19 +929,36 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
               mma_f16(sc[i][1], codes2<2>(wa), codes2<2>(wb), codes2<3>(wa), codes2<3>(wb), bq.z, bq.w);
             }
           }
+          const int row = nt * 8 + 2 * q;
+          const float4 r0 = s_row[row], r1 = s_row[row + 1];
+          const uint64_t fac = f2pack(r0.x, r1.x), qs = f2pack(r0.y, r1.y), lse = f2pack(-r0.z, -r1.z), rw = f2pack(r0.w, r1.w);
+          float v[2][4];
 #pragma unroll
-          for (int e = 0; e < 2; e++) {
-            const int row = nt * 8 + 2 * q + e;
-            const float4 rw = s_row[row];
-            const float2 bi = BIAS ? s_bias[row] : make_float2(0.f, 0.f);
-            float v[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-              v[i] = fmaf(ks[i], (sc[i >> 1][0][2 * (i & 1) + e] + sc[i >> 1][1][2 * (i & 1) + e]) * rw.x, km[i] * rw.y);
-            if (BIAS) kv4_scores(a.s, v, bi.x, __float_as_int(bi.y), start, [&](int i) { return kp[i]; });
-#pragma unroll
-            for (int i = 0; i < 4; i++) sum[i] = fmaf(rw.w, ex2(v[i] - rw.z), sum[i]);
+          for (int i = 0; i < 4; i++) {
+            const float *x = sc[i >> 1][0] + 2 * (i & 1), *y = sc[i >> 1][1] + 2 * (i & 1);
+            f2unpack(f2fma(f2pack(ks[i], ks[i]), f2mul(f2add(f2pack(x[0], x[1]), f2pack(y[0], y[1])), fac),
+                           f2mul(f2pack(km[i], km[i]), qs)), v[0][i], v[1][i]);
           }
+          if (BIAS) {
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              const float2 bi = s_bias[row + e];
+              kv4_scores(a.s, v[e], bi.x, __float_as_int(bi.y), start, [&](int i) { return kp[i]; });
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            float p[2];
+            f2unpack(f2add(f2pack(v[0][i], v[1][i]), lse), p[0], p[1]);
+            sum2[i] = f2fma(rw, f2pack(ex2(p[0]), ex2(p[1])), sum2[i]);
+          }
+        }
+        float sum[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          float lo, hi;
+          f2unpack(sum2[i], lo, hi);
+          sum[i] = lo + hi;
         }
         float mine = 0.f;
 #pragma unroll

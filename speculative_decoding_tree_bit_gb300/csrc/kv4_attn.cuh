@@ -31,33 +31,72 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// cap tanh(x / cap).  Scores far below the cap, nearly all of them, by tanh's
-// Taylor series to x^9 (off by 1.6e-8 at 0.3, where it ends); the others as 1 -
-// 2 / (1 + e^2x), off by 1.2e-7 of the cap.
-__device__ __forceinline__ float capped(float t, float cap) {
-  const float x = __fdividef(t, cap), u = x * x;
-  float p = fmaf(u, 62.f / 2835.f, -17.f / 315.f);
-  p = fmaf(p, u, 2.f / 15.f);
-  p = fmaf(p, u, -1.f / 3.f);
-  p = fmaf(p * u, t, t);
-  const float y = fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2(2.f * kLog2e * x)), cap);
-  return u < 0.09f ? p : y;
+// Pairs of fp32 values: one instruction for two.
+__device__ __forceinline__ uint64_t f2pack(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
 }
-
-// Scores of N keys from q.k (natural units in, base 2 out): cap, slope, masks.
-// The options' branches are outside the loops over the keys, which so overlap.
-// pos(i): position of key i.
+__device__ __forceinline__ void f2unpack(uint64_t r, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+__device__ __forceinline__ uint64_t f2fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Scores of N keys in base 2 from q.k: scale, cap, slope, masks.  The options'
+// branches lie outside the loops over the keys, which so overlap.  cap tanh(x /
+// cap): by tanh's Taylor series to x^9 while every x of the warp is below 0.3
+// (off by 1.6e-8 there; scores far below the cap are the rule), else as 1 - 2 /
+// (1 + e^2x), off by 1.2e-7 of the cap.  pos(i): position of key i.  By whole warps.
 template <int N, typename Pos>
 __device__ __forceinline__ void kv4_scores(const Kv4Score& s, float (&t)[N], float slope, int q_pos, int start, Pos pos) {
-#pragma unroll
-  for (int i = 0; i < N; i++) t[i] *= s.scale;
   if (s.cap > 0.f) {
+    const float in = __fdividef(s.scale, s.cap), out = s.cap * kLog2e;
+    float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; i++) t[i] = capped(t[i], s.cap);
+    for (int i = 0; i < N; i++) {
+      t[i] *= in;
+      top = fmaxf(top, fabsf(t[i]));
+    }
+    if (!__any_sync(0xffffffffu, top >= 0.3f)) {
+#pragma unroll
+      for (int i = 0; i < N; i++) {
+        const float u = t[i] * t[i], z = t[i] * out;
+        float p = fmaf(u, 62.f / 2835.f, -17.f / 315.f);
+        p = fmaf(p, u, 2.f / 15.f);
+        p = fmaf(p, u, -1.f / 3.f);
+        t[i] = fmaf(p * u, z, z);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i++) {
+        const float u = t[i] * t[i], z = t[i] * out;
+        float p = fmaf(u, 62.f / 2835.f, -17.f / 315.f);
+        p = fmaf(p, u, 2.f / 15.f);
+        p = fmaf(p, u, -1.f / 3.f);
+        const float y = fmaf(-2.f * out, __fdividef(1.f, 1.f + ex2(2.f * kLog2e * t[i])), out);
+        t[i] = u < 0.09f ? fmaf(p * u, z, z) : y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i++) t[i] *= s.scale * kLog2e;
   }
   if (s.slopes) {
 #pragma unroll
-    for (int i = 0; i < N; i++) t[i] = fmaf(slope, (float)(pos(i) - q_pos), t[i]);
+    for (int i = 0; i < N; i++) t[i] = fmaf(slope * kLog2e, (float)(pos(i) - q_pos), t[i]);
   }
   if (s.window > 0 || s.start) {
     const int64_t since = (int64_t)q_pos - (s.window > 0 ? s.window : INT32_MAX);
@@ -66,8 +105,6 @@ __device__ __forceinline__ void kv4_scores(const Kv4Score& s, float (&t)[N], flo
     for (int i = 0; i < N; i++)
       if (pos(i) < first) t[i] = -INFINITY;
   }
-#pragma unroll
-  for (int i = 0; i < N; i++) t[i] *= kLog2e;
 }
 
 // A bounded wait that looks at the clock and at the other warps' abort flag

@@ -7,7 +7,7 @@ namespace sdv {
 //
 // One warp stores a row's keys and values of kHeads kv heads: a half warp the
 // key, the other the value, D / 16 values a lane (one or half a 32-bit word of
-// codes); the heads' rows are all in flight before the first is used.  A row's
+// codes); the next head's row is on its way while one is worked on.  A row's
 // least and greatest value come from four shuffles.  Bound: bytes (4 D in, D +
 // 12 out per row and head).
 
@@ -21,6 +21,17 @@ __device__ __forceinline__ uint32_t bf2_min(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t bf2_max(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t bf2_sub(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
 
@@ -50,10 +61,9 @@ __global__ void __launch_bounds__(256) k_kv4_append(Kv4View c, const uint16_t* _
   const int h0 = blockIdx.y * kHeads, nh = min(kHeads, c.hkv - h0);
   const int s = src ? src[e] : e;
   const bool s_ok = s >= 0 && s < n_src;
-  uint32_t raw[kHeads][kV / 2];
-#pragma unroll
-  for (int i = 0; i < kHeads; i++)
-    if (s_ok && i < nh) load_row<kV>((half ? v : k) + (int64_t)s * row_stride + (h0 + i) * D + l * kV, raw[i]);
+  const uint16_t* x = (half ? v : k) + (s_ok ? (int64_t)s * row_stride : 0) + h0 * D + l * kV;
+  uint32_t next[kV / 2];
+  load_row<kV>(x, next);
   const int p = pos ? pos[e] : 0;
   const int r = request_of(cu, R, e);
   const int i0 = e - cu[r];
@@ -71,13 +81,16 @@ __global__ void __launch_bounds__(256) k_kv4_append(Kv4View c, const uint16_t* _
     if (lane == 0) set_status(status, SD_ERR_CAPACITY);
     return;
   }
+#pragma unroll 1
+  for (int i = 0; i < nh; i++) {
+    uint32_t raw[kV / 2];
 #pragma unroll
-  for (int i = 0; i < kHeads; i++) {
-    if (i >= nh) break;
+    for (int j = 0; j < kV / 2; j++) raw[j] = next[j];
+    if (i + 1 < nh) load_row<kV>(x + (i + 1) * D, next);
     // least and greatest, bf16 pairs at a time; a NaN stays one
-    uint32_t lo2 = raw[i][0], hi2 = raw[i][0];
+    uint32_t lo2 = raw[0], hi2 = raw[0];
 #pragma unroll
-    for (int j = 1; j < kV / 2; j++) lo2 = bf2_min(lo2, raw[i][j]), hi2 = bf2_max(hi2, raw[i][j]);
+    for (int j = 1; j < kV / 2; j++) lo2 = bf2_min(lo2, raw[j]), hi2 = bf2_max(hi2, raw[j]);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) {
       lo2 = bf2_min(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
@@ -103,7 +116,7 @@ __global__ void __launch_bounds__(256) k_kv4_append(Kv4View c, const uint16_t* _
     float far = 0.f, st[kV];
 #pragma unroll
     for (int j = 0; j < kV; j++) {
-      const float d = __uint_as_float(j & 1 ? raw[i][j >> 1] & 0xFFFF0000u : raw[i][j >> 1] << 16) - md;
+      const float d = __uint_as_float(j & 1 ? raw[j >> 1] & 0xFFFF0000u : raw[j >> 1] << 16) - md;
       st[j] = fmaf(d, inv, kBase + 8.f);
       far = fmaxf(far, fabsf(fmaf(d, inv, (kBase + 8.f) - st[j])));
     }
@@ -111,7 +124,7 @@ __global__ void __launch_bounds__(256) k_kv4_append(Kv4View c, const uint16_t* _
       const float h = 0.5f * sc;
 #pragma unroll
       for (int j = 0; j < kV; j++) {
-        const float d = __uint_as_float(j & 1 ? raw[i][j >> 1] & 0xFFFF0000u : raw[i][j >> 1] << 16) - md;
+        const float d = __uint_as_float(j & 1 ? raw[j >> 1] & 0xFFFF0000u : raw[j >> 1] << 16) - md;
         if (fine) {
           const float r = fmaf(-(st[j] - (kBase + 8.f)), sc, d);
           const bool odd = __float_as_uint(st[j]) & 1u;
@@ -184,12 +197,18 @@ __global__ void __launch_bounds__(256) k_kv4_read(Kv4View c, const int32_t* __re
 #pragma unroll
   for (int i = 0; i < kHeads; i++) {
     if (i >= nh) break;
-    const float sc = __uint_as_float(sm[i] << 16), md = __uint_as_float(sm[i] & 0xFFFF0000u);
-    uint32_t o[kV / 2];
+    // (code - 8) s + m in bf16 pairs, rounded once: 0x4300 | code is 128 + code,
+    // and code - 8 is exact.  Pair n of a word: nibbles n and n + 4
+    const uint32_t s2 = prmt(sm[i], 0, 0x1010), m2 = prmt(sm[i], 0, 0x3232);
+    uint32_t o[kV / 2], p[4];
+    const uint32_t wd = kV == 8 ? word[i] : (word[i] & 0xFFu) | (word[i] & 0xFF00u) << 8;
 #pragma unroll
-    for (int j = 0; j < kV / 2; j++) {
-      const int c0 = (int)(word[i] >> (8 * j) & 15) - 8, c1 = (int)(word[i] >> (8 * j + 4) & 15) - 8;
-      o[j] = pack_bf16x2(fmaf(sc, (float)c0, md), fmaf(sc, (float)c1, md));
+    for (int j = 0; j < kV / 2; j++) p[j] = bf2_fma(s2, bf2_sub((wd >> (4 * j) & 0x000F000Fu) | 0x43004300u, 0x43084308u), m2);
+    if constexpr (kV == 8) {
+      o[0] = prmt(p[0], p[1], 0x5410), o[1] = prmt(p[2], p[3], 0x5410);
+      o[2] = prmt(p[0], p[1], 0x7632), o[3] = prmt(p[2], p[3], 0x7632);
+    } else {
+      o[0] = prmt(p[0], p[1], 0x5410), o[1] = prmt(p[0], p[1], 0x7632);
     }
     uint16_t* dst = (half ? v_out : k_out) + ((int64_t)e * c.hkv + h0 + i) * D + l * kV;
     if constexpr (kV == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -304,20 +323,31 @@ __global__ void __launch_bounds__(kSelThreads) k_kv4_select(Kv4View s, Kv4View d
   uint32_t eq = __reduce_add_sync(0xffffffffu, n2);                         // of the least key, before this warp
   uint32_t o = __reduce_add_sync(0xffffffffu, n1) + min(eq, need);          // staying before this warp
   const uint32_t below = (1u << lane) - 1;
-  for (int t = t0 + lane; t - lane < t1; t += 32) {
-    const float wt = t < t1 ? w[t] : 0.f;
-    const int x = t < t1 ? kind(t, wt) : 0;
-    const uint32_t be = __ballot_sync(0xffffffffu, x == 2);
-    const bool stay = x == 1 || (x == 2 && eq + __popc(be & below) < need);
-    const uint32_t bs = __ballot_sync(0xffffffffu, stay);
-    const uint32_t at = o + __popc(bs & below);
-    if (stay && at < (uint32_t)budget) {
-      out[at] = t;
-      wd[at] = wt;
-      pd[at] = pos[t];
+  for (int t4 = t0 + lane; t4 - lane < t1; t4 += 128) {
+    float wt[4];
+    int ps[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const int t = min(t4 + 32 * k, ctx - 1);
+      wt[k] = w[t];
+      ps[k] = pos[t];
     }
-    eq += __popc(be);
-    o += __popc(bs);
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const int t = t4 + 32 * k;
+      const int x = t < t1 ? kind(t, wt[k]) : 0;
+      const uint32_t be = __ballot_sync(0xffffffffu, x == 2);
+      const bool stay = x == 1 || (x == 2 && eq + __popc(be & below) < need);
+      const uint32_t bs = __ballot_sync(0xffffffffu, stay);
+      const uint32_t at = o + __popc(bs & below);
+      if (stay && at < (uint32_t)budget) {
+        out[at] = t;
+        wd[at] = wt[k];
+        pd[at] = ps[k];
+      }
+      eq += __popc(be);
+      o += __popc(bs);
+    }
   }
 }
 

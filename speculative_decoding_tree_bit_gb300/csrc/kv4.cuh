@@ -46,6 +46,12 @@ __device__ __forceinline__ int kv4_vbyte(int t, int b) {
   return D == 128 ? b ^ ((t & 2) << 4) : b;
 }
 
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+
 // The request of row e, by the whole warp: a search 32 offsets at a time.
 __device__ __forceinline__ int request_of(const int32_t* __restrict__ cu, int R, int e) {
   const int lane = threadIdx.x & 31;

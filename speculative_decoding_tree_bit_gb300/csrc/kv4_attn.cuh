@@ -126,11 +126,6 @@ __device__ __forceinline__ bool kv4_wait(uint64_t* bar, uint32_t parity, volatil
   }
 }
 
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
 // 8x8 transpose of 16-bit values across the warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;

@@ -734,12 +734,15 @@ class KV4Cache:
         ws = self._ws.get(key)
         if ws is None:
             n = int(size(*args))
-            for k, (t, _, _) in self._ws.items():
+            for k, (_, _, _, t) in self._ws.items():
                 if k[0] == kind and t.numel() >= n:  # one buffer serves every call it is large enough for
                     break
             else:
                 t = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.device)
-            ws = self._ws[key] = (t, t.data_ptr(), t.numel())
+            view = t
+            if kind == "evict":
+                view = t[:n].view(torch.int32).view(*args)
+            ws = self._ws[key] = (view, t.data_ptr(), t.numel(), t)
         return ws
 
     def _at(self, at):
@@ -815,7 +818,7 @@ class KV4Cache:
             lse = torch.empty(n, hq, dtype=torch.float32, device=q.device)
         elif lse.dtype is not torch.float32 or lse.shape != (n, hq) or not lse.is_contiguous():
             raise ValueError("lse must be contiguous float32 [rows][n_q_heads]")
-        _, ws, ws_n = self._workspace("attn", self._lib.sd_kv4_attn_workspace, self.R, n, hq, self.n_kv_heads, D)
+        _, ws, ws_n, _ = self._workspace("attn", self._lib.sd_kv4_attn_workspace, self.R, n, hq, self.n_kv_heads, D)
         check(self._lib.sd_kv4_attn(self._ref, q.data_ptr(), qs, hq, rows.cu_ptr, rows.cu_host_ptr, self.R, kp, vp_, ks,
                                     _entries(anc, n, "anc", torch.int64), _entries(pos, n, "pos"),
                                     None if score is None else score.ref, max_ctx, out.data_ptr(), lse.data_ptr(), ws,
@@ -850,8 +853,7 @@ class KV4Cache:
         if dst is self or dst.R != self.R:
             raise ValueError("dst must be another cache of the same requests")
         budget = int(budget)
-        ws, ws_ptr, ws_n = self._workspace("evict", self._lib.sd_kv4_evict_workspace, self.R, self.n_kv_heads, budget)
+        kept, ws_ptr, ws_n, _ = self._workspace("evict", self._lib.sd_kv4_evict_workspace, self.R, self.n_kv_heads, budget)
         check(self._lib.sd_kv4_evict(self._ref, dst._ref, self.R, budget, recent, sinks, ws_ptr, ws_n,
                                      self._status_ptr, self._stream(stream)))
-        n = self.R * self.n_kv_heads * budget * 4
-        return ws[:n].view(torch.int32).view(self.R, self.n_kv_heads, budget)
+        return kept

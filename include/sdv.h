@@ -607,8 +607,11 @@ int sd_kv4_read(const sd_kv4* c, const int32_t* cu, const int32_t* cu_host, int3
  * launch; a longer request is read whole all the same.
  * out: bf16 [rows][n_q_heads][head_dim], 0 in a row that sees no key; lse
  * (optional): fp32 [rows][n_q_heads], the natural log of the sum of exp of
- * the scores, -inf in such a row.  P enters the products as two bf16 terms
- * (about 16 bits), the sums are fp32.
+ * the scores, -inf in such a row.  Scores and sums are fp32; a softmax weight
+ * enters its product with 11 bits (the rows' own values: 16), against the
+ * output's 8.  An own value row with a NaN or an infinity counts as NaN in every
+ * dim, as a held one does; out and lse are NaN in the rows that see such a row
+ * and in no others.
  * workspace: sd_kv4_attn_workspace bytes (rows = cu_host[R]), 256-byte
  * aligned, zeroed once by the caller and left ready for the next call; calls
  * that share one must not overlap.  Errors: SD_ERR_INVALID_ARG,

@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
           }
         }
         float top[NT][2];
+        uint32_t seen = 0;  // scores that count
         const int kpa = BIAS && ja < rq.m ? (a.row_pos ? a.row_pos[rq.n0 + ja] : rq.ctx + ja) : 0;
         const int kpb = BIAS && jb < rq.m ? (a.row_pos ? a.row_pos[rq.n0 + jb] : rq.ctx + jb) : 0;
 #pragma unroll
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
             }
             so[nt][e] = ja < rq.m && (anc >> ja & 1) ? ta : -INFINITY;
             so[nt][2 + e] = jb < rq.m && (anc >> jb & 1) ? tb : -INFINITY;
+            seen |= (uint32_t)(so[nt][e] != -INFINITY) << (4 * nt + e) | (uint32_t)(so[nt][2 + e] != -INFINITY) << (4 * nt + 2 + e);
             top[nt][e] = fmaxf(so[nt][e], so[nt][2 + e]);
           }
         grow(top);
@@ -298,60 +300,55 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
             pl[nt][i] = transpose8(lo);
           }
         // A product with a weight of 0 would carry a NaN or an infinity of a
-        // row's values to rows that do not see it: such keys are added one by one
+        // row's values to rows that do not see it: such a row counts as NaN in
+        // every dim, 0 here, and makes NaN the sums of the rows that see it
         const uint16_t* vn = a.v_new + (int64_t)rq.n0 * a.kv_stride + h * D + g * (D / 8);
-        uint32_t odd = 0;
+        uint32_t odd[4];
 #pragma unroll
         for (int b = 0; b < 4; b++) {
           const int kx = j0 + 8 * (b >> 1) + 2 * q + (b & 1);
+          uint32_t any = 0;
 #pragma unroll
           for (int c = 0; c < D / 64; c++) {
             const uint4 x = *reinterpret_cast<const uint4*>(vn + (kx < rq.m ? kx : 0) * a.kv_stride + 8 * c);
-            odd |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
+            any |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
                    ((x.z & 0x7F807F80u) + 0x00800080u) | ((x.w & 0x7F807F80u) + 0x00800080u);
           }
+          odd[b] = __ballot_sync(0xffffffffu, (any & 0x80008000u) != 0);
         }
-        if (!__any_sync(0xffffffffu, (odd & 0x80008000u) != 0)) {
+        if (odd[0] | odd[1] | odd[2] | odd[3]) {
 #pragma unroll
-          for (int c = 0; c < D / 64; c++) {
-            uint32_t x[4][4];
+          for (int i = 0; i < 2; i++) {
+            const int j = j0 + 8 * i + g;
+            const bool bad = j < rq.m && ((g & 1 ? odd[2 * i + 1] : odd[2 * i]) >> (g >> 1) & 0x11111111u);
 #pragma unroll
-            for (int b = 0; b < 4; b++) {
-              const int kx = j0 + 8 * (b >> 1) + 2 * q + (b & 1);
-              const uint4 v = *reinterpret_cast<const uint4*>(vn + (kx < rq.m ? kx : 0) * a.kv_stride + 8 * c);
-              x[b][0] = v.x, x[b][1] = v.y, x[b][2] = v.z, x[b][3] = v.w;
-            }
-#pragma unroll
-            for (int t = 0; t < 4; t++) {
-              const uint32_t f0 = prmt(x[0][t], x[1][t], 0x5410), f1 = prmt(x[0][t], x[1][t], 0x7632),
-                             f2 = prmt(x[2][t], x[3][t], 0x5410), f3 = prmt(x[2][t], x[3][t], 0x7632);
-#pragma unroll
-              for (int nt = 0; nt < NT; nt++) {
-                mma_bf16(o[nt][4 * c + t], f0, f1, f2, f3, ph[nt][0], ph[nt][1]);
-                mma_bf16(o[nt][4 * c + t], f0, f1, f2, f3, pl[nt][0], pl[nt][1]);
-              }
+            for (int nt = 0; nt < NT; nt++) {
+              const float x = __int_as_float(0x7FC00000);
+              const bool s0 = seen >> (4 * nt + 2 * i) & 1, s1 = seen >> (4 * nt + 2 * i + 1) & 1;
+              if (bad) l[nt] = f2add(l[nt], f2pack(s0 ? x : 0.f, s1 ? x : 0.f));
             }
           }
-        } else {
+        }
 #pragma unroll
-          for (int i = 0; i < 2; i++)
-            for (int gk = 0; gk < 8; gk++) {
-              const int j = j0 + 8 * i + gk;
-              if (j >= rq.m) break;
-              const uint16_t* p = vn + j * a.kv_stride;
+        for (int c = 0; c < D / 64; c++) {
+          uint32_t x[4][4];
 #pragma unroll
-              for (int nt = 0; nt < NT; nt++)
+          for (int b = 0; b < 4; b++) {
+            const int kx = j0 + 8 * (b >> 1) + 2 * q + (b & 1);
+            const bool bad = odd[b] >> q & 0x11111111u;
+            const uint4 v = *reinterpret_cast<const uint4*>(vn + (kx < rq.m ? kx : 0) * a.kv_stride + 8 * c);
+            x[b][0] = bad ? 0u : v.x, x[b][1] = bad ? 0u : v.y, x[b][2] = bad ? 0u : v.z, x[b][3] = bad ? 0u : v.w;
+          }
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                  const float w = __shfl_sync(0xffffffffu, so[nt][2 * i + e], 4 * gk + q);
-                  if ((s_anc[nt * 8 + 2 * q + e] >> j & 1) && w != 0.f)
+          for (int t = 0; t < 4; t++) {
+            const uint32_t f0 = prmt(x[0][t], x[1][t], 0x5410), f1 = prmt(x[0][t], x[1][t], 0x7632),
+                           f2 = prmt(x[2][t], x[3][t], 0x5410), f3 = prmt(x[2][t], x[3][t], 0x7632);
 #pragma unroll
-                    for (int t = 0; t < KK; t++) {
-                      o[nt][t][e] = fmaf(w, bf2f(p[2 * t]), o[nt][t][e]);
-                      o[nt][t][2 + e] = fmaf(w, bf2f(p[2 * t + 1]), o[nt][t][2 + e]);
-                    }
-                }
+            for (int nt = 0; nt < NT; nt++) {
+              mma_bf16(o[nt][4 * c + t], f0, f1, f2, f3, ph[nt][0], ph[nt][1]);
+              mma_bf16(o[nt][4 * c + t], f0, f1, f2, f3, pl[nt][0], pl[nt][1]);
             }
+          }
         }
       }
 

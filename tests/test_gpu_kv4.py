@@ -498,3 +498,108 @@ def test_a_bad_page_in_an_eviction_sets_the_status(M):
     dst = M.KV4Cache([[0, 1]], 2, 2, 128, 64)
     s.cache.evict(dst, 100, recent=100)
     assert s.cache.status() == 7
+
+
+# ------------------------------------- many rows a kv head (tensor cores) --
+
+@pytest.mark.parametrize("ms,G", [([25, 3, 12, 0, 1], 4), ([64, 1], 2), ([20, 13], 5), ([64, 2, 9], 16), ([33, 64], 3)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("opt", [dict(), dict(cap=20.0, slopes=True, gaps=True), dict(own=False, window=150)])
+def test_many_rows_and_mixed_requests(M, ms, G, D, opt):
+    """Requests of many and of few rows in one call: whole tiles, copies of
+    rows, rows over several segments."""
+    opt = dict(opt)
+    ctxs = [700, 40, 257, 64, 0][:len(ms)]
+    s = Setup(M, ctxs, D=D, page=32, gaps=opt.pop("gaps", False), seed=sum(ms) + G + D)
+    o = check_attention(M, s, ms, G=G, **opt)
+    check_observe(M, s, o, row_weight=[float(i % 2) for i in range(sum(ms))])
+
+
+@pytest.mark.parametrize("m,G", [(1, 1), (12, 1), (25, 4), (64, 5)])
+def test_a_long_context_against_64_bits_on_the_gpu(M, m, G):
+    """Enough keys that a warp walks many records: 131149 keys, 8 kv heads."""
+    D, hkv, ctx = 64, 8 if m * G > 64 else 32, 131149
+    g = torch.Generator(device="cuda").manual_seed(m)
+    c = M.KV4Cache(np.arange(-(-ctx // 128))[None][:, ::-1], -(-ctx // 128), hkv, D, 128)
+    K = torch.randn(ctx, hkv, D, generator=g, device="cuda").bfloat16()
+    V = torch.randn(ctx, hkv, D, generator=g, device="cuda").bfloat16()
+    q = (1.5 * torch.randn(m, hkv * G, D, generator=g, device="cuda")).bfloat16()
+    keys, rows = M.RequestRows([0, ctx]), M.RequestRows([0, m])
+    c.append(K, V, keys)
+    out, lse = c.attend(q, rows)
+    w = c.observe(q, lse, rows, out=torch.zeros_like(c.weight))
+    assert c.status() == 0
+    for h in range(0, hkv, 5):
+        kd, vd = ref.values(K[:, h].double()), ref.values(V[:, h].double())
+        want_w = torch.zeros(ctx, dtype=torch.float64, device="cuda")
+        for hq in range(h * G, h * G + G):
+            z = q[:, hq].double() @ kd.T / math.sqrt(D)
+            l = torch.logsumexp(z, 1)
+            p = torch.exp(z - l[:, None])
+            o = p @ vd
+            want_w += torch.exp(z - lse[:, hq].double()[:, None]).sum(0)
+            assert ((lse[:, hq].double() - l).abs() <= 2.0 ** -16).all()
+            # the softmax weights' 11 bits, over many keys: 2^-12 of the norm of p v
+            tol = H * o.abs() + 4 * 2.0 ** -12 * (p ** 2 @ vd ** 2).sqrt() + 2.0 ** -16
+            assert ((out[:, hq].double() - o).abs() <= tol).all()
+        assert ((w[0, h, :ctx].double() - want_w).abs() <= 2.0 ** -15 * want_w).all()
+
+
+@pytest.mark.parametrize("m,G", [(4, 2), (16, 4), (20, 4), (64, 4)])
+def test_a_bad_own_value_shows_only_where_it_is_seen(M, m, G):
+    s = Setup(M, [200], seed=m)
+    q, k, v = dev(rnd(s.g, m, 2 * G, 128)), dev(rnd(s.g, m, 2, 128)), dev(rnd(s.g, m, 2, 128))
+    rows = M.RequestRows([0, m])
+    anc = [1 << i | 1 for i in range(m)]  # a star: everyone sees the root and itself
+    good, _ = s.cache.attend(q, rows, k, v, anc=signed(anc))
+    v[2, 1, 7] = math.nan
+    v[3, 0, 100] = math.inf
+    out, lse = s.cache.attend(q, rows, k, v, anc=signed(anc))
+    torch.cuda.synchronize()
+    bad = torch.zeros(m, 2 * G, dtype=torch.bool, device="cuda")
+    bad[2, G:], bad[3, :G] = True, True
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    assert torch.equal(out[~bad], good[~bad]) and torch.isfinite(lse[~bad]).all()
+
+
+@pytest.mark.parametrize("ms,G", [([1, 1, 1], 4), ([8, 3, 16], 4), ([40, 2, 64], 4), ([64, 64, 5], 2)])
+def test_the_same_bits_from_cold_and_warm_caches(M, ms, G):
+    s = Setup(M, [1500, 260, 77], page=32, seed=33)
+    n = sum(ms)
+    q, k, v = dev(1.5 * rnd(s.g, n, 2 * G, 128)), dev(rnd(s.g, n, 2, 128)), dev(rnd(s.g, n, 2, 128))
+    rows = M.RequestRows(np.cumsum([0] + ms))
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    want = s.cache.attend(q, rows, k, v)
+    w = s.cache.observe(q, want[1], rows, out=torch.zeros_like(s.cache.weight))
+    for i in range(60):
+        if i % 2:
+            flush.zero_()
+        out, lse = s.cache.attend(q, rows, k, v)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        if i % 4 == 0:
+            assert torch.equal(w, s.cache.observe(q, lse, rows, out=torch.zeros_like(w)))
+    assert s.cache.status() == 0
+
+
+@pytest.mark.parametrize("ms", [[1, 1], [40, 64]])
+def test_a_bad_page_leaves_the_other_requests_alone(M, ms):
+    s = Setup(M, [300, 90], page=32, seed=17)
+    q = dev(rnd(s.g, sum(ms), 8, 128))
+    rows = M.RequestRows(np.cumsum([0] + ms))
+    good, lse = s.cache.attend(q, rows)
+    s.cache.page_table[0, 4] = -1
+    out, _ = s.cache.attend(q, rows)
+    assert s.cache.status() == 7
+    assert torch.equal(out[ms[0]:], good[ms[0]:]) and torch.isfinite(out).all()
+    s.cache.observe(q, lse, rows)
+    assert s.cache.status() == 7
+
+
+def test_the_serving_loop_example_runs(M):
+    import os
+    import runpy
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = runpy.run_path(os.path.join(root, "examples", "kv4_serving.py"))["main"](steps=12, seed=1, quiet=True)
+    assert r["status"] == 0 and r["evictions"] > 0 and max(r["ctx"]) <= r["limit"]
+    # against attention over the same keys in bf16: what 4 bits cost
+    assert r["error"] < 0.2

@@ -36,6 +36,8 @@ namespace sdv {
 // segments' units are dealt evenly over the CTAs, whatever the requests'
 // lengths; two CTAs an SM, so that one works while the other joins.
 
+constexpr int kMaxCtas = 512;
+
 template <int D, int NT, int W>
 struct AttnShape {
   static constexpr int RT = 8 * NT;
@@ -76,7 +78,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
   __shared__ Kv4Join s_join[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
 
-  if (warp == 0) kv4_share<RT, 1>(a, W, sh);
+  if (warp == 0) kv4_share<RT, 1>(a, 4 * W, sh);  // at least four units a warp while there is less than that a CTA
   if (tid == 0) {
     s_abort = 0;
     s_join[0] = s_join[1] = Kv4Join{};
@@ -621,50 +623,89 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
     if (!more) break;
   }
 
-  // join the parts of the segments that this CTA was the last to finish
-  __syncthreads();
+  // Join the parts of the segments that this CTA was the last to finish: first
+  // each row's factor of every part, a warp a row and a lane a part, then the
+  // parts' sums, four dims a thread and P parts of every one of its kItems in
+  // flight (a loop with one latency per item and eight parts took a third of
+  // a short call).
+  constexpr int kItems = (RT * (D / 4) + W * 32 - 1) / (W * 32), P = kItems > 1 ? 4 : 8;
+  static_assert(kMaxCtas * RT * 4 <= S::off_q, "factors take the place of the ring and the outputs");
+  float* s_f = reinterpret_cast<float*>(sm);  // [RT][n]
   for (int d = 0; d < 2; d++) {
+    __syncthreads();
     const Kv4Join jn = s_join[d];
     if (jn.n == 0) continue;
-    const int rows = min(RT, a.G * jn.m - jn.rc * RT);
+    const int n = jn.n, rows = min(RT, a.G * jn.m - jn.rc * RT);
     // c0's part is its last segment's unless the segment begins its share
     const int slot0 = 2 * jn.c0 + (sh.first(jn.c0) < jn.seg ? 1 : 0);
     auto part_of = [&](int c) { return a.part + (int64_t)(c == 0 ? slot0 : 2 * (jn.c0 + c)) * (RT * (D + 2)); };
-    for (int i = tid; i < rows * (D / 2); i += W * 32) {
-      const int row = i / (D / 2), x = i % (D / 2);
-      float M = -INFINITY, L = 0.f;
-      float2 acc = make_float2(0.f, 0.f);
-      for (int c = 0; c < jn.n; c += 8) {  // eight parts in flight
-        float2 ml[8], v[8];
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-          const float* pc = part_of(min(c + k, jn.n - 1));
-          ml[k] = __ldcg(reinterpret_cast<const float2*>(pc + RT * D) + row);
-          v[k] = __ldcg(reinterpret_cast<const float2*>(pc) + i);
-        }
-        float Mn = M;
-#pragma unroll
-        for (int k = 0; k < 8; k++) Mn = fmaxf(Mn, ml[k].x);
-        const float Ms = Mn == -INFINITY ? 0.f : Mn, al = ex2(M - Ms);
-        M = Mn;
-        L *= al;
-        acc.x *= al;
-        acc.y *= al;
-#pragma unroll
-        for (int k = 0; k < 8; k++)
-          if (c + k < jn.n) {
-            const float f = ex2(ml[k].x - Ms);
-            L = fmaf(f, ml[k].y, L);
-            acc.x = fmaf(f, v[k].x, acc.x);
-            acc.y = fmaf(f, v[k].y, acc.y);
-          }
-      }
-      const float inv = L == 0.f ? 0.f : 1.f / L;
+    auto row_out = [&](int row) {  // (row, query head) of the outputs
       const int rho = jn.rc * RT + row, gq = rho / jn.m;
-      const int64_t at = (int64_t)(jn.n0 + rho - gq * jn.m) * a.hq + jn.h * a.G + gq;
-      *reinterpret_cast<uint32_t*>(a.out + at * D + (x & 7) * (D / 8) + (x >> 3) * 2) =
-          pack_bf16x2(acc.x * inv, acc.y * inv);
-      if (x == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
+      return (int64_t)(jn.n0 + rho - gq * jn.m) * a.hq + jn.h * a.G + gq;
+    };
+    for (int row = warp; row < rows; row += W) {
+      float M = -INFINITY, L = 0.f;
+      float2 ml = make_float2(-INFINITY, 0.f);  // the last that this lane read
+      for (int c = lane; c < n; c += 32) {
+        ml = __ldcg(reinterpret_cast<const float2*>(part_of(c) + RT * D) + row);
+        M = fmaxf(M, ml.x);
+      }
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+      const float Ms = M == -INFINITY ? 0.f : M;
+      for (int c = lane; c < n; c += 32) {
+        if (n > 32) ml = __ldcg(reinterpret_cast<const float2*>(part_of(c) + RT * D) + row);
+        const float f = ex2(ml.x - Ms);
+        L = fmaf(f, ml.y, L);
+        s_f[row * n + c] = f;
+      }
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+      if (lane == 0) {
+        s_L[row] = L == 0.f ? 0.f : 1.f / L;
+        if (a.lse) a.lse[row_out(row)] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
+      }
+    }
+    __syncthreads();
+    float4 acc[kItems];
+#pragma unroll
+    for (int t = 0; t < kItems; t++) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < n; c += P) {
+      float4 v[kItems][P];
+#pragma unroll
+      for (int k = 0; k < P; k++) {
+        const float4* pc = reinterpret_cast<const float4*>(part_of(min(c + k, n - 1)));
+#pragma unroll
+        for (int t = 0; t < kItems; t++) {
+          const int i = tid + t * W * 32;
+          if (i < rows * (D / 4)) v[t][k] = __ldcg(pc + i);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < P; k++)
+        if (c + k < n) {
+#pragma unroll
+          for (int t = 0; t < kItems; t++) {
+            const int i = tid + t * W * 32;
+            if (i < rows * (D / 4)) {
+              const float f = s_f[i / (D / 4) * n + c + k];
+              acc[t].x = fmaf(f, v[t][k].x, acc[t].x);
+              acc[t].y = fmaf(f, v[t][k].y, acc[t].y);
+              acc[t].z = fmaf(f, v[t][k].z, acc[t].z);
+              acc[t].w = fmaf(f, v[t][k].w, acc[t].w);
+            }
+          }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kItems; t++) {
+      const int i = tid + t * W * 32;
+      if (i >= rows * (D / 4)) continue;
+      const int row = i / (D / 4), x = i % (D / 4) * 2;  // pairs x and x + 1, dims D/8 apart
+      const float inv = s_L[row];
+      uint16_t* o = a.out + row_out(row) * D + (x & 7) * (D / 8) + (x >> 3) * 2;
+      *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[t].x * inv, acc[t].y * inv);
+      *reinterpret_cast<uint32_t*>(o + D / 8) = pack_bf16x2(acc[t].z * inv, acc[t].w * inv);
     }
   }
 }
@@ -974,7 +1015,6 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
 // ---------------------------------------------------------------- launch --
 
 constexpr size_t kTicketBytes = 4096;  // one ticket a CTA
-constexpr int kMaxCtas = 1024;
 
 template <int D, int NT, int W>
 static int launch_attn_tile(const Kv4AttnArgs& a, int64_t units, bool bias, cudaStream_t st) {
@@ -1004,7 +1044,12 @@ static int launch_observe(const Kv4ObserveArgs& b, int64_t units, bool bias, cud
 }
 
 // Rows (query heads x nodes) that one kv head may have on the warp kernel;
-// more take the tensor cores.
+// more take the tensor cores.  Measured at 8 kv heads, D = 128, warp kernel
+// against tensor cores: 96 rows, one request of 2000 / 16000 / 65536 keys:
+// 27 / 51 / 139 us against 25 / 47 / 96; 64 rows: 20 / 44 / 104 against
+// 23 / 47 / 94, eight requests of 2000 / 16000: 41 / 178 against 44 / 155;
+// 32 rows, the same: 33 / 105 against 39 / 146.  With one tile of eight rows
+// a warp (NT = 1) eight warps fit, with two six.
 constexpr int kWarpRows = 64;
 
 template <int D>

@@ -205,7 +205,10 @@ struct Kv4Share {
 
 // By one warp, into shared memory.  With less work than 2 `width` units a CTA,
 // a CTA takes whole segments, or even parts of one of about `width` units, so
-// that fewer parts are joined; else every CTA takes its part.
+// that fewer parts are joined; else every CTA takes its part.  Measured with
+// the warp kernel (width 4 units a warp, against 1): one request of 2000
+// keys, 8 / 32 rows a kv head: 14 / 20 us against 18 / 31; a tree of 16 over
+// 2048 keys with its own keys: 29 against 27.
 template <int RT, int GU>
 __device__ __forceinline__ void kv4_share(const Kv4AttnArgs& a, int width, Kv4Share& sh) {
   const int lane = threadIdx.x & 31;

@@ -54,6 +54,11 @@ struct AttnShape {
   static constexpr int smem = off_ok + W * 2 * 4;
 };
 
+// A segment to join at a CTA's end: n parts (0: none) from CTA c0 on.
+struct Kv4Join {
+  int seg, n, c0, n0, m, h, rc;
+};
+
 template <int D, int NT, int W, bool BIAS>
 __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ Kv4AttnArgs a) {
   using S = AttnShape<D, NT, W>;
@@ -1053,10 +1058,10 @@ static int launch_observe(const Kv4ObserveArgs& b, int64_t units, bool bias, cud
 constexpr int kWarpRows = 64;
 
 template <int D>
-static int launch_attn(const Kv4AttnArgs& a, int total, int rows, int64_t segs, int64_t units, bool bias, cudaStream_t st) {
+static int launch_attn(const Kv4AttnArgs& a, int total, int rows, int64_t units, bool bias, cudaStream_t st) {
   if (rows <= 8) return launch_attn_tile<D, 1, 8>(a, units, bias, st);
   if (rows <= kWarpRows) return launch_attn_tile<D, 2, 6>(a, units, bias, st);
-  return kv4_launch_attn_tc(a, D, total, rows, segs, (units + 1) / 2, bias, st);
+  return kv4_launch_attn_tc(a, D, total, rows, (units + 1) / 2, bias, st);
 }
 
 // ---------------------------------------------------------------- checks --
@@ -1132,19 +1137,14 @@ extern "C" int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride,
   a.tickets = (int32_t*)workspace;
   a.part = (float*)((uint8_t*)workspace + kTicketBytes);
   int most = 0;
-  int64_t segs = 0;  // of the tensor-core kernel
-  for (int r = 0; r < R; r++) {
-    const int n = (cu_host[r + 1] - cu_host[r]) * a.G;
-    most = std::max(most, n);
-    segs += (int64_t)c->n_kv_heads * ((n + 255) / 256);
-  }
+  for (int r = 0; r < R; r++) most = std::max(most, (cu_host[r + 1] - cu_host[r]) * a.G);
   const int64_t ctx = max_ctx > 0 ? std::min<int64_t>(max_ctx, a.c.cap) : a.c.cap;
   const int64_t units = (int64_t)R * c->n_kv_heads * ((most + 31) / 32) * ((ctx + 31) / 32 + 2);
   if ((int64_t)R * c->n_kv_heads * ((most + 7) / 8) * ((a.c.cap + 31) / 32 + 2) > 0x7FFFFFFF)
     return kv4_bad(SD_ERR_UNSUPPORTED, who, "more than 2^31 runs of 32 keys");
   const bool bias = a.s.cap > 0.f || a.s.slopes || a.s.window > 0 || a.s.start;
-  return c->head_dim == 128 ? launch_attn<128>(a, rows, most, segs, units, bias, (cudaStream_t)stream)
-                            : launch_attn<64>(a, rows, most, segs, units, bias, (cudaStream_t)stream);
+  return c->head_dim == 128 ? launch_attn<128>(a, rows, most, units, bias, (cudaStream_t)stream)
+                            : launch_attn<64>(a, rows, most, units, bias, (cudaStream_t)stream);
 }
 
 extern "C" int sd_kv4_observe(const sd_kv4* c, const uint16_t* q, int64_t q_stride, int32_t n_q_heads,

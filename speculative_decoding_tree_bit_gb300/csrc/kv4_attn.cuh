@@ -19,9 +19,9 @@ struct Kv4AttnArgs {
   uint16_t* out;
   float* lse;
   int32_t* status;
-  int32_t* tickets;  // [grid], zero between calls
+  int32_t* tickets;  // [grid], zero between calls (warp kernel)
   float* part;       // [2 grid][rows of a tile][D + 2]
-  int4* joins;       // many rows: where a segment's parts lie, if a kernel of its own joins them
+  int4* joins;       // [R][hkv][kJoins]: where a segment's parts lie (tensor-core kernel)
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -266,14 +266,9 @@ __device__ __forceinline__ void kv4_share(const Kv4AttnArgs& a, int width, Kv4Sh
   }
 }
 
-// A segment to join at a CTA's end: n parts (0: none) from CTA c0 on.
-struct Kv4Join {
-  int seg, n, c0, n0, m, h, rc;
-};
-
 // Many rows a kv head (kv4_attn_tc.cu).
 size_t kv4_tc_workspace(int R, int hkv, int head_dim);
-int kv4_launch_attn_tc(const Kv4AttnArgs& a, int head_dim, int rows, int most, int64_t segs, int64_t units, bool bias,
+int kv4_launch_attn_tc(const Kv4AttnArgs& a, int head_dim, int rows, int most, int64_t units, bool bias,
                        cudaStream_t st);
 
 }  // namespace sdv

@@ -26,9 +26,8 @@
 // (four times), a copy in other lanes taking half (a quarter) of the keys and
 // leaving P 0 in the others': the products cost the same, the softmax is shared
 // by all schedulers, each of which reaches only its quarter of the lanes.  The
-// copies' partial sums are added in shared memory at a segment's end; a segment
-// that spans CTAs is joined in global memory by the last of them to finish, in
-// a fixed order.
+// copies' partial sums are added in shared memory at a segment's end; the parts
+// of a segment that spans CTAs are joined by a second kernel, in a fixed order.
 #include <algorithm>
 #include <type_traits>
 
@@ -181,88 +180,12 @@ struct TcRowsOf {
   __device__ __forceinline__ int first(int t) const { return base + (!WIDE || t == 0 ? 0 : split); }
 };
 
-// Joins the parts of a segment and writes its rows, by the softmax threads.
-template <int D, bool WIDE>
-__device__ __forceinline__ void tc_join(const Kv4AttnArgs& a, const Kv4Join& jn, int slot0, int st,
-                                        float2* s_ml) {
-  const int gm = a.G * jn.m, nc = (gm + kt::kRows - 1) / kt::kRows;
-  const TcRowsOf<WIDE> rw(gm, nc, jn.rc);
-  auto part_of = [&](int p) {
-    return a.part + (int64_t)(p == 0 ? slot0 : 2 * (jn.c0 + p)) * TcShape<D, WIDE>::kPart;
-  };
-  auto row_out = [&](int row) {
-    const int rho = rw.base + row, gq = rho / jn.m;
-    return (int64_t)(jn.n0 + rho - gq * jn.m) * a.hq + jn.h * a.G + gq;
-  };
-  // a row's maximum and sum, eight parts in flight
-  if (st < rw.rows) {
-    float M = -INFINITY, L = 0.f;
-    for (int c = 0; c < jn.n; c += 8) {
-      float2 ml[8];
-#pragma unroll
-      for (int k = 0; k < 8; k++) ml[k] = __ldcg(reinterpret_cast<const float2*>(part_of(min(c + k, jn.n - 1)) + kt::kRows * D) + st);
-      float Mn = M;
-#pragma unroll
-      for (int k = 0; k < 8; k++) Mn = fmaxf(Mn, ml[k].x);
-      const float Ms = Mn == -INFINITY ? 0.f : Mn;
-      L *= ex2(M - Ms);
-      M = Mn;
-#pragma unroll
-      for (int k = 0; k < 8; k++)
-        if (c + k < jn.n) L = fmaf(ex2(ml[k].x - Ms), ml[k].y, L);
-    }
-    if (a.lse) a.lse[row_out(st)] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
-    s_ml[st] = make_float2(M == -INFINITY ? 0.f : M, L == 0.f ? 0.f : 1.f / L);
-  }
-  bar_sync(2, kt::kSoftThreads);
-  // four pieces of four dims a thread, four parts of each in flight
-  const int items = rw.rows * (D / 4);
-  for (int i0 = st; i0 < items; i0 += 4 * kt::kSoftThreads) {
-    float4 acc[4];
-#pragma unroll
-    for (int q = 0; q < 4; q++) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = 0; c < jn.n; c += 4) {
-      float m[4][4];
-      float4 v[4][4];
-#pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const int i = min(i0 + q * kt::kSoftThreads, items - 1);
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-          const float* pc = part_of(min(c + k, jn.n - 1));
-          m[q][k] = __ldcg(pc + kt::kRows * D + 2 * (i / (D / 4)));
-          v[q][k] = __ldcg(reinterpret_cast<const float4*>(pc) + i);
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const float2 ml = s_ml[min(i0 + q * kt::kSoftThreads, items - 1) / (D / 4)];
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-          const float f = c + k < jn.n ? ex2(m[q][k] - ml.x) * ml.y : 0.f;
-          if (c + k < jn.n) {
-            acc[q].x = fmaf(f, v[q][k].x, acc[q].x);
-            acc[q].y = fmaf(f, v[q][k].y, acc[q].y);
-            acc[q].z = fmaf(f, v[q][k].z, acc[q].z);
-            acc[q].w = fmaf(f, v[q][k].w, acc[q].w);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < 4; q++) {
-      const int i = i0 + q * kt::kSoftThreads;
-      if (i < items)
-        *reinterpret_cast<uint2*>(a.out + row_out(i / (D / 4)) * D + 4 * (i % (D / 4))) =
-            make_uint2(pack_bf16x2(acc[q].x, acc[q].y), pack_bf16x2(acc[q].z, acc[q].w));
-    }
-  }
-  bar_sync(2, kt::kSoftThreads);
-}
-
-// The same by a kernel of its own, a warp a row, where a segment has many parts
-// (a few CTAs would join what the others wrote, 10 us of a 64-row tree over
-// 2048 keys against 3 for the launch).
+// Joins the parts of segments that span CTAs, a warp a row.  The last of a
+// segment's CTAs could do it and save the launch, but with many parts a
+// segment it leaves the other CTAs idle: 96 / 256 rows over 2000 keys 31 / 52
+// us against 24 / 28 with this kernel, over 65536 keys 113 / 206 against 96 /
+// 132; eight such requests of 2000 keys, one or two parts each, 49 / 70
+// against 49 / 67.
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(256) k_kv4_join(Kv4AttnArgs a, int rows) {
   pdl_wait();
@@ -461,7 +384,6 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   __shared__ int s_abort;
   __shared__ uint32_t s_tmem;
   __shared__ Kv4Share sh;
-  __shared__ Kv4Join s_join[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch();
 
@@ -479,7 +401,6 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
         mbar_init(&s_full[2 * t + b], 1), mbar_init(&p_full[2 * t + b], 4), mbar_init(&o_full[2 * t + b], 1);
     }
     s_abort = 0;
-    s_join[0] = s_join[1] = Kv4Join{};
     fence_mbar_init();
   }
   tc_fence_before();
@@ -918,28 +839,13 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
           bar_sync(2, kt::kSoftThreads);
         }
         tc_fence_before();
-        if (a.joins) {
-          if (st256 == 0 && w.ua == 0) {
-            const int last = sh.cta_of(w.seg + w.rq.nu - 1);
-            a.joins[((int64_t)w.r * a.c.hkv + h) * kt::kJoins + rc] =
-                make_int4(blockIdx.x, whole ? 0 : last - (int)blockIdx.x + 1, slot, 0);
-          }
-        } else if (!whole && st256 == 0) {
-          // is this the last of the segment's CTAs?  Acted on at this CTA's end.
-          Kv4Join jn{w.seg, 0, sh.cta_of(w.seg), w.rq.n0, w.rq.m, h, rc};
-          jn.n = sh.cta_of(w.seg + w.rq.nu - 1) - jn.c0 + 1;
-          if (atomic_add_acq_rel(a.tickets + jn.c0, 1) == jn.n - 1) {
-            a.tickets[jn.c0] = 0;
-            s_join[w.seg + w.rq.nu < sh.u1 ? 0 : 1] = jn;
-          }
+        if (st256 == 0 && w.ua == 0) {
+          const int last = sh.cta_of(w.seg + w.rq.nu - 1);
+          a.joins[((int64_t)w.r * a.c.hkv + h) * kt::kJoins + rc] =
+              make_int4(blockIdx.x, whole ? 0 : last - (int)blockIdx.x + 1, slot, 0);
         }
         op0 += n;
       } while (w.next(a, sh));
-      bar_sync(2, kt::kSoftThreads);
-      for (int d = 0; d < 2; d++) {
-        const Kv4Join jn = s_join[d];
-        if (jn.n) tc_join<D, WIDE>(a, jn, 2 * jn.c0 + (sh.first(jn.c0) < jn.seg ? 1 : 0), st256, s_ml);
-      }
   }
   tc_fence_before();
   __syncthreads();
@@ -956,30 +862,26 @@ size_t kv4_tc_workspace(int R, int hkv, int head_dim) {
 }
 
 template <int D, bool WIDE>
-static int launch_tc(Kv4AttnArgs a, int rows, int64_t segs, int64_t units, bool bias, cudaStream_t st) {
+static int launch_tc(Kv4AttnArgs a, int rows, int64_t units, bool bias, cudaStream_t st) {
   constexpr int smem = TcShape<D, WIDE>::smem;
   static const cudaError_t set[2] = {
       cudaFuncSetAttribute(k_kv4_attn_tc<D, false, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
       cudaFuncSetAttribute(k_kv4_attn_tc<D, true, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)};
   SD_CK(set[bias]);
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(num_sms(), units));
-  // many parts a segment: a kernel of its own joins them
-  const bool later = grid >= 3 * segs;
-  int4* joins = reinterpret_cast<int4*>(a.part);
+  a.joins = reinterpret_cast<int4*>(a.part);
   a.part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.part) + joins_bytes(a.R, a.c.hkv));
-  a.joins = later ? joins : nullptr;
   (bias ? k_kv4_attn_tc<D, true, WIDE> : k_kv4_attn_tc<D, false, WIDE>)<<<(unsigned)grid, kt::kThreads, smem, st>>>(a);
   SD_CK(cudaGetLastError());
-  if (later)
-    SD_CK(launch(k_kv4_join<D, WIDE>, dim3((unsigned)(((int64_t)rows * a.hq + 7) / 8)), dim3(256), 0, st, true, a, rows));
+  SD_CK(launch(k_kv4_join<D, WIDE>, dim3((unsigned)(((int64_t)rows * a.hq + 7) / 8)), dim3(256), 0, st, true, a, rows));
   return SD_OK;
 }
 
-int kv4_launch_attn_tc(const Kv4AttnArgs& a, int head_dim, int rows, int most, int64_t segs, int64_t units, bool bias,
+int kv4_launch_attn_tc(const Kv4AttnArgs& a, int head_dim, int rows, int most, int64_t units, bool bias,
                        cudaStream_t st) {
   if (head_dim == 128)
-    return most > 128 ? launch_tc<128, true>(a, rows, segs, units, bias, st) : launch_tc<128, false>(a, rows, segs, units, bias, st);
-  return most > 128 ? launch_tc<64, true>(a, rows, segs, units, bias, st) : launch_tc<64, false>(a, rows, segs, units, bias, st);
+    return most > 128 ? launch_tc<128, true>(a, rows, units, bias, st) : launch_tc<128, false>(a, rows, units, bias, st);
+  return most > 128 ? launch_tc<64, true>(a, rows, units, bias, st) : launch_tc<64, false>(a, rows, units, bias, st);
 }
 
 }  // namespace sdv

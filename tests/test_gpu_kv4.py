@@ -403,6 +403,31 @@ def test_another_stream_and_a_graph(M):
         assert all(torch.equal(a, b) for a, b in zip((out, lse, w), want))
 
 
+def test_many_rows_in_a_graph(M):
+    """Over 64 rows a kv head, a context whose parts are joined by a second
+    kernel, replayed with another context length and other rows."""
+    s = Setup(M, [5000, 700], seed=12)
+    cu = [0, 40, 70]
+    o = check_attention(M, s, [40, 30], G=8)
+    q, rows = o["qd"], o["rows"]
+    out, lse = torch.empty_like(q), torch.empty_like(o["lse"])
+    w = torch.zeros_like(s.cache.weight)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.cache.attend(q, rows, pos=o["posd"], out=out, lse=lse)
+        s.cache.observe(q, lse, rows, pos=o["posd"], out=w)
+    assert rows.cu.tolist() == cu
+    for ctxs in ([5000, 700], [64, 0], [4999, 699]):
+        s.cache.ctx_len.copy_(torch.tensor(ctxs))
+        want = s.cache.attend(q, rows, pos=o["posd"])
+        want_w = s.cache.observe(q, want[1], rows, pos=o["posd"], out=torch.zeros_like(w))
+        out.zero_(), lse.zero_(), w.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(w, want_w)
+    assert s.cache.status() == 0
+
+
 def test_the_same_call_gives_the_same_bits(M):
     s = Setup(M, [4000, 900], seed=10)
     q = dev(rnd(s.g, 20, 8, 128))

@@ -148,6 +148,13 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
     const int rows = min(RT, a.G * rq.m - rc * RT);
     const int start = BIAS && a.s.start ? a.s.start[r] : INT32_MIN;
 
+    // the own rows' lines on their way to the L2 while the queries are read
+    if (a.k_new && ua < rq.no)
+      for (int i = tid; i < rq.m * (D / 64); i += W * 32) {
+        const int64_t at = (int64_t)(rq.n0 + i / (D / 64)) * a.kv_stride + h * D + i % (D / 64) * 64;
+        prefetch_l2(a.k_new + at);
+        prefetch_l2(a.v_new + at);
+      }
     // the tile's query rows as B fragments; dims are taken in the order the
     // codes' nibbles give them
     if (first && tid / 32 * 32 >= RT * (D / 8)) begin();
@@ -158,6 +165,14 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
       const int node = ok ? rho % rq.m : 0, hq = h * a.G + (ok ? rho / rq.m : 0);
       uint4 x = make_uint4(0, 0, 0, 0);
       if (ok) x = *reinterpret_cast<const uint4*>(a.q + (int64_t)(rq.n0 + node) * a.q_stride + hq * D + oct * 8);
+      uint64_t anc = ok ? (2ull << node) - 1 : 0;
+      int pos = rq.ctx + node;
+      float slope = 0.f;
+      if (oct == 0) {
+        if (ok && a.anc) anc = a.anc[rq.n0 + node];
+        if (BIAS && a.row_pos) pos = a.row_pos[rq.n0 + node];
+        if (BIAS && a.s.slopes) slope = a.s.slopes[hq];
+      }
       if (first && i == tid) begin();  // behind the queries' own loads
       const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
       float f[8], qs = 0.f, big = 0.f;
@@ -184,9 +199,9 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
       if (oct == 0) {
         s_qs[row] = qs * sc2;
         s_fac[row] = pow2i(24 - e) * sc2;
-        s_slope[row] = BIAS && a.s.slopes ? a.s.slopes[hq] : 0.f;
-        s_pos[row] = a.row_pos ? a.row_pos[rq.n0 + node] : rq.ctx + node;
-        s_anc[row] = !ok ? 0ull : a.anc ? a.anc[rq.n0 + node] : (2ull << node) - 1;
+        s_slope[row] = slope;
+        s_pos[row] = pos;
+        s_anc[row] = anc;
       }
     }
     __syncthreads();

@@ -293,7 +293,8 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
             float ta = so[nt][e] * sc2, tb = so[nt][2 + e] * sc2;
             if (BIAS) {
               float tt[2] = {ta, tb};
-              kv4_scores(a.s, tt, s_slope[row], s_pos[row], start, [&](int i) { return i ? kpb : kpa; });
+              kv4_cap(a.s, tt);
+              kv4_bias(a.s, tt, s_slope[row], s_pos[row], start, [&](int i) { return i ? kpb : kpa; });
               ta = tt[0], tb = tt[1];
             }
             so[nt][e] = ja < rq.m && (anc >> ja & 1) ? ta : -INFINITY;
@@ -439,6 +440,14 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
           f2unpack(f2fma(f2pack(ks, ks), f2mul(f2pack(x[0], x[1]), fac[nt]), f2mul(f2pack(km, km), qs[nt])), x[0], x[1]);
         }
       }
+      if (BIAS) {
+        float t[8 * NT];
+#pragma unroll
+        for (int i = 0; i < 8 * NT; i++) t[i] = sc[i / (4 * NT)][i / 4 % NT][i % 4];
+        kv4_cap(a.s, t);
+#pragma unroll
+        for (int i = 0; i < 8 * NT; i++) sc[i / (4 * NT)][i / 4 % NT][i % 4] = t[i];
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -446,7 +455,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
           if (BIAS) {
             const int row = nt * 8 + 2 * q + e;
             float t[4] = {sc[0][nt][e], sc[0][nt][2 + e], sc[1][nt][e], sc[1][nt][2 + e]};
-            kv4_scores(a.s, t, s_slope[row], s_pos[row], start, [&](int i) { return kp[i]; });
+            kv4_bias(a.s, t, s_slope[row], s_pos[row], start, [&](int i) { return kp[i]; });
 #pragma unroll
             for (int i = 0; i < 4; i++) sc[i >> 1][nt][2 * (i & 1) + e] = t[i];
           }
@@ -998,10 +1007,16 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
                            f2mul(f2pack(km[i], km[i]), qs)), v[0][i], v[1][i]);
           }
           if (BIAS) {
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) t[i] = v[i & 1][i >> 1];
+            kv4_cap(a.s, t);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i & 1][i >> 1] = t[i];
 #pragma unroll
             for (int e = 0; e < 2; e++) {
               const float2 bi = s_bias[row + e];
-              kv4_scores(a.s, v[e], bi.x, __float_as_int(bi.y), start, [&](int i) { return kp[i]; });
+              kv4_bias(a.s, v[e], bi.x, __float_as_int(bi.y), start, [&](int i) { return kp[i]; });
             }
           }
 #pragma unroll

@@ -33,69 +33,52 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Pairs of fp32 values: one instruction for two.
-__device__ __forceinline__ uint64_t f2pack(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ void f2unpack(uint64_t r, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
-}
-__device__ __forceinline__ uint64_t f2fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-// Scores of N keys in base 2 from q.k: scale, cap, slope, masks.  The options'
-// branches lie outside the loops over the keys, which so overlap.  cap tanh(x /
-// cap): by tanh's Taylor series to x^9 while every x of the warp is below 0.3
-// (off by 1.6e-8 there; scores far below the cap are the rule), else as 1 - 2 /
-// (1 + e^2x), off by 1.2e-7 of the cap.  pos(i): position of key i.  By whole warps.
-template <int N, typename Pos>
-__device__ __forceinline__ void kv4_scores(const Kv4Score& s, float (&t)[N], float slope, int q_pos, int start, Pos pos) {
+// Scores in base 2 from q.k: scale and cap, pairs at a time.  cap tanh(x / cap):
+// by tanh's Taylor series to x^9 while every x of the warp is below 0.3 (off by
+// 1.6e-8 there; scores far below the cap are the rule), else as 1 - 2 / (1 +
+// e^2x), off by 1.2e-7 of the cap.  One branch for all N values, by whole warps.
+template <int N>
+__device__ __forceinline__ void kv4_cap(const Kv4Score& s, float (&t)[N]) {
   if (s.cap > 0.f) {
     const float in = __fdividef(s.scale, s.cap), out = s.cap * kLog2e;
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-      t[i] *= in;
-      top = fmaxf(top, fabsf(t[i]));
+    for (int i = 0; i < N; i += 2) {
+      f2unpack(f2mul(f2pack(t[i], t[i + 1]), f2pack(in, in)), t[i], t[i + 1]);
+      top = fmaxf(top, fmaxf(fabsf(t[i]), fabsf(t[i + 1])));
     }
+    auto series = [&](int i, float& a, float& b) {
+      const uint64_t x = f2pack(t[i], t[i + 1]), u = f2mul(x, x), z = f2mul(x, f2pack(out, out));
+      uint64_t q = f2fma(u, f2pack(62.f / 2835.f, 62.f / 2835.f), f2pack(-17.f / 315.f, -17.f / 315.f));
+      q = f2fma(q, u, f2pack(2.f / 15.f, 2.f / 15.f));
+      q = f2fma(q, u, f2pack(-1.f / 3.f, -1.f / 3.f));
+      f2unpack(f2fma(f2mul(q, u), z, z), a, b);
+    };
     if (!__any_sync(0xffffffffu, top >= 0.3f)) {
 #pragma unroll
-      for (int i = 0; i < N; i++) {
-        const float u = t[i] * t[i], z = t[i] * out;
-        float p = fmaf(u, 62.f / 2835.f, -17.f / 315.f);
-        p = fmaf(p, u, 2.f / 15.f);
-        p = fmaf(p, u, -1.f / 3.f);
-        t[i] = fmaf(p * u, z, z);
-      }
+      for (int i = 0; i < N; i += 2) series(i, t[i], t[i + 1]);
     } else {
 #pragma unroll
-      for (int i = 0; i < N; i++) {
-        const float u = t[i] * t[i], z = t[i] * out;
-        float p = fmaf(u, 62.f / 2835.f, -17.f / 315.f);
-        p = fmaf(p, u, 2.f / 15.f);
-        p = fmaf(p, u, -1.f / 3.f);
-        const float y = fmaf(-2.f * out, __fdividef(1.f, 1.f + ex2(2.f * kLog2e * t[i])), out);
-        t[i] = u < 0.09f ? fmaf(p * u, z, z) : y;
+      for (int i = 0; i < N; i += 2) {
+        float w[2];
+        series(i, w[0], w[1]);
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          const float y = fmaf(-2.f * out, __fdividef(1.f, 1.f + ex2(2.f * kLog2e * t[i + e])), out);
+          t[i + e] = fabsf(t[i + e]) < 0.3f ? w[e] : y;
+        }
       }
     }
   } else {
+    const float f = s.scale * kLog2e;
 #pragma unroll
-    for (int i = 0; i < N; i++) t[i] *= s.scale * kLog2e;
+    for (int i = 0; i < N; i += 2) f2unpack(f2mul(f2pack(t[i], t[i + 1]), f2pack(f, f)), t[i], t[i + 1]);
   }
+}
+
+// A row's slope and masks over N keys; pos(i): position of key i.
+template <int N, typename Pos>
+__device__ __forceinline__ void kv4_bias(const Kv4Score& s, float (&t)[N], float slope, int q_pos, int start, Pos pos) {
   if (s.slopes) {
 #pragma unroll
     for (int i = 0; i < N; i++) t[i] = fmaf(slope * kLog2e, (float)(pos(i) - q_pos), t[i]);

@@ -280,9 +280,10 @@ __device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint3
       }
       if (BIAS) {
 #pragma unroll
-        for (int c = 0; c < NC; c++) x[c] *= w.fac;
+        for (int c = 0; c < NC; c += 2) f2unpack(f2mul(f2pack(x[c], x[c + 1]), f2pack(w.fac, w.fac)), x[c], x[c + 1]);
         const int* kp = s_pos + st * 64 + w.key0;
-        kv4_scores(a.s, x, w.slope, w.qpos, w.start, [&](int c) { return kp[c]; });
+        kv4_cap(a.s, x);
+        kv4_bias(a.s, x, w.slope, w.qpos, w.start, [&](int c) { return kp[c]; });
       }
       if (info.x < 64 || (info.w & 1)) {  // not every key is held, or the rows' own keys
         const uint64_t held = (uint64_t)(uint32_t)info.z << 32 | (uint32_t)info.y;

@@ -91,14 +91,11 @@ __global__ void __launch_bounds__(256) k_kv4_append(Kv4View c, const uint16_t* _
     uint32_t lo2 = raw[0], hi2 = raw[0];
 #pragma unroll
     for (int j = 1; j < kV / 2; j++) lo2 = bf2_min(lo2, raw[j]), hi2 = bf2_max(hi2, raw[j]);
+    // (greatest, minus the least) as one pair across the lanes
+    uint32_t ext = bf2_max(prmt(hi2, lo2, 0x5410) ^ 0x80000000u, prmt(hi2, lo2, 0x7632) ^ 0x80000000u);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      lo2 = bf2_min(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
-      hi2 = bf2_max(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
-    }
-    lo2 = bf2_min(lo2, lo2 >> 16 | lo2 << 16);
-    hi2 = bf2_max(hi2, hi2 >> 16 | hi2 << 16);
-    const float lo = __uint_as_float(lo2 << 16), range = __uint_as_float(hi2 << 16) - lo;
+    for (int o = 8; o > 0; o >>= 1) ext = bf2_max(ext, __shfl_xor_sync(0xffffffffu, ext, o));
+    const float lo = -__uint_as_float(ext & 0xFFFF0000u), range = __uint_as_float(ext << 16) - lo;
     // s: the product with 1 / 15 is within two units of the quotient; the
     // division decides where that could turn the rounding to bf16
     float sq = range * (1.f / 15.f);
@@ -115,10 +112,16 @@ __global__ void __launch_bounds__(256) k_kv4_append(Kv4View c, const uint16_t* _
     const float inv = fine ? __fdividef(1.f, sc) : 0.f;
     float far = 0.f, st[kV];
 #pragma unroll
-    for (int j = 0; j < kV; j++) {
-      const float d = __uint_as_float(j & 1 ? raw[j >> 1] & 0xFFFF0000u : raw[j >> 1] << 16) - md;
-      st[j] = fmaf(d, inv, kBase + 8.f);
-      far = fmaxf(far, fabsf(fmaf(d, inv, (kBase + 8.f) - st[j])));
+    for (int j = 0; j < kV; j += 2) {
+      const uint64_t d = f2add(f2pack(__uint_as_float(raw[j >> 1] << 16), __uint_as_float(raw[j >> 1] & 0xFFFF0000u)),
+                               f2pack(-md, -md));
+      const uint64_t n = f2fma(d, f2pack(inv, inv), f2pack(kBase + 8.f, kBase + 8.f));
+      // the distance to the step taken: (n - base) - d inv, its size alone counts
+      const uint64_t off = f2fma(d, f2pack(-inv, -inv), f2add(n, f2pack(-kBase - 8.f, -kBase - 8.f)));
+      float o0, o1;
+      f2unpack(n, st[j], st[j + 1]);
+      f2unpack(off, o0, o1);
+      far = fmaxf(far, fmaxf(fabsf(o0), fabsf(o1)));
     }
     if (__any_sync(0xffffffffu, far > 0.5f - 4e-6f || !fine)) {
       const float h = 0.5f * sc;
@@ -135,10 +138,11 @@ __global__ void __launch_bounds__(256) k_kv4_append(Kv4View c, const uint16_t* _
         }
       }
     }
-    uint32_t word = 0;
+    // (the constant bits 0x4B400000 of each, shifted like its code, add up to kOnes)
+    constexpr uint32_t kOnes = kV == 8 ? 0x4B400000u * 0x11111111u : 0x4B400000u * 0x1111u;
+    uint32_t word = 0u - kOnes;
 #pragma unroll
-    for (int j = 0; j < kV; j++)
-      word += (__float_as_uint(fminf(fmaxf(st[j], kBase), kBase + 15.f)) - 0x4B400000u) << (4 * j);
+    for (int j = 0; j < kV; j++) word += __float_as_uint(fminf(fmaxf(st[j], kBase), kBase + 15.f)) << (4 * j);
     uint8_t* const rh = rec + (int64_t)i * c.gpp * kv4_rec(D);
     uint8_t* codes = rh + half * kv4_half(D) + (t & 31) * (D / 2);
     const int b = half ? kv4_vbyte<D>(t, l * (kV / 2)) : l * (kV / 2);

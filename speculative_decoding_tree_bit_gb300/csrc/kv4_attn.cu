@@ -948,7 +948,8 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
         const int stage = used % NS;
         const uint8_t* st = ring + stage * S::kStage;
         const int t = x * kKvGroup + 8 * q + g;  // the slot whose sum this lane writes
-        const float old = t < ctx ? (pass ? w_out[t] : b.decay * w_in[t]) : 0.f;
+        float old = 0.f;  // not looked at before the end
+        if (t < ctx) old = pass ? w_out[t] : w_in[t];
         if (!kv4_wait(&bar[stage], (used / NS) & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(31));
         const bool ok = s_ok[warp * NS + stage] != 0;
         uint32_t kw[4][D / 32];
@@ -1040,7 +1041,7 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
           sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
           if (q == i) mine = sum[i];
         }
-        if (t < ctx) w_out[t] = old + (ok ? mine : 0.f);
+        if (t < ctx) w_out[t] = (pass ? old : b.decay * old) + (ok ? mine : 0.f);
       }
       __syncthreads();  // s_q, s_row and s_node are free again
     }

@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(256) k_kv4_append(Kv4View c, const uint16_t* _
                                                     const int32_t* __restrict__ pos, const int32_t* at, bool advance,
                                                     int32_t* status) {
   constexpr int kV = D / 16;  // values of a lane
+  pdl_launch();
   const int e = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (e >= rows) return;
   const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(256) k_kv4_append(Kv4View c, const uint16_t* _
 // ctx_len[r] += the rows stored, once they are (append in place).
 __global__ void k_kv4_advance(int32_t* ctx_len, const int32_t* __restrict__ cu, const int32_t* __restrict__ count,
                               int R, int64_t cap) {
+  pdl_wait();
   const int r = blockIdx.x * blockDim.x + threadIdx.x;
   if (r >= R) return;
   const int n = count ? min(max(count[r], 0), cu[r + 1] - cu[r]) : cu[r + 1] - cu[r];
@@ -244,6 +246,7 @@ __global__ void __launch_bounds__(kSelThreads) k_kv4_select(Kv4View s, Kv4View d
   __shared__ uint32_t s_prefix, s_need, s_sum[2][32];
   const int h = blockIdx.x, r = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch();
   int ctx = s.ctx_len[r];
   if (ctx < 0 || ctx > s.cap) {
     if (tid == 0) set_status(status, SD_ERR_CAPACITY);
@@ -360,6 +363,7 @@ __global__ void __launch_bounds__(kSelThreads) k_kv4_select(Kv4View s, Kv4View d
 template <int D>
 __global__ void __launch_bounds__(256) k_kv4_move(Kv4View s, Kv4View d, int budget, const int32_t* __restrict__ list,
                                                   int32_t* status) {
+  pdl_wait();
   const int h = blockIdx.y, r = blockIdx.z, lane = threadIdx.x & 31;
   const int g = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int kept = min(d.ctx_len[r], budget);
@@ -412,6 +416,23 @@ __global__ void __launch_bounds__(256) k_kv4_move(Kv4View s, Kv4View d, int budg
 int kv4_bad(int code, const char* who, const char* what) {
   set_error(std::string(who) + ": " + what);
   return code;
+}
+
+// A kernel that may begin while the one before it ends (it calls pdl_wait()).
+// Unlike launch() it leaves the L1 as it is: asking for the shared memory of
+// the verify step's kernels costs an eviction of 16 x 16k keys 8 us.
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, int block, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -495,8 +516,7 @@ extern "C" int sd_kv4_append(const sd_kv4* c, const uint16_t* k, const uint16_t*
                                          in_place ? c->ctx_len : at, !in_place, status);
   SD_CK(cudaGetLastError());
   if (in_place) {
-    k_kv4_advance<<<(R + 127) / 128, 128, 0, st>>>(c->ctx_len, cu, count, R, view.cap);
-    SD_CK(cudaGetLastError());
+    SD_CK(launch_after(k_kv4_advance, dim3((R + 127) / 128), 128, st, c->ctx_len, cu, count, R, view.cap));
   }
   return SD_OK;
 }
@@ -546,7 +566,6 @@ extern "C" int sd_kv4_evict(const sd_kv4* src, const sd_kv4* dst, int32_t R, int
   SD_CK(cudaGetLastError());
   const int groups = (int)(((int64_t)budget + kKvGroup - 1) / kKvGroup);
   auto kern = src->head_dim == 128 ? k_kv4_move<128> : k_kv4_move<64>;
-  kern<<<dim3((groups + 7) / 8, src->n_kv_heads, R), 256, 0, st>>>(s, d, budget, list, status);
-  SD_CK(cudaGetLastError());
+  SD_CK(launch_after(kern, dim3((groups + 7) / 8, src->n_kv_heads, R), 256, st, s, d, budget, list, status));
   return SD_OK;
 }

@@ -8,8 +8,11 @@ namespace sdv {
 // One warp stores a row's keys and values of kHeads kv heads: a half warp the
 // key, the other the value, D / 16 values a lane (one or half a 32-bit word of
 // codes); the next head's row is on its way while one is worked on.  A row's
-// least and greatest value come from four shuffles.  Bound: bytes (4 D in, D +
-// 12 out per row and head).
+// least and greatest value come from four shuffles.  The bytes are few (4 D in,
+// D + 12 out per row and head); what bounds it is issue, 82% active: about 250
+// instructions a warp per row and head.  Four heads a warp share the row's
+// addresses and request (one head a warp: 92 us where four take 63).  Measured:
+// 16384 rows of 8 heads, D = 128: 37 us, 2.3 TB/s.
 
 constexpr int kHeads = 4;
 
@@ -172,7 +175,8 @@ __global__ void k_kv4_advance(int32_t* ctx_len, const int32_t* __restrict__ cu, 
 
 // ------------------------------------------------------------------ read --
 //
-// The append's warp and lanes, the other way.
+// The append's warp and lanes, the other way.  16384 rows of 8 heads, D = 128: 14
+// us, 6.1 TB/s.
 template <int D>
 __global__ void __launch_bounds__(256) k_kv4_read(Kv4View c, const int32_t* __restrict__ cu, int R, int rows,
                                                   const int32_t* __restrict__ at, uint16_t* __restrict__ k_out,
@@ -229,7 +233,7 @@ __global__ void __launch_bounds__(256) k_kv4_read(Kv4View c, const int32_t* __re
 // order-preserving integer keys); then each warp counts what stays of its run
 // of slots, and lists them in slot order with their positions and weights.
 // Bound: latency (the weights are read from the caches five times); the bytes
-// are few.
+// are few.  16 requests of 5000 to 16384 slots, 8 heads: 21 us.
 
 constexpr int kSelThreads = 1024;
 
@@ -359,7 +363,8 @@ __global__ void __launch_bounds__(kSelThreads) k_kv4_select(Kv4View s, Kv4View d
 }
 
 // Moves the rows that stay: one warp per group of 32 slots of dst, all of its
-// reads in flight before the first write.  Bound: bytes.
+// reads in flight before the first write.  Bound: bytes (2048 rows of 16 requests
+// and 8 heads, D = 128, 143 MB in and out: 17 us, the writes still in the L2).
 template <int D>
 __global__ void __launch_bounds__(256) k_kv4_move(Kv4View s, Kv4View d, int budget, const int32_t* __restrict__ list,
                                                   int32_t* status) {

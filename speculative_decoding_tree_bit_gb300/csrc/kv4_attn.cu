@@ -35,6 +35,12 @@ namespace sdv {
 // by the last CTA to finish, in CTA order (the same bits every time).  The
 // segments' units are dealt evenly over the CTAs, whatever the requests'
 // lengths; two CTAs an SM, so that one works while the other joins.
+//
+// Measured, 32 query and 8 kv heads, D = 128: 32 tokens over 1500 to 8192 keys 58
+// us, 3.0 TB/s (the ALU pipe 46% busy, issue 50%); 32 chains of 8 rows over 1024
+// to 4096 keys with a cap 92 us, 103 TFLOP/s (two tiles of rows a warp, six
+// warps; four tiles, four warps: 135 where two took 110); a tree of 16 over 2048
+// keys 25 us, most of it latency.
 
 constexpr int kMaxCtas = 512;
 
@@ -757,6 +763,10 @@ struct Kv4ObserveArgs {
 // that.  No sum crosses a warp, so there is nothing to join: a (request, kv
 // head)'s groups of 32 slots are dealt over the CTAs like the attention's.
 // More than kObsRows rows are taken in passes that add to the output.
+// Measured: 32 requests of 2 to 5 rows, 32 query and 8 kv heads, over 1500 to 8192
+// keys with positions: 43 us, 2.3 TB/s, 16 warps an SM waiting on their own
+// products and exponentials.  (Two tiles of rows at a time, for one making of the
+// codes' words: 59 where one takes 53.)
 
 constexpr int kObsWarps = 8, kObsRows = 128, kObsStages = 3;
 

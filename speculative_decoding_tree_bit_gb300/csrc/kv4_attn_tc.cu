@@ -28,6 +28,12 @@
 // by all schedulers, each of which reaches only its quarter of the lanes.  The
 // copies' partial sums are added in shared memory at a segment's end; the parts
 // of a segment that spans CTAs are joined by a second kernel, in a fixed order.
+//
+// Measured: a tree of 64 with 40 query and 8 kv heads over 131072 keys, D = 128
+// (WIDE, two segments of 160 rows a kv head): 382 us, 450 TFLOP/s; tensor pipe
+// 33%, issue 43%.  Bound by the softmax warps, two a scheduler, which wait for
+// tensor memory and their own chains (one score buffer a tile: 438 us; four
+// softmax warps: 500).
 #include <algorithm>
 #include <type_traits>
 

@@ -1094,7 +1094,8 @@ static int launch_observe(const Kv4ObserveArgs& b, int64_t units, bool bias, cud
 // against tensor cores: 96 rows, one request of 2000 / 16000 / 65536 keys:
 // 27 / 51 / 139 us against 25 / 47 / 96; 64 rows: 20 / 44 / 104 against
 // 23 / 47 / 94, eight requests of 2000 / 16000: 41 / 178 against 44 / 155;
-// 32 rows, the same: 33 / 105 against 39 / 146.  With one tile of eight rows
+// 32 rows, the same: 33 / 105 against 39 / 146.  (The contexts' lengths are on the
+// device, so the rule goes by the rows alone.)  With one tile of eight rows
 // a warp (NT = 1) eight warps fit, with two six.
 constexpr int kWarpRows = 64;
 
@@ -1140,7 +1141,7 @@ extern "C" size_t sd_kv4_attn_workspace(int32_t R, int32_t rows, int32_t n_q_hea
   if (R < 1 || rows < 0 || n_kv_heads < 1 || n_q_heads < n_kv_heads || n_q_heads % n_kv_heads ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  const size_t warp = (size_t)4 * num_sms() * 32 * (head_dim + 2) * sizeof(float);
+  const size_t warp = (size_t)4 * num_sms() * 16 * (head_dim + 2) * sizeof(float);  // two parts a CTA, two CTAs an SM
   const int most = std::min(rows, 64) * (n_q_heads / n_kv_heads);
   return kTicketBytes + (most > kWarpRows ? std::max(warp, kv4_tc_workspace(R, n_kv_heads, head_dim)) : warp);
 }

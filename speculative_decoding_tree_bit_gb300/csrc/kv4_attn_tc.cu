@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "kv4_attn.cuh"
+#include "kv4_rows.cuh"
 #include "tcgen05.cuh"
 
 namespace sdv {
@@ -168,22 +169,6 @@ struct TcWalk {
     if (u < rq.no) return a.k_new ? (rq.m + 31) / 32 : 1;
     return min(2, groups_end() - (rq.g0 + 2 * (u - rq.no)));
   }
-};
-
-// Rows of a segment: a request's G m rows in nc even runs.  Tile t holds `of(t)`
-// of them from row first(t) on, `copies` times, 128 / copies lanes apart.
-template <bool WIDE>
-struct TcRowsOf {
-  int base, rows, split, copies, run;
-  __device__ __forceinline__ TcRowsOf(int gm, int nc, int rc) {
-    run = ((gm + nc - 1) / nc + 31) / 32 * 32;
-    base = rc * run;
-    rows = min(run, gm - base);
-    split = WIDE ? min(rows, (rows / 2 + 31) / 32 * 32) : rows;
-    copies = WIDE || rows > 64 ? 1 : rows > 32 ? 2 : 4;
-  }
-  __device__ __forceinline__ int of(int t) const { return !WIDE || t == 0 ? split : rows - split; }
-  __device__ __forceinline__ int first(int t) const { return base + (!WIDE || t == 0 ? 0 : split); }
 };
 
 // Joins the parts of segments that span CTAs, a warp a row.  The last of a
@@ -701,7 +686,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
           const bool ok = ridx < rw.of(t);
           x.live = (ridx & ~31) < rw.of(t);
           x.key0 = idx / span * (64 / rw.copies);
-          const int rho = rw.first(t) + (ok ? ridx : 0), gq = rho / w.rq.m, node = rho - gq * w.rq.m;
+          const int rho = rw.row(t, ridx), gq = rho / w.rq.m, node = rho - gq * w.rq.m;
           const int hq = h * a.G + gq;
           x.start = BIAS && a.s.start ? a.s.start[w.r] : INT32_MIN;
           x.slope = BIAS && a.s.slopes ? a.s.slopes[hq] : 0.f;

@@ -758,6 +758,17 @@ class KV4Cache:
         if rows.R != self.R:
             raise ValueError(f"rows of {rows.R} requests on a cache of {self.R}")
 
+    def _score(self, score, hq):
+        """The score options' structure, their tensors long enough for hq
+        query heads and this cache's requests."""
+        if score is None:
+            return None
+        if score.slopes is not None and score.slopes.numel() < hq:
+            raise ValueError(f"slopes of {score.slopes.numel()} heads for {hq} query heads")
+        if score.start is not None and score.start.numel() < self.R:
+            raise ValueError(f"start of {score.start.numel()} requests on a cache of {self.R}")
+        return score.ref
+
     def _heads(self, q):
         hq = q.shape[1] if q.dim() == 3 else 0
         if hq == 0 or hq % self.n_kv_heads:
@@ -821,7 +832,7 @@ class KV4Cache:
         _, ws, ws_n, _ = self._workspace("attn", self._lib.sd_kv4_attn_workspace, self.R, n, hq, self.n_kv_heads, D)
         check(self._lib.sd_kv4_attn(self._ref, q.data_ptr(), qs, hq, rows.cu_ptr, rows.cu_host_ptr, self.R, kp, vp_, ks,
                                     _entries(anc, n, "anc", torch.int64), _entries(pos, n, "pos"),
-                                    None if score is None else score.ref, max_ctx, out.data_ptr(), lse.data_ptr(), ws,
+                                    self._score(score, hq), max_ctx, out.data_ptr(), lse.data_ptr(), ws,
                                     ws_n, self._status_ptr, self._stream(stream)))
         return out, lse
 
@@ -840,7 +851,7 @@ class KV4Cache:
         check(self._lib.sd_kv4_observe(self._ref, q.data_ptr(), qs, hq, _entries(lse, n * hq, "lse", torch.float32),
                                        rows.cu_ptr, rows.cu_host_ptr, self.R, _entries(pos, n, "pos"),
                                        _entries(row_weight, n, "row_weight", torch.float32),
-                                       None if score is None else score.ref, max_ctx, decay, out.data_ptr(),
+                                       self._score(score, hq), max_ctx, decay, out.data_ptr(),
                                        self._status_ptr, self._stream(stream)))
         return out
 

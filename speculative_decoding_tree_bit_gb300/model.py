@@ -629,6 +629,7 @@ class RequestRows:
             raise ValueError("cu must be [R+1] offsets that start at 0 and do not decrease")
         self.R, self.n = self.cu.size - 1, int(self.cu[-1])
         self.cu_dev = _i32(self.cu, device)
+        self.index = self.cu_dev.get_device()
         self.cu_ptr, self.cu_host_ptr = self.cu_dev.data_ptr(), self.cu.ctypes.data
 
 
@@ -649,9 +650,16 @@ class KV4Score:
 _BITS16 = (torch.bfloat16, torch.int16)
 
 
-def _rows16(t, n, heads, dim, what):
+def _here(t, index, what):
+    """Kernels read and write only what lies on their own GPU."""
+    if t.get_device() != index:
+        raise ValueError(f"{what} is on {t.device}, the cache on {'the CPU' if index < 0 else f'cuda:{index}'}")
+
+
+def _rows16(t, n, heads, dim, what, index):
     """The row stride in elements of a bf16 tensor (bfloat16 or int16 bits)
-    [n][heads][dim] whose rows may be strided; n None: any."""
+    [n][heads][dim] on GPU `index` whose rows may be strided; n None: any."""
+    _here(t, index, what)
     shape = t.shape
     if t.dtype not in _BITS16 or len(shape) != 3 or shape[1] != heads or shape[2] != dim or (n is not None and
                                                                                            shape[0] != n):
@@ -665,10 +673,11 @@ def _rows16(t, n, heads, dim, what):
     return st[0] if shape[0] > 1 else heads * dim
 
 
-def _entries(t, n, what, dtype=torch.int32):
-    """Pointer of an optional contiguous tensor of at least n entries."""
+def _entries(t, n, what, index, dtype=torch.int32):
+    """Pointer of an optional contiguous tensor of at least n entries on GPU `index`."""
     if t is None:
         return None
+    _here(t, index, what)
     if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous {dtype} of at least {n} entries")
     return t.data_ptr()
@@ -711,11 +720,13 @@ class KV4Cache:
         s.page_table, s.max_pages, s.ctx_len = self.page_table.data_ptr(), self.max_pages, self.ctx_len.data_ptr()
         self._s, self._ref = s, ctypes.byref(s)
         self._status_ptr, self._zero_ptr = self._status.data_ptr(), self._zero.data_ptr()
-        self._index = self.blocks.device.index
+        self._index = self.blocks.get_device()  # -1 on the CPU: every call is refused
         self._lib = lib()
 
     def _stream(self, stream):
-        if stream is not None or self._index is None:
+        if self._index < 0:
+            raise ValueError("the cache lies on the CPU: there is no path but the GPU's")
+        if stream is not None:
             return stream_ptr(stream)
         return torch._C._cuda_getCurrentRawStream(self._index)
 
@@ -749,7 +760,7 @@ class KV4Cache:
         if at is None:
             return None
         if isinstance(at, torch.Tensor):
-            return _entries(at, self.R, "at")
+            return _entries(at, self.R, "at", self._index)
         if at != 0:
             raise ValueError("at must be an int32 device tensor [R], or 0")
         return self._zero_ptr
@@ -757,16 +768,22 @@ class KV4Cache:
     def _rows(self, rows):
         if rows.R != self.R:
             raise ValueError(f"rows of {rows.R} requests on a cache of {self.R}")
+        if rows.index != self._index:
+            _here(rows.cu_dev, self._index, "rows")
 
     def _score(self, score, hq):
         """The score options' structure, their tensors long enough for hq
         query heads and this cache's requests."""
         if score is None:
             return None
-        if score.slopes is not None and score.slopes.numel() < hq:
-            raise ValueError(f"slopes of {score.slopes.numel()} heads for {hq} query heads")
-        if score.start is not None and score.start.numel() < self.R:
-            raise ValueError(f"start of {score.start.numel()} requests on a cache of {self.R}")
+        if score.slopes is not None:
+            _here(score.slopes, self._index, "slopes")
+            if score.slopes.numel() < hq:
+                raise ValueError(f"slopes of {score.slopes.numel()} heads for {hq} query heads")
+        if score.start is not None:
+            _here(score.start, self._index, "start")
+            if score.start.numel() < self.R:
+                raise ValueError(f"start of {score.start.numel()} requests on a cache of {self.R}")
         return score.ref
 
     def _heads(self, q):
@@ -782,12 +799,13 @@ class KV4Cache:
         each entry takes; count int32 [R]: entries of each request stored."""
         self._rows(rows)
         n = k.shape[0]
-        ks = _rows16(k, None, self.n_kv_heads, self.head_dim, "k")
-        if _rows16(v, n, self.n_kv_heads, self.head_dim, "v") != ks:
+        ks = _rows16(k, None, self.n_kv_heads, self.head_dim, "k", self._index)
+        if _rows16(v, n, self.n_kv_heads, self.head_dim, "v", self._index) != ks:
             raise ValueError("k and v must have one row stride")
         check(self._lib.sd_kv4_append(self._ref, k.data_ptr(), v.data_ptr(), ks, n, rows.cu_ptr, rows.cu_host_ptr,
-                                      rows.R, _entries(src, rows.n, "src"), _entries(count, rows.R, "count"),
-                                      _entries(pos, rows.n, "pos"), self._at(at), self._status_ptr,
+                                      rows.R, _entries(src, rows.n, "src", self._index),
+                                      _entries(count, rows.R, "count", self._index),
+                                      _entries(pos, rows.n, "pos", self._index), self._at(at), self._status_ptr,
                                       self._stream(stream)))
 
     def read(self, rows: RequestRows, at=0, dtype=torch.bfloat16, stream=None):
@@ -811,27 +829,31 @@ class KV4Cache:
         [n][n_q_heads])."""
         self._rows(rows)
         n, hq, D = rows.n, self._heads(q), self.head_dim
-        qs = _rows16(q, n, hq, D, "q")
+        qs = _rows16(q, n, hq, D, "q", self._index)
         kp = vp_ = None
         ks = 0
         if k is not None or v is not None:
             if k is None or v is None:
                 raise ValueError("k and v go together")
-            ks = _rows16(k, n, self.n_kv_heads, D, "k")
-            if _rows16(v, n, self.n_kv_heads, D, "v") != ks:
+            ks = _rows16(k, n, self.n_kv_heads, D, "k", self._index)
+            if _rows16(v, n, self.n_kv_heads, D, "v", self._index) != ks:
                 raise ValueError("k and v must have one row stride")
             kp, vp_ = k.data_ptr(), v.data_ptr()
         if out is None:
             out = torch.empty_like(q) if q.is_contiguous() else torch.empty(n, hq, D, dtype=q.dtype, device=q.device)
         elif out.shape != q.shape or out.dtype not in _BITS16 or not out.is_contiguous():
             raise ValueError("out must be contiguous bf16 of q's shape")
+        else:
+            _here(out, self._index, "out")
         if lse is None:
             lse = torch.empty(n, hq, dtype=torch.float32, device=q.device)
         elif lse.dtype is not torch.float32 or lse.shape != (n, hq) or not lse.is_contiguous():
             raise ValueError("lse must be contiguous float32 [rows][n_q_heads]")
+        else:
+            _here(lse, self._index, "lse")
         _, ws, ws_n, _ = self._workspace("attn", self._lib.sd_kv4_attn_workspace, self.R, n, hq, self.n_kv_heads, D)
         check(self._lib.sd_kv4_attn(self._ref, q.data_ptr(), qs, hq, rows.cu_ptr, rows.cu_host_ptr, self.R, kp, vp_, ks,
-                                    _entries(anc, n, "anc", torch.int64), _entries(pos, n, "pos"),
+                                    _entries(anc, n, "anc", self._index, torch.int64), _entries(pos, n, "pos", self._index),
                                     self._score(score, hq), max_ctx, out.data_ptr(), lse.data_ptr(), ws,
                                     ws_n, self._status_ptr, self._stream(stream)))
         return out, lse
@@ -843,14 +865,16 @@ class KV4Cache:
         attend returned it, row_weight float32 [n].  Returns out."""
         self._rows(rows)
         n, hq = rows.n, self._heads(q)
-        qs = _rows16(q, n, hq, self.head_dim, "q")
+        qs = _rows16(q, n, hq, self.head_dim, "q", self._index)
         if out is None:
             out = self.weight
         elif out.dtype is not torch.float32 or out.shape != self.weight.shape or not out.is_contiguous():
             raise ValueError("out must be contiguous float32 of the shape of weight")
-        check(self._lib.sd_kv4_observe(self._ref, q.data_ptr(), qs, hq, _entries(lse, n * hq, "lse", torch.float32),
-                                       rows.cu_ptr, rows.cu_host_ptr, self.R, _entries(pos, n, "pos"),
-                                       _entries(row_weight, n, "row_weight", torch.float32),
+        else:
+            _here(out, self._index, "out")
+        check(self._lib.sd_kv4_observe(self._ref, q.data_ptr(), qs, hq, _entries(lse, n * hq, "lse", self._index, torch.float32),
+                                       rows.cu_ptr, rows.cu_host_ptr, self.R, _entries(pos, n, "pos", self._index),
+                                       _entries(row_weight, n, "row_weight", self._index, torch.float32),
                                        self._score(score, hq), max_ctx, decay, out.data_ptr(),
                                        self._status_ptr, self._stream(stream)))
         return out
@@ -863,6 +887,7 @@ class KV4Cache:
         dst.ctx_len are unspecified)."""
         if dst is self or dst.R != self.R:
             raise ValueError("dst must be another cache of the same requests")
+        _here(dst.blocks, self._index, "dst")
         budget = int(budget)
         kept, ws_ptr, ws_n, _ = self._workspace("evict", self._lib.sd_kv4_evict_workspace, self.R, self.n_kv_heads, budget)
         check(self._lib.sd_kv4_evict(self._ref, dst._ref, self.R, budget, recent, sinks, ws_ptr, ws_n,

@@ -66,8 +66,8 @@ __global__ void __launch_bounds__(256) k_kv4_append(Kv4View c, const uint16_t* _
   const int s = src ? src[e] : e;
   const bool s_ok = s >= 0 && s < n_src;
   const uint16_t* x = (half ? v : k) + (s_ok ? (int64_t)s * row_stride : 0) + h0 * D + l * kV;
-  uint32_t next[kV / 2];
-  load_row<kV>(x, next);
+  uint32_t next[kV / 2] = {};
+  if (s_ok) load_row<kV>(x, next);  // k and v may have no rows at all
   const int p = pos ? pos[e] : 0;
   const int r = request_of(cu, R, e);
   const int i0 = e - cu[r];

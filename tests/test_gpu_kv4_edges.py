@@ -1,0 +1,99 @@
+"""The 4-bit cache on the GPU where it can go wrong: positions that do not lie
+behind the cache, rows that are NaN, values of very different sizes, calls
+without rows, streams and graphs.  Against the 64-bit definition.
+
+Tolerances, from the number formats.  With p the softmax weights and R_k the
+greatest magnitude of the held value row k, an output is off by at most
+  2^-8 |out|              its rounding to bf16,
+  2^-11 sum(p R)          a weight's rounding and a value's, 2^-12 each (fp16),
+  2 e sum(p R)            a score off by e, as a factor of each weight,
+  n 2^-24 sum(p R)        weights below fp16's normal range, n keys.
+e: the dot product's D + 16 roundings to fp32 of its terms' sizes, 2^-20 for the
+exponential, (1 + cap / 8) times that with a cap, and 2^-23 of the slope's term."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kv4_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+H = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def M():
+    from speculative_decoding_tree_bit_gb300 import model
+    return model
+
+
+def rnd(g, *shape):
+    return torch.randn(*shape, generator=g, dtype=torch.float64)
+
+
+def dev(x):
+    return x.to(torch.bfloat16).cuda()
+
+
+def i32(x):
+    return torch.as_tensor(x, dtype=torch.int32).cuda()
+
+
+def make(M, K, V, pos, room=0, page=32, extra=2):
+    """A cache whose request r holds the rows K[r], V[r] ([ctx][hkv][D]) at positions pos[r]."""
+    R, hkv, D = len(K), K[0].shape[1], K[0].shape[2]
+    pages = max(1, -(-(max(k.shape[0] for k in K) + room) // page))
+    n = R * pages + extra
+    table = np.random.default_rng(R + n).permutation(n)[:R * pages].reshape(R, pages)
+    c = M.KV4Cache(table, n, hkv, D, page)
+    c.blocks.fill_(0xFF)
+    rows = M.RequestRows(np.cumsum([0] + [k.shape[0] for k in K]))
+    if rows.n:
+        c.append(dev(torch.cat(K)), dev(torch.cat(V)), rows, pos=i32(torch.cat(pos)))
+    assert c.status() == 0
+    return c
+
+
+def expect(q, K, V, q_pos, k_pos, sees, cap=0.0, slope=0.0, window=0, start=None):
+    """One query head in 64 bits: (out, lse, scores, weights, tolerance of out, e)."""
+    D = q.shape[1]
+    z, size = ref.scores(q, K, q_pos, k_pos, 1 / math.sqrt(D), cap, slope, window, start)
+    z = z.masked_fill(~sees, -math.inf)
+    p, lse = ref.softmax(z)
+    far = float((q_pos[:, None] - k_pos[None]).abs().max()) * abs(slope) if K.shape[0] and q.shape[0] else 0.0
+    e = (D + 16) * 2.0 ** -24 * size + 2.0 ** -20 * (1 + cap / 8) + 2.0 ** -23 * far
+    out = p @ V
+    big = V.abs().amax(-1) if V.shape[0] else V.new_zeros(0)
+    tol = H * out.abs() + ((2.0 ** -11 + 2 * e + V.shape[0] * 2.0 ** -24) * (p @ big))[:, None]
+    return out, lse, z, p, tol, e
+
+
+def compare(got, got_lse, want, lse, tol, e, what=()):
+    none = lse == -math.inf
+    assert torch.equal(got_lse == -math.inf, none), what
+    err = (got - want).abs()
+    assert (err <= tol).all(), (*what, float((err / tol.clamp(min=1e-300)).max()))
+    err = (got_lse - lse)[~none].abs()
+    assert (err <= e + 2.0 ** -22 * lse[~none].abs() + 2.0 ** -18).all(), (*what, float(err.max()))
+
+
+# -------------------------------------------------- append from no source --
+
+def test_append_from_no_rows_at_all(M):
+    """n_src = 0: no source row exists, so none is read."""
+    import ctypes
+    from speculative_decoding_tree_bit_gb300 import check, lib, stream_ptr
+    c = M.KV4Cache([[0]], 1, 1, 64, 32)
+    x = torch.ones(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    rows, src, before = M.RequestRows([0, 2]), i32([0, -1]), c.blocks.clone()
+    def call(count):
+        check(lib().sd_kv4_append(ctypes.byref(c._s), x.data_ptr(), x.data_ptr(), 64, 0, rows.cu_dev.data_ptr(),
+                                  rows.cu.ctypes.data, 1, src.data_ptr(), count.data_ptr(), None, None,
+                                  c._status.data_ptr(), stream_ptr()))
+    zero, two = i32([0]), i32([2])
+    call(zero)
+    assert c.status() == 0 and c.ctx_len.tolist() == [0]
+    call(two)
+    assert c.status() == 7 and torch.equal(before, c.blocks)

@@ -613,8 +613,9 @@ int sd_kv4_read(const sd_kv4* c, const int32_t* cu, const int32_t* cu_host, int3
  * dim, as a held one does; out and lse are NaN in the rows that see such a row
  * and in no others.
  * workspace: sd_kv4_attn_workspace bytes (rows = cu_host[R]), 256-byte
- * aligned, zeroed once by the caller and left ready for the next call; calls
- * that share one must not overlap.  Errors: SD_ERR_INVALID_ARG,
+ * aligned, its first 4096 bytes zeroed once by the caller, ahead of the first
+ * call on its stream, and left ready for the next call; calls that share one
+ * must not overlap.  Errors: SD_ERR_INVALID_ARG,
  * SD_ERR_UNSUPPORTED, SD_ERR_WORKSPACE, SD_ERR_CUDA. */
 size_t sd_kv4_attn_workspace(int32_t R, int32_t rows, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim);
 int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride, int32_t n_q_heads, const int32_t* cu,

@@ -7,6 +7,7 @@ bf16 bit patterns as uint16 numpy arrays).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import numpy as np
@@ -648,6 +649,12 @@ class KV4Score:
 
 
 _BITS16 = (torch.bfloat16, torch.int16)
+KV4_TICKET_BYTES = 4096  # of sd_kv4_attn's workspace: zero before its first call
+
+
+def _on(stream):
+    """Tensors made within belong to the call's stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _here(t, index, what):
@@ -690,7 +697,8 @@ class KV4Cache:
     `observe` adds up the weight that rows give to the keys, `evict` copies
     what a budget keeps into another cache, `read` returns the values held.
     Calls that share a cache object share its workspace: issue them on one
-    stream."""
+    stream (or order the streams).  What a call with `stream` returns belongs to
+    that stream."""
 
     def __init__(self, page_table, n_pages: int, n_kv_heads: int, head_dim: int = 128, page_size: int = 64,
                  device="cuda"):
@@ -739,21 +747,27 @@ class KV4Cache:
     def nbytes(self) -> int:
         return self.blocks.numel() + 8 * self.pos.numel()
 
-    def _workspace(self, kind, size, *args):
-        """The workspace of `size(*args)` bytes, zeroed when made."""
+    def _workspace(self, kind, stream, size, *args):
+        """The workspace of `size(*args)` bytes, made on the call's stream: the
+        tickets in its first bytes are zero before the call's kernel counts in
+        them.  One made inside a capture belongs to its graph, whose replays zero
+        it, and serves that call alone."""
         key = (kind, args)
         ws = self._ws.get(key)
         if ws is None:
             n = int(size(*args))
-            for k, (_, _, _, t) in self._ws.items():
-                if k[0] == kind and t.numel() >= n:  # one buffer serves every call it is large enough for
-                    break
-            else:
-                t = torch.zeros(max(n, 256), dtype=torch.uint8, device=self.device)
-            view = t
-            if kind == "evict":
-                view = t[:n].view(torch.int32).view(*args)
-            ws = self._ws[key] = (view, t.data_ptr(), t.numel(), t)
+            t = next((w[3] for k, w in self._ws.items() if k[0] == kind and w[2] >= n), None)  # large enough already
+            keep = True
+            if t is None:
+                with _on(stream):
+                    t = torch.empty(max(n, 256), dtype=torch.uint8, device=self.device)
+                    if kind == "attn":
+                        t[:KV4_TICKET_BYTES].zero_()
+                    keep = not (t.is_cuda and torch.cuda.is_current_stream_capturing())
+            view = t[:n].view(torch.int32).view(*args) if kind == "evict" else t
+            ws = (view, t.data_ptr(), t.numel(), t)
+            if keep:
+                self._ws[key] = ws
         return ws
 
     def _at(self, at):
@@ -814,8 +828,9 @@ class KV4Cache:
         self._rows(rows)
         if dtype not in _BITS16:
             raise ValueError("dtype must be bfloat16, or int16 for its bits")
-        k = torch.empty(rows.n, self.n_kv_heads, self.head_dim, dtype=dtype, device=self.device)
-        v = torch.empty_like(k)
+        with _on(stream):
+            k = torch.empty(rows.n, self.n_kv_heads, self.head_dim, dtype=dtype, device=self.device)
+            v = torch.empty_like(k)
         check(self._lib.sd_kv4_read(self._ref, rows.cu_ptr, rows.cu_host_ptr, rows.R, self._at(at), k.data_ptr(),
                                     v.data_ptr(), self._status_ptr, self._stream(stream)))
         return k, v
@@ -840,18 +855,20 @@ class KV4Cache:
                 raise ValueError("k and v must have one row stride")
             kp, vp_ = k.data_ptr(), v.data_ptr()
         if out is None:
-            out = torch.empty_like(q) if q.is_contiguous() else torch.empty(n, hq, D, dtype=q.dtype, device=q.device)
+            with _on(stream):
+                out = torch.empty_like(q) if q.is_contiguous() else torch.empty(n, hq, D, dtype=q.dtype, device=q.device)
         elif out.shape != q.shape or out.dtype not in _BITS16 or not out.is_contiguous():
             raise ValueError("out must be contiguous bf16 of q's shape")
         else:
             _here(out, self._index, "out")
         if lse is None:
-            lse = torch.empty(n, hq, dtype=torch.float32, device=q.device)
+            with _on(stream):
+                lse = torch.empty(n, hq, dtype=torch.float32, device=q.device)
         elif lse.dtype is not torch.float32 or lse.shape != (n, hq) or not lse.is_contiguous():
             raise ValueError("lse must be contiguous float32 [rows][n_q_heads]")
         else:
             _here(lse, self._index, "lse")
-        _, ws, ws_n, _ = self._workspace("attn", self._lib.sd_kv4_attn_workspace, self.R, n, hq, self.n_kv_heads, D)
+        _, ws, ws_n, _ = self._workspace("attn", stream, self._lib.sd_kv4_attn_workspace, self.R, n, hq, self.n_kv_heads, D)
         check(self._lib.sd_kv4_attn(self._ref, q.data_ptr(), qs, hq, rows.cu_ptr, rows.cu_host_ptr, self.R, kp, vp_, ks,
                                     _entries(anc, n, "anc", self._index, torch.int64), _entries(pos, n, "pos", self._index),
                                     self._score(score, hq), max_ctx, out.data_ptr(), lse.data_ptr(), ws,
@@ -889,7 +906,8 @@ class KV4Cache:
             raise ValueError("dst must be another cache of the same requests")
         _here(dst.blocks, self._index, "dst")
         budget = int(budget)
-        kept, ws_ptr, ws_n, _ = self._workspace("evict", self._lib.sd_kv4_evict_workspace, self.R, self.n_kv_heads, budget)
+        kept, ws_ptr, ws_n, _ = self._workspace("evict", stream, self._lib.sd_kv4_evict_workspace, self.R, self.n_kv_heads,
+                                                 budget)
         check(self._lib.sd_kv4_evict(self._ref, dst._ref, self.R, budget, recent, sinks, ws_ptr, ws_n,
                                      self._status_ptr, self._stream(stream)))
         return kept

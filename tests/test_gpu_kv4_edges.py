@@ -97,3 +97,54 @@ def test_append_from_no_rows_at_all(M):
     assert c.status() == 0 and c.ctx_len.tolist() == [0]
     call(two)
     assert c.status() == 7 and torch.equal(before, c.blocks)
+
+
+# ----------------------------------------------------- streams and graphs --
+
+@pytest.mark.parametrize("m", [4, 40])
+def test_the_first_call_on_another_stream(M, m):
+    """The workspace is made ready on the stream of the call, whatever the
+    current stream is busy with."""
+    g = torch.Generator().manual_seed(m)
+    K, V = [ref.bf16(rnd(g, 3000, 2, 64))], [ref.bf16(rnd(g, 3000, 2, 64))]
+    c, d = (make(M, K, V, [torch.arange(3000)]) for _ in range(2))
+    q, rows = dev(rnd(g, m, 8, 64)), M.RequestRows([0, m])
+    want, want_lse = d.attend(q, rows)
+    pages = np.arange(8)[None]
+    dst, dst2 = M.KV4Cache(pages, 8, 2, 64, 32), M.KV4Cache(pages, 8, 2, 64, 32)
+    want_kept = d.evict(dst2, 200).clone()
+    # memory that the allocator may hand out again is not zero
+    junk = [torch.full((1 << 24,), 3, dtype=torch.int32, device="cuda") for _ in range(4)]
+    del junk
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    torch.cuda._sleep(200_000_000)  # about a tenth of a second on the current stream
+    out, lse = c.attend(q, rows, stream=other)
+    kept = c.evict(dst, 200, stream=other)
+    other.synchronize()
+    got = [t.clone() for t in (out, lse, kept)]
+    torch.cuda.synchronize()
+    assert c.status() == 0
+    assert torch.equal(got[0], want) and torch.equal(got[1], want_lse) and torch.equal(got[2], want_kept)
+
+
+def test_a_capture_before_any_other_call(M):
+    """The first attend inside a graph capture: eager calls before the first
+    replay, and replays after them, see a workspace that is ready."""
+    g = torch.Generator().manual_seed(2)
+    K, V = [ref.bf16(rnd(g, 3000, 2, 64))], [ref.bf16(rnd(g, 3000, 2, 64))]
+    c, d = (make(M, K, V, [torch.arange(3000)]) for _ in range(2))
+    q, rows = dev(rnd(g, 4, 8, 64)), M.RequestRows([0, 4])
+    want, want_lse = d.attend(q, rows)
+    out, lse = torch.zeros_like(want), torch.zeros_like(want_lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.attend(q, rows, out=out, lse=lse)
+    for _ in range(2):
+        a, b = c.attend(q, rows)
+        assert torch.equal(a, want) and torch.equal(b, want_lse)
+        out.zero_(), lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert c.status() == 0

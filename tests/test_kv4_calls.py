@@ -82,3 +82,27 @@ def test_a_cache_on_the_cpu_launches_nothing(M):
                  lambda: c.observe(q, torch.zeros(2, 4), rows), lambda: c.evict(d, 16)):
         with pytest.raises(ValueError, match="lies on the CPU"):
             call()
+
+
+def test_the_workspace_is_made_on_the_calls_stream(M, monkeypatch):
+    """... where its zeroing comes before the kernel, not on the current one;
+    and not kept when a capture only records that zeroing."""
+    import contextlib
+    entered = []
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: (entered.append(s), contextlib.nullcontext())[1])
+    c = M.KV4Cache(np.zeros((1, 1)), 1, 2, 128, 64, device="cpu")
+    size = lambda n: n  # noqa: E731
+    a = c._workspace("attn", "other", size, 5000)
+    assert entered == ["other"] and a[2] >= 5000 and int(a[3][:M.KV4_TICKET_BYTES].sum()) == 0
+    assert c._workspace("attn", "other", size, 5000) is a and entered == ["other"]
+    assert c._workspace("attn", None, size, 4500)[1] == a[1]  # large enough already
+    real = M.torch.empty
+    class Captured(torch.Tensor):
+        is_cuda = True
+    monkeypatch.setattr(M.torch, "empty", lambda *s, **k: real(*s, **k).as_subclass(Captured))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    b = c._workspace("attn", None, size, 9000)
+    assert c._workspace("attn", None, size, 9000) is not b
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    d = c._workspace("attn", None, size, 9000)
+    assert d[1] not in (a[1],) and c._workspace("attn", None, size, 9000) is d

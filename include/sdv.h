@@ -540,7 +540,7 @@ int sd_best_first_select(const int32_t* parents, const float* logprob, const int
  * max_pages + t / page_size].  A page may belong to several requests (a
  * shared prefix).  pos and weight: [R][n_kv_heads][max_pages * page_size],
  * 16-byte aligned, per request and slot the key's position in the text
- * (ascending with the slot) and the attention weight it collected.  ctx_len:
+ * (which does not fall from slot to slot) and the attention weight it collected.  ctx_len:
  * slots held per request.  page_size is a multiple of 32, head_dim 64 or 128.
  *
  * Rows of a call: request r owns rows cu[r] .. cu[r+1]-1 (cu int32 [R+1] on
@@ -602,7 +602,9 @@ int sd_kv4_read(const sd_kv4* c, const int32_t* cu, const int32_t* cu_host, int3
  * each [n_q_heads][head_dim]; k_new, v_new: rows kv_stride apart, each
  * [n_kv_heads][head_dim]; all 16-byte aligned; n_q_heads a multiple of
  * n_kv_heads, at most 16 query heads a kv head.  row_pos: position of each
- * row (null: ctx_len[r] + i); a request's first row has its least.  max_ctx:
+ * row (null: ctx_len[r] + i, which after an eviction lies before cached keys);
+ * a request's first row has its least.  Cached keys may stand at or after the
+ * rows (rows stored already): they are seen, as any key that is not hidden.  max_ctx:
  * the largest ctx_len the call can meet (0: the capacity), which sizes the
  * launch; a longer request is read whole all the same.
  * out: bf16 [rows][n_q_heads][head_dim], 0 in a row that sees no key; lse

@@ -97,18 +97,50 @@ struct Kv4Score {
   const int32_t* start;    // [R] or null
 };
 
-// First slot any row of a request can see, its rows standing at position p0
-// or later: positions ascend with the slots and no two are equal, so at most
-// (window - 1) cached keys lie inside the window and at most p0 - start
-// inside the document, the last ones.
-__device__ __forceinline__ int kv4_first(const Kv4Score& s, int r, int ctx, int p0) {
+// The least position that a row at position p0 or later sees.
+__device__ __forceinline__ int64_t kv4_since(const Kv4Score& s, int r, int p0) {
+  int64_t since = s.window > 0 ? (int64_t)p0 - s.window + 1 : INT64_MIN;
+  if (s.start) since = max(since, (int64_t)s.start[r]);
+  return since;
+}
+
+// First slot that rows at position p0 or later can see in any kv head, or one
+// before it: positions do not fall from slot to slot, so the slots before one
+// whose predecessor is hidden are hidden too.  The guess is right where
+// positions count up one by one to p0 or the row before it: one load a head
+// confirms it, and where it fails (rows cached already, positions past the
+// rows') the slot goes back in growing steps until a load does.
+__device__ __forceinline__ int kv4_guess(const Kv4Score& s, int r, int ctx, int p0) {
   int64_t n = ctx;
-  if (s.window > 0 && s.window - 1 < n) n = s.window - 1;
-  if (s.start) {
-    const int64_t d = (int64_t)p0 - s.start[r];
-    if (d < n) n = d < 0 ? 0 : d;
-  }
+  if (s.window > 0) n = min(n, (int64_t)s.window);
+  if (s.start) n = min(n, max((int64_t)0, (int64_t)p0 - s.start[r] + 1));
   return ctx - (int)n;
+}
+__device__ __forceinline__ int kv4_back(const int32_t* __restrict__ pos, int f, int64_t since) {
+  for (int step = kKvGroup; f > 0 && pos[f - 1] >= since; step *= 2) f = max(0, f - step);
+  return f;
+}
+// By a lane for a request of its own ...
+__device__ __forceinline__ int kv4_first_lane(const Kv4View& c, const Kv4Score& s, int r, int ctx, int p0) {
+  const int f = kv4_guess(s, r, ctx, p0);
+  const int64_t since = kv4_since(s, r, p0);
+  bool bad = false;
+  if (f > 0) {
+#pragma unroll 8
+    for (int h = 0; h < c.hkv; h++) bad |= c.pos[c.slot0(r, h) + f - 1] >= since;
+  }
+  int first = f;
+  if (bad)
+    for (int h = 0; h < c.hkv; h++) first = min(first, kv4_back(c.pos + c.slot0(r, h), f, since));
+  return first;
+}
+// ... and, the same, by a whole warp for one request.
+__device__ __forceinline__ int kv4_first(const Kv4View& c, const Kv4Score& s, int r, int ctx, int p0) {
+  const int f = kv4_guess(s, r, ctx, p0);
+  const int64_t since = kv4_since(s, r, p0);
+  int first = f;
+  for (int h = threadIdx.x & 31; h < c.hkv; h += 32) first = min(first, kv4_back(c.pos + c.slot0(r, h), f, since));
+  return __reduce_min_sync(0xffffffffu, first);
 }
 
 int kv4_check(const sd_kv4* c, int32_t R, const char* who, Kv4View* view);

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
   __shared__ Kv4Join s_join[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
 
-  if (warp == 0) kv4_share<RT, 1>(a, 4 * W, sh);  // at least four units a warp while there is less than that a CTA
+  if (warp == 0) kv4_share<RT, 1, BIAS>(a, 4 * W, sh);  // at least four units a warp while there is less than that a CTA
   if (tid == 0) {
     s_abort = 0;
     s_join[0] = s_join[1] = Kv4Join{};
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
   // records.  A lane holds the address of every 32nd of the warp's records.
   int r = sh.r0, s = sh.s0, seg = sh.seg0;
   const int u0 = sh.u0, u1 = sh.u1;
-  Kv4Req rq = kv4_req<RT>(a, r);
+  Kv4Req rq = kv4_req<RT, 1, BIAS>(a, r);
   int ua = u0 - seg, ub = min(rq.nu, u1 - seg);
   const uint8_t* addr;
   auto first_record = [&]() {  // the first of the segment's records that falls to this warp
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
     if (more) {
       if (++s == a.c.hkv * rq.nc) {
         s = 0;
-        do rq = kv4_req<RT>(a, ++r);
+        do rq = kv4_req<RT, 1, BIAS>(a, ++r);
         while (rq.nc == 0);
       }
       ua = 0;
@@ -864,8 +864,8 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
     u += g1 - g0;
     const int n0 = a.cu[r], m = min(max(a.cu[r + 1] - n0, 0), 64);
     const int start = BIAS && a.s.start ? a.s.start[r] : INT32_MIN;
-    const int first = a.s.window > 0 || a.s.start
-                          ? kv4_first(a.s, r, ctx, a.row_pos && m ? a.row_pos[n0] : ctx) / kKvGroup
+    const int first = BIAS && (a.s.window > 0 || a.s.start)
+                          ? kv4_first(a.c, a.s, r, ctx, a.row_pos && m ? a.row_pos[n0] : ctx) / kKvGroup
                           : 0;  // groups before it collect nothing
     if (warp == 0) {  // the rows that count
       int n = 0;

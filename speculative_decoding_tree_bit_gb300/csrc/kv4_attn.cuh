@@ -155,11 +155,21 @@ struct Kv4Req {
   int n0, m, ctx, g0, no, nu, nc;
 };
 
-template <int RT, int GU = 1>
-__device__ __forceinline__ Kv4Req kv4_req(const Kv4AttnArgs& a, int r) {
-  Kv4Req q;
+// A request's rows alone: n0, m and nc.
+template <int RT>
+__device__ __forceinline__ Kv4Req kv4_req_rows(const Kv4AttnArgs& a, int r) {
+  Kv4Req q = {};
   q.n0 = a.cu[r];
   q.m = min(max(a.cu[r + 1] - q.n0, 0), 64);
+  q.nc = (a.G * q.m + RT - 1) / RT;
+  return q;
+}
+
+// BIAS: the call has scoring options.  LANE: by a lane for a request of its
+// own, else by a whole warp for one.
+template <int RT, int GU, bool BIAS, bool LANE = false>
+__device__ __forceinline__ Kv4Req kv4_req(const Kv4AttnArgs& a, int r) {
+  Kv4Req q = kv4_req_rows<RT>(a, r);
   int ctx = a.c.ctx_len[r];
   if (ctx < 0 || ctx > a.c.cap) {
     set_status(a.status, SD_ERR_CAPACITY);
@@ -167,12 +177,14 @@ __device__ __forceinline__ Kv4Req kv4_req(const Kv4AttnArgs& a, int r) {
   }
   q.ctx = ctx;
   int first = 0;
-  if (a.s.window > 0 || a.s.start) first = kv4_first(a.s, r, ctx, a.row_pos && q.m ? a.row_pos[q.n0] : ctx);
+  if (BIAS && (a.s.window > 0 || a.s.start)) {
+    const int p0 = a.row_pos && q.m ? a.row_pos[q.n0] : ctx;
+    first = LANE ? kv4_first_lane(a.c, a.s, r, ctx, p0) : kv4_first(a.c, a.s, r, ctx, p0);
+  }
   q.g0 = first / kKvGroup;
   q.no = a.k_new ? (q.m + 32 * GU - 1) / (32 * GU) : 0;
   q.nu = q.no + (ctx > first ? ((ctx - 1) / kKvGroup - q.g0 + GU) / GU : 0);
   if (q.nu == 0) q.no = q.nu = 1;  // an empty run
-  q.nc = (a.G * q.m + RT - 1) / RT;
   return q;
 }
 
@@ -194,14 +206,14 @@ struct Kv4Share {
 // the warp kernel (width 4 units a warp, against 1): one request of 2000
 // keys, 8 / 32 rows a kv head: 14 / 20 us against 18 / 31; a tree of 16 over
 // 2048 keys with its own keys: 29 against 27.
-template <int RT, int GU>
+template <int RT, int GU, bool BIAS>
 __device__ __forceinline__ void kv4_share(const Kv4AttnArgs& a, int width, Kv4Share& sh) {
   const int lane = threadIdx.x & 31;
   int U = 0, segs = 0, lo = 0;
   Kv4Req rq = {};
   for (int base = 0; base < a.R; base += 32) {
     rq = {};
-    if (base + lane < a.R) rq = kv4_req<RT, GU>(a, base + lane);
+    if (base + lane < a.R) rq = kv4_req<RT, GU, BIAS, true>(a, base + lane);
     const int n = a.c.hkv * rq.nc * rq.nu;
     int run = n;
 #pragma unroll
@@ -224,7 +236,7 @@ __device__ __forceinline__ void kv4_share(const Kv4AttnArgs& a, int width, Kv4Sh
     for (int base = 0; base < a.R; base += 32) {
       if (a.R > 32) {
         rq = {};
-        if (base + lane < a.R) rq = kv4_req<RT, GU>(a, base + lane);
+        if (base + lane < a.R) rq = kv4_req<RT, GU, BIAS, true>(a, base + lane);
         const int n = a.c.hkv * rq.nc * rq.nu;
         int run = n;
 #pragma unroll

@@ -141,12 +141,13 @@ __device__ __forceinline__ int expo(uint32_t bits) { return (int)(bits >> 23 & 2
 // Exponent that keeps V operands of magnitude at most |x| (bits) below 2^-6.
 __device__ __forceinline__ int tc_exponent(uint32_t bits) { return expo(bits) + 7; }
 
-// A CTA's walk over its segments.
+// A CTA's walk over its segments, by whole warps.
+template <bool BIAS>
 struct TcWalk {
   int r, s, seg, ua, ub;
   Kv4Req rq;
   __device__ __forceinline__ TcWalk(const Kv4AttnArgs& a, const Kv4Share& sh) : r(sh.r0), s(sh.s0), seg(sh.seg0) {
-    rq = kv4_req<kt::kRows, 2>(a, r);
+    rq = kv4_req<kt::kRows, 2, BIAS>(a, r);
     ua = sh.u0 - seg;
     ub = min(rq.nu, sh.u1 - seg);
   }
@@ -155,7 +156,7 @@ struct TcWalk {
     if (seg >= sh.u1) return false;
     if (++s == a.c.hkv * rq.nc) {
       s = 0;
-      do rq = kv4_req<kt::kRows, 2>(a, ++r);
+      do rq = kv4_req<kt::kRows, 2, BIAS>(a, ++r);
       while (rq.nc == 0);
     }
     ua = 0;
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(256) k_kv4_join(Kv4AttnArgs a, int rows) {
   const int lane = threadIdx.x & 31;
   const int e = (int)(i / a.hq), hq = (int)(i - (int64_t)e * a.hq), h = hq / a.G;
   const int r = request_of(a.cu, a.R, e);
-  const Kv4Req rq = kv4_req<kt::kRows, 2>(a, r);
+  const Kv4Req rq = kv4_req_rows<kt::kRows>(a, r);
   if (rq.m == 0) return;
   const int rho = (hq - h * a.G) * rq.m + e - rq.n0;
   const int run = TcRowsOf<WIDE>(a.G * rq.m, rq.nc, 0).run, rc = rho / run, row = rho - rc * run;
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch();
 
-  if (warp == kt::kSoft) kv4_share<kt::kRows, 2>(a, 4, sh);
+  if (warp == kt::kSoft) kv4_share<kt::kRows, 2, BIAS>(a, 4, sh);
   if (warp == kt::kMma) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   } else if (warp >= kt::kLoad) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == kt::kLoad) {
-      TcWalk w(a, sh);
+      TcWalk<BIAS> w(a, sh);
       uint32_t n = 0;
       do {
         const int h = w.head(), c0 = max(w.ua, w.rq.no);
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
         // the whole warp walks and waits; one lane, elected, issues: so the
         // compiler keeps the operands in uniform registers (33 cycles a
         // product of 64 columns, against 45 and more under lane == 0)
-        TcWalk w(a, sh);
+        TcWalk<BIAS> w(a, sh);
         const uint32_t id0 = (1u << 4) | (8u << 24);  // fp32 += fp16 fp16, M = 128
         const uint32_t idv = id0 | (1u << 16) | ((uint32_t)(D / 8) << 17);
         const uint64_t kop = sdesc_sw128(smem_u32(sm)), vop = sdesc_mn(smem_u32(sm) + S::kOp),
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   } else if (warp < kt::kSoft) {
       // ------------------------------------------------------- operands --
       asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-      TcWalk w(a, sh);
+      TcWalk<BIAS> w(a, sh);
       const bool is_k = warp < 4;
       const int dt = tid & 127, dw = warp & 3;
       // eight lanes take four rows' neighbouring 16-byte pieces: two phases a
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   } else {
       // -------------------------------------------------------- softmax --
       asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-      TcWalk w(a, sh);
+      TcWalk<BIAS> w(a, sh);
       const int t = (warp - kt::kSoft) >> 2, st256 = tid - kt::kSoft * 32;
       const int idx = (warp & 3) * 32 + lane;                                // TMEM lane
       const uint32_t tb = tm + t * 256 + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes

@@ -840,7 +840,8 @@ class KV4Cache:
         """Attention of the rows over the cache and their own keys
         (sd_kv4_attn).  q [n][n_q_heads][head_dim], k, v [n][n_kv_heads]
         [head_dim] (or both None), anc int64 ancestor bits [n] (sd_tree_info;
-        None: causal), pos int32 [n].  Returns (out like q, lse float32
+        None: causal), pos int32 [n] (None: ctx_len + i, which an eviction
+        leaves behind the cached positions).  Returns (out like q, lse float32
         [n][n_q_heads])."""
         self._rows(rows)
         n, hq, D = rows.n, self._heads(q), self.head_dim

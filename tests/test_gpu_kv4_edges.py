@@ -79,6 +79,93 @@ def compare(got, got_lse, want, lse, tol, e, what=()):
     assert (err <= e + 2.0 ** -22 * lse[~none].abs() + 2.0 ** -18).all(), (*what, float(err.max()))
 
 
+# -------------------------------- rows that do not stand behind the cache --
+
+def attend_and_observe(M, c, K, V, pos, rows_of, q, G, q_pos, score_kw, own=None, posd=True):
+    """attend and observe of every request against the definition; q_pos: per request."""
+    rows = M.RequestRows(np.cumsum([0] + rows_of))
+    start = score_kw.get("start")
+    score = M.KV4Score(window=score_kw.get("window", 0), start=i32(start) if start is not None else None)
+    pd = i32([p for r in q_pos for p in r]) if posd else None
+    out, lse = c.attend(dev(q), rows, pos=pd, score=score)
+    w0 = torch.rand(c.weight.shape, generator=torch.Generator().manual_seed(7))
+    c.weight.copy_(w0)
+    w = c.observe(dev(q), lse, rows, pos=pd, score=score, decay=0.5, out=torch.full_like(c.weight, -3.0))
+    assert c.status() == 0
+    out, lse, w = out.double().cpu(), lse.double().cpu(), w.double().cpu()
+    for r in range(len(K)):
+        a, b = int(rows.cu[r]), int(rows.cu[r + 1])
+        qp = torch.tensor(q_pos[r], dtype=torch.int64)
+        hkv = K[r].shape[1]
+        want_w = 0.5 * w0[r, :, :K[r].shape[0]].double()
+        e_max = 0.0
+        for h in range(hkv * G):
+            held = ref.values(K[r][:, h // G]), ref.values(V[r][:, h // G])
+            kp = pos[r] if pos[r].dim() == 1 else pos[r][h // G]
+            sees = torch.ones(b - a, kp.numel(), dtype=torch.bool)
+            want, l, z, p, tol, e = expect(q[a:b, h], *held, qp, kp, sees, window=score_kw.get("window", 0),
+                                           start=start[r] if start is not None else None)
+            compare(out[a:b, h], lse[a:b, h], want, l, tol, e, (r, h))
+            want_w[h // G] += torch.exp(z - torch.where(l == -math.inf, math.inf, lse[a:b, h])[:, None]).sum(0)
+            e_max = max(e_max, e)
+        err = (w[r, :, :K[r].shape[0]] - want_w).abs()
+        assert (err <= (e_max + 2.0 ** -18) * want_w + 1e-12).all(), r
+
+
+@pytest.mark.parametrize("G", [2, 40])
+def test_a_token_that_is_cached_already_sees_its_whole_window(M, G):
+    """Append, then attend without own keys: the row's own key is the cache's
+    last, and the oldest key of the window may be alone in its group of 32."""
+    g = torch.Generator().manual_seed(G)
+    hkv, D = 1 if G > 16 else 2, 64
+    m, G = (5, 16) if G > 16 else (1, G)  # 80 rows a kv head: the tensor-core kernel
+    lens = list(range(100, 135))
+    K = [ref.bf16(rnd(g, n, hkv, D)) for n in lens]
+    V = [ref.bf16(rnd(g, n, hkv, D)) for n in lens]
+    pos = [torch.arange(n) for n in lens]
+    c = make(M, K, V, pos)
+    q = ref.bf16(rnd(g, m * len(lens), hkv * G, D))
+    q_pos = [[n - m + i for i in range(m)] for n in lens]
+    for kw in (dict(window=40), dict(window=1), dict(window=65), dict(start=[n - 34 for n in lens]),
+               dict(start=[n - 1 for n in lens], window=70), dict(start=[33] * len(lens))):
+        attend_and_observe(M, c, K, V, pos, [m] * len(lens), q, G, q_pos, kw)
+
+
+@pytest.mark.parametrize("m,G", [(8, 2), (64, 4)])
+def test_rows_that_are_all_cached_already(M, m, G):
+    g = torch.Generator().manual_seed(m)
+    hkv, D, n = 2, 128, 300
+    K, V = [ref.bf16(rnd(g, n, hkv, D))], [ref.bf16(rnd(g, n, hkv, D))]
+    pos = [torch.arange(n) * 2]
+    c = make(M, K, V, pos)
+    q = ref.bf16(rnd(g, m, hkv * G, D))
+    q_pos = [[2 * (n - m + i) for i in range(m)]]
+    for kw in (dict(window=33), dict(window=64), dict(start=[2 * (n - 90)]), dict(start=[2 * (n - m)], window=300)):
+        attend_and_observe(M, c, K, V, pos, [m], q, G, q_pos, kw)
+
+
+@pytest.mark.parametrize("m,G", [(1, 2), (6, 16)])
+@pytest.mark.parametrize("posd", [False, True])
+def test_positions_after_an_eviction(M, m, G, posd):
+    """The kept keys' positions pass ctx_len, and differ between the kv heads:
+    by default the rows stand at ctx_len + i, before most of the cache."""
+    g = torch.Generator().manual_seed(3 * m + G)
+    hkv, D, n, budget = 2, 64, 2000, 400
+    K, V = [ref.bf16(rnd(g, n, hkv, D)) for _ in range(2)], [ref.bf16(rnd(g, n, hkv, D)) for _ in range(2)]
+    c = make(M, K, V, [torch.arange(n)] * 2)
+    c.weight.copy_(torch.rand(c.weight.shape, generator=g))
+    dst = M.KV4Cache(np.arange(2 * 13).reshape(2, 13), 26, hkv, D, 32)
+    kept = c.evict(dst, budget, recent=20, sinks=4).long().cpu()
+    assert c.status() == 0
+    K = [torch.stack([K[r][kept[r, h], h] for h in range(hkv)], 1) for r in range(2)]
+    V = [torch.stack([V[r][kept[r, h], h] for h in range(hkv)], 1) for r in range(2)]
+    pos = [kept[r] for r in range(2)]
+    q = ref.bf16(rnd(g, 2 * m, hkv * G, D))
+    q_pos = [[(n if posd else budget) + i for i in range(m)]] * 2
+    for kw in (dict(window=150), dict(window=512), dict(start=[300, 0]), dict(start=[1000, 450], window=600)):
+        attend_and_observe(M, dst, K, V, pos, [m, m], q, G, q_pos, kw, posd=posd)
+
+
 # -------------------------------------------------- append from no source --
 
 def test_append_from_no_rows_at_all(M):

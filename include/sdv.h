@@ -629,9 +629,9 @@ int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride, int32_t n_
  * held slot t,
  *   weight_out = decay * weight + sum over rows and the query heads of the kv
  *                head of row_weight[row] exp(score - lse[row][q head]),
- * hidden keys and rows of lse -inf giving 0.  lse as sd_kv4_attn leaves it
- * (own keys included), row_weight fp32 [rows] (null: 1; the accepted rows' 1
- * and the others' 0 after a verified tree).  weight_out: laid out as
+ * hidden keys giving 0, and so rows whose lse is not finite (they see nothing,
+ * or a NaN).  lse as sd_kv4_attn leaves it (own keys included), row_weight fp32 [rows], finite (null: 1; the accepted rows' 1 and
+ * the others' 0 after a verified tree).  weight_out: laid out as
  * c->weight, may be c->weight itself.  The sums run in a fixed order (no
  * atomics).  Errors as sd_kv4_attn. */
 int sd_kv4_observe(const sd_kv4* c, const uint16_t* q, int64_t q_stride, int32_t n_q_heads, const float* lse,

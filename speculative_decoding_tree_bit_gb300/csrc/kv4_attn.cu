@@ -924,8 +924,13 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
         const int rho = pass * kObsRows + row;
         const bool ok = rho < rows;
         const int gq = ok ? rho / n : 0, node = ok ? s_node[rho - gq * n] : 0, hq = h * a.G + gq;
+        // a row that sees nothing, or whose lse is not finite, gives no weight:
+        // its queries (NaN, perhaps) are taken as 0 and its lse as infinite
+        const float lse = ok ? b.lse_in[(int64_t)(n0 + node) * a.hq + hq] : INFINITY;
+        const bool gives = fabsf(lse) < INFINITY;
         uint4 x = make_uint4(0, 0, 0, 0);
         if (ok) x = *reinterpret_cast<const uint4*>(a.q + (int64_t)(n0 + node) * a.q_stride + hq * D + oct * 8);
+        if (!gives) x = make_uint4(0, 0, 0, 0);
         const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
         float f[8], qs = 0.f, big = 0.f;
 #pragma unroll
@@ -945,10 +950,9 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
             make_uint4(pack_f16x2(f[0] * up, f[4] * up), pack_f16x2(f[1] * up4, f[5] * up4),
                        pack_f16x2(f[2] * up, f[6] * up), pack_f16x2(f[3] * up4, f[7] * up4));
         if (oct == 0) {
-          const float lse = ok ? b.lse_in[(int64_t)(n0 + node) * a.hq + hq] : -INFINITY;
-          s_row[row] = make_float4(pow2i(24 - e) * sc2, qs * sc2, lse == -INFINITY ? INFINITY : lse * kLog2e,
-                                   ok ? (b.row_weight ? b.row_weight[n0 + node] : 1.f) : 0.f);
-          s_bias[row] = make_float2(BIAS && a.s.slopes ? a.s.slopes[hq] : 0.f,
+          s_row[row] = make_float4(pow2i(24 - e) * sc2, qs * sc2, gives ? lse * kLog2e : INFINITY,
+                                   gives ? (b.row_weight ? b.row_weight[n0 + node] : 1.f) : 0.f);
+          s_bias[row] = make_float2(BIAS && a.s.slopes && gives ? a.s.slopes[hq] : 0.f,
                                     __int_as_float(a.row_pos ? a.row_pos[n0 + node] : ctx + node));
         }
       }

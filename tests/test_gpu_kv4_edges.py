@@ -166,6 +166,44 @@ def test_positions_after_an_eviction(M, m, G, posd):
         attend_and_observe(M, dst, K, V, pos, [m, m], q, G, q_pos, kw, posd=posd)
 
 
+# ------------------------------------------------------ NaN and its reach --
+
+@pytest.mark.parametrize("kw", [dict(), dict(window=40), dict(start=[30])])
+@pytest.mark.parametrize("m,G", [(3, 4), (33, 4)])
+def test_a_nan_row_gives_no_weight(M, m, G, kw):
+    """A bad own value leaves lse NaN in the row that sees it; the weights that
+    the other rows give stay, and the hidden keys' too."""
+    g = torch.Generator().manual_seed(m)
+    hkv, D, n = 2, 128, 120
+    K, V = ref.bf16(rnd(g, n, hkv, D)), ref.bf16(rnd(g, n, hkv, D))
+    c = make(M, [K], [V], [torch.arange(n)])
+    q, k, v = (ref.bf16(rnd(g, m, h, D)) for h in (hkv * G, hkv, hkv))
+    v[1, 0, 5] = math.nan
+    qd = dev(q)
+    qd[2, 1, 7] = math.inf  # and a query that is not finite
+    rows = M.RequestRows([0, m])
+    anc = torch.tensor([1 << i for i in range(m)], dtype=torch.int64).cuda()
+    qp = torch.full((m,), n, dtype=torch.int64)
+    score = M.KV4Score(window=kw.get("window", 0), start=i32(kw["start"]) if "start" in kw else None)
+    out, lse = c.attend(qd, rows, dev(k), dev(v), anc=anc, pos=i32(qp), score=score)
+    lse = lse.double().cpu()
+    assert torch.isnan(lse[1, :G]).all() and torch.isfinite(lse[1, G:]).all() and torch.isnan(lse[2, 1])
+    w0 = torch.rand(c.weight.shape, generator=g)
+    c.weight.copy_(w0)
+    got = c.observe(qd, lse.float().cuda(), rows, pos=i32(qp), score=score, decay=0.5)[0, :, :n].double().cpu()
+    want = 0.5 * w0[0, :, :n].double()
+    e_max = 0.0
+    for h in range(hkv * G):
+        _, _, z, _, _, e = expect(q[:, h], ref.values(K[:, h // G]), ref.values(V[:, h // G]), qp, torch.arange(n),
+                                  torch.ones(m, n, dtype=torch.bool), window=kw.get("window", 0),
+                                  start=kw["start"][0] if "start" in kw else None)
+        fine = torch.isfinite(lse[:, h])
+        want[h // G] += torch.exp(z[fine] - lse[fine, h][:, None]).sum(0)
+        e_max = max(e_max, e)
+    assert torch.isfinite(got).all()
+    assert ((got - want).abs() <= (e_max + 2.0 ** -18) * want).all()
+
+
 # -------------------------------------------------- append from no source --
 
 def test_append_from_no_rows_at_all(M):

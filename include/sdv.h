@@ -630,7 +630,8 @@ int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride, int32_t n_
  *   weight_out = decay * weight + sum over rows and the query heads of the kv
  *                head of row_weight[row] exp(score - lse[row][q head]),
  * hidden keys giving 0, and so rows whose lse is not finite (they see nothing,
- * or a NaN).  lse as sd_kv4_attn leaves it (own keys included), row_weight fp32 [rows], finite (null: 1; the accepted rows' 1 and
+ * or a NaN) and keys held as NaN.  lse as sd_kv4_attn leaves it (own keys
+ * included), row_weight fp32 [rows], finite (null: 1; the accepted rows' 1 and
  * the others' 0 after a verified tree).  weight_out: laid out as
  * c->weight, may be c->weight itself.  The sums run in a fixed order (no
  * atomics).  Errors as sd_kv4_attn. */

@@ -965,7 +965,7 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
         float old = 0.f;  // not looked at before the end
         if (t < ctx) old = pass ? w_out[t] : w_in[t];
         if (!kv4_wait(&bar[stage], (used / NS) & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(31));
-        const bool ok = s_ok[warp * NS + stage] != 0;
+        bool ok = s_ok[warp * NS + stage] != 0;  // of the slot that this lane writes
         uint32_t kw[4][D / 32];
         float ks[4], km[4];
         int kp[4];
@@ -982,6 +982,8 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
           const uint32_t w = *reinterpret_cast<const uint32_t*>(st + 16 * D + (8 * i + g) * 4);
           ks[i] = __uint_as_float(w << 16);
           km[i] = fmaf(-8.f, ks[i], __uint_as_float(w & 0xFFFF0000u));
+          // a key held as NaN collects nothing: who sees it has no finite lse
+          if (ks[i] != ks[i]) ks[i] = km[i] = 0.f, ok &= i != q;
           kp[i] = BIAS ? *reinterpret_cast<const int*>(st + kv4_half(D) + (8 * i + g) * 4) : 0;
         }
         __syncwarp();

@@ -204,6 +204,34 @@ def test_a_nan_row_gives_no_weight(M, m, G, kw):
     assert ((got - want).abs() <= (e_max + 2.0 ** -18) * want).all()
 
 
+# ------------------------------------------------------- keys held as NaN --
+
+def test_a_key_held_as_nan_collects_nothing(M):
+    """Seen by a row of weight 0 alone, or by a row whose lse it has made NaN."""
+    g = torch.Generator().manual_seed(4)
+    hkv, D, n = 1, 64, 64
+    K, V = ref.bf16(rnd(g, n, hkv, D)), ref.bf16(rnd(g, n, hkv, D))
+    bad = K.clone()
+    bad[20] = math.nan
+    c = make(M, [bad], [V], [torch.arange(n)])
+    q = ref.bf16(rnd(g, 3, 2, D))
+    rows, qp = M.RequestRows([0, 3]), torch.tensor([n - 20, n + 10, n + 12])
+    score = M.KV4Score(window=40)  # the first row sees key 20, the others do not
+    _, lse = c.attend(dev(q), rows, pos=i32(qp), score=score)
+    assert torch.isnan(lse[0]).all() and torch.isfinite(lse[1:]).all()
+    for weight in ([0.0, 1.0, 1.0], [1.0, 1.0, 0.5]):
+        got = c.observe(dev(q), lse, rows, pos=i32(qp), score=score, row_weight=torch.tensor(weight).cuda(),
+                        out=torch.zeros_like(c.weight))[0, 0, :n].double().cpu()
+        want = torch.zeros(n, dtype=torch.float64)
+        for h in range(2):
+            z, size = ref.scores(q[:, h], ref.values(K[:, 0]), qp, torch.arange(n), 1 / 8.0, window=40)
+            for r in (1, 2):
+                want += weight[r] * torch.exp(z[r] - float(lse[r, h]))
+        assert got[20] == 0 and torch.isfinite(got).all()
+        e = (D + 16) * 2.0 ** -24 * size + 2.0 ** -18
+        assert ((got - want).abs() <= e * want).all()
+
+
 # -------------------------------------------------- append from no source --
 
 def test_append_from_no_rows_at_all(M):

@@ -544,7 +544,9 @@ int sd_best_first_select(const int32_t* parents, const float* logprob, const int
  * slots held per request.  page_size is a multiple of 32, head_dim 64 or 128.
  *
  * Rows of a call: request r owns rows cu[r] .. cu[r+1]-1 (cu int32 [R+1] on
- * the device, the same values in cu_host).  A page id outside the pool or a
+ * the device, the same values in cu_host).  With no rows at all the rows'
+ * arrays may be null; sd_kv4_observe then fades the weights, the other calls do
+ * nothing.  A page id outside the pool or a
  * context beyond the capacity sets *status (device int32, caller-owned) to
  * SD_ERR_CAPACITY; such slots are neither read nor written.  Calls are
  * asynchronous on `stream`. */

@@ -508,7 +508,7 @@ extern "C" int sd_kv4_append(const sd_kv4* c, const uint16_t* k, const uint16_t*
   if (int rc = kv4_check(c, R, who, &view)) return rc;
   if (int rc = kv4_check_rows(cu, cu_host, R, who)) return rc;
   const int rows = cu_host[R];
-  if (!k || !v || !aligned16(k) || !aligned16(v)) return kv4_bad(SD_ERR_INVALID_ARG, who, "k and v must be set and 16-byte aligned");
+  if (rows && (!k || !v || !aligned16(k) || !aligned16(v))) return kv4_bad(SD_ERR_INVALID_ARG, who, "k and v must be set and 16-byte aligned");
   if (row_stride < (int64_t)c->n_kv_heads * c->head_dim || row_stride % 8)
     return kv4_bad(SD_ERR_INVALID_ARG, who, "row_stride must cover a row and be a multiple of 8");
   if (n_src < 0 || (!src && n_src < rows)) return kv4_bad(SD_ERR_INVALID_ARG, who, "fewer rows in k and v than in cu");
@@ -532,10 +532,10 @@ extern "C" int sd_kv4_read(const sd_kv4* c, const int32_t* cu, const int32_t* cu
   Kv4View view;
   if (int rc = kv4_check(c, R, who, &view)) return rc;
   if (int rc = kv4_check_rows(cu, cu_host, R, who)) return rc;
-  if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
-    return kv4_bad(SD_ERR_INVALID_ARG, who, "k_out and v_out must be set and 16-byte aligned");
   const int rows = cu_host[R];
   if (rows == 0) return SD_OK;
+  if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
+    return kv4_bad(SD_ERR_INVALID_ARG, who, "k_out and v_out must be set and 16-byte aligned");
   const dim3 grid((rows + 7) / 8, (c->n_kv_heads + kHeads - 1) / kHeads);
   auto kern = c->head_dim == 128 ? k_kv4_read<128> : k_kv4_read<64>;
   kern<<<grid, 256, 0, (cudaStream_t)stream>>>(view, cu, R, rows, at, k_out, v_out, status);

@@ -1120,7 +1120,8 @@ static int check_call(const char* who, const sd_kv4* c, const uint16_t* q, int64
   if (int rc = kv4_check(c, R, who, &a->c)) return rc;
   if (int rc = kv4_check_rows(cu, cu_host, R, who)) return rc;
   if (int rc = kv4_check_score(score, who, &a->s, c->head_dim)) return rc;
-  if (!q || (reinterpret_cast<uintptr_t>(q) & 15)) return kv4_bad(SD_ERR_INVALID_ARG, who, "q must be set and 16-byte aligned");
+  if (cu_host[R] && (!q || (reinterpret_cast<uintptr_t>(q) & 15)))
+    return kv4_bad(SD_ERR_INVALID_ARG, who, "q must be set and 16-byte aligned");
   if (hq < c->n_kv_heads || hq % c->n_kv_heads)
     return kv4_bad(SD_ERR_INVALID_ARG, who, "n_q_heads must be a multiple of n_kv_heads");
   if (hq / c->n_kv_heads > 16) return kv4_bad(SD_ERR_UNSUPPORTED, who, "at most 16 query heads a kv head");
@@ -1160,6 +1161,8 @@ extern "C" int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride,
   const char* who = "sd_kv4_attn";
   Kv4AttnArgs a = {};
   if (int rc = check_call(who, c, q, q_stride, n_q_heads, cu, cu_host, R, score, max_ctx, &a)) return rc;
+  const int rows = cu_host[R];
+  if (rows == 0) return SD_OK;  // the arrays of no rows may be null
   if (!out || (reinterpret_cast<uintptr_t>(out) & 15)) return kv4_bad(SD_ERR_INVALID_ARG, who, "out must be set and 16-byte aligned");
   if (!k_new != !v_new) return kv4_bad(SD_ERR_INVALID_ARG, who, "k_new and v_new go together");
   if (k_new) {
@@ -1168,12 +1171,10 @@ extern "C" int sd_kv4_attn(const sd_kv4* c, const uint16_t* q, int64_t q_stride,
       return kv4_bad(SD_ERR_INVALID_ARG, who,
                      "k_new and v_new must be 16-byte aligned, kv_stride must cover a row and be a multiple of 8");
   }
-  const int rows = cu_host[R];
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return kv4_bad(SD_ERR_INVALID_ARG, who, "workspace must be set and 256-byte aligned");
   if (workspace_bytes < sd_kv4_attn_workspace(R, rows, n_q_heads, c->n_kv_heads, c->head_dim))
     return kv4_bad(SD_ERR_WORKSPACE, who, "workspace too small");
-  if (rows == 0) return SD_OK;
   a.k_new = k_new;
   a.v_new = v_new;
   a.kv_stride = kv_stride;
@@ -1202,7 +1203,7 @@ extern "C" int sd_kv4_observe(const sd_kv4* c, const uint16_t* q, int64_t q_stri
   const char* who = "sd_kv4_observe";
   Kv4ObserveArgs b = {};
   if (int rc = check_call(who, c, q, q_stride, n_q_heads, cu, cu_host, R, score, max_ctx, &b.a)) return rc;
-  if (!lse) return kv4_bad(SD_ERR_INVALID_ARG, who, "null lse");
+  if (!lse && cu_host[R]) return kv4_bad(SD_ERR_INVALID_ARG, who, "null lse");
   if (!weight_out || (reinterpret_cast<uintptr_t>(weight_out) & 15))
     return kv4_bad(SD_ERR_INVALID_ARG, who, "weight_out must be set and 16-byte aligned");
   if (!(decay >= 0.f) || !(decay <= 1e30f)) return kv4_bad(SD_ERR_INVALID_ARG, who, "decay must be finite and not negative");

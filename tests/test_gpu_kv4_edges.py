@@ -232,6 +232,31 @@ def test_a_key_held_as_nan_collects_nothing(M):
         assert ((got - want).abs() <= e * want).all()
 
 
+# ----------------------------------------------------- calls without rows --
+
+def test_calls_without_rows(M):
+    g = torch.Generator().manual_seed(1)
+    K, V = [ref.bf16(rnd(g, 70, 2, 64)), ref.bf16(rnd(g, 3, 2, 64))], [ref.bf16(rnd(g, 70, 2, 64)), ref.bf16(rnd(g, 3, 2, 64))]
+    c = make(M, K, V, [torch.arange(70), torch.arange(3)])
+    none = M.RequestRows([0, 0, 0])
+    kv, q = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    before = c.blocks.clone()
+    c.append(kv, kv, none)
+    assert c.ctx_len.tolist() == [70, 3] and torch.equal(before, c.blocks)
+    k, v = c.read(none)
+    assert k.shape == v.shape == (0, 2, 64)
+    out, lse = c.attend(q, none, kv, kv)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    out, lse = c.attend(q, none)
+    for score in (None, M.KV4Score(window=5)):
+        w0 = torch.rand_like(c.weight)
+        c.weight.copy_(w0)
+        c.observe(q, lse, none, decay=0.25, score=score)  # the weights fade all the same
+        assert c.status() == 0
+        for r, n in enumerate((70, 3)):
+            assert torch.equal(c.weight[r, :, :n], 0.25 * w0[r, :, :n]) and torch.equal(c.weight[r, :, n:], w0[r, :, n:])
+
+
 # -------------------------------------------------- append from no source --
 
 def test_append_from_no_rows_at_all(M):

@@ -106,3 +106,15 @@ def test_the_workspace_is_made_on_the_calls_stream(M, monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     d = c._workspace("attn", None, size, 9000)
     assert d[1] not in (a[1],) and c._workspace("attn", None, size, 9000) is d
+
+
+def test_calls_without_rows_take_null_arrays(M):
+    """As an empty tensor's pointer is."""
+    import ctypes
+    ptr, L = 4096, sdv.lib()
+    c, cu = sdv.KV4(ptr, ptr, ptr, 8, 64, 2, 128, ptr, 4, ptr), np.array([0, 0, 0], np.int32)
+    b, h = ctypes.byref(c), cu.ctypes.data
+    assert L.sd_kv4_append(b, None, None, 256, 0, ptr, h, 2, None, None, None, None, None, None) == 0
+    assert L.sd_kv4_read(b, ptr, h, 2, None, None, None, None, None) == 0
+    assert L.sd_kv4_attn(b, None, 512, 4, ptr, h, 2, None, None, 0, None, None, None, 0, None, None, ptr, 1 << 24, None,
+                         None) == 0

@@ -548,7 +548,9 @@ int sd_best_first_select(const int32_t* parents, const float* logprob, const int
  * arrays may be null; sd_kv4_observe then fades the weights, the other calls do
  * nothing.  A page id outside the pool or a
  * context beyond the capacity sets *status (device int32, caller-owned) to
- * SD_ERR_CAPACITY; such slots are neither read nor written.  Calls are
+ * SD_ERR_CAPACITY; such slots are neither read nor written.  (sd_kv4_read gives
+ * NaN for them, and a slot that sd_kv4_evict keeps of such a page is held as NaN
+ * in dst.)  Calls are
  * asynchronous on `stream`. */
 typedef struct {
   uint8_t* blocks;

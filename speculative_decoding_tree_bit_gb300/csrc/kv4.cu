@@ -189,16 +189,15 @@ __global__ void __launch_bounds__(256) k_kv4_read(Kv4View c, const int32_t* __re
   const int r = request_of(cu, R, e);
   const int64_t t64 = (int64_t)(at ? at[r] : 0) + e - cu[r];
   const uint8_t* rec = t64 >= 0 && t64 < c.cap ? c.record(D, r, h0, (int)(t64 / kKvGroup)) : nullptr;
-  if (!rec) {
-    if (lane == 0) set_status(status, SD_ERR_CAPACITY);
-    return;
-  }
+  if (!rec && lane == 0) set_status(status, SD_ERR_CAPACITY);
   const int t = (int)t64;
   const int b = half ? kv4_vbyte<D>(t, l * (kV / 2)) : l * (kV / 2);
   uint32_t word[kHeads], sm[kHeads];
 #pragma unroll
   for (int i = 0; i < kHeads; i++)
-    if (i < nh) {
+    if (!rec) {
+      word[i] = 0, sm[i] = 0x7FC07FC0u;  // no such slot: NaN
+    } else if (i < nh) {
       const uint8_t* part = rec + (int64_t)i * c.gpp * kv4_rec(D) + half * kv4_half(D);
       const uint8_t* codes = part + (t & 31) * (D / 2) + b;
       word[i] = kV == 8 ? *reinterpret_cast<const uint32_t*>(codes) : *reinterpret_cast<const uint16_t*>(codes);
@@ -390,6 +389,7 @@ __global__ void __launch_bounds__(256) k_kv4_move(Kv4View s, Kv4View d, int budg
   bool ok[32 / kKeys];
 #pragma unroll
   for (int half = 0; half < 2; half++) {
+    sm[half] = 0x7FC07FC0u;  // a kept row whose page is not there is held as NaN, whatever dst's record held
     if (src) sm[half] = *reinterpret_cast<const uint32_t*>(src + half * kv4_half(D) + 16 * D + (from & 31) * 4);
 #pragma unroll
     for (int i = 0; i < 32 / kKeys; i++) {
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(256) k_kv4_move(Kv4View s, Kv4View d, int budg
   }
 #pragma unroll
   for (int half = 0; half < 2; half++) {
-    if (src) *reinterpret_cast<uint32_t*>(dst + half * kv4_half(D) + 16 * D + lane * 4) = sm[half];
+    if (t < kept) *reinterpret_cast<uint32_t*>(dst + half * kv4_half(D) + 16 * D + lane * 4) = sm[half];
 #pragma unroll
     for (int i = 0; i < 32 / kKeys; i++) {
       const int j = i * kKeys + lane / kCh, ch = lane % kCh;

@@ -277,6 +277,30 @@ def test_append_from_no_rows_at_all(M):
     assert c.status() == 7 and torch.equal(before, c.blocks)
 
 
+# -------------------------------------------------------------- bad pages --
+
+def test_a_row_of_a_bad_page_is_nan_after_an_eviction_and_when_read(M):
+    """Not what the destination's page held before, which may be another request's."""
+    g = torch.Generator().manual_seed(13)
+    K, V = [ref.bf16(rnd(g, 200, 2, 128))], [ref.bf16(rnd(g, 200, 2, 128))]
+    c = make(M, K, V, [torch.arange(200)])
+    dst = make(M, [ref.bf16(rnd(g, 128, 2, 128))], [ref.bf16(rnd(g, 128, 2, 128))], [torch.arange(128)])
+    c.page_table[0, 4] = -4  # slots 128 .. 159
+    kept = c.evict(dst, 100, recent=100)
+    assert c.status() == 7
+    k, v = dst.read(M.RequestRows([0, 100]))
+    want = (kept[0].t() >= 128) & (kept[0].t() < 160)
+    assert want.any() and not want.all()
+    assert torch.equal(torch.isnan(k).all(-1), want) and torch.equal(torch.isnan(v).all(-1), want)
+    assert torch.equal(torch.isnan(k).any(-1), want) and torch.equal(torch.isnan(v).any(-1), want)
+    k, v = c.read(M.RequestRows([0, 200]))
+    assert c.status() == 7
+    want = (torch.arange(200) >= 128) & (torch.arange(200) < 160)
+    for x in (k, v):
+        assert torch.equal(torch.isnan(x).flatten(1).all(1).cpu(), want)
+        assert torch.equal(torch.isnan(x).flatten(1).any(1).cpu(), want)
+
+
 # ----------------------------------------------------- streams and graphs --
 
 @pytest.mark.parametrize("m", [4, 40])

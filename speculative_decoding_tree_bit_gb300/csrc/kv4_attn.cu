@@ -21,11 +21,13 @@ namespace sdv {
 // (a sum over many keys would lose what the offset 8 sum(p s) cancels):
 // output = sum (p s)(c - 8) + sum p m.  Queries are bf16, exact in fp16 after
 // a power of two that brings a row's greatest value below 2^15 (values
-// 2^-31 of it and less lose bits).  A weight p s enters as one fp16 term
+// 2^-27 of it and less lose bits).  A weight p s enters as one fp16 term
 // with 11 bits, 2^-12 of its value against the 2^-9 of the output's own
-// rounding; a power of two that follows the greatest s keeps it at most 2^13,
-// so weights down to 2^-38 of the greatest count.  The rows' own keys and
-// values are bf16 products, their weights two bf16 terms.
+// rounding.  p's reference follows the row's scores plus the exponents of the
+// values that it sees (a unit's greatest for all of its keys where they are
+// within 2^6), so weights down to 2^-16 of the row's greatest keep their bits,
+// down to 2^-26 count, and no value that a row does not see moves them.  The
+// rows' own keys and values are bf16 products, their weights two bf16 terms.
 //
 // A warp works on its own: it takes every W-th unit of the CTA's segment, and
 // keeps a ring of two 32-slot records, one bulk copy each, filled a unit
@@ -36,13 +38,13 @@ namespace sdv {
 // segments' units are dealt evenly over the CTAs, whatever the requests'
 // lengths; two CTAs an SM, so that one works while the other joins.
 //
-// Measured, 32 query and 8 kv heads, D = 128: 32 tokens over 1500 to 8192 keys 58
-// us, 3.0 TB/s (the ALU pipe 46% busy, issue 50%); 32 chains of 8 rows over 1024
-// to 4096 keys with a cap 92 us, 103 TFLOP/s (two tiles of rows a warp, six
+// Measured, 32 query and 8 kv heads, D = 128: 32 tokens over 1500 to 8192 keys 50
+// us, 3.5 TB/s; 32 chains of 8 rows over 1024 to 4096 keys with a cap 90 us, 105 TFLOP/s (two tiles of rows a warp, six
 // warps; four tiles, four warps: 135 where two took 110); a tree of 16 over 2048
 // keys 25 us, most of it latency.
 
 constexpr int kMaxCtas = 512;
+constexpr float kUnset = 3e38f;  // a row's reference before it sees a key
 
 template <int D, int NT, int W>
 struct AttnShape {
@@ -211,44 +213,52 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
       }
     }
     __syncthreads();
+    // Of a lane's two rows: l, mv, o are sums of p = 2^(x + ref), p m and p s (c -
+    // 8) 2^-9 over the keys so far, x their scores.  11 - ref is the greatest x
+    // + E so far, give or take: a value row's magnitudes lie below 2^(E + 1).  One
+    // reference for all three, so that p s fits fp16 and only what a row sees moves it
     float o[NT][KK][4];
-    float mx[NT][2];
-    uint64_t l[NT], mv[NT], fac[NT], qs[NT];  // of a lane's two rows
+    uint64_t l[NT], mv[NT], fac[NT], qs[NT], ref[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
 #pragma unroll
       for (int t = 0; t < KK; t++) o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
-      mx[nt][0] = mx[nt][1] = -INFINITY;
+      ref[nt] = f2pack(kUnset, kUnset);
       l[nt] = mv[nt] = 0;
       fac[nt] = f2pack(s_fac[nt * 8 + 2 * q], s_fac[nt * 8 + 2 * q + 1]);
       qs[nt] = f2pack(s_qs[nt * 8 + 2 * q], s_qs[nt * 8 + 2 * q + 1]);
     }
-    // values' weights are p s vup: vup 2^13 over the power of two at or above
-    // the greatest s so far (bits vtop), which leaves o short by vup 2^-9
-    float vup = 512.f;
-    uint32_t vtop = 0;
 
-    float sc[2][NT][4];  // scores (base 2), then weights, of keys 16 i + g, 16 i + g + 8
-    // a greater maximum anywhere in the warp rescales what it has so far
-    auto grow = [&](const float (&top)[NT][2]) {
-      bool grows = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; nt++) grows |= top[nt][0] > mx[nt][0] || top[nt][1] > mx[nt][1];
-      if (!__any_sync(0xffffffffu, grows)) return;
+    float sc[2][NT][4];  // scores (base 2) of keys 16 i + g, 16 i + g + 8
+    // p s < 2^(x + E + ref - 2) has to stay below 2^15: a lane's greatest x + E
+    // past 17 - ref, anywhere in the warp, rescales what it has so far
+    auto over = [&](const float (&top)[NT][2], float ev) {
+      bool any = false;
 #pragma unroll
       for (int nt = 0; nt < NT; nt++) {
-        float al[2];
+        float r0, r1;
+        f2unpack(ref[nt], r0, r1);
+        any |= top[nt][0] + r0 > 17.f - ev || top[nt][1] + r1 > 17.f - ev;
+      }
+      return __any_sync(0xffffffffu, any) != 0;
+    };
+    auto grow = [&](const float (&top)[NT][2]) {  // top: a lane's greatest x + E
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) {
+        float al[2], r[2];
+        f2unpack(ref[nt], r[0], r[1]);
 #pragma unroll
         for (int e = 0; e < 2; e++) {
           float t = top[nt][e];
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-          const float mn = fmaxf(mx[nt][e], t);
-          al[e] = mn == -INFINITY ? 1.f : ex2(mx[nt][e] - mn);
-          mx[nt][e] = mn;
+          const float rn = fminf(r[e], 11.f - t);
+          al[e] = ex2(rn - r[e]);
+          r[e] = rn;
         }
         const uint64_t al2 = f2pack(al[0], al[1]);
+        ref[nt] = f2pack(r[0], r[1]);
         l[nt] = f2mul(l[nt], al2);
         mv[nt] = f2mul(mv[nt], al2);
 #pragma unroll
@@ -260,6 +270,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
         }
       }
     };
+    auto exponent = [](float x) { return fmaxf((float)((int)(__float_as_uint(x) >> 23) - 127), -90.f); };  // of x >= 0
 
     // the rows' own keys, in runs of 32, 16 at a time
     for (int u = ua + warp; u < min(ub, rq.no); u += W)
@@ -308,21 +319,17 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
             seen |= (uint32_t)(so[nt][e] != -INFINITY) << (4 * nt + e) | (uint32_t)(so[nt][2 + e] != -INFINITY) << (4 * nt + 2 + e);
             top[nt][e] = fmaxf(so[nt][e], so[nt][2 + e]);
           }
-        grow(top);
-        const float wup = vup * (1.f / 512.f);
+        if (over(top, 0.f)) grow(top);  // E counted as 0
         uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
           for (int i = 0; i < 2; i++) {
-            float p[2];
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-              p[e] = ex2(so[nt][2 * i + e] - (mx[nt][e] == -INFINITY ? 0.f : mx[nt][e]));
-              so[nt][2 * i + e] = p[e] * wup;
-            }
-            l[nt] = f2add(l[nt], f2pack(p[0], p[1]));
-            const float w0 = so[nt][2 * i], w1 = so[nt][2 * i + 1];
+            float p[2], w0, w1;
+            f2unpack(f2add(f2pack(so[nt][2 * i], so[nt][2 * i + 1]), ref[nt]), p[0], p[1]);
+            const uint64_t pp = f2pack(ex2(p[0]), ex2(p[1]));
+            l[nt] = f2add(l[nt], pp);
+            f2unpack(f2mul(pp, f2pack(1.f / 512.f, 1.f / 512.f)), w0, w1);
             const uint32_t hi = pack_bf16x2(w0, w1);
             const uint32_t lo = pack_bf16x2(w0 - __uint_as_float(hi << 16), w1 - __uint_as_float(hi & 0xFFFF0000u));
             ph[nt][i] = transpose8(hi);
@@ -381,6 +388,52 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
         }
       }
 
+    // The own rows' E was counted as 0.  Where all of a row's sums are small (two
+    // of its tiles mostly say that they are not), its reference goes up again
+    if (a.k_new && ua + warp < min(ub, rq.no)) {
+      uint32_t fine = 15;
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          const float big = fmaxf(fmaxf(fabsf(o[nt][0][e]), fabsf(o[nt][0][2 + e])), fmaxf(fabsf(o[nt][1][e]), fabsf(o[nt][1][2 + e])));
+          const bool none = __uint_as_float((uint32_t)(ref[nt] >> (32 * e))) == kUnset;  // a row that sees no own key
+          uint32_t rows = __ballot_sync(0xffffffffu, big > 0.0625f || none);
+          rows |= rows >> 16;
+          rows |= rows >> 8;
+          fine &= rows | rows >> 4;
+        }
+      if (fine != 15) {
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+          float up[2];
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            float big = 0.f;
+#pragma unroll
+            for (int t = 0; t < KK; t++) big = fmaxf(big, fmaxf(fabsf(o[nt][t][e]), fabsf(o[nt][t][2 + e])));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 4));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 8));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 16));
+            up[e] = fmaxf(-exponent(big), 0.f);
+          }
+          float r0, r1;
+          f2unpack(ref[nt], r0, r1);
+          ref[nt] = f2pack(r0 + up[0], r1 + up[1]);
+          up[0] = ex2(up[0]);
+          up[1] = ex2(up[1]);
+          l[nt] = f2mul(l[nt], f2pack(up[0], up[1]));
+#pragma unroll
+          for (int t = 0; t < KK; t++) {
+            o[nt][t][0] *= up[0];
+            o[nt][t][1] *= up[1];
+            o[nt][t][2] *= up[0];
+            o[nt][t][3] *= up[1];
+          }
+        }
+      }
+    }
+
     int k = 0;
     for (int u = first_record(); u < ub; u += W) {
       const int stage = used & 1;
@@ -423,7 +476,8 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
       float vs[4], vm[4];
       int kp[4];
       float top[NT][2];
-      uint32_t vb = 0, nan = 0;
+      float vb = 0.f;
+      uint32_t nan = 0;
 #pragma unroll
       for (int nt = 0; nt < NT; nt++) top[nt][0] = top[nt][1] = -INFINITY;
 #pragma unroll
@@ -438,7 +492,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
         vm[i] = in ? __uint_as_float(vw & 0xFFFF0000u) : 0.f;
         // a value row held as NaN: 0 here, and the sum of whoever sees it NaN below
         if (vs[i] != vs[i]) vs[i] = vm[i] = 0.f, nan |= 1u << i;
-        vb = max(vb, __float_as_uint(vs[i]));
+        vb = fmaxf(vb, fmaf(8.f, vs[i], fabsf(vm[i])));
         kp[i] = BIAS ? *reinterpret_cast<const int*>(st + kv4_rec(D) + kl * 4) : 0;
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
@@ -472,18 +526,28 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
             top[nt][e] = fmaxf(top[nt][e], x);
           }
         }
-      grow(top);
-      if (__any_sync(0xffffffffu, vb > vtop)) {
-        const uint32_t b = __reduce_max_sync(0xffffffffu, vb);
-        vtop = b | 0x007FFFFFu;  // up to the next power of two
-        const float up = pow2i(min(max(13 + 126 - (int)(b >> 23), -100), 100)), ratio = up / vup;
-        vup = up;
+      if (over(top, exponent(vb))) {
+        float least = 3e38f;  // of the unit's magnitudes other than 0
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++)
+        for (int i = 0; i < 4; i++)
+          if (vs[i] != 0.f || vm[i] != 0.f) least = fminf(least, fmaf(8.f, vs[i], fabsf(vm[i])));
+        const float hi = exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vb)))),
+                    lo = exponent(__uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(least))));
+        if (__builtin_expect(hi - lo <= 6.f, 1)) {  // E of the unit's greatest for all
 #pragma unroll
-          for (int t = 0; t < KK; t++)
+          for (int nt = 0; nt < NT; nt++) top[nt][0] += hi, top[nt][1] += hi;
+        } else {
 #pragma unroll
-            for (int e = 0; e < 4; e++) o[nt][t][e] *= ratio;
+          for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              top[nt][e] = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 4; i++)
+                top[nt][e] = fmaxf(top[nt][e], sc[i >> 1][nt][2 * (i & 1) + e] + exponent(fmaf(8.f, vs[i], fabsf(vm[i]))));
+            }
+        }
+        grow(top);
       }
       if (__any_sync(0xffffffffu, nan != 0)) {
 #pragma unroll
@@ -500,17 +564,15 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
       uint32_t pf[NT][2][2];
 #pragma unroll
       for (int nt = 0; nt < NT; nt++) {
-        const uint64_t ms = f2pack(mx[nt][0] == -INFINITY ? 0.f : -mx[nt][0], mx[nt][1] == -INFINITY ? 0.f : -mx[nt][1]);
 #pragma unroll
         for (int i = 0; i < 4; i++) {
           const float* x = sc[i >> 1][nt] + 2 * (i & 1);
-          const float vsu = vs[i] * vup;
           float p[2], w[2];
-          f2unpack(f2add(f2pack(x[0], x[1]), ms), p[0], p[1]);
+          f2unpack(f2add(f2pack(x[0], x[1]), ref[nt]), p[0], p[1]);
           const uint64_t pp = f2pack(ex2(p[0]), ex2(p[1]));
           l[nt] = f2add(l[nt], pp);
           mv[nt] = f2fma(pp, f2pack(vm[i], vm[i]), mv[nt]);
-          f2unpack(f2mul(pp, f2pack(vsu, vsu)), w[0], w[1]);
+          f2unpack(f2mul(pp, f2pack(vs[i], vs[i])), w[0], w[1]);
           pf[nt][i >> 1][i & 1] = transpose8(pack_f16x2(w[0], w[1]));
         }
       }
@@ -579,7 +641,6 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
     }
 
     // join the warps
-    const float down = 512.f / vup;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -592,7 +653,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
         }
         const int row = nt * 8 + 2 * q + e;
         if (g == 0) {
-          s_m[warp * RT + row] = mx[nt][e];
+          s_m[warp * RT + row] = -__uint_as_float((uint32_t)(ref[nt] >> (32 * e)));
           s_l[warp * RT + row] = le;
         }
         // float pairs [dims 2t, 2t + 1 of lane group g]: 8 t + g, rows 4 banks
@@ -600,7 +661,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
         float2* dst = reinterpret_cast<float2*>(s_o) + (warp * RT + row) * S::kPairs + g;
 #pragma unroll
         for (int t = 0; t < KK; t++)
-          dst[8 * t] = make_float2(fmaf(o[nt][t][e], down, mve), fmaf(o[nt][t][2 + e], down, mve));
+          dst[8 * t] = make_float2(fmaf(o[nt][t][e], 512.f, mve), fmaf(o[nt][t][2 + e], 512.f, mve));
       }
     __syncthreads();
     float* part = a.part + (int64_t)slot * (RT * (D + 2));  // [RT][D/2] pairs, then [RT] (max, sum)

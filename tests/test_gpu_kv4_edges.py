@@ -232,6 +232,93 @@ def test_a_key_held_as_nan_collects_nothing(M):
         assert ((got - want).abs() <= e * want).all()
 
 
+# ----------------------------------------- values of very different sizes --
+
+def check_values(M, K, V, q, k, v, G, anc, pos=None, start=None, page=32):
+    """One request, against the definition with the tolerance above."""
+    n, hkv, D = K.shape
+    m = q.shape[0]
+    kp = torch.arange(n) if pos is None else pos
+    qp = torch.full((m,), int(kp[-1]) + 1 if n else 0, dtype=torch.int64)
+    c = make(M, [K], [V], [kp], page=page)
+    score = M.KV4Score(start=i32([start])) if start is not None else None
+    ancd = torch.tensor([a - (1 << 64) if a >> 63 else a for a in anc], dtype=torch.int64).cuda()
+    out, lse = c.attend(dev(q), M.RequestRows([0, m]), dev(k), dev(v), anc=ancd, pos=i32(qp), score=score)
+    assert c.status() == 0
+    out, lse = out.double().cpu(), lse.double().cpu()
+    own = torch.tensor([[bool(a >> j & 1) for j in range(m)] for a in anc])
+    for h in range(hkv * G):
+        Kh = torch.cat([ref.values(K[:, h // G]), k[:, h // G]])
+        Vh = torch.cat([ref.values(V[:, h // G]), v[:, h // G]])
+        sees = torch.cat([torch.ones(m, n, dtype=torch.bool), own], 1)
+        want, l, _, _, tol, e = expect(q[:, h], Kh, Vh, qp, torch.cat([kp, qp]), sees, start=start)
+        compare(out[:, h], lse[:, h], want, l, tol, e, (h,))
+
+
+SHAPES = [(1, 4, 128), (6, 4, 128), (7, 2, 64)]
+
+
+@pytest.mark.parametrize("m,G,D", SHAPES)
+def test_values_from_2_to_the_minus_14_to_2_to_the_14(M, m, G, D):
+    g = torch.Generator().manual_seed(m * G)
+    n, hkv = 333, 2
+    K, k = ref.bf16(rnd(g, n, hkv, D)), ref.bf16(rnd(g, m, hkv, D))
+    size = lambda r: torch.exp2((28 * torch.rand(r, hkv, 1, generator=g, dtype=torch.float64) - 14).round())  # noqa: E731
+    V, v = ref.bf16(rnd(g, n, hkv, D) * size(n)), ref.bf16(rnd(g, m, hkv, D) * size(m))
+    anc = [(1 << i) | 1 for i in range(m)]
+    check_values(M, K, V, ref.bf16(2 * rnd(g, m, hkv * G, D)), k, v, G, anc)
+
+
+@pytest.mark.parametrize("m,G,D", SHAPES)
+@pytest.mark.parametrize("where", ["own", "cached", "both"])
+@pytest.mark.parametrize("huge", [1e30, 2.0 ** 20])
+def test_a_huge_value_that_no_row_or_one_row_sees(M, m, G, D, where, huge):
+    """A draft row that is nobody's ancestor but its own (its output is its
+    affair), and cached keys before the document, leave the others as they are."""
+    g = torch.Generator().manual_seed(m + G)
+    n, hkv = 290, 2
+    K, k = ref.bf16(rnd(g, n, hkv, D)), ref.bf16(rnd(g, m, hkv, D))
+    V, v = ref.bf16(rnd(g, n, hkv, D)), ref.bf16(rnd(g, m, hkv, D))
+    if where != "cached":
+        v[m - 1] *= huge
+    if where != "own":
+        V[3], V[70], V[99] = V[3] * huge, V[70] * huge, V[99] * -huge
+    anc = [(1 << i) | 1 for i in range(m)]
+    check_values(M, K, ref.bf16(V), ref.bf16(1.5 * rnd(g, m, hkv * G, D)), k, ref.bf16(v), G, anc,
+                 start=100 if where != "own" else None)
+
+
+@pytest.mark.parametrize("m,G,D", SHAPES)
+def test_a_large_value_of_little_weight(M, m, G, D):
+    """Seen, but with a weight that makes it count as little as the others."""
+    g = torch.Generator().manual_seed(m + 3 * G)
+    n, hkv = 160, 1
+    V, v = ref.bf16(rnd(g, n, hkv, D)), ref.bf16(rnd(g, m, hkv, D))
+    q = torch.zeros(m, G, D, dtype=torch.float64)
+    q[..., 0] = 16.0
+    K, k = 0.01 * rnd(g, n, hkv, D), 0.01 * rnd(g, m, hkv, D)
+    K[77, 0, 0] = k[0, 0, 0] = -0.69 * 24 * math.sqrt(D) / 16  # a weight of 2^-24
+    V[77] *= 2.0 ** 22
+    v[0] *= 2.0 ** 22
+    check_values(M, ref.bf16(K), ref.bf16(V), q, ref.bf16(k), ref.bf16(v), G, [(1 << i) | 1 for i in range(m)])
+
+
+@pytest.mark.parametrize("m,G,D", [(6, 4, 128)])
+def test_values_of_zero_and_of_one_size(M, m, G, D):
+    """Rows of zeros, constant rows, and rows near the least and greatest sizes."""
+    g = torch.Generator().manual_seed(m + 5 * G)
+    n, hkv = 200, 1
+    K, k = ref.bf16(rnd(g, n, hkv, D)), ref.bf16(rnd(g, m, hkv, D))
+    q = ref.bf16(rnd(g, m, G, D))
+    anc = [(2 << i) - 1 for i in range(m)]
+    V, v = torch.zeros(n, hkv, D, dtype=torch.float64), torch.zeros(m, hkv, D, dtype=torch.float64)
+    check_values(M, K, V, q, k, v, G, anc)
+    V[40:90], v[2] = 3.0, -0.5
+    check_values(M, K, V, q, k, v, G, anc)
+    for size in (2.0 ** -80, 2.0 ** 80):
+        check_values(M, K, ref.bf16(size * rnd(g, n, hkv, D)), q, k, ref.bf16(size * rnd(g, m, hkv, D)), G, anc)
+
+
 # ----------------------------------------------------- calls without rows --
 
 def test_calls_without_rows(M):

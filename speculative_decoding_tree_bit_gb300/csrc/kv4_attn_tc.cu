@@ -9,17 +9,22 @@
 //  * 16: records into a ring of eight, one bulk copy each;
 //  * 0..3 and 4..7: nibbles to fp16 operands, K's and V's.
 //    K's codes as they are (subnormal code 2^-24; the key's scale and middle
-//    are applied to its score, as in the warp kernel); V's as values, s (code -
-//    8) + m in one fp16 multiply-add per pair, times a power of two that
-//    follows the greatest value (11 bits, against the output's 8).  The rows'
-//    own keys are a tile of 64 in the same form, bf16 to fp16 after a power of
-//    two per key;
+//    are applied to its score, as in the warp kernel); V's as values, s code + (m
+//    - 8 s) in one fp16 multiply-add per pair after a power of two, 2^-E for all
+//    keys of the unit (11 bits of the value and of m - 8 s, against the output's
+//    8).  The rows' own keys are a tile of 64 in the same form, bf16 to fp16 after a
+//    power of two, per key for K;
 //  * 17: the products;
 //  * 8..15: softmax, a thread per row: the scores of 64 keys from TMEM, maximum,
-//    exponentials, P back.  The running maximum may lag by 2^8 before O is
-//    rescaled in TMEM (fp16 P: exponentials are taken 2^5 up, at most 2^13).
+//    exponentials, P back.  A row's reference, its greatest score + E, may lag by
+//    2^6 before O is rescaled in TMEM (fp16 P: exponentials are taken 2^9 up, at
+//    most 2^15).  So weights down to 2^-17 of the row's greatest p |v| keep their 11
+//    bits, down to 2^-28 count.  A unit whose values differ in size by more than
+//    2^6 holds no keys for the products: the same warps take it by fp32
+//    multiply-adds, after the run of 64 units that it lies in (a unit of 160
+//    rows 11 us).  So nothing that a row does not see moves its weights or values.
 // (18 and 19 do nothing: they complete a warpgroup.  Registers a scheduler:
-// 5 warps x 96 = 2 x 64 decoding + 2 x 152 softmax + 48.)
+// 5 warps x 96 = 2 x 72 decoding + 2 x 144 softmax + 48.)
 // WIDE: the first rows of a segment are tile 0's, the others tile 1's, up to
 // 256.  Not WIDE (at most 128 rows a segment): both tiles hold the same rows and
 // take alternate key tiles.  With at most 64 (32) rows a tile holds them twice
@@ -48,6 +53,9 @@ constexpr int kSoft = 8, kLoad = 16, kMma = 17, kThreads = 20 * 32, kSoftThreads
 constexpr int kRaw = 8;
 constexpr int kRows = 256;  // of a segment, at most
 constexpr int kJoins = 4;   // segments of a (request, kv head), at most: 64 rows x 16 heads
+constexpr int kUp = -5;       // V operands are values times 2^(kUp - E), below 2^kUp: s 2^(24 + kUp - E) fits fp16
+constexpr int kApart = 6;     // the keys of a unit share one E while their magnitudes are within 2^6
+constexpr float kBase = 9.f;  // P is 2^kBase at the reference, 2^15 at most
 }  // namespace kt
 
 template <int D, bool WIDE>
@@ -62,11 +70,11 @@ struct TcShape {
   static constexpr int off_raw = off_q + (kQs > 256 * kX * 4 ? kQs : 256 * kX * 4);  // [kRaw][kStage]
   static constexpr int off_sc = off_raw + kt::kRaw * kStage;         // [NS][32] key pairs: (m / s - 8) twice, s twice
   static constexpr int off_pos = off_sc + NS * 64 * 8;               // [NS][64]
-  static constexpr int off_info = off_pos + NS * 64 * 4;             // [NS] (keys held, masks of either half, exponent of V << 1 | own)
+  static constexpr int off_info = off_pos + NS * 64 * 4;             // [NS] (keys held + kTcOwn, masks of either half, E)
   static constexpr int off_bar = off_info + NS * 16;
   static constexpr int off_ok = off_bar + (2 * kt::kRaw + 2 * NS + 14) * 8;
-  static constexpr int off_vmax = off_ok + kt::kRaw * 4;             // [4]
-  static constexpr int off_ml = off_vmax + 16;                       // [2 t][128] (max, sum)
+  static constexpr int off_vmax = off_ok + kt::kRaw * 4;             // [4] (greatest, least magnitude)
+  static constexpr int off_ml = off_vmax + 32;                       // [2 t][128] (reference, sum)
   static constexpr int off_inv = off_ml + 256 * 8;                   // [kRows] 1 / sum
   static constexpr int smem = off_inv + kt::kRows * 4 + 1024;
   static constexpr int kPart = kt::kRows * (D + 2);                  // floats of a part: [rows][D], then [rows] (max, sum)
@@ -138,8 +146,10 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
 // Exponent e of |x| < 2^(e+1); -127 of 0 and subnormals.
 __device__ __forceinline__ int expo(uint32_t bits) { return (int)(bits >> 23 & 255) - 127; }
 
-// Exponent that keeps V operands of magnitude at most |x| (bits) below 2^-6.
-__device__ __forceinline__ int tc_exponent(uint32_t bits) { return expo(bits) + 7; }
+// A bound on the magnitudes of a row with scale s and middle m, as bits.
+__device__ __forceinline__ uint32_t kv4_magnitude(float s, float m) { return __float_as_uint(fmaf(8.f, s, fabsf(m))); }
+// E of values of magnitude at most |x| (bits), which lie below 2^E.
+__device__ __forceinline__ int tc_exponent(uint32_t bits) { return min(max(expo(bits) + 1, -90), 126); }
 
 // A CTA's walk over its segments, by whole warps.
 template <bool BIAS>
@@ -237,24 +247,55 @@ struct TcRow {
   int qpos, start, key0;   // position, document start, the copy's first key of a tile
   uint64_t anc;
   bool live;               // the warp has rows
-  float m, l;
-  int E;                   // V's exponent in O
+  float ref, l;            // the greatest score + E, give or take 6; the sum of 2^(kBase + x - ref)
   bool any;
 };
 
-// The softmax of a segment's units of tile t, NC keys of each (the copy's share).
+constexpr int kTcOwn = 256;  // s_info: the rows' own keys
+
+// The scores of a tile's keys key0 .. key0 + N - 1 from TMEM (times 1 / fac without
+// options), -inf where the row does not see the key.
+template <bool BIAS, int N>
+__device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, const TcRow& w, uint32_t tmem, int key0, const int4& info,
+                                          const float2* s_sc, const int* s_pos, float (&x)[N]) {
+  tmem_ld(tmem + key0, x);
+  const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(s_sc + key0);
+  const uint64_t qq = f2pack(w.qsf, w.qsf);
+#pragma unroll
+  for (int c = 0; c < N; c += 2) {
+    const ulonglong2 v = sc[c / 2];
+    f2unpack(f2mul(f2fma(v.x, qq, f2pack(x[c], x[c + 1])), v.y), x[c], x[c + 1]);
+  }
+  if (BIAS) {
+#pragma unroll
+    for (int c = 0; c < N; c += 2) f2unpack(f2mul(f2pack(x[c], x[c + 1]), f2pack(w.fac, w.fac)), x[c], x[c + 1]);
+    const int* kp = s_pos + key0;
+    kv4_cap(a.s, x);
+    kv4_bias(a.s, x, w.slope, w.qpos, w.start, [&](int c) { return kp[c]; });
+  }
+  if (info.x != 64) {  // not every key is held, or the rows' own keys
+    const uint64_t held = (uint64_t)(uint32_t)info.z << 32 | (uint32_t)info.y;
+    const uint64_t see = (info.x & kTcOwn ? held & w.anc : held) >> key0;
+#pragma unroll
+    for (int c = 0; c < N; c++)
+      if (!(see >> c & 1)) x[c] = -INFINITY;
+  }
+}
+
+// The softmax of units [i0, n) of tile t, NC keys of each (the copy's share).
 template <int D, bool BIAS, bool WIDE, int NC>
 __device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint32_t tb, int i0, int n, uint32_t op0,
                                            uint32_t& par, uint64_t* s_full, uint64_t* op_full, uint64_t* p_full,
                                            uint64_t* o_full, const float2* s_sc, const int* s_pos, const int4* s_info,
                                            int* s_abort) {
   constexpr int NS = TcShape<D, WIDE>::NS, step = WIDE ? 1 : 2;
-  uint32_t buf = 0;  // first TMEM column of the unit's scores: 0 or 64
   const int lane = threadIdx.x & 31;
+  const float f = BIAS ? 1.f : w.fac;  // > 0
 #pragma unroll 1
-  for (int i = i0; i < n; i += step, buf ^= 64) {
+  for (int i = i0; i < n; i += step) {
     const uint32_t st = (op0 + i) % NS;
-    const int b = buf >> 6;
+    const int b = WIDE ? i & 1 : i >> 1 & 1;
+    const uint32_t buf = b * 64;  // first TMEM column of the unit's scores
     if (!kv4_wait(s_full + b, par >> b & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(33));
     par ^= 1u << b;
     if (!kv4_wait(&op_full[st], (op0 + i) / NS & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(34));
@@ -262,45 +303,21 @@ __device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint3
     const int4 info = s_info[st];
     if (w.live) {
       float x[NC];
-      tmem_ld(tb + buf + w.key0, x);
-      const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(s_sc + st * 64 + w.key0);
-      const uint64_t qq = f2pack(w.qsf, w.qsf);
-#pragma unroll
-      for (int c = 0; c < NC; c += 2) {
-        const ulonglong2 v = sc[c / 2];
-        f2unpack(f2mul(f2fma(v.x, qq, f2pack(x[c], x[c + 1])), v.y), x[c], x[c + 1]);
-      }
-      if (BIAS) {
-#pragma unroll
-        for (int c = 0; c < NC; c += 2) f2unpack(f2mul(f2pack(x[c], x[c + 1]), f2pack(w.fac, w.fac)), x[c], x[c + 1]);
-        const int* kp = s_pos + st * 64 + w.key0;
-        kv4_cap(a.s, x);
-        kv4_bias(a.s, x, w.slope, w.qpos, w.start, [&](int c) { return kp[c]; });
-      }
-      if (info.x < 64 || (info.w & 1)) {  // not every key is held, or the rows' own keys
-        const uint64_t held = (uint64_t)(uint32_t)info.z << 32 | (uint32_t)info.y;
-        const uint64_t see = (info.w & 1 ? held & w.anc : held) >> w.key0;
-#pragma unroll
-        for (int c = 0; c < NC; c++)
-          if (!(see >> c & 1)) x[c] = -INFINITY;
-      }
+      tc_scores<BIAS>(a, w, tb + buf, w.key0, info, s_sc + st * 64, s_pos + st * 64, x);
       float t4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
       for (int c = 4; c < NC; c++) t4[c & 3] = fmaxf(t4[c & 3], x[c]);
-      const float f = BIAS ? 1.f : w.fac;
-      const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f;  // f > 0
-      const int E = info.w >> 1;
-      const bool grows = top > w.m + 8.f || (w.m == -INFINITY && top > w.m);
-      const bool moves = w.any && E != w.E;
-      if (__any_sync(0xffffffffu, grows) || moves) {
+      const float E = __int_as_float(info.w);
+      const float top = fmaf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), f, E);
+      const bool grows = top > w.ref + 6.f || (w.ref == -INFINITY && top > w.ref);
+      if (__any_sync(0xffffffffu, grows)) {
         float al = 1.f;
         if (grows) {
-          al = ex2(w.m - top);
-          w.m = top;
+          al = ex2(w.ref - top);
+          w.ref = top;
           w.l *= al;
         }
         if (w.any) {
-          if (moves) al *= pow2i(max(w.E - E, -126));
           // the product before may still be adding to O (the one before that was
           // done before these scores)
           if (!kv4_wait(o_full + (b ^ 1), par >> (b ^ 1) & 1 ^ 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(35));
@@ -316,7 +333,7 @@ __device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint3
           }
         }
       }
-      const float off = 5.f - (w.m == -INFINITY ? 0.f : w.m);
+      const float off = kt::kBase + E - (w.ref == -INFINITY ? 0.f : w.ref);
       uint32_t p[NC / 2];
       uint64_t l4[2] = {0, 0};
       const uint64_t ff = f2pack(f, f), oo = f2pack(off, off);
@@ -332,7 +349,7 @@ __device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint3
       {
         float l0, l1;
         f2unpack(f2add(l4[0], l4[1]), l0, l1);
-        w.l += l0 + l1;
+        w.l = fmaf(l0 + l1, ex2(-E), w.l);
       }
       if constexpr (NC == 64) {
         tmem_st(tb + buf, p);
@@ -343,11 +360,117 @@ __device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint3
         tmem_st(tb + buf, y);
       }
     }
-    w.E = info.w >> 1;
     w.any = true;
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(p_full + b);
+  }
+}
+
+// One unit whose values differ too much in size for one power of two (the
+// products left it out), by fp32 multiply-adds: a thread per row, four keys at a
+// time from global memory, O in TMEM.  Rare, so kept small rather than fast.
+template <int D, bool BIAS>
+__device__ __forceinline__ void tc_apart(const Kv4AttnArgs& a, TcRow& w, const Kv4Req& rq, int r, int h, int u, int nk,
+                                         const uint16_t* q, float scale, uint32_t tb) {
+  const bool own = u < rq.no;
+#pragma unroll 1
+  for (int k0 = w.key0; k0 < w.key0 + nk; k0 += 4) {
+    const int g = rq.g0 + 2 * (u - rq.no) + (k0 >> 5), slot = k0 & 31;
+    const int held = own ? (a.k_new ? rq.m - k0 : 0) : rq.ctx - g * kKvGroup - slot;  // of the four
+    if (held <= 0) break;
+    const uint8_t* const rec = own ? nullptr : a.c.record(D, r, h, g);
+    if (!own && !rec) continue;
+    // eight dims of key j of the four, or of its value
+    auto eight = [&](int j, int d, bool value, float (&f)[8]) {
+      if (own) {
+        const uint4 v = *reinterpret_cast<const uint4*>((value ? a.v_new : a.k_new) +
+                                                        (int64_t)(rq.n0 + min(k0 + j, rq.m - 1)) * a.kv_stride + h * D + d * 8);
+        const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) f[2 * i] = __uint_as_float(vs[i] << 16), f[2 * i + 1] = __uint_as_float(vs[i] & 0xFFFF0000u);
+      } else {
+        const uint8_t* const part = rec + (value ? kv4_half(D) : 0);
+        const uint32_t c = *reinterpret_cast<const uint32_t*>(part + (slot + j) * (D / 2) + (value ? kv4_vbyte<D>(slot + j, d * 4) : d * 4));
+        const uint32_t sm = *reinterpret_cast<const uint32_t*>(part + 16 * D + (slot + j) * 4);
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+          f[i] = fmaf((float)((int)(c >> (4 * i) & 15) - 8), __uint_as_float(sm << 16), __uint_as_float(sm & 0xFFFF0000u));
+      }
+    };
+    float x[4] = {0.f, 0.f, 0.f, 0.f}, big[4] = {0.f, 0.f, 0.f, 0.f};
+    bool odd[4] = {false, false, false, false};
+#pragma unroll 1
+    for (int d = 0; d < D / 8; d++) {
+      const uint4 v = *reinterpret_cast<const uint4*>(q + d * 8);
+      const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        float f[8];
+        eight(j, d, false, f);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          x[j] = fmaf(__uint_as_float(vs[i] << 16), f[2 * i], fmaf(__uint_as_float(vs[i] & 0xFFFF0000u), f[2 * i + 1], x[j]));
+        eight(j, d, true, f);
+#pragma unroll
+        for (int i = 0; i < 8; i++) big[j] = fmaxf(big[j], fabsf(f[i])), odd[j] |= !(fabsf(f[i]) <= 3.4e38f);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++) x[j] *= scale;
+    if (BIAS) {
+      int kp[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int k = own ? min(k0 + j, rq.m - 1) : slot + j;
+        kp[j] = !own ? a.c.pos[a.c.slot0(r, h) + g * kKvGroup + k] : a.row_pos ? a.row_pos[rq.n0 + k] : rq.ctx + k;
+      }
+      kv4_cap(a.s, x);
+      kv4_bias(a.s, x, w.slope, w.qpos, w.start, [&](int j) { return kp[j]; });
+    }
+    float top = w.ref, e[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      e[j] = (float)tc_exponent(__float_as_uint(big[j]));
+      if (odd[j] && x[j] != -INFINITY) x[j] = __int_as_float(0x7FC00000);
+      if (j >= held || (own && !(w.anc >> (k0 + j) & 1))) x[j] = -INFINITY;
+      top = fmaxf(top, x[j] + e[j]);
+    }
+    const float al = top > w.ref ? ex2(w.ref - top) : 1.f;
+    w.ref = top;
+    w.l *= al;
+    const float off = top == -INFINITY ? 0.f : -top;
+    float p[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      p[j] = ex2(x[j] + off);
+      w.l = fmaf(p[j], pow2i((int)kt::kBase), w.l);
+      p[j] = odd[j] ? 0.f : p[j] * pow2i((int)kt::kBase + kt::kUp);  // O's sums are that much up
+    }
+#pragma unroll 1
+    for (int d = 0; d < D / 8; d += 2) {
+      float o[16];
+      tmem_ld(tb + 128 + d * 8, o);
+      uint32_t y[16];
+#pragma unroll
+      for (int half = 0; half < 2; half++) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) o[8 * half + i] *= al;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          float f[8];
+          eight(j, d + half, true, f);
+#pragma unroll
+          for (int i = 0; i < 8; i++) {  // columns hold dims 0 4 1 5 2 6 3 7 of each eight
+            float& c = o[8 * half + (i & 3) * 2 + (i >> 2)];
+            c = fmaf(p[j], odd[j] ? 0.f : f[i], c);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; i++) y[i] = __float_as_uint(o[i]);
+      tmem_st(tb + 128 + d * 8, y);
+    }
   }
 }
 
@@ -370,13 +493,14 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   uint64_t* const p_full = s_full + 4;               // [t][buffer] weights written (4 warps)
   uint64_t* const o_full = p_full + 4;               // [t][buffer] the product with V done (commit)
   int* const s_ok = reinterpret_cast<int*>(sm + S::off_ok);
-  uint32_t* const s_vmax = reinterpret_cast<uint32_t*>(sm + S::off_vmax);
+  uint2* const s_vmax = reinterpret_cast<uint2*>(sm + S::off_vmax);
   float2* const s_ml = reinterpret_cast<float2*>(sm + S::off_ml);
   float* const s_inv = reinterpret_cast<float*>(sm + S::off_inv);
   float* const s_x = reinterpret_cast<float*>(sm + S::off_q);
   __shared__ int s_abort;
   __shared__ uint32_t s_tmem;
   __shared__ Kv4Share sh;
+  __shared__ uint64_t s_apart[8];  // units to take apart, of a run of 64: a ring, as the decoders are up to 6 units ahead
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch();
 
@@ -507,7 +631,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
     }
   } else if (warp < kt::kSoft) {
       // ------------------------------------------------------- operands --
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       TcWalk<BIAS> w(a, sh);
       const bool is_k = warp < 4;
       const int dt = tid & 127, dw = warp & 3;
@@ -517,18 +641,26 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
       const int cg = (D == 128 ? 2 * (dw >> 1) : 0) + (lane & 1);
       const bool mine = D == 128 || dw < 2;
       const uint32_t at0 = (is_k ? 0 : S::kOp) + (cg >> 1) * 8192 + row * 128;
-      uint32_t op = 0, nraw = 0;
+      uint32_t op = 0, nraw = 0, runs = 0;  // runs: of 64 units, begun
       do {
-        int E = -100;  // V operands are values times 2^-E, below 2^-6
         const int h = w.head();
+        // what the softmax warps need of a unit; one to take apart holds no keys for them
+        auto put_info = [&](int st, int u, bool apart, int keys, int lo, int hi, int E) {
+          if (apart) s_apart[runs & 7] |= 1ull << ((u - w.ua) & 63);
+          s_info[st] = apart ? make_int4(0, 0, 0, __float_as_int((float)E)) : make_int4(keys, lo, hi, __float_as_int((float)E));
+        };
         for (int u = w.ua; u < w.ub; u++, op++) {
+          if (((u - w.ua) & 63) == 0) {
+            runs++;
+            if (!is_k && dt == 64) s_apart[runs & 7] = 0;
+          }
           const int st = op % NS;
           uint8_t* const dst = sm + st * 2 * S::kOp;
           if (u >= w.rq.no) {
             const int ga = w.rq.g0 + 2 * (u - w.rq.no), ng = w.groups(a, u);
             // everything this thread needs of the records, then their slots are free
             int lim[2] = {0, 0};
-            uint32_t sm0[2] = {0, 0}, ksm = 0, ksv = 0, vb = 0;
+            uint32_t sm0[2] = {0, 0}, ksm = 0, ksv = 0, most = 0, other = 0;
             uint4 x[2];
             int kpos = 0;
 #pragma unroll
@@ -550,8 +682,9 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
                 if (mine) x[gi] = *reinterpret_cast<const uint4*>(v + row * (D / 2) + (D == 128 ? cg ^ (row & 2) : cg) * 16);
                 sm0[gi] = *reinterpret_cast<const uint32_t*>(v + 16 * D + row * 4);
                 const uint32_t vw = *reinterpret_cast<const uint32_t*>(v + 16 * D + lane * 4);
-                const float b = fmaf(8.f, __uint_as_float(vw << 16), fabsf(__uint_as_float(vw & 0xFFFF0000u)));
-                if (lane < lim[gi] && b <= 3.4e38f) vb = max(vb, __float_as_uint(b));
+                const uint32_t big = kv4_magnitude(__uint_as_float(vw << 16), __uint_as_float(vw & 0xFFFF0000u));
+                other = most;
+                most = lane < lim[gi] && big < 0x7F800000u ? big : 0;
               }
             }
             __syncwarp();
@@ -584,17 +717,20 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
                       make_uint4(codes2<0>(xs[j]), codes2<1>(xs[j]), codes2<2>(xs[j]), codes2<3>(xs[j]));
               }
             } else {
-              E = min(max(E, tc_exponent(__reduce_max_sync(0xffffffffu, vb))), 120);
-              if (dt == 0)
-                s_info[st] = make_int4(lim[0] + lim[1], lim[0] == 32 ? -1 : (1 << lim[0]) - 1,
-                                       lim[1] == 32 ? -1 : (1 << lim[1]) - 1, E * 2);
+              // one E for the unit's keys; magnitudes of 0 do not count
+              const uint32_t top = __reduce_max_sync(0xffffffffu, max(most, other));
+              const uint32_t far = max(top, (uint32_t)kt::kApart << 23) - ((uint32_t)kt::kApart << 23);
+              const bool apart = __any_sync(0xffffffffu, (most && most < far) || (other && other < far));
+              const int E = tc_exponent(top);
+              if (dt == 64) put_info(st, u, apart, lim[0] + lim[1], lim[0] == 32 ? -1 : (1 << lim[0]) - 1,
+                                     lim[1] == 32 ? -1 : (1 << lim[1]) - 1, E);
 #pragma unroll
               for (int gi = 0; gi < 2; gi++) {
                 if (gi >= ng || !mine) break;
                 float s = __uint_as_float(sm0[gi] << 16), m = __uint_as_float(sm0[gi] & 0xFFFF0000u);
                 if (row >= lim[gi] || !(s <= 3.4e38f)) s = m = 0.f;  // not held, or NaN: its scores say so
-                const uint32_t me = h2dup(s * pow2i(24 - E)), mo = h2dup(s * pow2i(20 - E)),
-                               cc = h2dup(fmaf(-8.f, s, m) * pow2i(-E));
+                const uint32_t me = h2dup(s * pow2i(24 + kt::kUp - E)), mo = h2dup(s * pow2i(20 + kt::kUp - E)),
+                               cc = h2dup(fmaf(-8.f, s, m) * pow2i(kt::kUp - E));
                 const uint32_t xs[4] = {x[gi].x, x[gi].y, x[gi].z, x[gi].w};
 #pragma unroll
                 for (int j = 0; j < 4; j++)
@@ -641,7 +777,8 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
               }
             };
             if (is_k) {
-              const bool odd = a.k_new && row_max(a.v_new) >= 0x7F800000u;
+              const uint32_t vbig = a.k_new ? row_max(a.v_new) : 0;
+              const bool odd = vbig >= 0x7F800000u;
               const int e = min(max(10 - expo(a.k_new ? row_max(a.k_new) : 0), -100), 100);  // the greatest below 2^11; odd dims 2^4 up
               store(a.k_new, pow2i(e), pow2i(e + 4), false);
               if (half == 0) {
@@ -651,16 +788,21 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
                 if (BIAS && in) s_pos[st * 64 + j] = a.row_pos ? a.row_pos[w.rq.n0 + j] : w.rq.ctx + j;
               }
             } else {
-              const uint32_t big = a.k_new ? row_max(a.v_new) : 0;
+              uint32_t big = a.k_new ? row_max(a.v_new) : 0;
               const bool odd = big >= 0x7F800000u;
-              const uint32_t wm = __reduce_max_sync(0xffffffffu, odd ? 0u : big);
-              if (lane == 0) s_vmax[dw] = wm;
+              if (odd) big = 0;
+              const uint32_t most = __reduce_max_sync(0xffffffffu, big), least = __reduce_min_sync(0xffffffffu, big - 1u);
+              if (lane == 0) s_vmax[dw] = make_uint2(most, least);
               bar_sync(1, 128);
-              E = min(max(E, tc_exponent(max(max(s_vmax[0], s_vmax[1]), max(s_vmax[2], s_vmax[3])))), 120);
+              uint2 v = s_vmax[0];
+#pragma unroll
+              for (int i = 1; i < 4; i++) v = make_uint2(max(v.x, s_vmax[i].x), min(v.y, s_vmax[i].y));
               bar_sync(1, 128);
-              store(a.v_new, pow2i(-E), pow2i(-E), odd);
-              if (dt == 0)
-                s_info[st] = make_int4(m, m >= 32 ? -1 : (1 << m) - 1, m >= 64 ? -1 : m > 32 ? (1 << (m - 32)) - 1 : 0, E * 2 + 1);
+              const int E = tc_exponent(v.x);
+              const bool apart = v.x && v.y + 1u + ((uint32_t)kt::kApart << 23) < v.x;
+              store(a.v_new, pow2i(kt::kUp - E), pow2i(kt::kUp - E), odd);
+              if (dt == 64) put_info(st, u, apart, m + kTcOwn, m >= 32 ? -1 : (1 << m) - 1,
+                                     m >= 64 ? -1 : m > 32 ? (1 << (m - 32)) - 1 : 0, E);
             }
           }
           fence_async_smem();
@@ -670,18 +812,19 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
       } while (w.next(a, sh));
   } else {
       // -------------------------------------------------------- softmax --
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
       TcWalk<BIAS> w(a, sh);
       const int t = (warp - kt::kSoft) >> 2, st256 = tid - kt::kSoft * 32;
       const int idx = (warp & 3) * 32 + lane;                                // TMEM lane
       const uint32_t tb = tm + t * 256 + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
       const float scale = BIAS ? 1.f : a.s.scale * kLog2e;
-      uint32_t op0 = 0, par = 0;  // par: parity of the units done in either buffer
+      uint32_t op0 = 0, par = 0, runs = 0;  // par: parity of the units done in either buffer
       do {
         const int h = w.head(), rc = w.s - h * w.rq.nc, n = w.ub - w.ua;
         const TcRowsOf<WIDE> rw(a.G * w.rq.m, w.rq.nc, rc);
         const int span = 128 / rw.copies;  // lanes of a copy
         TcRow x;
+        const uint16_t* q;
         {
           const int ridx = idx % span;
           const bool ok = ridx < rw.of(t);
@@ -693,11 +836,11 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
           x.slope = BIAS && a.s.slopes ? a.s.slopes[hq] : 0.f;
           x.qpos = a.row_pos ? a.row_pos[w.rq.n0 + node] : w.rq.ctx + node;
           x.anc = a.anc ? a.anc[w.rq.n0 + node] : (2ull << node) - 1;
-          x.m = -INFINITY;
+          x.ref = -INFINITY;
           x.l = 0.f;
-          x.E = 0;
           x.any = false;
-          const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(w.rq.n0 + node) * a.q_stride + hq * D);
+          q = a.q + (int64_t)(w.rq.n0 + node) * a.q_stride + hq * D;
+          const uint4* src = reinterpret_cast<const uint4*>(q);
           uint4 v[D / 8];
 #pragma unroll
           for (int i = 0; i < D / 8; i++) v[i] = ok ? src[i] : make_uint4(0, 0, 0, 0);
@@ -736,14 +879,24 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
         __syncwarp();
         if (lane == 0 && (WIDE || t == 0)) mbar_arrive(&q_full[t]);
 
-        {
+        for (int i0 = 0; i0 < n; i0 += 64) {
+          const int i1 = min(n, i0 + 64);
           auto run = [&](auto nc) {
-            tc_softmax<D, BIAS, WIDE, decltype(nc)::value>(a, x, tb, WIDE ? 0 : t, n, op0, par, &s_full[2 * t], op_full, &p_full[2 * t],
-                                                           &o_full[2 * t], s_sc, s_pos, s_info, &s_abort);
+            tc_softmax<D, BIAS, WIDE, decltype(nc)::value>(a, x, tb, i0 + (WIDE ? 0 : t), i1, op0, par, &s_full[2 * t], op_full,
+                                                           &p_full[2 * t], &o_full[2 * t], s_sc, s_pos, s_info, &s_abort);
           };
           if (WIDE || rw.copies == 1) run(std::integral_constant<int, 64>());
           else if (rw.copies == 2) run(std::integral_constant<int, 32>());
           else run(std::integral_constant<int, 16>());
+          runs++;
+          uint64_t apart = s_apart[runs & 7] & (~0ull >> (64 - (i1 - i0)));
+          if (!WIDE) apart &= 0x5555555555555555ull << t;  // this tile's units, which it has waited for
+          if (apart && x.live) {
+            for (int b = 0; b < 2; b++) wait(&o_full[2 * t + b], (par >> b) ^ 1);
+            tc_fence_after();
+            for (; apart; apart &= apart - 1)
+              tc_apart<D, BIAS>(a, x, w.rq, w.r, h, w.ua + i0 + __ffsll((long long)apart) - 1, 64 / rw.copies, q, scale, tb);
+          }
         }
         if (x.any) {
           // the last two products may be under way
@@ -755,7 +908,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
         const bool whole = w.ua == 0 && w.ub == w.rq.nu;
         const int slot = 2 * blockIdx.x + (w.seg + w.ua > sh.u0 ? 1 : 0);
         float* part = a.part + (int64_t)slot * S::kPart;
-        s_ml[t * 128 + idx] = x.live ? make_float2(x.m, x.l) : make_float2(-INFINITY, 0.f);
+        s_ml[t * 128 + idx] = x.live ? make_float2(x.ref, x.l) : make_float2(-INFINITY, 0.f);
         bar_sync(2, kt::kSoftThreads);
         auto lane_of = [&](int row, int j) {  // copy j of a row: [t][lane]
           if (WIDE) return row < rw.split ? row : 128 + row - rw.split;
@@ -772,7 +925,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
               if (j < nsub) M = fmaxf(M, s_ml[lane_of(row, j)].x);
           }
           const float Ms = M == -INFINITY ? 0.f : M;
-          f = x.any ? ex2(x.m - Ms) * pow2i(x.E) : 0.f;
+          f = x.any ? ex2(x.ref - Ms) * pow2i(-kt::kUp) : 0.f;
           if (ridx < rw.of(t) && (WIDE || idx + t * 128 == row)) {  // one thread a row
 #pragma unroll
             for (int j = 0; j < 8; j++)
@@ -784,10 +937,10 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
               if (a.lse) {
                 const int rho = rw.base + row, gq = rho / w.rq.m;
                 a.lse[(int64_t)(w.rq.n0 + rho - gq * w.rq.m) * a.hq + h * a.G + gq] =
-                    L == 0.f ? -INFINITY : (M - 5.f + log2f(L)) * (1.f / kLog2e);
+                    L == 0.f ? -INFINITY : (M - kt::kBase + log2f(L)) * (1.f / kLog2e);
               }
             } else {
-              __stcg(reinterpret_cast<float2*>(part + kt::kRows * D) + row, make_float2(M - 5.f, L));
+              __stcg(reinterpret_cast<float2*>(part + kt::kRows * D) + row, make_float2(M - kt::kBase, L));
             }
             s_inv[row] = L == 0.f ? 0.f : 1.f / L;
           }

@@ -12,19 +12,20 @@
 //    are applied to its score, as in the warp kernel); V's as values, s code + (m
 //    - 8 s) in one fp16 multiply-add per pair after a power of two, 2^-E for all
 //    keys of the unit (11 bits of the value and of m - 8 s, against the output's
-//    8).  The rows' own keys are a tile of 64 in the same form, bf16 to fp16 after a
-//    power of two, per key for K;
+//    8).  A unit whose values differ in size by more than 2^6 is taken apart: each
+//    key has an E of its own, which its weight makes up for.  The rows' own keys
+//    are a tile of 64 in the same form, bf16 to fp16 after a power of two, per key
+//    for K;
 //  * 17: the products;
 //  * 8..15: softmax, a thread per row: the scores of 64 keys from TMEM, maximum,
 //    exponentials, P back.  A row's reference, its greatest score + E, may lag by
 //    2^6 before O is rescaled in TMEM (fp16 P: exponentials are taken 2^9 up, at
 //    most 2^15).  So weights down to 2^-17 of the row's greatest p |v| keep their 11
-//    bits, down to 2^-28 count.  A unit whose values differ in size by more than
-//    2^6 holds no keys for the products: the same warps take it by fp32
-//    multiply-adds, after the run of 64 units that it lies in (a unit of 160
-//    rows 11 us).  So nothing that a row does not see moves its weights or values.
+//    bits, down to 2^-28 count, and nothing that a row does not see moves its
+//    weights or values.  (A factor per key in every unit, not in those taken apart
+//    alone: 412 us where the tree of 64 below takes 362.)
 // (18 and 19 do nothing: they complete a warpgroup.  Registers a scheduler:
-// 5 warps x 96 = 2 x 72 decoding + 2 x 144 softmax + 48.)
+// 5 warps x 96 = 2 x 72 decoding + 2 x 144 softmax + 48, or 80 and 136, 64 and 152.)
 // WIDE: the first rows of a segment are tile 0's, the others tile 1's, up to
 // 256.  Not WIDE (at most 128 rows a segment): both tiles hold the same rows and
 // take alternate key tiles.  With at most 64 (32) rows a tile holds them twice
@@ -35,10 +36,12 @@
 // of a segment that spans CTAs are joined by a second kernel, in a fixed order.
 //
 // Measured: a tree of 64 with 40 query and 8 kv heads over 131072 keys, D = 128
-// (WIDE, two segments of 160 rows a kv head): 382 us, 450 TFLOP/s; tensor pipe
-// 33%, issue 43%.  Bound by the softmax warps, two a scheduler, which wait for
-// tensor memory and their own chains (one score buffer a tile: 438 us; four
-// softmax warps: 500).
+// (WIDE, two segments of 160 rows a kv head): 362 us, 475 TFLOP/s; with every
+// unit taken apart 603.  The 160 rows are split 96 / 64, so that the schedulers
+// have 2, 2, 1 and 0 softmax warps, and the products run 512 rows for 320; bound
+// by the two schedulers' softmax warps, which wait for tensor memory and their own
+// chains (one score buffer a tile took 438 us where two took 397; four softmax
+// warps, 500).  Not WIDE, 8 requests of 128 rows over 16000 keys: 187 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -58,7 +61,7 @@ constexpr int kApart = 6;     // the keys of a unit share one E while their magn
 constexpr float kBase = 9.f;  // P is 2^kBase at the reference, 2^15 at most
 }  // namespace kt
 
-template <int D, bool WIDE>
+template <int D, bool WIDE, bool BIAS = false>
 struct TcShape {
   static constexpr int NS = WIDE ? 3 : 4;                            // operand stages
   static constexpr int kStage = kv4_rec(D) + 128;
@@ -70,13 +73,18 @@ struct TcShape {
   static constexpr int off_raw = off_q + (kQs > 256 * kX * 4 ? kQs : 256 * kX * 4);  // [kRaw][kStage]
   static constexpr int off_sc = off_raw + kt::kRaw * kStage;         // [NS][32] key pairs: (m / s - 8) twice, s twice
   static constexpr int off_pos = off_sc + NS * 64 * 8;               // [NS][64]
-  static constexpr int off_info = off_pos + NS * 64 * 4;             // [NS] (keys held + kTcOwn, masks of either half, E)
+  static constexpr int off_e = off_pos + NS * 64 * 4;                // [NS][64] E of a key, in units taken apart
+  static constexpr int off_info = off_e + NS * 64 * 4;               // [NS] (keys held + kTcOwn + kTcApart, masks of either half, E)
   static constexpr int off_bar = off_info + NS * 16;
   static constexpr int off_ok = off_bar + (2 * kt::kRaw + 2 * NS + 14) * 8;
   static constexpr int off_vmax = off_ok + kt::kRaw * 4;             // [4] (greatest, least magnitude)
   static constexpr int off_ml = off_vmax + 32;                       // [2 t][128] (reference, sum)
   static constexpr int off_inv = off_ml + 256 * 8;                   // [kRows] 1 / sum
   static constexpr int smem = off_inv + kt::kRows * 4 + 1024;
+  // Registers of the decoding warps; the softmax warps have 216 less these.  Each
+  // form's best of 64, 72 and 80 (96 rows over 65536 keys: 107, 107, 104 us; with
+  // a cap 116, 123, 123; 320 rows over 131072 keys 388, 362, 397).
+  static constexpr int kDecodeRegs = WIDE ? 72 : BIAS ? 64 : 80;
   static constexpr int kPart = kt::kRows * (D + 2);                  // floats of a part: [rows][D], then [rows] (max, sum)
 };
 
@@ -119,6 +127,11 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16])
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
       : "memory");
 }
 // D (tmem) (+)= A (smem) * B (smem)^T, or A (tmem) * B (smem), fp16.
@@ -251,7 +264,7 @@ struct TcRow {
   bool any;
 };
 
-constexpr int kTcOwn = 256;  // s_info: the rows' own keys
+constexpr int kTcOwn = 256, kTcApart = 512;  // s_info: the rows' own keys; each key has its E in s_e
 
 // The scores of a tile's keys key0 .. key0 + N - 1 from TMEM (times 1 / fac without
 // options), -inf where the row does not see the key.
@@ -273,7 +286,7 @@ __device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, const TcRow& w, 
     kv4_cap(a.s, x);
     kv4_bias(a.s, x, w.slope, w.qpos, w.start, [&](int c) { return kp[c]; });
   }
-  if (info.x != 64) {  // not every key is held, or the rows' own keys
+  if ((info.x & ~kTcApart) != 64) {  // not every key is held, or the rows' own keys
     const uint64_t held = (uint64_t)(uint32_t)info.z << 32 | (uint32_t)info.y;
     const uint64_t see = (info.x & kTcOwn ? held & w.anc : held) >> key0;
 #pragma unroll
@@ -282,207 +295,160 @@ __device__ __forceinline__ void tc_scores(const Kv4AttnArgs& a, const TcRow& w, 
   }
 }
 
-// The softmax of units [i0, n) of tile t, NC keys of each (the copy's share).
+// O times al, a row's own factor, in TMEM.  The product before may still be adding
+// to O (the one before that was done before these scores).
+template <int D>
+__device__ __forceinline__ void tc_rescale(uint32_t tb, float al, uint64_t* o_full, uint32_t parity, int* s_abort, int32_t* status) {
+  if (!kv4_wait(o_full, parity, s_abort)) set_status(status, SD_TIMEOUT_AT(35));
+  tc_fence_after();
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    float o[16];
+    tmem_ld(tb + 128 + c, o);
+    uint32_t y[16];
+#pragma unroll
+    for (int k = 0; k < 16; k++) y[k] = __float_as_uint(o[k] * al);
+    tmem_st(tb + 128 + c, y);
+  }
+}
+
+// One unit whose values differ too much in size for one E: each key has its own.
+// Rare, so 16 keys at a time and the scores twice; P takes the place of scores
+// that are already read.
+template <int D, bool BIAS>
+__device__ __forceinline__ void tc_apart(const Kv4AttnArgs& a, TcRow& w, uint32_t tb, uint32_t buf, int nk, const int4& info,
+                                         const float2* s_sc, const int* s_pos, const float* s_e, uint64_t* o_full,
+                                         uint32_t parity, int* s_abort) {
+  const float f = BIAS ? 1.f : w.fac;
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c0 = w.key0; c0 < w.key0 + nk; c0 += 16) {
+    float x[16];
+    tc_scores<BIAS>(a, w, tb + buf, c0, info, s_sc, s_pos, x);
+#pragma unroll
+    for (int c = 0; c < 16; c++) top = fmaxf(top, fmaf(x[c], f, s_e[c0 + c]));
+  }
+  const bool grows = top > w.ref + 6.f || (w.ref == -INFINITY && top > w.ref);
+  if (__any_sync(0xffffffffu, grows)) {
+    const float al = grows ? ex2(w.ref - top) : 1.f;
+    if (grows) w.ref = top;
+    w.l *= al;
+    if (w.any) tc_rescale<D>(tb, al, o_full, parity, s_abort, a.status);
+  }
+  const float off = kt::kBase - (w.ref == -INFINITY ? 0.f : w.ref);
+#pragma unroll 1
+  for (int c0 = w.key0; c0 < w.key0 + nk; c0 += 16) {
+    float x[16];
+    tc_scores<BIAS>(a, w, tb + buf, c0, info, s_sc, s_pos, x);
+    uint32_t p[8];
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+      const float e0 = s_e[c0 + c], e1 = s_e[c0 + c + 1];
+      const float p0 = ex2(fmaf(x[c], f, off + e0)), p1 = ex2(fmaf(x[c + 1], f, off + e1));
+      w.l = fmaf(p0, ex2(-e0), fmaf(p1, ex2(-e1), w.l));
+      p[c / 2] = pack_f16x2(p0, p1);
+    }
+    tmem_st(tb + buf + c0 / 2, p);
+  }
+  const uint32_t none[8] = {};
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 16)
+    if (c < w.key0 || c >= w.key0 + nk) tmem_st(tb + buf + c / 2, none);
+}
+
+// The softmax of a segment's units of tile t, NC keys of each (the copy's share).
 template <int D, bool BIAS, bool WIDE, int NC>
 __device__ __forceinline__ void tc_softmax(const Kv4AttnArgs& a, TcRow& w, uint32_t tb, int i0, int n, uint32_t op0,
                                            uint32_t& par, uint64_t* s_full, uint64_t* op_full, uint64_t* p_full,
-                                           uint64_t* o_full, const float2* s_sc, const int* s_pos, const int4* s_info,
-                                           int* s_abort) {
+                                           uint64_t* o_full, const float2* s_sc, const int* s_pos, const float* s_e,
+                                           const int4* s_info, int* s_abort) {
   constexpr int NS = TcShape<D, WIDE>::NS, step = WIDE ? 1 : 2;
   const int lane = threadIdx.x & 31;
   const float f = BIAS ? 1.f : w.fac;  // > 0
 #pragma unroll 1
-  for (int i = i0; i < n; i += step) {
+  for (int i = i0; i < n;) {
+#pragma unroll 1
+    for (; i < n; i += step) {
+      const uint32_t st = (op0 + i) % NS;
+      const int b = WIDE ? i & 1 : i >> 1 & 1;
+      const uint32_t buf = b * 64;  // first TMEM column of the unit's scores
+      if (!kv4_wait(s_full + b, par >> b & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(33));
+      par ^= 1u << b;
+      if (!kv4_wait(&op_full[st], (op0 + i) / NS & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(34));
+      tc_fence_after();
+      const int4 info = s_info[st];
+      if (info.x & kTcApart) break;
+      if (w.live) {
+        float x[NC];
+        tc_scores<BIAS>(a, w, tb + buf, w.key0, info, s_sc + st * 64, s_pos + st * 64, x);
+        float t4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < NC; c++) t4[c & 3] = fmaxf(t4[c & 3], x[c]);
+        const float E = __int_as_float(info.w);
+        const float top = fmaf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), f, E);
+        const bool grows = top > w.ref + 6.f || (w.ref == -INFINITY && top > w.ref);
+        if (__any_sync(0xffffffffu, grows)) {
+          const float al = grows ? ex2(w.ref - top) : 1.f;
+          if (grows) w.ref = top;
+          w.l *= al;
+          if (w.any) tc_rescale<D>(tb, al, o_full + (b ^ 1), par >> (b ^ 1) & 1 ^ 1, s_abort, a.status);
+        }
+        const float off = kt::kBase + E - (w.ref == -INFINITY ? 0.f : w.ref);
+        uint32_t p[NC / 2];
+        uint64_t l4[2] = {0, 0};
+        const uint64_t ff = f2pack(f, f), oo = f2pack(off, off);
+#pragma unroll
+        for (int c = 0; c < NC; c += 2) {
+          float p0, p1;
+          f2unpack(f2fma(f2pack(x[c], x[c + 1]), ff, oo), p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          l4[c >> 1 & 1] = f2add(l4[c >> 1 & 1], f2pack(p0, p1));
+          p[c / 2] = pack_f16x2(p0, p1);
+        }
+        {
+          float l0, l1;
+          f2unpack(f2add(l4[0], l4[1]), l0, l1);
+          w.l = fmaf(l0 + l1, ex2(-E), w.l);
+        }
+        if constexpr (NC == 64) {
+          tmem_st(tb + buf, p);
+        } else {
+          uint32_t y[32];
+#pragma unroll
+          for (int c = 0; c < 32; c++) y[c] = c / (NC / 2) * NC == w.key0 ? p[c % (NC / 2)] : 0u;
+          tmem_st(tb + buf, y);
+        }
+      }
+      w.any = true;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full + b);
+    }
+    if (i >= n) break;
     const uint32_t st = (op0 + i) % NS;
     const int b = WIDE ? i & 1 : i >> 1 & 1;
-    const uint32_t buf = b * 64;  // first TMEM column of the unit's scores
-    if (!kv4_wait(s_full + b, par >> b & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(33));
-    par ^= 1u << b;
-    if (!kv4_wait(&op_full[st], (op0 + i) / NS & 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(34));
-    tc_fence_after();
-    const int4 info = s_info[st];
-    if (w.live) {
-      float x[NC];
-      tc_scores<BIAS>(a, w, tb + buf, w.key0, info, s_sc + st * 64, s_pos + st * 64, x);
-      float t4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-      for (int c = 4; c < NC; c++) t4[c & 3] = fmaxf(t4[c & 3], x[c]);
-      const float E = __int_as_float(info.w);
-      const float top = fmaf(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), f, E);
-      const bool grows = top > w.ref + 6.f || (w.ref == -INFINITY && top > w.ref);
-      if (__any_sync(0xffffffffu, grows)) {
-        float al = 1.f;
-        if (grows) {
-          al = ex2(w.ref - top);
-          w.ref = top;
-          w.l *= al;
-        }
-        if (w.any) {
-          // the product before may still be adding to O (the one before that was
-          // done before these scores)
-          if (!kv4_wait(o_full + (b ^ 1), par >> (b ^ 1) & 1 ^ 1, s_abort)) set_status(a.status, SD_TIMEOUT_AT(35));
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            float o[16];
-            tmem_ld(tb + 128 + c, o);
-            uint32_t y[16];
-#pragma unroll
-            for (int k = 0; k < 16; k++) y[k] = __float_as_uint(o[k] * al);
-            tmem_st(tb + 128 + c, y);
-          }
-        }
-      }
-      const float off = kt::kBase + E - (w.ref == -INFINITY ? 0.f : w.ref);
-      uint32_t p[NC / 2];
-      uint64_t l4[2] = {0, 0};
-      const uint64_t ff = f2pack(f, f), oo = f2pack(off, off);
-#pragma unroll
-      for (int c = 0; c < NC; c += 2) {
-        float p0, p1;
-        f2unpack(f2fma(f2pack(x[c], x[c + 1]), ff, oo), p0, p1);
-        p0 = ex2(p0);
-        p1 = ex2(p1);
-        l4[c >> 1 & 1] = f2add(l4[c >> 1 & 1], f2pack(p0, p1));
-        p[c / 2] = pack_f16x2(p0, p1);
-      }
-      {
-        float l0, l1;
-        f2unpack(f2add(l4[0], l4[1]), l0, l1);
-        w.l = fmaf(l0 + l1, ex2(-E), w.l);
-      }
-      if constexpr (NC == 64) {
-        tmem_st(tb + buf, p);
-      } else {
-        uint32_t y[32];
-#pragma unroll
-        for (int c = 0; c < 32; c++) y[c] = c / (NC / 2) * NC == w.key0 ? p[c % (NC / 2)] : 0u;
-        tmem_st(tb + buf, y);
-      }
-    }
+    if (w.live)
+      tc_apart<D, BIAS>(a, w, tb, b * 64, NC, s_info[st], s_sc + st * 64, s_pos + st * 64, s_e + st * 64, o_full + (b ^ 1),
+                        par >> (b ^ 1) & 1 ^ 1, s_abort);
     w.any = true;
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(p_full + b);
-  }
-}
-
-// One unit whose values differ too much in size for one power of two (the
-// products left it out), by fp32 multiply-adds: a thread per row, four keys at a
-// time from global memory, O in TMEM.  Rare, so kept small rather than fast.
-template <int D, bool BIAS>
-__device__ __forceinline__ void tc_apart(const Kv4AttnArgs& a, TcRow& w, const Kv4Req& rq, int r, int h, int u, int nk,
-                                         const uint16_t* q, float scale, uint32_t tb) {
-  const bool own = u < rq.no;
-#pragma unroll 1
-  for (int k0 = w.key0; k0 < w.key0 + nk; k0 += 4) {
-    const int g = rq.g0 + 2 * (u - rq.no) + (k0 >> 5), slot = k0 & 31;
-    const int held = own ? (a.k_new ? rq.m - k0 : 0) : rq.ctx - g * kKvGroup - slot;  // of the four
-    if (held <= 0) break;
-    const uint8_t* const rec = own ? nullptr : a.c.record(D, r, h, g);
-    if (!own && !rec) continue;
-    // eight dims of key j of the four, or of its value
-    auto eight = [&](int j, int d, bool value, float (&f)[8]) {
-      if (own) {
-        const uint4 v = *reinterpret_cast<const uint4*>((value ? a.v_new : a.k_new) +
-                                                        (int64_t)(rq.n0 + min(k0 + j, rq.m - 1)) * a.kv_stride + h * D + d * 8);
-        const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; i++) f[2 * i] = __uint_as_float(vs[i] << 16), f[2 * i + 1] = __uint_as_float(vs[i] & 0xFFFF0000u);
-      } else {
-        const uint8_t* const part = rec + (value ? kv4_half(D) : 0);
-        const uint32_t c = *reinterpret_cast<const uint32_t*>(part + (slot + j) * (D / 2) + (value ? kv4_vbyte<D>(slot + j, d * 4) : d * 4));
-        const uint32_t sm = *reinterpret_cast<const uint32_t*>(part + 16 * D + (slot + j) * 4);
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-          f[i] = fmaf((float)((int)(c >> (4 * i) & 15) - 8), __uint_as_float(sm << 16), __uint_as_float(sm & 0xFFFF0000u));
-      }
-    };
-    float x[4] = {0.f, 0.f, 0.f, 0.f}, big[4] = {0.f, 0.f, 0.f, 0.f};
-    bool odd[4] = {false, false, false, false};
-#pragma unroll 1
-    for (int d = 0; d < D / 8; d++) {
-      const uint4 v = *reinterpret_cast<const uint4*>(q + d * 8);
-      const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        float f[8];
-        eight(j, d, false, f);
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-          x[j] = fmaf(__uint_as_float(vs[i] << 16), f[2 * i], fmaf(__uint_as_float(vs[i] & 0xFFFF0000u), f[2 * i + 1], x[j]));
-        eight(j, d, true, f);
-#pragma unroll
-        for (int i = 0; i < 8; i++) big[j] = fmaxf(big[j], fabsf(f[i])), odd[j] |= !(fabsf(f[i]) <= 3.4e38f);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; j++) x[j] *= scale;
-    if (BIAS) {
-      int kp[4];
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const int k = own ? min(k0 + j, rq.m - 1) : slot + j;
-        kp[j] = !own ? a.c.pos[a.c.slot0(r, h) + g * kKvGroup + k] : a.row_pos ? a.row_pos[rq.n0 + k] : rq.ctx + k;
-      }
-      kv4_cap(a.s, x);
-      kv4_bias(a.s, x, w.slope, w.qpos, w.start, [&](int j) { return kp[j]; });
-    }
-    float top = w.ref, e[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      e[j] = (float)tc_exponent(__float_as_uint(big[j]));
-      if (odd[j] && x[j] != -INFINITY) x[j] = __int_as_float(0x7FC00000);
-      if (j >= held || (own && !(w.anc >> (k0 + j) & 1))) x[j] = -INFINITY;
-      top = fmaxf(top, x[j] + e[j]);
-    }
-    const float al = top > w.ref ? ex2(w.ref - top) : 1.f;
-    w.ref = top;
-    w.l *= al;
-    const float off = top == -INFINITY ? 0.f : -top;
-    float p[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      p[j] = ex2(x[j] + off);
-      w.l = fmaf(p[j], pow2i((int)kt::kBase), w.l);
-      p[j] = odd[j] ? 0.f : p[j] * pow2i((int)kt::kBase + kt::kUp);  // O's sums are that much up
-    }
-#pragma unroll 1
-    for (int d = 0; d < D / 8; d += 2) {
-      float o[16];
-      tmem_ld(tb + 128 + d * 8, o);
-      uint32_t y[16];
-#pragma unroll
-      for (int half = 0; half < 2; half++) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) o[8 * half + i] *= al;
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          float f[8];
-          eight(j, d + half, true, f);
-#pragma unroll
-          for (int i = 0; i < 8; i++) {  // columns hold dims 0 4 1 5 2 6 3 7 of each eight
-            float& c = o[8 * half + (i & 3) * 2 + (i >> 2)];
-            c = fmaf(p[j], odd[j] ? 0.f : f[i], c);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 16; i++) y[i] = __float_as_uint(o[i]);
-      tmem_st(tb + 128 + d * 8, y);
-    }
+    i += step;
   }
 }
 
 template <int D, bool BIAS, bool WIDE>
 __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_constant__ Kv4AttnArgs a) {
-  using S = TcShape<D, WIDE>;
+  using S = TcShape<D, WIDE, BIAS>;
   constexpr int NS = S::NS;
   extern __shared__ uint8_t smem_tc[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_tc) + 1023) & ~uintptr_t(1023));
   uint8_t* const raw = sm + S::off_raw;
   float2* const s_sc = reinterpret_cast<float2*>(sm + S::off_sc);
   int* const s_pos = reinterpret_cast<int*>(sm + S::off_pos);
+  float* const s_e = reinterpret_cast<float*>(sm + S::off_e);
   int4* const s_info = reinterpret_cast<int4*>(sm + S::off_info);
   uint64_t* const raw_full = reinterpret_cast<uint64_t*>(sm + S::off_bar);  // record landed
   uint64_t* const raw_empty = raw_full + kt::kRaw;   // record decoded (8 warps)
@@ -500,7 +466,6 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   __shared__ int s_abort;
   __shared__ uint32_t s_tmem;
   __shared__ Kv4Share sh;
-  __shared__ uint64_t s_apart[8];  // units to take apart, of a run of 64: a ring, as the decoders are up to 6 units ahead
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch();
 
@@ -531,7 +496,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
   if (sh.u0 >= sh.u1) {
     // no work for this CTA
   } else if (warp >= kt::kLoad) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(48));
     if (warp == kt::kLoad) {
       TcWalk<BIAS> w(a, sh);
       uint32_t n = 0;
@@ -631,7 +596,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
     }
   } else if (warp < kt::kSoft) {
       // ------------------------------------------------------- operands --
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kDecodeRegs));
       TcWalk<BIAS> w(a, sh);
       const bool is_k = warp < 4;
       const int dt = tid & 127, dw = warp & 3;
@@ -641,19 +606,13 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
       const int cg = (D == 128 ? 2 * (dw >> 1) : 0) + (lane & 1);
       const bool mine = D == 128 || dw < 2;
       const uint32_t at0 = (is_k ? 0 : S::kOp) + (cg >> 1) * 8192 + row * 128;
-      uint32_t op = 0, nraw = 0, runs = 0;  // runs: of 64 units, begun
+      uint32_t op = 0, nraw = 0;
       do {
         const int h = w.head();
-        // what the softmax warps need of a unit; one to take apart holds no keys for them
-        auto put_info = [&](int st, int u, bool apart, int keys, int lo, int hi, int E) {
-          if (apart) s_apart[runs & 7] |= 1ull << ((u - w.ua) & 63);
-          s_info[st] = apart ? make_int4(0, 0, 0, __float_as_int((float)E)) : make_int4(keys, lo, hi, __float_as_int((float)E));
+        auto put_info = [&](int st, bool apart, int keys, int lo, int hi, int E) {  // what the softmax warps need of a unit
+          s_info[st] = make_int4(keys + (apart ? kTcApart : 0), lo, hi, __float_as_int((float)E));
         };
         for (int u = w.ua; u < w.ub; u++, op++) {
-          if (((u - w.ua) & 63) == 0) {
-            runs++;
-            if (!is_k && dt == 64) s_apart[runs & 7] = 0;
-          }
           const int st = op % NS;
           uint8_t* const dst = sm + st * 2 * S::kOp;
           if (u >= w.rq.no) {
@@ -717,20 +676,22 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
                       make_uint4(codes2<0>(xs[j]), codes2<1>(xs[j]), codes2<2>(xs[j]), codes2<3>(xs[j]));
               }
             } else {
-              // one E for the unit's keys; magnitudes of 0 do not count
+              // one E for the unit's keys, or one a key; magnitudes of 0 do not count
               const uint32_t top = __reduce_max_sync(0xffffffffu, max(most, other));
               const uint32_t far = max(top, (uint32_t)kt::kApart << 23) - ((uint32_t)kt::kApart << 23);
               const bool apart = __any_sync(0xffffffffu, (most && most < far) || (other && other < far));
               const int E = tc_exponent(top);
-              if (dt == 64) put_info(st, u, apart, lim[0] + lim[1], lim[0] == 32 ? -1 : (1 << lim[0]) - 1,
+              if (dt == 64) put_info(st, apart, lim[0] + lim[1], lim[0] == 32 ? -1 : (1 << lim[0]) - 1,
                                      lim[1] == 32 ? -1 : (1 << lim[1]) - 1, E);
+              if (apart && dw < 2) s_e[st * 64 + dt] = (float)tc_exponent(dw == ng - 1 ? most : ng == 2 ? other : 0u);
 #pragma unroll
               for (int gi = 0; gi < 2; gi++) {
                 if (gi >= ng || !mine) break;
                 float s = __uint_as_float(sm0[gi] << 16), m = __uint_as_float(sm0[gi] & 0xFFFF0000u);
                 if (row >= lim[gi] || !(s <= 3.4e38f)) s = m = 0.f;  // not held, or NaN: its scores say so
-                const uint32_t me = h2dup(s * pow2i(24 + kt::kUp - E)), mo = h2dup(s * pow2i(20 + kt::kUp - E)),
-                               cc = h2dup(fmaf(-8.f, s, m) * pow2i(kt::kUp - E));
+                const int e = apart ? tc_exponent(kv4_magnitude(s, m)) : E;
+                const uint32_t me = h2dup(s * pow2i(24 + kt::kUp - e)), mo = h2dup(s * pow2i(20 + kt::kUp - e)),
+                               cc = h2dup(fmaf(-8.f, s, m) * pow2i(kt::kUp - e));
                 const uint32_t xs[4] = {x[gi].x, x[gi].y, x[gi].z, x[gi].w};
 #pragma unroll
                 for (int j = 0; j < 4; j++)
@@ -800,8 +761,10 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
               bar_sync(1, 128);
               const int E = tc_exponent(v.x);
               const bool apart = v.x && v.y + 1u + ((uint32_t)kt::kApart << 23) < v.x;
-              store(a.v_new, pow2i(kt::kUp - E), pow2i(kt::kUp - E), odd);
-              if (dt == 64) put_info(st, u, apart, m + kTcOwn, m >= 32 ? -1 : (1 << m) - 1,
+              const int e = apart ? tc_exponent(big) : E;
+              if (apart && half == 0) s_e[st * 64 + j] = (float)e;
+              store(a.v_new, pow2i(kt::kUp - e), pow2i(kt::kUp - e), odd);
+              if (dt == 64) put_info(st, apart, m + kTcOwn, m >= 32 ? -1 : (1 << m) - 1,
                                      m >= 64 ? -1 : m > 32 ? (1 << (m - 32)) - 1 : 0, E);
             }
           }
@@ -812,19 +775,18 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
       } while (w.next(a, sh));
   } else {
       // -------------------------------------------------------- softmax --
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(216 - S::kDecodeRegs));
       TcWalk<BIAS> w(a, sh);
       const int t = (warp - kt::kSoft) >> 2, st256 = tid - kt::kSoft * 32;
       const int idx = (warp & 3) * 32 + lane;                                // TMEM lane
       const uint32_t tb = tm + t * 256 + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
       const float scale = BIAS ? 1.f : a.s.scale * kLog2e;
-      uint32_t op0 = 0, par = 0, runs = 0;  // par: parity of the units done in either buffer
+      uint32_t op0 = 0, par = 0;  // par: parity of the units done in either buffer
       do {
         const int h = w.head(), rc = w.s - h * w.rq.nc, n = w.ub - w.ua;
         const TcRowsOf<WIDE> rw(a.G * w.rq.m, w.rq.nc, rc);
         const int span = 128 / rw.copies;  // lanes of a copy
         TcRow x;
-        const uint16_t* q;
         {
           const int ridx = idx % span;
           const bool ok = ridx < rw.of(t);
@@ -839,8 +801,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
           x.ref = -INFINITY;
           x.l = 0.f;
           x.any = false;
-          q = a.q + (int64_t)(w.rq.n0 + node) * a.q_stride + hq * D;
-          const uint4* src = reinterpret_cast<const uint4*>(q);
+          const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(w.rq.n0 + node) * a.q_stride + hq * D);
           uint4 v[D / 8];
 #pragma unroll
           for (int i = 0; i < D / 8; i++) v[i] = ok ? src[i] : make_uint4(0, 0, 0, 0);
@@ -879,24 +840,14 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
         __syncwarp();
         if (lane == 0 && (WIDE || t == 0)) mbar_arrive(&q_full[t]);
 
-        for (int i0 = 0; i0 < n; i0 += 64) {
-          const int i1 = min(n, i0 + 64);
+        {
           auto run = [&](auto nc) {
-            tc_softmax<D, BIAS, WIDE, decltype(nc)::value>(a, x, tb, i0 + (WIDE ? 0 : t), i1, op0, par, &s_full[2 * t], op_full,
-                                                           &p_full[2 * t], &o_full[2 * t], s_sc, s_pos, s_info, &s_abort);
+            tc_softmax<D, BIAS, WIDE, decltype(nc)::value>(a, x, tb, WIDE ? 0 : t, n, op0, par, &s_full[2 * t], op_full, &p_full[2 * t],
+                                                           &o_full[2 * t], s_sc, s_pos, s_e, s_info, &s_abort);
           };
           if (WIDE || rw.copies == 1) run(std::integral_constant<int, 64>());
           else if (rw.copies == 2) run(std::integral_constant<int, 32>());
           else run(std::integral_constant<int, 16>());
-          runs++;
-          uint64_t apart = s_apart[runs & 7] & (~0ull >> (64 - (i1 - i0)));
-          if (!WIDE) apart &= 0x5555555555555555ull << t;  // this tile's units, which it has waited for
-          if (apart && x.live) {
-            for (int b = 0; b < 2; b++) wait(&o_full[2 * t + b], (par >> b) ^ 1);
-            tc_fence_after();
-            for (; apart; apart &= apart - 1)
-              tc_apart<D, BIAS>(a, x, w.rq, w.r, h, w.ua + i0 + __ffsll((long long)apart) - 1, 64 / rw.copies, q, scale, tb);
-          }
         }
         if (x.any) {
           // the last two products may be under way

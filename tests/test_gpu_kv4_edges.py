@@ -474,3 +474,46 @@ def test_a_capture_before_any_other_call(M):
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
     assert c.status() == 0
+
+
+# ----------------------------------------------- second kernels in graphs --
+
+def test_append_and_evict_in_a_graph(M):
+    """Their second kernels begin while the first end; replayed, they do what
+    the eager calls do."""
+    g = torch.Generator().manual_seed(6)
+    n = [150, 64, 0]
+    K, V = [ref.bf16(rnd(g, x, 2, 128)) for x in n], [ref.bf16(rnd(g, x, 2, 128)) for x in n]
+    def fresh():
+        c = make(M, K, V, [torch.arange(x) for x in n], room=90)
+        c.weight.copy_(torch.rand(c.weight.shape, generator=torch.Generator().manual_seed(5)))
+        return c, M.KV4Cache(np.arange(12).reshape(3, 4), 12, 2, 128, 32)
+    rows, x = M.RequestRows([0, 5, 6, 10]), dev(rnd(g, 10, 2, 128))
+    y, count = dev(rnd(g, 10, 2, 128)), i32([3, 1, 4])
+    def step(c, dst):
+        c.append(x, y, rows, count=count)
+        c.evict(dst, 100, recent=10, sinks=2)
+    c, dst = fresh()
+    step(c, dst)  # the workspace
+    eager = []
+    c, dst = fresh()
+    for _ in range(3):
+        step(c, dst)
+        eager.append([t.clone() for t in (c.ctx_len, c.pos, c.blocks, dst.ctx_len, dst.pos, dst.weight)] +
+                     list(dst.read(M.RequestRows(np.cumsum([0] + dst.ctx_len.tolist())))))
+    c, dst = fresh()
+    first = [t.clone() for t in (c.ctx_len, c.pos, c.blocks, c.weight)]
+    step(c, dst)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(c, dst)
+    for t, v in zip((c.ctx_len, c.pos, c.blocks, c.weight), first):
+        t.copy_(v)
+    dst.pos.zero_(), dst.weight.zero_(), dst.ctx_len.zero_()
+    for want in eager:
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [c.ctx_len, c.pos, c.blocks, dst.ctx_len, dst.pos, dst.weight]
+        got += list(dst.read(M.RequestRows(np.cumsum([0] + dst.ctx_len.tolist()))))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert c.status() == 0 and c.ctx_len.tolist() == [159, 67, 12]

@@ -657,6 +657,14 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+def _empty(stream, shape, dtype, device):
+    """A tensor of the call's stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _here(t, index, what):
     """Kernels read and write only what lies on their own GPU."""
     if t.get_device() != index:
@@ -828,9 +836,8 @@ class KV4Cache:
         self._rows(rows)
         if dtype not in _BITS16:
             raise ValueError("dtype must be bfloat16, or int16 for its bits")
-        with _on(stream):
-            k = torch.empty(rows.n, self.n_kv_heads, self.head_dim, dtype=dtype, device=self.device)
-            v = torch.empty_like(k)
+        k = _empty(stream, (rows.n, self.n_kv_heads, self.head_dim), dtype, self.device)
+        v = _empty(stream, k.shape, dtype, self.device)
         check(self._lib.sd_kv4_read(self._ref, rows.cu_ptr, rows.cu_host_ptr, rows.R, self._at(at), k.data_ptr(),
                                     v.data_ptr(), self._status_ptr, self._stream(stream)))
         return k, v
@@ -856,15 +863,13 @@ class KV4Cache:
                 raise ValueError("k and v must have one row stride")
             kp, vp_ = k.data_ptr(), v.data_ptr()
         if out is None:
-            with _on(stream):
-                out = torch.empty_like(q) if q.is_contiguous() else torch.empty(n, hq, D, dtype=q.dtype, device=q.device)
+            out = _empty(stream, q.shape, q.dtype, self.device)
         elif out.shape != q.shape or out.dtype not in _BITS16 or not out.is_contiguous():
             raise ValueError("out must be contiguous bf16 of q's shape")
         else:
             _here(out, self._index, "out")
         if lse is None:
-            with _on(stream):
-                lse = torch.empty(n, hq, dtype=torch.float32, device=q.device)
+            lse = _empty(stream, (n, hq), torch.float32, self.device)
         elif lse.dtype is not torch.float32 or lse.shape != (n, hq) or not lse.is_contiguous():
             raise ValueError("lse must be contiguous float32 [rows][n_q_heads]")
         else:

@@ -987,10 +987,17 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
         const int gq = ok ? rho / n : 0, node = ok ? s_node[rho - gq * n] : 0, hq = h * a.G + gq;
         // a row that sees nothing, or whose lse is not finite, gives no weight:
         // its queries (NaN, perhaps) are taken as 0 and its lse as infinite
-        const float lse = ok ? b.lse_in[(int64_t)(n0 + node) * a.hq + hq] : INFINITY;
-        const bool gives = fabsf(lse) < INFINITY;
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (ok) x = *reinterpret_cast<const uint4*>(a.q + (int64_t)(n0 + node) * a.q_stride + hq * D + oct * 8);
+        float lse = INFINITY, rw = 1.f, slope = 0.f;
+        int pos = ctx + node;
+        if (ok) {
+          x = *reinterpret_cast<const uint4*>(a.q + (int64_t)(n0 + node) * a.q_stride + hq * D + oct * 8);
+          lse = b.lse_in[(int64_t)(n0 + node) * a.hq + hq];
+          if (b.row_weight) rw = b.row_weight[n0 + node];
+          if (BIAS && a.s.slopes) slope = a.s.slopes[hq];
+        }
+        if (BIAS && a.row_pos) pos = a.row_pos[n0 + node];
+        const bool gives = fabsf(lse) < INFINITY;
         if (!gives) x = make_uint4(0, 0, 0, 0);
         const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
         float f[8], qs = 0.f, big = 0.f;
@@ -1011,10 +1018,8 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
             make_uint4(pack_f16x2(f[0] * up, f[4] * up), pack_f16x2(f[1] * up4, f[5] * up4),
                        pack_f16x2(f[2] * up, f[6] * up), pack_f16x2(f[3] * up4, f[7] * up4));
         if (oct == 0) {
-          s_row[row] = make_float4(pow2i(24 - e) * sc2, qs * sc2, gives ? lse * kLog2e : INFINITY,
-                                   gives ? (b.row_weight ? b.row_weight[n0 + node] : 1.f) : 0.f);
-          s_bias[row] = make_float2(BIAS && a.s.slopes && gives ? a.s.slopes[hq] : 0.f,
-                                    __int_as_float(a.row_pos ? a.row_pos[n0 + node] : ctx + node));
+          s_row[row] = make_float4(pow2i(24 - e) * sc2, qs * sc2, gives ? lse * kLog2e : INFINITY, gives ? rw : 0.f);
+          s_bias[row] = make_float2(gives ? slope : 0.f, __int_as_float(pos));
         }
       }
       __syncthreads();
@@ -1026,7 +1031,7 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
         float old = 0.f;  // not looked at before the end
         if (t < ctx) old = pass ? w_out[t] : w_in[t];
         if (!kv4_wait(&bar[stage], (used / NS) & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(31));
-        bool ok = s_ok[warp * NS + stage] != 0;  // of the slot that this lane writes
+        const bool ok = s_ok[warp * NS + stage] != 0;
         uint32_t kw[4][D / 32];
         float ks[4], km[4];
         int kp[4];
@@ -1043,8 +1048,6 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
           const uint32_t w = *reinterpret_cast<const uint32_t*>(st + 16 * D + (8 * i + g) * 4);
           ks[i] = __uint_as_float(w << 16);
           km[i] = fmaf(-8.f, ks[i], __uint_as_float(w & 0xFFFF0000u));
-          // a key held as NaN collects nothing: who sees it has no finite lse
-          if (ks[i] != ks[i]) ks[i] = km[i] = 0.f, ok &= i != q;
           kp[i] = BIAS ? *reinterpret_cast<const int*>(st + kv4_half(D) + (8 * i + g) * 4) : 0;
         }
         __syncwarp();
@@ -1111,14 +1114,15 @@ __global__ void __launch_bounds__(kObsWarps * 32, 2) k_kv4_observe(const __grid_
           f2unpack(sum2[i], lo, hi);
           sum[i] = lo + hi;
         }
-        float mine = 0.f;
+        float mine = 0.f, s = 0.f;  // of the slot that this lane writes
 #pragma unroll
         for (int i = 0; i < 4; i++) {
           sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
           sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-          if (q == i) mine = sum[i];
+          if (q == i) mine = sum[i], s = ks[i];
         }
-        if (t < ctx) w_out[t] = (pass ? old : b.decay * old) + (ok ? mine : 0.f);
+        // a key held as NaN collects nothing: who sees it has no finite lse
+        if (t < ctx) w_out[t] = (pass ? old : b.decay * old) + (ok && s == s ? mine : 0.f);
       }
       __syncthreads();  // s_q, s_row and s_node are free again
     }

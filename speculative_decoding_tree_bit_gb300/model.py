@@ -836,8 +836,8 @@ class KV4Cache:
         self._rows(rows)
         if dtype not in _BITS16:
             raise ValueError("dtype must be bfloat16, or int16 for its bits")
-        k = _empty(stream, (rows.n, self.n_kv_heads, self.head_dim), dtype, self.device)
-        v = _empty(stream, k.shape, dtype, self.device)
+        k = _empty(stream, (rows.n, self.n_kv_heads, self.head_dim), dtype, self.blocks.device)
+        v = torch.empty_like(k) if stream is None else _empty(stream, k.shape, dtype, k.device)
         check(self._lib.sd_kv4_read(self._ref, rows.cu_ptr, rows.cu_host_ptr, rows.R, self._at(at), k.data_ptr(),
                                     v.data_ptr(), self._status_ptr, self._stream(stream)))
         return k, v
@@ -863,13 +863,13 @@ class KV4Cache:
                 raise ValueError("k and v must have one row stride")
             kp, vp_ = k.data_ptr(), v.data_ptr()
         if out is None:
-            out = _empty(stream, q.shape, q.dtype, self.device)
+            out = torch.empty_like(q) if stream is None and q.is_contiguous() else _empty(stream, q.shape, q.dtype, q.device)
         elif out.shape != q.shape or out.dtype not in _BITS16 or not out.is_contiguous():
             raise ValueError("out must be contiguous bf16 of q's shape")
         else:
             _here(out, self._index, "out")
         if lse is None:
-            lse = _empty(stream, (n, hq), torch.float32, self.device)
+            lse = _empty(stream, (n, hq), torch.float32, q.device)
         elif lse.dtype is not torch.float32 or lse.shape != (n, hq) or not lse.is_contiguous():
             raise ValueError("lse must be contiguous float32 [rows][n_q_heads]")
         else:

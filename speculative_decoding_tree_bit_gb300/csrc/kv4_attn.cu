@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(W * 32, 2) k_kv4_attn(const __grid_constant__ 
   // records.  A lane holds the address of every 32nd of the warp's records.
   int r = sh.r0, s = sh.s0, seg = sh.seg0;
   const int u0 = sh.u0, u1 = sh.u1;
-  Kv4Req rq = kv4_req<RT, 1, BIAS>(a, r);
+  Kv4Req rq = BIAS && NT == 1 ? sh.rq : kv4_req<RT, 1, BIAS>(a, r);  // short calls wait for the window's check once
   int ua = u0 - seg, ub = min(rq.nu, u1 - seg);
   const uint8_t* addr;
   auto first_record = [&]() {  // the first of the segment's records that falls to this warp

@@ -193,6 +193,7 @@ __device__ __forceinline__ Kv4Req kv4_req(const Kv4AttnArgs& a, int r) {
 // request r0.
 struct Kv4Share {
   int r0, s0, seg0, u0, u1, each, more;
+  Kv4Req rq;  // of request r0
   __device__ __forceinline__ int first(int c) const { return c * each + min(c, more); }
   __device__ __forceinline__ int cta_of(int u) const {
     const int big = more * (each + 1);
@@ -249,6 +250,7 @@ __device__ __forceinline__ void kv4_share(const Kv4AttnArgs& a, int width, Kv4Sh
       }
       if (u0 >= lo && u0 < lo + a.c.hkv * rq.nc * rq.nu) {
         sh.r0 = base + lane;
+        sh.rq = rq;
         sh.s0 = (u0 - lo) / rq.nu;
         sh.seg0 = lo + (u0 - lo) / rq.nu * rq.nu;
       }

@@ -613,9 +613,13 @@ int sd_kv4_read(const sd_kv4* c, const int32_t* cu, const int32_t* cu_host, int3
  * launch; a longer request is read whole all the same.
  * out: bf16 [rows][n_q_heads][head_dim], 0 in a row that sees no key; lse
  * (optional): fp32 [rows][n_q_heads], the natural log of the sum of exp of
- * the scores, -inf in such a row.  Scores and sums are fp32; a softmax weight
- * enters its product with 11 bits (the rows' own values: 16), against the
- * output's 8.  An own value row with a NaN or an infinity counts as NaN in every
+ * the scores, -inf in such a row.  Scores and sums are fp32.  A softmax weight
+ * enters its product with 11 bits, against the output's 8 (that of one of the
+ * rows' own values with 16 where a kv head has at most 64 rows); with more than
+ * 64 rows a kv head the values, and their m - 8 s, have 11 bits too.  Only what a
+ * row sees bears on its weights and values.  Queries up to 2^115 in size, keys up
+ * to 2^110, values that a row sees up to 2^100.  An own value row with a NaN or an
+ * infinity counts as NaN in every
  * dim, as a held one does; out and lse are NaN in the rows that see such a row
  * and in no others.
  * workspace: sd_kv4_attn_workspace bytes (rows = cu_host[R]), 256-byte

@@ -11,8 +11,9 @@ namespace sdv {
 // least and greatest value come from four shuffles.  The bytes are few (4 D in,
 // D + 12 out per row and head); what bounds it is issue, 82% active: about 250
 // instructions a warp per row and head.  Four heads a warp share the row's
-// addresses and request (one head a warp: 92 us where four take 63).  Measured:
-// 16384 rows of 8 heads, D = 128: 37 us, 2.3 TB/s.
+// addresses and request (with one, storing and reading back 16384 rows took 92 us
+// where four took 63; both take 52 now).  Measured: 16384 rows of 8 heads, D = 128,
+// stored: 37 us, 2.3 TB/s of the 85 MB read and written.
 
 constexpr int kHeads = 4;
 

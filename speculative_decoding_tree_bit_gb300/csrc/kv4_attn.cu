@@ -39,9 +39,10 @@ namespace sdv {
 // lengths; two CTAs an SM, so that one works while the other joins.
 //
 // Measured, 32 query and 8 kv heads, D = 128: 32 tokens over 1500 to 8192 keys 50
-// us, 3.5 TB/s; 32 chains of 8 rows over 1024 to 4096 keys with a cap 90 us, 105 TFLOP/s (two tiles of rows a warp, six
-// warps; four tiles, four warps: 135 where two took 110); a tree of 16 over 2048
-// keys 25 us, most of it latency.
+// us, 3.4 TB/s (the ALU pipe 51% busy, issue 53%); 32 chains of 8 rows over 1024
+// to 4096 keys with a cap 90 us, 106 TFLOP/s (two tiles of rows a warp, six warps;
+// four tiles, four warps: 135 where two took 110); a tree of 16 over 2048 keys 25
+// us, most of it latency.
 
 constexpr int kMaxCtas = 512;
 constexpr float kUnset = 3e38f;  // a row's reference before it sees a key
@@ -825,7 +826,7 @@ struct Kv4ObserveArgs {
 // head)'s groups of 32 slots are dealt over the CTAs like the attention's.
 // More than kObsRows rows are taken in passes that add to the output.
 // Measured: 32 requests of 2 to 5 rows, 32 query and 8 kv heads, over 1500 to 8192
-// keys with positions: 43 us, 2.3 TB/s, 16 warps an SM waiting on their own
+// keys with positions: 41 us, 2.4 TB/s, 16 warps an SM waiting on their own
 // products and exponentials.  (Two tiles of rows at a time, for one making of the
 // codes' words: 59 where one takes 53.)
 
@@ -1161,13 +1162,16 @@ static int launch_observe(const Kv4ObserveArgs& b, int64_t units, bool bias, cud
 }
 
 // Rows (query heads x nodes) that one kv head may have on the warp kernel;
-// more take the tensor cores.  Measured at 8 kv heads, D = 128, warp kernel
-// against tensor cores: 96 rows, one request of 2000 / 16000 / 65536 keys:
-// 27 / 51 / 139 us against 25 / 47 / 96; 64 rows: 20 / 44 / 104 against
-// 23 / 47 / 94, eight requests of 2000 / 16000: 41 / 178 against 44 / 155;
-// 32 rows, the same: 33 / 105 against 39 / 146.  (The contexts' lengths are on the
-// device, so the rule goes by the rows alone.)  With one tile of eight rows
-// a warp (NT = 1) eight warps fit, with two six.
+// more take the tensor cores.  Measured at 8 kv heads, D = 128, calls one after
+// another from a graph, warp kernel against tensor cores, us:
+//   rows   one request of 2000, 16000, 65536 keys    eight of 2000, 16000
+//   96     19, 45, 128 / 20, 46, 100                 52, 242 / 46, 173
+//   64     16, 37, 92 / 19, 43, 91                   36, 165 / 41, 151
+//   32     16, 28, 58 / 18, 42, 90                   28, 94 / 40, 153
+// The rule goes by the rows of the largest request alone: at 64 rows and the
+// longest contexts the tensor cores would save a tenth, and a batch of one large
+// tree and single tokens would do better on both kernels.  With one tile of eight
+// rows a warp (NT = 1) eight warps fit, with two six.
 constexpr int kWarpRows = 64;
 
 template <int D>

@@ -23,7 +23,7 @@
 //    most 2^15).  So weights down to 2^-17 of the row's greatest p |v| keep their 11
 //    bits, down to 2^-28 count, and nothing that a row does not see moves its
 //    weights or values.  (A factor per key in every unit, not in those taken apart
-//    alone: 412 us where the tree of 64 below takes 362.)
+//    alone: 412 us where the tree of 64 below took 362.)
 // (18 and 19 do nothing: they complete a warpgroup.  Registers a scheduler:
 // 5 warps x 96 = 2 x 72 decoding + 2 x 144 softmax + 48, or 80 and 136, 64 and 152.)
 // WIDE: the first rows of a segment are tile 0's, the others tile 1's, up to
@@ -36,7 +36,7 @@
 // of a segment that spans CTAs are joined by a second kernel, in a fixed order.
 //
 // Measured: a tree of 64 with 40 query and 8 kv heads over 131072 keys, D = 128
-// (WIDE, two segments of 160 rows a kv head): 362 us, 475 TFLOP/s; with every
+// (WIDE, two segments of 160 rows a kv head): 366 us, 470 TFLOP/s; with every
 // unit taken apart 603.  The 160 rows are split 96 / 64, so that the schedulers
 // have 2, 2, 1 and 0 softmax warps, and the products run 512 rows for 320; bound
 // by the two schedulers' softmax warps, which wait for tensor memory and their own
@@ -161,8 +161,9 @@ __device__ __forceinline__ int expo(uint32_t bits) { return (int)(bits >> 23 & 2
 
 // A bound on the magnitudes of a row with scale s and middle m, as bits.
 __device__ __forceinline__ uint32_t kv4_magnitude(float s, float m) { return __float_as_uint(fmaf(8.f, s, fabsf(m))); }
-// E of values of magnitude at most |x| (bits), which lie below 2^E.
-__device__ __forceinline__ int tc_exponent(uint32_t bits) { return min(max(expo(bits) + 1, -90), 126); }
+// E of values of magnitude at most |x| (bits), which lie below 2^E; past 2^121 the
+// operands have to be finite, no more.
+__device__ __forceinline__ int tc_exponent(uint32_t bits) { return min(max(expo(bits) + 1, -90), 121); }
 
 // A CTA's walk over its segments, by whole warps.
 template <bool BIAS>
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
                 const uint32_t vw = *reinterpret_cast<const uint32_t*>(v + 16 * D + lane * 4);
                 const uint32_t big = kv4_magnitude(__uint_as_float(vw << 16), __uint_as_float(vw & 0xFFFF0000u));
                 other = most;
-                most = lane < lim[gi] && big < 0x7F800000u ? big : 0;
+                most = lane < lim[gi] && big <= 0x7F800000u ? min(big, 0x7F7FFFFFu) : 0;  // NaN does not count
               }
             }
             __syncwarp();
@@ -689,6 +690,7 @@ __global__ void __launch_bounds__(kt::kThreads, 1) k_kv4_attn_tc(const __grid_co
                 if (gi >= ng || !mine) break;
                 float s = __uint_as_float(sm0[gi] << 16), m = __uint_as_float(sm0[gi] & 0xFFFF0000u);
                 if (row >= lim[gi] || !(s <= 3.4e38f)) s = m = 0.f;  // not held, or NaN: its scores say so
+                s = fminf(s, 3e35f);  // below 2^118: s 2^(24 + kUp - E) is finite
                 const int e = apart ? tc_exponent(kv4_magnitude(s, m)) : E;
                 const uint32_t me = h2dup(s * pow2i(24 + kt::kUp - e)), mo = h2dup(s * pow2i(20 + kt::kUp - e)),
                                cc = h2dup(fmaf(-8.f, s, m) * pow2i(kt::kUp - e));

@@ -290,6 +290,22 @@ def test_a_huge_value_that_no_row_or_one_row_sees(M, m, G, D, where, huge):
 
 
 @pytest.mark.parametrize("m,G,D", SHAPES)
+def test_the_greatest_finite_values_where_no_row_sees_them(M, m, G, D):
+    g = torch.Generator().manual_seed(m + 7 * G)
+    n, hkv = 290, 2
+    K, k = ref.bf16(rnd(g, n, hkv, D)), ref.bf16(rnd(g, m, hkv, D))
+    V, v = rnd(g, n, hkv, D), rnd(g, m, hkv, D)
+    huge = lambda *s: 1e38 + 2e38 * torch.rand(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    V[3], V[64:70], V[99] = huge(hkv, D), huge(6, hkv, D), -huge(hkv, D)
+    V[50] = 2.4e38 + 0.45 * huge(hkv, D) - 0.45e38  # 8 s + m passes fp32
+    anc = [(1 << i) | 1 for i in range(m)]
+    if m > 1:
+        v[m - 1] = huge(hkv, D)
+        anc[m - 1] = 1  # nobody's, not even its own
+    check_values(M, K, ref.bf16(V), ref.bf16(1.5 * rnd(g, m, hkv * G, D)), k, ref.bf16(v), G, anc, start=100)
+
+
+@pytest.mark.parametrize("m,G,D", SHAPES)
 def test_a_large_value_of_little_weight(M, m, G, D):
     """Seen, but with a weight that makes it count as little as the others."""
     g = torch.Generator().manual_seed(m + 3 * G)

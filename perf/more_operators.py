@@ -198,7 +198,7 @@ def prepare(case, seed):
                                                             slow=c["slow"])}[c["scaling"]]()
             st["op"] = sdv.Rope(c["d"], c["rot"], c["base"], interleaved=c["interleaved"], scaling=scaling)
         elif c["op"] == "sample":
-            st["op"] = sdv.Sampler(c["V"], c["n"])
+            st["op"] = sdv.sample
         else:
             st["op"] = sdv.PromptAttention(c["hq"], c["hkv"], c["d"])
             st["rows"], st["keys"] = sdv.RequestRows(st["rows"]), sdv.RequestRows(st["keys"])

@@ -664,6 +664,116 @@ size_t sd_kv4_evict_workspace(int32_t R, int32_t n_kv_heads, int32_t budget);
 int sd_kv4_evict(const sd_kv4* src, const sd_kv4* dst, int32_t R, int32_t budget, int32_t recent, int32_t sinks,
                  void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
 
+/* ------------------------------------------------- rotary positions -- */
+/* Rotary positions of queries and keys outside the step (its own q/k/v
+ * product turns them in its epilogue, half layout, all 128 dims): rows that go
+ * to sd_prompt_attn, sd_kv4_append and sd_kv4_attn.  No counterpart in the pages.
+ * Pair i of a head's first rot_dim dims, (i, i + rot_dim / 2) or where
+ * interleaved (2 i, 2 i + 1), turns by the angle pos f_i:
+ *   (a, b) -> amplitude (a cos - b sin, a sin + b cos);
+ * the dims from rot_dim on are copied.  One rounding to bf16, at the end.
+ *
+ * f_i = base^(-2 i / rot_dim), scaled for contexts past the trained one:
+ *   SD_ROPE_LINEAR  f / factor;
+ *   SD_ROPE_BANDS   with t = original f / 2 pi (turns in the trained context):
+ *                   f where t > high, f / factor where t < low, between them
+ *                   (t - low) / (high - low) of the first and the rest of the second;
+ *   SD_ROPE_RAMP    f below pair lo, f / factor from pair hi on, in proportion
+ *                   between them; lo, hi: the pairs of `high` and `low` turns in
+ *                   the trained context, rounded down and up, kept in 0 .. rot_dim - 1
+ *                   (hi = lo: 0.001 apart).
+ * amplitude <= 0: 0.1 ln(factor) + 1 for SD_ROPE_RAMP, else 1. */
+enum { SD_ROPE_PLAIN = 0, SD_ROPE_LINEAR = 1, SD_ROPE_BANDS = 2, SD_ROPE_RAMP = 3 };
+typedef struct {
+  int32_t kind;
+  double factor, original, low, high, amplitude;
+} sd_rope_scaling;
+
+/* The pairs' turns a position, f_i / 2 pi, as fractions of 2^64 (host, u64
+ * [rot_dim / 2]), and the amplitude.  pos turns mod 2^64 is the angle of any int32
+ * position, to 2^-33 of a turn at worst.  scaling null: plain.  Errors:
+ * SD_ERR_INVALID_ARG (rot_dim odd or not positive; base, factor, original, low or
+ * high not positive and finite where used; low >= high). */
+int sd_rope_turns_host(int32_t rot_dim, double base, const sd_rope_scaling* scaling, uint64_t* turns, float* amplitude);
+
+/* Rotate the rows of q and of k (k null with n_kv_heads 0) by their positions
+ * (device int32 [rows]; a negative one turns back, which is also the gradient).
+ * q, k, q_out, k_out: bf16, rows *_stride elements apart, a row [heads][head_dim]
+ * contiguous; out may be the input itself (same pointer and stride), else they
+ * must not overlap.  turns: device copy of sd_rope_turns_host's.  1 <= head_dim <=
+ * 1024, rot_dim even, <= head_dim.  Asynchronous on `stream`.  Errors:
+ * SD_ERR_INVALID_ARG, SD_ERR_CUDA. */
+int sd_rope(const uint64_t* turns, float amplitude, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+            const int32_t* pos, int32_t rows, const uint16_t* q, int64_t q_stride, int32_t n_q_heads, uint16_t* q_out,
+            int64_t q_out_stride, const uint16_t* k, int64_t k_stride, int32_t n_kv_heads, uint16_t* k_out,
+            int64_t k_out_stride, void* stream);
+
+/* ------------------------------------------- attention over prompts -- */
+/* Causal attention of whole prompts, or of the next chunk of one: the bf16 form
+ * that fills a cache, beside sd_kv4_attn, which takes at most 64 rows a request
+ * over cached keys.  No counterpart in the pages.  Request r owns rows cu_q[r] ..
+ * cu_q[r+1]-1 of q and keys cu_k[r] .. cu_k[r+1]-1 of k and v (int32 [R+1] on the
+ * device and the same values on the host; cu_k null: cu_q).  With m rows and n
+ * keys, row i stands at position n - m + i and sees the keys 0 .. n - m + i, of them
+ * with score->window > 0 those less than window back; a request may have no rows, or
+ * fewer keys than rows (its first rows then see nothing).  Scores as sd_kv4_score
+ * has them (scale, softcap, slopes, window; start must be null: requests are
+ * packed), position of key j being j.
+ * q: bf16, rows q_stride elements apart, each [n_q_heads][head_dim]; k, v: rows
+ * kv_stride apart, each [n_kv_heads][head_dim]; all 16-byte aligned, strides
+ * multiples of 8; head_dim 64 or 128; n_q_heads a multiple of n_kv_heads, at most
+ * 128 query heads a kv head.
+ * out: bf16 [rows][n_q_heads][head_dim], 16-byte aligned, 0 in a row that sees no
+ * key; lse (optional): fp32 [rows][n_q_heads], the natural log of the sum of exp of
+ * the scores, -inf in such a row.  Scores, sums and outputs are accumulated in
+ * fp32; a softmax weight enters its product in bf16, as the output leaves.  What a
+ * row does not see does not bear on it, a NaN or an infinity among it; rows behind
+ * cu_q[R] are left as they were.
+ * workspace: sd_prompt_attn_workspace bytes, 256-byte aligned, any content; calls
+ * that share one must not overlap.  *status (device int32, caller-owned) gets
+ * SD_ERR_TIMEOUT where a bounded wait gave up.  Asynchronous on `stream`.  Errors:
+ * SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED (head_dim, heads), SD_ERR_WORKSPACE,
+ * SD_ERR_CUDA. */
+size_t sd_prompt_attn_workspace(int32_t head_dim);
+int sd_prompt_attn(const uint16_t* q, int64_t q_stride, int32_t n_q_heads, const uint16_t* k, const uint16_t* v,
+                   int64_t kv_stride, int32_t n_kv_heads, int32_t head_dim, const int32_t* cu_q,
+                   const int32_t* cu_q_host, const int32_t* cu_k, const int32_t* cu_k_host, int32_t R,
+                   const sd_kv4_score* score, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                   int32_t* status, void* stream);
+
+/* ------------------------------------------------- sampled tokens -- */
+/* A token of each row of logits from given random numbers: sampled decoding
+ * beside the greedy argmax.  ("SpecPilot ...", "Core Idea", item 4, forces the
+ * target's own tokens; tokens sampled at every node in the argmax's place make
+ * sd_accept's walk accept exactly what sampling token by token would have given.)
+ * Of a row's tokens, by falling logit, equal ones by index, with weights w =
+ * exp((logit - most) / temperature):
+ *   top_k > 0 keeps the first top_k; min_p > 0 of those the ones of w >= min_p; top_p
+ *   < 1 of those the shortest run that holds top_p of their sum, one at least;
+ *   the token is the first whose running sum passes u times the sum W of what is
+ *   kept.
+ * temperature <= 0 keeps the first alone (greedy).  A NaN and -inf are never kept
+ * (a row of nothing else: token -1, logprob -inf, kept 0); beside +inf every other
+ * token weighs 0.  -0 and 0 are equal.  Weights and their sums are held to 2^-45 of
+ * the greatest weight, in whole numbers, so a result does not depend on the order
+ * of its sums.
+ * logits: bf16 [rows][vocab], row_stride elements apart, any alignment; u: fp32
+ * [rows], clamped to [0, 1 - 2^-24], NaN as 0.  Each setting is one number for all
+ * rows, or where its pointer is set a device array [rows].  tokens int32 [rows];
+ * logprob (optional) fp32 [rows]: ln(w / W) of the token; kept (optional) int32
+ * [rows].  1 <= vocab <= 524160.  Asynchronous on `stream`, no workspace.
+ * Errors: SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED (vocab), SD_ERR_CUDA. */
+typedef struct {
+  float temperature, top_p, min_p;
+  int32_t top_k;
+  const float* temperature_rows;
+  const float* top_p_rows;
+  const float* min_p_rows;
+  const int32_t* top_k_rows;
+} sd_sampling;
+int sd_sample(const uint16_t* logits, int64_t row_stride, int32_t rows, int32_t vocab, const sd_sampling* settings,
+              const float* u, int32_t* tokens, float* logprob, int32_t* kept, void* stream);
+
 /* -------------------------------------------------------- tiny verify -- */
 /* One linear layer and an lm_head: logits = (bf16(act W1^T)) Wlm^T, argmax
  * per node in fp32, then greedy acceptance over the tree.  act: bf16 [M][K];

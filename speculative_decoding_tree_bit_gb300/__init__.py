@@ -74,6 +74,16 @@ class KV4ScoreArgs(ctypes.Structure):
                 ("start", vp)]
 
 
+class RopeScalingArgs(ctypes.Structure):
+    _fields_ = [("kind", i32), ("factor", ctypes.c_double), ("original", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class Sampling(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("top_p", ctypes.c_float), ("min_p", ctypes.c_float), ("top_k", i32),
+                ("temperature_rows", vp), ("top_p_rows", vp), ("min_p_rows", vp), ("top_k_rows", vp)]
+
+
 P = ctypes.POINTER
 _SIGS = {
     "sd_last_error": (ctypes.c_char_p, []),
@@ -126,6 +136,13 @@ _SIGS = {
                                       ctypes.c_float, vp, vp, vp]),
     "sd_kv4_evict_workspace": (ctypes.c_size_t, [i32, i32, i32]),
     "sd_kv4_evict": (ctypes.c_int, [P(KV4), P(KV4), i32, i32, i32, i32, vp, ctypes.c_size_t, vp, vp]),
+    "sd_rope_turns_host": (ctypes.c_int, [i32, ctypes.c_double, P(RopeScalingArgs), vp, P(ctypes.c_float)]),
+    "sd_rope": (ctypes.c_int, [vp, ctypes.c_float, i32, i32, i32, vp, i32, vp, i64, i32, vp, i64, vp, i64, i32, vp, i64,
+                               vp]),
+    "sd_prompt_attn_workspace": (ctypes.c_size_t, [i32]),
+    "sd_prompt_attn": (ctypes.c_int, [vp, i64, i32, vp, vp, i64, i32, i32, vp, vp, vp, vp, i32, P(KV4ScoreArgs), vp, vp,
+                                      vp, ctypes.c_size_t, vp, vp]),
+    "sd_sample": (ctypes.c_int, [vp, i64, i32, i32, P(Sampling), vp, vp, vp, vp, vp]),
     "sd_tiny_workspace": (ctypes.c_size_t, [i64, i64, i64, i32]),
     "sd_tiny_verify": (ctypes.c_int, [P(W12Tensor), P(W12Tensor), vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp,
                                       ctypes.c_size_t, vp]),

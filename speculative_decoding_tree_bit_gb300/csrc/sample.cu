@@ -1,0 +1,571 @@
+// Tokens sampled from logits: temperature, top-k, min-p, top-p.
+//
+// A bf16 logit is one of 65536 keys, so a row is a histogram: everything a
+// sampled token depends on follows from how often each key occurs, and its weight
+// is computed once a key.  One cluster takes a row: each CTA counts its slice in
+// shared memory (16-bit counters, so at most 65528 tokens a CTA), the CTAs sum the
+// binades (128 keys) that occur, one warp walks the binades' counts and sums down to
+// the cuts and the token's key, and the CTA that holds the key's occurrence looks it
+// up in its slice.
+//
+// Weights are whole numbers, 2^44 exp((logit - most) / temperature), from pairs
+// of fp32 values good to about 2^-46, and their sums are 64-bit whole numbers (2^44
+// times 2^19 tokens): results do not depend on the order of a sum, and a u next
+// to a border of 2^-17 (1 / vocab) falls on the right side.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace sdv {
+
+namespace sp {
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kSlice = 65528;          // tokens of a CTA, at most: whole vectors, 16-bit counters
+constexpr int kMaxCluster = 8;
+constexpr int kMaxVocab = (1 << 19) - 128;
+constexpr int kBlocks = 513;           // binades of either sign, and zero's once more
+constexpr int kOne = 44;               // weights are multiples of 2^-kOne
+constexpr float kLog2e = 1.4426950408889634f;
+}  // namespace sp
+
+// exp of a double by its series, at compile time (|x| < 1).
+constexpr double cexp(double x) {
+  double t = 1, s = 1;
+  for (int i = 1; i < 30; i++) t *= x / i, s += t;
+  return s;
+}
+struct Exp2Table {
+  float hi[32], lo[32];
+  constexpr Exp2Table() : hi(), lo() {
+    for (int j = 0; j < 32; j++) {
+      const double v = cexp(0.693147180559945309417 * j / 32);
+      hi[j] = (float)v;
+      lo[j] = (float)(v - (double)hi[j]);
+    }
+  }
+};
+__device__ const Exp2Table kExp2 = Exp2Table();
+
+// What a row's weights go by.
+struct RowScale {
+  float most;      // greatest logit
+  float ch, cl;    // log2(e) / temperature as a pair; 0 where greedy
+  float zh, zl;    // log2(min_p) as a pair; -inf: none
+};
+
+// log2 of the weight of logit l as a pair (p + e).
+__device__ __forceinline__ void log2_weight(float l, const RowScale& r, float& p, float& e) {
+  const float s = __fadd_rn(l, -r.most), b = __fadd_rn(s, -l);
+  const float d = __fadd_rn(__fadd_rn(l, -__fadd_rn(s, -b)), __fadd_rn(-r.most, -b));  // l - most = s + d
+  p = __fmul_rn(s, r.ch);
+  e = __fmaf_rn(s, r.ch, -p);
+  e = __fmaf_rn(s, r.cl, e);
+  e = __fmaf_rn(d, r.ch, e);
+}
+
+// Whether the weight of logit l is at least min_p.
+__device__ __forceinline__ bool at_least(float l, const RowScale& r) {
+  float p, e;
+  log2_weight(l, r, p, e);
+  return l >= r.most || __fadd_rn(__fadd_rn(p, -r.zh), __fadd_rn(e, -r.zl)) >= 0.f;
+}
+
+// The weight of logit l <= most in multiples of 2^-44, and as fp32.
+__device__ __forceinline__ uint64_t weight_of(float l, const RowScale& r, const float2* s_exp2, float* w32 = nullptr) {
+  if (l == r.most) {  // beside +inf too
+    if (w32) *w32 = 1.f;
+    return 1ull << sp::kOne;
+  }
+  float p, e;
+  log2_weight(l, r, p, e);
+  if (w32) *w32 = 0.f;
+  if (!(p > -60.f)) return 0;
+  // p + e = m / 32 + f + e, |f| <= 1 / 64
+  const float mf = rintf(p * 32.f);
+  const int m = (int)mf;
+  const float f = __fmaf_rn(mf, -1.f / 32.f, p);
+  constexpr double kLn2 = 0.693147180559945309417;
+  constexpr float ln2h = (float)kLn2, ln2l = (float)(kLn2 - (double)ln2h);
+  const float th = __fmul_rn(f, ln2h);
+  float tl = __fmaf_rn(f, ln2h, -th);
+  tl = __fmaf_rn(f, ln2l, tl);
+  tl = __fmaf_rn(e, ln2h, tl);
+  // e^t - 1 = t + t^2 / 2 + ..., t and t^2 / 2 as pairs
+  const float sq = __fmul_rn(th, th);
+  const float sqe = __fmaf_rn(th, tl + tl, __fmaf_rn(th, th, -sq));
+  const float c3 = __fmul_rn(__fmul_rn(sq, th), __fmaf_rn(th, __fmaf_rn(th, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f));
+  const float h = 0.5f * sq;
+  const float sh = __fadd_rn(th, h);
+  const float se = __fadd_rn(h, -__fadd_rn(sh, -th));
+  const float sl = __fadd_rn(se, __fadd_rn(c3, __fmaf_rn(0.5f, sqe, tl)));
+  // times 2^(j / 32)
+  const int n = m >> 5;
+  const float2 t = s_exp2[m & 31];
+  const float ph = __fmul_rn(t.x, sh);
+  float pl = __fmaf_rn(t.x, sh, -ph);
+  pl = __fmaf_rn(t.x, sl, pl);
+  pl = __fmaf_rn(t.y, sh, pl);
+  const float rh = __fadd_rn(t.x, ph);
+  const float re = __fadd_rn(ph, -__fadd_rn(rh, -t.x));
+  const float rl = __fadd_rn(__fadd_rn(re, pl), t.y);
+  if (w32) *w32 = rh * __int_as_float((127 + n) << 23);
+  // rh has 24 bits: a whole number times 2^-24 at least
+  const uint64_t v = ((uint64_t)(uint32_t)(rh * 16777216.f) << (sp::kOne - 24)) + (int64_t)(int)rintf(rl * 0x1p44f);
+  return n == 0 ? v : n < -sp::kOne - 2 ? 0 : (v + (1ull << (-n - 1))) >> -n;
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 ld_cluster_u2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+struct SampleArgs {
+  const uint16_t* logits;
+  int64_t stride;
+  int rows, V, slice;  // slice: tokens of a CTA, a multiple of 8
+  sd_sampling s;
+  const float* u;
+  int32_t* tokens;
+  float* logprob;
+  int32_t* kept;
+};
+
+struct SampleShared {
+  uint32_t bins[32768];           // counters of keys 2 i and 2 i + 1
+  uint64_t mass[sp::kBlocks];     // of the binades that occur, by falling logit (the first CTA's)
+  uint32_t count[sp::kBlocks];
+  float2 exp2[32];
+  float top[sp::kWarps];
+  uint32_t lo[sp::kWarps], hi[sp::kWarps];
+  uint32_t span[3];               // of the CTA: greatest logit (fp32 bits), least and greatest magnitude
+  float ch, cl, zh, zl;           // RowScale
+  uint32_t key, nth;              // the token's key and which of the CTA's occurrences it is (-1: none here)
+  uint32_t tot[8 * sp::kWarps];   // occurrences a vector round and warp
+  uint32_t at;
+};
+
+// The binades that occur, by falling logit: those of magnitudes e1 .. e0, zero's
+// and the subnormals' (0), then the negative ones.
+struct Binades {
+  int e0, e1;
+  __device__ __forceinline__ int n() const { return 2 * (e1 - e0 + 1) + (e0 > 0); }
+  // raw bits of the binade's first key, the greatest; the others follow by step
+  __device__ __forceinline__ uint32_t exponent(int i, bool& neg) const {
+    const int m = e1 - e0 + 1;
+    neg = i >= m + (e0 > 0);
+    return neg ? e0 + (i - m - (e0 > 0)) : i < m ? e1 - i : 0;
+  }
+};
+
+// Key `j` of 0 .. 127 of a binade in falling order, as raw bits.
+__device__ __forceinline__ uint32_t key_bits(uint32_t e, bool neg, int j) {
+  return (neg ? 0x8000u : 0u) | e << 7 | (neg ? j : 127 - j);
+}
+
+// The counts of a lane's four keys 4 lane .. 4 lane + 3 (falling order) of a
+// binade, over the cluster.
+__device__ __forceinline__ void lane_counts(uint32_t bins, int C, uint32_t e, bool neg, int lane, uint32_t (&c)[4]) {
+  const uint32_t word = ((neg ? 0x8000u : 0u) | e << 7) / 2 + (neg ? 2 * lane : 62 - 2 * lane);
+  c[0] = c[1] = c[2] = c[3] = 0;
+  for (int k = 0; k < C; k++) {
+    const uint2 w = ld_cluster_u2(cluster_map(bins + 4 * word, k));
+    c[0] += w.x & 0xFFFF, c[1] += w.x >> 16, c[2] += w.y & 0xFFFF, c[3] += w.y >> 16;
+  }
+  if (!neg) {
+    const uint32_t a = c[0], b = c[1];
+    c[0] = c[3], c[1] = c[2], c[2] = b, c[3] = a;
+  }
+}
+
+// Sums of `v` over the lanes before this one.
+template <typename T>
+__device__ __forceinline__ T before_lane(T v, int lane) {
+  T run = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T x = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += x;
+  }
+  return run - v;
+}
+
+// ceil or floor of p W for a float 0 <= p < 1.
+__device__ __forceinline__ uint64_t share_of(float p, uint64_t W, bool up) {
+  if (!(p > 0.f)) return 0;
+  const uint32_t b = __float_as_uint(p);
+  const int e = b >> 23;
+  const uint64_t m = (b & 0x7FFFFF) | (e ? 0x800000 : 0);
+  const int k = 150 - (e ? e : 1);  // p = m 2^-k, k >= 24
+  const uint64_t lo = m * W, hi = __umul64hi(m, W);
+  uint64_t q, rest;
+  if (k < 64) {
+    q = hi << (64 - k) | lo >> k;
+    rest = lo << (64 - k);
+  } else {
+    q = k < 128 ? hi >> (k - 64) : 0;
+    rest = (k < 128 ? hi << 1 << (127 - k) : hi) | lo;
+  }
+  return q + (up && rest);
+}
+
+// A place in the falling order: binade i, key j.
+struct Place {
+  int i, j;
+  uint64_t count, mass;  // before key j
+  uint64_t w;            // the key's weight
+};
+
+// By one warp: the first key at which the running count (or mass) of the row
+// reaches `goal` (at least goal, or more than it where `past`).  The caller knows
+// that it does.
+template <bool MASS>
+__device__ Place find(const SampleShared& sh, uint32_t bins, int C, const Binades& b, const RowScale& rs, uint64_t goal,
+                      bool past) {
+  const int lane = threadIdx.x & 31, n = b.n(), each = (n + 31) / 32;
+  const int i0 = min(n, lane * each), i1 = min(n, i0 + each);
+  uint64_t c = 0, m = 0;
+  for (int i = i0; i < i1; i++) c += sh.count[i], m += sh.mass[i];
+  uint64_t cb = before_lane(c, lane), mb = before_lane(m, lane);
+  auto reached = [&](uint64_t x) { return past ? x > goal : x >= goal; };
+  const bool here = reached(MASS ? mb + m : cb + c) && (MASS ? m : c) > 0;
+  const int who = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  Place p = {};
+  if (lane == who) {
+    int i = i0;
+    for (; i < i1 - 1; i++) {
+      if (sh.count[i] && reached(MASS ? mb + sh.mass[i] : cb + sh.count[i])) break;
+      cb += sh.count[i], mb += sh.mass[i];
+    }
+    p.i = i;
+  }
+  p.i = __shfl_sync(0xffffffffu, p.i, max(who, 0));
+  cb = __shfl_sync(0xffffffffu, cb, max(who, 0));
+  mb = __shfl_sync(0xffffffffu, mb, max(who, 0));
+  bool neg;
+  const uint32_t e = b.exponent(p.i, neg);
+  uint32_t k[4];
+  lane_counts(bins, C, e, neg, lane, k);
+  uint64_t w[4];
+  c = m = 0;
+#pragma unroll
+  for (int x = 0; x < 4; x++) {
+    w[x] = k[x] ? weight_of(bf2f((uint16_t)key_bits(e, neg, 4 * lane + x)), rs, sh.exp2) : 0;
+    c += k[x], m += k[x] * w[x];
+  }
+  cb += before_lane(c, lane);
+  mb += before_lane(m, lane);
+  const bool in = reached(MASS ? mb + m : cb + c) && c > 0;
+  const int at = max(__ffs(__ballot_sync(0xffffffffu, in)) - 1, 0);
+  int j = 0;
+  uint64_t ww = 0;
+#pragma unroll
+  for (int x = 0; x < 4; x++) {  // the first of the lane's keys that reaches it
+    const bool before = j == x && !(k[x] && reached(MASS ? mb + k[x] * w[x] : cb + k[x]));
+    if (before && x < 3) cb += k[x], mb += k[x] * w[x], j = x + 1;
+    if (j == x) ww = w[x];
+  }
+  p.j = 4 * at + __shfl_sync(0xffffffffu, j, at);
+  p.count = __shfl_sync(0xffffffffu, cb, at);
+  p.mass = __shfl_sync(0xffffffffu, mb, at);
+  p.w = __shfl_sync(0xffffffffu, ww, at);
+  return p;
+}
+
+__device__ __forceinline__ void tally(SampleShared& sh, uint32_t b, float& top, uint32_t& lo, uint32_t& hi) {
+  const uint32_t mag = b & 0x7FFFu;
+  if (mag > 0x7F80u || b == 0xFF80u) return;
+  if (mag == 0) b = 0;  // -0 is 0
+  atomicAdd(&sh.bins[b >> 1], b & 1 ? 0x10000u : 1u);
+  top = fmaxf(top, __uint_as_float(b << 16));
+  lo = min(lo, mag - 1);  // zero is the greatest
+  hi = max(hi, mag);
+}
+
+__global__ void __launch_bounds__(sp::kThreads, 1) k_sample(const __grid_constant__ SampleArgs a) {
+  extern __shared__ __align__(16) uint8_t smem_sp[];
+  SampleShared& sh = *reinterpret_cast<SampleShared*>(smem_sp);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t C;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(C));
+  const int rank = (int)cluster_rank(), row = blockIdx.x / C;
+
+  // ---- count the slice: vectors on 16-byte addresses, their ends masked
+  const uint16_t* x = a.logits + (int64_t)row * a.stride;
+  const int shift = (int)((reinterpret_cast<uintptr_t>(x) >> 1) & 7);  // tokens before x in its vector
+  const int v0 = rank * (a.slice / 8), v1 = min((a.V + shift + 7) / 8, v0 + a.slice / 8);
+  const uint4* xv = reinterpret_cast<const uint4*>(x - shift);
+  auto token = [&](int v, int k) { return v * 8 + k - shift; };  // of element k of vector v
+  auto load = [&](int v, uint32_t (&w)[4]) {
+    if (v >= v1) {
+      w[0] = w[1] = w[2] = w[3] = 0xFFFFFFFFu;  // NaN
+    } else if (token(v, 0) >= 0 && token(v, 7) < a.V) {
+      const uint4 u = xv[v];
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const int t = token(v, k);
+        const uint32_t e = t >= 0 && t < a.V ? x[t] : 0xFFFFu;
+        w[k / 2] = k & 1 ? w[k / 2] | e << 16 : e;
+      }
+    }
+  };
+  for (int i = tid; i < 8192; i += sp::kThreads) reinterpret_cast<uint4*>(sh.bins)[i] = make_uint4(0, 0, 0, 0);
+  if (tid < 32) sh.exp2[tid] = make_float2(kExp2.hi[tid], kExp2.lo[tid]);
+  const float temperature = a.s.temperature_rows ? a.s.temperature_rows[row] : a.s.temperature;
+  const float min_p = a.s.min_p_rows ? a.s.min_p_rows[row] : a.s.min_p;
+  __syncthreads();
+  float top = -INFINITY;
+  uint32_t lo = 0xFFFFFFFFu, hi = 0;
+  for (int v = v0 + tid; v < v1; v += sp::kThreads) {
+    uint32_t w[4];
+    load(v, w);
+#pragma unroll
+    for (int k = 0; k < 4; k++) tally(sh, w[k] & 0xFFFF, top, lo, hi), tally(sh, w[k] >> 16, top, lo, hi);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) sh.top[warp] = top, sh.lo[warp] = lo, sh.hi[warp] = hi;
+  __syncthreads();
+  if (warp == 0) {
+    top = sh.top[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    lo = __reduce_min_sync(0xffffffffu, sh.lo[lane]);
+    hi = __reduce_max_sync(0xffffffffu, sh.hi[lane]);
+    if (lane == 0) sh.span[0] = __float_as_uint(top), sh.span[1] = lo, sh.span[2] = hi;
+  } else if (tid == 32) {  // fp64 is slow here: by one thread
+    const double scale = temperature > 0.f ? 1.4426950408889634074 / (double)temperature : 0.0;
+    sh.ch = (float)fmin(scale, 3e38);
+    sh.cl = scale < 3e38 ? (float)(scale - (double)sh.ch) : 0.f;
+    const double z = min_p > 0.f ? log2((double)fminf(min_p, 1.f)) : -1e30;
+    sh.zh = (float)z;
+    sh.zl = (float)(z - (double)sh.zh);
+  }
+  cluster_sync_all();
+
+  // ---- the row's greatest logit and its binades
+  const uint32_t bins = smem_u32(sh.bins), span = smem_u32(sh.span);
+  top = -INFINITY, lo = 0xFFFFFFFFu, hi = 0;
+  for (int k = 0; k < (int)C; k++) {
+    const uint32_t at = cluster_map(span, k);
+    top = fmaxf(top, __uint_as_float(ld_cluster_u32(at)));
+    lo = min(lo, ld_cluster_u32(at + 4));
+    hi = max(hi, ld_cluster_u32(at + 8));
+  }
+  const bool none = top == -INFINITY;
+  Binades bn;
+  bn.e1 = hi >> 7;
+  bn.e0 = min((int)((lo == 0xFFFFFFFFu ? 0u : lo + 1) >> 7), bn.e1);
+  RowScale rs;
+  rs.most = top;
+  rs.ch = sh.ch, rs.cl = sh.cl, rs.zh = sh.zh, rs.zl = sh.zl;
+
+  // ---- each binade's count and sum, into the first CTA
+  if (!none) {
+    const uint32_t mass0 = cluster_map(smem_u32(sh.mass), 0), count0 = cluster_map(smem_u32(sh.count), 0);
+    for (int i = warp * C + rank; i < bn.n(); i += sp::kWarps * C) {
+      bool neg;
+      const uint32_t e = bn.exponent(i, neg);
+      uint32_t c[4], n = 0;
+      uint64_t m = 0;
+      lane_counts(bins, C, e, neg, lane, c);
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        if (c[k]) n += c[k], m += c[k] * weight_of(bf2f((uint16_t)key_bits(e, neg, 4 * lane + k)), rs, sh.exp2);
+      n = __reduce_add_sync(0xffffffffu, n);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+      if (lane == 0) st_cluster_u64(mass0 + 8 * i, m), st_cluster_u32(count0 + 4 * i, n);
+    }
+  }
+  cluster_sync_all();
+
+  // ---- the cuts and the token's key, by one warp
+  if (rank == 0 && warp == 0) {
+    uint32_t key = 0, nth = 0xFFFFFFFFu;
+    if (!none) {
+      const int n = bn.n();
+      uint64_t N = 0, W = 0;
+      for (int i = lane; i < n; i += 32) N += sh.count[i], W += sh.mass[i];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        N += __shfl_xor_sync(0xffffffffu, N, o);
+        W += __shfl_xor_sync(0xffffffffu, W, o);
+      }
+      const int top_k = a.s.top_k_rows ? a.s.top_k_rows[row] : a.s.top_k;
+      const float top_p = a.s.top_p_rows ? a.s.top_p_rows[row] : a.s.top_p;
+      const uint64_t K = !(temperature > 0.f) ? 1 : top_k > 0 ? top_k : N;
+      if (K < N) {
+        const Place p = find<false>(sh, bins, C, bn, rs, K, false);
+        N = K;
+        W = p.mass + (K - p.count) * p.w;
+      }
+      if (rs.zh > -1e29f) {
+        // the first binade whose last key is below min_p
+        int i = n;
+        for (int c = 0; c < n && i == n; c += 32) {
+          bool neg = false, below = false;
+          if (c + lane < n) {
+            const uint32_t e = bn.exponent(c + lane, neg);
+            below = !at_least(bf2f((uint16_t)key_bits(e, neg, 127)), rs);
+          }
+          const uint32_t f = __ballot_sync(0xffffffffu, below);
+          if (f) i = c + __ffs(f) - 1;
+        }
+        if (i < n) {
+          uint64_t cb = 0, mb = 0;
+          for (int c = lane; c < i; c += 32) cb += sh.count[c], mb += sh.mass[c];
+          bool neg;
+          const uint32_t e = bn.exponent(i, neg);
+          uint32_t c[4];
+          lane_counts(bins, C, e, neg, lane, c);
+#pragma unroll
+          for (int k = 0; k < 4; k++) {
+            const float l = bf2f((uint16_t)key_bits(e, neg, 4 * lane + k));
+            if (c[k] && at_least(l, rs)) cb += c[k], mb += c[k] * weight_of(l, rs, sh.exp2);
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            cb += __shfl_xor_sync(0xffffffffu, cb, o);
+            mb += __shfl_xor_sync(0xffffffffu, mb, o);
+          }
+          if (cb < N) N = cb, W = mb;
+        }
+      }
+      if (top_p < 1.f) {
+        const uint64_t goal = max(share_of(top_p, W, true), (uint64_t)1);
+        const Place p = find<true>(sh, bins, C, bn, rs, goal, false);
+        const uint64_t r = (goal - p.mass + p.w - 1) / p.w;
+        if (p.count + r < N) N = p.count + r, W = p.mass + r * p.w;
+      }
+      float u = a.u[row];
+      u = u > 0.f ? fminf(u, 1.f - 0x1p-24f) : 0.f;
+      const uint64_t goal = share_of(u, W, false);
+      const Place p = find<true>(sh, bins, C, bn, rs, goal, true);
+      const uint32_t r = (uint32_t)((goal - p.mass) / p.w);
+      bool neg;
+      const uint32_t e = bn.exponent(p.i, neg);
+      key = key_bits(e, neg, p.j);
+      // the CTA that holds occurrence r
+      uint32_t mine = 0;
+      if (lane < (int)C) mine = ld_cluster_u32(cluster_map(bins + 4 * (key >> 1), lane)) >> (key & 1 ? 16 : 0) & 0xFFFF;
+      const uint32_t before = before_lane(mine, lane);
+      if (lane < (int)C) {
+        const uint32_t to = cluster_map(smem_u32(&sh.key), lane);
+        st_cluster_u32(to, key);
+        st_cluster_u32(to + 4, r >= before && r < before + mine ? r - before : 0xFFFFFFFFu);
+      }
+      if (lane == 0) {
+        float w32;
+        const uint64_t w = weight_of(bf2f((uint16_t)key), rs, sh.exp2, &w32);
+        if (a.logprob) a.logprob[row] = 0.f - log1pf((float)(W - w) * 0x1p-44f / w32);
+        if (a.kept) a.kept[row] = (int32_t)N;
+      }
+    } else if (lane < (int)C) {
+      st_cluster_u32(cluster_map(smem_u32(&sh.nth), lane), nth);
+      if (lane == 0) {
+        a.tokens[row] = -1;
+        if (a.logprob) a.logprob[row] = -INFINITY;
+        if (a.kept) a.kept[row] = 0;
+      }
+    }
+  }
+  cluster_sync_all();
+
+  // ---- occurrence nth of the key in this slice
+  const uint32_t key = sh.key, nth = sh.nth;
+  if (nth == 0xFFFFFFFFu) return;
+  auto matches = [&](int v) {
+    uint32_t w[4], f = 0;
+    load(v, w);
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      uint32_t b = w[k / 2] >> (k & 1 ? 16 : 0) & 0xFFFF;
+      if (b == 0x8000u) b = 0;
+      f |= (uint32_t)(b == key) << k;
+    }
+    return f;
+  };
+  const int rounds = (v1 - v0 + sp::kThreads - 1) / sp::kThreads;  // at most 8
+  for (int i = 0; i < rounds; i++) {
+    const uint32_t n = __reduce_add_sync(0xffffffffu, __popc(matches(v0 + i * sp::kThreads + tid)));
+    if (lane == 0) sh.tot[i * sp::kWarps + warp] = n;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t run = 0, where = 0, left = 0;
+    bool found = false;
+    for (int c = 0; c < rounds && !found; c++) {
+      const uint32_t n = sh.tot[c * 32 + lane], b = run + before_lane(n, lane);
+      const uint32_t f = __ballot_sync(0xffffffffu, nth >= b && nth < b + n);
+      if (f) {
+        found = true;
+        where = c * 32 + __ffs(f) - 1;
+        left = nth - __shfl_sync(0xffffffffu, b, __ffs(f) - 1);
+      }
+      run = __shfl_sync(0xffffffffu, b + n, 31);
+    }
+    if (found) {
+      const int v = v0 + (int)(where / 32) * sp::kThreads + (int)(where % 32) * 32 + lane;
+      uint32_t f = matches(v);
+      const uint32_t n = __popc(f), b = before_lane(n, lane);
+      if (left >= b && left < b + n) {
+        for (uint32_t k = b; k < left; k++) f &= f - 1;
+        a.tokens[row] = token(v, __ffs(f) - 1);
+      }
+    }
+  }
+}
+
+static int sample_bad(int code, const char* what) {
+  set_error(std::string("sd_sample: ") + what);
+  return code;
+}
+
+}  // namespace sdv
+
+using namespace sdv;
+
+extern "C" int sd_sample(const uint16_t* logits, int64_t row_stride, int32_t rows, int32_t vocab,
+                         const sd_sampling* settings, const float* u, int32_t* tokens, float* logprob, int32_t* kept,
+                         void* stream) {
+  if (rows < 0 || vocab < 1) return sample_bad(SD_ERR_INVALID_ARG, "rows >= 0 and vocab >= 1 are needed");
+  if (vocab > sp::kMaxVocab) return sample_bad(SD_ERR_UNSUPPORTED, "vocab must be at most 524160");
+  if (!settings) return sample_bad(SD_ERR_INVALID_ARG, "null settings");
+  const sd_sampling& s = *settings;
+  if ((!s.temperature_rows && !(s.temperature >= 0.f && s.temperature <= 3e38f)) || (!s.top_k_rows && s.top_k < 0) ||
+      (!s.top_p_rows && !(s.top_p > 0.f)) || (!s.min_p_rows && !(s.min_p >= 0.f && s.min_p <= 1.f)))
+    return sample_bad(SD_ERR_INVALID_ARG, "temperature and top_k must not be negative, top_p must be positive, min_p in [0, 1]");
+  if (rows == 0) return SD_OK;
+  if (!logits || !u || !tokens) return sample_bad(SD_ERR_INVALID_ARG, "null argument");
+  if (rows > 1 && row_stride < vocab) return sample_bad(SD_ERR_INVALID_ARG, "row_stride is shorter than a row");
+  if ((uintptr_t)logits & 1) return sample_bad(SD_ERR_INVALID_ARG, "logits must be 2-byte aligned");
+  const int vecs = (vocab + 7 + 7) / 8;  // a row may begin anywhere in its first vector
+  auto slice = [&](int c) { return (vecs + c - 1) / c * 8; };
+  int C = 1;
+  while (slice(C) > sp::kSlice) C *= 2;
+  // few rows: more CTAs a row while each still has 4096 tokens
+  while (C < sp::kMaxCluster && (int64_t)rows * C * 2 <= num_sms() && vocab >= 4096 * 2 * C) C *= 2;
+  if ((int64_t)rows * C > 0x7FFFFFFF) return sample_bad(SD_ERR_UNSUPPORTED, "too many rows");
+  static const cudaError_t set = cudaFuncSetAttribute(k_sample, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SampleShared));
+  SD_CK(set);
+  const SampleArgs a = {logits, row_stride, rows, vocab, slice(C), s, u, tokens, logprob, kept};
+  SD_CK(launch_cluster(k_sample, dim3((unsigned)(rows * C)), dim3(sp::kThreads), sizeof(SampleShared), (cudaStream_t)stream,
+                       false, C, a));
+  return SD_OK;
+}

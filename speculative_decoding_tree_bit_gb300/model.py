@@ -13,8 +13,8 @@ import ctypes
 import numpy as np
 import torch
 
-from . import (KV, KV4, KV4ScoreArgs, LayerWeights, ModelConfig, ModelWeights, PagedKV, W12Meta, W12Tensor, check, lib,
-               stream_ptr)
+from . import (KV, KV4, KV4ScoreArgs, LayerWeights, ModelConfig, ModelWeights, PagedKV, RopeScalingArgs, Sampling, W12Meta,
+               W12Tensor, check, lib, stream_ptr)
 
 
 def _ptr(t) -> int:
@@ -917,3 +917,208 @@ class KV4Cache:
         check(self._lib.sd_kv4_evict(self._ref, dst._ref, self.R, budget, recent, sinks, ws_ptr, ws_n,
                                      self._status_ptr, self._stream(stream)))
         return kept
+
+
+def _raw_stream(stream, index, what):
+    """The call's stream on GPU `index`, which must be the current one: the
+    kernels run on the current GPU and read only their own."""
+    if index < 0:
+        raise ValueError(f"{what} lies on the CPU: there is no path but the GPU's")
+    if torch._C._cuda_getDevice() != index:
+        raise ValueError(f"{what} lies on cuda:{index}, which is not the current GPU")
+    if stream is not None:
+        return stream_ptr(stream)
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _same_gpu(t, index, what):
+    if t.get_device() != index:
+        raise ValueError(f"{what} is on {t.device}, other tensors of the call on {'the CPU' if index < 0 else f'cuda:{index}'}")
+
+
+class RopeScaling:
+    """Frequencies for contexts past the trained one (sd_rope_scaling)."""
+
+    def __init__(self, kind: int, factor: float, original: float = 1.0, low: float = 1.0, high: float = 2.0,
+                 amplitude: float = 0.0):
+        self.args = RopeScalingArgs(int(kind), float(factor), float(original), float(low), float(high), float(amplitude))
+
+    @classmethod
+    def linear(cls, factor: float):
+        """f / factor."""
+        return cls(1, factor)
+
+    @classmethod
+    def bands(cls, factor: float, original: float, low: float = 1.0, high: float = 4.0):
+        """f where a pair makes more than `high` turns in `original` positions, f /
+        factor where it makes less than `low`, between them in proportion."""
+        return cls(2, factor, original, low, high)
+
+    @classmethod
+    def ramp(cls, factor: float, original: float, fast: float = 32.0, slow: float = 1.0, amplitude: float = 0.0):
+        """f up to the pair of `fast` turns in `original` positions, f / factor from
+        the pair of `slow` turns on, in proportion between them; sines and cosines
+        times amplitude (0: 0.1 ln(factor) + 1)."""
+        return cls(3, factor, original, slow, fast, amplitude)
+
+
+class Rope:
+    """Rotary positions (sd_rope): the frequencies of a head's first rot_dim
+    dims, kept on the device."""
+
+    def __init__(self, head_dim: int = 128, rot_dim: int | None = None, base: float = 1e6, interleaved: bool = False,
+                 scaling: RopeScaling | None = None, device="cuda"):
+        self.head_dim, self.rot_dim = int(head_dim), int(head_dim if rot_dim is None else rot_dim)
+        if self.head_dim < 1 or self.rot_dim < 2 or self.rot_dim % 2 or self.rot_dim > self.head_dim:
+            raise ValueError("rot_dim must be even, 2 .. head_dim")
+        self.interleaved = bool(interleaved)
+        turns = np.zeros(self.rot_dim // 2, dtype=np.uint64)
+        amplitude = ctypes.c_float()
+        self._lib = lib()
+        check(self._lib.sd_rope_turns_host(self.rot_dim, float(base), None if scaling is None else ctypes.byref(scaling.args),
+                                           turns.ctypes.data, ctypes.byref(amplitude)))
+        self.amplitude = float(amplitude.value)
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self._index, self._turns_ptr = self.turns.get_device(), self.turns.data_ptr()
+
+    def _out(self, out, x, what, stream):
+        if out is None:
+            if stream is None and x.is_contiguous():
+                return torch.empty_like(x), x.shape[1] * self.head_dim
+            return _empty(stream, x.shape, x.dtype, x.device), x.shape[1] * self.head_dim
+        _same_gpu(out, self._index, what)
+        if out.dtype != x.dtype:
+            raise ValueError(f"{what} must have the type of its input")
+        return out, _rows16(out, x.shape[0], x.shape[1], self.head_dim, what, self._index)
+
+    def __call__(self, q, k, pos, q_out=None, k_out=None, stream=None):
+        """Rows turned by their positions: q [rows][n_q_heads][head_dim], k
+        [rows][n_kv_heads][head_dim] or None, rows may be strided (slices of one
+        projection); pos int32 [rows], a negative one turns back.  q_out, k_out: as q
+        and k, q and k themselves for in place.  Returns (q_out, k_out)."""
+        idx, D = self._index, self.head_dim
+        s = _raw_stream(stream, idx, "the frequencies")
+        _same_gpu(q, idx, "q")
+        if q.dim() != 3 or (k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0])):
+            raise ValueError("q and k must be [rows][heads][head_dim] of the same rows")
+        n, hq = q.shape[0], q.shape[1]
+        qs = _rows16(q, n, hq, D, "q", idx)
+        q_out, qos = self._out(q_out, q, "q_out", stream)
+        hk = ks = kos = 0
+        kp = kop = None
+        if k is not None:
+            _same_gpu(k, idx, "k")
+            hk = k.shape[1]
+            ks = _rows16(k, n, hk, D, "k", idx)
+            k_out, kos = self._out(k_out, k, "k_out", stream)
+            kp, kop = k.data_ptr(), k_out.data_ptr()
+        elif k_out is not None:
+            raise ValueError("k_out without k")
+        _same_gpu(pos, idx, "pos")
+        check(self._lib.sd_rope(self._turns_ptr, self.amplitude, D, self.rot_dim, self.interleaved,
+                                _entries(pos, n, "pos", idx), n, q.data_ptr(), qs, hq, q_out.data_ptr(), qos, kp, ks, hk, kop,
+                                kos, s))
+        return q_out, k_out
+
+
+class PromptAttention:
+    """Causal attention of packed prompts, or of their next chunks, in bf16
+    (sd_prompt_attn): what KV4Cache.attend does for up to 64 rows a request, for any
+    number of rows over keys that are not cached yet."""
+
+    def __init__(self, n_q_heads: int, n_kv_heads: int, head_dim: int = 128, device="cuda"):
+        if head_dim not in (64, 128):
+            raise ValueError("head_dim must be 64 or 128")
+        if n_kv_heads < 1 or n_q_heads < 1 or n_q_heads % n_kv_heads or n_q_heads // n_kv_heads > 128:
+            raise ValueError("n_q_heads must be a multiple of n_kv_heads, at most 128 a kv head")
+        self.n_q_heads, self.n_kv_heads, self.head_dim = int(n_q_heads), int(n_kv_heads), int(head_dim)
+        self._lib = lib()
+        self._status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._status_ptr, self._index = self._status.data_ptr(), self._status.get_device()
+        self._ws_bytes = 0
+
+    def status(self) -> int:
+        """The device status of the calls so far (synchronises), then cleared."""
+        st = int(self._status.item())
+        self._status.zero_()
+        return st
+
+    def __call__(self, q, k, v, rows: RequestRows, keys: RequestRows | None = None, score: KV4Score | None = None, out=None,
+                 lse=None, stream=None):
+        """q [rows.n][n_q_heads][head_dim], k and v [keys.n][n_kv_heads]
+        [head_dim] (keys None: as many as rows); the last row of a request stands at
+        its last key.  Rows may be strided.  score: scale, softcap, slopes and window.
+        Returns (out like q, lse float32 [rows.n][n_q_heads])."""
+        idx, D, hq, hk = self._index, self.head_dim, self.n_q_heads, self.n_kv_heads
+        s = _raw_stream(stream, idx, "the operator")
+        keys = rows if keys is None else keys
+        if keys.R != rows.R:
+            raise ValueError(f"keys of {keys.R} requests for rows of {rows.R}")
+        for t, what in ((rows, "rows"), (keys, "keys")):
+            if t.index != idx:
+                _same_gpu(t.cu_dev, idx, what)
+        for t, what in ((q, "q"), (k, "k"), (v, "v")):
+            _same_gpu(t, idx, what)
+        qs = _rows16(q, rows.n, hq, D, "q", idx)
+        ks = _rows16(k, keys.n, hk, D, "k", idx)
+        if _rows16(v, keys.n, hk, D, "v", idx) != ks:
+            raise ValueError("k and v must have one row stride")
+        ref = None
+        if score is not None:
+            if score.start is not None:
+                raise ValueError("start has no meaning here: requests are packed")
+            if score.slopes is not None:
+                _same_gpu(score.slopes, idx, "slopes")
+                if score.slopes.numel() < hq:
+                    raise ValueError(f"slopes of {score.slopes.numel()} heads for {hq} query heads")
+            ref = score.ref
+        if out is None:
+            out = torch.empty_like(q) if stream is None and q.is_contiguous() else _empty(stream, q.shape, q.dtype, q.device)
+        else:
+            _same_gpu(out, idx, "out")
+            if out.shape != q.shape or out.dtype not in _BITS16 or not out.is_contiguous():
+                raise ValueError("out must be contiguous bf16 of q's shape")
+        if lse is None:
+            lse = _empty(stream, (rows.n, hq), torch.float32, q.device)
+        else:
+            _same_gpu(lse, idx, "lse")
+            if lse.dtype is not torch.float32 or lse.shape != (rows.n, hq) or not lse.is_contiguous():
+                raise ValueError("lse must be contiguous float32 [rows][n_q_heads]")
+        if not self._ws_bytes:
+            self._ws_bytes = int(self._lib.sd_prompt_attn_workspace(D))
+        # of the call alone: two calls, streams or graphs share none
+        ws = _empty(stream, (self._ws_bytes,), torch.uint8, q.device)
+        check(self._lib.sd_prompt_attn(q.data_ptr(), qs, hq, k.data_ptr(), v.data_ptr(), ks, hk, D, rows.cu_ptr,
+                                       rows.cu_host_ptr, keys.cu_ptr, keys.cu_host_ptr, rows.R, ref, out.data_ptr(),
+                                       lse.data_ptr(), ws.data_ptr(), self._ws_bytes, self._status_ptr, s))
+        return out, lse
+
+
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None):
+    """A token of each row of logits (sd_sample): logits bf16 [rows][vocab]
+    (bfloat16 or its bits in int16), rows may be strided; u float32 [rows]
+    in [0, 1).  Each setting is a number, or a tensor [rows] (float32, top_k
+    int32).  Returns tokens int32 [rows], logprob float32 [rows] (of the token
+    among what is kept) and kept int32 [rows].  tokens may stand in for the argmax of
+    sd_accept: the walk then accepts what sampling token by token would have given."""
+    index = logits.get_device()
+    s = _raw_stream(stream, index, "logits")
+    if logits.dtype not in _BITS16 or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be bf16 [rows][vocab], a row's tokens together")
+    n, vocab = logits.shape
+    a = Sampling()
+    for name, x, kind, dtype in (("temperature", temperature, float, torch.float32), ("top_p", top_p, float, torch.float32),
+                                 ("min_p", min_p, float, torch.float32), ("top_k", top_k, int, torch.int32)):
+        if isinstance(x, torch.Tensor):
+            _same_gpu(x, index, name)
+            setattr(a, name + "_rows", _entries(x, n, name, index, dtype))
+        else:
+            setattr(a, name, kind(x))
+    _same_gpu(u, index, "u")
+    tokens = _empty(stream, (n,), torch.int32, logits.device)
+    logprob = _empty(stream, (n,), torch.float32, logits.device)
+    kept = _empty(stream, (n,), torch.int32, logits.device)
+    check(lib().sd_sample(logits.data_ptr(), logits.stride(0) if n > 1 else vocab, n, vocab, ctypes.byref(a),
+                          _entries(u, n, "u", index, torch.float32), tokens.data_ptr(), logprob.data_ptr(), kept.data_ptr(),
+                          s))
+    return {"tokens": tokens, "logprob": logprob, "kept": kept}

@@ -1,0 +1,201 @@
+"""Attention over packed prompts against the definition in 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import request_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def M():
+    from speculative_decoding_tree_bit_gb300 import model
+    return model
+
+
+def inputs(m, keys, hq, hkv, d, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    n, s = sum(m), sum(keys)
+    q = (1.5 * torch.randn(n, hq, d, generator=g)).bfloat16().cuda()
+    k = (torch.randn(s, hkv, d, generator=g) * (0.5 + torch.rand(hkv, d, generator=g)) + 0.5 * torch.randn(hkv, d, generator=g)).bfloat16().cuda()
+    v = torch.randn(s, hkv, d, generator=g).bfloat16().cuda()
+    return q, k, v
+
+
+def run(M, m, keys, q, k, v, score=None, stream=None, **kw):
+    op = M.PromptAttention(q.shape[1], k.shape[1], q.shape[2])
+    rows = M.RequestRows(np.cumsum([0] + list(m)))
+    held = M.RequestRows(np.cumsum([0] + list(keys)))
+    out, lse = op(q, k, v, rows, held, score=score, stream=stream, **kw)
+    torch.cuda.synchronize()
+    assert op.status() == 0
+    return out, lse
+
+
+def same(out, lse, m, keys, q, k, v, **kw):
+    f = lambda t: t.cpu().double()  # noqa: E731
+    want, want_lse, tol, tol_lse = ref.attend(f(q), f(k), f(v), np.cumsum([0] + list(m)), np.cumsum([0] + list(keys)), **kw)
+    out, lse = f(out), f(lse)
+    assert torch.equal(torch.isinf(lse), torch.isinf(want_lse))
+    some = ~torch.isinf(want_lse)
+    assert ((lse - want_lse).abs()[some] <= tol_lse[some]).all(), (lse - want_lse).abs()[some].max()
+    bad = (out - want).abs() > tol
+    assert not bad.any(), (bad.nonzero()[:5], (out - want).abs()[bad].max(), int(bad.sum()))
+
+
+def check(M, m, keys, hq, hkv, d, seed=0, cap=0.0, slopes=None, window=0, scale=0.0):
+    q, k, v = inputs(m, keys, hq, hkv, d, seed)
+    sl = None if slopes is None else slopes.cuda()
+    out, lse = run(M, m, keys, q, k, v, M.KV4Score(scale=scale, softcap=cap, slopes=sl, window=window))
+    same(out, lse, m, keys, q, k, v, cap=cap, slopes=slopes, window=window, scale=scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 257, 700])
+def test_one_prompt(M, n, d):
+    check(M, [n], [n], 8, 2, d, seed=n)
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (2, 1), (3, 1), (5, 1), (8, 1), (7, 7), (10, 2), (32, 8), (16, 1), (33, 1), (64, 1), (65, 1),
+                                    (100, 1), (128, 1)])
+def test_head_groups(M, hq, hkv):
+    check(M, [70, 3], [70, 3], hq, hkv, 128, seed=hq)
+    check(M, [70, 3], [200, 140], hq, hkv, 64, seed=hq + 1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_packed_ragged(M, d):
+    """Requests without rows, without keys, of one token; rows before the keys see nothing."""
+    m = [5, 0, 1, 130, 0, 64, 300, 7, 3]
+    keys = [5, 40, 1, 130, 0, 200, 300, 3, 0]
+    check(M, m, keys, 8, 2, d, seed=1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m,past", [(1, 1), (1, 127), (1, 128), (1, 5000), (17, 1000), (64, 2049), (200, 3000)])
+def test_next_chunk(M, m, past, d):
+    check(M, [m], [m + past], 8, 2, d, seed=m)
+
+
+@pytest.mark.parametrize("window", [1, 2, 100, 128, 129, 500, 100000])
+@pytest.mark.parametrize("d", [64, 128])
+def test_window(M, window, d):
+    check(M, [300, 20, 1], [300, 700, 900], 4, 2, d, seed=window, window=window)
+
+
+def test_options(M):
+    slopes = torch.exp2(-torch.arange(1, 9).float())
+    for d in (64, 128):
+        check(M, [150, 9], [150, 400], 8, 4, d, cap=20.0)
+        check(M, [150, 9], [150, 400], 8, 4, d, slopes=slopes)
+        check(M, [150, 9], [150, 400], 8, 4, d, cap=50.0, slopes=slopes, window=70)
+        check(M, [150, 9], [150, 400], 8, 4, d, scale=0.3)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_requests_of_few_rows(M, d):
+    rng = np.random.default_rng(3)
+    m = rng.integers(0, 6, 200).tolist()
+    keys = [int(x + rng.integers(0, 300)) for x in m]
+    check(M, m, keys, 4, 1, d, seed=2)
+
+
+def test_long_contexts(M):
+    """Work split over the keys and joined; far offsets."""
+    check(M, [2, 1], [20011, 9000], 4, 1, 128, seed=4)
+    check(M, [40], [20000], 5, 1, 64, seed=5)
+
+
+def test_large_and_small_scores(M):
+    """Softmax statistics over a wide range: a maximum that keeps growing, and one key that takes all."""
+    m = keys = [400]
+    q, k, v = inputs(m, keys, 4, 2, 128, 6)
+    k = (k.float() * torch.linspace(0.01, 6.0, 400, device="cuda")[:, None, None]).bfloat16()
+    out, lse = run(M, m, keys, q, k, v)
+    same(out, lse, m, keys, q, k, v)
+    k = k.flip(0).contiguous()
+    out, lse = run(M, m, keys, q, k, v)
+    same(out, lse, m, keys, q, k, v)
+    out, lse = run(M, m, keys, (q.float() * 1e-30).bfloat16(), k, v)
+    same(out, lse, m, keys, (q.float() * 1e-30).bfloat16(), k, v)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("d", [64, 128])
+def test_bad_values_only_reach_the_rows_that_see_them(M, bad, d):
+    """In a key or a value: earlier rows, other requests and other kv heads stay as they were."""
+    m, keys = [200, 150, 30], [200, 150, 400]
+    q, k, v = inputs(m, keys, 4, 2, d, 7)
+    clean, clean_lse = run(M, m, keys, q, k, v)
+    for key, of in ((60, "v"), (199, "v"), (200 + 149, "v"), (130, "k"), (350 + 399, "v"), (350 + 398, "k"), (350, "v")):
+        k2, v2 = k.clone(), v.clone()
+        (k2 if of == "k" else v2)[key, 1, 5] = bad
+        out, lse = run(M, m, keys, q, k2, v2)
+        r = 0 if key < 200 else 1 if key < 350 else 2
+        at, first = key - [0, 200, 350][r], [0, 200, 350][r]
+        row0 = first + max(0, at - (keys[r] - m[r]))  # the first row that sees it
+        end = first + m[r]
+        hit = torch.zeros(sum(m), 4, dtype=torch.bool, device="cuda")
+        hit[row0:end, 2:] = True
+        assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit]), (key, of)
+        if of == "v":
+            assert (~torch.isfinite(out[hit][:, 5].float())).all(), (key, of)
+            rest = [i for i in range(d) if i != 5]
+            assert torch.equal(out[hit][:, rest], clean[hit][:, rest]) and torch.equal(lse[hit], clean_lse[hit])
+
+
+def test_nothing_beyond_the_last_row_is_written(M):
+    q, k, v = inputs([70], [70], 4, 2, 128)
+    big, big_lse = torch.full((75, 4, 128), 7.0).bfloat16().cuda(), torch.full((75, 4), 7.0).cuda()
+    out, lse = run(M, [70], [70], q, k, v, out=big[:70], lse=big_lse[:70])
+    assert (big[70:] == 7).all() and (big_lse[70:] == 7).all()
+    same(out, lse, [70], [70], q, k, v)
+
+
+def test_strided_rows(M):
+    """q, k and v as slices of one projection's output; bits in int16."""
+    qkv = torch.randn(190, 8 + 4, 64, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    q, k, v = qkv[:, :8], qkv[:, 8:10], qkv[:, 10:]
+    out, lse = run(M, [100, 90], [100, 90], q, k, v)
+    same(out, lse, [100, 90], [100, 90], q, k, v)
+    b = qkv.view(torch.int16)
+    out2, _ = run(M, [100, 90], [100, 90], b[:, :8], b[:, 8:10], b[:, 10:])
+    assert out2.dtype is torch.int16 and torch.equal(out2.view(torch.bfloat16), out)
+
+
+def test_same_bits_every_time_and_on_streams_and_graphs(M):
+    m, keys = [3, 500, 40], [4000, 500, 40]
+    q, k, v = inputs(m, keys, 8, 2, 128, 9)
+    want, want_lse = run(M, m, keys, q, k, v)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for stream in (None, s):
+        out, lse = run(M, m, keys, q, k, v, stream=stream)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    op = M.PromptAttention(8, 2, 128)
+    rows, held = M.RequestRows(np.cumsum([0] + m)), M.RequestRows(np.cumsum([0] + keys))
+    op(q, k, v, rows, held)
+    graphs = []
+    for _ in range(2):  # two graphs and eager calls between their replays
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, *op(q, k, v, rows, held)))
+    q.copy_(q.flip(0))
+    want, want_lse = op(q, k, v, rows, held)
+    with torch.cuda.stream(s):
+        graphs[0][0].replay()
+    graphs[1][0].replay()
+    again, _ = op(q, k, v, rows, held)
+    torch.cuda.synchronize()
+    for _, out, lse in graphs:
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert torch.equal(again, want)
+
+
+def test_no_rows(M):
+    q, k, v = inputs([0, 0], [5, 0], 4, 2, 64)
+    out, lse = run(M, [0, 0], [5, 0], q, k, v)
+    assert out.numel() == 0 and lse.numel() == 0

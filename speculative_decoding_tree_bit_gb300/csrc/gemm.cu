@@ -256,6 +256,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+void* tensor_map_encoder() { return reinterpret_cast<void*>(encode_fn()); }
+
 int make_x_map(XMap* xm, const uint16_t* x, int rows_total, int64_t K, int box_rows) {
   auto fn = encode_fn();
   if (!fn) {

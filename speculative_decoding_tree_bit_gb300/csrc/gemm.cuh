@@ -76,6 +76,8 @@ struct XMap {
   int rows_total;
   int box_rows;
 };
+// cuTensorMapEncodeTiled (PFN_cuTensorMapEncodeTiled_v12000), null where the driver has none.
+void* tensor_map_encoder();
 int make_x_map(XMap* xm, const uint16_t* x, int rows_total, int64_t K, int box_rows);
 
 // y = epilogue(x W^T) for rows [0, M).  With gemm_use_tc(M) one tcgen05

@@ -1,60 +1,846 @@
-// Causal attention over packed prompts.
+// Causal attention over packed prompts on the tensor cores (tcgen05 + TMEM).
+//
+//   o_i = sum_j exp(s_ij - lse_i) v_j,  s_ij = q_i . k_j scale over the keys j that row
+//   i sees,
+// in one pass over the keys with a row's running maximum and sum.  The rows of a kv
+// head's query heads are packed, token by token, into tiles of 128 (T = 128 / G tokens
+// of G heads), so that K and V are read once for the group and a single token fills G
+// rows.  A unit is a kv head and 2 T tokens (two tiles, WIDE) or up to T (one); its
+// steps are tiles of 128 keys.  Warps:
+//  * 0..3 and 4..7: softmax, a thread a row: 128 scores from TMEM, maximum,
+//    exponentials, P (bf16) back over its scores; then the outputs.  A wide unit
+//    gives each of the two groups a tile of rows, a narrow one alternate steps of the
+//    same rows, joined through shared memory.  A row's reference may lag its maximum
+//    by 2^8 before O is rescaled in TMEM.
+//  * 8: the products: S = Q K^T and O += P V, those of one tile while the other is in
+//    its softmax.  TMEM: [S 128][S 128][O D][O D].
+//  * 9: Q, K and V by TMA.
+//  * 10, 11: in steps where some row does not see some key, look for infinities and
+//    NaNs in V (P is 0 there, and 0 times those is not) and take them out of the
+//    operand; the rows that do see them get them back at the end (s_bad).
+// The steps are dealt evenly over the CTAs, by the host (it has the lengths): a
+// unit may be split over its keys; its parts are joined by a second kernel.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <vector>
+
+#include "gemm.cuh"
 #include "kv4_attn.cuh"
+#include "tcgen05.cuh"
 
 namespace sdv {
 
-struct PromptArgs {
-  const uint16_t* q;
-  const uint16_t* k;
-  const uint16_t* v;
-  int64_t q_stride, kv_stride;
-  int hq, hkv, G, R;
-  const int32_t* cu_q;
-  const int32_t* cu_k;
-  Kv4Score s;
-  uint16_t* out;
-  float* lse;
+namespace pa {
+constexpr int kThreads = 384, kMma = 8, kLoad = 9, kCheck = 10;
+constexpr int kMaxCta = 160;
+constexpr int kNK = 2, kNV = 3;  // stages of K and of V
+constexpr float kLag = 8.f;
+constexpr int kXs = 20;          // floats of a row being exchanged (16 used)
+}  // namespace pa
+
+// Where a CTA's share begins: step of the unit (request, kv head, token block).
+struct PaAt {
+  int r, h, i, step;
 };
 
-// A warp per row and query head, D / 32 dims a lane, one key at a time.
+struct PaArgs {
+  CUtensorMap qmap, kmap, vmap;
+  PaAt at[pa::kMaxCta + 1];  // [grid + 1]: a share ends where the next begins
+  Kv4Score s;
+  const uint16_t* v;
+  int64_t kv_stride;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int R, hq, hkv, G, T, U;   // T: tokens of a tile, U: of a unit (T or 2 T)
+  uint16_t* out;
+  float* lse;
+  float* part;
+  int32_t* status;
+};
+
+// Joins of split units: [first CTA, parts].
+struct PaJoins {
+  PaAt at[pa::kMaxCta];  // step: parts
+  int cta[pa::kMaxCta];
+  int n;
+};
+
 template <int D>
-__global__ void __launch_bounds__(256) k_prompt_attn(PromptArgs a, int rows) {
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= (int64_t)rows * a.hq) return;
-  constexpr int N = D / 32;
-  const int lane = threadIdx.x & 31, row = (int)(i / a.hq), h = (int)(i - (int64_t)row * a.hq);
-  const int r = request_of(a.cu_q, a.R, row);
-  const int m = a.cu_q[r + 1] - a.cu_q[r], n = a.cu_k[r + 1] - a.cu_k[r];
-  const int p = n - m + row - a.cu_q[r];
-  float q[N], o[N] = {};
-  for (int d = 0; d < N; d++) q[d] = bf2f(a.q[row * a.q_stride + h * D + lane * N + d]);
-  float top = -INFINITY, l = 0.f;
-  const float slope = a.s.slopes ? a.s.slopes[h] * kLog2e : 0.f;
-  for (int j = a.s.window > 0 ? max(0, p - a.s.window + 1) : 0; j <= p; j++) {
-    const int64_t at = (int64_t)(a.cu_k[r] + j) * a.kv_stride + h / a.G * D + lane * N;
-    float x[1] = {0.f};
-    for (int d = 0; d < N; d++) x[0] += q[d] * bf2f(a.k[at + d]);
-    for (int e = 16; e > 0; e >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], e);
-    float y[2] = {x[0], x[0]};
-    kv4_cap(a.s, y);
-    const float t = fmaf(slope, (float)(j - p), y[0]);
-    const float up = fmaxf(top, t), us = up == -INFINITY ? 0.f : up;
-    const float f = ex2(top - us), w = ex2(t - us);
-    l = l * f + w;
-    for (int d = 0; d < N; d++) o[d] = o[d] * f + w * bf2f(a.v[at + d]);
-    top = up;
+struct PaShape {
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int off_k = 2 * kTile, off_v = off_k + pa::kNK * kTile;
+  static constexpr int off_x = D == 128 ? kTile : off_v + pa::kNV * kTile;  // [128][kXs] floats; narrow units leave Q's second tile free
+  static constexpr int off_ml = off_v + pa::kNV * kTile + (D == 128 ? 0 : 128 * pa::kXs * 4);
+  static constexpr int off_bar = off_ml + 128 * 8;
+  static constexpr int smem = off_bar + 64 * 8 + 1024;
+  static constexpr int kPart = 256 * (D + 2);  // floats of a part: [row][D], then [row] (reference, sum)
+};
+
+// A unit's rows and steps.
+struct PaUnit {
+  int r, h, i;
+  int m, n, q0, k0;    // rows and keys of the request, their first
+  int nu;              // units a kv head
+  int tok, tc;         // first token, tokens
+  int p0;              // position of the first
+  int lo, steps;       // first key tile, tiles (0: no row sees a key)
+  bool wide;
+  __device__ __forceinline__ void request(const PaArgs& a) {
+    q0 = a.cu_q[r], m = a.cu_q[r + 1] - q0;
+    k0 = a.cu_k[r], n = a.cu_k[r + 1] - k0;
+    nu = (m + a.U - 1) / a.U;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  for (int d = 0; d < N; d++) a.out[i * D + lane * N + d] = f2bf(o[d] * inv);
-  if (lane == 0 && a.lse) a.lse[i] = l == 0.f ? -INFINITY : (top + log2f(l)) * (1.f / kLog2e);
+  __device__ __forceinline__ void unit(const PaArgs& a) {
+    tok = i * a.U;
+    tc = min(a.U, m - tok);
+    wide = tc > a.T;
+    p0 = n - m + tok;
+    const int p1 = p0 + tc - 1;
+    lo = first_tile(a, p0);
+    steps = p1 < 0 ? 0 : p1 / 128 + 1 - lo;
+  }
+  // the tile of the first key that a row at position p sees
+  static __device__ __forceinline__ int first_tile(const PaArgs& a, int p) {
+    return a.s.window > 0 && p >= 0 ? max(p - a.s.window + 1, 0) / 128 : 0;
+  }
+  // some row of positions pa .. pb does not see some key of tile j
+  static __device__ __forceinline__ bool masked(const PaArgs& a, int j, int pa, int pb) {
+    return j * 128 + 127 > pa || (a.s.window > 0 && pb >= 0 && j * 128 < pb - a.s.window + 1);
+  }
+  // steps [x, y) of those from ua to ub in which tile t of a wide unit has keys
+  __device__ __forceinline__ void range(const PaArgs& a, int t, int ua, int ub, int& x, int& y) const {
+    const int f = p0 + t * a.T, l = p0 + (t ? tc : a.T) - 1;
+    x = max(ua, first_tile(a, f) - lo);
+    y = l < 0 ? x : min(ub, l / 128 + 1 - lo);
+    y = max(x, y);
+  }
+};
+
+// A CTA's walk over its units.
+struct PaWalk : PaUnit {
+  int ua, ub;
+  PaAt end;
+  bool first;
+  __device__ __forceinline__ PaWalk(const PaArgs& a) {
+    const PaAt b = a.at[blockIdx.x];
+    end = a.at[blockIdx.x + 1];
+    r = b.r, h = b.h, i = b.i, ua = b.step;
+    first = true;
+  }
+  __device__ __forceinline__ bool next(const PaArgs& a) {
+    if (!first) {
+      ua = 0;
+      if (++i == nu) {
+        i = 0;
+        if (++h == a.hkv) {
+          h = 0;
+          do r++;
+          while (r < end.r && a.cu_q[r + 1] == a.cu_q[r]);
+        }
+      }
+    }
+    if (r > end.r || (r == end.r && (h > end.h || (h == end.h && (i > end.i || (i == end.i && ua >= end.step)))))) return false;
+    if (r >= a.R) return false;
+    if (first || i == 0) request(a);
+    first = false;
+    unit(a);
+    ub = r == end.r && h == end.h && i == end.i ? end.step : max(1, steps);
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return ua == 0 && ub == max(1, steps); }
+  __device__ __forceinline__ int part_slot() const { return 2 * blockIdx.x + (ua == 0); }
+};
+
+// 128 consecutive fp32 columns of this thread's TMEM lane, waited for.
+__device__ __forceinline__ void pa_tmem_ld(uint32_t taddr, float (&v)[128]) {
+  uint32_t r[128];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]), "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]), "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 128; i++) v[i] = __uint_as_float(r[i]);
+}
+template <int N>
+__device__ __forceinline__ void pa_tmem_st(uint32_t taddr, const uint32_t (&r)[N]);
+template <>
+__device__ __forceinline__ void pa_tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+               "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pa_bf16x2(float lo, float hi) {
+  uint32_t y;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+  return y;
+}
+__device__ __forceinline__ void pa_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// D (tmem) (+)= A (tmem) * B (smem).
+__device__ __forceinline__ void pa_umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tma3d_g2s(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+// B operand with its N side (dims) contiguous, 128-byte swizzle: rows of 64 dims, 8
+// keys 1024 bytes, panels of 64 dims 16384 bytes apart.
+__device__ __forceinline__ uint64_t pa_sdesc_v(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(16384 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// What a softmax thread keeps of its row over a unit.
+struct PaRow {
+  float ref, l;  // reference (base 2), sum of 2^(score - ref)
+  bool any;      // the group had steps
+};
+
+// One step of a tile: scores from TMEM, P back.  kb: first key; see0 .. see1: the
+// keys that the row sees; masked: some row of the tile does not see some key.
+template <int D, bool BIAS>
+__device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, uint32_t to, int kb, int see0, int see1,
+                                        bool masked, float f, float slope) {
+  float x[128];
+  pa_tmem_ld(ts, x);
+  if (BIAS) {
+    kv4_cap(a.s, x);
+    const float far = (float)(kb - see1);  // the row stands at see1
+#pragma unroll
+    for (int c = 0; c < 128; c++) x[c] = fmaf(slope, far + c, x[c]);
+  }
+  if (masked) {
+    const int a0 = see0 - kb, a1 = see1 - kb;
+#pragma unroll
+    for (int c = 0; c < 128; c++)
+      if (c < a0 || c > a1) x[c] = -INFINITY;
+  }
+  float t4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+  for (int c = 4; c < 128; c += 8) {
+#pragma unroll
+    for (int e = 0; e < 4; e++) t4[e] = c + 4 + e < 128 ? fmaxf(t4[e], fmaxf(x[c + e], x[c + 4 + e])) : fmaxf(t4[e], x[c + e]);
+  }
+  const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f;
+  const bool grows = top > w.ref + pa::kLag || (w.ref == -INFINITY && top > w.ref);
+  if (__any_sync(0xffffffffu, grows)) {
+    const float al = grows ? ex2(w.ref - top) : 1.f;
+    if (grows) w.ref = top;
+    w.l *= al;
+    if (w.any) {  // the product before is done: its commit came before these scores'
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        float o[16];
+        tmem_ld16(to + c, o);
+        uint32_t y[16];
+#pragma unroll
+        for (int k = 0; k < 16; k++) y[k] = __float_as_uint(o[k] * al);
+        pa_tmem_st(to + c, y);
+      }
+    }
+  }
+  const float off = w.ref == -INFINITY ? 0.f : -w.ref;
+  const uint64_t ff = f2pack(f, f), oo = f2pack(off, off);
+  uint64_t l2[2] = {0, 0};
+#pragma unroll
+  for (int c0 = 0; c0 < 128; c0 += 32) {
+    uint32_t p[16];
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      float p0, p1;
+      f2unpack(f2fma(f2pack(x[c0 + c], x[c0 + c + 1]), ff, oo), p0, p1);
+      p0 = ex2(p0);
+      p1 = ex2(p1);
+      l2[c >> 1 & 1] = f2add(l2[c >> 1 & 1], f2pack(p0, p1));
+      p[c / 2] = pa_bf16x2(p0, p1);
+    }
+    pa_tmem_st(ts + c0 / 2, p);
+  }
+  float l0, l1;
+  f2unpack(f2add(l2[0], l2[1]), l0, l1);
+  w.l += l0 + l1;
+  pa_wait_st();
+  w.any = true;
+}
+
+template <int D, bool BIAS>
+__global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_constant__ PaArgs a) {
+  using S = PaShape<D>;
+  extern __shared__ uint8_t smem_pa[];
+  uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_pa) + 1023) & ~uintptr_t(1023));
+  uint64_t* const q_full = reinterpret_cast<uint64_t*>(sm + S::off_bar);
+  uint64_t* const q_empty = q_full + 1;            // products with Q done (commit), exchange done (8 warps)
+  uint64_t* const k_full = q_empty + 1;            // [kNK]
+  uint64_t* const k_empty = k_full + pa::kNK;
+  uint64_t* const v_full = k_empty + pa::kNK;      // [kNV]
+  uint64_t* const v_empty = v_full + pa::kNV;      // products done (commit), looked at (2 warps)
+  uint64_t* const v_ok = v_empty + pa::kNV;        // looked at (2 warps)
+  uint64_t* const s_full = v_ok + pa::kNV;         // [t] scores ready (commit)
+  uint64_t* const p_full = s_full + 2;             // [t] weights written (4 warps)
+  uint64_t* const o_full = p_full + 2;             // [t] a unit's last product done (commit)
+  uint64_t* const o_empty = o_full + 2;            // [t] outputs read (4 warps)
+  float2* const s_ml = reinterpret_cast<float2*>(sm + S::off_ml);
+  float* const s_x = reinterpret_cast<float*>(sm + S::off_x);
+  __shared__ int s_abort;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_bad[8][2];  // [unit with steps, mod 8][checking warp]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch();
+
+  if (warp == pa::kMma) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    mbar_init(q_full, 1), mbar_init(q_empty, 9);
+    for (int i = 0; i < pa::kNK; i++) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
+    for (int i = 0; i < pa::kNV; i++) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 3), mbar_init(&v_ok[i], 2);
+    for (int t = 0; t < 2; t++) mbar_init(&s_full[t], 1), mbar_init(&p_full[t], 4), mbar_init(&o_full[t], 1), mbar_init(&o_empty[t], 4);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = s_tmem;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!kv4_wait(bar, parity & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(40));
+  };
+  PaWalk w(a);
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(72));
+    if (warp == pa::kLoad) {
+      uint32_t nk = 0, nv = 0, units = 0;
+      while (w.next(a)) {
+        if (w.steps == 0) continue;  // no row sees a key: the softmax warps write the rows
+        const int n = w.ub - w.ua;
+        auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, int step) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(full, S::kTile);
+#pragma unroll
+            for (int d = 0; d < D; d += 64) tma3d_g2s(dst + d * 256, map, d, w.h, w.k0 + (w.lo + step) * 128, full);
+          }
+          __syncwarp();
+        };
+        auto load_k = [&](int step) {
+          const uint32_t st = nk % pa::kNK;
+          wait(&k_empty[st], (nk / pa::kNK & 1) ^ 1);
+          load(sm + S::off_k + st * S::kTile, &a.kmap, &k_full[st], step);
+          nk++;
+        };
+        auto load_v = [&](int step) {
+          const uint32_t st = nv % pa::kNV;
+          wait(&v_empty[st], (nv / pa::kNV & 1) ^ 1);
+          load(sm + S::off_v + st * S::kTile, &a.vmap, &v_full[st], step);
+          nv++;
+        };
+        load_k(w.ua);
+        wait(q_empty, (units & 1) ^ 1);
+        if (lane == 0) {
+          const int tiles = w.wide ? 2 : 1;
+          mbar_arrive_expect_tx(q_full, tiles * (D / 64) * 128 * a.G * a.T);
+          for (int t = 0; t < tiles; t++)
+            for (int d = 0; d < D; d += 64)
+              tma3d_g2s(sm + t * S::kTile + d * 256, &a.qmap, d, w.h * a.G, w.q0 + w.tok + t * a.T, q_full);
+        }
+        __syncwarp();
+        for (int u = w.ua; u < w.ua + n; u++) {
+          if (u + 1 < w.ua + n) load_k(u + 1);
+          load_v(u);
+        }
+        units++;
+      }
+    } else if (warp == pa::kMma) {
+      const uint32_t id0 = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);  // fp32 += bf16 bf16, M = 128
+      const uint32_t ids = id0 | (16u << 17), idv = id0 | (1u << 16) | ((uint32_t)(D / 8) << 17);
+      const uint64_t qd = sdesc_sw128(smem_u32(sm)), kd = sdesc_sw128(smem_u32(sm + S::off_k)),
+                     vd = pa_sdesc_v(smem_u32(sm + S::off_v));
+      uint32_t nk = 0, nv = 0, units = 0, pp = 0, po = 3;  // pp, po: parities of p_full and o_empty
+      while (w.next(a)) {
+        if (w.steps == 0) continue;
+        const int n = w.ub - w.ua;
+        bool begun[2] = {false, false};
+        auto scores = [&](int t, int x, bool release) {  // step x of the share
+          const uint32_t st = (nk + x) % pa::kNK;
+          wait(&k_full[st], (nk + x) / pa::kNK);
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t q = qd + (w.wide ? t : 0) * (S::kTile >> 4), k = kd + st * (S::kTile >> 4);
+#pragma unroll
+            for (int c = 0; c < D / 16; c++)
+              umma_bf16(tm + t * 128, q + (c >> 2) * (16384 >> 4) + (c & 3) * 2, k + (c >> 2) * (16384 >> 4) + (c & 3) * 2, ids, c > 0);
+            umma_commit(&s_full[t]);
+            if (release) umma_commit(&k_empty[st]);
+          }
+          __syncwarp();
+        };
+        auto values = [&](int t, int x, bool masked, bool last, bool release) {
+          const uint32_t st = (nv + x) % pa::kNV;
+          if (!begun[t]) {
+            wait(&o_empty[t], po >> t);
+            po ^= 1u << t;
+          }
+          wait(&v_full[st], (nv + x) / pa::kNV);
+          if (masked) wait(&v_ok[st], (nv + x) / pa::kNV);
+          wait(&p_full[t], pp >> t);
+          pp ^= 1u << t;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int c = 0; c < 8; c++)
+              pa_umma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * c, vd + st * (S::kTile >> 4) + c * (2048 >> 4), idv, begun[t] || c > 0);
+            if (last) umma_commit(&o_full[t]);
+            if (release) umma_commit(&v_empty[st]);
+          }
+          __syncwarp();
+          begun[t] = true;
+        };
+        wait(q_full, units);
+        tc_fence_after();
+        const int p1 = w.p0 + w.tc - 1;
+        auto masked = [&](int x) { return PaUnit::masked(a, w.lo + w.ua + x, w.p0, p1); };
+        auto q_done = [&]() {
+          if (elect_one()) umma_commit(q_empty);
+          __syncwarp();
+        };
+        if (w.wide) {
+          int x[2], y[2];
+          for (int t = 0; t < 2; t++) {
+            w.range(a, t, w.ua, w.ub, x[t], y[t]);
+            x[t] -= w.ua, y[t] -= w.ua;
+          }
+          for (int u = -1; u < n; u++) {
+            bool v[2], s[2];
+            for (int t = 0; t < 2; t++) v[t] = u >= x[t] && u < y[t], s[t] = u + 1 >= x[t] && u + 1 < y[t];
+            for (int t = 0; t < 2; t++) {
+              if (v[t]) values(t, u, masked(u), u == y[t] - 1, t == 1 || !v[1]);
+              if (s[t]) scores(t, u + 1, t == 1 || !s[1]);
+            }
+            if (u == n - 2) q_done();
+          }
+        } else {
+          for (int u = 0; u < min(n, 2); u++) scores(u, u, true);
+          if (n <= 2) q_done();
+          for (int u = 0; u < n; u++) {
+            values(u & 1, u, masked(u), u >= n - 2, true);
+            if (u + 2 < n) {
+              scores(u & 1, u + 2, true);
+              if (u + 3 == n) q_done();
+            }
+          }
+        }
+        nk += n, nv += n;
+        units++;
+      }
+    } else {
+      // ----------------------------------------------- looking at values --
+      const int half = warp - pa::kCheck;
+      uint32_t nv = 0, units = 0;
+      while (w.next(a)) {
+        if (w.steps == 0) continue;
+        const int n = w.ub - w.ua, p1 = w.p0 + w.tc - 1;
+        if (lane == 0) s_bad[units & 7][half] = 0;
+        for (int x = 0; x < n; x++, nv++) {
+          const uint32_t st = nv % pa::kNV;
+          wait(&v_full[st], nv / pa::kNV);
+          if (PaUnit::masked(a, w.lo + w.ua + x, w.p0, p1)) {
+            uint4* const v = reinterpret_cast<uint4*>(sm + S::off_v + st * S::kTile + half * (S::kTile / 2));
+            uint32_t odd = 0;  // bit 15 of a half word: its exponent is all ones
+#pragma unroll 8
+            for (int i = lane; i < S::kTile / 32; i += 32) {
+              const uint4 u = v[i];
+              odd |= ((u.x & 0x7F807F80u) + 0x00800080u) | ((u.y & 0x7F807F80u) + 0x00800080u) |
+                     ((u.z & 0x7F807F80u) + 0x00800080u) | ((u.w & 0x7F807F80u) + 0x00800080u);
+            }
+            if (__any_sync(0xffffffffu, odd & 0x80008000u)) {
+              if (lane == 0) s_bad[units & 7][half] = 1;
+              uint32_t* const vw = reinterpret_cast<uint32_t*>(v);
+              for (int i = lane; i < S::kTile / 8; i += 32) {
+                const uint32_t u = vw[i], o = ((u & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                if (o) vw[i] = u & ~((o >> 15) * 0xFFFFu);
+              }
+            }
+            fence_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&v_ok[st]);
+            mbar_arrive(&v_empty[st]);
+          }
+        }
+        units++;
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- softmax --
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(216));
+    const int t = warp >> 2, idx = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t ts = tm + t * 128 + lanes, to = tm + 256 + t * 128 + lanes;
+    const float f = BIAS ? 1.f : a.s.scale * kLog2e;
+    const int tok_of = idx / a.G, g = idx - tok_of * a.G;
+    uint32_t some = 0, sp = 0, op = 0;  // units with steps; parities of s_full and o_full
+    while (w.next(a)) {
+      const int base = w.wide ? t * a.T : 0;           // the tile's first token in the unit
+      const int toks = min(a.T, w.tc - base);          // tokens of the tile, > 0
+      const bool live = tok_of < toks;
+      const int p = w.p0 + base + min(tok_of, toks - 1);
+      const int see0 = a.s.window > 0 && p >= 0 ? max(p - a.s.window + 1, 0) : 0;
+      const int hq = w.h * a.G + min(g, a.G - 1);
+      const float slope = BIAS && a.s.slopes ? a.s.slopes[hq] * kLog2e : 0.f;
+      const int pa0 = w.p0 + base, pb0 = pa0 + toks - 1;
+      PaRow row = {-INFINITY, 0.f, false};
+      const bool pair = !w.wide && w.steps;            // the groups share the rows
+      int x = 0, y = 0, by = 1;
+      if (w.steps) {
+        wait(q_full, some);  // no group is a unit ahead of the others' barriers
+        if (!pair && lane == 0) mbar_arrive(q_empty);  // nothing to exchange
+        if (w.wide) w.range(a, t, w.ua, w.ub, x, y);
+        else x = w.ua + t, y = w.ub, by = 2;
+      }
+#pragma unroll 1
+      for (int u = x; u < y; u += by) {
+        wait(&s_full[t], sp);
+        sp ^= 1;
+        tc_fence_after();
+        const int j = w.lo + u;
+        pa_step<D, BIAS>(a, row, ts, to, j * 128, see0, p, PaUnit::masked(a, j, pa0, pb0), f, slope);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t]);
+      }
+      bool bad = false;
+      if (row.any) {
+        wait(&o_full[t], op);
+        op ^= 1;
+        tc_fence_after();
+        bad = *(volatile int*)&s_bad[some & 7][0] | *(volatile int*)&s_bad[some & 7][1];
+      }
+      // infinities and NaNs that were taken out of V and that the row sees
+      auto give_back = [&](float (&o)[16], int c) {
+        for (int u = x; u < y; u += by) {
+          const int j = w.lo + u;
+          if (!PaUnit::masked(a, j, w.p0, w.p0 + w.tc - 1)) continue;
+          for (int key = max(j * 128, see0); key <= min(j * 128 + 127, p); key++) {
+            const uint16_t* v = a.v + (int64_t)(w.k0 + key) * a.kv_stride + w.h * D + c;
+#pragma unroll
+            for (int e = 0; e < 16; e++)
+              if ((v[e] & 0x7F80) == 0x7F80) o[e] += bf2f(v[e]);
+          }
+        }
+      };
+      const bool whole = w.whole();
+      const int64_t at = (int64_t)(w.q0 + w.tok + base + tok_of) * a.hq + hq;
+      float* const part = a.part + (int64_t)w.part_slot() * S::kPart;
+      // (reference, sum) of the row and the outputs' factors
+      float M = row.ref, L = row.l, mine = 1.f, other = 0.f;
+      if (pair) {
+        if (t == 1) s_ml[idx] = make_float2(row.ref, row.l);
+        bar_sync(1, 256);
+        if (t == 0) {
+          const float2 ml = s_ml[idx];
+          M = fmaxf(row.ref, ml.x);
+          const float Ms = M == -INFINITY ? 0.f : M;
+          mine = row.any ? ex2(row.ref - Ms) : 0.f;
+          other = ml.x == -INFINITY ? 0.f : ex2(ml.x - Ms);
+          L = mine * row.l + other * ml.y;
+          if (!(ml.y == ml.y)) L = ml.y, other = ml.y;  // a NaN among the other's scores
+        }
+      }
+      const bool writes = live && (w.wide || t == 0);
+      const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+      if (writes) {
+        if (whole) {
+          if (a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
+        } else {
+          __stcg(reinterpret_cast<float2*>(part + 256 * D) + t * 128 + idx, make_float2(M, L));
+        }
+      }
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        float o[16];
+        if (row.any) tmem_ld16(to + c, o);
+#pragma unroll
+        for (int e = 0; e < 16; e++) o[e] = row.any && row.l != 0.f ? o[e] : 0.f;
+        if (bad && live) give_back(o, c);
+        if (pair) {
+          float4* const xr = reinterpret_cast<float4*>(s_x + idx * pa::kXs);
+          if (t == 1) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) xr[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          bar_sync(1, 256);
+          if (t == 0) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+              const float4 v = xr[e];
+              o[4 * e] = fmaf(other, v.x, mine * o[4 * e]);
+              o[4 * e + 1] = fmaf(other, v.y, mine * o[4 * e + 1]);
+              o[4 * e + 2] = fmaf(other, v.z, mine * o[4 * e + 2]);
+              o[4 * e + 3] = fmaf(other, v.w, mine * o[4 * e + 3]);
+            }
+          }
+          bar_sync(1, 256);
+        }
+        if (writes) {
+          if (whole) {
+            uint4* const dst = reinterpret_cast<uint4*>(a.out + at * D + c);
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+              dst[e] = make_uint4(pa_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), pa_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                  pa_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pa_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          } else {
+            float4* const dst = reinterpret_cast<float4*>(part + (int64_t)(t * 128 + idx) * D + c);
+#pragma unroll
+            for (int e = 0; e < 4; e++) __stcg(dst + e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+          }
+        }
+      }
+      tc_fence_before();
+      if (pair) fence_async_smem();  // Q's second tile may be loaded where the exchange was
+      __syncwarp();
+      if (lane == 0) {
+        if (row.any) mbar_arrive(&o_empty[t]);
+        if (pair) mbar_arrive(q_empty);
+      }
+      some += w.steps > 0;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == pa::kMma) {
+    tc_fence_after();
+    tmem_dealloc(tm, 512);
+  }
+}
+
+// Joins the parts of the units that CTAs share, a warp a row, in CTA order.
+template <int D>
+__global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ PaJoins jn, const int32_t* cu_q, int hq, int G, int T,
+                                                     int U, const float* parts, uint16_t* out, float* lse) {
+  pdl_wait();
+  const PaAt b = jn.at[blockIdx.x];
+  const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);  // tile * 128 + row of it
+  const int q0 = cu_q[b.r], m = cu_q[b.r + 1] - q0, tc = min(U, m - b.i * U);
+  const int idx = row & 127, tk = idx / G, tok = (row >> 7) * T + tk;
+  if (tk >= T || tok >= tc) return;
+  const int head = b.h * G + idx - tk * G;
+  const int c0 = jn.cta[blockIdx.x], n = b.step;
+  auto part_of = [&](int p) { return parts + (int64_t)(p == 0 ? 2 * c0 + 1 : 2 * (c0 + p)) * PaShape<D>::kPart; };
+  float M = -INFINITY, L = 0.f;
+  for (int p = lane; p < n; p += 32) M = fmaxf(M, __ldcg(part_of(p) + 256 * D + 2 * row));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float Ms = M == -INFINITY ? 0.f : M;
+  constexpr int kF = D / 32;
+  float acc[kF] = {};
+  for (int c = 0; c < n; c += 8) {
+    float2 ml[8];
+    float v[8][kF];
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      const float* pc = part_of(min(c + k, n - 1));
+      ml[k] = __ldcg(reinterpret_cast<const float2*>(pc + 256 * D) + row);
+      if constexpr (kF == 4) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(pc + (int64_t)row * D) + lane);
+        v[k][0] = u.x, v[k][1] = u.y, v[k][2] = u.z, v[k][3] = u.w;
+      } else {
+        const float2 u = __ldcg(reinterpret_cast<const float2*>(pc + (int64_t)row * D) + lane);
+        v[k][0] = u.x, v[k][1] = u.y;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+      if (c + k < n && !(ml[k].y == 0.f)) {
+        const float f = ex2(ml[k].x - Ms);
+        L = fmaf(f, ml[k].y, L);
+#pragma unroll
+        for (int q = 0; q < kF; q++) acc[q] = fmaf(f, v[k][q], acc[q]);
+      }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int64_t at = (int64_t)(q0 + b.i * U + tok) * hq + head;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(out + at * D) + lane * (kF / 2);
+#pragma unroll
+  for (int q = 0; q < kF; q += 2) dst[q / 2] = pa_bf16x2(acc[q] * inv, acc[q + 1] * inv);
+  if (lane == 0 && lse) lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
+}
+
+// ------------------------------------------------------------------ host --
+
+// How a call's units are dealt over at most `ctas` CTAs: where each share begins,
+// and the units that are split.
+struct PaPlan {
+  int ctas = 0, U = 0;
+  std::vector<PaAt> at;    // [ctas + 1]
+  std::vector<PaAt> join;  // step: parts
+  std::vector<int> first;  // CTA of a join's first part
+};
+
+static int tiles_of(int64_t p0, int64_t p1, int window) {
+  if (p1 < 0) return 0;
+  const int64_t lo = window > 0 ? std::max<int64_t>(p0 - window + 1, 0) / 128 : 0;
+  return (int)(p1 / 128 + 1 - lo);
+}
+
+// A wide step costs 2, a narrow one 1, a unit's beginning and end kUnit.
+constexpr int kUnit = 3, kPiece = 4;
+
+static void pa_plan(PaPlan& pl, const int32_t* cu_q, const int32_t* cu_k, int R, int hkv, int T, int window, int ctas) {
+  auto m_of = [&](int r) { return cu_q[r + 1] - cu_q[r]; };
+  // Few rows: a tile a unit, its keys shared by both groups.
+  int64_t wide_units = 0;
+  for (int r = 0; r < R; r++) wide_units += (int64_t)hkv * ((m_of(r) + 2 * T - 1) / (2 * T));
+  pl.U = wide_units * 2 <= ctas ? T : 2 * T;
+  const int U = pl.U;
+  struct Unit {
+    int steps, cost;  // of the unit; a step's
+  };
+  std::vector<Unit> units;           // of a kv head, request after request
+  std::vector<int64_t> cost0;        // before each unit, within its request and kv head
+  std::vector<int> begin(R + 1);
+  std::vector<int64_t> head_cost(R);
+  int64_t total = 0, pieces = 0;
+  for (int r = 0; r < R; r++) {
+    begin[r] = (int)units.size();
+    const int m = m_of(r), past = cu_k[r + 1] - cu_k[r] - m;
+    int64_t c = 0;
+    for (int t = 0; t < m; t += U) {
+      const int tc = std::min(U, m - t);
+      const Unit u = {std::max(1, tiles_of((int64_t)past + t, (int64_t)past + t + tc - 1, window)), tc > T ? 2 : 1};
+      units.push_back(u);
+      cost0.push_back(c);
+      c += kUnit + (int64_t)u.steps * u.cost;
+      pieces += (int64_t)hkv * ((u.steps + kPiece - 1) / kPiece);
+    }
+    head_cost[r] = c;
+    total += c * hkv;
+  }
+  begin[R] = (int)units.size();
+  auto add = [&](int r, int h, int i, int step) {
+    pl.at.push_back({r, h, i, step});
+  };
+  if (pieces <= ctas) {
+    // little work: every unit in even pieces of about kPiece steps, a CTA each
+    for (int r = 0; r < R; r++)
+      for (int h = 0; h < hkv; h++)
+        for (int i = 0; i < begin[r + 1] - begin[r]; i++) {
+          const int n = units[begin[r] + i].steps, k = (n + kPiece - 1) / kPiece;
+          for (int x = 0; x < k; x++) add(r, h, i, (int)((int64_t)n * x / k));
+        }
+  } else {
+    int r = 0;
+    int64_t before = 0;  // cost of the requests before r
+    for (int c = 0; c < ctas; c++) {
+      const int64_t want = total * c / ctas;
+      while (r + 1 < R && want >= before + head_cost[r] * hkv) before += head_cost[r] * hkv, r++;
+      if (begin[r + 1] == begin[r]) continue;
+      int h = (int)std::min<int64_t>((want - before) / head_cost[r], hkv - 1);
+      const int64_t in = want - before - head_cost[r] * h;
+      const int nu = begin[r + 1] - begin[r];
+      int i = (int)(std::upper_bound(cost0.begin() + begin[r], cost0.begin() + begin[r + 1], in) - (cost0.begin() + begin[r])) - 1;
+      const Unit& u = units[begin[r] + i];
+      int step = (int)((in - cost0[begin[r] + i] - kUnit / 2) / u.cost);
+      // no part of less than three steps
+      if (step < 3) step = 0;
+      if (step > u.steps - 3) {
+        step = 0;
+        if (in - cost0[begin[r] + i] >= 3 && ++i == nu) {
+          i = 0;
+          if (++h == hkv) {
+            h = 0;
+            int q = r + 1;
+            while (q < R && begin[q + 1] == begin[q]) q++;
+            if (q == R) break;
+            if (!pl.at.empty() && pl.at.back().r == q && pl.at.back().h == 0 && pl.at.back().i == 0) continue;
+            add(q, 0, 0, 0);
+            continue;
+          }
+        }
+      }
+      const PaAt x = {r, h, i, step};
+      if (!pl.at.empty()) {
+        const PaAt& y = pl.at.back();
+        const bool after = x.r != y.r ? x.r > y.r : x.h != y.h ? x.h > y.h : x.i != y.i ? x.i > y.i : x.step > y.step;
+        if (!after) continue;
+      }
+      pl.at.push_back(x);
+    }
+  }
+  pl.ctas = (int)pl.at.size();
+  add(R, 0, 0, 0);
+  for (int c = 1; c < pl.ctas; c++) {
+    if (pl.at[c].step == 0) continue;
+    const PaAt& x = pl.at[c];
+    if (!pl.join.empty() && pl.join.back().r == x.r && pl.join.back().h == x.h && pl.join.back().i == x.i) {
+      pl.join.back().step++;
+    } else {
+      pl.join.push_back({x.r, x.h, x.i, 2});
+      pl.first.push_back(c - 1);
+    }
+  }
+}
+
+static int pa_map(CUtensorMap* map, const uint16_t* p, int D, int64_t heads, int64_t rows, int64_t stride, int box_heads,
+                  int box_rows, const char* who) {
+  auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!fn) {
+    set_error("cuTensorMapEncodeTiled unavailable");
+    return SD_ERR_CUDA;
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows}, es[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_error(std::string(who) + ": cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
+    return SD_ERR_CUDA;
+  }
+  return SD_OK;
+}
+
+template <int D>
+static int pa_launch(PaArgs& a, const PaPlan& pl, cudaStream_t st) {
+  constexpr int smem = PaShape<D>::smem;
+  static const cudaError_t set[2] = {
+      cudaFuncSetAttribute(k_prompt_attn<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+      cudaFuncSetAttribute(k_prompt_attn<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)};
+  const bool bias = a.s.cap > 0.f || a.s.slopes;
+  SD_CK(set[bias]);
+  (bias ? k_prompt_attn<D, true> : k_prompt_attn<D, false>)<<<(unsigned)pl.ctas, pa::kThreads, smem, st>>>(a);
+  SD_CK(cudaGetLastError());
+  if (!pl.join.empty()) {
+    PaJoins j;
+    j.n = (int)pl.join.size();
+    std::copy(pl.join.begin(), pl.join.end(), j.at);
+    std::copy(pl.first.begin(), pl.first.end(), j.cta);
+    const dim3 grid((unsigned)j.n, a.U > a.T ? 32 : 16);
+    SD_CK(launch(k_prompt_join<D>, grid, dim3(256), 0, st, true, j, a.cu_q, a.hq, a.G, a.T, a.U, (const float*)a.part, a.out, a.lse));
+  }
+  return SD_OK;
 }
 
 }  // namespace sdv
 
 using namespace sdv;
 
+static int pa_ctas() { return std::min(num_sms(), pa::kMaxCta); }
+
 extern "C" size_t sd_prompt_attn_workspace(int32_t head_dim) {
-  return head_dim == 64 || head_dim == 128 ? 256 : 0;
+  if (head_dim != 64 && head_dim != 128) return 0;
+  return (size_t)2 * pa_ctas() * (head_dim == 128 ? PaShape<128>::kPart : PaShape<64>::kPart) * sizeof(float);
 }
 
 extern "C" int sd_prompt_attn(const uint16_t* q, int64_t q_stride, int32_t n_q_heads, const uint16_t* k, const uint16_t* v,
@@ -71,7 +857,7 @@ extern "C" int sd_prompt_attn(const uint16_t* q, int64_t q_stride, int32_t n_q_h
   if (!cu_k != !cu_k_host) return kv4_bad(SD_ERR_INVALID_ARG, who, "cu_k and cu_k_host go together");
   if (!cu_k) cu_k = cu_q, cu_k_host = cu_q_host;
   if (int rc = kv4_check_rows(cu_k, cu_k_host, R, who)) return rc;
-  PromptArgs a = {};
+  PaArgs a = {};
   if (int rc = kv4_check_score(score, who, &a.s, head_dim)) return rc;
   if (a.s.start) return kv4_bad(SD_ERR_INVALID_ARG, who, "score->start must be null: requests are packed");
   const int rows = cu_q_host[R], keys = cu_k_host[R];
@@ -83,12 +869,24 @@ extern "C" int sd_prompt_attn(const uint16_t* q, int64_t q_stride, int32_t n_q_h
     return kv4_bad(SD_ERR_INVALID_ARG, who, "strides must cover a row and be multiples of 8");
   if (!workspace || ((uintptr_t)workspace & 255)) return kv4_bad(SD_ERR_INVALID_ARG, who, "workspace must be set and 256-byte aligned");
   if (workspace_bytes < sd_prompt_attn_workspace(head_dim)) return kv4_bad(SD_ERR_WORKSPACE, who, "workspace too small");
-  a.q = q, a.k = k, a.v = v, a.q_stride = q_stride, a.kv_stride = kv_stride;
+  if ((int64_t)rows * n_q_heads > 0x7FFFFFFF) return kv4_bad(SD_ERR_UNSUPPORTED, who, "more than 2^31 rows and heads");
+  a.v = v, a.kv_stride = kv_stride;
   a.hq = n_q_heads, a.hkv = n_kv_heads, a.G = n_q_heads / n_kv_heads, a.R = R;
-  a.cu_q = cu_q, a.cu_k = cu_k, a.out = out, a.lse = lse;
-  const int64_t blocks = ((int64_t)rows * n_q_heads + 7) / 8;
-  if (blocks > 0x7FFFFFFF) return kv4_bad(SD_ERR_UNSUPPORTED, who, "too many rows");
-  (head_dim == 128 ? k_prompt_attn<128> : k_prompt_attn<64>)<<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(a, rows);
-  SD_CK(cudaGetLastError());
-  return SD_OK;
+  a.T = 128 / a.G;
+  a.cu_q = cu_q, a.cu_k = cu_k, a.out = out, a.lse = lse, a.part = (float*)workspace, a.status = status;
+  PaPlan pl;
+  try {
+    pa_plan(pl, cu_q_host, cu_k_host, R, n_kv_heads, a.T, a.s.window, pa_ctas());
+  } catch (const std::exception&) {
+    return kv4_bad(SD_ERR_OOM, who, "out of host memory");
+  }
+  a.U = pl.U;
+  std::copy(pl.at.begin(), pl.at.end(), a.at);
+  if (int rc = pa_map(&a.qmap, q, head_dim, n_q_heads, rows, q_stride, a.G, a.T, who)) return rc;
+  // no keys: the maps are not read
+  if (int rc = pa_map(&a.kmap, keys ? k : q, head_dim, keys ? n_kv_heads : n_q_heads, keys ? keys : rows, keys ? kv_stride : q_stride, 1, 128, who))
+    return rc;
+  if (int rc = pa_map(&a.vmap, keys ? v : q, head_dim, keys ? n_kv_heads : n_q_heads, keys ? keys : rows, keys ? kv_stride : q_stride, 1, 128, who))
+    return rc;
+  return head_dim == 128 ? pa_launch<128>(a, pl, (cudaStream_t)stream) : pa_launch<64>(a, pl, (cudaStream_t)stream);
 }

@@ -369,74 +369,93 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
       while (w.next(a)) {
         if (w.steps == 0) continue;
         const int n = w.ub - w.ua;
-        bool begun[2] = {false, false};
-        auto scores = [&](int t, int x, bool release) {  // step x of the share
-          const uint32_t st = (nk + x) % pa::kNK;
-          wait(&k_full[st], (nk + x) / pa::kNK);
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t q = qd + (w.wide ? t : 0) * (S::kTile >> 4), k = kd + st * (S::kTile >> 4);
-#pragma unroll
-            for (int c = 0; c < D / 16; c++)
-              umma_bf16(tm + t * 128, q + (c >> 2) * (16384 >> 4) + (c & 3) * 2, k + (c >> 2) * (16384 >> 4) + (c & 3) * 2, ids, c > 0);
-            umma_commit(&s_full[t]);
-            if (release) umma_commit(&k_empty[st]);
-          }
-          __syncwarp();
+        const uint32_t nk1 = nk, nv1 = nv;
+        const int p1 = w.p0 + w.tc - 1;
+        auto kstage = [&](int x) { return (nk1 + x) % pa::kNK; };
+        auto vstage = [&](int x) { return (nv1 + x) % pa::kNV; };
+        auto wait_k = [&](int x) { wait(&k_full[kstage(x)], (nk1 + x) / pa::kNK); };
+        auto wait_v = [&](int x) {
+          wait(&v_full[vstage(x)], (nv1 + x) / pa::kNV);
+          if (PaUnit::masked(a, w.lo + w.ua + x, w.p0, p1)) wait(&v_ok[vstage(x)], (nv1 + x) / pa::kNV);
         };
-        auto values = [&](int t, int x, bool masked, bool last, bool release) {
-          const uint32_t st = (nv + x) % pa::kNV;
-          if (!begun[t]) {
+        // by the elected lane: scores of step x, and the product with the values of step x
+        auto scores = [&](int t, int x, bool release, bool last) {
+          const uint64_t q = qd + (w.wide ? t : 0) * (S::kTile >> 4), k = kd + kstage(x) * (S::kTile >> 4);
+#pragma unroll
+          for (int c = 0; c < D / 16; c++)
+            umma_bf16(tm + t * 128, q + (c >> 2) * (16384 >> 4) + (c & 3) * 2, k + (c >> 2) * (16384 >> 4) + (c & 3) * 2, ids, c > 0);
+          umma_commit(&s_full[t]);
+          if (release) umma_commit(&k_empty[kstage(x)]);
+          if (last) umma_commit(q_empty);
+        };
+        auto values = [&](int t, int x, bool first, bool last, bool release) {
+          const uint64_t v = vd + vstage(x) * (S::kTile >> 4);
+#pragma unroll
+          for (int c = 0; c < 8; c++)
+            pa_umma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * c, v + c * (2048 >> 4), idv, !first || c > 0);
+          if (last) umma_commit(&o_full[t]);
+          if (release) umma_commit(&v_empty[vstage(x)]);
+        };
+        auto wait_p = [&](int t, bool first) {
+          if (first) {
             wait(&o_empty[t], po >> t);
             po ^= 1u << t;
           }
-          wait(&v_full[st], (nv + x) / pa::kNV);
-          if (masked) wait(&v_ok[st], (nv + x) / pa::kNV);
           wait(&p_full[t], pp >> t);
           pp ^= 1u << t;
           tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int c = 0; c < 8; c++)
-              pa_umma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * c, vd + st * (S::kTile >> 4) + c * (2048 >> 4), idv, begun[t] || c > 0);
-            if (last) umma_commit(&o_full[t]);
-            if (release) umma_commit(&v_empty[st]);
-          }
-          __syncwarp();
-          begun[t] = true;
         };
+        // The barriers of K and V are waited for ahead of P's, while the softmax runs:
+        // between P and the next scores there is nothing but the products.
         wait(q_full, units);
+        wait_k(0);
         tc_fence_after();
-        const int p1 = w.p0 + w.tc - 1;
-        auto masked = [&](int x) { return PaUnit::masked(a, w.lo + w.ua + x, w.p0, p1); };
-        auto q_done = [&]() {
-          if (elect_one()) umma_commit(q_empty);
-          __syncwarp();
-        };
         if (w.wide) {
           int x[2], y[2];
+#pragma unroll
           for (int t = 0; t < 2; t++) {
             w.range(a, t, w.ua, w.ub, x[t], y[t]);
             x[t] -= w.ua, y[t] -= w.ua;
           }
-          for (int u = -1; u < n; u++) {
-            bool v[2], s[2];
-            for (int t = 0; t < 2; t++) v[t] = u >= x[t] && u < y[t], s[t] = u + 1 >= x[t] && u + 1 < y[t];
+          if (elect_one()) {
+            if (x[0] == 0 && y[0] > 0) scores(0, 0, x[1] > 0 || y[1] == 0, n == 1 && (x[1] > 0 || y[1] == 0));
+            if (x[1] == 0 && y[1] > 0) scores(1, 0, true, n == 1);
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int u = 0; u < n; u++) {
+            wait_v(u);
+            if (u + 1 < n) wait_k(u + 1);
+            const bool s1 = u + 1 >= x[1] && u + 1 < y[1], v1 = u >= x[1] && u < y[1];
+#pragma unroll
             for (int t = 0; t < 2; t++) {
-              if (v[t]) values(t, u, masked(u), u == y[t] - 1, t == 1 || !v[1]);
-              if (s[t]) scores(t, u + 1, t == 1 || !s[1]);
+              const bool v = u >= x[t] && u < y[t], s = u + 1 >= x[t] && u + 1 < y[t];
+              if (v) wait_p(t, u == x[t]);
+              if (elect_one()) {
+                if (v) values(t, u, u == x[t], u == y[t] - 1, t == 1 || !v1);
+                if (s) scores(t, u + 1, t == 1 || !s1, u + 2 == n && (t == 1 || !s1));
+              }
+              __syncwarp();
             }
-            if (u == n - 2) q_done();
           }
         } else {
-          for (int u = 0; u < min(n, 2); u++) scores(u, u, true);
-          if (n <= 2) q_done();
+          if (n > 1) wait_k(1);
+          if (elect_one()) {
+            scores(0, 0, true, n == 1);
+            if (n > 1) scores(1, 1, true, n == 2);
+          }
+          __syncwarp();
+#pragma unroll 1
           for (int u = 0; u < n; u++) {
-            values(u & 1, u, masked(u), u >= n - 2, true);
-            if (u + 2 < n) {
-              scores(u & 1, u + 2, true);
-              if (u + 3 == n) q_done();
+            wait_v(u);
+            if (u + 2 < n) wait_k(u + 2);
+            const int t = u & 1;
+            wait_p(t, u < 2);
+            if (elect_one()) {
+              values(t, u, u < 2, u >= n - 2, true);
+              if (u + 2 < n) scores(t, u + 2, true, u + 3 == n);
             }
+            __syncwarp();
           }
         }
         nk += n, nv += n;

@@ -6,18 +6,18 @@
 // head's query heads are packed, token by token, into tiles of 128 (T = 128 / G tokens
 // of G heads), so that K and V are read once for the group and a single token fills G
 // rows.  A unit is a kv head and 2 T tokens (two tiles, WIDE) or up to T (one); its
-// steps are tiles of 128 keys.  Warps:
+// steps are 128 keys.  Warps:
 //  * 0..3 and 4..7: softmax, a thread a row: 128 scores from TMEM, maximum,
 //    exponentials, P (bf16) back over its scores; then the outputs.  A wide unit
 //    gives each of the two groups a tile of rows, a narrow one alternate steps of the
 //    same rows, joined through shared memory.  A row's reference may lag its maximum
 //    by 2^8 before O is rescaled in TMEM.
-//  * 8: the products: S = Q K^T and O += P V, those of one tile while the other is in
-//    its softmax.  TMEM: [S 128][S 128][O D][O D].
-//  * 9: Q, K and V by TMA.
-//  * 10, 11: in steps where some row does not see some key, look for infinities and
-//    NaNs in V (P is 0 there, and 0 times those is not) and take them out of the
-//    operand; the rows that do see them get them back at the end (s_bad).
+//  * 8, 9: the products of one group each: S = Q K^T and O += P V, those of one group
+//    while the other is in its softmax.  TMEM: [S 128][S 128][O D][O D].
+//  * 10: Q, K and V by TMA.
+//  * 11: in steps where some row does not see some key, looks for infinities and NaNs
+//    in V (P is 0 there, and 0 times those is not) and takes them out of the operand;
+//    the rows that do see them get them back at the end.
 // The steps are dealt evenly over the CTAs, by the host (it has the lengths): a
 // unit may be split over its keys; its parts are joined by a second kernel.
 #include <cudaTypedefs.h>
@@ -32,7 +32,8 @@
 namespace sdv {
 
 namespace pa {
-constexpr int kThreads = 384, kMma = 8, kLoad = 9, kCheck = 10;
+constexpr int kThreads = 384, kMma = 8, kLoad = 10, kCheck = 11;
+constexpr int kKeys = 128;       // of a step
 constexpr int kMaxCta = 160;
 constexpr int kNK = 2, kNV = 3;  // stages of K and of V
 constexpr float kLag = 8.f;
@@ -68,10 +69,10 @@ struct PaJoins {
 
 template <int D>
 struct PaShape {
-  static constexpr int kTile = 128 * D * 2;
-  static constexpr int off_k = 2 * kTile, off_v = off_k + pa::kNK * kTile;
-  static constexpr int off_x = D == 128 ? kTile : off_v + pa::kNV * kTile;  // [128][kXs] floats; narrow units leave Q's second tile free
-  static constexpr int off_ml = off_v + pa::kNV * kTile + (D == 128 ? 0 : 128 * pa::kXs * 4);
+  static constexpr int kTile = 128 * D * 2, kStep = pa::kKeys * D * 2;
+  static constexpr int off_k = 2 * kTile, off_v = off_k + pa::kNK * kStep;
+  static constexpr int off_x = kTile;  // [128][kXs] floats: narrow units leave Q's second tile free
+  static constexpr int off_ml = off_v + pa::kNV * kStep;
   static constexpr int off_bar = off_ml + 128 * 8;
   static constexpr int smem = off_bar + 64 * 8 + 1024;
   static constexpr int kPart = 256 * (D + 2);  // floats of a part: [row][D], then [row] (reference, sum)
@@ -84,7 +85,7 @@ struct PaUnit {
   int nu;              // units a kv head
   int tok, tc;         // first token, tokens
   int p0;              // position of the first
-  int lo, steps;       // first key tile, tiles (0: no row sees a key)
+  int lo, steps;       // first step's number (key / 128), steps (0: no row sees a key)
   bool wide;
   __device__ __forceinline__ void request(const PaArgs& a) {
     q0 = a.cu_q[r], m = a.cu_q[r + 1] - q0;
@@ -97,22 +98,22 @@ struct PaUnit {
     wide = tc > a.T;
     p0 = n - m + tok;
     const int p1 = p0 + tc - 1;
-    lo = first_tile(a, p0);
-    steps = p1 < 0 ? 0 : p1 / 128 + 1 - lo;
+    lo = first_step(a, p0);
+    steps = p1 < 0 ? 0 : p1 / pa::kKeys + 1 - lo;
   }
-  // the tile of the first key that a row at position p sees
-  static __device__ __forceinline__ int first_tile(const PaArgs& a, int p) {
-    return a.s.window > 0 && p >= 0 ? max(p - a.s.window + 1, 0) / 128 : 0;
+  // the step of the first key that a row at position p sees
+  static __device__ __forceinline__ int first_step(const PaArgs& a, int p) {
+    return a.s.window > 0 && p >= 0 ? max(p - a.s.window + 1, 0) / pa::kKeys : 0;
   }
-  // some row of positions pa .. pb does not see some key of tile j
+  // some row of positions pa .. pb does not see some key of step j
   static __device__ __forceinline__ bool masked(const PaArgs& a, int j, int pa, int pb) {
-    return j * 128 + 127 > pa || (a.s.window > 0 && pb >= 0 && j * 128 < pb - a.s.window + 1);
+    return j * pa::kKeys + pa::kKeys - 1 > pa || (a.s.window > 0 && pb >= 0 && j * pa::kKeys < pb - a.s.window + 1);
   }
   // steps [x, y) of those from ua to ub in which tile t of a wide unit has keys
   __device__ __forceinline__ void range(const PaArgs& a, int t, int ua, int ub, int& x, int& y) const {
     const int f = p0 + t * a.T, l = p0 + (t ? tc : a.T) - 1;
-    x = max(ua, first_tile(a, f) - lo);
-    y = l < 0 ? x : min(ub, l / 128 + 1 - lo);
+    x = max(ua, first_step(a, f) - lo);
+    y = l < 0 ? x : min(ub, l / pa::kKeys + 1 - lo);
     y = max(x, y);
   }
 };
@@ -199,17 +200,31 @@ __device__ __forceinline__ uint64_t pa_sdesc_v(uint32_t saddr) {
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// A bounded wait in few instructions (all of the kernel's code has to stay in the
+// instruction cache): past the limit it sets *abort, which ends every wait.
+__device__ __forceinline__ void pa_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = globaltimer();
+#pragma unroll 1
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); i++) {
+    if (i % 64) continue;  // a try suspends the warp for a while by itself
+    if (*abort) return;
+    if (globaltimer() - t0 > kWaitLimitNs) *abort = 1;
+  }
+}
+
 // What a softmax thread keeps of its row over a unit.
 struct PaRow {
   float ref, l;  // reference (base 2), sum of 2^(score - ref)
-  bool any;      // the group had steps
+  int done;      // steps
 };
 
-// One step of a tile: scores from TMEM, P back.  kb: first key; see0 .. see1: the
-// keys that the row sees; masked: some row of the tile does not see some key.
-template <int D, bool BIAS>
+// One step: scores from TMEM, P back in two halves, said by half(0) and half(1).  kb:
+// first key; see0 .. see1: the keys that the row sees; masked: some row of the tile
+// does not see some key.
+template <int D, bool BIAS, typename Half>
 __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, uint32_t to, int kb, int see0, int see1,
-                                        bool masked, float f, float slope) {
+                                        bool masked, float f, float slope, Half half) {
   float x[128];
   pa_tmem_ld(ts, x);
   if (BIAS) {
@@ -226,17 +241,19 @@ __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, 
   }
   float t4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-  for (int c = 4; c < 128; c += 8) {
+  for (int c = 4; c < 124; c += 8) {
 #pragma unroll
-    for (int e = 0; e < 4; e++) t4[e] = c + 4 + e < 128 ? fmaxf(t4[e], fmaxf(x[c + e], x[c + 4 + e])) : fmaxf(t4[e], x[c + e]);
+    for (int e = 0; e < 4; e++) t4[e] = fmaxf(t4[e], fmaxf(x[c + e], x[c + 4 + e]));
   }
+#pragma unroll
+  for (int e = 0; e < 4; e++) t4[e] = fmaxf(t4[e], x[124 + e]);
   const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f;
   const bool grows = top > w.ref + pa::kLag || (w.ref == -INFINITY && top > w.ref);
   if (__any_sync(0xffffffffu, grows)) {
     const float al = grows ? ex2(w.ref - top) : 1.f;
     if (grows) w.ref = top;
     w.l *= al;
-    if (w.any) {  // the product before is done: its commit came before these scores'
+    if (w.done) {  // the product before is done: its commit came before these scores'
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         float o[16];
@@ -264,12 +281,15 @@ __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, 
       p[c / 2] = pa_bf16x2(p0, p1);
     }
     pa_tmem_st(ts + c0 / 2, p);
+    if (c0 % 64 == 32) {
+      pa_wait_st();
+      half(c0 / 64);
+    }
   }
   float l0, l1;
   f2unpack(f2add(l2[0], l2[1]), l0, l1);
   w.l += l0 + l1;
-  pa_wait_st();
-  w.any = true;
+  w.done++;
 }
 
 template <int D, bool BIAS>
@@ -278,21 +298,21 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
   extern __shared__ uint8_t smem_pa[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_pa) + 1023) & ~uintptr_t(1023));
   uint64_t* const q_full = reinterpret_cast<uint64_t*>(sm + S::off_bar);
-  uint64_t* const q_empty = q_full + 1;            // products with Q done (commit), exchange done (8 warps)
+  uint64_t* const q_empty = q_full + 1;            // products with Q done (2 commits), exchange done (8 warps)
   uint64_t* const k_full = q_empty + 1;            // [kNK]
-  uint64_t* const k_empty = k_full + pa::kNK;
+  uint64_t* const k_empty = k_full + pa::kNK;      // [kNK] products done (2)
   uint64_t* const v_full = k_empty + pa::kNK;      // [kNV]
-  uint64_t* const v_empty = v_full + pa::kNV;      // products done (commit), looked at (2 warps)
-  uint64_t* const v_ok = v_empty + pa::kNV;        // looked at (2 warps)
-  uint64_t* const s_full = v_ok + pa::kNV;         // [t] scores ready (commit)
-  uint64_t* const p_full = s_full + 2;             // [t] weights written (4 warps)
-  uint64_t* const o_full = p_full + 2;             // [t] a unit's last product done (commit)
+  uint64_t* const v_empty = v_full + pa::kNV;      // [kNV] products done (2), looked at
+  uint64_t* const v_ok = v_empty + pa::kNV;        // [kNV] looked at
+  uint64_t* const s_full = v_ok + pa::kNV;         // [t] scores ready, the products before them done (commit)
+  uint64_t* const p_full = s_full + 2;             // [t][half] weights written (4 warps)
+  uint64_t* const o_full = p_full + 4;             // [t] a unit's last product done (commit)
   uint64_t* const o_empty = o_full + 2;            // [t] outputs read (4 warps)
   float2* const s_ml = reinterpret_cast<float2*>(sm + S::off_ml);
   float* const s_x = reinterpret_cast<float*>(sm + S::off_x);
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_turn;  // s_turn: 1 while a group's products are being issued
   __shared__ uint32_t s_tmem;
-  __shared__ int s_bad[8][2];  // [unit with steps, mod 8][checking warp]
+  __shared__ int s_bad[8];  // [unit with steps, mod 8]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch();
 
@@ -301,19 +321,31 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
     tmem_relinquish();
   }
   if (tid == 0) {
-    mbar_init(q_full, 1), mbar_init(q_empty, 9);
-    for (int i = 0; i < pa::kNK; i++) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 1);
-    for (int i = 0; i < pa::kNV; i++) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 3), mbar_init(&v_ok[i], 2);
-    for (int t = 0; t < 2; t++) mbar_init(&s_full[t], 1), mbar_init(&p_full[t], 4), mbar_init(&o_full[t], 1), mbar_init(&o_empty[t], 4);
+    mbar_init(q_full, 1), mbar_init(q_empty, 10);
+    for (int i = 0; i < pa::kNK; i++) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 2);
+    for (int i = 0; i < pa::kNV; i++) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 3), mbar_init(&v_ok[i], 1);
+    for (int t = 0; t < 2; t++) {
+      mbar_init(&s_full[t], 1), mbar_init(&o_full[t], 1), mbar_init(&o_empty[t], 4);
+      mbar_init(&p_full[2 * t], 4), mbar_init(&p_full[2 * t + 1], 4);
+    }
     s_abort = 0;
+    s_turn = 0;
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = s_tmem;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!kv4_wait(bar, parity & 1, &s_abort)) set_status(a.status, SD_TIMEOUT_AT(40));
+  auto wait = [&](uint64_t* bar, uint32_t parity) { pa_wait(smem_u32(bar), parity & 1, &s_abort); };
+  // One group's products at a time: those of both, interleaved, would end together,
+  // and the softmax of both would run together, with the tensor cores idle.
+  auto turn = [&]() {
+    const uint64_t t0 = globaltimer();
+#pragma unroll 1
+    while (atomicCAS(&s_turn, 0, 1) != 0) {
+      if (*(volatile int*)&s_abort) return;
+      if (globaltimer() - t0 > kWaitLimitNs) *(volatile int*)&s_abort = 1;
+    }
   };
   PaWalk w(a);
 
@@ -326,22 +358,22 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
         const int n = w.ub - w.ua;
         auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, int step) {
           if (lane == 0) {
-            mbar_arrive_expect_tx(full, S::kTile);
+            mbar_arrive_expect_tx(full, S::kStep);
 #pragma unroll
-            for (int d = 0; d < D; d += 64) tma3d_g2s(dst + d * 256, map, d, w.h, w.k0 + (w.lo + step) * 128, full);
+            for (int d = 0; d < D; d += 64) tma3d_g2s(dst + d * 256, map, d, w.h, w.k0 + (w.lo + step) * pa::kKeys, full);
           }
           __syncwarp();
         };
         auto load_k = [&](int step) {
           const uint32_t st = nk % pa::kNK;
           wait(&k_empty[st], (nk / pa::kNK & 1) ^ 1);
-          load(sm + S::off_k + st * S::kTile, &a.kmap, &k_full[st], step);
+          load(sm + S::off_k + st * S::kStep, &a.kmap, &k_full[st], step);
           nk++;
         };
         auto load_v = [&](int step) {
           const uint32_t st = nv % pa::kNV;
           wait(&v_empty[st], (nv / pa::kNV & 1) ^ 1);
-          load(sm + S::off_v + st * S::kTile, &a.vmap, &v_full[st], step);
+          load(sm + S::off_v + st * S::kStep, &a.vmap, &v_full[st], step);
           nv++;
         };
         load_k(w.ua);
@@ -360,131 +392,119 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
         }
         units++;
       }
-    } else if (warp == pa::kMma) {
-      const uint32_t id0 = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);  // fp32 += bf16 bf16, M = 128
-      const uint32_t ids = id0 | (16u << 17), idv = id0 | (1u << 16) | ((uint32_t)(D / 8) << 17);
-      const uint64_t qd = sdesc_sw128(smem_u32(sm)), kd = sdesc_sw128(smem_u32(sm + S::off_k)),
-                     vd = pa_sdesc_v(smem_u32(sm + S::off_v));
-      uint32_t nk = 0, nv = 0, units = 0, pp = 0, po = 3;  // pp, po: parities of p_full and o_empty
-      while (w.next(a)) {
-        if (w.steps == 0) continue;
-        const int n = w.ub - w.ua;
-        const uint32_t nk1 = nk, nv1 = nv;
-        const int p1 = w.p0 + w.tc - 1;
-        auto kstage = [&](int x) { return (nk1 + x) % pa::kNK; };
-        auto vstage = [&](int x) { return (nv1 + x) % pa::kNV; };
-        auto wait_k = [&](int x) { wait(&k_full[kstage(x)], (nk1 + x) / pa::kNK); };
-        auto wait_v = [&](int x) {
-          wait(&v_full[vstage(x)], (nv1 + x) / pa::kNV);
-          if (PaUnit::masked(a, w.lo + w.ua + x, w.p0, p1)) wait(&v_ok[vstage(x)], (nv1 + x) / pa::kNV);
-        };
-        // by the elected lane: scores of step x, and the product with the values of step x
-        auto scores = [&](int t, int x, bool release, bool last) {
-          const uint64_t q = qd + (w.wide ? t : 0) * (S::kTile >> 4), k = kd + kstage(x) * (S::kTile >> 4);
-#pragma unroll
-          for (int c = 0; c < D / 16; c++)
-            umma_bf16(tm + t * 128, q + (c >> 2) * (16384 >> 4) + (c & 3) * 2, k + (c >> 2) * (16384 >> 4) + (c & 3) * 2, ids, c > 0);
-          umma_commit(&s_full[t]);
-          if (release) umma_commit(&k_empty[kstage(x)]);
-          if (last) umma_commit(q_empty);
-        };
-        auto values = [&](int t, int x, bool first, bool last, bool release) {
-          const uint64_t v = vd + vstage(x) * (S::kTile >> 4);
-#pragma unroll
-          for (int c = 0; c < 8; c++)
-            pa_umma_ts(tm + 256 + t * 128, tm + t * 128 + 8 * c, v + c * (2048 >> 4), idv, !first || c > 0);
-          if (last) umma_commit(&o_full[t]);
-          if (release) umma_commit(&v_empty[vstage(x)]);
-        };
-        auto wait_p = [&](int t, bool first) {
-          if (first) {
-            wait(&o_empty[t], po >> t);
-            po ^= 1u << t;
+    } else if (warp < pa::kLoad) {
+      if (elect_one()) {  // one lane throughout
+        const int t = warp - pa::kMma;
+        const uint32_t id0 = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);  // fp32 += bf16 bf16, M = 128
+        const uint32_t ids = id0 | ((uint32_t)(pa::kKeys / 8) << 17), idv = id0 | (1u << 16) | ((uint32_t)(D / 8) << 17);
+        const uint64_t kd = sdesc_sw128(smem_u32(sm + S::off_k)), vd = pa_sdesc_v(smem_u32(sm + S::off_v));
+        const uint32_t ts = tm + t * 128, to = tm + 256 + t * 128;
+        uint32_t nk = 0, nv = 0, units = 0, pp = 0, po = 1;  // stages taken, units; parities of p_full and o_empty
+        while (w.next(a)) {
+          if (w.steps == 0) continue;
+          const int n = w.ub - w.ua, p1 = w.p0 + w.tc - 1, j0 = w.lo + w.ua;
+          // the group's steps: x, x + by, ... below y
+          int x = t, y = n, by = 2;
+          if (w.wide) {
+            w.range(a, t, w.ua, w.ub, x, y);
+            x -= w.ua, y -= w.ua, by = 1;
           }
-          wait(&p_full[t], pp >> t);
-          pp ^= 1u << t;
-          tc_fence_after();
-        };
-        // The barriers of K and V are waited for ahead of P's, while the softmax runs:
-        // between P and the next scores there is nothing but the products.
-        wait(q_full, units);
-        wait_k(0);
-        tc_fence_after();
-        if (w.wide) {
-          int x[2], y[2];
-#pragma unroll
-          for (int t = 0; t < 2; t++) {
-            w.range(a, t, w.ua, w.ub, x[t], y[t]);
-            x[t] -= w.ua, y[t] -= w.ua;
-          }
-          if (elect_one()) {
-            if (x[0] == 0 && y[0] > 0) scores(0, 0, x[1] > 0 || y[1] == 0, n == 1 && (x[1] > 0 || y[1] == 0));
-            if (x[1] == 0 && y[1] > 0) scores(1, 0, true, n == 1);
-          }
-          __syncwarp();
-#pragma unroll 1
-          for (int u = 0; u < n; u++) {
-            wait_v(u);
-            if (u + 1 < n) wait_k(u + 1);
-            const bool s1 = u + 1 >= x[1] && u + 1 < y[1], v1 = u >= x[1] && u < y[1];
-#pragma unroll
-            for (int t = 0; t < 2; t++) {
-              const bool v = u >= x[t] && u < y[t], s = u + 1 >= x[t] && u + 1 < y[t];
-              if (v) wait_p(t, u == x[t]);
-              if (elect_one()) {
-                if (v) values(t, u, u == x[t], u == y[t] - 1, t == 1 || !v1);
-                if (s) scores(t, u + 1, t == 1 || !s1, u + 2 == n && (t == 1 || !s1));
-              }
-              __syncwarp();
+          const uint64_t qd = sdesc_sw128(smem_u32(sm + (w.wide ? t : 0) * S::kTile));
+          // every step's stages are released by both groups, so that neither gets ahead
+          int k = 0, v = 0;  // steps whose K and V are taken
+          auto pass_k = [&](int u) {
+            for (; k < u; k++, nk++) {
+              wait(&k_full[nk % pa::kNK], nk / pa::kNK);
+              mbar_arrive(&k_empty[nk % pa::kNK]);
             }
-          }
-        } else {
-          if (n > 1) wait_k(1);
-          if (elect_one()) {
-            scores(0, 0, true, n == 1);
-            if (n > 1) scores(1, 1, true, n == 2);
-          }
-          __syncwarp();
-#pragma unroll 1
-          for (int u = 0; u < n; u++) {
-            wait_v(u);
-            if (u + 2 < n) wait_k(u + 2);
-            const int t = u & 1;
-            wait_p(t, u < 2);
-            if (elect_one()) {
-              values(t, u, u < 2, u >= n - 2, true);
-              if (u + 2 < n) scores(t, u + 2, true, u + 3 == n);
+          };
+          auto pass_v = [&](int u) {
+            for (; v < u; v++, nv++) {
+              wait(&v_full[nv % pa::kNV], nv / pa::kNV);
+              mbar_arrive(&v_empty[nv % pa::kNV]);
             }
-            __syncwarp();
+          };
+          auto scores = [&](int u) {  // of step u, whose K is there
+            const uint32_t st = nk % pa::kNK;
+            const uint64_t kk = kd + st * (S::kStep >> 4);
+#pragma unroll
+            for (int c = 0; c < D / 16; c++)
+              umma_bf16(ts, qd + (c >> 2) * (16384 >> 4) + (c & 3) * 2, kk + (c >> 2) * (16384 >> 4) + (c & 3) * 2, ids, c > 0);
+            umma_commit(&s_full[t]);
+            umma_commit(&k_empty[st]);
+            if (u + by >= y) umma_commit(q_empty);
+            k++, nk++;
+          };
+          wait(q_full, units);
+          if (x < y) {
+            pass_k(x);
+            wait(&k_full[nk % pa::kNK], nk / pa::kNK);
+            tc_fence_after();
+            scores(x);
           }
+#pragma unroll 1
+          for (int u = x; u < y; u += by) {
+            // K and V are waited for ahead of P, while the softmax runs: between P and the
+            // next scores there is nothing but the products
+            pass_v(u);
+            const uint32_t st = nv % pa::kNV;
+            wait(&v_full[st], nv / pa::kNV);
+            if (PaUnit::masked(a, j0 + u, w.p0, p1)) wait(&v_ok[st], nv / pa::kNV);
+            if (u + by < y) {
+              pass_k(u + by);
+              wait(&k_full[nk % pa::kNK], nk / pa::kNK);
+            }
+            if (u == x) {
+              wait(&o_empty[t], po);
+              po ^= 1;
+            }
+            const uint64_t vv = vd + st * (S::kStep >> 4);
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              wait(&p_full[2 * t + h], pp);
+              if (h == 0) turn();
+              tc_fence_after();
+#pragma unroll
+              for (int c = 4 * h; c < 4 * h + 4; c++)
+                pa_umma_ts(to, ts + 8 * c, vv + c * (2048 >> 4), idv, u > x || c > 0);
+            }
+            pp ^= 1;
+            if (u + by < y) scores(u + by);
+            else umma_commit(&o_full[t]);
+            umma_commit(&v_empty[st]);
+            atomicExch(&s_turn, 0);
+            v++, nv++;
+          }
+          pass_k(n);
+          pass_v(n);
+          if (x >= y) mbar_arrive(q_empty);
+          units++;
         }
-        nk += n, nv += n;
-        units++;
       }
+      __syncwarp();
     } else {
       // ----------------------------------------------- looking at values --
-      const int half = warp - pa::kCheck;
       uint32_t nv = 0, units = 0;
       while (w.next(a)) {
         if (w.steps == 0) continue;
         const int n = w.ub - w.ua, p1 = w.p0 + w.tc - 1;
-        if (lane == 0) s_bad[units & 7][half] = 0;
+        if (lane == 0) s_bad[units & 7] = 0;
         for (int x = 0; x < n; x++, nv++) {
           const uint32_t st = nv % pa::kNV;
           wait(&v_full[st], nv / pa::kNV);
           if (PaUnit::masked(a, w.lo + w.ua + x, w.p0, p1)) {
-            uint4* const v = reinterpret_cast<uint4*>(sm + S::off_v + st * S::kTile + half * (S::kTile / 2));
+            uint4* const v = reinterpret_cast<uint4*>(sm + S::off_v + st * S::kStep);
             uint32_t odd = 0;  // bit 15 of a half word: its exponent is all ones
 #pragma unroll 8
-            for (int i = lane; i < S::kTile / 32; i += 32) {
+            for (int i = lane; i < S::kStep / 16; i += 32) {
               const uint4 u = v[i];
               odd |= ((u.x & 0x7F807F80u) + 0x00800080u) | ((u.y & 0x7F807F80u) + 0x00800080u) |
                      ((u.z & 0x7F807F80u) + 0x00800080u) | ((u.w & 0x7F807F80u) + 0x00800080u);
             }
             if (__any_sync(0xffffffffu, odd & 0x80008000u)) {
-              if (lane == 0) s_bad[units & 7][half] = 1;
+              if (lane == 0) s_bad[units & 7] = 1;
               uint32_t* const vw = reinterpret_cast<uint32_t*>(v);
-              for (int i = lane; i < S::kTile / 8; i += 32) {
+              for (int i = lane; i < S::kStep / 4; i += 32) {
                 const uint32_t u = vw[i], o = ((u & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
                 if (o) vw[i] = u & ~((o >> 15) * 0xFFFFu);
               }
@@ -518,7 +538,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
       const int hq = w.h * a.G + min(g, a.G - 1);
       const float slope = BIAS && a.s.slopes ? a.s.slopes[hq] * kLog2e : 0.f;
       const int pa0 = w.p0 + base, pb0 = pa0 + toks - 1;
-      PaRow row = {-INFINITY, 0.f, false};
+      PaRow row = {-INFINITY, 0.f, 0};
       const bool pair = !w.wide && w.steps;            // the groups share the rows
       int x = 0, y = 0, by = 1;
       if (w.steps) {
@@ -533,24 +553,25 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
         sp ^= 1;
         tc_fence_after();
         const int j = w.lo + u;
-        pa_step<D, BIAS>(a, row, ts, to, j * 128, see0, p, PaUnit::masked(a, j, pa0, pb0), f, slope);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t]);
+        pa_step<D, BIAS>(a, row, ts, to, j * pa::kKeys, see0, p, PaUnit::masked(a, j, pa0, pb0), f, slope, [&](int h) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
+        });
       }
       bool bad = false;
-      if (row.any) {
+      if (row.done) {
         wait(&o_full[t], op);
         op ^= 1;
         tc_fence_after();
-        bad = *(volatile int*)&s_bad[some & 7][0] | *(volatile int*)&s_bad[some & 7][1];
+        bad = *(volatile int*)&s_bad[some & 7];
       }
       // infinities and NaNs that were taken out of V and that the row sees
       auto give_back = [&](float (&o)[16], int c) {
         for (int u = x; u < y; u += by) {
           const int j = w.lo + u;
           if (!PaUnit::masked(a, j, w.p0, w.p0 + w.tc - 1)) continue;
-          for (int key = max(j * 128, see0); key <= min(j * 128 + 127, p); key++) {
+          for (int key = max(j * pa::kKeys, see0); key <= min(j * pa::kKeys + pa::kKeys - 1, p); key++) {
             const uint16_t* v = a.v + (int64_t)(w.k0 + key) * a.kv_stride + w.h * D + c;
 #pragma unroll
             for (int e = 0; e < 16; e++)
@@ -570,7 +591,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           const float2 ml = s_ml[idx];
           M = fmaxf(row.ref, ml.x);
           const float Ms = M == -INFINITY ? 0.f : M;
-          mine = row.any ? ex2(row.ref - Ms) : 0.f;
+          mine = row.done ? ex2(row.ref - Ms) : 0.f;
           other = ml.x == -INFINITY ? 0.f : ex2(ml.x - Ms);
           L = mine * row.l + other * ml.y;
           if (!(ml.y == ml.y)) L = ml.y, other = ml.y;  // a NaN among the other's scores
@@ -588,9 +609,9 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         float o[16];
-        if (row.any) tmem_ld16(to + c, o);
+        if (row.done) tmem_ld16(to + c, o);
 #pragma unroll
-        for (int e = 0; e < 16; e++) o[e] = row.any && row.l != 0.f ? o[e] : 0.f;
+        for (int e = 0; e < 16; e++) o[e] = row.done && row.l != 0.f ? o[e] : 0.f;
         if (bad && live) give_back(o, c);
         if (pair) {
           float4* const xr = reinterpret_cast<float4*>(s_x + idx * pa::kXs);
@@ -629,7 +650,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
       if (pair) fence_async_smem();  // Q's second tile may be loaded where the exchange was
       __syncwarp();
       if (lane == 0) {
-        if (row.any) mbar_arrive(&o_empty[t]);
+        if (row.done) mbar_arrive(&o_empty[t]);
         if (pair) mbar_arrive(q_empty);
       }
       some += w.steps > 0;
@@ -640,6 +661,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
   if (warp == pa::kMma) {
     tc_fence_after();
     tmem_dealloc(tm, 512);
+    if (s_abort && lane == 0) set_status(a.status, SD_TIMEOUT_AT(40));
   }
 }
 
@@ -706,10 +728,10 @@ struct PaPlan {
   std::vector<int> first;  // CTA of a join's first part
 };
 
-static int tiles_of(int64_t p0, int64_t p1, int window) {
+static int steps_of(int64_t p0, int64_t p1, int window) {
   if (p1 < 0) return 0;
-  const int64_t lo = window > 0 ? std::max<int64_t>(p0 - window + 1, 0) / 128 : 0;
-  return (int)(p1 / 128 + 1 - lo);
+  const int64_t lo = window > 0 ? std::max<int64_t>(p0 - window + 1, 0) / pa::kKeys : 0;
+  return (int)(p1 / pa::kKeys + 1 - lo);
 }
 
 // A wide step costs 2, a narrow one 1, a unit's beginning and end kUnit.
@@ -736,7 +758,7 @@ static void pa_plan(PaPlan& pl, const int32_t* cu_q, const int32_t* cu_k, int R,
     int64_t c = 0;
     for (int t = 0; t < m; t += U) {
       const int tc = std::min(U, m - t);
-      const Unit u = {std::max(1, tiles_of((int64_t)past + t, (int64_t)past + t + tc - 1, window)), tc > T ? 2 : 1};
+      const Unit u = {std::max(1, steps_of((int64_t)past + t, (int64_t)past + t + tc - 1, window)), tc > T ? 2 : 1};
       units.push_back(u);
       cost0.push_back(c);
       c += kUnit + (int64_t)u.steps * u.cost;
@@ -774,7 +796,7 @@ static void pa_plan(PaPlan& pl, const int32_t* cu_q, const int32_t* cu_k, int R,
       if (step < 3) step = 0;
       if (step > u.steps - 3) {
         step = 0;
-        if (in - cost0[begin[r] + i] >= 3 && ++i == nu) {
+        if (in - cost0[begin[r] + i] >= kUnit && ++i == nu) {
           i = 0;
           if (++h == hkv) {
             h = 0;
@@ -903,9 +925,9 @@ extern "C" int sd_prompt_attn(const uint16_t* q, int64_t q_stride, int32_t n_q_h
   std::copy(pl.at.begin(), pl.at.end(), a.at);
   if (int rc = pa_map(&a.qmap, q, head_dim, n_q_heads, rows, q_stride, a.G, a.T, who)) return rc;
   // no keys: the maps are not read
-  if (int rc = pa_map(&a.kmap, keys ? k : q, head_dim, keys ? n_kv_heads : n_q_heads, keys ? keys : rows, keys ? kv_stride : q_stride, 1, 128, who))
+  if (int rc = pa_map(&a.kmap, keys ? k : q, head_dim, keys ? n_kv_heads : n_q_heads, keys ? keys : rows, keys ? kv_stride : q_stride, 1, pa::kKeys, who))
     return rc;
-  if (int rc = pa_map(&a.vmap, keys ? v : q, head_dim, keys ? n_kv_heads : n_q_heads, keys ? keys : rows, keys ? kv_stride : q_stride, 1, 128, who))
+  if (int rc = pa_map(&a.vmap, keys ? v : q, head_dim, keys ? n_kv_heads : n_q_heads, keys ? keys : rows, keys ? kv_stride : q_stride, 1, pa::kKeys, who))
     return rc;
   return head_dim == 128 ? pa_launch<128>(a, pl, (cudaStream_t)stream) : pa_launch<64>(a, pl, (cudaStream_t)stream);
 }

@@ -14,7 +14,7 @@
 //    by 2^8 before O is rescaled in TMEM.
 //  * 8, 9: the products of one group each: S = Q K^T and O += P V, those of one group
 //    while the other is in its softmax.  TMEM: [S 128][S 128][O D][O D].
-//  * 10: Q, K and V by TMA.
+//  * 10: walks the CTA's units, says what each is (PaDesc), and loads Q, K and V by TMA.
 //  * 11: in steps where some row does not see some key, looks for infinities and NaNs
 //    in V (P is 0 there, and 0 times those is not) and takes them out of the operand;
 //    the rows that do see them get them back at the end.
@@ -32,10 +32,11 @@
 namespace sdv {
 
 namespace pa {
-constexpr int kThreads = 384, kMma = 8, kLoad = 10, kCheck = 11;
+constexpr int kThreads = 384, kMma = 8, kLoad = 10;
 constexpr int kKeys = 128;       // of a step
 constexpr int kMaxCta = 160;
-constexpr int kNK = 2, kNV = 3;  // stages of K and of V
+constexpr int kNK = 2, kNV = 2;  // stages of K and of V
+constexpr int kNU = 4;           // units being described
 constexpr float kLag = 8.f;
 constexpr int kXs = 20;          // floats of a row being exchanged (16 used)
 }  // namespace pa
@@ -72,11 +73,34 @@ struct PaShape {
   static constexpr int kTile = 128 * D * 2, kStep = pa::kKeys * D * 2;
   static constexpr int off_k = 2 * kTile, off_v = off_k + pa::kNK * kStep;
   static constexpr int off_x = kTile;  // [128][kXs] floats: narrow units leave Q's second tile free
-  static constexpr int off_ml = off_v + pa::kNV * kStep;
+  static constexpr int off_o = off_v + pa::kNV * kStep;            // [8 warps][32 rows][64 dims] bf16
+  static constexpr int off_ml = off_o + 8 * 4096;
   static constexpr int off_bar = off_ml + 128 * 8;
-  static constexpr int smem = off_bar + 64 * 8 + 1024;
+  static constexpr int off_ctl = off_bar + 64 * 8;                 // PaCtl
+  static constexpr int smem = off_ctl + 512;
   static constexpr int kPart = 256 * (D + 2);  // floats of a part: [row][D], then [row] (reference, sum)
 };
+
+// A unit, or a share of its steps, as the CTA's warps need it.  Steps are counted from
+// the unit's first.
+struct PaDesc {
+  int n;               // steps of the share; 0: no row sees a key, -1: the end
+  int wide, tc;        // two tiles; tokens
+  int h, k0, lo;       // kv head; the request's first key; number (key / 128) of step 0
+  int tok, p0;         // row of the first token, its position
+  int ua;              // first step of the share
+  int part;            // -1: the unit is whole; else the slot of its part
+  int m0, m1;          // steps from m0 up to m1: every row sees every key
+  int x[2], y[2];      // steps x, x + 1 (narrow: x + 2), ... below y are a group's
+  int g0[2], g1[2];    // as m0, m1, for the rows of a group's tile
+};
+struct PaCtl {
+  PaDesc unit[pa::kNU];
+  int abort, turn;     // turn: 1 while a group's products are being issued
+  uint32_t tmem;
+  int bad[8];          // [unit with steps, mod 8]: infinities or NaNs were taken out of V
+};
+static_assert(sizeof(PaCtl) <= 512, "PaShape::smem");
 
 // A unit's rows and steps.
 struct PaUnit {
@@ -85,7 +109,7 @@ struct PaUnit {
   int nu;              // units a kv head
   int tok, tc;         // first token, tokens
   int p0;              // position of the first
-  int lo, steps;       // first step's number (key / 128), steps (0: no row sees a key)
+  int lo, steps;       // first step's number, steps (0: no row sees a key)
   bool wide;
   __device__ __forceinline__ void request(const PaArgs& a) {
     q0 = a.cu_q[r], m = a.cu_q[r + 1] - q0;
@@ -105,16 +129,15 @@ struct PaUnit {
   static __device__ __forceinline__ int first_step(const PaArgs& a, int p) {
     return a.s.window > 0 && p >= 0 ? max(p - a.s.window + 1, 0) / pa::kKeys : 0;
   }
-  // some row of positions pa .. pb does not see some key of step j
-  static __device__ __forceinline__ bool masked(const PaArgs& a, int j, int pa, int pb) {
-    return j * pa::kKeys + pa::kKeys - 1 > pa || (a.s.window > 0 && pb >= 0 && j * pa::kKeys < pb - a.s.window + 1);
+  // steps [x, y) in which rows of positions f .. l all see every key
+  __device__ __forceinline__ void seen(const PaArgs& a, int f, int l, int& x, int& y) const {
+    x = a.s.window > 0 && l >= 0 ? (int)(((int64_t)max(l - a.s.window + 1, 0) + pa::kKeys - 1) / pa::kKeys) - lo : 0;
+    y = f >= 0 ? (int)(((int64_t)f + 1) / pa::kKeys) - lo : 0;
   }
-  // steps [x, y) of those from ua to ub in which tile t of a wide unit has keys
-  __device__ __forceinline__ void range(const PaArgs& a, int t, int ua, int ub, int& x, int& y) const {
-    const int f = p0 + t * a.T, l = p0 + (t ? tc : a.T) - 1;
+  // steps [x, y) of those from ua to ub in which a tile of positions f .. l has keys
+  __device__ __forceinline__ void range(const PaArgs& a, int f, int l, int ua, int ub, int& x, int& y) const {
     x = max(ua, first_step(a, f) - lo);
-    y = l < 0 ? x : min(ub, l / pa::kKeys + 1 - lo);
-    y = max(x, y);
+    y = l < 0 ? x : max(x, min(ub, l / pa::kKeys + 1 - lo));
   }
 };
 
@@ -149,20 +172,45 @@ struct PaWalk : PaUnit {
     ub = r == end.r && h == end.h && i == end.i ? end.step : max(1, steps);
     return true;
   }
-  __device__ __forceinline__ bool whole() const { return ua == 0 && ub == max(1, steps); }
-  __device__ __forceinline__ int part_slot() const { return 2 * blockIdx.x + (ua == 0); }
+  __device__ __forceinline__ void describe(const PaArgs& a, PaDesc& d) const {
+    d.n = steps ? ub - ua : 0;
+    d.wide = wide, d.tc = tc;
+    d.h = h, d.k0 = k0, d.lo = lo;
+    d.tok = q0 + tok, d.p0 = p0, d.ua = ua;
+    d.part = ua == 0 && ub == max(1, steps) ? -1 : 2 * (int)blockIdx.x + (ua == 0);
+    seen(a, p0, p0 + tc - 1, d.m0, d.m1);
+    for (int t = 0; t < 2; t++) {
+      const int f = p0 + (wide ? t * a.T : 0), l = p0 + (wide && t == 0 ? a.T : tc) - 1;
+      seen(a, f, l, d.g0[t], d.g1[t]);
+      if (wide) {
+        range(a, f, l, ua, ub, d.x[t], d.y[t]);
+      } else {
+        d.x[t] = ua + t;
+        d.y[t] = ub;
+      }
+    }
+  }
 };
 
-// 128 consecutive fp32 columns of this thread's TMEM lane, waited for.
-__device__ __forceinline__ void pa_tmem_ld(uint32_t taddr, float (&v)[128]) {
-  uint32_t r[128];
+// 64 consecutive 32-bit columns of this thread's TMEM lane: asked for, and waited for
+// (the registers are tied to the wait, so that no use moves above it).
+__device__ __forceinline__ void pa_tmem_ld(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n\ttcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]), "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]), "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(taddr)
       : "memory");
-#pragma unroll
-  for (int i = 0; i < 128; i++) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void pa_wait_ld(uint32_t (&r)[64]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]), "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]), "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]), "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]), "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
+               :
+               : "memory");
+}
+__device__ __forceinline__ float pa_max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
 template <int N>
 __device__ __forceinline__ void pa_tmem_st(uint32_t taddr, const uint32_t (&r)[N]);
@@ -216,38 +264,92 @@ __device__ __forceinline__ void pa_wait(uint32_t bar, uint32_t parity, volatile 
 // What a softmax thread keeps of its row over a unit.
 struct PaRow {
   float ref, l;  // reference (base 2), sum of 2^(score - ref)
-  int done;      // steps
+  bool done;     // the group had steps
 };
+
+// 64 scores of a row: cap and slope, and -inf for the keys that it does not see (kb:
+// first key; see0 .. see1: the keys it sees).
+template <bool BIAS>
+__device__ __forceinline__ void pa_scores(const PaArgs& a, float (&x)[64], int kb, int see0, int see1, bool masked, float slope) {
+  if (BIAS) {
+    kv4_cap(a.s, x);
+    if (a.s.slopes) {
+      const float far = (float)(kb - see1);  // the row stands at see1
+#pragma unroll
+      for (int c = 0; c < 64; c++) x[c] = fmaf(slope, far + c, x[c]);
+    }
+  }
+  if (masked) {
+    // sixteens of which every row of the warp sees all are passed over
+    const int a0 = see0 - kb, a1 = see1 - kb;
+    const int w0 = __reduce_max_sync(0xffffffffu, a0), w1 = __reduce_min_sync(0xffffffffu, a1);
+#pragma unroll
+    for (int c0 = 0; c0 < 64; c0 += 16) {
+      if (w0 <= c0 && w1 >= c0 + 15) continue;
+#pragma unroll
+      for (int c = c0; c < c0 + 16; c++)
+        if (c < a0 || c > a1) x[c] = -INFINITY;
+    }
+  }
+}
+__device__ __forceinline__ float pa_max(const float (&x)[64]) {
+  float t4[4];
+#pragma unroll
+  for (int e = 0; e < 4; e++) t4[e] = pa_max3(x[e], x[e + 4], x[e + 8]);
+#pragma unroll
+  for (int c = 12; c < 60; c += 8) {
+#pragma unroll
+    for (int e = 0; e < 4; e++) t4[e] = pa_max3(t4[e], x[c + e], x[c + 4 + e]);
+  }
+  return fmaxf(pa_max3(t4[0], x[60], x[61]), fmaxf(pa_max3(t4[1], x[62], x[63]), fmaxf(t4[2], t4[3])));
+}
+// 64 weights 2^(x f + off) of a row as bf16 pairs into TMEM; their sum.
+__device__ __forceinline__ float pa_weights(const float (&x)[64], float f, float off, uint32_t taddr) {
+  const uint64_t ff = f2pack(f, f), oo = f2pack(off, off);
+  uint64_t l2[2] = {0, 0};
+#pragma unroll
+  for (int c0 = 0; c0 < 64; c0 += 32) {
+    uint32_t p[16];
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      float p0, p1;
+      f2unpack(f2fma(f2pack(x[c0 + c], x[c0 + c + 1]), ff, oo), p0, p1);
+      p0 = ex2(p0);
+      p1 = ex2(p1);
+      l2[c >> 1 & 1] = f2add(l2[c >> 1 & 1], f2pack(p0, p1));
+      p[c / 2] = pa_bf16x2(p0, p1);
+    }
+    pa_tmem_st(taddr + c0 / 2, p);
+  }
+  float l0, l1;
+  f2unpack(f2add(l2[0], l2[1]), l0, l1);
+  return l0 + l1;
+}
 
 // One step: scores from TMEM, P back in two halves, said by half(0) and half(1).  kb:
 // first key; see0 .. see1: the keys that the row sees; masked: some row of the tile
-// does not see some key.
+// does not see some key.  The first half's weights are taken with the reference as it
+// is while the maximum is found, and again in the rare step where that grew past it.
 template <int D, bool BIAS, typename Half>
 __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, uint32_t to, int kb, int see0, int see1,
                                         bool masked, float f, float slope, Half half) {
-  float x[128];
-  pa_tmem_ld(ts, x);
-  if (BIAS) {
-    kv4_cap(a.s, x);
-    const float far = (float)(kb - see1);  // the row stands at see1
-#pragma unroll
-    for (int c = 0; c < 128; c++) x[c] = fmaf(slope, far + c, x[c]);
+  uint32_t r0[64], r1[64];
+  pa_tmem_ld(ts, r0);
+  pa_tmem_ld(ts + 64, r1);
+  pa_wait_ld(r0);
+  pa_wait_ld(r1);
+  float (&x0)[64] = reinterpret_cast<float (&)[64]>(r0);
+  float (&x1)[64] = reinterpret_cast<float (&)[64]>(r1);
+  if (BIAS || masked) {
+    pa_scores<BIAS>(a, x0, kb, see0, see1, masked, slope);
+    pa_scores<BIAS>(a, x1, kb + 64, see0, see1, masked, slope);
   }
-  if (masked) {
-    const int a0 = see0 - kb, a1 = see1 - kb;
-#pragma unroll
-    for (int c = 0; c < 128; c++)
-      if (c < a0 || c > a1) x[c] = -INFINITY;
+  if (!w.done) {  // the unit's first step
+    w.ref = fmaxf(pa_max(x0), pa_max(x1)) * f;
+    if (!(w.ref > -INFINITY)) w.ref = -INFINITY;  // NaN too
   }
-  float t4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-  for (int c = 4; c < 124; c += 8) {
-#pragma unroll
-    for (int e = 0; e < 4; e++) t4[e] = fmaxf(t4[e], fmaxf(x[c + e], x[c + 4 + e]));
-  }
-#pragma unroll
-  for (int e = 0; e < 4; e++) t4[e] = fmaxf(t4[e], x[124 + e]);
-  const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f;
+  float l = pa_weights(x0, f, w.ref == -INFINITY ? 0.f : -w.ref, ts);
+  const float top = fmaxf(pa_max(x0), pa_max(x1)) * f;
   const bool grows = top > w.ref + pa::kLag || (w.ref == -INFINITY && top > w.ref);
   if (__any_sync(0xffffffffu, grows)) {
     const float al = grows ? ex2(w.ref - top) : 1.f;
@@ -264,40 +366,28 @@ __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, 
         pa_tmem_st(to + c, y);
       }
     }
+    l = pa_weights(x0, f, w.ref == -INFINITY ? 0.f : -w.ref, ts);
   }
-  const float off = w.ref == -INFINITY ? 0.f : -w.ref;
-  const uint64_t ff = f2pack(f, f), oo = f2pack(off, off);
-  uint64_t l2[2] = {0, 0};
-#pragma unroll
-  for (int c0 = 0; c0 < 128; c0 += 32) {
-    uint32_t p[16];
-#pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      float p0, p1;
-      f2unpack(f2fma(f2pack(x[c0 + c], x[c0 + c + 1]), ff, oo), p0, p1);
-      p0 = ex2(p0);
-      p1 = ex2(p1);
-      l2[c >> 1 & 1] = f2add(l2[c >> 1 & 1], f2pack(p0, p1));
-      p[c / 2] = pa_bf16x2(p0, p1);
-    }
-    pa_tmem_st(ts + c0 / 2, p);
-    if (c0 % 64 == 32) {
-      pa_wait_st();
-      half(c0 / 64);
-    }
-  }
-  float l0, l1;
-  f2unpack(f2add(l2[0], l2[1]), l0, l1);
-  w.l += l0 + l1;
-  w.done++;
+  w.l += l;
+  pa_wait_st();
+  half(0);
+  w.l += pa_weights(x1, f, w.ref == -INFINITY ? 0.f : -w.ref, ts + 32);
+  pa_wait_st();
+  half(1);
+  w.done = true;
 }
 
 template <int D, bool BIAS>
 __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_constant__ PaArgs a) {
   using S = PaShape<D>;
-  extern __shared__ uint8_t smem_pa[];
-  uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_pa) + 1023) & ~uintptr_t(1023));
-  uint64_t* const q_full = reinterpret_cast<uint64_t*>(sm + S::off_bar);
+  extern __shared__ __align__(1024) uint8_t sm[];  // the only shared memory, so that it begins on a swizzle's boundary
+  if (smem_u32(sm) & 1023) {
+    set_status(a.status, SD_ERR_CUDA);
+    return;
+  }
+  uint64_t* const u_full = reinterpret_cast<uint64_t*>(sm + S::off_bar);  // [kNU] unit described
+  uint64_t* const u_empty = u_full + pa::kNU;      // [kNU] unit done (8 softmax warps, 2 products', 1 looking at V)
+  uint64_t* const q_full = u_empty + pa::kNU;
   uint64_t* const q_empty = q_full + 1;            // products with Q done (2 commits), exchange done (8 warps)
   uint64_t* const k_full = q_empty + 1;            // [kNK]
   uint64_t* const k_empty = k_full + pa::kNK;      // [kNK] products done (2)
@@ -308,19 +398,16 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
   uint64_t* const p_full = s_full + 2;             // [t][half] weights written (4 warps)
   uint64_t* const o_full = p_full + 4;             // [t] a unit's last product done (commit)
   uint64_t* const o_empty = o_full + 2;            // [t] outputs read (4 warps)
-  float2* const s_ml = reinterpret_cast<float2*>(sm + S::off_ml);
-  float* const s_x = reinterpret_cast<float*>(sm + S::off_x);
-  __shared__ int s_abort, s_turn;  // s_turn: 1 while a group's products are being issued
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_bad[8];  // [unit with steps, mod 8]
+  PaCtl& ctl = *reinterpret_cast<PaCtl*>(sm + S::off_ctl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch();
 
   if (warp == pa::kMma) {
-    tmem_alloc(&s_tmem, 512);
+    tmem_alloc(&ctl.tmem, 512);
     tmem_relinquish();
   }
   if (tid == 0) {
+    for (int i = 0; i < pa::kNU; i++) mbar_init(&u_full[i], 1), mbar_init(&u_empty[i], 11);
     mbar_init(q_full, 1), mbar_init(q_empty, 10);
     for (int i = 0; i < pa::kNK; i++) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 2);
     for (int i = 0; i < pa::kNV; i++) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 3), mbar_init(&v_ok[i], 1);
@@ -328,70 +415,73 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
       mbar_init(&s_full[t], 1), mbar_init(&o_full[t], 1), mbar_init(&o_empty[t], 4);
       mbar_init(&p_full[2 * t], 4), mbar_init(&p_full[2 * t + 1], 4);
     }
-    s_abort = 0;
-    s_turn = 0;
+    ctl.abort = ctl.turn = 0;
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tm = s_tmem;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { pa_wait(smem_u32(bar), parity & 1, &s_abort); };
+  const uint32_t tm = ctl.tmem;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { pa_wait(smem_u32(bar), parity & 1, &ctl.abort); };
   // One group's products at a time: those of both, interleaved, would end together,
   // and the softmax of both would run together, with the tensor cores idle.
   auto turn = [&]() {
     const uint64_t t0 = globaltimer();
 #pragma unroll 1
-    while (atomicCAS(&s_turn, 0, 1) != 0) {
-      if (*(volatile int*)&s_abort) return;
-      if (globaltimer() - t0 > kWaitLimitNs) *(volatile int*)&s_abort = 1;
+    while (atomicCAS(&ctl.turn, 0, 1) != 0) {
+      if (*(volatile int*)&ctl.abort) return;
+      if (globaltimer() - t0 > kWaitLimitNs) *(volatile int*)&ctl.abort = 1;
     }
   };
-  PaWalk w(a);
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(72));
     if (warp == pa::kLoad) {
-      uint32_t nk = 0, nv = 0, units = 0;
-      while (w.next(a)) {
-        if (w.steps == 0) continue;  // no row sees a key: the softmax warps write the rows
-        const int n = w.ub - w.ua;
-        auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, int step) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(full, S::kStep);
+      if (elect_one()) {
+        PaWalk w(a);
+        uint32_t nk = 0, nv = 0, units = 0;
+#pragma unroll 1
+        for (uint32_t i = 0;; i++) {
+          const bool more = w.next(a);
+          PaDesc& d = ctl.unit[i % pa::kNU];
+          wait(&u_empty[i % pa::kNU], (i / pa::kNU & 1) ^ 1);
+          if (more) w.describe(a, d);
+          else d.n = -1;
+          mbar_arrive(&u_full[i % pa::kNU]);
+          if (!more) break;
+          if (w.steps == 0) continue;  // no row sees a key: the softmax warps write the rows
+          const int n = w.ub - w.ua, key0 = w.k0 + (w.lo + w.ua) * pa::kKeys;
+          auto load_k = [&](int u) {
+            const uint32_t st = nk % pa::kNK;
+            wait(&k_empty[st], (nk / pa::kNK & 1) ^ 1);
+            mbar_arrive_expect_tx(&k_full[st], S::kStep);
 #pragma unroll
-            for (int d = 0; d < D; d += 64) tma3d_g2s(dst + d * 256, map, d, w.h, w.k0 + (w.lo + step) * pa::kKeys, full);
-          }
-          __syncwarp();
-        };
-        auto load_k = [&](int step) {
-          const uint32_t st = nk % pa::kNK;
-          wait(&k_empty[st], (nk / pa::kNK & 1) ^ 1);
-          load(sm + S::off_k + st * S::kStep, &a.kmap, &k_full[st], step);
-          nk++;
-        };
-        auto load_v = [&](int step) {
-          const uint32_t st = nv % pa::kNV;
-          wait(&v_empty[st], (nv / pa::kNV & 1) ^ 1);
-          load(sm + S::off_v + st * S::kStep, &a.vmap, &v_full[st], step);
-          nv++;
-        };
-        load_k(w.ua);
-        wait(q_empty, (units & 1) ^ 1);
-        if (lane == 0) {
+            for (int c = 0; c < D; c += 64)
+              tma3d_g2s(sm + S::off_k + st * S::kStep + c * 256, &a.kmap, c, w.h, key0 + u * pa::kKeys, &k_full[st]);
+            nk++;
+          };
+          load_k(0);
+          wait(q_empty, (units & 1) ^ 1);
           const int tiles = w.wide ? 2 : 1;
           mbar_arrive_expect_tx(q_full, tiles * (D / 64) * 128 * a.G * a.T);
           for (int t = 0; t < tiles; t++)
-            for (int d = 0; d < D; d += 64)
-              tma3d_g2s(sm + t * S::kTile + d * 256, &a.qmap, d, w.h * a.G, w.q0 + w.tok + t * a.T, q_full);
+            for (int c = 0; c < D; c += 64)
+              tma3d_g2s(sm + t * S::kTile + c * 256, &a.qmap, c, w.h * a.G, w.q0 + w.tok + t * a.T, q_full);
+#pragma unroll 1
+          for (int u = 0; u < n; u++) {
+            if (u + 1 < n) load_k(u + 1);
+            const uint32_t st = nv % pa::kNV;
+            wait(&v_empty[st], (nv / pa::kNV & 1) ^ 1);
+            mbar_arrive_expect_tx(&v_full[st], S::kStep);
+#pragma unroll
+            for (int c = 0; c < D; c += 64)
+              tma3d_g2s(sm + S::off_v + st * S::kStep + c * 256, &a.vmap, c, w.h, key0 + u * pa::kKeys, &v_full[st]);
+            nv++;
+          }
+          units++;
         }
-        __syncwarp();
-        for (int u = w.ua; u < w.ua + n; u++) {
-          if (u + 1 < w.ua + n) load_k(u + 1);
-          load_v(u);
-        }
-        units++;
       }
+      __syncwarp();
     } else if (warp < pa::kLoad) {
       if (elect_one()) {  // one lane throughout
         const int t = warp - pa::kMma;
@@ -400,25 +490,30 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
         const uint64_t kd = sdesc_sw128(smem_u32(sm + S::off_k)), vd = pa_sdesc_v(smem_u32(sm + S::off_v));
         const uint32_t ts = tm + t * 128, to = tm + 256 + t * 128;
         uint32_t nk = 0, nv = 0, units = 0, pp = 0, po = 1;  // stages taken, units; parities of p_full and o_empty
-        while (w.next(a)) {
-          if (w.steps == 0) continue;
-          const int n = w.ub - w.ua, p1 = w.p0 + w.tc - 1, j0 = w.lo + w.ua;
-          // the group's steps: x, x + by, ... below y
-          int x = t, y = n, by = 2;
-          if (w.wide) {
-            w.range(a, t, w.ua, w.ub, x, y);
-            x -= w.ua, y -= w.ua, by = 1;
+#pragma unroll 1
+        for (uint32_t i = 0;; i++) {
+          const PaDesc& d = ctl.unit[i % pa::kNU];
+          wait(&u_full[i % pa::kNU], i / pa::kNU);
+          const int n = d.n;
+          if (n <= 0) {
+            if (n < 0) break;
+            mbar_arrive(&u_empty[i % pa::kNU]);
+            continue;
           }
-          const uint64_t qd = sdesc_sw128(smem_u32(sm + (w.wide ? t : 0) * S::kTile));
+          // the group's steps: x, x + by, ... below y
+          const int by = d.wide ? 1 : 2, x = d.x[t] - d.ua, y = d.y[t] - d.ua, m0 = d.m0 - d.ua, m1 = d.m1 - d.ua;
+          const uint64_t qd = sdesc_sw128(smem_u32(sm + (d.wide ? t : 0) * S::kTile));
           // every step's stages are released by both groups, so that neither gets ahead
           int k = 0, v = 0;  // steps whose K and V are taken
           auto pass_k = [&](int u) {
+#pragma unroll 1
             for (; k < u; k++, nk++) {
               wait(&k_full[nk % pa::kNK], nk / pa::kNK);
               mbar_arrive(&k_empty[nk % pa::kNK]);
             }
           };
           auto pass_v = [&](int u) {
+#pragma unroll 1
             for (; v < u; v++, nv++) {
               wait(&v_full[nv % pa::kNV], nv / pa::kNV);
               mbar_arrive(&v_empty[nv % pa::kNV]);
@@ -436,48 +531,52 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
             k++, nk++;
           };
           wait(q_full, units);
-          if (x < y) {
-            pass_k(x);
-            wait(&k_full[nk % pa::kNK], nk / pa::kNK);
-            tc_fence_after();
-            scores(x);
-          }
+          // Step u's values after its P, and the scores of the next; u = x - by begins.
 #pragma unroll 1
-          for (int u = x; u < y; u += by) {
+          for (int u = x - by; u < y; u += by) {
+            if (x >= y) break;
+            const bool more = u + by < y;
             // K and V are waited for ahead of P, while the softmax runs: between P and the
             // next scores there is nothing but the products
-            pass_v(u);
-            const uint32_t st = nv % pa::kNV;
-            wait(&v_full[st], nv / pa::kNV);
-            if (PaUnit::masked(a, j0 + u, w.p0, p1)) wait(&v_ok[st], nv / pa::kNV);
-            if (u + by < y) {
+            if (more) {
               pass_k(u + by);
               wait(&k_full[nk % pa::kNK], nk / pa::kNK);
             }
-            if (u == x) {
-              wait(&o_empty[t], po);
-              po ^= 1;
-            }
-            const uint64_t vv = vd + st * (S::kStep >> 4);
+            if (u >= x) {
+              pass_v(u);
+              wait(&v_full[nv % pa::kNV], nv / pa::kNV);
+              if (u < m0 || u >= m1) wait(&v_ok[nv % pa::kNV], nv / pa::kNV);
+              if (u == x) {
+                wait(&o_empty[t], po);
+                po ^= 1;
+              }
+              const uint64_t vv = vd + nv % pa::kNV * (S::kStep >> 4);
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-              wait(&p_full[2 * t + h], pp);
-              if (h == 0) turn();
+              for (int h = 0; h < 2; h++) {
+                wait(&p_full[2 * t + h], pp);
+                if (h == 0) turn();
+                tc_fence_after();
+#pragma unroll
+                for (int c = 4 * h; c < 4 * h + 4; c++)
+                  pa_umma_ts(to, ts + 8 * c, vv + c * (2048 >> 4), idv, u > x || c > 0);
+              }
+              pp ^= 1;
+            } else {
+              turn();
               tc_fence_after();
-#pragma unroll
-              for (int c = 4 * h; c < 4 * h + 4; c++)
-                pa_umma_ts(to, ts + 8 * c, vv + c * (2048 >> 4), idv, u > x || c > 0);
             }
-            pp ^= 1;
-            if (u + by < y) scores(u + by);
+            if (more) scores(u + by);
             else umma_commit(&o_full[t]);
-            umma_commit(&v_empty[st]);
-            atomicExch(&s_turn, 0);
-            v++, nv++;
+            if (u >= x) {
+              umma_commit(&v_empty[nv % pa::kNV]);
+              v++, nv++;
+            }
+            atomicExch(&ctl.turn, 0);
           }
           pass_k(n);
           pass_v(n);
           if (x >= y) mbar_arrive(q_empty);
+          mbar_arrive(&u_empty[i % pa::kNU]);
           units++;
         }
       }
@@ -485,39 +584,48 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
     } else {
       // ----------------------------------------------- looking at values --
       uint32_t nv = 0, units = 0;
-      while (w.next(a)) {
-        if (w.steps == 0) continue;
-        const int n = w.ub - w.ua, p1 = w.p0 + w.tc - 1;
-        if (lane == 0) s_bad[units & 7] = 0;
-        for (int x = 0; x < n; x++, nv++) {
-          const uint32_t st = nv % pa::kNV;
-          wait(&v_full[st], nv / pa::kNV);
-          if (PaUnit::masked(a, w.lo + w.ua + x, w.p0, p1)) {
-            uint4* const v = reinterpret_cast<uint4*>(sm + S::off_v + st * S::kStep);
-            uint32_t odd = 0;  // bit 15 of a half word: its exponent is all ones
+#pragma unroll 1
+      for (uint32_t i = 0;; i++) {
+        const PaDesc& d = ctl.unit[i % pa::kNU];
+        wait(&u_full[i % pa::kNU], i / pa::kNU);
+        const int n = d.n, m0 = d.m0 - d.ua, m1 = d.m1 - d.ua;
+        if (n < 0) break;
+        if (n > 0) {
+          if (lane == 0) ctl.bad[units & 7] = 0;
+#pragma unroll 1
+          for (int u = 0; u < n; u++, nv++) {
+            const uint32_t st = nv % pa::kNV;
+            wait(&v_full[st], nv / pa::kNV);
+            if (u < m0 || u >= m1) {
+              uint4* const v = reinterpret_cast<uint4*>(sm + S::off_v + st * S::kStep);
+              uint32_t odd = 0;  // bit 15 of a half word: its exponent is all ones
 #pragma unroll 8
-            for (int i = lane; i < S::kStep / 16; i += 32) {
-              const uint4 u = v[i];
-              odd |= ((u.x & 0x7F807F80u) + 0x00800080u) | ((u.y & 0x7F807F80u) + 0x00800080u) |
-                     ((u.z & 0x7F807F80u) + 0x00800080u) | ((u.w & 0x7F807F80u) + 0x00800080u);
-            }
-            if (__any_sync(0xffffffffu, odd & 0x80008000u)) {
-              if (lane == 0) s_bad[units & 7] = 1;
-              uint32_t* const vw = reinterpret_cast<uint32_t*>(v);
-              for (int i = lane; i < S::kStep / 4; i += 32) {
-                const uint32_t u = vw[i], o = ((u & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-                if (o) vw[i] = u & ~((o >> 15) * 0xFFFFu);
+              for (int e = lane; e < S::kStep / 16; e += 32) {
+                const uint4 z = v[e];
+                odd |= ((z.x & 0x7F807F80u) + 0x00800080u) | ((z.y & 0x7F807F80u) + 0x00800080u) |
+                       ((z.z & 0x7F807F80u) + 0x00800080u) | ((z.w & 0x7F807F80u) + 0x00800080u);
               }
+              if (__any_sync(0xffffffffu, odd & 0x80008000u)) {
+                if (lane == 0) ctl.bad[units & 7] = 1;
+                uint32_t* const vw = reinterpret_cast<uint32_t*>(v);
+#pragma unroll 1
+                for (int e = lane; e < S::kStep / 4; e += 32) {
+                  const uint32_t z = vw[e], o = ((z & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                  if (o) vw[e] = z & ~((o >> 15) * 0xFFFFu);
+                }
+              }
+              fence_async_smem();
             }
-            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&v_ok[st]);
+              mbar_arrive(&v_empty[st]);
+            }
           }
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&v_ok[st]);
-            mbar_arrive(&v_empty[st]);
-          }
+          units++;
         }
-        units++;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&u_empty[i % pa::kNU]);
       }
     }
   } else {
@@ -527,64 +635,53 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t ts = tm + t * 128 + lanes, to = tm + 256 + t * 128 + lanes;
     const float f = BIAS ? 1.f : a.s.scale * kLog2e;
-    const int tok_of = idx / a.G, g = idx - tok_of * a.G;
+    const int tok_of = idx / a.G;
     uint32_t some = 0, sp = 0, op = 0;  // units with steps; parities of s_full and o_full
-    while (w.next(a)) {
-      const int base = w.wide ? t * a.T : 0;           // the tile's first token in the unit
-      const int toks = min(a.T, w.tc - base);          // tokens of the tile, > 0
-      const bool live = tok_of < toks;
-      const int p = w.p0 + base + min(tok_of, toks - 1);
+#pragma unroll 1
+    for (uint32_t i = 0;; i++) {
+      const PaDesc& d = ctl.unit[i % pa::kNU];
+      wait(&u_full[i % pa::kNU], i / pa::kNU);
+      const int n = d.n;
+      if (n < 0) break;
+      // the row's token in the unit; rows past the last token follow it, and are not written
+      const int tok = min((d.wide ? t * a.T : 0) + tok_of, d.tc - 1);
+      const int p = d.p0 + tok;
       const int see0 = a.s.window > 0 && p >= 0 ? max(p - a.s.window + 1, 0) : 0;
-      const int hq = w.h * a.G + min(g, a.G - 1);
-      const float slope = BIAS && a.s.slopes ? a.s.slopes[hq] * kLog2e : 0.f;
-      const int pa0 = w.p0 + base, pb0 = pa0 + toks - 1;
-      PaRow row = {-INFINITY, 0.f, 0};
-      const bool pair = !w.wide && w.steps;            // the groups share the rows
-      int x = 0, y = 0, by = 1;
-      if (w.steps) {
+      const bool pair = !d.wide && n > 0;              // the groups share the rows
+      PaRow row = {-INFINITY, 0.f, false};
+      if (n > 0) {
         wait(q_full, some);  // no group is a unit ahead of the others' barriers
         if (!pair && lane == 0) mbar_arrive(q_empty);  // nothing to exchange
-        if (w.wide) w.range(a, t, w.ua, w.ub, x, y);
-        else x = w.ua + t, y = w.ub, by = 2;
-      }
+        const float slope = BIAS && a.s.slopes ? a.s.slopes[d.h * a.G + idx % a.G] * kLog2e : 0.f;
+        const int by = d.wide ? 1 : 2, y = d.y[t], g0 = d.g0[t], g1 = d.g1[t];
+        int kb = (d.lo + d.x[t]) * pa::kKeys;
 #pragma unroll 1
-      for (int u = x; u < y; u += by) {
-        wait(&s_full[t], sp);
-        sp ^= 1;
-        tc_fence_after();
-        const int j = w.lo + u;
-        pa_step<D, BIAS>(a, row, ts, to, j * pa::kKeys, see0, p, PaUnit::masked(a, j, pa0, pb0), f, slope, [&](int h) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
-        });
+        for (int u = d.x[t]; u < y; u += by, kb += by * pa::kKeys) {
+          wait(&s_full[t], sp);
+          sp ^= 1;
+          tc_fence_after();
+          pa_step<D, BIAS>(a, row, ts, to, kb, see0, p, u < g0 || u >= g1, f, slope, [&](int h) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
+          });
+        }
       }
       bool bad = false;
       if (row.done) {
         wait(&o_full[t], op);
         op ^= 1;
         tc_fence_after();
-        bad = *(volatile int*)&s_bad[some & 7];
+        bad = *(volatile int*)&ctl.bad[some & 7];
       }
-      // infinities and NaNs that were taken out of V and that the row sees
-      auto give_back = [&](float (&o)[16], int c) {
-        for (int u = x; u < y; u += by) {
-          const int j = w.lo + u;
-          if (!PaUnit::masked(a, j, w.p0, w.p0 + w.tc - 1)) continue;
-          for (int key = max(j * pa::kKeys, see0); key <= min(j * pa::kKeys + pa::kKeys - 1, p); key++) {
-            const uint16_t* v = a.v + (int64_t)(w.k0 + key) * a.kv_stride + w.h * D + c;
-#pragma unroll
-            for (int e = 0; e < 16; e++)
-              if ((v[e] & 0x7F80) == 0x7F80) o[e] += bf2f(v[e]);
-          }
-        }
-      };
-      const bool whole = w.whole();
-      const int64_t at = (int64_t)(w.q0 + w.tok + base + tok_of) * a.hq + hq;
-      float* const part = a.part + (int64_t)w.part_slot() * S::kPart;
+      const bool whole = d.part < 0;
+      const bool live = (d.wide ? t * a.T : 0) + tok_of < d.tc && tok_of < a.T;
+      const int64_t at = (int64_t)(d.tok + tok) * a.hq + d.h * a.G + idx % a.G;  // the row of out
+      float* const part = a.part + (int64_t)d.part * S::kPart;
       // (reference, sum) of the row and the outputs' factors
       float M = row.ref, L = row.l, mine = 1.f, other = 0.f;
       if (pair) {
+        float2* const s_ml = reinterpret_cast<float2*>(sm + S::off_ml);
         if (t == 1) s_ml[idx] = make_float2(row.ref, row.l);
         bar_sync(1, 256);
         if (t == 0) {
@@ -597,9 +694,9 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           if (!(ml.y == ml.y)) L = ml.y, other = ml.y;  // a NaN among the other's scores
         }
       }
-      const bool writes = live && (w.wide || t == 0);
-      const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
-      if (writes) {
+      const bool writes = d.wide || t == 0;  // a narrow unit's rows are the first group's to write
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      if (writes && live) {
         if (whole) {
           if (a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
         } else {
@@ -612,9 +709,23 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
         if (row.done) tmem_ld16(to + c, o);
 #pragma unroll
         for (int e = 0; e < 16; e++) o[e] = row.done && row.l != 0.f ? o[e] : 0.f;
-        if (bad && live) give_back(o, c);
+        if (bad && live) {
+          // infinities and NaNs that were taken out of V and that the row sees
+#pragma unroll 1
+          for (int u = d.x[t]; u < d.y[t]; u += d.wide ? 1 : 2) {
+            if (u >= d.m0 && u < d.m1) continue;
+            const int kb = (d.lo + u) * pa::kKeys;
+#pragma unroll 1
+            for (int key = max(kb, see0); key <= min(kb + pa::kKeys - 1, p); key++) {
+              const uint16_t* v = a.v + (int64_t)(d.k0 + key) * a.kv_stride + d.h * D + c;
+#pragma unroll
+              for (int e = 0; e < 16; e++)
+                if ((v[e] & 0x7F80) == 0x7F80) o[e] += bf2f(v[e]);
+            }
+          }
+        }
         if (pair) {
-          float4* const xr = reinterpret_cast<float4*>(s_x + idx * pa::kXs);
+          float4* const xr = reinterpret_cast<float4*>(sm + S::off_x) + idx * (pa::kXs / 4);
           if (t == 1) {
 #pragma unroll
             for (int e = 0; e < 4; e++) xr[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
@@ -632,18 +743,33 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           }
           bar_sync(1, 256);
         }
-        if (writes) {
-          if (whole) {
-            uint4* const dst = reinterpret_cast<uint4*>(a.out + at * D + c);
-#pragma unroll
-            for (int e = 0; e < 2; e++)
-              dst[e] = make_uint4(pa_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), pa_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                  pa_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pa_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-          } else {
+        if (!writes) continue;
+        if (!whole) {
+          if (live) {
             float4* const dst = reinterpret_cast<float4*>(part + (int64_t)(t * 128 + idx) * D + c);
 #pragma unroll
             for (int e = 0; e < 4; e++) __stcg(dst + e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
           }
+          continue;
+        }
+        // 64 dims of the warp's rows through shared memory (pieces of 16 bytes, their
+        // order turned by the row), so that eight lanes write a row's 128 bytes
+        uint4* const so = reinterpret_cast<uint4*>(sm + S::off_o + warp * 4096);
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+          so[lane * 8 + (((c / 8 & 7) + e) ^ (lane & 7))] =
+              make_uint4(pa_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), pa_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                         pa_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pa_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+        if (c % 64 == 48) {
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            const int r = e * 4 + (lane >> 3);
+            const int64_t to_row = __shfl_sync(0xffffffffu, live ? at : (int64_t)-1, r);
+            if (to_row >= 0)
+              *reinterpret_cast<uint4*>(a.out + to_row * D + (c - 48) + (lane & 7) * 8) = so[r * 8 + ((lane & 7) ^ (r & 7))];
+          }
+          __syncwarp();
         }
       }
       tc_fence_before();
@@ -652,8 +778,9 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
       if (lane == 0) {
         if (row.done) mbar_arrive(&o_empty[t]);
         if (pair) mbar_arrive(q_empty);
+        mbar_arrive(&u_empty[i % pa::kNU]);
       }
-      some += w.steps > 0;
+      some += n > 0;
     }
   }
   tc_fence_before();
@@ -661,7 +788,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
   if (warp == pa::kMma) {
     tc_fence_after();
     tmem_dealloc(tm, 512);
-    if (s_abort && lane == 0) set_status(a.status, SD_TIMEOUT_AT(40));
+    if (ctl.abort && lane == 0) set_status(a.status, SD_TIMEOUT_AT(40));
   }
 }
 

@@ -503,32 +503,35 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           // the group's steps: x, x + by, ... below y
           const int by = d.wide ? 1 : 2, x = d.x[t] - d.ua, y = d.y[t] - d.ua, m0 = d.m0 - d.ua, m1 = d.m1 - d.ua;
           const uint64_t qd = sdesc_sw128(smem_u32(sm + (d.wide ? t : 0) * S::kTile));
-          // every step's stages are released by both groups, so that neither gets ahead
-          int k = 0, v = 0;  // steps whose K and V are taken
+          // A wide unit's stages are released by both groups, those that one of them has no use
+          // for too (so it never misses a phase of their barriers); a narrow unit's by the
+          // one group that uses them, in the other's name as well.
+          int k = 0, v = 0;  // a wide unit's steps whose K and V are taken
           auto pass_k = [&](int u) {
 #pragma unroll 1
-            for (; k < u; k++, nk++) {
-              wait(&k_full[nk % pa::kNK], nk / pa::kNK);
-              mbar_arrive(&k_empty[nk % pa::kNK]);
+            for (; by == 1 && k < u; k++) {
+              wait(&k_full[(nk + k) % pa::kNK], (nk + k) / pa::kNK);
+              mbar_arrive(&k_empty[(nk + k) % pa::kNK]);
             }
           };
           auto pass_v = [&](int u) {
 #pragma unroll 1
-            for (; v < u; v++, nv++) {
-              wait(&v_full[nv % pa::kNV], nv / pa::kNV);
-              mbar_arrive(&v_empty[nv % pa::kNV]);
+            for (; by == 1 && v < u; v++) {
+              wait(&v_full[(nv + v) % pa::kNV], (nv + v) / pa::kNV);
+              mbar_arrive(&v_empty[(nv + v) % pa::kNV]);
             }
           };
           auto scores = [&](int u) {  // of step u, whose K is there
-            const uint32_t st = nk % pa::kNK;
+            const uint32_t st = (nk + u) % pa::kNK;
             const uint64_t kk = kd + st * (S::kStep >> 4);
 #pragma unroll
             for (int c = 0; c < D / 16; c++)
               umma_bf16(ts, qd + (c >> 2) * (16384 >> 4) + (c & 3) * 2, kk + (c >> 2) * (16384 >> 4) + (c & 3) * 2, ids, c > 0);
             umma_commit(&s_full[t]);
             umma_commit(&k_empty[st]);
+            if (by == 2) mbar_arrive(&k_empty[st]);
             if (u + by >= y) umma_commit(q_empty);
-            k++, nk++;
+            k++;
           };
           wait(q_full, units);
           // Step u's values after its P, and the scores of the next; u = x - by begins.
@@ -540,17 +543,18 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
             // next scores there is nothing but the products
             if (more) {
               pass_k(u + by);
-              wait(&k_full[nk % pa::kNK], nk / pa::kNK);
+              wait(&k_full[(nk + u + by) % pa::kNK], (nk + u + by) / pa::kNK);
             }
+            const uint32_t vs = (nv + u) % pa::kNV;
             if (u >= x) {
               pass_v(u);
-              wait(&v_full[nv % pa::kNV], nv / pa::kNV);
-              if (u < m0 || u >= m1) wait(&v_ok[nv % pa::kNV], nv / pa::kNV);
+              wait(&v_full[vs], (nv + u) / pa::kNV);
+              if (u < m0 || u >= m1) wait(&v_ok[vs], (nv + u) / pa::kNV);
               if (u == x) {
                 wait(&o_empty[t], po);
                 po ^= 1;
               }
-              const uint64_t vv = vd + nv % pa::kNV * (S::kStep >> 4);
+              const uint64_t vv = vd + vs * (S::kStep >> 4);
 #pragma unroll
               for (int h = 0; h < 2; h++) {
                 wait(&p_full[2 * t + h], pp);
@@ -568,8 +572,9 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
             if (more) scores(u + by);
             else umma_commit(&o_full[t]);
             if (u >= x) {
-              umma_commit(&v_empty[nv % pa::kNV]);
-              v++, nv++;
+              umma_commit(&v_empty[vs]);
+              if (by == 2) mbar_arrive(&v_empty[vs]);
+              v++;
             }
             atomicExch(&ctl.turn, 0);
           }
@@ -577,6 +582,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           pass_v(n);
           if (x >= y) mbar_arrive(q_empty);
           mbar_arrive(&u_empty[i % pa::kNU]);
+          nk += n, nv += n;
           units++;
         }
       }

@@ -10,8 +10,10 @@
 //  * 0..3 and 4..7: softmax, a thread a row: 128 scores from TMEM, maximum,
 //    exponentials, P (bf16) back over its scores; then the outputs.  A wide unit
 //    gives each of the two groups a tile of rows, a narrow one alternate steps of the
-//    same rows, joined through shared memory.  A row's reference may lag its maximum
-//    by 2^8 before O is rescaled in TMEM.
+//    same rows, joined through shared memory.  A step's weights are taken with the
+//    reference that the steps before left, so that its maximum is looked for behind
+//    them, while the products run: P and O may be large, not inaccurate, and O is
+//    rescaled in TMEM only when the maximum has grown by 2^8.
 //  * 8, 9: the products of one group each: S = Q K^T and O += P V, those of one group
 //    while the other is in its softmax.  TMEM: [S 128][S 128][O D][O D].
 //  * 10: walks the CTA's units, says what each is (PaDesc), and loads Q, K and V by TMA.
@@ -38,6 +40,7 @@ constexpr int kMaxCta = 160;
 constexpr int kNK = 2, kNV = 2;  // stages of K and of V
 constexpr int kNU = 4;           // units being described
 constexpr float kLag = 8.f;
+constexpr float kMost = 0x1p60f;  // of a row's weights in half a step
 constexpr int kXs = 20;          // floats of a row being exchanged (16 used)
 }  // namespace pa
 
@@ -264,7 +267,9 @@ __device__ __forceinline__ void pa_wait(uint32_t bar, uint32_t parity, volatile 
 // What a softmax thread keeps of its row over a unit.
 struct PaRow {
   float ref, l;  // reference (base 2), sum of 2^(score - ref)
+  float top;     // the greatest score
   bool done;     // the group had steps
+  bool live;     // the lane has a row
 };
 
 // 64 scores of a row: cap and slope, and -inf for the keys that it does not see (kb:
@@ -326,54 +331,75 @@ __device__ __forceinline__ float pa_weights(const float (&x)[64], float f, float
   return l0 + l1;
 }
 
+// A greater reference for the rows that ask for one, O (where it holds anything) and
+// the sum with it.
+template <int D>
+__device__ __forceinline__ void pa_grow(PaRow& w, uint32_t to, float top, bool held) {
+  const bool grows = top > w.ref + pa::kLag;
+  const float al = grows ? ex2(w.ref - top) : 1.f;
+  if (grows) w.ref = top;
+  w.l *= al;
+  if (held) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+      float o[16];
+      tmem_ld16(to + c, o);
+      uint32_t y[16];
+#pragma unroll
+      for (int k = 0; k < 16; k++) y[k] = __float_as_uint(o[k] * al);
+      pa_tmem_st(to + c, y);
+    }
+  }
+}
+
 // One step: scores from TMEM, P back in two halves, said by half(0) and half(1).  kb:
 // first key; see0 .. see1: the keys that the row sees; masked: some row of the tile
-// does not see some key.  The first half's weights are taken with the reference as it
-// is while the maximum is found, and again in the rare step where that grew past it.
-template <int D, bool BIAS, typename Half>
+// does not see some key; first(): waits for the product of the first half.  O is at
+// rest until half(0): its last product's commit came before these scores'.
+template <int D, bool BIAS, typename Half, typename First>
 __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, uint32_t to, int kb, int see0, int see1,
-                                        bool masked, float f, float slope, Half half) {
+                                        bool masked, float f, float slope, Half half, First first) {
   uint32_t r0[64], r1[64];
-  pa_tmem_ld(ts, r0);
-  pa_tmem_ld(ts + 64, r1);
-  pa_wait_ld(r0);
-  pa_wait_ld(r1);
   float (&x0)[64] = reinterpret_cast<float (&)[64]>(r0);
   float (&x1)[64] = reinterpret_cast<float (&)[64]>(r1);
+  pa_tmem_ld(ts, r0);
+  pa_wait_ld(r0);
+  pa_tmem_ld(ts + 64, r1);
   if (BIAS || masked) {
+    pa_wait_ld(r1);
     pa_scores<BIAS>(a, x0, kb, see0, see1, masked, slope);
     pa_scores<BIAS>(a, x1, kb + 64, see0, see1, masked, slope);
   }
-  if (!w.done) {  // the unit's first step
-    w.ref = fmaxf(pa_max(x0), pa_max(x1)) * f;
-    if (!(w.ref > -INFINITY)) w.ref = -INFINITY;  // NaN too
+  auto off = [&]() { return w.ref == -INFINITY ? 0.f : -w.ref; };
+  // the first keys that a row sees give its reference; the steps before may have left
+  // a greater one
+  if (__any_sync(0xffffffffu, w.live && (w.ref == -INFINITY || w.top > w.ref + pa::kLag))) {
+    pa_wait_ld(r1);
+    if (w.ref == -INFINITY) w.ref = fmaxf(fmaxf(pa_max(x0), pa_max(x1)) * f, -INFINITY);  // no NaN
+    pa_grow<D>(w, to, w.top, w.done);
   }
-  float l = pa_weights(x0, f, w.ref == -INFINITY ? 0.f : -w.ref, ts);
-  const float top = fmaxf(pa_max(x0), pa_max(x1)) * f;
-  const bool grows = top > w.ref + pa::kLag || (w.ref == -INFINITY && top > w.ref);
-  if (__any_sync(0xffffffffu, grows)) {
-    const float al = grows ? ex2(w.ref - top) : 1.f;
-    if (grows) w.ref = top;
-    w.l *= al;
-    if (w.done) {  // the product before is done: its commit came before these scores'
-#pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
-        float o[16];
-        tmem_ld16(to + c, o);
-        uint32_t y[16];
-#pragma unroll
-        for (int k = 0; k < 16; k++) y[k] = __float_as_uint(o[k] * al);
-        pa_tmem_st(to + c, y);
-      }
-    }
-    l = pa_weights(x0, f, w.ref == -INFINITY ? 0.f : -w.ref, ts);
+  float l = pa_weights(x0, f, off(), ts);
+  auto far = [&]() { return w.live && !(l < pa::kMost) && w.l == w.l; };  // past the reference, or the first NaN
+  if (__any_sync(0xffffffffu, far())) {
+    w.top = fmaxf(w.top, pa_max(x0) * f);
+    pa_grow<D>(w, to, w.top, w.done);
+    l = pa_weights(x0, f, off(), ts);
   }
   w.l += l;
   pa_wait_st();
   half(0);
-  w.l += pa_weights(x1, f, w.ref == -INFINITY ? 0.f : -w.ref, ts + 32);
+  pa_wait_ld(r1);
+  l = pa_weights(x1, f, off(), ts + 32);
+  if (__any_sync(0xffffffffu, far())) {
+    w.top = fmaxf(w.top, pa_max(x1) * f);
+    first();
+    pa_grow<D>(w, to, w.top, true);
+    l = pa_weights(x1, f, off(), ts + 32);
+  }
+  w.l += l;
   pa_wait_st();
   half(1);
+  w.top = fmaxf(w.top, fmaxf(pa_max(x0), pa_max(x1)) * f);
   w.done = true;
 }
 
@@ -396,7 +422,8 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
   uint64_t* const v_ok = v_empty + pa::kNV;        // [kNV] looked at
   uint64_t* const s_full = v_ok + pa::kNV;         // [t] scores ready, the products before them done (commit)
   uint64_t* const p_full = s_full + 2;             // [t][half] weights written (4 warps)
-  uint64_t* const o_full = p_full + 4;             // [t] a unit's last product done (commit)
+  uint64_t* const h_full = p_full + 4;             // [t] the product of P's first half done (commit)
+  uint64_t* const o_full = h_full + 2;             // [t] a unit's last product done (commit)
   uint64_t* const o_empty = o_full + 2;            // [t] outputs read (4 warps)
   PaCtl& ctl = *reinterpret_cast<PaCtl*>(sm + S::off_ctl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -412,7 +439,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
     for (int i = 0; i < pa::kNK; i++) mbar_init(&k_full[i], 1), mbar_init(&k_empty[i], 2);
     for (int i = 0; i < pa::kNV; i++) mbar_init(&v_full[i], 1), mbar_init(&v_empty[i], 3), mbar_init(&v_ok[i], 1);
     for (int t = 0; t < 2; t++) {
-      mbar_init(&s_full[t], 1), mbar_init(&o_full[t], 1), mbar_init(&o_empty[t], 4);
+      mbar_init(&s_full[t], 1), mbar_init(&h_full[t], 1), mbar_init(&o_full[t], 1), mbar_init(&o_empty[t], 4);
       mbar_init(&p_full[2 * t], 4), mbar_init(&p_full[2 * t + 1], 4);
     }
     ctl.abort = ctl.turn = 0;
@@ -563,6 +590,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
 #pragma unroll
                 for (int c = 4 * h; c < 4 * h + 4; c++)
                   pa_umma_ts(to, ts + 8 * c, vv + c * (2048 >> 4), idv, u > x || c > 0);
+                if (h == 0) umma_commit(&h_full[t]);
               }
               pp ^= 1;
             } else {
@@ -642,7 +670,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
     const uint32_t ts = tm + t * 128 + lanes, to = tm + 256 + t * 128 + lanes;
     const float f = BIAS ? 1.f : a.s.scale * kLog2e;
     const int tok_of = idx / a.G;
-    uint32_t some = 0, sp = 0, op = 0;  // units with steps; parities of s_full and o_full
+    uint32_t some = 0, sp = 0, hp = 0, op = 0;  // units with steps; parities of s_full, h_full and o_full
 #pragma unroll 1
     for (uint32_t i = 0;; i++) {
       const PaDesc& d = ctl.unit[i % pa::kNU];
@@ -654,7 +682,8 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
       const int p = d.p0 + tok;
       const int see0 = a.s.window > 0 && p >= 0 ? max(p - a.s.window + 1, 0) : 0;
       const bool pair = !d.wide && n > 0;              // the groups share the rows
-      PaRow row = {-INFINITY, 0.f, false};
+      const bool live = (d.wide ? t * a.T : 0) + tok_of < d.tc && tok_of < a.T;
+      PaRow row = {-INFINITY, 0.f, -INFINITY, false, live};
       if (n > 0) {
         wait(q_full, some);  // no group is a unit ahead of the others' barriers
         if (!pair && lane == 0) mbar_arrive(q_empty);  // nothing to exchange
@@ -670,7 +699,11 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
+          }, [&]() {
+            wait(&h_full[t], hp);
+            tc_fence_after();
           });
+          hp ^= 1;
         }
       }
       bool bad = false;
@@ -681,7 +714,6 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
         bad = *(volatile int*)&ctl.bad[some & 7];
       }
       const bool whole = d.part < 0;
-      const bool live = (d.wide ? t * a.T : 0) + tok_of < d.tc && tok_of < a.T;
       const int64_t at = (int64_t)(d.tok + tok) * a.hq + d.h * a.G + idx % a.G;  // the row of out
       float* const part = a.part + (int64_t)d.part * S::kPart;
       // (reference, sum) of the row and the outputs' factors
@@ -709,73 +741,91 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           __stcg(reinterpret_cast<float2*>(part + 256 * D) + t * 128 + idx, make_float2(M, L));
         }
       }
-#pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
-        float o[16];
-        if (row.done) tmem_ld16(to + c, o);
+      // What a row's 64 dims from c on come to goes out through shared memory (pieces of
+      // 16 bytes, their order turned by the row), so that eight lanes write a row's 128
+      // bytes: a lane a row took 4000 cycles a unit.
+      uint4* const so = reinterpret_cast<uint4*>(sm + S::off_o + warp * 4096);
+      auto put = [&](int piece, const float* o) {
+        so[lane * 8 + (piece ^ (lane & 7))] = make_uint4(pa_bf16x2(o[0] * inv, o[1] * inv), pa_bf16x2(o[2] * inv, o[3] * inv),
+                                                         pa_bf16x2(o[4] * inv, o[5] * inv), pa_bf16x2(o[6] * inv, o[7] * inv));
+      };
+      auto write = [&](int c) {
+        __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 16; e++) o[e] = row.done && row.l != 0.f ? o[e] : 0.f;
-        if (bad && live) {
-          // infinities and NaNs that were taken out of V and that the row sees
+        for (int e = 0; e < 8; e++) {
+          const int r = e * 4 + (lane >> 3), to_row = __shfl_sync(0xffffffffu, live ? (int)at : -1, r);
+          if (to_row >= 0)
+            *reinterpret_cast<uint4*>(a.out + (int64_t)to_row * D + c + (lane & 7) * 8) = so[r * 8 + ((lane & 7) ^ (r & 7))];
+        }
+        __syncwarp();
+      };
+      const bool some_sum = row.done && row.l != 0.f;
+      if (whole && !pair && row.done && !bad) {
 #pragma unroll 1
-          for (int u = d.x[t]; u < d.y[t]; u += d.wide ? 1 : 2) {
-            if (u >= d.m0 && u < d.m1) continue;
-            const int kb = (d.lo + u) * pa::kKeys;
-#pragma unroll 1
-            for (int key = max(kb, see0); key <= min(kb + pa::kKeys - 1, p); key++) {
-              const uint16_t* v = a.v + (int64_t)(d.k0 + key) * a.kv_stride + d.h * D + c;
+        for (int c = 0; c < D; c += 64) {
+          uint32_t r[64];
+          pa_tmem_ld(to + c, r);
+          pa_wait_ld(r);
+          float (&o)[64] = reinterpret_cast<float (&)[64]>(r);
+          if (!some_sum) {
 #pragma unroll
-              for (int e = 0; e < 16; e++)
-                if ((v[e] & 0x7F80) == 0x7F80) o[e] += bf2f(v[e]);
+            for (int e = 0; e < 64; e++) o[e] = 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; e++) put(e, o + 8 * e);
+          write(c);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          if (row.done) tmem_ld16(to + c, o);
+#pragma unroll
+          for (int e = 0; e < 16; e++) o[e] = some_sum ? o[e] : 0.f;
+          if (bad && live) {
+            // infinities and NaNs that were taken out of V and that the row sees
+#pragma unroll 1
+            for (int u = d.x[t]; u < d.y[t]; u += d.wide ? 1 : 2) {
+              if (u >= d.m0 && u < d.m1) continue;
+              const int kb = (d.lo + u) * pa::kKeys;
+#pragma unroll 1
+              for (int key = max(kb, see0); key <= min(kb + pa::kKeys - 1, p); key++) {
+                const uint16_t* v = a.v + (int64_t)(d.k0 + key) * a.kv_stride + d.h * D + c;
+#pragma unroll
+                for (int e = 0; e < 16; e++)
+                  if ((v[e] & 0x7F80) == 0x7F80) o[e] += bf2f(v[e]);
+              }
             }
           }
-        }
-        if (pair) {
-          float4* const xr = reinterpret_cast<float4*>(sm + S::off_x) + idx * (pa::kXs / 4);
-          if (t == 1) {
+          if (pair) {
+            float4* const xr = reinterpret_cast<float4*>(sm + S::off_x) + idx * (pa::kXs / 4);
+            if (t == 1) {
 #pragma unroll
-            for (int e = 0; e < 4; e++) xr[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          }
-          bar_sync(1, 256);
-          if (t == 0) {
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-              const float4 v = xr[e];
-              o[4 * e] = fmaf(other, v.x, mine * o[4 * e]);
-              o[4 * e + 1] = fmaf(other, v.y, mine * o[4 * e + 1]);
-              o[4 * e + 2] = fmaf(other, v.z, mine * o[4 * e + 2]);
-              o[4 * e + 3] = fmaf(other, v.w, mine * o[4 * e + 3]);
+              for (int e = 0; e < 4; e++) xr[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
+            bar_sync(1, 256);
+            if (t == 0) {
+#pragma unroll
+              for (int e = 0; e < 4; e++) {
+                const float4 v = xr[e];
+                o[4 * e] = fmaf(other, v.x, mine * o[4 * e]);
+                o[4 * e + 1] = fmaf(other, v.y, mine * o[4 * e + 1]);
+                o[4 * e + 2] = fmaf(other, v.z, mine * o[4 * e + 2]);
+                o[4 * e + 3] = fmaf(other, v.w, mine * o[4 * e + 3]);
+              }
+            }
+            bar_sync(1, 256);
           }
-          bar_sync(1, 256);
-        }
-        if (!writes) continue;
-        if (!whole) {
-          if (live) {
+          if (!writes) continue;
+          if (whole) {
+            put(c / 8 & 7, o);
+            put((c / 8 & 7) + 1, o + 8);
+            if (c % 64 == 48) write(c - 48);
+          } else if (live) {
             float4* const dst = reinterpret_cast<float4*>(part + (int64_t)(t * 128 + idx) * D + c);
 #pragma unroll
             for (int e = 0; e < 4; e++) __stcg(dst + e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
           }
-          continue;
-        }
-        // 64 dims of the warp's rows through shared memory (pieces of 16 bytes, their
-        // order turned by the row), so that eight lanes write a row's 128 bytes
-        uint4* const so = reinterpret_cast<uint4*>(sm + S::off_o + warp * 4096);
-#pragma unroll
-        for (int e = 0; e < 2; e++)
-          so[lane * 8 + (((c / 8 & 7) + e) ^ (lane & 7))] =
-              make_uint4(pa_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), pa_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                         pa_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pa_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-        if (c % 64 == 48) {
-          __syncwarp();
-#pragma unroll
-          for (int e = 0; e < 8; e++) {
-            const int r = e * 4 + (lane >> 3);
-            const int64_t to_row = __shfl_sync(0xffffffffu, live ? at : (int64_t)-1, r);
-            if (to_row >= 0)
-              *reinterpret_cast<uint4*>(a.out + to_row * D + (c - 48) + (lane & 7) * 8) = so[r * 8 + ((lane & 7) ^ (r & 7))];
-          }
-          __syncwarp();
         }
       }
       tc_fence_before();

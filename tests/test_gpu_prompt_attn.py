@@ -123,6 +123,23 @@ def test_large_and_small_scores(M):
     same(out, lse, m, keys, (q.float() * 1e-30).bfloat16(), k, v)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", [(3,), (63,), (64,), (127,), (128, 200), (10, 70, 140, 260, 330), (399,)])
+def test_scores_that_leap(M, at, d):
+    """A key whose score passes all before it by hundreds, in either half of a step of 128 keys."""
+    m, keys = [400, 30], [400, 300]
+    q, k, v = inputs(m, keys, 4, 2, d, 8)
+    q = (q.abs() + 0.5).bfloat16()
+    size = 40.0
+    for j in at:
+        for first in (0, 400):
+            if j < (400 if first == 0 else 300):
+                k[first + j] = size
+        size *= 1.5
+    out, lse = run(M, m, keys, q, k, v)
+    same(out, lse, m, keys, q, k, v)
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("d", [64, 128])
 def test_bad_values_only_reach_the_rows_that_see_them(M, bad, d):

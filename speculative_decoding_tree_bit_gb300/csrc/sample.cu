@@ -4,9 +4,9 @@
 // sampled token depends on follows from how often each key occurs, and its weight
 // is computed once a key.  One cluster takes a row: each CTA counts its slice in
 // shared memory (16-bit counters, so at most 65528 tokens a CTA), the CTAs sum the
-// binades (128 keys) that occur, one warp walks the binades' counts and sums down to
-// the cuts and the token's key, and the CTA that holds the key's occurrence looks it
-// up in its slice.
+// binades (128 keys) that occur and their weights into the first one's memory, one warp
+// there walks their running sums down to the cuts and the token's key, and the CTA
+// that holds the key's occurrence looks it up in its slice, which is still in registers.
 //
 // Weights are whole numbers, 2^44 exp((logit - most) / temperature), from pairs
 // of fp32 values good to about 2^-46, and their sums are 64-bit whole numbers (2^44
@@ -24,6 +24,8 @@ constexpr int kSlice = 65528;          // tokens of a CTA, at most: whole vector
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = (1 << 19) - 128;
 constexpr int kBlocks = 513;           // binades of either sign, and zero's once more
+constexpr int kTable = 48;             // binades whose keys' counts and weights are kept
+constexpr int kHeld = 5;               // vectors of 8 tokens that a thread keeps
 constexpr int kOne = 44;               // weights are multiples of 2^-kOne
 constexpr float kLog2e = 1.4426950408889634f;
 }  // namespace sp
@@ -48,38 +50,37 @@ __device__ const Exp2Table kExp2 = Exp2Table();
 
 // What a row's weights go by.
 struct RowScale {
-  float most;      // greatest logit
-  float ch, cl;    // log2(e) / temperature as a pair; 0 where greedy
-  float zh, zl;    // log2(min_p) as a pair; -inf: none
+  float most;    // greatest logit
+  float ch, cl;  // log2(e) / temperature as a pair; 0 where greedy
 };
 
-// log2 of the weight of logit l as a pair (p + e).
-__device__ __forceinline__ void log2_weight(float l, const RowScale& r, float& p, float& e) {
+// A weight 2^n (h + l), h + l in [1, 2].
+struct Weight {
+  float h, l;
+  int n;
+  // in multiples of 2^-44: h has 24 bits, a whole number times 2^-24 at least
+  __device__ __forceinline__ uint64_t whole() const {
+    const uint64_t v = ((uint64_t)(uint32_t)(h * 16777216.f) << (sp::kOne - 24)) + (int64_t)(int)rintf(l * 0x1p44f);
+    return n == 0 ? v : n < -sp::kOne - 2 ? 0 : (v + (1ull << (-n - 1))) >> -n;
+  }
+  __device__ __forceinline__ float value() const { return h * __int_as_float((127 + max(n, -126)) << 23); }
+  __device__ __forceinline__ bool at_least(float p) const {
+    const float q = p * __int_as_float((127 + min(-n, 126)) << 23);
+    return __fadd_rn(__fadd_rn(h, -q), l) >= 0.f;
+  }
+};
+
+// The weight of logit l <= most; n = -200 where it is below 2^-120.
+__device__ __forceinline__ Weight weight_of(float l, const RowScale& r, const float2* s_exp2) {
+  // l - most = s + d, log2 of the weight p + e
   const float s = __fadd_rn(l, -r.most), b = __fadd_rn(s, -l);
-  const float d = __fadd_rn(__fadd_rn(l, -__fadd_rn(s, -b)), __fadd_rn(-r.most, -b));  // l - most = s + d
-  p = __fmul_rn(s, r.ch);
-  e = __fmaf_rn(s, r.ch, -p);
+  const float d = __fadd_rn(__fadd_rn(l, -__fadd_rn(s, -b)), __fadd_rn(-r.most, -b));
+  float p = __fmul_rn(s, r.ch);
+  float e = __fmaf_rn(s, r.ch, -p);
   e = __fmaf_rn(s, r.cl, e);
   e = __fmaf_rn(d, r.ch, e);
-}
-
-// Whether the weight of logit l is at least min_p.
-__device__ __forceinline__ bool at_least(float l, const RowScale& r) {
-  float p, e;
-  log2_weight(l, r, p, e);
-  return l >= r.most || __fadd_rn(__fadd_rn(p, -r.zh), __fadd_rn(e, -r.zl)) >= 0.f;
-}
-
-// The weight of logit l <= most in multiples of 2^-44, and as fp32.
-__device__ __forceinline__ uint64_t weight_of(float l, const RowScale& r, const float2* s_exp2, float* w32 = nullptr) {
-  if (l == r.most) {  // beside +inf too
-    if (w32) *w32 = 1.f;
-    return 1ull << sp::kOne;
-  }
-  float p, e;
-  log2_weight(l, r, p, e);
-  if (w32) *w32 = 0.f;
-  if (!(p > -60.f)) return 0;
+  const bool one = l >= r.most, none = !one && !(p > -120.f);  // beside +inf too
+  if (one || none) p = e = 0.f;
   // p + e = m / 32 + f + e, |f| <= 1 / 64
   const float mf = rintf(p * 32.f);
   const int m = (int)mf;
@@ -99,19 +100,16 @@ __device__ __forceinline__ uint64_t weight_of(float l, const RowScale& r, const 
   const float se = __fadd_rn(h, -__fadd_rn(sh, -th));
   const float sl = __fadd_rn(se, __fadd_rn(c3, __fmaf_rn(0.5f, sqe, tl)));
   // times 2^(j / 32)
-  const int n = m >> 5;
   const float2 t = s_exp2[m & 31];
   const float ph = __fmul_rn(t.x, sh);
   float pl = __fmaf_rn(t.x, sh, -ph);
   pl = __fmaf_rn(t.x, sl, pl);
   pl = __fmaf_rn(t.y, sh, pl);
-  const float rh = __fadd_rn(t.x, ph);
-  const float re = __fadd_rn(ph, -__fadd_rn(rh, -t.x));
-  const float rl = __fadd_rn(__fadd_rn(re, pl), t.y);
-  if (w32) *w32 = rh * __int_as_float((127 + n) << 23);
-  // rh has 24 bits: a whole number times 2^-24 at least
-  const uint64_t v = ((uint64_t)(uint32_t)(rh * 16777216.f) << (sp::kOne - 24)) + (int64_t)(int)rintf(rl * 0x1p44f);
-  return n == 0 ? v : n < -sp::kOne - 2 ? 0 : (v + (1ull << (-n - 1))) >> -n;
+  Weight w;
+  w.h = __fadd_rn(t.x, ph);
+  w.l = __fadd_rn(__fadd_rn(__fadd_rn(ph, -__fadd_rn(w.h, -t.x)), pl), t.y);
+  w.n = none ? -200 : m >> 5;
+  return w;
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -126,6 +124,12 @@ __device__ __forceinline__ uint2 ld_cluster_u2(uint32_t addr) {
 }
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void st_cluster_2u64(uint32_t addr, uint64_t a, uint64_t b) {
+  asm volatile("st.shared::cluster.v2.u64 [%0], {%1, %2};" ::"r"(addr), "l"(a), "l"(b) : "memory");
 }
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
@@ -144,16 +148,16 @@ struct SampleArgs {
 
 struct SampleShared {
   uint32_t bins[32768];           // counters of keys 2 i and 2 i + 1
-  uint64_t mass[sp::kBlocks];     // of the binades that occur, by falling logit (the first CTA's)
-  uint32_t count[sp::kBlocks];
+  uint64_t weight[sp::kTable][128];  // of the first CTA: the row's keys by falling logit, weights
+  uint32_t keys[sp::kTable][128];    // and counts
+  uint64_t mass[sp::kBlocks];     // of the binades that occur, by falling logit: sums of weights, and counts;
+  uint32_t count[sp::kBlocks];    // then running ones
   float2 exp2[32];
   float top[sp::kWarps];
   uint32_t lo[sp::kWarps], hi[sp::kWarps];
   uint32_t span[3];               // of the CTA: greatest logit (fp32 bits), least and greatest magnitude
-  float ch, cl, zh, zl;           // RowScale
   uint32_t key, nth;              // the token's key and which of the CTA's occurrences it is (-1: none here)
-  uint32_t tot[8 * sp::kWarps];   // occurrences a vector round and warp
-  uint32_t at;
+  uint32_t tot[8 * sp::kWarps];   // occurrences a round of vectors and warp
 };
 
 // The binades that occur, by falling logit: those of magnitudes e1 .. e0, zero's
@@ -176,16 +180,31 @@ __device__ __forceinline__ uint32_t key_bits(uint32_t e, bool neg, int j) {
 
 // The counts of a lane's four keys 4 lane .. 4 lane + 3 (falling order) of a
 // binade, over the cluster.
-__device__ __forceinline__ void lane_counts(uint32_t bins, int C, uint32_t e, bool neg, int lane, uint32_t (&c)[4]) {
+template <int C>
+__device__ __forceinline__ void lane_counts(uint32_t bins, uint32_t e, bool neg, int lane, uint32_t (&c)[4]) {
   const uint32_t word = ((neg ? 0x8000u : 0u) | e << 7) / 2 + (neg ? 2 * lane : 62 - 2 * lane);
+  uint2 w[C];
+#pragma unroll
+  for (int k = 0; k < C; k++) w[k] = ld_cluster_u2(cluster_map(bins + 4 * word, k));
   c[0] = c[1] = c[2] = c[3] = 0;
-  for (int k = 0; k < C; k++) {
-    const uint2 w = ld_cluster_u2(cluster_map(bins + 4 * word, k));
-    c[0] += w.x & 0xFFFF, c[1] += w.x >> 16, c[2] += w.y & 0xFFFF, c[3] += w.y >> 16;
-  }
+#pragma unroll
+  for (int k = 0; k < C; k++) c[0] += w[k].x & 0xFFFF, c[1] += w[k].x >> 16, c[2] += w[k].y & 0xFFFF, c[3] += w[k].y >> 16;
   if (!neg) {
     const uint32_t a = c[0], b = c[1];
     c[0] = c[3], c[1] = c[2], c[2] = b, c[3] = a;
+  }
+}
+// Their weights too.
+template <int C>
+__device__ __forceinline__ void lane_keys(uint32_t bins, const Binades& b, int i, const RowScale& rs, const float2* s_exp2, int lane,
+                                          uint32_t (&k)[4], uint64_t (&w)[4]) {
+  bool neg;
+  const uint32_t e = b.exponent(i, neg);
+  lane_counts<C>(bins, e, neg, lane, k);
+#pragma unroll
+  for (int x = 0; x < 4; x++) {
+    const uint64_t v = weight_of(bf2f((uint16_t)key_bits(e, neg, 4 * lane + x)), rs, s_exp2).whole();
+    w[x] = k[x] ? v : 0;  // a key that does not occur may lie above the greatest logit
   }
 }
 
@@ -227,47 +246,58 @@ struct Place {
   uint64_t w;            // the key's weight
 };
 
-// By one warp: the first key at which the running count (or mass) of the row
+struct LaneKeys {
+  uint32_t k[4];
+  uint64_t w[4];
+};
+template <int C>
+__device__ __noinline__ LaneKeys keys_not_kept(uint32_t bins, int e0, int e1, int i, float most, float ch, float cl, const float2* s_exp2) {
+  LaneKeys r;
+  lane_keys<C>(bins, Binades{e0, e1}, i, RowScale{most, ch, cl}, s_exp2, threadIdx.x & 31, r.k, r.w);
+  return r;
+}
+
+// A lane's four keys of binade i, as they were kept.
+template <int C>
+__device__ __forceinline__ void kept_keys(const SampleShared& sh, uint32_t bins, const Binades& b, int i, const RowScale& rs, int lane,
+                                          uint32_t (&k)[4], uint64_t (&w)[4]) {
+  if (i >= sp::kTable) {
+    const LaneKeys r = keys_not_kept<C>(bins, b.e0, b.e1, i, rs.most, rs.ch, rs.cl, sh.exp2);
+#pragma unroll
+    for (int x = 0; x < 4; x++) k[x] = r.k[x], w[x] = r.w[x];
+    return;
+  }
+  const uint4 c = reinterpret_cast<const uint4*>(sh.keys[i])[lane];
+  const ulonglong2 u = reinterpret_cast<const ulonglong2*>(sh.weight[i])[2 * lane], v = reinterpret_cast<const ulonglong2*>(sh.weight[i])[2 * lane + 1];
+  k[0] = c.x, k[1] = c.y, k[2] = c.z, k[3] = c.w;
+  w[0] = u.x, w[1] = u.y, w[2] = v.x, w[3] = v.y;
+}
+
+// By one warp: the first key at which the row's running count (or mass)
 // reaches `goal` (at least goal, or more than it where `past`).  The caller knows
 // that it does.
-template <bool MASS>
-__device__ Place find(const SampleShared& sh, uint32_t bins, int C, const Binades& b, const RowScale& rs, uint64_t goal,
-                      bool past) {
-  const int lane = threadIdx.x & 31, n = b.n(), each = (n + 31) / 32;
-  const int i0 = min(n, lane * each), i1 = min(n, i0 + each);
-  uint64_t c = 0, m = 0;
-  for (int i = i0; i < i1; i++) c += sh.count[i], m += sh.mass[i];
-  uint64_t cb = before_lane(c, lane), mb = before_lane(m, lane);
+template <bool MASS, int C>
+__device__ __forceinline__ Place find(const SampleShared& sh, uint32_t bins, const Binades& b, const RowScale& rs, uint64_t goal,
+                                      bool past) {
+  const int lane = threadIdx.x & 31, n = b.n();
   auto reached = [&](uint64_t x) { return past ? x > goal : x >= goal; };
-  const bool here = reached(MASS ? mb + m : cb + c) && (MASS ? m : c) > 0;
-  const int who = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
   Place p = {};
-  if (lane == who) {
-    int i = i0;
-    for (; i < i1 - 1; i++) {
-      if (sh.count[i] && reached(MASS ? mb + sh.mass[i] : cb + sh.count[i])) break;
-      cb += sh.count[i], mb += sh.mass[i];
+  for (int c = 0; c < n; c += 32) {
+    const uint32_t f = __ballot_sync(0xffffffffu, c + lane < n && reached(MASS ? sh.mass[c + lane] : sh.count[c + lane]));
+    if (f) {
+      p.i = c + __ffs(f) - 1;
+      break;
     }
-    p.i = i;
   }
-  p.i = __shfl_sync(0xffffffffu, p.i, max(who, 0));
-  cb = __shfl_sync(0xffffffffu, cb, max(who, 0));
-  mb = __shfl_sync(0xffffffffu, mb, max(who, 0));
-  bool neg;
-  const uint32_t e = b.exponent(p.i, neg);
-  uint32_t k[4];
-  lane_counts(bins, C, e, neg, lane, k);
-  uint64_t w[4];
-  c = m = 0;
+  uint64_t cb = p.i ? sh.count[p.i - 1] : 0, mb = p.i ? sh.mass[p.i - 1] : 0;
+  uint32_t k[4], c = 0;
+  uint64_t w[4], m = 0;
+  kept_keys<C>(sh, bins, b, p.i, rs, lane, k, w);
 #pragma unroll
-  for (int x = 0; x < 4; x++) {
-    w[x] = k[x] ? weight_of(bf2f((uint16_t)key_bits(e, neg, 4 * lane + x)), rs, sh.exp2) : 0;
-    c += k[x], m += k[x] * w[x];
-  }
+  for (int x = 0; x < 4; x++) c += k[x], m += k[x] * w[x];
   cb += before_lane(c, lane);
   mb += before_lane(m, lane);
-  const bool in = reached(MASS ? mb + m : cb + c) && c > 0;
-  const int at = max(__ffs(__ballot_sync(0xffffffffu, in)) - 1, 0);
+  const int at = max(__ffs(__ballot_sync(0xffffffffu, c > 0 && reached(MASS ? mb + m : cb + c))) - 1, 0);
   int j = 0;
   uint64_t ww = 0;
 #pragma unroll
@@ -293,12 +323,22 @@ __device__ __forceinline__ void tally(SampleShared& sh, uint32_t b, float& top, 
   hi = max(hi, mag);
 }
 
+// Eight tokens from t on, NaN where the row x of V tokens has none.
+__device__ __noinline__ uint4 edge_vector(const uint16_t* x, int t, int V) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 8; k++) {
+    const uint32_t e = t + k >= 0 && t + k < V ? x[t + k] : 0xFFFFu;
+    w[k / 2] = k & 1 ? w[k / 2] | e << 16 : e;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int C>
 __global__ void __launch_bounds__(sp::kThreads, 1) k_sample(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) uint8_t smem_sp[];
   SampleShared& sh = *reinterpret_cast<SampleShared*>(smem_sp);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t C;
-  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(C));
   const int rank = (int)cluster_rank(), row = blockIdx.x / C;
 
   // ---- count the slice: vectors on 16-byte addresses, their ends masked
@@ -308,32 +348,37 @@ __global__ void __launch_bounds__(sp::kThreads, 1) k_sample(const __grid_constan
   const uint4* xv = reinterpret_cast<const uint4*>(x - shift);
   auto token = [&](int v, int k) { return v * 8 + k - shift; };  // of element k of vector v
   auto load = [&](int v, uint32_t (&w)[4]) {
-    if (v >= v1) {
-      w[0] = w[1] = w[2] = w[3] = 0xFFFFFFFFu;  // NaN
-    } else if (token(v, 0) >= 0 && token(v, 7) < a.V) {
-      const uint4 u = xv[v];
-      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; k++) {
-        const int t = token(v, k);
-        const uint32_t e = t >= 0 && t < a.V ? x[t] : 0xFFFFu;
-        w[k / 2] = k & 1 ? w[k / 2] | e << 16 : e;
-      }
+    uint4 u = make_uint4(0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu);  // NaN
+    if (v < v1) {
+      if (token(v, 0) >= 0 && token(v, 7) < a.V) u = xv[v];
+      else u = edge_vector(x, token(v, 0), a.V);
     }
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
   };
-  for (int i = tid; i < 8192; i += sp::kThreads) reinterpret_cast<uint4*>(sh.bins)[i] = make_uint4(0, 0, 0, 0);
-  if (tid < 32) sh.exp2[tid] = make_float2(kExp2.hi[tid], kExp2.lo[tid]);
+  uint32_t held[sp::kHeld][4];  // all of a thread's loads in flight while the counters are cleared
+#pragma unroll
+  for (int i = 0; i < sp::kHeld; i++) load(v0 + i * sp::kThreads + tid, held[i]);
   const float temperature = a.s.temperature_rows ? a.s.temperature_rows[row] : a.s.temperature;
   const float min_p = a.s.min_p_rows ? a.s.min_p_rows[row] : a.s.min_p;
+  const float top_p = a.s.top_p_rows ? a.s.top_p_rows[row] : a.s.top_p;
+  const int top_k = a.s.top_k_rows ? a.s.top_k_rows[row] : a.s.top_k;
+  const float u_row = a.u[row];
+#pragma unroll
+  for (int i = 0; i < 8; i++) reinterpret_cast<uint4*>(sh.bins)[tid + i * sp::kThreads] = make_uint4(0, 0, 0, 0);
+  if (tid < 32) sh.exp2[tid] = make_float2(kExp2.hi[tid], kExp2.lo[tid]);
   __syncthreads();
   float top = -INFINITY;
   uint32_t lo = 0xFFFFFFFFu, hi = 0;
-  for (int v = v0 + tid; v < v1; v += sp::kThreads) {
-    uint32_t w[4];
-    load(v, w);
+  auto tally4 = [&](const uint32_t (&w)[4]) {
 #pragma unroll
     for (int k = 0; k < 4; k++) tally(sh, w[k] & 0xFFFF, top, lo, hi), tally(sh, w[k] >> 16, top, lo, hi);
+  };
+#pragma unroll
+  for (int i = 0; i < sp::kHeld; i++) tally4(held[i]);
+  for (int v = v0 + sp::kHeld * sp::kThreads + tid; v < v1; v += sp::kThreads) {
+    uint32_t w[4];
+    load(v, w);
+    tally4(w);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -348,20 +393,14 @@ __global__ void __launch_bounds__(sp::kThreads, 1) k_sample(const __grid_constan
     lo = __reduce_min_sync(0xffffffffu, sh.lo[lane]);
     hi = __reduce_max_sync(0xffffffffu, sh.hi[lane]);
     if (lane == 0) sh.span[0] = __float_as_uint(top), sh.span[1] = lo, sh.span[2] = hi;
-  } else if (tid == 32) {  // fp64 is slow here: by one thread
-    const double scale = temperature > 0.f ? 1.4426950408889634074 / (double)temperature : 0.0;
-    sh.ch = (float)fmin(scale, 3e38);
-    sh.cl = scale < 3e38 ? (float)(scale - (double)sh.ch) : 0.f;
-    const double z = min_p > 0.f ? log2((double)fminf(min_p, 1.f)) : -1e30;
-    sh.zh = (float)z;
-    sh.zl = (float)(z - (double)sh.zh);
   }
   cluster_sync_all();
 
   // ---- the row's greatest logit and its binades
   const uint32_t bins = smem_u32(sh.bins), span = smem_u32(sh.span);
   top = -INFINITY, lo = 0xFFFFFFFFu, hi = 0;
-  for (int k = 0; k < (int)C; k++) {
+#pragma unroll
+  for (int k = 0; k < C; k++) {
     const uint32_t at = cluster_map(span, k);
     top = fmaxf(top, __uint_as_float(ld_cluster_u32(at)));
     lo = min(lo, ld_cluster_u32(at + 4));
@@ -373,20 +412,30 @@ __global__ void __launch_bounds__(sp::kThreads, 1) k_sample(const __grid_constan
   bn.e0 = min((int)((lo == 0xFFFFFFFFu ? 0u : lo + 1) >> 7), bn.e1);
   RowScale rs;
   rs.most = top;
-  rs.ch = sh.ch, rs.cl = sh.cl, rs.zh = sh.zh, rs.zl = sh.zl;
+  {  // log2(e) / temperature: the quotient and its remainder's
+    constexpr float lh = (float)1.4426950408889634074, ll = (float)(1.4426950408889634074 - (double)lh);
+    const float q = __fdiv_rn(lh, temperature);
+    const bool fine = temperature > 0.f && q < 3e38f;
+    rs.ch = temperature > 0.f ? fminf(q, 3e38f) : 0.f;
+    rs.cl = fine ? __fdiv_rn(__fadd_rn(__fmaf_rn(-q, temperature, lh), ll), temperature) : 0.f;
+  }
 
-  // ---- each binade's count and sum, into the first CTA
+  // ---- each binade's keys, count and sum, into the first CTA
   if (!none) {
     const uint32_t mass0 = cluster_map(smem_u32(sh.mass), 0), count0 = cluster_map(smem_u32(sh.count), 0);
+    const uint32_t keys0 = cluster_map(smem_u32(sh.keys), 0), weight0 = cluster_map(smem_u32(sh.weight), 0);
     for (int i = warp * C + rank; i < bn.n(); i += sp::kWarps * C) {
-      bool neg;
-      const uint32_t e = bn.exponent(i, neg);
       uint32_t c[4], n = 0;
-      uint64_t m = 0;
-      lane_counts(bins, C, e, neg, lane, c);
+      uint64_t w[4], m = 0;
+      lane_keys<C>(bins, bn, i, rs, sh.exp2, lane, c, w);
 #pragma unroll
-      for (int k = 0; k < 4; k++)
-        if (c[k]) n += c[k], m += c[k] * weight_of(bf2f((uint16_t)key_bits(e, neg, 4 * lane + k)), rs, sh.exp2);
+      for (int k = 0; k < 4; k++) n += c[k], m += c[k] * w[k];
+      if (i < sp::kTable) {
+        const uint32_t at = i * 128 + 4 * lane;
+        st_cluster_u4(keys0 + 4 * at, c[0], c[1], c[2], c[3]);
+        st_cluster_2u64(weight0 + 8 * at, w[0], w[1]);
+        st_cluster_2u64(weight0 + 8 * at + 16, w[2], w[3]);
+      }
       n = __reduce_add_sync(0xffffffffu, n);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
@@ -399,84 +448,81 @@ __global__ void __launch_bounds__(sp::kThreads, 1) k_sample(const __grid_constan
   if (rank == 0 && warp == 0) {
     uint32_t key = 0, nth = 0xFFFFFFFFu;
     if (!none) {
-      const int n = bn.n();
-      uint64_t N = 0, W = 0;
-      for (int i = lane; i < n; i += 32) N += sh.count[i], W += sh.mass[i];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        N += __shfl_xor_sync(0xffffffffu, N, o);
-        W += __shfl_xor_sync(0xffffffffu, W, o);
+      // running counts and sums, a run of binades a lane
+      const int n = bn.n(), each = (n + 31) / 32, i0 = min(n, lane * each), i1 = min(n, i0 + each);
+      uint32_t c = 0;
+      uint64_t m = 0;
+      for (int i = i0; i < i1; i++) c += sh.count[i], m += sh.mass[i];
+      uint32_t cb = before_lane(c, lane);
+      uint64_t mb = before_lane(m, lane);
+      for (int i = i0; i < i1; i++) {
+        cb += sh.count[i], mb += sh.mass[i];
+        sh.count[i] = cb, sh.mass[i] = mb;
       }
-      const int top_k = a.s.top_k_rows ? a.s.top_k_rows[row] : a.s.top_k;
-      const float top_p = a.s.top_p_rows ? a.s.top_p_rows[row] : a.s.top_p;
+      __syncwarp();
+      uint64_t N = sh.count[n - 1], W = sh.mass[n - 1];
       const uint64_t K = !(temperature > 0.f) ? 1 : top_k > 0 ? top_k : N;
       if (K < N) {
-        const Place p = find<false>(sh, bins, C, bn, rs, K, false);
+        const Place p = find<false, C>(sh, bins, bn, rs, K, false);
         N = K;
         W = p.mass + (K - p.count) * p.w;
       }
-      if (rs.zh > -1e29f) {
-        // the first binade whose last key is below min_p
+      if (min_p > 0.f) {
+        const float least = fminf(min_p, 1.f);
+        // the first binade whose last key weighs less
         int i = n;
         for (int c = 0; c < n && i == n; c += 32) {
           bool neg = false, below = false;
           if (c + lane < n) {
             const uint32_t e = bn.exponent(c + lane, neg);
-            below = !at_least(bf2f((uint16_t)key_bits(e, neg, 127)), rs);
+            below = !weight_of(bf2f((uint16_t)key_bits(e, neg, 127)), rs, sh.exp2).at_least(least);
           }
           const uint32_t f = __ballot_sync(0xffffffffu, below);
           if (f) i = c + __ffs(f) - 1;
         }
         if (i < n) {
-          uint64_t cb = 0, mb = 0;
-          for (int c = lane; c < i; c += 32) cb += sh.count[c], mb += sh.mass[c];
           bool neg;
           const uint32_t e = bn.exponent(i, neg);
-          uint32_t c[4];
-          lane_counts(bins, C, e, neg, lane, c);
+          uint32_t k[4], cc = 0;
+          uint64_t w[4], mm = 0;
+          kept_keys<C>(sh, bins, bn, i, rs, lane, k, w);
 #pragma unroll
-          for (int k = 0; k < 4; k++) {
-            const float l = bf2f((uint16_t)key_bits(e, neg, 4 * lane + k));
-            if (c[k] && at_least(l, rs)) cb += c[k], mb += c[k] * weight_of(l, rs, sh.exp2);
-          }
+          for (int x = 0; x < 4; x++)
+            if (k[x] && weight_of(bf2f((uint16_t)key_bits(e, neg, 4 * lane + x)), rs, sh.exp2).at_least(least)) cc += k[x], mm += k[x] * w[x];
+          cc = __reduce_add_sync(0xffffffffu, cc) + (i ? sh.count[i - 1] : 0);
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            cb += __shfl_xor_sync(0xffffffffu, cb, o);
-            mb += __shfl_xor_sync(0xffffffffu, mb, o);
-          }
-          if (cb < N) N = cb, W = mb;
+          for (int o = 16; o > 0; o >>= 1) mm += __shfl_xor_sync(0xffffffffu, mm, o);
+          mm += i ? sh.mass[i - 1] : 0;
+          if (cc < N) N = cc, W = mm;
         }
       }
       if (top_p < 1.f) {
         const uint64_t goal = max(share_of(top_p, W, true), (uint64_t)1);
-        const Place p = find<true>(sh, bins, C, bn, rs, goal, false);
+        const Place p = find<true, C>(sh, bins, bn, rs, goal, false);
         const uint64_t r = (goal - p.mass + p.w - 1) / p.w;
         if (p.count + r < N) N = p.count + r, W = p.mass + r * p.w;
       }
-      float u = a.u[row];
-      u = u > 0.f ? fminf(u, 1.f - 0x1p-24f) : 0.f;
+      const float u = u_row > 0.f ? fminf(u_row, 1.f - 0x1p-24f) : 0.f;
       const uint64_t goal = share_of(u, W, false);
-      const Place p = find<true>(sh, bins, C, bn, rs, goal, true);
+      const Place p = find<true, C>(sh, bins, bn, rs, goal, true);
       const uint32_t r = (uint32_t)((goal - p.mass) / p.w);
       bool neg;
       const uint32_t e = bn.exponent(p.i, neg);
       key = key_bits(e, neg, p.j);
       // the CTA that holds occurrence r
       uint32_t mine = 0;
-      if (lane < (int)C) mine = ld_cluster_u32(cluster_map(bins + 4 * (key >> 1), lane)) >> (key & 1 ? 16 : 0) & 0xFFFF;
+      if (lane < C) mine = ld_cluster_u32(cluster_map(bins + 4 * (key >> 1), lane)) >> (key & 1 ? 16 : 0) & 0xFFFF;
       const uint32_t before = before_lane(mine, lane);
-      if (lane < (int)C) {
+      if (lane < C) {
         const uint32_t to = cluster_map(smem_u32(&sh.key), lane);
         st_cluster_u32(to, key);
         st_cluster_u32(to + 4, r >= before && r < before + mine ? r - before : 0xFFFFFFFFu);
       }
       if (lane == 0) {
-        float w32;
-        const uint64_t w = weight_of(bf2f((uint16_t)key), rs, sh.exp2, &w32);
-        if (a.logprob) a.logprob[row] = 0.f - log1pf((float)(W - w) * 0x1p-44f / w32);
+        if (a.logprob) a.logprob[row] = 0.f - log1pf((float)(W - p.w) * 0x1p-44f / weight_of(bf2f((uint16_t)key), rs, sh.exp2).value());
         if (a.kept) a.kept[row] = (int32_t)N;
       }
-    } else if (lane < (int)C) {
+    } else if (lane < C) {
       st_cluster_u32(cluster_map(smem_u32(&sh.nth), lane), nth);
       if (lane == 0) {
         a.tokens[row] = -1;
@@ -490,9 +536,8 @@ __global__ void __launch_bounds__(sp::kThreads, 1) k_sample(const __grid_constan
   // ---- occurrence nth of the key in this slice
   const uint32_t key = sh.key, nth = sh.nth;
   if (nth == 0xFFFFFFFFu) return;
-  auto matches = [&](int v) {
-    uint32_t w[4], f = 0;
-    load(v, w);
+  auto matches4 = [&](const uint32_t (&w)[4]) {
+    uint32_t f = 0;
 #pragma unroll
     for (int k = 0; k < 8; k++) {
       uint32_t b = w[k / 2] >> (k & 1 ? 16 : 0) & 0xFFFF;
@@ -501,8 +546,19 @@ __global__ void __launch_bounds__(sp::kThreads, 1) k_sample(const __grid_constan
     }
     return f;
   };
+  auto matches = [&](int v) {
+    uint32_t w[4];
+    load(v, w);
+    return matches4(w);
+  };
   const int rounds = (v1 - v0 + sp::kThreads - 1) / sp::kThreads;  // at most 8
-  for (int i = 0; i < rounds; i++) {
+#pragma unroll
+  for (int i = 0; i < sp::kHeld; i++) {
+    if (i >= rounds) break;
+    const uint32_t n = __reduce_add_sync(0xffffffffu, __popc(matches4(held[i])));
+    if (lane == 0) sh.tot[i * sp::kWarps + warp] = n;
+  }
+  for (int i = sp::kHeld; i < rounds; i++) {
     const uint32_t n = __reduce_add_sync(0xffffffffu, __popc(matches(v0 + i * sp::kThreads + tid)));
     if (lane == 0) sh.tot[i * sp::kWarps + warp] = n;
   }
@@ -562,10 +618,16 @@ extern "C" int sd_sample(const uint16_t* logits, int64_t row_stride, int32_t row
   // few rows: more CTAs a row while each still has 4096 tokens
   while (C < sp::kMaxCluster && (int64_t)rows * C * 2 <= num_sms() && vocab >= 4096 * 2 * C) C *= 2;
   if ((int64_t)rows * C > 0x7FFFFFFF) return sample_bad(SD_ERR_UNSUPPORTED, "too many rows");
-  static const cudaError_t set = cudaFuncSetAttribute(k_sample, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SampleShared));
+  const void* kerns[4] = {(const void*)k_sample<1>, (const void*)k_sample<2>, (const void*)k_sample<4>, (const void*)k_sample<8>};
+  static const cudaError_t set = [&]() {
+    cudaError_t e = cudaSuccess;
+    for (const void* k : kerns)
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SampleShared));
+    return e;
+  }();
   SD_CK(set);
   const SampleArgs a = {logits, row_stride, rows, vocab, slice(C), s, u, tokens, logprob, kept};
-  SD_CK(launch_cluster(k_sample, dim3((unsigned)(rows * C)), dim3(sp::kThreads), sizeof(SampleShared), (cudaStream_t)stream,
-                       false, C, a));
+  auto kern = C == 1 ? k_sample<1> : C == 2 ? k_sample<2> : C == 4 ? k_sample<4> : k_sample<8>;
+  SD_CK(launch_cluster(kern, dim3((unsigned)(rows * C)), dim3(sp::kThreads), sizeof(SampleShared), (cudaStream_t)stream, false, C, a));
   return SD_OK;
 }

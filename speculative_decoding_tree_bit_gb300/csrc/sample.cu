@@ -2,11 +2,14 @@
 //
 // A bf16 logit is one of 65536 keys, so a row is a histogram: everything a
 // sampled token depends on follows from how often each key occurs, and its weight
-// is computed once a key.  One cluster takes a row: each CTA counts its slice in
-// shared memory (16-bit counters, so at most 65528 tokens a CTA), the CTAs sum the
-// binades (128 keys) that occur and their weights into the first one's memory, one warp
-// there walks their running sums down to the cuts and the token's key, and the CTA
-// that holds the key's occurrence looks it up in its slice, which is still in registers.
+// is computed once a key.  A row's keys are counted in shared memory; of each binade
+// (128 keys) that occurs the count and the sum of weights are taken; one warp walks
+// their running sums down to the cuts and the token's key, and the key's occurrence is
+// looked up in the row.  Two kernels:
+//  * many rows: a CTA a row, counters of the magnitudes 2^-24 .. 2^15 and of zero
+//    (40 KB, two CTAs an SM); a row with others is left to the next kernel;
+//  * few rows: a cluster of up to 8 CTAs a row, 16-bit counters of all 65536 keys (so at
+//    most 65528 tokens a CTA), summed through distributed shared memory.
 //
 // Weights are whole numbers, 2^44 exp((logit - most) / temperature), from pairs
 // of fp32 values good to about 2^-46, and their sums are 64-bit whole numbers (2^44
@@ -27,6 +30,11 @@ constexpr int kBlocks = 513;           // binades of either sign, and zero's onc
 constexpr int kTable = 48;             // binades whose keys' counts and weights are kept
 constexpr int kHeld = 5;               // vectors of 8 tokens that a thread keeps
 constexpr int kOne = 44;               // weights are multiples of 2^-kOne
+constexpr int kRowThreads = 512, kRowWarps = kRowThreads / 32;
+constexpr int kLeast = 127 - 24, kSpan = 39;     // exponents of the row kernel's binades
+constexpr int kRowKeys = kSpan * 128;            // of either sign
+constexpr int kRowBlocks = 2 * kSpan + 1;        // positive ones falling, zero, negative ones
+constexpr int kLater = INT32_MIN;                // token of a row that is left to the next kernel
 constexpr float kLog2e = 1.4426950408889634f;
 }  // namespace sp
 
@@ -246,6 +254,7 @@ struct Place {
   uint64_t w;            // the key's weight
 };
 
+// The row's keys as the cluster's first CTA keeps them.
 struct LaneKeys {
   uint32_t k[4];
   uint64_t w[4];
@@ -256,53 +265,100 @@ __device__ __noinline__ LaneKeys keys_not_kept(uint32_t bins, int e0, int e1, in
   lane_keys<C>(bins, Binades{e0, e1}, i, RowScale{most, ch, cl}, s_exp2, threadIdx.x & 31, r.k, r.w);
   return r;
 }
-
-// A lane's four keys of binade i, as they were kept.
 template <int C>
-__device__ __forceinline__ void kept_keys(const SampleShared& sh, uint32_t bins, const Binades& b, int i, const RowScale& rs, int lane,
-                                          uint32_t (&k)[4], uint64_t (&w)[4]) {
-  if (i >= sp::kTable) {
-    const LaneKeys r = keys_not_kept<C>(bins, b.e0, b.e1, i, rs.most, rs.ch, rs.cl, sh.exp2);
-#pragma unroll
-    for (int x = 0; x < 4; x++) k[x] = r.k[x], w[x] = r.w[x];
-    return;
+struct ClusterKeys {
+  const SampleShared& sh;
+  uint32_t bins;
+  Binades b;
+  const RowScale& rs;
+  __device__ __forceinline__ int n() const { return b.n(); }
+  __device__ __forceinline__ uint32_t bits(int i, int j) const {
+    bool neg;
+    const uint32_t e = b.exponent(i, neg);
+    return key_bits(e, neg, j);
   }
-  const uint4 c = reinterpret_cast<const uint4*>(sh.keys[i])[lane];
-  const ulonglong2 u = reinterpret_cast<const ulonglong2*>(sh.weight[i])[2 * lane], v = reinterpret_cast<const ulonglong2*>(sh.weight[i])[2 * lane + 1];
-  k[0] = c.x, k[1] = c.y, k[2] = c.z, k[3] = c.w;
-  w[0] = u.x, w[1] = u.y, w[2] = v.x, w[3] = v.y;
-}
+  __device__ __forceinline__ void lane_of(int i, int lane, uint32_t (&k)[4], uint64_t (&w)[4]) const {
+    if (i >= sp::kTable) {
+      const LaneKeys r = keys_not_kept<C>(bins, b.e0, b.e1, i, rs.most, rs.ch, rs.cl, sh.exp2);
+#pragma unroll
+      for (int x = 0; x < 4; x++) k[x] = r.k[x], w[x] = r.w[x];
+      return;
+    }
+    const uint4 c = reinterpret_cast<const uint4*>(sh.keys[i])[lane];
+    const ulonglong2 u = reinterpret_cast<const ulonglong2*>(sh.weight[i])[2 * lane],
+                     v = reinterpret_cast<const ulonglong2*>(sh.weight[i])[2 * lane + 1];
+    k[0] = c.x, k[1] = c.y, k[2] = c.z, k[3] = c.w;
+    w[0] = u.x, w[1] = u.y, w[2] = v.x, w[3] = v.y;
+  }
+};
+
+// The row kernel's counters: of positive keys, negative ones, zero.
+struct RowKeys {
+  const uint32_t* bins;
+  const float2* exp2;
+  RowScale rs;
+  __device__ __forceinline__ int n() const { return sp::kRowBlocks; }
+  __device__ __forceinline__ uint32_t bits(int i, int j) const {
+    if (i == sp::kSpan) return 0;
+    const bool neg = i > sp::kSpan;
+    return key_bits(neg ? sp::kLeast + i - sp::kSpan - 1 : sp::kLeast + sp::kSpan - 1 - i, neg, j);
+  }
+  __device__ __forceinline__ void counts(int i, int lane, uint32_t (&k)[4]) const {
+    if (i == sp::kSpan) {
+      k[0] = lane == 0 ? bins[2 * sp::kRowKeys] : 0;
+      k[1] = k[2] = k[3] = 0;
+    } else if (i > sp::kSpan) {
+      const uint4 u = *reinterpret_cast<const uint4*>(bins + sp::kRowKeys + (i - sp::kSpan - 1) * 128 + 4 * lane);
+      k[0] = u.x, k[1] = u.y, k[2] = u.z, k[3] = u.w;
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4*>(bins + (sp::kSpan - 1 - i) * 128 + 124 - 4 * lane);
+      k[0] = u.w, k[1] = u.z, k[2] = u.y, k[3] = u.x;
+    }
+  }
+  __device__ __forceinline__ void lane_of(int i, int lane, uint32_t (&k)[4], uint64_t (&w)[4]) const {
+    counts(i, lane, k);
+#pragma unroll
+    for (int x = 0; x < 4; x++) {
+      const uint64_t v = weight_of(bf2f((uint16_t)bits(i, 4 * lane + x)), rs, exp2).whole();
+      w[x] = k[x] ? v : 0;
+    }
+  }
+};
 
 // By one warp: the first key at which the row's running count (or mass)
 // reaches `goal` (at least goal, or more than it where `past`).  The caller knows
 // that it does.
-template <bool MASS, int C>
-__device__ __forceinline__ Place find(const SampleShared& sh, uint32_t bins, const Binades& b, const RowScale& rs, uint64_t goal,
-                                      bool past) {
-  const int lane = threadIdx.x & 31, n = b.n();
-  auto reached = [&](uint64_t x) { return past ? x > goal : x >= goal; };
+template <typename Keys>
+__device__ __forceinline__ Place find(const Keys& keys, const uint32_t* count, const uint64_t* mass, uint64_t goal, bool by_mass, bool past) {
+  const int lane = threadIdx.x & 31, n = keys.n();
+  auto reached = [&](uint64_t c, uint64_t m) {
+    const uint64_t x = by_mass ? m : c;
+    return past ? x > goal : x >= goal;
+  };
   Place p = {};
+#pragma unroll 1
   for (int c = 0; c < n; c += 32) {
-    const uint32_t f = __ballot_sync(0xffffffffu, c + lane < n && reached(MASS ? sh.mass[c + lane] : sh.count[c + lane]));
+    const int i = min(c + lane, n - 1);
+    const uint32_t f = __ballot_sync(0xffffffffu, reached(count[i], mass[i]));
     if (f) {
-      p.i = c + __ffs(f) - 1;
+      p.i = min(c + __ffs(f) - 1, n - 1);
       break;
     }
   }
-  uint64_t cb = p.i ? sh.count[p.i - 1] : 0, mb = p.i ? sh.mass[p.i - 1] : 0;
+  uint64_t cb = p.i ? count[p.i - 1] : 0, mb = p.i ? mass[p.i - 1] : 0;
   uint32_t k[4], c = 0;
   uint64_t w[4], m = 0;
-  kept_keys<C>(sh, bins, b, p.i, rs, lane, k, w);
+  keys.lane_of(p.i, lane, k, w);
 #pragma unroll
   for (int x = 0; x < 4; x++) c += k[x], m += k[x] * w[x];
   cb += before_lane(c, lane);
   mb += before_lane(m, lane);
-  const int at = max(__ffs(__ballot_sync(0xffffffffu, c > 0 && reached(MASS ? mb + m : cb + c))) - 1, 0);
+  const int at = max(__ffs(__ballot_sync(0xffffffffu, c > 0 && reached(cb + c, mb + m))) - 1, 0);
   int j = 0;
   uint64_t ww = 0;
 #pragma unroll
   for (int x = 0; x < 4; x++) {  // the first of the lane's keys that reaches it
-    const bool before = j == x && !(k[x] && reached(MASS ? mb + k[x] * w[x] : cb + k[x]));
+    const bool before = j == x && !(k[x] && reached(cb + k[x], mb + k[x] * w[x]));
     if (before && x < 3) cb += k[x], mb += k[x] * w[x], j = x + 1;
     if (j == x) ww = w[x];
   }
@@ -311,6 +367,116 @@ __device__ __forceinline__ Place find(const SampleShared& sh, uint32_t bins, con
   p.mass = __shfl_sync(0xffffffffu, mb, at);
   p.w = __shfl_sync(0xffffffffu, ww, at);
   return p;
+}
+
+struct RowSettings {
+  float temperature, top_p, min_p, u;
+  int top_k;
+  __device__ __forceinline__ RowSettings(const sd_sampling& s, const float* us, int row) {
+    temperature = s.temperature_rows ? s.temperature_rows[row] : s.temperature;
+    top_p = s.top_p_rows ? s.top_p_rows[row] : s.top_p;
+    min_p = s.min_p_rows ? s.min_p_rows[row] : s.min_p;
+    top_k = s.top_k_rows ? s.top_k_rows[row] : s.top_k;
+    u = us[row];
+  }
+  __device__ __forceinline__ RowScale scale(float most) const {  // log2(e) / temperature: the quotient and its remainder's
+    constexpr float lh = (float)1.4426950408889634074, ll = (float)(1.4426950408889634074 - (double)lh);
+    const float q = __fdiv_rn(lh, temperature);
+    RowScale r = {most, temperature > 0.f ? fminf(q, 3e38f) : 0.f, 0.f};
+    if (temperature > 0.f && q < 3e38f) r.cl = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, temperature, lh), ll), temperature);
+    return r;
+  }
+};
+
+struct Chosen {
+  uint32_t key, r;   // the token's key and which of its occurrences it is
+  uint64_t w, W;     // its weight, the sum of what is kept
+  uint32_t N;        // how many are kept
+};
+
+// By one warp: the cuts and the token's key, from the binades' counts and sums
+// (which become running ones).
+template <typename Keys>
+__device__ __forceinline__ Chosen walk(const Keys& keys, uint32_t* count, uint64_t* mass, const RowScale& rs, const float2* exp2,
+                                       const RowSettings& set) {
+  const int lane = threadIdx.x & 31;
+  // a run of binades a lane
+  const int n = keys.n(), each = (n + 31) / 32, i0 = min(n, lane * each), i1 = min(n, i0 + each);
+  uint32_t c = 0;
+  uint64_t m = 0;
+#pragma unroll 1
+  for (int i = i0; i < i1; i++) c += count[i], m += mass[i];
+  uint32_t cb = before_lane(c, lane);
+  uint64_t mb = before_lane(m, lane);
+#pragma unroll 1
+  for (int i = i0; i < i1; i++) {
+    cb += count[i], mb += mass[i];
+    count[i] = cb, mass[i] = mb;
+  }
+  __syncwarp();
+  uint64_t N = count[n - 1], W = mass[n - 1];
+  const uint64_t K = !(set.temperature > 0.f) ? 1 : set.top_k > 0 ? set.top_k : N;
+  Place p = {};
+  // top-k, min-p, top-p, the token: one search after the other
+#pragma unroll 1
+  for (int stage = 0; stage < 4; stage++) {
+    if (stage == 1) {
+      if (!(set.min_p > 0.f)) continue;
+      const float least = fminf(set.min_p, 1.f);
+      // the first binade whose last key weighs less
+      int i = n;
+#pragma unroll 1
+      for (int b = 0; b < n && i == n; b += 32) {
+        const bool below = b + lane < n && !weight_of(bf2f((uint16_t)keys.bits(min(b + lane, n - 1), 127)), rs, exp2).at_least(least);
+        const uint32_t f = __ballot_sync(0xffffffffu, below);
+        if (f) i = b + __ffs(f) - 1;
+      }
+      if (i == n) continue;
+      uint32_t k[4], cc = 0;
+      uint64_t w[4], mm = 0;
+      keys.lane_of(i, lane, k, w);
+#pragma unroll
+      for (int x = 0; x < 4; x++)
+        if (weight_of(bf2f((uint16_t)keys.bits(i, 4 * lane + x)), rs, exp2).at_least(least)) cc += k[x], mm += k[x] * w[x];
+      cc = __reduce_add_sync(0xffffffffu, cc) + (i ? count[i - 1] : 0);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mm += __shfl_xor_sync(0xffffffffu, mm, o);
+      mm += i ? mass[i - 1] : 0;
+      if (cc < N) N = cc, W = mm;
+      continue;
+    }
+    if ((stage == 0 && K >= N) || (stage == 2 && !(set.top_p < 1.f))) continue;
+    const float u = set.u > 0.f ? fminf(set.u, 1.f - 0x1p-24f) : 0.f;
+    uint64_t goal = K;
+    if (stage) {
+      goal = share_of(stage == 2 ? set.top_p : u, W, stage == 2);
+      if (stage == 2 && goal == 0) goal = 1;
+    }
+    p = find(keys, count, mass, goal, stage > 0, stage == 3);
+    if (stage == 0) {
+      N = K;
+      W = p.mass + (K - p.count) * p.w;
+      continue;
+    }
+    const uint64_t r = (goal - p.mass + (stage == 2 ? p.w - 1 : 0)) / p.w;
+    if (stage == 2) {
+      if (p.count + r < N) N = p.count + r, W = p.mass + r * p.w;
+    } else {
+      p.count = r;
+    }
+  }
+  return {keys.bits(p.i, p.j), (uint32_t)p.count, p.w, W, (uint32_t)N};
+}
+
+// The token's logarithm and the count (by one thread).
+__device__ __forceinline__ void write_row(const SampleArgs& a, int row, const Chosen& ch, const RowScale& rs, const float2* exp2) {
+  if (a.logprob) a.logprob[row] = 0.f - log1pf((float)(ch.W - ch.w) * 0x1p-44f / weight_of(bf2f((uint16_t)ch.key), rs, exp2).value());
+  if (a.kept) a.kept[row] = (int32_t)ch.N;
+}
+__device__ __forceinline__ void write_empty(const SampleArgs& a, int row) {
+  a.tokens[row] = -1;
+  if (a.logprob) a.logprob[row] = -INFINITY;
+  if (a.kept) a.kept[row] = 0;
 }
 
 __device__ __forceinline__ void tally(SampleShared& sh, uint32_t b, float& top, uint32_t& lo, uint32_t& hi) {
@@ -334,258 +500,323 @@ __device__ __noinline__ uint4 edge_vector(const uint16_t* x, int t, int V) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A row as vectors of eight tokens on 16-byte addresses, its ends masked.
+struct RowView {
+  const uint16_t* x;
+  const uint4* xv;
+  int shift, V;  // tokens before x in its vector
+  __device__ __forceinline__ RowView(const SampleArgs& a, int row) : x(a.logits + (int64_t)row * a.stride), V(a.V) {
+    shift = (int)((reinterpret_cast<uintptr_t>(x) >> 1) & 7);
+    xv = reinterpret_cast<const uint4*>(x - shift);
+  }
+  __device__ __forceinline__ int vectors() const { return (V + shift + 7) / 8; }
+  __device__ __forceinline__ int token(int v, int k) const { return v * 8 + k - shift; }
+  // vector v, NaN at and past `end`
+  __device__ __forceinline__ void load(int v, int end, uint32_t (&w)[4]) const {
+    uint4 u = make_uint4(0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu);
+    if (v < end) {
+      if (token(v, 0) >= 0 && token(v, 7) < V) u = xv[v];
+      else u = edge_vector(x, token(v, 0), V);
+    }
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  }
+};
+// The elements of a vector that are the key, as bits.
+__device__ __forceinline__ uint32_t matches(const uint32_t (&w)[4], uint32_t key) {
+  uint32_t f = 0;
+#pragma unroll
+  for (int k = 0; k < 8; k++) {
+    uint32_t b = w[k / 2] >> (k & 1 ? 16 : 0) & 0xFFFF;
+    if (b == 0x8000u) b = 0;
+    f |= (uint32_t)(b == key) << k;
+  }
+  return f;
+}
+// By one warp: the token of occurrence nth of the key in vectors v0 .. end of a row, of
+// which round i's by warp w are tot[i * WARPS + w].
+template <int WARPS>
+__device__ __forceinline__ void look_up(const SampleArgs& a, int row, const RowView& rv, int v0, int end, int rounds, const uint32_t* tot,
+                                        uint32_t key, uint32_t nth) {
+  const int lane = threadIdx.x & 31, n = rounds * WARPS;
+  uint32_t run = 0;
+#pragma unroll 1
+  for (int c = 0; c < n; c += 32) {
+    const uint32_t m = c + lane < n ? tot[c + lane] : 0, b = run + before_lane(m, lane);
+    const uint32_t f = __ballot_sync(0xffffffffu, nth >= b && nth < b + m);
+    run = __shfl_sync(0xffffffffu, b + m, 31);
+    if (!f) continue;
+    const int where = c + __ffs(f) - 1;
+    const uint32_t left = nth - __shfl_sync(0xffffffffu, b, __ffs(f) - 1);
+    const int v = v0 + (where / WARPS * WARPS + where % WARPS) * 32 + lane;
+    uint32_t w[4];
+    rv.load(v, end, w);
+    uint32_t g = matches(w, key);
+    const uint32_t h = __popc(g), before = before_lane(h, lane);
+    if (left >= before && left < before + h) {
+      for (uint32_t k = before; k < left; k++) g &= g - 1;
+      a.tokens[row] = rv.token(v, __ffs(g) - 1);
+    }
+    return;
+  }
+}
+
+// A cluster a row.  `only`: the rows that the row kernel left.
 template <int C>
-__global__ void __launch_bounds__(sp::kThreads, 1) k_sample(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(sp::kThreads, 1) k_sample(const __grid_constant__ SampleArgs a, bool only) {
   extern __shared__ __align__(16) uint8_t smem_sp[];
   SampleShared& sh = *reinterpret_cast<SampleShared*>(smem_sp);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = (int)cluster_rank(), row = blockIdx.x / C;
-
-  // ---- count the slice: vectors on 16-byte addresses, their ends masked
-  const uint16_t* x = a.logits + (int64_t)row * a.stride;
-  const int shift = (int)((reinterpret_cast<uintptr_t>(x) >> 1) & 7);  // tokens before x in its vector
-  const int v0 = rank * (a.slice / 8), v1 = min((a.V + shift + 7) / 8, v0 + a.slice / 8);
-  const uint4* xv = reinterpret_cast<const uint4*>(x - shift);
-  auto token = [&](int v, int k) { return v * 8 + k - shift; };  // of element k of vector v
-  auto load = [&](int v, uint32_t (&w)[4]) {
-    uint4 u = make_uint4(0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu);  // NaN
-    if (v < v1) {
-      if (token(v, 0) >= 0 && token(v, 7) < a.V) u = xv[v];
-      else u = edge_vector(x, token(v, 0), a.V);
+  const int rank = (int)cluster_rank();
+  if (only) pdl_wait();
+#pragma unroll 1
+  for (int row = blockIdx.x / C; row < a.rows; row += gridDim.x / C) {
+    if (only && a.tokens[row] != sp::kLater) continue;
+    __syncthreads();
+    // ---- count the slice
+    const RowView rv(a, row);
+    const int v0 = rank * (a.slice / 8), v1 = min(rv.vectors(), v0 + a.slice / 8);
+    uint32_t held[sp::kHeld][4];  // all of a thread's loads in flight while the counters are cleared
+#pragma unroll
+    for (int i = 0; i < sp::kHeld; i++) rv.load(v0 + i * sp::kThreads + tid, v1, held[i]);
+    const RowSettings set(a.s, a.u, row);
+#pragma unroll
+    for (int i = 0; i < 8; i++) reinterpret_cast<uint4*>(sh.bins)[tid + i * sp::kThreads] = make_uint4(0, 0, 0, 0);
+    if (tid < 32) sh.exp2[tid] = make_float2(kExp2.hi[tid], kExp2.lo[tid]);
+    __syncthreads();
+    float top = -INFINITY;
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+    auto tally4 = [&](const uint32_t (&w)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; k++) tally(sh, w[k] & 0xFFFF, top, lo, hi), tally(sh, w[k] >> 16, top, lo, hi);
+    };
+#pragma unroll
+    for (int i = 0; i < sp::kHeld; i++) tally4(held[i]);
+#pragma unroll 1
+    for (int v = v0 + sp::kHeld * sp::kThreads + tid; v < v1; v += sp::kThreads) {
+      uint32_t w[4];
+      rv.load(v, v1, w);
+      tally4(w);
     }
-    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-  };
-  uint32_t held[sp::kHeld][4];  // all of a thread's loads in flight while the counters are cleared
-#pragma unroll
-  for (int i = 0; i < sp::kHeld; i++) load(v0 + i * sp::kThreads + tid, held[i]);
-  const float temperature = a.s.temperature_rows ? a.s.temperature_rows[row] : a.s.temperature;
-  const float min_p = a.s.min_p_rows ? a.s.min_p_rows[row] : a.s.min_p;
-  const float top_p = a.s.top_p_rows ? a.s.top_p_rows[row] : a.s.top_p;
-  const int top_k = a.s.top_k_rows ? a.s.top_k_rows[row] : a.s.top_k;
-  const float u_row = a.u[row];
-#pragma unroll
-  for (int i = 0; i < 8; i++) reinterpret_cast<uint4*>(sh.bins)[tid + i * sp::kThreads] = make_uint4(0, 0, 0, 0);
-  if (tid < 32) sh.exp2[tid] = make_float2(kExp2.hi[tid], kExp2.lo[tid]);
-  __syncthreads();
-  float top = -INFINITY;
-  uint32_t lo = 0xFFFFFFFFu, hi = 0;
-  auto tally4 = [&](const uint32_t (&w)[4]) {
-#pragma unroll
-    for (int k = 0; k < 4; k++) tally(sh, w[k] & 0xFFFF, top, lo, hi), tally(sh, w[k] >> 16, top, lo, hi);
-  };
-#pragma unroll
-  for (int i = 0; i < sp::kHeld; i++) tally4(held[i]);
-  for (int v = v0 + sp::kHeld * sp::kThreads + tid; v < v1; v += sp::kThreads) {
-    uint32_t w[4];
-    load(v, w);
-    tally4(w);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  if (lane == 0) sh.top[warp] = top, sh.lo[warp] = lo, sh.hi[warp] = hi;
-  __syncthreads();
-  if (warp == 0) {
-    top = sh.top[lane];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    lo = __reduce_min_sync(0xffffffffu, sh.lo[lane]);
-    hi = __reduce_max_sync(0xffffffffu, sh.hi[lane]);
-    if (lane == 0) sh.span[0] = __float_as_uint(top), sh.span[1] = lo, sh.span[2] = hi;
-  }
-  cluster_sync_all();
-
-  // ---- the row's greatest logit and its binades
-  const uint32_t bins = smem_u32(sh.bins), span = smem_u32(sh.span);
-  top = -INFINITY, lo = 0xFFFFFFFFu, hi = 0;
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) sh.top[warp] = top, sh.lo[warp] = lo, sh.hi[warp] = hi;
+    __syncthreads();
+    if (warp == 0) {
+      top = sh.top[lane];
 #pragma unroll
-  for (int k = 0; k < C; k++) {
-    const uint32_t at = cluster_map(span, k);
-    top = fmaxf(top, __uint_as_float(ld_cluster_u32(at)));
-    lo = min(lo, ld_cluster_u32(at + 4));
-    hi = max(hi, ld_cluster_u32(at + 8));
-  }
-  const bool none = top == -INFINITY;
-  Binades bn;
-  bn.e1 = hi >> 7;
-  bn.e0 = min((int)((lo == 0xFFFFFFFFu ? 0u : lo + 1) >> 7), bn.e1);
-  RowScale rs;
-  rs.most = top;
-  {  // log2(e) / temperature: the quotient and its remainder's
-    constexpr float lh = (float)1.4426950408889634074, ll = (float)(1.4426950408889634074 - (double)lh);
-    const float q = __fdiv_rn(lh, temperature);
-    const bool fine = temperature > 0.f && q < 3e38f;
-    rs.ch = temperature > 0.f ? fminf(q, 3e38f) : 0.f;
-    rs.cl = fine ? __fdiv_rn(__fadd_rn(__fmaf_rn(-q, temperature, lh), ll), temperature) : 0.f;
-  }
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      lo = __reduce_min_sync(0xffffffffu, sh.lo[lane]);
+      hi = __reduce_max_sync(0xffffffffu, sh.hi[lane]);
+      if (lane == 0) sh.span[0] = __float_as_uint(top), sh.span[1] = lo, sh.span[2] = hi;
+    }
+    cluster_sync_all();
 
-  // ---- each binade's keys, count and sum, into the first CTA
-  if (!none) {
-    const uint32_t mass0 = cluster_map(smem_u32(sh.mass), 0), count0 = cluster_map(smem_u32(sh.count), 0);
-    const uint32_t keys0 = cluster_map(smem_u32(sh.keys), 0), weight0 = cluster_map(smem_u32(sh.weight), 0);
-    for (int i = warp * C + rank; i < bn.n(); i += sp::kWarps * C) {
-      uint32_t c[4], n = 0;
-      uint64_t w[4], m = 0;
-      lane_keys<C>(bins, bn, i, rs, sh.exp2, lane, c, w);
+    // ---- the row's greatest logit and its binades
+    const uint32_t bins = smem_u32(sh.bins), span = smem_u32(sh.span);
+    top = -INFINITY, lo = 0xFFFFFFFFu, hi = 0;
 #pragma unroll
-      for (int k = 0; k < 4; k++) n += c[k], m += c[k] * w[k];
-      if (i < sp::kTable) {
-        const uint32_t at = i * 128 + 4 * lane;
-        st_cluster_u4(keys0 + 4 * at, c[0], c[1], c[2], c[3]);
-        st_cluster_2u64(weight0 + 8 * at, w[0], w[1]);
-        st_cluster_2u64(weight0 + 8 * at + 16, w[2], w[3]);
+    for (int k = 0; k < C; k++) {
+      const uint32_t at = cluster_map(span, k);
+      top = fmaxf(top, __uint_as_float(ld_cluster_u32(at)));
+      lo = min(lo, ld_cluster_u32(at + 4));
+      hi = max(hi, ld_cluster_u32(at + 8));
+    }
+    const bool none = top == -INFINITY;
+    Binades bn;
+    bn.e1 = hi >> 7;
+    bn.e0 = min((int)((lo == 0xFFFFFFFFu ? 0u : lo + 1) >> 7), bn.e1);
+    const RowScale rs = set.scale(top);
+
+    // ---- each binade's keys, count and sum, into the first CTA
+    if (!none) {
+      const uint32_t mass0 = cluster_map(smem_u32(sh.mass), 0), count0 = cluster_map(smem_u32(sh.count), 0);
+      const uint32_t keys0 = cluster_map(smem_u32(sh.keys), 0), weight0 = cluster_map(smem_u32(sh.weight), 0);
+#pragma unroll 1
+      for (int i = warp * C + rank; i < bn.n(); i += sp::kWarps * C) {
+        uint32_t c[4], n = 0;
+        uint64_t w[4], m = 0;
+        lane_keys<C>(bins, bn, i, rs, sh.exp2, lane, c, w);
+#pragma unroll
+        for (int k = 0; k < 4; k++) n += c[k], m += c[k] * w[k];
+        if (i < sp::kTable) {
+          const uint32_t at = i * 128 + 4 * lane;
+          st_cluster_u4(keys0 + 4 * at, c[0], c[1], c[2], c[3]);
+          st_cluster_2u64(weight0 + 8 * at, w[0], w[1]);
+          st_cluster_2u64(weight0 + 8 * at + 16, w[2], w[3]);
+        }
+        n = __reduce_add_sync(0xffffffffu, n);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+        if (lane == 0) st_cluster_u64(mass0 + 8 * i, m), st_cluster_u32(count0 + 4 * i, n);
       }
-      n = __reduce_add_sync(0xffffffffu, n);
+    }
+    cluster_sync_all();
+
+    // ---- the cuts and the token's key, by one warp
+    if (rank == 0 && warp == 0) {
+      if (!none) {
+        const Chosen ch = walk(ClusterKeys<C>{sh, bins, bn, rs}, sh.count, sh.mass, rs, sh.exp2, set);
+        // the CTA that holds the occurrence
+        uint32_t mine = 0;
+        if (lane < C) mine = ld_cluster_u32(cluster_map(bins + 4 * (ch.key >> 1), lane)) >> (ch.key & 1 ? 16 : 0) & 0xFFFF;
+        const uint32_t before = before_lane(mine, lane);
+        if (lane < C) {
+          const uint32_t to = cluster_map(smem_u32(&sh.key), lane);
+          st_cluster_u32(to, ch.key);
+          st_cluster_u32(to + 4, ch.r >= before && ch.r < before + mine ? ch.r - before : 0xFFFFFFFFu);
+        }
+        if (lane == 0) write_row(a, row, ch, rs, sh.exp2);
+      } else {
+        if (lane < C) st_cluster_u32(cluster_map(smem_u32(&sh.nth), lane), 0xFFFFFFFFu);
+        if (lane == 0) write_empty(a, row);
+      }
+    }
+    cluster_sync_all();
+
+    // ---- occurrence nth of the key in this slice
+    const uint32_t key = sh.key, nth = sh.nth;
+    if (nth == 0xFFFFFFFFu) continue;
+    const int rounds = (v1 - v0 + sp::kThreads - 1) / sp::kThreads;  // at most 8
+#pragma unroll
+    for (int i = 0; i < sp::kHeld; i++) {
+      if (i >= rounds) break;
+      const uint32_t n = __reduce_add_sync(0xffffffffu, __popc(matches(held[i], key)));
+      if (lane == 0) sh.tot[i * sp::kWarps + warp] = n;
+    }
+#pragma unroll 1
+    for (int i = sp::kHeld; i < rounds; i++) {
+      uint32_t w[4];
+      rv.load(v0 + i * sp::kThreads + tid, v1, w);
+      const uint32_t n = __reduce_add_sync(0xffffffffu, __popc(matches(w, key)));
+      if (lane == 0) sh.tot[i * sp::kWarps + warp] = n;
+    }
+    __syncthreads();
+    if (warp == 0) look_up<sp::kWarps>(a, row, rv, v0, v1, rounds, sh.tot, key, nth);
+  }
+}
+
+struct RowShared {
+  uint32_t bins[2 * sp::kRowKeys + 4];  // counters: positive keys, negative ones, zero
+  uint64_t mass[sp::kRowBlocks + 1];
+  uint32_t count[sp::kRowBlocks + 1];
+  float2 exp2[32];
+  uint32_t other, key, nth;
+  uint32_t tot[129 * sp::kRowWarps];    // occurrences a round of vectors and warp
+};
+
+// A CTA a row.
+__global__ void __launch_bounds__(sp::kRowThreads, 2) k_sample_row(const __grid_constant__ SampleArgs a) {
+  extern __shared__ __align__(16) uint8_t smem_sp[];
+  RowShared& sh = *reinterpret_cast<RowShared*>(smem_sp);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.x;
+  const RowView rv(a, row);
+  const int end = rv.vectors();
+  constexpr int U = 4;  // vectors of a thread in flight, twice
+  uint32_t w[U][4];
+#pragma unroll
+  for (int i = 0; i < U; i++) rv.load(tid + i * sp::kRowThreads, end, w[i]);
+  const RowSettings set(a.s, a.u, row);
+  for (int i = tid; i < 2 * sp::kRowKeys / 4 + 1; i += sp::kRowThreads) reinterpret_cast<uint4*>(sh.bins)[i] = make_uint4(0, 0, 0, 0);
+  if (tid < 32) sh.exp2[tid] = make_float2(kExp2.hi[tid], kExp2.lo[tid]);
+  if (tid == 0) sh.other = 0;
+  __syncthreads();
+  bool other = false;  // a magnitude that has no counter
+  auto count1 = [&](uint32_t b) {
+    const uint32_t mag = b & 0x7FFFu, i = mag - (sp::kLeast << 7);
+    if (i < (uint32_t)sp::kRowKeys) {
+      atomicAdd(&sh.bins[i + (b >> 15) * sp::kRowKeys], 1u);
+    } else if (mag == 0) {
+      atomicAdd(&sh.bins[2 * sp::kRowKeys], 1u);
+    } else if (mag <= 0x7F80u && b != 0xFF80u) {
+      other = true;
+    }
+  };
+#pragma unroll 1
+  for (int v = tid; v < end; v += U * sp::kRowThreads) {
+    uint32_t next[U][4];
+#pragma unroll
+    for (int i = 0; i < U; i++) rv.load(v + (U + i) * sp::kRowThreads, end, next[i]);
+#pragma unroll
+    for (int i = 0; i < U; i++) {
+#pragma unroll
+      for (int k = 0; k < 4; k++) count1(w[i][k] & 0xFFFF), count1(w[i][k] >> 16);
+    }
+#pragma unroll
+    for (int i = 0; i < U; i++) {
+#pragma unroll
+      for (int k = 0; k < 4; k++) w[i][k] = next[i][k];
+    }
+  }
+  if (__any_sync(0xffffffffu, other) && lane == 0) sh.other = 1;
+  __syncthreads();
+  if (sh.other) {
+    if (tid == 0) a.tokens[row] = sp::kLater;
+    return;
+  }
+
+  // ---- the binades' counts, the greatest logit, their sums
+  RowKeys keys = {sh.bins, sh.exp2, {}};
+#pragma unroll 1
+  for (int i = warp; i < sp::kRowBlocks; i += sp::kRowWarps) {
+    uint32_t k[4];
+    keys.counts(i, lane, k);
+    const uint32_t n = __reduce_add_sync(0xffffffffu, k[0] + k[1] + k[2] + k[3]);
+    if (lane == 0) sh.count[i] = n;
+  }
+  __syncthreads();
+  int first = -1;
+#pragma unroll
+  for (int c = 0; c < sp::kRowBlocks; c += 32) {
+    const uint32_t f = __ballot_sync(0xffffffffu, c + lane < sp::kRowBlocks && sh.count[c + lane] > 0);
+    if (first < 0 && f) first = c + __ffs(f) - 1;
+  }
+  if (first < 0) {
+    if (tid == 0) write_empty(a, row);
+    return;
+  }
+  {
+    uint32_t k[4];
+    keys.counts(first, lane, k);
+    const uint32_t j = __reduce_min_sync(0xffffffffu, k[0] ? 4 * lane : k[1] ? 4 * lane + 1 : k[2] ? 4 * lane + 2 : k[3] ? 4 * lane + 3 : 128);
+    keys.rs = set.scale(bf2f((uint16_t)keys.bits(first, j)));
+  }
+#pragma unroll 1
+  for (int i = warp; i < sp::kRowBlocks; i += sp::kRowWarps) {
+    uint64_t m = 0;
+    if (sh.count[i]) {
+      uint32_t k[4];
+      uint64_t x[4];
+      keys.lane_of(i, lane, k, x);
+#pragma unroll
+      for (int e = 0; e < 4; e++) m += k[e] * x[e];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-      if (lane == 0) st_cluster_u64(mass0 + 8 * i, m), st_cluster_u32(count0 + 4 * i, n);
     }
-  }
-  cluster_sync_all();
-
-  // ---- the cuts and the token's key, by one warp
-  if (rank == 0 && warp == 0) {
-    uint32_t key = 0, nth = 0xFFFFFFFFu;
-    if (!none) {
-      // running counts and sums, a run of binades a lane
-      const int n = bn.n(), each = (n + 31) / 32, i0 = min(n, lane * each), i1 = min(n, i0 + each);
-      uint32_t c = 0;
-      uint64_t m = 0;
-      for (int i = i0; i < i1; i++) c += sh.count[i], m += sh.mass[i];
-      uint32_t cb = before_lane(c, lane);
-      uint64_t mb = before_lane(m, lane);
-      for (int i = i0; i < i1; i++) {
-        cb += sh.count[i], mb += sh.mass[i];
-        sh.count[i] = cb, sh.mass[i] = mb;
-      }
-      __syncwarp();
-      uint64_t N = sh.count[n - 1], W = sh.mass[n - 1];
-      const uint64_t K = !(temperature > 0.f) ? 1 : top_k > 0 ? top_k : N;
-      if (K < N) {
-        const Place p = find<false, C>(sh, bins, bn, rs, K, false);
-        N = K;
-        W = p.mass + (K - p.count) * p.w;
-      }
-      if (min_p > 0.f) {
-        const float least = fminf(min_p, 1.f);
-        // the first binade whose last key weighs less
-        int i = n;
-        for (int c = 0; c < n && i == n; c += 32) {
-          bool neg = false, below = false;
-          if (c + lane < n) {
-            const uint32_t e = bn.exponent(c + lane, neg);
-            below = !weight_of(bf2f((uint16_t)key_bits(e, neg, 127)), rs, sh.exp2).at_least(least);
-          }
-          const uint32_t f = __ballot_sync(0xffffffffu, below);
-          if (f) i = c + __ffs(f) - 1;
-        }
-        if (i < n) {
-          bool neg;
-          const uint32_t e = bn.exponent(i, neg);
-          uint32_t k[4], cc = 0;
-          uint64_t w[4], mm = 0;
-          kept_keys<C>(sh, bins, bn, i, rs, lane, k, w);
-#pragma unroll
-          for (int x = 0; x < 4; x++)
-            if (k[x] && weight_of(bf2f((uint16_t)key_bits(e, neg, 4 * lane + x)), rs, sh.exp2).at_least(least)) cc += k[x], mm += k[x] * w[x];
-          cc = __reduce_add_sync(0xffffffffu, cc) + (i ? sh.count[i - 1] : 0);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) mm += __shfl_xor_sync(0xffffffffu, mm, o);
-          mm += i ? sh.mass[i - 1] : 0;
-          if (cc < N) N = cc, W = mm;
-        }
-      }
-      if (top_p < 1.f) {
-        const uint64_t goal = max(share_of(top_p, W, true), (uint64_t)1);
-        const Place p = find<true, C>(sh, bins, bn, rs, goal, false);
-        const uint64_t r = (goal - p.mass + p.w - 1) / p.w;
-        if (p.count + r < N) N = p.count + r, W = p.mass + r * p.w;
-      }
-      const float u = u_row > 0.f ? fminf(u_row, 1.f - 0x1p-24f) : 0.f;
-      const uint64_t goal = share_of(u, W, false);
-      const Place p = find<true, C>(sh, bins, bn, rs, goal, true);
-      const uint32_t r = (uint32_t)((goal - p.mass) / p.w);
-      bool neg;
-      const uint32_t e = bn.exponent(p.i, neg);
-      key = key_bits(e, neg, p.j);
-      // the CTA that holds occurrence r
-      uint32_t mine = 0;
-      if (lane < C) mine = ld_cluster_u32(cluster_map(bins + 4 * (key >> 1), lane)) >> (key & 1 ? 16 : 0) & 0xFFFF;
-      const uint32_t before = before_lane(mine, lane);
-      if (lane < C) {
-        const uint32_t to = cluster_map(smem_u32(&sh.key), lane);
-        st_cluster_u32(to, key);
-        st_cluster_u32(to + 4, r >= before && r < before + mine ? r - before : 0xFFFFFFFFu);
-      }
-      if (lane == 0) {
-        if (a.logprob) a.logprob[row] = 0.f - log1pf((float)(W - p.w) * 0x1p-44f / weight_of(bf2f((uint16_t)key), rs, sh.exp2).value());
-        if (a.kept) a.kept[row] = (int32_t)N;
-      }
-    } else if (lane < C) {
-      st_cluster_u32(cluster_map(smem_u32(&sh.nth), lane), nth);
-      if (lane == 0) {
-        a.tokens[row] = -1;
-        if (a.logprob) a.logprob[row] = -INFINITY;
-        if (a.kept) a.kept[row] = 0;
-      }
-    }
-  }
-  cluster_sync_all();
-
-  // ---- occurrence nth of the key in this slice
-  const uint32_t key = sh.key, nth = sh.nth;
-  if (nth == 0xFFFFFFFFu) return;
-  auto matches4 = [&](const uint32_t (&w)[4]) {
-    uint32_t f = 0;
-#pragma unroll
-    for (int k = 0; k < 8; k++) {
-      uint32_t b = w[k / 2] >> (k & 1 ? 16 : 0) & 0xFFFF;
-      if (b == 0x8000u) b = 0;
-      f |= (uint32_t)(b == key) << k;
-    }
-    return f;
-  };
-  auto matches = [&](int v) {
-    uint32_t w[4];
-    load(v, w);
-    return matches4(w);
-  };
-  const int rounds = (v1 - v0 + sp::kThreads - 1) / sp::kThreads;  // at most 8
-#pragma unroll
-  for (int i = 0; i < sp::kHeld; i++) {
-    if (i >= rounds) break;
-    const uint32_t n = __reduce_add_sync(0xffffffffu, __popc(matches4(held[i])));
-    if (lane == 0) sh.tot[i * sp::kWarps + warp] = n;
-  }
-  for (int i = sp::kHeld; i < rounds; i++) {
-    const uint32_t n = __reduce_add_sync(0xffffffffu, __popc(matches(v0 + i * sp::kThreads + tid)));
-    if (lane == 0) sh.tot[i * sp::kWarps + warp] = n;
+    if (lane == 0) sh.mass[i] = m;
   }
   __syncthreads();
   if (warp == 0) {
-    uint32_t run = 0, where = 0, left = 0;
-    bool found = false;
-    for (int c = 0; c < rounds && !found; c++) {
-      const uint32_t n = sh.tot[c * 32 + lane], b = run + before_lane(n, lane);
-      const uint32_t f = __ballot_sync(0xffffffffu, nth >= b && nth < b + n);
-      if (f) {
-        found = true;
-        where = c * 32 + __ffs(f) - 1;
-        left = nth - __shfl_sync(0xffffffffu, b, __ffs(f) - 1);
-      }
-      run = __shfl_sync(0xffffffffu, b + n, 31);
-    }
-    if (found) {
-      const int v = v0 + (int)(where / 32) * sp::kThreads + (int)(where % 32) * 32 + lane;
-      uint32_t f = matches(v);
-      const uint32_t n = __popc(f), b = before_lane(n, lane);
-      if (left >= b && left < b + n) {
-        for (uint32_t k = b; k < left; k++) f &= f - 1;
-        a.tokens[row] = token(v, __ffs(f) - 1);
-      }
+    const Chosen ch = walk(keys, sh.count, sh.mass, keys.rs, sh.exp2, set);
+    if (lane == 0) {
+      sh.key = ch.key, sh.nth = ch.r;
+      write_row(a, row, ch, keys.rs, sh.exp2);
     }
   }
+  __syncthreads();
+  pdl_launch();
+  const uint32_t key = sh.key, nth = sh.nth;
+  const int rounds = (end + sp::kRowThreads - 1) / sp::kRowThreads;
+#pragma unroll 4
+  for (int i = 0; i < rounds; i++) {
+    uint32_t x[4];
+    rv.load(i * sp::kRowThreads + tid, end, x);
+    const uint32_t n = __reduce_add_sync(0xffffffffu, __popc(matches(x, key)));
+    if (lane == 0) sh.tot[i * sp::kRowWarps + warp] = n;
+  }
+  __syncthreads();
+  if (warp == 0) look_up<sp::kRowWarps>(a, row, rv, 0, end, rounds, sh.tot, key, nth);
 }
 
 static int sample_bad(int code, const char* what) {
@@ -617,17 +848,23 @@ extern "C" int sd_sample(const uint16_t* logits, int64_t row_stride, int32_t row
   while (slice(C) > sp::kSlice) C *= 2;
   // few rows: more CTAs a row while each still has 4096 tokens
   while (C < sp::kMaxCluster && (int64_t)rows * C * 2 <= num_sms() && vocab >= 4096 * 2 * C) C *= 2;
-  if ((int64_t)rows * C > 0x7FFFFFFF) return sample_bad(SD_ERR_UNSUPPORTED, "too many rows");
-  const void* kerns[4] = {(const void*)k_sample<1>, (const void*)k_sample<2>, (const void*)k_sample<4>, (const void*)k_sample<8>};
-  static const cudaError_t set = [&]() {
-    cudaError_t e = cudaSuccess;
+  static const cudaError_t set = []() {
+    const void* kerns[4] = {(const void*)k_sample<1>, (const void*)k_sample<2>, (const void*)k_sample<4>, (const void*)k_sample<8>};
+    cudaError_t e = cudaFuncSetAttribute(k_sample_row, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(RowShared));
     for (const void* k : kerns)
       if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SampleShared));
     return e;
   }();
   SD_CK(set);
   const SampleArgs a = {logits, row_stride, rows, vocab, slice(C), s, u, tokens, logprob, kept};
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool many = (int64_t)rows * C > num_sms();
+  if (many) {
+    k_sample_row<<<rows, sp::kRowThreads, sizeof(RowShared), st>>>(a);
+    SD_CK(cudaGetLastError());
+  }
   auto kern = C == 1 ? k_sample<1> : C == 2 ? k_sample<2> : C == 4 ? k_sample<4> : k_sample<8>;
-  SD_CK(launch_cluster(kern, dim3((unsigned)(rows * C)), dim3(sp::kThreads), sizeof(SampleShared), (cudaStream_t)stream, false, C, a));
+  const int clusters = many ? std::min(rows, 32) : rows;
+  SD_CK(launch_cluster(kern, dim3((unsigned)(clusters * C)), dim3(sp::kThreads), sizeof(SampleShared), st, many, C, a, many));
   return SD_OK;
 }

@@ -113,6 +113,35 @@ def test_tiny_magnitudes_keep_their_order(M):
     check(M, x, u, top_k=1500)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=7, temperature=0.8), dict(top_p=0.7, min_p=0.01), dict(temperature=0.0)])
+def test_many_rows_with_special_values(M, kw):
+    """Many rows, some with magnitudes past 2^15 or below 2^-24, infinities, masks of every kind, nothing left."""
+    x, u = normal(220, 1501, seed=14)
+    x[3] = -math.inf
+    x[10, 5] = 1e30
+    x[11, 5], x[11, 700] = -1e30, 1e-30
+    x[40] = torch.finfo(torch.bfloat16).min
+    x[41, 9] = math.inf
+    x[42, :1500] = -math.inf
+    x[43, ::3] = math.nan
+    x[44] = 0.0
+    x[45] = (x[45].float() * 1e-9).bfloat16()
+    x[46] = torch.finfo(torch.bfloat16).min
+    x[46, 1500] = 3.0
+    x[219] = math.nan
+    check(M, x, u, **kw)
+
+
+def test_long_rows_one_cta_each(M):
+    x, u = normal(160, 40000, seed=15)
+    check(M, x[:, 3:], u, temperature=1.2)
+    x = torch.zeros(153, 140000).bfloat16().cuda()  # one key, more than 16 bits of it
+    u = torch.rand(153, generator=torch.Generator().manual_seed(3)).cuda()
+    got = M.sample(x, u)
+    want = torch.floor(u.double() * 140000).to(torch.int32)
+    assert torch.equal(got["tokens"], want) and (got["kept"] == 140000).all()
+
+
 def test_u_is_clamped(M):
     x, _ = normal(5, 300, seed=2)
     u = torch.tensor([-1.0, math.nan, 1.0, 7.0, math.inf]).cuda()

@@ -521,16 +521,17 @@ struct RowView {
     w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
   }
 };
-// The elements of a vector that are the key, as bits.
+// The elements of a vector that are the key, as bits; -0 is 0.
 __device__ __forceinline__ uint32_t matches(const uint32_t (&w)[4], uint32_t key) {
+  const uint32_t both = key * 0x10001u, of = key == 0 ? 0x7FFF7FFFu : 0xFFFFFFFFu;
   uint32_t f = 0;
 #pragma unroll
-  for (int k = 0; k < 8; k++) {
-    uint32_t b = w[k / 2] >> (k & 1 ? 16 : 0) & 0xFFFF;
-    if (b == 0x8000u) b = 0;
-    f |= (uint32_t)(b == key) << k;
+  for (int k = 0; k < 4; k++) {
+    const uint32_t x = (w[k] & of) ^ both;  // bit 15 of a half below: it is zero
+    const uint32_t z = ~(((x & 0x7FFF7FFFu) + 0x7FFF7FFFu) | x) & 0x80008000u;
+    f |= z >> (15 - 2 * k);                 // elements 2 k at bit 2 k, 2 k + 1 at bit 16 + 2 k
   }
-  return f;
+  return (f & 0x55u) | (f >> 15 & 0xAAu);
 }
 // By one warp: the token of occurrence nth of the key in vectors v0 .. end of a row, of
 // which round i's by warp w are tot[i * WARPS + w].
@@ -567,7 +568,13 @@ __global__ void __launch_bounds__(sp::kThreads, 1) k_sample(const __grid_constan
   SampleShared& sh = *reinterpret_cast<SampleShared*>(smem_sp);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster_rank();
-  if (only) pdl_wait();
+  if (only) {  // none of this cluster's rows (which only it changes) is left: the rule
+    pdl_wait();
+    bool left = false;
+    for (int64_t r = blockIdx.x / C + (int64_t)tid * (gridDim.x / C); r < a.rows; r += (int64_t)sp::kThreads * (gridDim.x / C))
+      left |= a.tokens[r] == sp::kLater;
+    if (!__syncthreads_or(left)) return;
+  }
 #pragma unroll 1
   for (int row = blockIdx.x / C; row < a.rows; row += gridDim.x / C) {
     if (only && a.tokens[row] != sp::kLater) continue;
@@ -733,16 +740,35 @@ __global__ void __launch_bounds__(sp::kRowThreads, 2) k_sample_row(const __grid_
       other = true;
     }
   };
+  auto count8 = [&](const uint32_t (&w)[4]) {
+    // bit 15 of a half: its magnitude has a counter
+    constexpr uint32_t least = sp::kLeast << 7, past = least + sp::kRowKeys;
+    uint32_t in = 0x80008000u;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const uint32_t m = w[k] & 0x7FFF7FFFu;
+      in &= (m + (0x8000u - least) * 0x10001u) & ~(m + (0x8000u - past) * 0x10001u);
+    }
+    if (in == 0x80008000u) {
+      uint32_t* const at = sh.bins - least;
+#pragma unroll
+      for (int k = 0; k < 4; k++) {  // a negative key's counter: its bits less what lies between
+        const uint32_t b = w[k] & 0xFFFFu, c = w[k] >> 16;
+        atomicAdd(at + (int)(b - (b >> 15) * (0x8000u - sp::kRowKeys)), 1u);
+        atomicAdd(at + (int)(c - (c >> 15) * (0x8000u - sp::kRowKeys)), 1u);
+      }
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < 8; k++) count1((k < 4 ? k < 2 ? w[0] : w[1] : k < 6 ? w[2] : w[3]) >> 16 * (k & 1) & 0xFFFF);
+    }
+  };
 #pragma unroll 1
   for (int v = tid; v < end; v += U * sp::kRowThreads) {
     uint32_t next[U][4];
 #pragma unroll
     for (int i = 0; i < U; i++) rv.load(v + (U + i) * sp::kRowThreads, end, next[i]);
 #pragma unroll
-    for (int i = 0; i < U; i++) {
-#pragma unroll
-      for (int k = 0; k < 4; k++) count1(w[i][k] & 0xFFFF), count1(w[i][k] >> 16);
-    }
+    for (int i = 0; i < U; i++) count8(w[i]);
 #pragma unroll
     for (int i = 0; i < U; i++) {
 #pragma unroll

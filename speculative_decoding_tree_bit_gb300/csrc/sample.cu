@@ -79,7 +79,7 @@ struct Weight {
 };
 
 // The weight of logit l <= most; n = -200 where it is below 2^-120.
-__device__ __forceinline__ Weight weight_of(float l, const RowScale& r, const float2* s_exp2) {
+__device__ __forceinline__ Weight weight_here(float l, const RowScale& r, const float2* s_exp2) {
   // l - most = s + d, log2 of the weight p + e
   const float s = __fadd_rn(l, -r.most), b = __fadd_rn(s, -l);
   const float d = __fadd_rn(__fadd_rn(l, -__fadd_rn(s, -b)), __fadd_rn(-r.most, -b));
@@ -118,6 +118,13 @@ __device__ __forceinline__ Weight weight_of(float l, const RowScale& r, const fl
   w.l = __fadd_rn(__fadd_rn(__fadd_rn(ph, -__fadd_rn(w.h, -t.x)), pl), t.y);
   w.n = none ? -200 : m >> 5;
   return w;
+}
+// Called where one weight is wanted; where four are, they are worked out side by side.
+__device__ __noinline__ Weight weight_at(float l, float most, float ch, float cl, const float2* s_exp2) {
+  return weight_here(l, RowScale{most, ch, cl}, s_exp2);
+}
+__device__ __forceinline__ Weight weight_of(float l, const RowScale& r, const float2* s_exp2) {
+  return weight_at(l, r.most, r.ch, r.cl, s_exp2);
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -211,7 +218,7 @@ __device__ __forceinline__ void lane_keys(uint32_t bins, const Binades& b, int i
   lane_counts<C>(bins, e, neg, lane, k);
 #pragma unroll
   for (int x = 0; x < 4; x++) {
-    const uint64_t v = weight_of(bf2f((uint16_t)key_bits(e, neg, 4 * lane + x)), rs, s_exp2).whole();
+    const uint64_t v = weight_here(bf2f((uint16_t)key_bits(e, neg, 4 * lane + x)), rs, s_exp2).whole();
     w[x] = k[x] ? v : 0;  // a key that does not occur may lie above the greatest logit
   }
 }
@@ -229,7 +236,7 @@ __device__ __forceinline__ T before_lane(T v, int lane) {
 }
 
 // ceil or floor of p W for a float 0 <= p < 1.
-__device__ __forceinline__ uint64_t share_of(float p, uint64_t W, bool up) {
+__device__ __noinline__ uint64_t share_of(float p, uint64_t W, bool up) {
   if (!(p > 0.f)) return 0;
   const uint32_t b = __float_as_uint(p);
   const int e = b >> 23;
@@ -319,7 +326,7 @@ struct RowKeys {
     counts(i, lane, k);
 #pragma unroll
     for (int x = 0; x < 4; x++) {
-      const uint64_t v = weight_of(bf2f((uint16_t)bits(i, 4 * lane + x)), rs, exp2).whole();
+      const uint64_t v = weight_here(bf2f((uint16_t)bits(i, 4 * lane + x)), rs, exp2).whole();
       w[x] = k[x] ? v : 0;
     }
   }
@@ -710,7 +717,8 @@ struct RowShared {
   uint32_t count[sp::kRowBlocks + 1];
   float2 exp2[32];
   uint32_t other, key, nth;
-  uint32_t tot[129 * sp::kRowWarps];    // occurrences a round of vectors and warp
+  uint32_t tot[8 * sp::kRowWarps];      // occurrences a round of vectors and warp
+  uint32_t done[sp::kRowWarps];
 };
 
 // A CTA a row.
@@ -784,12 +792,18 @@ __global__ void __launch_bounds__(sp::kRowThreads, 2) k_sample_row(const __grid_
 
   // ---- the binades' counts, the greatest logit, their sums
   RowKeys keys = {sh.bins, sh.exp2, {}};
-#pragma unroll 1
-  for (int i = warp; i < sp::kRowBlocks; i += sp::kRowWarps) {
+  constexpr int kEach = (sp::kRowBlocks + sp::kRowWarps - 1) / sp::kRowWarps;
+  uint32_t sums[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; e++) {
     uint32_t k[4];
-    keys.counts(i, lane, k);
-    const uint32_t n = __reduce_add_sync(0xffffffffu, k[0] + k[1] + k[2] + k[3]);
-    if (lane == 0) sh.count[i] = n;
+    keys.counts(min(warp + e * sp::kRowWarps, sp::kRowBlocks - 1), lane, k);
+    sums[e] = __reduce_add_sync(0xffffffffu, k[0] + k[1] + k[2] + k[3]);
+  }
+  if (lane == 0) {
+#pragma unroll
+    for (int e = 0; e < kEach; e++)
+      if (warp + e * sp::kRowWarps < sp::kRowBlocks) sh.count[warp + e * sp::kRowWarps] = sums[e];
   }
   __syncthreads();
   int first = -1;
@@ -834,15 +848,28 @@ __global__ void __launch_bounds__(sp::kRowThreads, 2) k_sample_row(const __grid_
   pdl_launch();
   const uint32_t key = sh.key, nth = sh.nth;
   const int rounds = (end + sp::kRowThreads - 1) / sp::kRowThreads;
-#pragma unroll 4
-  for (int i = 0; i < rounds; i++) {
-    uint32_t x[4];
-    rv.load(i * sp::kRowThreads + tid, end, x);
-    const uint32_t n = __reduce_add_sync(0xffffffffu, __popc(matches(x, key)));
-    if (lane == 0) sh.tot[i * sp::kRowWarps + warp] = n;
+  uint32_t before = 0;  // occurrences in the rounds done
+#pragma unroll 1
+  for (int i = 0; i < rounds; i += 2 * U) {
+    uint32_t x[2 * U][4], all = 0;
+#pragma unroll
+    for (int j = 0; j < 2 * U; j++) rv.load((i + j) * sp::kRowThreads + tid, end, x[j]);
+#pragma unroll
+    for (int j = 0; j < 2 * U; j++) {
+      const uint32_t n = __reduce_add_sync(0xffffffffu, __popc(matches(x[j], key)));
+      if (lane == 0) sh.tot[j * sp::kRowWarps + warp] = n;  // none past the row's end
+      all += n;
+    }
+    if (lane == 0) sh.done[warp] = all;
+    __syncthreads();
+    const uint32_t here = __reduce_add_sync(0xffffffffu, lane < sp::kRowWarps ? sh.done[lane] : 0u);
+    if (nth < before + here) {
+      if (warp == 0) look_up<sp::kRowWarps>(a, row, rv, i * sp::kRowThreads, end, 2 * U, sh.tot, key, nth - before);
+      return;
+    }
+    before += here;
+    __syncthreads();
   }
-  __syncthreads();
-  if (warp == 0) look_up<sp::kRowWarps>(a, row, rv, 0, end, rounds, sh.tot, key, nth);
 }
 
 static int sample_bad(int code, const char* what) {

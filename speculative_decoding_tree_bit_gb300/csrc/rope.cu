@@ -29,16 +29,58 @@ struct RopeArgs {
   int heads[2];
   int rows, rot, D;        // rot: rot_dim
   int groups;              // threads of a row and a run of heads
-  int each, runs;          // heads of a run; runs a row
+  int each;                // heads of a run, at most
+  int q_runs, runs;        // runs of a row: of queries, and in all
   float amplitude;
 };
+
+struct HeadRun {
+  const uint16_t* in;
+  uint16_t* out;
+  int n;
+};
+
+__device__ __forceinline__ HeadRun head_run(const RopeArgs& a, int64_t row, int run) {
+  const bool k = run >= a.q_runs;
+  const int h = (k ? run - a.q_runs : run) * a.each;
+  return {(k ? a.in[1] : a.in[0]) + row * (k ? a.in_stride[1] : a.in_stride[0]) + (int64_t)h * a.D,
+          (k ? a.out[1] : a.out[0]) + row * (k ? a.out_stride[1] : a.out_stride[0]) + (int64_t)h * a.D,
+          min(a.each, (k ? a.heads[1] : a.heads[0]) - h)};
+}
+
+// Eight pairs of two pieces: (p, q) becomes (p c - q s, p s + q c), each rounded once.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn_pairs(uint32_t* u, uint32_t* v, const float* c, const float* s) {
+  if (INTERLEAVED) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      uint32_t& wd = i < 4 ? u[i] : v[i - 4];
+      const float p = __uint_as_float(wd << 16), q = __uint_as_float(wd & 0xFFFF0000u);
+      wd = pack_bf16x2(fmaf(p, c[i], -q * s[i]), fmaf(p, s[i], q * c[i]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const float p0 = __uint_as_float(u[i] << 16), p1 = __uint_as_float(u[i] & 0xFFFF0000u);
+      const float q0 = __uint_as_float(v[i] << 16), q1 = __uint_as_float(v[i] & 0xFFFF0000u);
+      u[i] = pack_bf16x2(fmaf(p0, c[2 * i], -q0 * s[2 * i]), fmaf(p1, c[2 * i + 1], -q1 * s[2 * i + 1]));
+      v[i] = pack_bf16x2(fmaf(p0, s[2 * i], q0 * c[2 * i]), fmaf(p1, s[2 * i + 1], q1 * c[2 * i + 1]));
+    }
+  }
+}
 
 // A thread has eight pairs of a row (two 16-byte pieces a head) and turns them in
 // `each` heads, so their sines are computed once for all of those; the pieces of
 // the dims that do not turn are copied by further threads.  Bound by memory: each
-// value crosses once.
+// value crosses once.  What counts is how much a thread has under way, because a
+// store may not pass a load of the same tensor and so ends a run of loads: 403 MB
+// (16384 rows, 40 + 8 heads of 128) take 69 us with one head's loads at a time, 63
+// with two, 61 (6.6 TB/s) with four, 64 with eight and the fewer warps of their
+// registers.  4099 rows of 16 + 16 heads of 64, interleaved, 32 dims turned: 7.4 us.
+constexpr int kBatch = 4;
+
 template <bool INTERLEAVED>
-__global__ void __launch_bounds__(256) k_rope(RopeArgs a) {
+__global__ void __launch_bounds__(256, 3) k_rope(RopeArgs a) {
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t part = id / a.groups;
   const int g = (int)(id - part * a.groups);
@@ -63,37 +105,25 @@ __global__ void __launch_bounds__(256) k_rope(RopeArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; i++) rope_angle(a.turns[g * 8 + i], p, a.amplitude, c[i], s[i]);
   }
-  const int h_end = min((run + 1) * a.each, a.heads[0] + a.heads[1]);
-#pragma unroll 4
-  for (int h = run * a.each; h < h_end; h++) {
-    const int w = h >= a.heads[0];
-    const int hh = w ? h - a.heads[0] : h;
-    const uint16_t* x = a.in[w] + row * a.in_stride[w] + hh * a.D;
-    uint16_t* y = a.out[w] + row * a.out_stride[w] + hh * a.D;
-    uint4 u = *reinterpret_cast<const uint4*>(x + d0);
-    uint4 v = two ? *reinterpret_cast<const uint4*>(x + d1) : make_uint4(0, 0, 0, 0);
-    if (turn) {
-      uint32_t* const uw = &u.x;
-      uint32_t* const vw = &v.x;
-      if (INTERLEAVED) {
+  const HeadRun r = head_run(a, row, run);
+  const uint16_t* x = r.in;
+  uint16_t* y = r.out;
+  for (int left = r.n; left > 0; left -= kBatch, x += kBatch * a.D, y += kBatch * a.D) {
+    // a store may not pass a load of the same tensor, so kBatch heads' loads come first
+    uint4 u[kBatch], v[kBatch];
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-          uint32_t& wd = i < 4 ? uw[i] : vw[i - 4];
-          const float p = __uint_as_float(wd << 16), q = __uint_as_float(wd & 0xFFFF0000u);
-          wd = pack_bf16x2(fmaf(p, c[i], -q * s[i]), fmaf(p, s[i], q * c[i]));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const float p0 = __uint_as_float(uw[i] << 16), p1 = __uint_as_float(uw[i] & 0xFFFF0000u);
-          const float q0 = __uint_as_float(vw[i] << 16), q1 = __uint_as_float(vw[i] & 0xFFFF0000u);
-          uw[i] = pack_bf16x2(fmaf(p0, c[2 * i], -q0 * s[2 * i]), fmaf(p1, c[2 * i + 1], -q1 * s[2 * i + 1]));
-          vw[i] = pack_bf16x2(fmaf(p0, s[2 * i], q0 * c[2 * i]), fmaf(p1, s[2 * i + 1], q1 * c[2 * i + 1]));
-        }
-      }
+    for (int j = 0; j < kBatch; j++) {
+      if (j >= left) break;
+      u[j] = *reinterpret_cast<const uint4*>(x + j * a.D + d0);
+      if (two) v[j] = *reinterpret_cast<const uint4*>(x + j * a.D + d1);
     }
-    *reinterpret_cast<uint4*>(y + d0) = u;
-    if (two) *reinterpret_cast<uint4*>(y + d1) = v;
+#pragma unroll
+    for (int j = 0; j < kBatch; j++) {
+      if (j >= left) break;
+      if (turn) turn_pairs<INTERLEAVED>(&u[j].x, &v[j].x, c, s);
+      *reinterpret_cast<uint4*>(y + j * a.D + d0) = u[j];
+      if (two) *reinterpret_cast<uint4*>(y + j * a.D + d1) = v[j];
+    }
   }
 }
 
@@ -113,12 +143,10 @@ __global__ void __launch_bounds__(256) k_rope_any(RopeArgs a) {
   const int d1 = INTERLEAVED ? d0 + 1 : d0 + np;
   float c = 1.f, s = 0.f;
   if (turn) rope_angle(a.turns[g], a.pos[row], a.amplitude, c, s);
-  const int h_end = min((run + 1) * a.each, a.heads[0] + a.heads[1]);
-  for (int h = run * a.each; h < h_end; h++) {
-    const int w = h >= a.heads[0];
-    const int hh = w ? h - a.heads[0] : h;
-    const uint16_t* x = a.in[w] + row * a.in_stride[w] + (int64_t)hh * a.D;
-    uint16_t* y = a.out[w] + row * a.out_stride[w] + (int64_t)hh * a.D;
+  const HeadRun r = head_run(a, row, run);
+  const uint16_t* x = r.in;
+  uint16_t* y = r.out;
+  for (int j = 0; j < r.n; j++, x += a.D, y += a.D) {
     if (turn) {
       const float p = bf2f(x[d0]), q = bf2f(x[d1]);
       y[d0] = f2bf(fmaf(p, c, -q * s));
@@ -211,16 +239,19 @@ extern "C" int sd_rope(const uint64_t* turns, float amplitude, int32_t head_dim,
       clash(q_out, q_out_stride, qn, k_out, k_out_stride, kn, false))
     return bad("an output overlaps a tensor that is not its own input");
   RopeArgs a = {turns, pos, {q, k}, {q_out, k_out}, {q_stride, k_stride}, {q_out_stride, k_out_stride},
-                {n_q_heads, n_kv_heads}, rows, rot_dim, head_dim, 0, 0, 0, amplitude};
+                {n_q_heads, n_kv_heads}, rows, rot_dim, head_dim, 0, 0, 0, 0, amplitude};
   const uintptr_t al = (uintptr_t)q | (uintptr_t)q_out | (uintptr_t)k | (uintptr_t)k_out;
   const int64_t st = q_stride | q_out_stride | (n_kv_heads ? k_stride | k_out_stride : 0);
   const bool wide = al % 16 == 0 && st % 8 == 0 && head_dim % 8 == 0 && rot_dim % 16 == 0;
   a.groups = wide ? rot_dim / 16 + (head_dim - rot_dim + 15) / 16 : rot_dim / 2 + head_dim - rot_dim;
-  // heads of a thread: as many as leave every SM 1024 threads
+  // heads of a thread: eight spread the sines' cost enough (four and 16 take 66 us
+  // for the 61 of the kernel's comment, 48 take 74), fewer where eight would leave
+  // SMs without a CTA
   const int heads = n_q_heads + n_kv_heads;
   const int64_t threads = (int64_t)rows * a.groups * heads;
-  a.each = (int)std::min<int64_t>(heads, std::max<int64_t>(1, threads / ((int64_t)num_sms() * 1024)));
-  a.runs = (heads + a.each - 1) / a.each;
+  a.each = (int)std::min<int64_t>(8, std::max<int64_t>(1, threads / ((int64_t)num_sms() * 256)));
+  a.q_runs = (n_q_heads + a.each - 1) / a.each;
+  a.runs = a.q_runs + (n_kv_heads + a.each - 1) / a.each;
   const int64_t blocks = ((int64_t)rows * a.runs * a.groups + 255) / 256;
   if (blocks > 0x7FFFFFFF) return bad("too many rows");
   auto kern = wide ? (interleaved ? k_rope<true> : k_rope<false>) : (interleaved ? k_rope_any<true> : k_rope_any<false>);

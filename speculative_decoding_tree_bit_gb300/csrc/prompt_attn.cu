@@ -11,10 +11,11 @@
 //  * 0..3 and 4..7: softmax, a thread a row: 128 scores from TMEM, maximum,
 //    exponentials, P (bf16) back over its scores; then the outputs.  A wide unit
 //    gives each of the two groups a tile of rows, a narrow one alternate steps of the
-//    same rows, joined through shared memory.  A step's weights are taken with the
-//    reference that the steps before left, so that its maximum is looked for behind
-//    them, while the products run: P and O may be large, not inaccurate, and O is
-//    rescaled in TMEM only when the maximum has grown by 2^8.
+//    same rows, joined through shared memory.  A row's reference is the greatest score
+//    of the first half step in which it sees a key, and stays: weights, P and O may be
+//    large, not inaccurate.  Only where half a step's weights come to 2^20 is it raised
+//    and O rescaled in TMEM (looking for the maximum in every step: 177 us for 166 on
+//    8 prompts of 2048).
 //  * 8, 9: the products of one group each: S = Q K^T and O += P V, those of one group
 //    while the other is in its softmax.  TMEM: [S 128][S 128][O D][O D].
 //  * 10: walks the CTA's units, says what each is (PaDesc), and loads Q, K and V by TMA.
@@ -42,7 +43,7 @@ constexpr int kMaxCta = 160;
 constexpr int kNK = 2, kNV = 2;  // stages of K and of V
 constexpr int kNU = 4;           // units being described
 constexpr float kLag = 8.f;
-constexpr float kMost = 0x1p60f;  // of a row's weights in half a step
+constexpr float kMost = 0x1p20f;  // of a row's weights in half a step
 constexpr int kXs = 20;          // floats of a row being exchanged (16 used)
 }  // namespace pa
 
@@ -271,7 +272,6 @@ __device__ __forceinline__ void pa_wait(uint32_t bar, uint32_t parity, volatile 
 // What a softmax thread keeps of its row over a unit.
 struct PaRow {
   float ref, l;  // reference (base 2), sum of 2^(score - ref)
-  float top;     // the greatest score
   bool done;     // the group had steps
   bool live;     // the lane has a row
 };
@@ -400,20 +400,17 @@ __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, 
   auto far = [&](float l) { return w.live && !(l < pa::kMost) && w.l == w.l; };  // past the reference, or the first NaN
   auto weights = [&](float (&x)[64], int h) {
     if (MODE != kPlain || masked) pa_scores<MODE>(a, x, 64 * h, kb + 64 * h, see0, see1, masked, slope);
-    // the first keys that a row sees give its reference (nothing is held of it before);
-    // the steps before may have left a greater one
-    if (__any_sync(0xffffffffu, w.live && (w.ref == -INFINITY || (h == 0 && w.top > w.ref + pa::kLag)))) {
+    // the first keys that a row sees give its reference (nothing is held of it before)
+    if (__any_sync(0xffffffffu, w.live && w.ref == -INFINITY)) {
       if (w.ref == -INFINITY) w.ref = fmaxf(fmaf(pa_max(x), f, base), -INFINITY);  // no NaN
-      if (h == 0) pa_grow<D>(w, to, w.top, w.done);
     }
     float l;
 #pragma unroll 1
     for (;;) {
       l = pa_weights(x, f, off(), ts + 32 * h);
       if (!__any_sync(0xffffffffu, far(l))) break;
-      w.top = fmaxf(w.top, fmaf(pa_max(x), f, base));
       if (h == 1) first();
-      pa_grow<D>(w, to, w.top, h == 1 || w.done);
+      pa_grow<D>(w, to, fmaf(pa_max(x), f, base), h == 1 || w.done);
       if (!(l == l)) w.l = l;
     }
     w.l += l;
@@ -424,12 +421,10 @@ __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, 
   if (MODE == kPlain) {
     pa_wait_ld(r1);
   } else {
-    w.top = fmaxf(w.top, fmaf(pa_max(x0), f, base));
     pa_tmem_ld(ts + 64, r0);
     pa_wait_ld(r0);
   }
   weights(x1, 1);
-  w.top = fmaxf(w.top, fmaf(MODE == kPlain ? fmaxf(pa_max(x0), pa_max(x1)) : pa_max(x1), f, base));
   w.done = true;
 }
 
@@ -713,7 +708,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
       const int see0 = a.s.window > 0 && p >= 0 ? max(p - a.s.window + 1, 0) : 0;
       const bool pair = !d.wide && n > 1;              // the groups share the rows
       const bool live = (d.wide ? t * a.T : 0) + tok_of < d.tc && tok_of < a.T;
-      PaRow row = {-INFINITY, 0.f, -INFINITY, false, live};
+      PaRow row = {-INFINITY, 0.f, false, live};
       if (n > 0) {
         wait(q_full, some);  // no group is a unit ahead of the others' barriers
         if (!pair && lane == 0) mbar_arrive(q_empty);  // nothing to exchange

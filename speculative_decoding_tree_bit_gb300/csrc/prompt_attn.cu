@@ -282,7 +282,7 @@ constexpr int kPlain = 0, kSlopes = 1, kCapped = 2;
 // 64 scores of a row, from key c0 of a step on: cap and slope, and -inf for the keys
 // that it does not see (kb: the first one's number; see0 .. see1: the keys it sees).
 template <int MODE>
-__device__ __forceinline__ void pa_scores(const PaArgs& a, float (&x)[64], int c0, int kb, int see0, int see1, bool masked,
+__device__ __forceinline__ void pa_scores(const PaArgs& a, float (&x)[64], int kb, int see0, int see1, bool masked,
                                           float slope) {
   if (MODE == kCapped) {
     // tanh's Taylor series to x^9 where every score of the warp is below 0.3 of the cap
@@ -309,7 +309,7 @@ __device__ __forceinline__ void pa_scores(const PaArgs& a, float (&x)[64], int c
   }
   if (MODE == kSlopes || (MODE == kCapped && a.s.slopes)) {
 #pragma unroll
-    for (int c = 0; c < 64; c++) x[c] = fmaf(slope, (float)(c0 + c), x[c]);
+    for (int c = 0; c < 64; c++) x[c] = fmaf(slope, (float)c, x[c]);
   }
   if (masked) {
     // sixteens of which every row of the warp sees all are passed over
@@ -386,20 +386,15 @@ __device__ __forceinline__ void pa_grow(PaRow& w, uint32_t to, float top, bool h
 // rest until half(0): its last product's commit came before these scores'.
 template <int D, int MODE, typename Half, typename First>
 __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, uint32_t to, int kb, int see0, int see1,
-                                        bool masked, float f, float slope, float base, Half half, First first) {
-  // Without options the second half is asked for ahead of the first one's weights, and
-  // both are looked through for the maximum at the end; with them, half after half, in
-  // as many registers less.
-  uint32_t r0[64], r1[64];
-  float (&x0)[64] = reinterpret_cast<float (&)[64]>(r0);
-  float (&x1)[64] = reinterpret_cast<float (&)[64]>(MODE == kPlain ? r1 : r0);
-  pa_tmem_ld(ts, r0);
-  pa_wait_ld(r0);
-  if (MODE == kPlain) pa_tmem_ld(ts + 64, r1);
-  auto off = [&]() { return w.ref == -INFINITY ? 0.f : base - w.ref; };
+                                        bool masked, float f, float slope, float slope2, float base, Half half, First first) {
   auto far = [&](float l) { return w.live && !(l < pa::kMost) && w.l == w.l; };  // past the reference, or the first NaN
-  auto weights = [&](float (&x)[64], int h) {
-    if (MODE != kPlain || masked) pa_scores<MODE>(a, x, 64 * h, kb + 64 * h, see0, see1, masked, slope);
+#pragma unroll 1
+  for (int h = 0; h < 2; h++, base += 64.f * slope2) {
+    uint32_t r[64];
+    float (&x)[64] = reinterpret_cast<float (&)[64]>(r);
+    pa_tmem_ld(ts + 64 * h, r);
+    pa_wait_ld(r);
+    if (MODE != kPlain || masked) pa_scores<MODE>(a, x, kb + 64 * h, see0, see1, masked, slope);
     // the first keys that a row sees give its reference (nothing is held of it before)
     if (__any_sync(0xffffffffu, w.live && w.ref == -INFINITY)) {
       if (w.ref == -INFINITY) w.ref = fmaxf(fmaf(pa_max(x), f, base), -INFINITY);  // no NaN
@@ -407,7 +402,7 @@ __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, 
     float l;
 #pragma unroll 1
     for (;;) {
-      l = pa_weights(x, f, off(), ts + 32 * h);
+      l = pa_weights(x, f, w.ref == -INFINITY ? 0.f : base - w.ref, ts + 32 * h);
       if (!__any_sync(0xffffffffu, far(l))) break;
       if (h == 1) first();
       pa_grow<D>(w, to, fmaf(pa_max(x), f, base), h == 1 || w.done);
@@ -416,15 +411,7 @@ __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, 
     w.l += l;
     pa_wait_st();
     half(h);
-  };
-  weights(x0, 0);
-  if (MODE == kPlain) {
-    pa_wait_ld(r1);
-  } else {
-    pa_tmem_ld(ts + 64, r0);
-    pa_wait_ld(r0);
   }
-  weights(x1, 1);
   w.done = true;
 }
 
@@ -720,7 +707,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           wait(&s_full[t], sp);
           sp ^= 1;
           tc_fence_after();
-          pa_step<D, MODE>(a, row, ts, to, kb, see0, p, u < g0 || u >= g1, f, slope, MODE != kPlain ? slope2 * (float)(kb - p) : 0.f, [&](int h) {
+          pa_step<D, MODE>(a, row, ts, to, kb, see0, p, u < g0 || u >= g1, f, slope, slope2, MODE != kPlain ? slope2 * (float)(kb - p) : 0.f, [&](int h) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[2 * t + h]);

@@ -718,13 +718,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           hp ^= 1;
         }
       }
-      bool bad = false;
-      if (row.done) {
-        wait(&o_full[t], op);
-        op ^= 1;
-        tc_fence_after();
-        bad = *(volatile int*)&ctl.bad[some & 7];
-      }
+      // while the last product runs: sums and factors
       const bool whole = d.part < 0;
       const int64_t at = (int64_t)(d.tok + tok) * a.hq + d.h * a.G + idx % a.G;  // the row of out
       float* const part = a.part + (int64_t)d.part * S::kPart;
@@ -772,6 +766,13 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
         __syncwarp();
       };
       const bool some_sum = row.done && row.l != 0.f;
+      bool bad = false;
+      if (row.done) {
+        wait(&o_full[t], op);
+        op ^= 1;
+        tc_fence_after();
+        bad = *(volatile int*)&ctl.bad[some & 7];
+      }
       if (whole && !pair && row.done && !bad) {
 #pragma unroll 1
         for (int c = 0; c < D; c += 64) {

@@ -723,8 +723,8 @@ int sd_rope(const uint64_t* turns, float amplitude, int32_t head_dim, int32_t ro
  * kv_stride apart, each [n_kv_heads][head_dim]; all 16-byte aligned, strides
  * multiples of 8; head_dim 64 or 128; n_q_heads a multiple of n_kv_heads, at most
  * 128 query heads a kv head.
- * out: bf16 [rows][n_q_heads][head_dim], 16-byte aligned, 0 in a row that sees no
- * key; lse (optional): fp32 [rows][n_q_heads], the natural log of the sum of exp of
+ * out: bf16 [rows][n_q_heads][head_dim], 16-byte aligned, apart from q, k and v (units
+ * of rows run in any order), 0 in a row that sees no key; lse (optional): fp32 [rows][n_q_heads], the natural log of the sum of exp of
  * the scores, -inf in such a row.  Scores, sums and outputs are accumulated in
  * fp32; a softmax weight enters its product in bf16, as the output leaves.  What a
  * row does not see does not bear on it, a NaN or an infinity among it; rows behind
@@ -733,7 +733,7 @@ int sd_rope(const uint64_t* turns, float amplitude, int32_t head_dim, int32_t ro
  * that share one must not overlap.  *status (device int32, caller-owned) gets
  * SD_ERR_TIMEOUT where a bounded wait gave up.  Asynchronous on `stream`.  Errors:
  * SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED (head_dim, heads), SD_ERR_WORKSPACE,
- * SD_ERR_CUDA. */
+ * SD_ERR_OOM (host), SD_ERR_CUDA. */
 size_t sd_prompt_attn_workspace(int32_t head_dim);
 int sd_prompt_attn(const uint16_t* q, int64_t q_stride, int32_t n_q_heads, const uint16_t* k, const uint16_t* v,
                    int64_t kv_stride, int32_t n_kv_heads, int32_t head_dim, const int32_t* cu_q,

@@ -1109,6 +1109,13 @@ extern "C" int sd_prompt_attn(const uint16_t* q, int64_t q_stride, int32_t n_q_h
     return kv4_bad(SD_ERR_INVALID_ARG, who, "strides must cover a row and be multiples of 8");
   if (!workspace || ((uintptr_t)workspace & 255)) return kv4_bad(SD_ERR_INVALID_ARG, who, "workspace must be set and 256-byte aligned");
   if (workspace_bytes < sd_prompt_attn_workspace(head_dim)) return kv4_bad(SD_ERR_WORKSPACE, who, "workspace too small");
+  auto meets = [&](const uint16_t* x, int64_t n, int64_t stride, int heads) {  // out's rows and n of another tensor
+    const uintptr_t x0 = (uintptr_t)x, x1 = x0 + 2 * ((uintptr_t)(n - 1) * stride + (uintptr_t)heads * head_dim);
+    const uintptr_t o0 = (uintptr_t)out, o1 = o0 + 2 * (uintptr_t)rows * n_q_heads * head_dim;
+    return n > 0 && x0 < o1 && o0 < x1;
+  };
+  if (meets(q, rows, q_stride, n_q_heads) || meets(k, keys, kv_stride, n_kv_heads) || meets(v, keys, kv_stride, n_kv_heads))
+    return kv4_bad(SD_ERR_INVALID_ARG, who, "out overlaps q, k or v");
   if ((int64_t)rows * n_q_heads > 0x7FFFFFFF) return kv4_bad(SD_ERR_UNSUPPORTED, who, "more than 2^31 rows and heads");
   a.v = v, a.kv_stride = kv_stride;
   a.hq = n_q_heads, a.hkv = n_kv_heads, a.G = n_q_heads / n_kv_heads, a.R = R;

@@ -123,6 +123,20 @@ def test_prompt_refusals(L):
     assert L.sd_prompt_attn_workspace(96) == 0 and L.sd_prompt_attn_workspace(64) > 0
 
 
+def test_prompt_output_over_an_input(L):
+    """2 rows of 2 heads, 4 keys of 1: out over any part of q, k or v is refused."""
+    cu, ck = np.array([0, 2], np.int32), np.array([0, 4], np.int32)
+    q, k, vv = 4096, 8192, 12288  # 2 x 256 bytes; 4 rows of 128, 512 apart
+
+    def call(out):
+        v = lambda x: ctypes.c_void_p(x)  # noqa: E731
+        return L.sd_prompt_attn(v(q), 128, 2, v(k), v(vv), 256, 1, 64, v(256), cu.ctypes.data, v(256), ck.ctypes.data, 1, None, v(out),
+                                None, v(256), 1 << 40, None, None)
+
+    for out in (q, q - 496, q + 496, k, k + 3 * 512 + 112, k - 496, vv, vv + 3 * 512 + 112):
+        assert call(out) == 1 and b"overlaps" in L.sd_last_error(), out
+
+
 def test_prompt_binding_refuses(M):
     for a in ((8, 3, 64), (8, 2, 96), (0, 1, 64), (129, 1, 64)):
         with pytest.raises(ValueError):

@@ -42,8 +42,8 @@ constexpr int kKeys = 128;       // of a step
 constexpr int kMaxCta = 160;
 constexpr int kNK = 2, kNV = 2;  // stages of K and of V
 constexpr int kNU = 4;           // units being described
-constexpr float kLag = 8.f;
 constexpr float kMost = 0x1p20f;  // of a row's weights in half a step
+constexpr float kExact = 0x1p20f;  // offsets from references up to here are good to 2^-3
 constexpr int kXs = 20;          // floats of a row being exchanged (16 used)
 }  // namespace pa
 
@@ -358,11 +358,11 @@ __device__ __forceinline__ float pa_weights(const float (&x)[64], float f, float
   return l0 + l1;
 }
 
-// A greater reference for the rows that ask for one, O (where it holds anything) and
-// the sum with it.
+// A greater reference for the rows whose greatest score asks for one, O (where it holds
+// anything) and the sum with it.
 template <int D>
 __device__ __forceinline__ void pa_grow(PaRow& w, uint32_t to, float top, bool held) {
-  const bool grows = top > w.ref + pa::kLag;
+  const bool grows = top > w.ref;
   const float al = grows ? ex2(w.ref - top) : 1.f;
   if (grows) w.ref = top;
   w.l *= al;
@@ -395,18 +395,35 @@ __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, 
     pa_tmem_ld(ts + 64 * h, r);
     pa_wait_ld(r);
     if (MODE != kPlain || masked) pa_scores<MODE>(a, x, kb + 64 * h, see0, see1, masked, slope);
-    // the first keys that a row sees give its reference (nothing is held of it before)
-    if (__any_sync(0xffffffffu, w.live && w.ref == -INFINITY)) {
-      if (w.ref == -INFINITY) w.ref = fmaxf(fmaf(pa_max(x), f, base), -INFINITY);  // no NaN
+    // A row's reference is the greatest score of the first keys that it sees (nothing is
+    // held of it before).  Where it, or base, passes 2^20 its last place shows in the
+    // exponent, and a weight could be anything: such scores are rounded first, so that
+    // the greatest weighs 1.
+    auto large = [&]() { return !(fmaxf(fabsf(w.ref), fabsf(base)) <= pa::kExact); };  // or no reference yet
+    float l = 0.f;
+    bool done = false;
+    if (!__any_sync(0xffffffffu, w.live && large())) {
+      l = pa_weights(x, f, base - w.ref, ts + 32 * h);
+      done = !__any_sync(0xffffffffu, far(l));
+    } else if (w.ref == -INFINITY) {
+      w.ref = fmaxf(fmaf(pa_max(x), f, base), -INFINITY);  // no NaN
     }
-    float l;
+    if (__builtin_expect(!done, 0)) {
+      float fx = f, bx = base;
+      bool scored = false;
 #pragma unroll 1
-    for (;;) {
-      l = pa_weights(x, f, w.ref == -INFINITY ? 0.f : base - w.ref, ts + 32 * h);
-      if (!__any_sync(0xffffffffu, far(l))) break;
-      if (h == 1) first();
-      pa_grow<D>(w, to, fmaf(pa_max(x), f, base), h == 1 || w.done);
-      if (!(l == l)) w.l = l;
+      for (int again = 0;; again++) {  // the second time under the greatest score: l <= 2^7
+        if (!scored && large()) {
+#pragma unroll
+          for (int c = 0; c < 64; c++) x[c] = fmaf(x[c], f, base);
+          fx = 1.f, bx = 0.f, scored = true;
+        }
+        l = pa_weights(x, fx, w.ref == -INFINITY ? 0.f : bx - w.ref, ts + 32 * h);
+        if (again == 1 || !__any_sync(0xffffffffu, far(l))) break;
+        if (h == 1) first();
+        pa_grow<D>(w, to, fmaf(pa_max(x), fx, bx), h == 1 || w.done);
+        if (!(l == l)) w.l = l;
+      }
     }
     w.l += l;
     pa_wait_st();

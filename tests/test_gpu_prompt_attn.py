@@ -140,6 +140,39 @@ def test_scores_that_leap(M, at, d):
     same(out, lse, m, keys, q, k, v)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("power", [10, 18, 26, 55])
+def test_scores_whose_last_place_passes_an_exponent(M, power, d):
+    """Scores of 2^25 to 2^116: the last place of one is more than an exponent holds.  All
+    keys but one have one score: rows before it average what they see, the others take it,
+    and every weight is 0 or 1."""
+    m, keys = [300, 40], [300, 400]
+    _, _, v = inputs(m, keys, 4, 2, d, 9)
+    q = torch.full((340, 4, d), 3.0 * 2.0 ** power).bfloat16().cuda()
+    k = torch.full((700, 2, d), -1.5 * 2.0 ** power).bfloat16().cuda()
+    for j in (70, 300 + 377):
+        k[j] = 2.0 ** power
+    out, lse = run(M, m, keys, q, k, v)
+    f = lambda t: t.cpu().double()  # noqa: E731
+    want, want_lse, _, _ = ref.attend(f(q), f(k), f(v), np.cumsum([0] + m), np.cumsum([0] + keys))
+    assert torch.isfinite(out).all()
+    # the output in bf16, a sum of at most 400 values in fp32
+    assert ((f(out) - want).abs() <= ref.BF16 * want.abs() + 400 * 2.0 ** -24 * f(v).abs().max()).all()
+    assert ((f(lse) - want_lse).abs() <= 2.0 ** -20 * want_lse.abs()).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("slope", [1e10, 1e25])
+def test_slopes_that_leave_the_nearest_key(M, slope, d):
+    m, keys = [150, 3], [150, 300]
+    q, k, v = inputs(m, keys, 4, 2, d, 10)
+    slopes = torch.full((4,), slope)
+    out, lse = run(M, m, keys, q, k, v, M.KV4Score(slopes=slopes.cuda()))
+    own = torch.cat([v[:150], v[150 + 297:]]).repeat_interleave(2, 1)
+    assert torch.equal(out, own)
+    assert (lse.abs().cpu() <= 300 * slope * 2.0 ** -21 + 1e3).all()  # far keys' distance is taken off again
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("d", [64, 128])
 def test_bad_values_only_reach_the_rows_that_see_them(M, bad, d):

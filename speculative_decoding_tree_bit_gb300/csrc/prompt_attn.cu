@@ -15,7 +15,8 @@
 //    of the first half step in which it sees a key, and stays: weights, P and O may be
 //    large, not inaccurate.  Only where half a step's weights come to 2^20 is it raised
 //    and O rescaled in TMEM (looking for the maximum in every step: 177 us for 166 on
-//    8 prompts of 2048).
+//    8 prompts of up to 2048).  One body of code serves both halves of a step and all
+//    lengths (written out twice: 166 us for 139, and 181 for 133 with caps and a window).
 //  * 8, 9: the products of one group each: S = Q K^T and O += P V, those of one group
 //    while the other is in its softmax.  TMEM: [S 128][S 128][O D][O D].
 //  * 10: walks the CTA's units, says what each is (PaDesc), and loads Q, K and V by TMA.
@@ -24,6 +25,16 @@
 //    the rows that do see them get them back at the end.
 // The steps are dealt evenly over the CTAs, by the host (it has the lengths): a
 // unit may be split over its keys; its parts are joined by a second kernel.
+//
+// What bounds it: per group a round of scores (512 cycles of products at D = 128), the
+// softmax of 128 scores a thread, and the second half's product, one after the other;
+// two groups in turn make a step of two tiles in about 2600 cycles, of which 2048 are
+// products.  A softmax warp's instructions count (a step's 64 weights take 540 cycles
+// at 2.5 instructions each), not the exponential unit (ncu: 36%), and so does fetching
+// them: all of the loop stays small.  One GB300: 16384 rows, 32 query and 8 kv heads of
+// 128: 1340 us, 1640 TFLOP/s (0.85 of the measured cuBLAS burst, 0.94 of its sustained
+// rate); 8 prompts of up to 2048: 140 us; 512 rows over 33280 keys, 40 heads: 270 us; 16
+// single tokens over 1.5 to 8k keys, 68 us, 5.1 TB/s.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -878,7 +889,10 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
   }
 }
 
-// Joins the parts of the units that CTAs share, a warp a row, in CTA order.
+// Joins the parts of the units that CTAs share, a warp a row, in CTA order (so a call
+// gives the same bits every time): o = sum 2^(ref_c - ref) o_c / sum 2^(ref_c - ref) l_c.
+// Bound by the latency of the parts' loads, four parts of a row in flight: 16 us for 40 MB
+// when they are not in the L2 (they were written just before), 5 to 10 for fewer rows.
 template <int D>
 __global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ PaJoins jn, const int32_t* cu_q, int hq, int G, int T,
                                                      int U, const float* parts, uint16_t* out, float* lse) {
@@ -953,7 +967,10 @@ constexpr int kUnit = 8, kPiece = 4;
 
 static void pa_plan(PaPlan& pl, const int32_t* cu_q, const int32_t* cu_k, int R, int hkv, int T, int window, int ctas) {
   auto m_of = [&](int r) { return cu_q[r + 1] - cu_q[r]; };
-  // Few rows: a tile a unit, its keys shared by both groups.
+  // Few rows: a tile a unit, its keys shared by both groups, so that more CTAs have a unit's
+  // beginning and end (32 heads of 128: 512 rows 11.9 us for 13.0, 64 rows over 8192
+  // keys 23.4 for 24.4; over long contexts K and V are read more often, 512 rows over
+  // 8192 keys 63 for 59).
   int64_t wide_units = 0;
   for (int r = 0; r < R; r++) wide_units += (int64_t)hkv * ((m_of(r) + 2 * T - 1) / (2 * T));
   pl.U = wide_units * 2 <= ctas ? T : 2 * T;

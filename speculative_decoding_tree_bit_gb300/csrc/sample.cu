@@ -11,6 +11,12 @@
 //  * few rows: a cluster of up to 8 CTAs a row, 16-bit counters of all 65536 keys (so at
 //    most 65528 tokens a CTA), summed through distributed shared memory.
 //
+// What bounds them: of 256 rows of 151936 (78 MB; 57 us, 1.4 TB/s) the counting takes half,
+// 5.5 cycles a warp's atomic in shared memory with two CTAs an SM (bank conflicts of 32
+// random keys), the walk of one warp 15% by its latency, the look-up 10%.  With counters of
+// 16 bits and a cluster a row the same took 130 us.  One row (22 us, a cluster of 8): the latency of its phases and of three
+// cluster barriers.
+//
 // Weights are whole numbers, 2^44 exp((logit - most) / temperature), from pairs
 // of fp32 values good to about 2^-46, and their sums are 64-bit whole numbers (2^44
 // times 2^19 tokens): results do not depend on the order of a sum, and a u next
@@ -897,21 +903,37 @@ extern "C" int sd_sample(const uint16_t* logits, int64_t row_stride, int32_t row
   if ((uintptr_t)logits & 1) return sample_bad(SD_ERR_INVALID_ARG, "logits must be 2-byte aligned");
   const int vecs = (vocab + 7 + 7) / 8;  // a row may begin anywhere in its first vector
   auto slice = [&](int c) { return (vecs + c - 1) / c * 8; };
-  int C = 1;
-  while (slice(C) > sp::kSlice) C *= 2;
-  // few rows: more CTAs a row while each still has 4096 tokens
-  while (C < sp::kMaxCluster && (int64_t)rows * C * 2 <= num_sms() && vocab >= 4096 * 2 * C) C *= 2;
+  // clusters of 1, 2, 4 and 8 CTAs that the card holds at once (of 8 fewer than its SMs /
+  // 8: a cluster lies within one group of SMs)
+  static int held[4] = {};
   static const cudaError_t set = []() {
     const void* kerns[4] = {(const void*)k_sample<1>, (const void*)k_sample<2>, (const void*)k_sample<4>, (const void*)k_sample<8>};
     cudaError_t e = cudaFuncSetAttribute(k_sample_row, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(RowShared));
-    for (const void* k : kerns)
-      if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SampleShared));
+    for (int i = 0; i < 4; i++) {
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(kerns[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SampleShared));
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(1u << i), cfg.blockDim = dim3(sp::kThreads), cfg.dynamicSmemBytes = sizeof(SampleShared);
+      cudaLaunchAttribute at = {};
+      at.id = cudaLaunchAttributeClusterDimension;
+      at.val.clusterDim.x = 1u << i, at.val.clusterDim.y = at.val.clusterDim.z = 1;
+      cfg.attrs = &at, cfg.numAttrs = 1;
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&held[i], kerns[i], &cfg);
+    }
     return e;
   }();
   SD_CK(set);
+  auto at_once = [&](int c) { return held[c == 1 ? 0 : c == 2 ? 1 : c == 4 ? 2 : 3]; };
+  int C = 1;
+  while (slice(C) > sp::kSlice) C *= 2;
+  // few rows: more CTAs a row while each still has 4096 tokens and every row its cluster
+  while (C < sp::kMaxCluster && rows <= at_once(2 * C) && vocab >= 4096 * 2 * C) C *= 2;
   const SampleArgs a = {logits, row_stride, rows, vocab, slice(C), s, u, tokens, logprob, kept};
   cudaStream_t st = (cudaStream_t)stream;
-  const bool many = (int64_t)rows * C > num_sms();
+  // More rows than clusters at once, or a row of 16384 and not four CTAs for each: a CTA a row,
+  // two an SM.  151936 tokens: 8 rows 20 us by clusters of 8, 34 a CTA each, 32 rows 22 (by
+  // 4) and 34, 64 rows 41 and 34, 256 rows 142 and 51; 32000 tokens: 32 rows 17.4 (by 4)
+  // and 16.5, 64 rows 18.7 (by 2) and 16.3, 128 rows 20.7 (by 1) and 16.5.
+  const bool many = rows > at_once(C) || (C < 4 && vocab >= 4096 * 4);
   if (many) {
     k_sample_row<<<rows, sp::kRowThreads, sizeof(RowShared), st>>>(a);
     SD_CK(cudaGetLastError());

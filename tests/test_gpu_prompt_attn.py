@@ -109,6 +109,24 @@ def test_long_contexts(M):
     check(M, [40], [20000], 5, 1, 64, seed=5)
 
 
+def test_keys_past_32_bit_offsets(M):
+    """K and V of 2^31 elements and more: one token's greatest key near the end, the rest as one value."""
+    n, hkv, d = 2_200_000, 8, 128
+    k = torch.zeros(n, hkv, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.ones(n, hkv, d, dtype=torch.bfloat16, device="cuda")
+    k[n - 5], v[n - 5] = 4.0, -3.0  # score 4 sqrt(d): weight e^45 for 1
+    k[3], v[3] = 4.0, 5.0
+    q = torch.ones(1, 16, d).bfloat16().cuda()
+    out, lse = run(M, [1], [n], q, k, v)
+    x = 4 * math.sqrt(d)
+    # two equal weights of 1 - 2^-40: (5 - 3) / 2
+    assert (out.double() - 1.0).abs().max() <= ref.BF16
+    assert (lse.double() - (x + math.log(2.0))).abs().max() <= 2.0 ** -18 * x
+    window = M.KV4Score(window=1000)
+    out, lse = run(M, [1], [n], q, k, v, window)
+    assert (out.double() + 3.0).abs().max() <= 3 * ref.BF16
+
+
 def test_large_and_small_scores(M):
     """Softmax statistics over a wide range: a maximum that keeps growing, and one key that takes all."""
     m = keys = [400]

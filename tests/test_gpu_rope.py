@@ -105,6 +105,17 @@ def test_a_negative_position_turns_back_and_is_the_gradient(M):
         assert abs((f(z + e) - f(z - e)).item() / (2 * h) - by[at].item()) <= ref.BF16 * abs(by[at].item()) + 2.0 ** -17
 
 
+def test_rows_past_32_bit_offsets(M):
+    """2^31 elements and more, in place: the last rows as a call of their own turns them."""
+    op, n = M.Rope(128), 430_000
+    x = torch.randn(64, 40, 128, device="cuda").bfloat16().repeat(n // 64 + 1, 1, 1)[:n].contiguous()
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    last = x[-100:].clone()
+    want_q, want_k = op(last[:, :32], last[:, 32:], pos[-100:].clone())
+    op(x[:, :32], x[:, 32:], pos, q_out=x[:, :32], k_out=x[:, 32:])
+    assert torch.equal(x[-100:, :32], want_q) and torch.equal(x[-100:, 32:], want_k)
+
+
 def test_graph_and_stream(M):
     op = M.Rope()
     q, k, pos = rows(33, 8, 128, 1), rows(33, 2, 128, 2), torch.arange(33, dtype=torch.int32).cuda()

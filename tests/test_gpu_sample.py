@@ -142,6 +142,20 @@ def test_long_rows_one_cta_each(M):
     assert torch.equal(got["tokens"], want) and (got["kept"] == 140000).all()
 
 
+@pytest.mark.parametrize("special", [False, True])
+def test_rows_past_32_bit_offsets(M, special):
+    """2^31 elements and more: the last rows as a call of their own samples them."""
+    V, n = 151936, 14200
+    row, u = normal(40, V, seed=31)
+    if special:  # magnitudes that the kernel of many rows leaves to the other one
+        row[7::13, 5] = 1e30
+    x = row.repeat(n // 40, 1)
+    us = u.repeat(n // 40)
+    got, want = M.sample(x, us, temperature=0.9, top_p=0.95), M.sample(row, u, temperature=0.9, top_p=0.95)
+    for k in want:
+        assert torch.equal(got[k].reshape(-1, 40), want[k].expand(n // 40, 40)), k
+
+
 def test_u_is_clamped(M):
     x, _ = normal(5, 300, seed=2)
     u = torch.tensor([-1.0, math.nan, 1.0, 7.0, math.inf]).cuda()

@@ -2,14 +2,14 @@
 //
 //   o_i = sum_j exp(s_ij - lse_i) v_j,  s_ij = q_i . k_j scale over the keys j that row
 //   i sees,
-// in one pass over the keys with a row's running maximum and sum.  The rows of a kv
+// in one pass over the keys with a row's reference and running sum.  The rows of a kv
 // head's query heads are packed, token by token, into tiles of 128 (T = 128 / G tokens
 // of G heads), so that K and V are read once for the group and a single token fills G
 // rows.  A unit is a kv head and 2 T tokens (two tiles, WIDE) or up to T (one); its
 // steps are 128 keys, the last ones first: a row meets its own and the nearest keys at
 // once, which with slopes are the greatest scores.  Warps:
-//  * 0..3 and 4..7: softmax, a thread a row: 128 scores from TMEM, maximum,
-//    exponentials, P (bf16) back over its scores; then the outputs.  A wide unit
+//  * 0..3 and 4..7: softmax, a thread a row: 128 scores from TMEM, their
+//    exponentials, P (bf16) back over them; then the outputs.  A wide unit
 //    gives each of the two groups a tile of rows, a narrow one alternate steps of the
 //    same rows, joined through shared memory.  A row's reference is the greatest score
 //    of the first half step in which it sees a key, and stays: weights, P and O may be
@@ -34,7 +34,7 @@
 // them: all of the loop stays small.  One GB300: 16384 rows, 32 query and 8 kv heads of
 // 128: 1340 us, 1640 TFLOP/s (0.85 of the measured cuBLAS burst, 0.94 of its sustained
 // rate); 8 prompts of up to 2048: 140 us; 512 rows over 33280 keys, 40 heads: 270 us; 16
-// single tokens over 1.5 to 8k keys, 68 us, 5.1 TB/s.
+// single tokens over 1.5 to 8k keys: 66 us, 5.2 TB/s.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -891,12 +891,12 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
 
 // Joins the parts of the units that CTAs share, a warp a row, in CTA order (so a call
 // gives the same bits every time): o = sum 2^(ref_c - ref) o_c / sum 2^(ref_c - ref) l_c.
-// Bound by the latency of the parts' loads, four parts of a row in flight: 16 us for 40 MB
-// when they are not in the L2 (they were written just before), 5 to 10 for fewer rows.
+// Bound by the latency of the parts' loads, four parts of a row in flight: 12.7
+// us for the 40 MB of 151 split units with a cold L2 (they were written just before), 4.5
+// to 10 for fewer; with a pass of its own for the maximum 16.9 and 5.3 to 12.9.
 template <int D>
 __global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ PaJoins jn, const int32_t* cu_q, int hq, int G, int T,
                                                      int U, const float* parts, uint16_t* out, float* lse) {
-  pdl_wait();
   const PaAt b = jn.at[blockIdx.x];
   const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5);  // tile * 128 + row of it
   const int q0 = cu_q[b.r], m = cu_q[b.r + 1] - q0, tc = min(U, m - b.i * U);
@@ -905,11 +905,8 @@ __global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ PaJ
   const int head = b.h * G + idx - tk * G;
   const int c0 = jn.cta[blockIdx.x], n = b.step;
   auto part_of = [&](int p) { return parts + (int64_t)(p == 0 ? 2 * c0 + 1 : 2 * (c0 + p)) * PaShape<D>::kPart; };
+  pdl_wait();  // up to here only what the first kernel does not write
   float M = -INFINITY, L = 0.f;
-  for (int p = lane; p < n; p += 32) M = fmaxf(M, __ldcg(part_of(p) + 256 * D + 2 * row));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float Ms = M == -INFINITY ? 0.f : M;
   constexpr int kF = D / 32;
   float acc[kF] = {};
   for (int c = 0; c < n; c += 4) {
@@ -917,7 +914,9 @@ __global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ PaJ
     float v[4][kF];
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-      const float* pc = part_of(min(c + k, n - 1));
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (c + k >= n) continue;
+      const float* pc = part_of(c + k);
       ml[k] = __ldcg(reinterpret_cast<const float2*>(pc + 256 * D) + row);
       if constexpr (kF == 4) {
         const float4 u = __ldcg(reinterpret_cast<const float4*>(pc + (int64_t)row * D) + lane);
@@ -927,9 +926,17 @@ __global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ PaJ
         v[k][0] = u.x, v[k][1] = u.y;
       }
     }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < 4; k++) top = fmaxf(top, ml[k].x);
+    const float Ms = top == -INFINITY ? 0.f : top, al = ex2(M - Ms);
+    M = top;
+    L *= al;
+#pragma unroll
+    for (int q = 0; q < kF; q++) acc[q] *= al;
 #pragma unroll
     for (int k = 0; k < 4; k++)
-      if (c + k < n && !(ml[k].y == 0.f)) {
+      if (!(ml[k].y == 0.f)) {
         const float f = ex2(ml[k].x - Ms);
         L = fmaf(f, ml[k].y, L);
 #pragma unroll

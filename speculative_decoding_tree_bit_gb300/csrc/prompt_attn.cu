@@ -34,7 +34,7 @@
 // them: all of the loop stays small.  One GB300: 16384 rows, 32 query and 8 kv heads of
 // 128: 1340 us, 1640 TFLOP/s (0.85 of the measured cuBLAS burst, 0.94 of its sustained
 // rate); 8 prompts of up to 2048: 140 us; 512 rows over 33280 keys, 40 heads: 270 us; 16
-// single tokens over 1.5 to 8k keys: 66 us, 5.2 TB/s.
+// single tokens over 1.5 to 8k keys: 68 us, 5.1 TB/s.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -465,6 +465,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
   uint64_t* const h_full = p_full + 4;             // [t] the product of P's first half done (commit)
   uint64_t* const o_full = h_full + 2;             // [t] a unit's last product done (commit)
   uint64_t* const o_empty = o_full + 2;            // [t] outputs read (4 warps)
+  uint64_t* const x_full = o_empty + 2;            // groups that share rows meet (8 warps)
   PaCtl& ctl = *reinterpret_cast<PaCtl*>(sm + S::off_ctl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch();
@@ -482,6 +483,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
       mbar_init(&s_full[t], 1), mbar_init(&h_full[t], 1), mbar_init(&o_full[t], 1), mbar_init(&o_empty[t], 4);
       mbar_init(&p_full[2 * t], 4), mbar_init(&p_full[2 * t + 1], 4);
     }
+    mbar_init(x_full, 8);
     ctl.abort = ctl.turn = 0;
     fence_mbar_init();
   }
@@ -710,7 +712,16 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
     const uint32_t ts = tm + t * 128 + lanes, to = tm + 256 + t * 128 + lanes;
     const float f = MODE == kCapped ? 1.f : a.s.scale * kLog2e;  // base 2 from a capped score, or from q.k
     const int tok_of = idx / a.G;
-    uint32_t some = 0, sp = 0, hp = 0, op = 0;  // units with steps; parities of s_full, h_full and o_full
+    uint32_t some = 0, sp = 0, hp = 0, op = 0, xp = 0;  // units with steps; parities of s_full, h_full, o_full and x_full
+    // not a named barrier: after a wait that gave up the warps may differ in their units.
+    // Within a limit, because every other wait of the warps to come is
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x_full);
+      while (!mbar_try_wait(smem_u32(x_full), xp) && !*(volatile int*)&ctl.abort) {
+      }
+      xp ^= 1;
+    };
 #pragma unroll 1
     for (uint32_t i = 0;; i++) {
       const PaDesc& d = ctl.unit[i % pa::kNU];
@@ -755,7 +766,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
       if (pair) {
         float2* const s_ml = reinterpret_cast<float2*>(sm + S::off_ml);
         if (t == 1) s_ml[idx] = make_float2(row.ref, row.l);
-        bar_sync(1, 256);
+        meet();
         if (t == 0) {
           const float2 ml = s_ml[idx];
           M = fmaxf(row.ref, ml.x);
@@ -844,7 +855,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
 #pragma unroll
               for (int e = 0; e < 4; e++) xr[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
-            bar_sync(1, 256);
+            meet();
             if (t == 0) {
 #pragma unroll
               for (int e = 0; e < 4; e++) {
@@ -855,7 +866,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
                 o[4 * e + 3] = fmaf(other, v.w, mine * o[4 * e + 3]);
               }
             }
-            bar_sync(1, 256);
+            meet();
           }
           if (!writes) continue;
           if (whole) {

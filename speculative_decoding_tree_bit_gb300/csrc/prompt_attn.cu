@@ -573,9 +573,15 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           const int by = d.wide ? 1 : 2, x = d.x[t] - d.ua, y = d.y[t] - d.ua, m0 = d.m0 - d.ua, m1 = d.m1 - d.ua;
           const uint64_t qd = sdesc_sw128(smem_u32(sm + (d.wide ? t : 0) * S::kTile));
           // A wide unit's stages are released by both groups, those that one of them has no use
-          // for too (so it never misses a phase of their barriers); a narrow unit's by the
-          // one group that uses them, in the other's name as well.
-          int k = 0, v = 0;  // a wide unit's steps whose K and V are taken
+          // for too; a narrow unit's by the one group that uses them, in the other's name as
+          // well.  A wait for a phase is one only while the phase before it is known to be
+          // over, and may not come two phases late: no group may lose sight of a stage.  A
+          // narrow unit of several steps keeps both in sight: its Q is released after its
+          // outputs, so the next unit's is not there before all of its stages were used.  One
+          // of a single step releases Q once K is used, ahead of its V: the group without a
+          // step waits for that V, and releases it, itself.
+          const bool both = by == 1 || n == 1;  // V is released by both groups
+          int k = 0, v = 0;  // steps whose K (wide units') and V (both groups') are taken
           auto pass_k = [&](int u) {
 #pragma unroll 1
             for (; by == 1 && k < u; k++) {
@@ -585,7 +591,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           };
           auto pass_v = [&](int u) {
 #pragma unroll 1
-            for (; by == 1 && v < u; v++) {
+            for (; both && v < u; v++) {
               wait(&v_full[(nv + v) % pa::kNV], (nv + v) / pa::kNV);
               mbar_arrive(&v_empty[(nv + v) % pa::kNV]);
             }
@@ -643,14 +649,14 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
             else umma_commit(&o_full[t]);
             if (u >= x) {
               umma_commit(&v_empty[vs]);
-              if (by == 2) mbar_arrive(&v_empty[vs]);
+              if (!both) mbar_arrive(&v_empty[vs]);
               v++;
             }
             atomicExch(&ctl.turn, 0);
           }
+          if (x >= y) mbar_arrive(q_empty);
           pass_k(n);
           pass_v(n);
-          if (x >= y) mbar_arrive(q_empty);
           mbar_arrive(&u_empty[i % pa::kNU]);
           nk += n, nv += n;
           units++;

@@ -103,6 +103,18 @@ def test_many_requests_of_few_rows(M, d):
     check(M, m, keys, 4, 1, d, seed=2)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_single_rows_over_one_and_few_steps_of_keys(M, d):
+    """Units of one step of 128 keys and of two or three behind one another in a CTA: only one of the
+    two groups of rows has a use for the first one's values, and both for the next one's."""
+    keys = [(1 + 37 * i % 128, 129 + 91 * i % 256, 1 + 53 * i % 128, 257 + 29 * i % 128, 513 + i % 7)[i % 5] for i in range(900)]
+    check(M, [1] * 900, keys, 2, 1, d, seed=21)
+    # between prompts, whose units hold two tiles
+    m = [1, 1, 300, 1, 1, 1, 129] * 40
+    keys = [m[i] + (0, 200, 0, 100, 380, 17, 260)[i % 7] for i in range(280)]
+    check(M, m, keys, 2, 1, d, seed=22)
+
+
 def test_long_contexts(M):
     """Work split over the keys and joined; far offsets."""
     check(M, [2, 1], [20011, 9000], 4, 1, 128, seed=4)

@@ -726,7 +726,11 @@ int sd_rope(const uint64_t* turns, float amplitude, int32_t head_dim, int32_t ro
  * out: bf16 [rows][n_q_heads][head_dim], 16-byte aligned, apart from q, k and v (units
  * of rows run in any order), 0 in a row that sees no key; lse (optional): fp32 [rows][n_q_heads], the natural log of the sum of exp of
  * the scores, -inf in such a row.  Scores, sums and outputs are accumulated in
- * fp32; a softmax weight enters its product in bf16, as the output leaves.  What a
+ * fp32; a softmax weight enters its product in bf16, as the output leaves.  Values of
+ * up to 2^127 in size give finite outputs (scores up to 2^24; past those, where a score's
+ * last place is more than the weights have room for, up to 2^127 over the number of keys);
+ * those below 2^-120 lose bits; a weight below 2^-100 of the row's greatest may count as
+ * 0.  What a
  * row does not see does not bear on it, a NaN or an infinity among it; rows behind
  * cu_q[R] are left as they were.
  * workspace: sd_prompt_attn_workspace bytes, 256-byte aligned, any content; calls

@@ -11,12 +11,14 @@
 //  * 0..3 and 4..7: softmax, a thread a row: 128 scores from TMEM, their
 //    exponentials, P (bf16) back over them; then the outputs.  A wide unit
 //    gives each of the two groups a tile of rows, a narrow one alternate steps of the
-//    same rows, joined through shared memory.  A row's reference is the greatest score
-//    of the first half step in which it sees a key, and stays: weights, P and O may be
-//    large, not inaccurate.  Only where half a step's weights come to 2^20 is it raised
-//    and O rescaled in TMEM (looking for the maximum in every step: 177 us for 166 on
-//    8 prompts of up to 2048).  One body of code serves both halves of a step and all
-//    lengths (written out twice: 166 us for 139, and 181 for 133 with caps and a window).
+//    same rows, joined through shared memory.  A row's weights are 2^(score - reference),
+//    the reference kBias above the greatest score of the first half step in which the
+//    row sees a key; it stays, and only where the weights would come to 1/2 in all is it
+//    raised and O rescaled in TMEM (looking for the maximum in every step: 177 us for
+//    166 on 8 prompts of up to 2048).  So O never passes the greatest value of the row's
+//    keys, and fp32 holds it down to the bias.  One body of code serves both halves of a
+//    step and all lengths (written out twice: 166 us for 139, and 181 for 133 with caps
+//    and a window).
 //  * 8, 9: the products of one group each: S = Q K^T and O += P V, those of one group
 //    while the other is in its softmax.  TMEM: [S 128][S 128][O D][O D].
 //  * 10: walks the CTA's units, says what each is (PaDesc), and loads Q, K and V by TMA.
@@ -53,7 +55,11 @@ constexpr int kKeys = 128;       // of a step
 constexpr int kMaxCta = 160;
 constexpr int kNK = 2, kNV = 2;  // stages of K and of V
 constexpr int kNU = 4;           // units being described
-constexpr float kMost = 0x1p20f;  // of a row's weights in half a step
+constexpr float kMost = 0.5f;    // of a row's weights so far
+// Of a reference over a score: a value of 2^-126 has 8 bits left (O is held in multiples
+// of 2^-149).  8 prompts of up to 2048 take 151 us with 11, 148 with 13, 144 with 15 and
+// 143 with 17; one of 16384 1473, 1377, 1347 and 1347.
+constexpr float kBias = 15.f;
 constexpr float kExact = 0x1p20f;  // offsets from references up to here are good to 2^-3
 constexpr int kXs = 20;          // floats of a row being exchanged (16 used)
 }  // namespace pa
@@ -369,8 +375,8 @@ __device__ __forceinline__ float pa_weights(const float (&x)[64], float f, float
   return l0 + l1;
 }
 
-// A greater reference for the rows whose greatest score asks for one, O (where it holds
-// anything) and the sum with it.
+// The reference raised to `top` where that is greater, O (where it holds anything) and
+// the sum with it.
 template <int D>
 __device__ __forceinline__ void pa_grow(PaRow& w, uint32_t to, float top, bool held) {
   const bool grows = top > w.ref;
@@ -398,7 +404,7 @@ __device__ __forceinline__ void pa_grow(PaRow& w, uint32_t to, float top, bool h
 template <int D, int MODE, typename Half, typename First>
 __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, uint32_t to, int kb, int see0, int see1,
                                         bool masked, float f, float slope, float slope2, float base, Half half, First first) {
-  auto far = [&](float l) { return w.live && !(l < pa::kMost) && w.l == w.l; };  // past the reference, or the first NaN
+  auto far = [&](float l) { return w.live && !(w.l + l < pa::kMost) && w.l == w.l; };  // too much, or the first NaN
 #pragma unroll 1
   for (int h = 0; h < 2; h++, base += 64.f * slope2) {
     uint32_t r[64];
@@ -406,10 +412,10 @@ __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, 
     pa_tmem_ld(ts + 64 * h, r);
     pa_wait_ld(r);
     if (MODE != kPlain || masked) pa_scores<MODE>(a, x, kb + 64 * h, see0, see1, masked, slope);
-    // A row's reference is the greatest score of the first keys that it sees (nothing is
-    // held of it before).  Where it, or base, passes 2^20 its last place shows in the
+    // A row's reference goes by the greatest score of the first keys that it sees (nothing
+    // is held of it before).  Where it, or base, passes 2^20 its last place shows in the
     // exponent, and a weight could be anything: such scores are rounded first, so that
-    // the greatest weighs 1.
+    // the greatest weighs 2^-kBias, or 1 where the bias is less than a last place.
     auto large = [&]() { return !(fmaxf(fabsf(w.ref), fabsf(base)) <= pa::kExact); };  // or no reference yet
     float l = 0.f;
     bool done = false;
@@ -417,13 +423,13 @@ __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, 
       l = pa_weights(x, f, base - w.ref, ts + 32 * h);
       done = !__any_sync(0xffffffffu, far(l));
     } else if (w.ref == -INFINITY) {
-      w.ref = fmaxf(fmaf(pa_max(x), f, base), -INFINITY);  // no NaN
+      w.ref = fmaxf(fmaf(pa_max(x), f, base), -INFINITY) + pa::kBias;  // no NaN
     }
     if (__builtin_expect(!done, 0)) {
       float fx = f, bx = base;
       bool scored = false;
 #pragma unroll 1
-      for (int again = 0;; again++) {  // the second time under the greatest score: l <= 2^7
+      for (int again = 0;; again++) {  // the second time under a reference that holds them
         if (!scored && large()) {
 #pragma unroll
           for (int c = 0; c < 64; c++) x[c] = fmaf(x[c], f, base);
@@ -432,7 +438,10 @@ __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, 
         l = pa_weights(x, fx, w.ref == -INFINITY ? 0.f : bx - w.ref, ts + 32 * h);
         if (again == 1 || !__any_sync(0xffffffffu, far(l))) break;
         if (h == 1) first();
-        pa_grow<D>(w, to, fmaf(pa_max(x), fx, bx), h == 1 || w.done);
+        // by the greatest score, and by what has come together (of any row within 2^4 of the
+        // limit, so that a warp seldom comes here)
+        const float top = fmaf(pa_max(x), fx, bx) + pa::kBias;
+        pa_grow<D>(w, to, w.l + l >= pa::kMost / 16 ? fmaxf(top, w.ref + 10.f) : top, h == 1 || w.done);
         if (!(l == l)) w.l = l;
       }
     }
@@ -923,6 +932,8 @@ __global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ PaJ
   const int c0 = jn.cta[blockIdx.x], n = b.step;
   auto part_of = [&](int p) { return parts + (int64_t)(p == 0 ? 2 * c0 + 1 : 2 * (c0 + p)) * PaShape<D>::kPart; };
   pdl_wait();  // up to here only what the first kernel does not write
+  // a part's weights come to less than 1/2: those of n parts are scaled so that they all do
+  const float share = (float)(32 - __clz(n - 1));
   float M = -INFINITY, L = 0.f;
   constexpr int kF = D / 32;
   float acc[kF] = {};
@@ -954,7 +965,7 @@ __global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ PaJ
 #pragma unroll
     for (int k = 0; k < 4; k++)
       if (!(ml[k].y == 0.f)) {
-        const float f = ex2(ml[k].x - Ms);
+        const float f = ex2(ml[k].x - Ms - share);
         L = fmaf(f, ml[k].y, L);
 #pragma unroll
         for (int q = 0; q < kF; q++) acc[q] = fmaf(f, v[k][q], acc[q]);
@@ -965,7 +976,7 @@ __global__ void __launch_bounds__(256) k_prompt_join(const __grid_constant__ PaJ
   uint32_t* dst = reinterpret_cast<uint32_t*>(out + at * D) + lane * (kF / 2);
 #pragma unroll
   for (int q = 0; q < kF; q += 2) dst[q / 2] = pa_bf16x2(acc[q] * inv, acc[q + 1] * inv);
-  if (lane == 0 && lse) lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
+  if (lane == 0 && lse) lse[at] = L == 0.f ? -INFINITY : (M + (log2f(L) + share)) * (1.f / kLog2e);
 }
 
 // ------------------------------------------------------------------ host --

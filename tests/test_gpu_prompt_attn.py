@@ -192,6 +192,43 @@ def test_scores_whose_last_place_passes_an_exponent(M, power, d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [1e30, 1e34, 1e36, 1e38])
+@pytest.mark.parametrize("m,n", [(1, 128), (300, 300), (40, 1000), (3, 40000)])
+def test_finite_values_give_finite_outputs(M, d, size, m, n):
+    """Values of one sign and of both near the type's end, under equal weights and under keys of a later
+    half step that weigh 2^7, 2^18.8 and 2^20 times the first ones."""
+    g = torch.Generator().manual_seed(n)
+    q = torch.ones(m, 2, d).bfloat16().cuda()
+    values = ((0.5 + 0.5 * torch.rand(n, 1, d, generator=g)) * size).bfloat16()
+    signs = torch.sign(torch.randn(n, 1, d, generator=g)).bfloat16()
+    for at in (0.0, 5.0, 13.0, 14.0):
+        k = torch.zeros(n, 1, d).bfloat16()
+        k[100::128] = at / math.sqrt(d)
+        for v in (values, values * signs):
+            out, lse = run(M, [m], [n], q, k.cuda(), v.cuda())
+            same(out, lse, [m], [n], q, k, v)
+    slopes, score = torch.tensor([0.5, -0.01]), dict(cap=20.0, window=600)
+    out, lse = run(M, [m], [n], q, k.cuda(), v.cuda(), M.KV4Score(softcap=20.0, slopes=slopes.cuda(), window=600))
+    same(out, lse, [m], [n], q, k, v, slopes=slopes, **score)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [1e-30, 1e-34, 1e-36])
+@pytest.mark.parametrize("m,n", [(1, 128), (300, 300), (3, 40000)])
+def test_small_values_keep_their_bits(M, d, size, m, n):
+    """An output relative to its own size, all values positive: both roundings (2^-8) and the fp32 steps
+    (request_ref), and of the sums, held in multiples of 2^-149, eight a half step's product: a row's weights
+    come to 2^-15 at least."""
+    q, k, _ = inputs([m], [n], 2, 1, d, 3)
+    v = ((0.5 + 0.5 * torch.rand(n, 1, d, generator=torch.Generator().manual_seed(n))) * size).bfloat16().cuda()
+    out, lse = run(M, [m], [n], q, k, v)
+    f = lambda t: t.cpu().double()  # noqa: E731
+    want, _, tol, _ = ref.attend(f(q), f(k), f(v), [0, m], [0, n])
+    lost = 2.0 ** -149 * 8 * (n // 64 + 2) * 2.0 ** 15
+    assert ((f(out) - want).abs() <= tol - 2.0 ** -130 + lost).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("slope", [1e10, 1e25])
 def test_slopes_that_leave_the_nearest_key(M, slope, d):
     m, keys = [150, 3], [150, 300]

@@ -66,6 +66,12 @@ const char* sd_version(void);
  * *status (device int32, caller-owned, not cleared here) to SD_ERR_TIMEOUT.
  * Errors: SD_ERR_INVALID_ARG, SD_ERR_CUDA (launch). */
 int sd_debug_bounded_wait(int32_t* status, int64_t limit_ns, int32_t which, void* stream);
+/* The same inside sd_prompt_attn: in this process's calls from now on a wait gives up after
+ * limit_ns, and a thread block loads the values of at most `loads` steps of keys, so that
+ * one with more to do waits for what does not come; its kernel then ends, with what it has
+ * under way, as after any wait that gave up.  limit_ns 0: as before.  Errors:
+ * SD_ERR_INVALID_ARG (limit_ns past 2 s or negative, loads negative). */
+int sd_debug_prompt_wait(int64_t limit_ns, int64_t loads);
 
 /* Event log of the streamed W12 GEMM launches (diagnostics: where a launch
  * of several GEMMs spends its time).  While a buffer is set (device memory,

@@ -89,6 +89,7 @@ _SIGS = {
     "sd_last_error": (ctypes.c_char_p, []),
     "sd_version": (ctypes.c_char_p, []),
     "sd_debug_bounded_wait": (ctypes.c_int, [vp, i64, i32, vp]),
+    "sd_debug_prompt_wait": (ctypes.c_int, [i64, i64]),
     "sd_stream_set_trace": (ctypes.c_int, [vp, i64]),
     "sd_attn_set_trace": (ctypes.c_int, [vp, i64]),
     "sd_stream_trace_launches": (i32, []),

@@ -40,6 +40,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <vector>
 
@@ -82,6 +83,8 @@ struct PaArgs {
   float* lse;
   float* part;
   int32_t* status;
+  uint32_t limit;  // of a wait, in ns
+  uint32_t loads;  // steps' values that a CTA loads at most: all, but for sd_debug_prompt_wait
   // cap tanh(x scale / cap) log2(e) = x (k0 + k1 x^2 + ... + k4 x^8) while |x| <= series
   float k0, k1, k2, k3, k4, series;
 };
@@ -122,6 +125,7 @@ struct PaDesc {
 struct PaCtl {
   PaDesc unit[pa::kNU];
   int abort, turn;     // turn: 1 while a group's products are being issued
+  int late;            // as abort, of what is waited for at the end
   uint32_t tmem;
   int bad[8];          // [unit with steps, mod 8]: infinities or NaNs were taken out of V
 };
@@ -273,16 +277,24 @@ __device__ __forceinline__ uint64_t pa_sdesc_v(uint32_t saddr) {
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+__device__ __forceinline__ uint32_t pa_clock() {  // ns, mod 2^32
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+
 // A bounded wait in few instructions (all of the kernel's code has to stay in the
-// instruction cache): past the limit it sets *abort, which ends every wait.
-__device__ __forceinline__ void pa_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+// instruction cache): past the limit it sets *abort, which ends every wait.  What a warp
+// does after a wait that gave up stays within its buffers and its unit's rows: it goes by
+// a PaDesc that was written, and no other is written from then on.
+__device__ __forceinline__ void pa_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t limit) {
   if (mbar_try_wait(bar, parity)) return;
-  const uint64_t t0 = globaltimer();
+  const uint32_t t0 = pa_clock();
 #pragma unroll 1
   for (uint32_t i = 1; !mbar_try_wait(bar, parity); i++) {
     if (i % 64) continue;  // a try suspends the warp for a while by itself
     if (*abort) return;
-    if (globaltimer() - t0 > kWaitLimitNs) *abort = 1;
+    if (pa_clock() - t0 > limit) *abort = 1;
   }
 }
 
@@ -417,32 +429,54 @@ __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, 
     // exponent, and a weight could be anything: such scores are rounded first, so that
     // the greatest weighs 2^-kBias, or 1 where the bias is less than a last place.
     auto large = [&]() { return !(fmaxf(fabsf(w.ref), fabsf(base)) <= pa::kExact); };  // or no reference yet
-    float l = 0.f;
-    bool done = false;
-    if (!__any_sync(0xffffffffu, w.live && large())) {
-      l = pa_weights(x, f, base - w.ref, ts + 32 * h);
-      done = !__any_sync(0xffffffffu, far(l));
-    } else if (w.ref == -INFINITY) {
-      w.ref = fmaxf(fmaf(pa_max(x), f, base), -INFINITY) + pa::kBias;  // no NaN
-    }
-    if (__builtin_expect(!done, 0)) {
-      float fx = f, bx = base;
-      bool scored = false;
-#pragma unroll 1
-      for (int again = 0;; again++) {  // the second time under a reference that holds them
-        if (!scored && large()) {
+    float l = 0.f, fx = f, bx = base;  // a score is fx x + bx
+    auto reference = [&]() { w.ref = fmaxf(fmaf(pa_max(x), fx, bx), -INFINITY) + pa::kBias; };  // no NaN
+    auto round = [&]() {
 #pragma unroll
-          for (int c = 0; c < 64; c++) x[c] = fmaf(x[c], f, base);
-          fx = 1.f, bx = 0.f, scored = true;
+      for (int c = 0; c < 64; c++) x[c] = fmaf(x[c], fx, bx);
+      fx = 1.f, bx = 0.f;
+    };
+    auto weights = [&]() { l = pa_weights(x, fx, w.ref == -INFINITY ? 0.f : bx - w.ref, ts + 32 * h); };
+    auto raise = [&]() {
+      if (h == 1) first();
+      // by the greatest score, and by what has come together (of any row within 2^4 of the
+      // limit, so that a warp seldom comes here)
+      const float top = fmaf(pa_max(x), fx, bx) + pa::kBias;
+      pa_grow<D>(w, to, w.l + l >= pa::kMost / 16 ? fmaxf(top, w.ref + 10.f) : top, h == 1 || w.done);
+      if (!(l == l)) w.l = l;
+    };
+    // At most two passes: the second is under a reference that holds the weights.  Without
+    // options the usual pass has a body of its own (one prompt of 16384: 1345 us, 1430
+    // without); with them the instructions fetched count more (5 ragged prompts with cap,
+    // slopes and a window: 164 us with it, 138 without).
+    if (MODE == kPlain) {
+      bool done = false;
+      if (!__any_sync(0xffffffffu, w.live && large())) {
+        l = pa_weights(x, f, base - w.ref, ts + 32 * h);
+        done = !__any_sync(0xffffffffu, far(l));
+      } else if (w.ref == -INFINITY) {
+        reference();
+      }
+      if (__builtin_expect(!done, 0)) {
+        bool rounded = false;
+#pragma unroll 1
+        for (int again = 0;; again++) {
+          if (!rounded && large()) round(), rounded = true;
+          weights();
+          if (again == 1 || !__any_sync(0xffffffffu, far(l))) break;
+          raise();
         }
-        l = pa_weights(x, fx, w.ref == -INFINITY ? 0.f : bx - w.ref, ts + 32 * h);
+      }
+    } else {
+#pragma unroll 1
+      for (int again = 0;; again++) {
+        if (__any_sync(0xffffffffu, w.live && large())) {
+          if (w.ref == -INFINITY) reference();
+          if (large()) round();  // what is rounded stays as it is
+        }
+        weights();
         if (again == 1 || !__any_sync(0xffffffffu, far(l))) break;
-        if (h == 1) first();
-        // by the greatest score, and by what has come together (of any row within 2^4 of the
-        // limit, so that a warp seldom comes here)
-        const float top = fmaf(pa_max(x), fx, bx) + pa::kBias;
-        pa_grow<D>(w, to, w.l + l >= pa::kMost / 16 ? fmaxf(top, w.ref + 10.f) : top, h == 1 || w.done);
-        if (!(l == l)) w.l = l;
+        raise();
       }
     }
     w.l += l;
@@ -475,6 +509,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
   uint64_t* const o_full = h_full + 2;             // [t] a unit's last product done (commit)
   uint64_t* const o_empty = o_full + 2;            // [t] outputs read (4 warps)
   uint64_t* const x_full = o_empty + 2;            // groups that share rows meet (8 warps)
+  uint64_t* const t_done = x_full + 1;             // [t] all of a group's products done (commit)
   PaCtl& ctl = *reinterpret_cast<PaCtl*>(sm + S::off_ctl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch();
@@ -492,23 +527,24 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
       mbar_init(&s_full[t], 1), mbar_init(&h_full[t], 1), mbar_init(&o_full[t], 1), mbar_init(&o_empty[t], 4);
       mbar_init(&p_full[2 * t], 4), mbar_init(&p_full[2 * t + 1], 4);
     }
-    mbar_init(x_full, 8);
-    ctl.abort = ctl.turn = 0;
+    mbar_init(x_full, 8), mbar_init(&t_done[0], 1), mbar_init(&t_done[1], 1);
+    ctl.abort = ctl.turn = ctl.late = 0;
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = ctl.tmem;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { pa_wait(smem_u32(bar), parity & 1, &ctl.abort); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { pa_wait(smem_u32(bar), parity & 1, &ctl.abort, a.limit); };
+  auto aborted = [&]() { return *(volatile int*)&ctl.abort != 0; };
   // One group's products at a time: those of both, interleaved, would end together,
   // and the softmax of both would run together, with the tensor cores idle.
   auto turn = [&]() {
-    const uint64_t t0 = globaltimer();
+    const uint32_t t0 = pa_clock();
 #pragma unroll 1
     while (atomicCAS(&ctl.turn, 0, 1) != 0) {
-      if (*(volatile int*)&ctl.abort) return;
-      if (globaltimer() - t0 > kWaitLimitNs) *(volatile int*)&ctl.abort = 1;
+      if (aborted()) return;
+      if (pa_clock() - t0 > a.limit) *(volatile int*)&ctl.abort = 1;
     }
   };
 
@@ -517,12 +553,19 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
     if (warp == pa::kLoad) {
       if (elect_one()) {
         PaWalk w(a);
-        uint32_t nk = 0, nv = 0, units = 0;
+        uint32_t nk = 0, nv = 0, nq = 0;
+        bool on = true;
+        // after a wait that gave up nothing more is described or loaded: a stage's next copy
+        // would begin while the one before it may be under way
+        auto free = [&](uint64_t* bar, uint32_t parity) {
+          wait(bar, parity);
+          return on = !aborted();
+        };
 #pragma unroll 1
-        for (uint32_t i = 0;; i++) {
+        for (uint32_t i = 0; on; i++) {
           const bool more = w.next(a);
           PaDesc& d = ctl.unit[i % pa::kNU];
-          wait(&u_empty[i % pa::kNU], (i / pa::kNU & 1) ^ 1);
+          if (!free(&u_empty[i % pa::kNU], (i / pa::kNU & 1) ^ 1)) break;
           if (more) w.describe(a, d);
           else d.n = -1;
           mbar_arrive(&u_full[i % pa::kNU]);
@@ -531,7 +574,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           const int n = w.ub - w.ua, key0 = w.k0 + (w.hi - w.ua) * pa::kKeys;
           auto load_k = [&](int u) {
             const uint32_t st = nk % pa::kNK;
-            wait(&k_empty[st], (nk / pa::kNK & 1) ^ 1);
+            if (!free(&k_empty[st], (nk / pa::kNK & 1) ^ 1)) return;
             mbar_arrive_expect_tx(&k_full[st], S::kStep);
 #pragma unroll
             for (int c = 0; c < D; c += 64)
@@ -539,24 +582,34 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
             nk++;
           };
           load_k(0);
-          wait(q_empty, (units & 1) ^ 1);
+          if (!on || !free(q_empty, (nq & 1) ^ 1)) break;
           const int tiles = w.wide ? 2 : 1;
           mbar_arrive_expect_tx(q_full, tiles * (D / 64) * 128 * a.G * a.T);
           for (int t = 0; t < tiles; t++)
             for (int c = 0; c < D; c += 64)
               tma3d_g2s(sm + t * S::kTile + c * 256, &a.qmap, c, w.h * a.G, w.q0 + w.tok + t * a.T, q_full);
+          nq++;
 #pragma unroll 1
-          for (int u = 0; u < n; u++) {
+          for (int u = 0; u < n && on; u++) {
             if (u + 1 < n) load_k(u + 1);
             const uint32_t st = nv % pa::kNV;
-            wait(&v_empty[st], (nv / pa::kNV & 1) ^ 1);
+            on = on && nv < a.loads;
+            if (!on || !free(&v_empty[st], (nv / pa::kNV & 1) ^ 1)) break;
             mbar_arrive_expect_tx(&v_full[st], S::kStep);
 #pragma unroll
             for (int c = 0; c < D; c += 64)
               tma3d_g2s(sm + S::off_v + st * S::kStep + c * 256, &a.vmap, c, w.h, key0 - u * pa::kKeys, &v_full[st]);
             nv++;
           }
-          units++;
+        }
+        // the CTA ends with no copy and no product under way, whatever its warps did: the
+        // last phases of K's and V's stages and of Q, and both groups' commits
+        static_assert(pa::kNK == 2 && pa::kNV == 2, "two stages each");
+#pragma unroll 1
+        for (uint32_t e = 0; e < 7; e++) {
+          uint64_t* const bar = e < 2 ? &k_full[e] : e < 4 ? &v_full[e - 2] : e == 4 ? q_full : &t_done[e - 5];
+          const uint32_t n = e < 2 ? nk + 1 - e : e < 4 ? nv + 3 - e : e == 4 ? 2 * nq : 2;  // twice the phases begun
+          if (n > 1) pa_wait(smem_u32(bar), (n / 2 - 1) & 1, &ctl.late, (uint32_t)kWaitLimitNs);
         }
       }
       __syncwarp();
@@ -573,6 +626,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           const PaDesc& d = ctl.unit[i % pa::kNU];
           wait(&u_full[i % pa::kNU], i / pa::kNU);
           const int n = d.n;
+          if (aborted()) break;
           if (n <= 0) {
             if (n < 0) break;
             mbar_arrive(&u_empty[i % pa::kNU]);
@@ -621,7 +675,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           // Step u's values after its P, and the scores of the next; u = x - by begins.
 #pragma unroll 1
           for (int u = x - by; u < y; u += by) {
-            if (x >= y) break;
+            if (x >= y || aborted()) break;
             const bool more = u + by < y;
             // K and V are waited for ahead of P, while the softmax runs: between P and the
             // next scores there is nothing but the products
@@ -670,6 +724,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           nk += n, nv += n;
           units++;
         }
+        umma_commit(&t_done[t]);
       }
       __syncwarp();
     } else {
@@ -680,7 +735,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
         const PaDesc& d = ctl.unit[i % pa::kNU];
         wait(&u_full[i % pa::kNU], i / pa::kNU);
         const int n = d.n, m0 = d.m0 - d.ua, m1 = d.m1 - d.ua;
-        if (n < 0) break;
+        if (__any_sync(0xffffffffu, aborted() || n < 0)) break;
         if (n > 0) {
           if (lane == 0) ctl.bad[units & 7] = 0;
 #pragma unroll 1
@@ -728,12 +783,11 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
     const float f = MODE == kCapped ? 1.f : a.s.scale * kLog2e;  // base 2 from a capped score, or from q.k
     const int tok_of = idx / a.G;
     uint32_t some = 0, sp = 0, hp = 0, op = 0, xp = 0;  // units with steps; parities of s_full, h_full, o_full and x_full
-    // not a named barrier: after a wait that gave up the warps may differ in their units.
-    // Within a limit, because every other wait of the warps to come is
+    // not a named barrier: after a wait that gave up the warps may differ in their units
     auto meet = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(x_full);
-      while (!mbar_try_wait(smem_u32(x_full), xp) && !*(volatile int*)&ctl.abort) {
+      while (!mbar_try_wait(smem_u32(x_full), xp) && !aborted()) {
       }
       xp ^= 1;
     };
@@ -742,7 +796,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
       const PaDesc& d = ctl.unit[i % pa::kNU];
       wait(&u_full[i % pa::kNU], i / pa::kNU);
       const int n = d.n;
-      if (n < 0) break;
+      if (__any_sync(0xffffffffu, aborted() || n < 0)) break;
       // the row's token in the unit; rows past the last token follow it, and are not written
       const int tok = min((d.wide ? t * a.T : 0) + tok_of, d.tc - 1);
       const int p = d.p0 + tok;
@@ -911,7 +965,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
   if (warp == pa::kMma) {
     tc_fence_after();
     tmem_dealloc(tm, 512);
-    if (ctl.abort && lane == 0) set_status(a.status, SD_TIMEOUT_AT(40));
+    if ((ctl.abort | ctl.late) && lane == 0) set_status(a.status, SD_TIMEOUT_AT(40));
   }
 }
 
@@ -1145,6 +1199,20 @@ static int pa_launch(PaArgs& a, const PaPlan& pl, cudaStream_t st) {
 
 using namespace sdv;
 
+// Of the calls to come (sd_debug_prompt_wait).
+static std::atomic<uint32_t> pa_limit{(uint32_t)kWaitLimitNs};
+static std::atomic<uint32_t> pa_loads{UINT32_MAX};
+
+extern "C" int sd_debug_prompt_wait(int64_t limit_ns, int64_t loads) {
+  if (limit_ns < 0 || limit_ns > (int64_t)kWaitLimitNs || loads < 0) {
+    set_error("sd_debug_prompt_wait: a limit of 0 .. 2 s and loads >= 0 are needed");
+    return SD_ERR_INVALID_ARG;
+  }
+  pa_limit = (uint32_t)(limit_ns ? limit_ns : (int64_t)kWaitLimitNs);
+  pa_loads = limit_ns ? (uint32_t)std::min<int64_t>(loads, UINT32_MAX) : UINT32_MAX;
+  return SD_OK;
+}
+
 static int pa_ctas() { return std::min(num_sms(), pa::kMaxCta); }
 
 extern "C" size_t sd_prompt_attn_workspace(int32_t head_dim) {
@@ -1190,6 +1258,7 @@ extern "C" int sd_prompt_attn(const uint16_t* q, int64_t q_stride, int32_t n_q_h
   a.hq = n_q_heads, a.hkv = n_kv_heads, a.G = n_q_heads / n_kv_heads, a.R = R;
   a.T = 128 / a.G;
   a.cu_q = cu_q, a.cu_k = cu_k, a.out = out, a.lse = lse, a.part = (float*)workspace, a.status = status;
+  a.limit = pa_limit, a.loads = pa_loads;
   if (a.s.cap > 0.f) {
     const double in = (double)a.s.scale / a.s.cap, out = (double)a.s.cap * 1.4426950408889634;
     a.k0 = (float)(out * in);

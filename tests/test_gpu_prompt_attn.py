@@ -312,6 +312,38 @@ def test_same_bits_every_time_and_on_streams_and_graphs(M):
     assert torch.equal(again, want)
 
 
+@pytest.mark.parametrize("loads", [0, 1, 2, 5])
+@pytest.mark.parametrize("m,keys,d,window", [([900], [900], 128, 0), ([700, 30], [900, 2000], 64, 130), ([1, 1, 2], [3000, 700, 5000], 128, 0),
+                                             ([40] * 30, [700] * 30, 128, 0)])
+def test_a_wait_that_runs_out_ends_the_call(M, loads, m, keys, d, window):
+    """Values that do not come (after `loads` steps of a CTA's): every wait for what they would bring gives up after
+    20 ms, the call ends with its status and writes nothing past its rows, and the next one is right."""
+    import time
+
+    from speculative_decoding_tree_bit_gb300 import check as ck, lib
+    q, k, v = inputs(m, keys, 4, 2, d, 12)
+    n = sum(m)
+    big, big_lse = torch.full((n + 9, 4, d), 7.0).bfloat16().cuda(), torch.full((n + 9, 4), 7.0).cuda()
+    op = M.PromptAttention(4, 2, d)
+    rows, held = M.RequestRows(np.cumsum([0] + m)), M.RequestRows(np.cumsum([0] + keys))
+    score = M.KV4Score(window=window)
+    torch.cuda.synchronize()
+    try:
+        ck(lib().sd_debug_prompt_wait(20_000_000, loads))
+        t0 = time.perf_counter()
+        op(q, k, v, rows, held, score=score, out=big[:n], lse=big_lse[:n])
+        torch.cuda.synchronize()
+        dt = time.perf_counter() - t0
+    finally:
+        ck(lib().sd_debug_prompt_wait(0, 0))
+    done = op.status()
+    assert done == 6 if loads == 0 else done in (0, 6)  # a CTA with no more steps than that ends as ever
+    assert dt < 1.5 and (done == 0 or dt >= 0.018)
+    assert (big[n:] == 7).all() and (big_lse[n:] == 7).all()
+    out, lse = run(M, m, keys, q, k, v, score)
+    same(out, lse, m, keys, q, k, v, window=window)
+
+
 def test_no_rows(M):
     q, k, v = inputs([0, 0], [5, 0], 4, 2, 64)
     out, lse = run(M, [0, 0], [5, 0], q, k, v)

@@ -147,6 +147,11 @@ def test_prompt_binding_refuses(M):
         op(q, k, k, M.RequestRows([0, 3], device="cpu"))
 
 
+def test_prompt_wait_refusals(L):
+    assert [L.sd_debug_prompt_wait(*x) for x in ((-1, 0), (2_000_000_001, 0), (1000, -1))] == [1, 1, 1]
+    assert L.sd_debug_prompt_wait(0, 0) == 0
+
+
 def test_sample_refusals(L, M):
     v = lambda x: ctypes.c_void_p(x)  # noqa: E731
 

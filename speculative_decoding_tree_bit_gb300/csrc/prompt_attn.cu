@@ -308,8 +308,9 @@ struct PaRow {
 // What a call's scores have: nothing, slopes, a cap (and slopes or none).
 constexpr int kPlain = 0, kSlopes = 1, kCapped = 2;
 
-// 64 scores of a row, from key c0 of a step on: cap and slope, and -inf for the keys
-// that it does not see (kb: the first one's number; see0 .. see1: the keys it sees).
+// 64 scores of a row, from key c0 of a step on: scale, cap and slope in base 2 (none:
+// q.k), and -inf for the keys that it does not see (kb: the first one's number; see0 ..
+// see1: the keys it sees).
 template <int MODE>
 __device__ __forceinline__ void pa_scores(const PaArgs& a, float (&x)[64], int kb, int see0, int see1, bool masked,
                                           float slope) {
@@ -335,6 +336,11 @@ __device__ __forceinline__ void pa_scores(const PaArgs& a, float (&x)[64], int k
         f2unpack(f2mul(q, z), x[c], x[c + 1]);
       }
     }
+  }
+  if (MODE == kSlopes) {  // the scale ahead of the slope: one over the other may pass fp32
+    const float f = a.s.scale * kLog2e;
+#pragma unroll
+    for (int c = 0; c < 64; c += 2) f2unpack(f2mul(f2pack(x[c], x[c + 1]), f2pack(f, f)), x[c], x[c + 1]);
   }
   if (MODE == kSlopes || (MODE == kCapped && a.s.slopes)) {
 #pragma unroll
@@ -410,12 +416,12 @@ __device__ __forceinline__ void pa_grow(PaRow& w, uint32_t to, float top, bool h
 
 // One step: scores from TMEM, P back in two halves, said by half(0) and half(1).  kb:
 // first key; see0 .. see1: the keys that the row sees; masked: some row of the tile
-// does not see some key; scores are f (x + slope c) + base, c a key's number in the
+// does not see some key; scores are f x + slope2 c + base, c a key's number in the
 // step; first(): waits for the product of the first half.  O is at
 // rest until half(0): its last product's commit came before these scores'.
 template <int D, int MODE, typename Half, typename First>
 __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, uint32_t to, int kb, int see0, int see1,
-                                        bool masked, float f, float slope, float slope2, float base, Half half, First first) {
+                                        bool masked, float f, float slope2, float base, Half half, First first) {
   auto far = [&](float l) { return w.live && !(w.l + l < pa::kMost) && w.l == w.l; };  // too much, or the first NaN
 #pragma unroll 1
   for (int h = 0; h < 2; h++, base += 64.f * slope2) {
@@ -423,7 +429,7 @@ __device__ __forceinline__ void pa_step(const PaArgs& a, PaRow& w, uint32_t ts, 
     float (&x)[64] = reinterpret_cast<float (&)[64]>(r);
     pa_tmem_ld(ts + 64 * h, r);
     pa_wait_ld(r);
-    if (MODE != kPlain || masked) pa_scores<MODE>(a, x, kb + 64 * h, see0, see1, masked, slope);
+    if (MODE != kPlain || masked) pa_scores<MODE>(a, x, kb + 64 * h, see0, see1, masked, slope2);
     // A row's reference goes by the greatest score of the first keys that it sees (nothing
     // is held of it before).  Where it, or base, passes 2^20 its last place shows in the
     // exponent, and a weight could be anything: such scores are rounded first, so that
@@ -780,7 +786,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
     const int t = warp >> 2, idx = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t ts = tm + t * 128 + lanes, to = tm + 256 + t * 128 + lanes;
-    const float f = MODE == kCapped ? 1.f : a.s.scale * kLog2e;  // base 2 from a capped score, or from q.k
+    const float f = MODE == kPlain ? a.s.scale * kLog2e : 1.f;  // base 2 from q.k, or from what pa_scores gives
     const int tok_of = idx / a.G;
     uint32_t some = 0, sp = 0, hp = 0, op = 0, xp = 0;  // units with steps; parities of s_full, h_full, o_full and x_full
     // not a named barrier: after a wait that gave up the warps may differ in their units
@@ -807,7 +813,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
       if (n > 0) {
         wait(q_full, some);  // no group is a unit ahead of the others' barriers
         if (!pair && lane == 0) mbar_arrive(q_empty);  // nothing to exchange
-        const float slope2 = MODE != kPlain && a.s.slopes ? a.s.slopes[d.h * a.G + idx % a.G] * kLog2e : 0.f, slope = slope2 / f;
+        const float slope2 = MODE != kPlain && a.s.slopes ? a.s.slopes[d.h * a.G + idx % a.G] * kLog2e : 0.f;
         const int by = d.wide ? 1 : 2, y = d.y[t], g0 = d.g0[t], g1 = d.g1[t];
         int kb = (d.hi - d.x[t]) * pa::kKeys;
 #pragma unroll 1
@@ -815,7 +821,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1) k_prompt_attn(const __grid_co
           wait(&s_full[t], sp);
           sp ^= 1;
           tc_fence_after();
-          pa_step<D, MODE>(a, row, ts, to, kb, see0, p, u < g0 || u >= g1, f, slope, slope2, MODE != kPlain ? slope2 * (float)(kb - p) : 0.f, [&](int h) {
+          pa_step<D, MODE>(a, row, ts, to, kb, see0, p, u < g0 || u >= g1, f, slope2, MODE != kPlain ? slope2 * (float)(kb - p) : 0.f, [&](int h) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[2 * t + h]);

@@ -240,6 +240,20 @@ def test_slopes_that_leave_the_nearest_key(M, slope, d):
     assert (lse.abs().cpu() <= 300 * slope * 2.0 ** -21 + 1e3).all()  # far keys' distance is taken off again
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale,slope", [(1e-14, 1e25), (1e-39, 0.25), (1e-30, 1e9), (1e-3, 0.5), (100.0, 1e36), (1e-39, 1e36), (1e-39, 0.0)])
+def test_slopes_beside_any_scale(M, scale, slope, d):
+    """Scale and slope a range apart that fp32 does not hold."""
+    m, keys = [150, 3], [150, 300]
+    q, k, v = inputs(m, keys, 4, 2, d, 10)
+    slopes = torch.full((4,), slope)
+    out, lse = run(M, m, keys, q, k, v, M.KV4Score(scale=scale, slopes=slopes.cuda()))
+    if slope < 1e20:
+        same(out, lse, m, keys, q, k, v, scale=scale, slopes=slopes)
+    else:  # the nearest key alone
+        assert torch.equal(out, torch.cat([v[:150], v[150 + 297:]]).repeat_interleave(2, 1)) and torch.isfinite(lse).all()
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("d", [64, 128])
 def test_bad_values_only_reach_the_rows_that_see_them(M, bad, d):

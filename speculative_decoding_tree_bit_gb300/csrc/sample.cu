@@ -397,7 +397,8 @@ struct RowSettings {
     constexpr float lh = (float)1.4426950408889634074, ll = (float)(1.4426950408889634074 - (double)lh);
     const float q = __fdiv_rn(lh, temperature);
     RowScale r = {most, temperature > 0.f ? fminf(q, 3e38f) : 0.f, 0.f};
-    if (temperature > 0.f && q < 3e38f) r.cl = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, temperature, lh), ll), temperature);
+    // (an infinite temperature: every weight is 1, and there is no remainder)
+    if (q > 0.f && q < 3e38f) r.cl = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, temperature, lh), ll), temperature);
     return r;
   }
 };

@@ -77,6 +77,15 @@ def test_settings_by_row(M):
     check(M, x, u, temperature=t, top_k=k, top_p=p, min_p=m)
 
 
+@pytest.mark.parametrize("rows", [6, 200])
+def test_an_infinite_temperature_of_a_row(M, rows):
+    """Every token weighs 1, beside rows of other temperatures."""
+    x, u = normal(rows, 3000, seed=41)
+    t = torch.tensor([math.inf, 1.0, math.inf, 50.0]).repeat(rows // 4 + 1)[:rows].cuda()
+    for kw in (dict(), dict(min_p=0.5), dict(min_p=1.0), dict(top_k=7, min_p=0.1), dict(top_p=0.5)):
+        check(M, x, u, temperature=t, **kw)
+
+
 def test_ties_take_the_lowest_index(M):
     x = torch.zeros(4, 70000).bfloat16().cuda()
     u = torch.tensor([0.0, 0.25, 0.5, 1 - 2.0 ** -24]).cuda()

@@ -80,12 +80,12 @@ struct Weight {
   }
   __device__ __forceinline__ float value() const { return h * __int_as_float((127 + max(n, -126)) << 23); }
   __device__ __forceinline__ bool at_least(float p) const {
-    const float q = p * __int_as_float((127 + min(-n, 126)) << 23);
+    const float q = p * __int_as_float((127 + min(-n, 126)) << 23) * __int_as_float((127 + max(-n - 126, 0)) << 23);
     return __fadd_rn(__fadd_rn(h, -q), l) >= 0.f;
   }
 };
 
-// The weight of logit l <= most; n = -200 where it is below 2^-120.
+// The weight of logit l <= most; n = -200 where it is below 2^-151, less than any min_p.
 __device__ __forceinline__ Weight weight_here(float l, const RowScale& r, const float2* s_exp2) {
   // l - most = s + d, log2 of the weight p + e
   const float s = __fadd_rn(l, -r.most), b = __fadd_rn(s, -l);
@@ -94,7 +94,7 @@ __device__ __forceinline__ Weight weight_here(float l, const RowScale& r, const 
   float e = __fmaf_rn(s, r.ch, -p);
   e = __fmaf_rn(s, r.cl, e);
   e = __fmaf_rn(d, r.ch, e);
-  const bool one = l >= r.most, none = !one && !(p > -120.f);  // beside +inf too
+  const bool one = l >= r.most, none = !one && !(p > -151.f);  // beside +inf too
   if (one || none) p = e = 0.f;
   // p + e = m / 32 + f + e, |f| <= 1 / 64
   const float mf = rintf(p * 32.f);

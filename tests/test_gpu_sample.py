@@ -86,6 +86,17 @@ def test_an_infinite_temperature_of_a_row(M, rows):
         check(M, x, u, temperature=t, **kw)
 
 
+@pytest.mark.parametrize("rows", [3, 200])
+def test_min_p_of_any_size(M, rows):
+    """Down to the least fp32 number, beside weights as small, and beside an infinity, where the others weigh 0."""
+    x, u = normal(rows, 1000, seed=43)
+    x[:, 0] = 100.0
+    x[:, 1:20] = torch.linspace(0.0, 30.0, 19).bfloat16().cuda()
+    x[1, 5] = math.inf
+    for p in (2.0 ** -119, 1e-37, 1e-40, 1e-45):
+        check(M, x, u, min_p=p)
+
+
 def test_ties_take_the_lowest_index(M):
     x = torch.zeros(4, 70000).bfloat16().cuda()
     u = torch.tensor([0.0, 0.25, 0.5, 1 - 2.0 ** -24]).cuda()

@@ -66,7 +66,7 @@ __device__ const Exp2Table kExp2 = Exp2Table();
 // What a row's weights go by.
 struct RowScale {
   float most;    // greatest logit
-  float ch, cl;  // log2(e) / temperature as a pair; 0 where greedy
+  float ch, cl;  // 2 log2(e) / temperature as a pair; 0 where greedy
 };
 
 // A weight 2^n (h + l), h + l in [1, 2].
@@ -87,9 +87,10 @@ struct Weight {
 
 // The weight of logit l <= most; n = -200 where it is below 2^-151, less than any min_p.
 __device__ __forceinline__ Weight weight_here(float l, const RowScale& r, const float2* s_exp2) {
-  // l - most = s + d, log2 of the weight p + e
-  const float s = __fadd_rn(l, -r.most), b = __fadd_rn(s, -l);
-  const float d = __fadd_rn(__fadd_rn(l, -__fadd_rn(s, -b)), __fadd_rn(-r.most, -b));
+  // (l - most) / 2 = s + d (l - most may pass fp32), log2 of the weight p + e
+  const float half = 0.5f * r.most;
+  const float s = __fmaf_rn(l, 0.5f, -half), b = __fmaf_rn(l, -0.5f, s);
+  const float d = __fadd_rn(__fmaf_rn(l, 0.5f, -__fadd_rn(s, -b)), __fadd_rn(-half, -b));
   float p = __fmul_rn(s, r.ch);
   float e = __fmaf_rn(s, r.ch, -p);
   e = __fmaf_rn(s, r.cl, e);
@@ -396,9 +397,10 @@ struct RowSettings {
   __device__ __forceinline__ RowScale scale(float most) const {  // log2(e) / temperature: the quotient and its remainder's
     constexpr float lh = (float)1.4426950408889634074, ll = (float)(1.4426950408889634074 - (double)lh);
     const float q = __fdiv_rn(lh, temperature);
-    RowScale r = {most, temperature > 0.f ? fminf(q, 3e38f) : 0.f, 0.f};
-    // (an infinite temperature: every weight is 1, and there is no remainder)
-    if (q > 0.f && q < 3e38f) r.cl = __fdiv_rn(__fadd_rn(__fmaf_rn(-q, temperature, lh), ll), temperature);
+    RowScale r = {most, temperature > 0.f ? 2.f * q : 0.f, 0.f};
+    // (infinitely large or below 2^-126: every weight is 1, or all but the greatest's 0)
+    if (q > 0.f && temperature >= 0x1p-126f) r.cl = 2.f * __fdiv_rn(__fadd_rn(__fmaf_rn(-q, temperature, lh), ll), temperature);
+    if (temperature > 0.f && temperature < 0x1p-126f) r.ch = INFINITY;
     return r;
   }
 };

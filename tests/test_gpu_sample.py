@@ -97,6 +97,26 @@ def test_min_p_of_any_size(M, rows):
         check(M, x, u, min_p=p)
 
 
+def test_logits_further_apart_than_fp32(M):
+    x, u = normal(4, 500, seed=44)
+    big = torch.finfo(torch.bfloat16).max
+    x[0, 3], x[0, 4] = big, -big
+    x[1], x[1, 9] = -big, big
+    x[2, 3], x[2, 4] = big / 2, -big
+    rows = x.cpu().double()
+    for t in (3e37, 1e38, 2.9e38):
+        for kw in (dict(), dict(top_p=0.5), dict(min_p=0.2)):
+            got = M.sample(x, u, temperature=t, **kw)
+            f = lambda v: torch.tensor(v, dtype=torch.float32).item()  # noqa: E731
+            for r in range(4):
+                token, logprob, kept = ref.sample_row(rows[r], u[r].item(), f(t), 0, f(kw.get("top_p", 1.0)), f(kw.get("min_p", 0.0)))
+                assert (got["tokens"][r].item(), got["kept"][r].item()) == (token, kept), (t, kw, r)
+                # as check, and 500 weights each rounded to a multiple of 2^-44 (row 1: weights of 2^-32 beside one of 1),
+                # of which the logarithm of 1 + x takes no more than x
+                off = abs(got["logprob"][r].item() - logprob)
+                assert off <= 2.0 ** -20 * (abs(logprob) + min(1.0, abs(logprob))) + 2.0 ** -43 + 500 * 2.0 ** -45, (t, kw, r)
+
+
 def test_ties_take_the_lowest_index(M):
     x = torch.zeros(4, 70000).bfloat16().cuda()
     u = torch.tensor([0.0, 0.25, 0.5, 1 - 2.0 ** -24]).cuda()

@@ -634,6 +634,12 @@ class RequestRows:
         self.cu_ptr, self.cu_host_ptr = self.cu_dev.data_ptr(), self.cu.ctypes.data
 
 
+def _i32_most(x) -> int:
+    """A count as an int32 argument, which ctypes would cut to its low bits: more than any
+    call can have is the most, less than any refused one the least."""
+    return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
+
+
 class KV4Score:
     """Scoring options of KV4Cache.attend and observe (sd_kv4_score)."""
 
@@ -644,7 +650,7 @@ class KV4Score:
         if start is not None and (start.dtype != torch.int32 or not start.is_contiguous()):
             raise ValueError("start must be contiguous int32")
         self.slopes, self.start = slopes, start
-        self.args = KV4ScoreArgs(float(scale), float(softcap), _ptr(slopes), int(window), _ptr(start))
+        self.args = KV4ScoreArgs(float(scale), float(softcap), _ptr(slopes), _i32_most(window), _ptr(start))
         self.ref = ctypes.byref(self.args)
 
 
@@ -1108,7 +1114,7 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=Non
     n, vocab = logits.shape
     a = Sampling()
     for name, x, kind, dtype in (("temperature", temperature, float, torch.float32), ("top_p", top_p, float, torch.float32),
-                                 ("min_p", min_p, float, torch.float32), ("top_k", top_k, int, torch.int32)):
+                                 ("min_p", min_p, float, torch.float32), ("top_k", top_k, _i32_most, torch.int32)):
         if isinstance(x, torch.Tensor):
             _same_gpu(x, index, name)
             setattr(a, name + "_rows", _entries(x, n, name, index, dtype))

@@ -117,6 +117,14 @@ def test_logits_further_apart_than_fp32(M):
                 assert off <= 2.0 ** -20 * (abs(logprob) + min(1.0, abs(logprob))) + 2.0 ** -43 + 500 * 2.0 ** -45, (t, kw, r)
 
 
+def test_a_top_k_past_32_bits_keeps_everything(M):
+    x, u = normal(3, 500, seed=45)
+    got, want = M.sample(x, u, top_k=2 ** 32 + 5), M.sample(x, u)
+    assert torch.equal(got["kept"], want["kept"]) and torch.equal(got["tokens"], want["tokens"])
+    with pytest.raises(Exception, match="top_k"):
+        M.sample(x, u, top_k=-2 ** 32 + 3)
+
+
 def test_ties_take_the_lowest_index(M):
     x = torch.zeros(4, 70000).bfloat16().cuda()
     u = torch.tensor([0.0, 0.25, 0.5, 1 - 2.0 ** -24]).cuda()

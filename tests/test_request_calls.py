@@ -167,3 +167,8 @@ def test_sample_refusals(L, M):
     assert call(V=524161, stride=524161) == 2
     with pytest.raises(ValueError, match="CPU"):
         M.sample(torch.zeros(2, 10).bfloat16(), torch.zeros(2))
+
+
+def test_counts_past_32_bits_are_the_most(M):
+    """Not their low bits: a window or a top_k of 2^32 + 5 keeps everything."""
+    assert [M.KV4Score(window=w).args.window for w in (2 ** 32 + 5, 2 ** 31, 7, -2 ** 32 + 3)] == [2 ** 31 - 1, 2 ** 31 - 1, 7, -2 ** 31]

@@ -697,7 +697,9 @@ typedef struct {
 
 /* The pairs' turns a position, f_i / 2 pi, as fractions of 2^64 (host, u64
  * [rot_dim / 2]), and the amplitude.  pos turns mod 2^64 is the angle of any int32
- * position, to 2^-33 of a turn at worst.  scaling null: plain.  Errors:
+ * position; f_i is worked out in 64-bit floating point, which is off by at most 2^-53 of a
+ * turn a position (f_i up to 1; that many times f_i above): 2^-33 at 2^20 positions, 2^-22
+ * at the last one.  scaling null: plain.  Errors:
  * SD_ERR_INVALID_ARG (rot_dim odd or not positive; base, factor, original, low or
  * high not positive and finite where used; low >= high). */
 int sd_rope_turns_host(int32_t rot_dim, double base, const sd_rope_scaling* scaling, uint64_t* turns, float* amplitude);

@@ -9,9 +9,10 @@ namespace sdv {
 // ------------------------------------------------------------------ angles --
 //
 // A pair's frequency is kept as turns a position, a fraction of 2^64, so the
-// angle of any int32 position is one wrapping product: its upper half is the turn
-// to 2^-33 as a signed fraction, which sincospi takes after one conversion.  (In
-// fp32 pos f would be off by 0.06 rad at position 10^6.)
+// angle of any int32 position is one wrapping product: its upper half is the turn as a
+// signed fraction, cut at 2^-32, which sincospi takes after one conversion (2^-26 of a
+// turn).  The frequency itself comes from 64-bit floating point, off by at most 2^-53 of
+// a turn a position.  (In fp32 pos f would be off by 0.06 rad at position 10^6.)
 
 __device__ __forceinline__ void rope_angle(uint64_t turns, int pos, float amplitude, float& c, float& s) {
   const int32_t frac = (int32_t)(((uint64_t)(int64_t)pos * turns) >> 32);

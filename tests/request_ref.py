@@ -1,5 +1,6 @@
 """Rotary positions, attention over packed prompts and sampled tokens in 64
 bits, from their definitions (test infrastructure)."""
+import decimal
 import math
 
 import numpy as np
@@ -30,6 +31,28 @@ def frequencies(rot, base, kind="plain", factor=1.0, original=1.0, low=1.0, high
             f = f * (1 - s) + f / factor * s
         out.append(f)
     return np.array(out)
+
+
+def exact_turns(rot, base, kind="plain", factor=1, original=1, low=1, high=2):
+    """[rot / 2] turns a position to 50 digits: the formulas of `frequencies` over 2 pi."""
+    with decimal.localcontext(decimal.Context(prec=60)):
+        D = decimal.Decimal
+        pi = D("3.14159265358979323846264338327950288419716939937510582097494459")
+        log, factor, original, low, high = D(base).ln(), D(factor), D(original), D(low), D(high)
+        if kind == "ramp":
+            lo, hi = (rot * (original / (2 * pi * t)).ln() / (2 * log) for t in (high, low))
+            lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), rot - 1)
+        out = []
+        for i in range(rot // 2):
+            f, part = (log * -2 * i / rot).exp(), D(1)
+            if kind == "linear":
+                part = D(0)
+            if kind == "bands":
+                part = min(max((original * f / (2 * pi) - low) / (high - low), D(0)), D(1))
+            if kind == "ramp":
+                part = 1 - min(max(D(i - lo) / max(D(hi - lo), D("0.001")), D(0)), D(1))
+            out.append((part * f + (1 - part) * f / factor) / (2 * pi))
+        return out
 
 
 def rotate(x, pos, freq, amplitude=1.0, interleaved=False):

@@ -78,6 +78,25 @@ def test_in_place_on_slices_of_one_projection(M, d, rot):
     assert torch.equal(qkv[:, 10:], before[:, 10:])
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_the_last_positions(M, kind):
+    """Against angles to 60 digits: 2^31 positions off by 2^-53 of a turn each, the turn cut at 2^-32 and as fp32 2^-26,
+    sine and cosine 2^-22 and the products 2^-23 of themselves."""
+    op = M.Rope(64, 64, 5e5, False, scaling(M, kind))
+    pos = [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 4097, 1 << 20]
+    x = rows(4, 3, 64, 11)
+    got = op(x, None, torch.tensor(pos, dtype=torch.int32).cuda())[0].cpu().double()
+    amp = 0.1 * np.log(4.0) + 1 if kind == "ramp" else 1.0
+    turns = ref.exact_turns(64, 5e5, kind, **KINDS[kind])
+    angle = torch.tensor([[float(t * p % 1) for t in turns] for p in pos], dtype=torch.float64) * (2 * np.pi)
+    c, s = (amp * torch.cos(angle))[:, None], (amp * torch.sin(angle))[:, None]
+    x = x.cpu().double()
+    a, b = x[..., :32], x[..., 32:]
+    want = torch.cat([a * c - b * s, a * s + b * c], -1)
+    slack = amp * (a.abs() + b.abs()).repeat(1, 1, 2) * (2 * np.pi * (2.0 ** -22 + 2.0 ** -32 + 2.0 ** -26) + 2.0 ** -22 + 2.0 ** -22)
+    assert ((got - want).abs() <= ref.BF16 * (want.abs() + slack) + slack).all()
+
+
 def test_unaligned_rows(M):
     """Addresses that 16-byte pieces do not fit."""
     op = M.Rope(64, 64, 1e4)

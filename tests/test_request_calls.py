@@ -46,6 +46,25 @@ def test_turns_are_the_frequencies(L, kind, rot, base):
         assert abs(math.cos(2 * math.pi * frac) - math.cos(pos * freq[0])) < 1e-9
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rot,base", [(2, 1e4), (20, 1e4), (64, 5e5), (96, 1e7), (128, 1e6), (256, 1e4)])
+def test_turns_against_60_digits(L, kind, rot, base):
+    """All pairs, off by at most the documented 2^-53 of a turn a position: of f <= 1 and f / 2 pi <= 0.16 the power is
+    off by its own rounding (2^-53) and its exponent's (y e^-y 2^-53, at most 0.4), the scaling by four
+    roundings (2^-53 each) and the quotient by its own and pi's (2^-54): (1 + 0.4 + 4) 0.16 2^-53 + 0.16 2^-52."""
+    a = KINDS[kind]
+    args = sdv.RopeScalingArgs(list(KINDS).index(kind), a.get("factor", 1), a.get("original", 1), a.get("low", 1), a.get("high", 2), 0)
+    turns, amp = np.zeros(rot // 2, np.uint64), ctypes.c_float()
+    assert L.sd_rope_turns_host(rot, base, ctypes.byref(args), turns.ctypes.data, ctypes.byref(amp)) == 0
+    want = ref.exact_turns(rot, base, kind, **a)
+    off = [abs(float(int(t) - w * 2 ** 64)) for t, w in zip(turns, want)]
+    assert max(off) <= 2.0 ** (64 - 53)
+    for pos in (2 ** 31 - 1, -2 ** 31, 2 ** 20, -5):
+        for t, w in zip(turns, want):
+            d = float((int(t) * pos - w * pos * 2 ** 64) % 2 ** 64) / 2.0 ** 64
+            assert min(d % 1.0, 1.0 - d % 1.0) <= abs(pos) * 2.0 ** -53
+
+
 def test_turns_refusals(L):
     out, amp = np.zeros(64, np.uint64), ctypes.c_float()
     call = lambda rot=128, base=1e6, s=None: L.sd_rope_turns_host(  # noqa: E731

@@ -1001,7 +1001,9 @@ class Rope:
         """Rows turned by their positions: q [rows][n_q_heads][head_dim], k
         [rows][n_kv_heads][head_dim] or None, rows may be strided (slices of one
         projection); pos int32 [rows], a negative one turns back.  q_out, k_out: as q
-        and k, q and k themselves for in place.  Returns (q_out, k_out)."""
+        and k, q and k themselves for in place (which leaves slices of one projection
+        with the row stride that PromptAttention and KV4Cache ask of k and v); else
+        contiguous tensors are made.  Returns (q_out, k_out)."""
         idx, D = self._index, self.head_dim
         s = _raw_stream(stream, idx, "the frequencies")
         _same_gpu(q, idx, "q")
@@ -1053,7 +1055,8 @@ class PromptAttention:
                  lse=None, stream=None):
         """q [rows.n][n_q_heads][head_dim], k and v [keys.n][n_kv_heads]
         [head_dim] (keys None: as many as rows); the last row of a request stands at
-        its last key.  Rows may be strided.  score: scale, softcap, slopes and window.
+        its last key.  Rows may be strided, those of k and v by one stride: both slices of
+        one projection, or both contiguous.  score: scale, softcap, slopes and window.
         Returns (out like q, lse float32 [rows.n][n_q_heads])."""
         idx, D, hq, hk = self._index, self.head_dim, self.n_q_heads, self.n_kv_heads
         s = _raw_stream(stream, idx, "the operator")
@@ -1068,7 +1071,7 @@ class PromptAttention:
         qs = _rows16(q, rows.n, hq, D, "q", idx)
         ks = _rows16(k, keys.n, hk, D, "k", idx)
         if _rows16(v, keys.n, hk, D, "v", idx) != ks:
-            raise ValueError("k and v must have one row stride")
+            raise ValueError("k and v must have one row stride: slices of one projection, turned in place, or contiguous")
         ref = None
         if score is not None:
             if score.start is not None:
@@ -1106,7 +1109,8 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=Non
     in [0, 1).  Each setting is a number, or a tensor [rows] (float32, top_k
     int32).  Returns tokens int32 [rows], logprob float32 [rows] (of the token
     among what is kept) and kept int32 [rows].  tokens may stand in for the argmax of
-    sd_accept: the walk then accepts what sampling token by token would have given."""
+    sd_accept, which a decoder of one's own calls (Model.verify walks its argmax): the
+    walk then accepts what sampling token by token would have given."""
     index = logits.get_device()
     s = _raw_stream(stream, index, "logits")
     if logits.dtype not in _BITS16 or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):

@@ -198,3 +198,25 @@ def test_the_path_in_a_graph(M):
             assert torch.equal(got[n], want[n]), n
         assert torch.equal(ctx, s.cache.ctx_len)
     assert s.attention.status() == 0 and s.cache.status() == 0 and s.status.item() == 0
+
+
+def test_the_readme_s_prompt(M):
+    """Slices of one projection, turned in place, attended and stored; k turned into a tensor of its own is refused
+    beside a slice of v, and taken with a v of its own."""
+    m, d = [70, 9], 128
+    qkv = torch.randn(79, HQ + 2 * HKV, d, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    kept = qkv.clone()
+    q, k, v = qkv[:, :HQ], qkv[:, HQ:HQ + HKV], qkv[:, HQ + HKV:]
+    pos = torch.tensor([i for n in m for i in range(n)], dtype=torch.int32).cuda()
+    rope, prompts, attention = M.Rope(d), M.RequestRows(np.cumsum([0] + m)), M.PromptAttention(HQ, HKV, d)
+    cache = M.KV4Cache(np.arange(6).reshape(2, 3), 6, HKV, d, 32)
+    rope(q, k, pos, q_out=q, k_out=k)
+    out, lse = attention(q, k, v, prompts)
+    cache.append(k, v, prompts)
+    q2, k2 = rope(kept[:, :HQ], kept[:, HQ:HQ + HKV], pos)
+    assert torch.equal(q2, q) and torch.equal(k2, k)
+    with pytest.raises(ValueError, match="one row stride"):
+        attention(q2, k2, v, prompts)
+    again, lse2 = attention(q2, k2, v.contiguous(), prompts)
+    assert torch.equal(again, out) and torch.equal(lse2, lse)
+    assert cache.ctx_len.tolist() == m and attention.status() == 0 and cache.status() == 0

@@ -725,22 +725,22 @@ int sd_rope(const uint64_t* turns, float amplitude, int32_t head_dim, int32_t ro
  * keys, row i stands at position n - m + i and sees the keys 0 .. n - m + i, of them
  * with score->window > 0 those less than window back; a request may have no rows, or
  * fewer keys than rows (its first rows then see nothing).  Scores as sd_kv4_score
- * has them (scale, softcap, slopes, window; start must be null: requests are
- * packed), position of key j being j.
+ * has them (scale, softcap, slopes of up to 1e36, window; start must be null: requests
+ * are packed), position of key j being j.
  * q: bf16, rows q_stride elements apart, each [n_q_heads][head_dim]; k, v: rows
  * kv_stride apart, each [n_kv_heads][head_dim]; all 16-byte aligned, strides
  * multiples of 8; head_dim 64 or 128; n_q_heads a multiple of n_kv_heads, at most
  * 128 query heads a kv head.
  * out: bf16 [rows][n_q_heads][head_dim], 16-byte aligned, apart from q, k and v (units
- * of rows run in any order), 0 in a row that sees no key; lse (optional): fp32 [rows][n_q_heads], the natural log of the sum of exp of
- * the scores, -inf in such a row.  Scores, sums and outputs are accumulated in
- * fp32; a softmax weight enters its product in bf16, as the output leaves.  Values of
- * up to 2^127 in size give finite outputs (scores up to 2^24; past those, where a score's
- * last place is more than the weights have room for, up to 2^127 over the number of keys);
- * those below 2^-120 lose bits; a weight below 2^-100 of the row's greatest may count as
- * 0.  What a
- * row does not see does not bear on it, a NaN or an infinity among it; rows behind
- * cu_q[R] are left as they were.
+ * of rows run in any order), 0 in a row that sees no key; lse (optional): fp32
+ * [rows][n_q_heads], the natural log of the sum of exp of the scores, -inf in such a row.
+ * Scores, sums and outputs are accumulated in fp32; a softmax weight enters its product
+ * in bf16, as the output leaves.  Values of up to 2^127 in size give finite outputs
+ * (scores up to 2^24; past those, where a score's last place is more than the weights
+ * have room for, values of up to 2^127 over the number of keys); values below 2^-120 lose
+ * bits, and a weight below 2^-100 of the row's greatest may count as 0.  What a row does
+ * not see does not bear on it, a NaN or an infinity among it; rows behind cu_q[R] are
+ * left as they were.
  * workspace: sd_prompt_attn_workspace bytes, 256-byte aligned, any content; calls
  * that share one must not overlap.  *status (device int32, caller-owned) gets
  * SD_ERR_TIMEOUT where a bounded wait gave up.  Asynchronous on `stream`.  Errors:
@@ -757,21 +757,28 @@ int sd_prompt_attn(const uint16_t* q, int64_t q_stride, int32_t n_q_heads, const
 /* A token of each row of logits from given random numbers: sampled decoding
  * beside the greedy argmax.  ("SpecPilot ...", "Core Idea", item 4, forces the
  * target's own tokens; tokens sampled at every node in the argmax's place make
- * sd_accept's walk accept exactly what sampling token by token would have given.)
+ * sd_accept's walk accept exactly what sampling token by token would have given.  That
+ * is for a decoder of the caller's own, which calls sd_accept by itself and stores the path
+ * (sd_kv4_append takes it): sd_verify_step and sd_verify_batch walk their own argmax.)
  * Of a row's tokens, by falling logit, equal ones by index, with weights w =
  * exp((logit - most) / temperature):
  *   top_k > 0 keeps the first top_k; min_p > 0 of those the ones of w >= min_p; top_p
  *   < 1 of those the shortest run that holds top_p of their sum, one at least;
  *   the token is the first whose running sum passes u times the sum W of what is
  *   kept.
- * temperature <= 0 keeps the first alone (greedy).  A NaN and -inf are never kept
- * (a row of nothing else: token -1, logprob -inf, kept 0); beside +inf every other
- * token weighs 0.  -0 and 0 are equal.  Weights and their sums are held to 2^-45 of
- * the greatest weight, in whole numbers, so a result does not depend on the order
- * of its sums.
+ * temperature 0 keeps the first alone (greedy); one below 2^-126 keeps the weights of the
+ * greatest logit's tokens alone.  A NaN and -inf are never kept (a row of nothing else:
+ * token -1, logprob -inf, kept 0); beside +inf every other token weighs 0.  -0 and 0
+ * are equal.  Weights are whole multiples of 2^-44 of the greatest one, each within 2^-44 of
+ * its value, and their sums are exact (so of V tokens within V 2^-44), so a result does not
+ * depend on the order of its sums.
  * logits: bf16 [rows][vocab], row_stride elements apart, any alignment; u: fp32
  * [rows], clamped to [0, 1 - 2^-24], NaN as 0.  Each setting is one number for all
- * rows, or where its pointer is set a device array [rows].  tokens int32 [rows];
+ * rows (temperature 0 .. 3e38, top_p above 0, min_p 0 .. 1, top_k not negative, else
+ * refused), or where its pointer is set a device array [rows], whose numbers are taken as
+ * they come: temperature negative or NaN as 0, infinite: every weight 1; top_p up to 0
+ * keeps one token, NaN all; min_p above 1 as 1, negative or NaN as 0; top_k negative as 0.
+ * tokens int32 [rows];
  * logprob (optional) fp32 [rows]: ln(w / W) of the token; kept (optional) int32
  * [rows].  1 <= vocab <= 524160.  Asynchronous on `stream`, no workspace.
  * Errors: SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED (vocab), SD_ERR_CUDA. */

@@ -125,6 +125,21 @@ def test_a_top_k_past_32_bits_keeps_everything(M):
         M.sample(x, u, top_k=-2 ** 32 + 3)
 
 
+@pytest.mark.parametrize("rows", [4, 160])
+def test_settings_of_a_row_past_their_range(M, rows):
+    """Numbers that are refused for all rows are taken as the header says where rows have their own."""
+    x, u = normal(rows, 700, seed=46)
+    pair = lambda a, b, dtype=torch.float32: torch.tensor([a, b], dtype=dtype).repeat(rows // 2).cuda()  # noqa: E731
+    for name, a, b, as_a, as_b in (("temperature", -1.0, math.nan, 0.0, 0.0), ("top_p", 0.0, -2.0, 1e-6, 1e-6), ("top_p", math.nan, 3.0, 1.0, 1.0),
+                                   ("min_p", 7.0, -1.0, 1.0, 0.0), ("min_p", math.nan, 0.5, 0.0, 0.5)):
+        got, want = M.sample(x, u, **{name: pair(a, b)}), check(M, x, u, **{name: pair(as_a, as_b)})
+        for k in want:
+            assert torch.equal(got[k], want[k]), (name, a, b, k)
+    got, want = M.sample(x, u, top_k=pair(-5, 9, torch.int32)), check(M, x, u, top_k=pair(0, 9, torch.int32))
+    for k in want:
+        assert torch.equal(got[k], want[k])
+
+
 def test_ties_take_the_lowest_index(M):
     x = torch.zeros(4, 70000).bfloat16().cuda()
     u = torch.tensor([0.0, 0.25, 0.5, 1 - 2.0 ** -24]).cuda()

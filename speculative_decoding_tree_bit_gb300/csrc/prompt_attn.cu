@@ -16,9 +16,12 @@
 //    row sees a key; it stays, and only where the weights would come to 1/2 in all is it
 //    raised and O rescaled in TMEM (looking for the maximum in every step: 177 us for
 //    166 on 8 prompts of up to 2048).  So O never passes the greatest value of the row's
-//    keys, and fp32 holds it down to the bias.  One body of code serves both halves of a
-//    step and all lengths (written out twice: 166 us for 139, and 181 for 133 with caps
-//    and a window).
+//    keys, and fp32 holds it down to the bias.  P is bf16, as V is: a second term for what
+//    the rounding leaves would make three products of two (568 us more for one prompt
+//    of 16384 at the full rate); an output is off by 0.0019 to 0.0023 of its norm, where
+//    its own rounding alone gives 0.0016.  One body of code serves both halves of a step
+//    and all lengths (written out twice, 8 prompts took a fifth longer, the window with
+//    caps a third).
 //  * 8, 9: the products of one group each: S = Q K^T and O += P V, those of one group
 //    while the other is in its softmax.  TMEM: [S 128][S 128][O D][O D].
 //  * 10: walks the CTA's units, says what each is (PaDesc), and loads Q, K and V by TMA.
@@ -32,11 +35,13 @@
 // softmax of 128 scores a thread, and the second half's product, one after the other;
 // two groups in turn make a step of two tiles in about 2600 cycles, of which 2048 are
 // products.  A softmax warp's instructions count (a step's 64 weights take 540 cycles
-// at 2.5 instructions each), not the exponential unit (ncu: 36%), and so does fetching
-// them: all of the loop stays small.  One GB300: 16384 rows, 32 query and 8 kv heads of
-// 128: 1340 us, 1640 TFLOP/s (0.85 of the measured cuBLAS burst, 0.94 of its sustained
-// rate); 8 prompts of up to 2048: 140 us; 512 rows over 33280 keys, 40 heads: 270 us; 16
-// single tokens over 1.5 to 8k keys: 68 us, 5.1 TB/s.
+// at 2.5 instructions each), not the exponential unit (ncu: 39%), and so does fetching
+// them: all of the loop stays small.  Where scores have options and heads are 64, that
+// chain waits for itself (issue 45%, tensor pipe 16%).  One GB300: 16384 rows, 32 query and
+// 8 kv heads of 128: 1360 us, 1620 TFLOP/s (0.84 of the measured cuBLAS burst, 0.93 of
+// its sustained rate); 8 prompts of up to 2048: 147 us; 512 rows over 33280 keys, 40
+// heads: 272 us; 16 single tokens over 1.5 to 8k keys: 69 us, 5.0 TB/s; 5 prompts of up to
+// 3001, 16 heads of 64, cap, slopes and window: 138 us.
 #include <cudaTypedefs.h>
 
 #include <algorithm>

@@ -358,6 +358,35 @@ def test_a_wait_that_runs_out_ends_the_call(M, loads, m, keys, d, window):
     same(out, lse, m, keys, q, k, v, window=window)
 
 
+@pytest.mark.parametrize("m,keys,d,window", [([900] * 20, [900] * 20, 128, 0), ([700, 30] * 30, [900, 2000] * 30, 64, 130),
+                                             ([1, 1, 2] * 50, [3000, 100, 300] * 50, 128, 0)])
+def test_waits_of_a_microsecond(M, m, keys, d, window):
+    """A limit that any wait may pass: a call ends early with its status or is right, and writes nothing past its rows."""
+    from speculative_decoding_tree_bit_gb300 import check as ck, lib
+    q, k, v = inputs(m, keys, 4, 2, d, 13)
+    n = sum(m)
+    op = M.PromptAttention(4, 2, d)
+    rows, held = M.RequestRows(np.cumsum([0] + m)), M.RequestRows(np.cumsum([0] + keys))
+    score = M.KV4Score(window=window)
+    want, want_lse = op(q, k, v, rows, held, score=score)
+    assert op.status() == 0
+    for limit in (1, 1000, 3000, 10000) * 3:
+        big, big_lse = torch.full((n + 9, 4, d), 7.0).bfloat16().cuda(), torch.full((n + 9, 4), 7.0).cuda()
+        torch.cuda.synchronize()
+        try:
+            ck(lib().sd_debug_prompt_wait(limit, 2 ** 31))
+            op(q, k, v, rows, held, score=score, out=big[:n], lse=big_lse[:n])
+            torch.cuda.synchronize()
+        finally:
+            ck(lib().sd_debug_prompt_wait(0, 0))
+        done = op.status()
+        assert done in (0, 6) and (big[n:] == 7).all() and (big_lse[n:] == 7).all()
+        if done == 0:
+            assert torch.equal(big[:n], want) and torch.equal(big_lse[:n], want_lse)
+    out, lse = op(q, k, v, rows, held, score=score)
+    assert op.status() == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 def test_no_rows(M):
     q, k, v = inputs([0, 0], [5, 0], 4, 2, 64)
     out, lse = run(M, [0, 0], [5, 0], q, k, v)
